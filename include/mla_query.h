@@ -63,6 +63,10 @@ extern "C" {
                                max(amax / 6, 2^-9); the 32 scales at byte
                                256, block s at 256 + 8 * (s % 4) + s / 4;
                                64 unscaled E4M3 k_pe at byte 288          */
+#define MLA_KV_FP8_E4M3_PAGE 3 /* the row of MLA_KV_FP8_E4M3 with a scale for
+                               each page: k_scale is FP32 [num_pages], and a
+                               row is divided by its page's (no counterpart on
+                               the pages)                                    */
 
 /* Bits of the device error flag (mla_query_get_error). */
 #define MLA_DEVERR_BAD_SLOT 1u /* a slot >= num_pages * page_size was skipped   */
@@ -72,6 +76,10 @@ extern "C" {
                                   index or address failed its bounds check and
                                   the access was skipped; bit 8 + s is set for
                                   check site s (results are not valid)        */
+
+#define MLA_DEVERR_REFUSED 8u  /* mla_tables_step left a request as it was (no
+                                  pages, no room for its tokens, or a length
+                                  its table row cannot hold)                 */
 
 /* Compute paths (mla_query_set_path). */
 #define MLA_PATH_AUTO 0 /* the default: MLA_PATH_FMA for one token at small
@@ -139,11 +147,12 @@ MLA_API int mla_query_create(mla_query_t* out, int num_heads, const void* w_qb,
  *                 (page "mla.query", method insert); a slot >= num_pages *
  *                 page_size is skipped and sets MLA_DEVERR_BAD_SLOT.
  *   kv_cache      device uint8 [num_pages][page_size][row], row = 576
- *                 (MLA_KV_FP8_E4M3), 656 (MLA_KV_FP8_DS_MLA) or 352
- *                 (MLA_KV_NVFP4_DS_MLA) bytes; slot s lives at page
+ *                 (MLA_KV_FP8_E4M3, MLA_KV_FP8_E4M3_PAGE), 656
+ *                 (MLA_KV_FP8_DS_MLA) or 352 (MLA_KV_NVFP4_DS_MLA) bytes; slot s lives at page
  *                 s / page_size, offset s % page_size.
- *   layout        MLA_KV_FP8_E4M3, MLA_KV_FP8_DS_MLA or MLA_KV_NVFP4_DS_MLA.
+ *   layout        one of MLA_KV_*.
  *   k_scale       device FP32 [1]; the per-tensor layout divides by it
+ *                 (MLA_KV_FP8_E4M3_PAGE: FP32 [num_pages], by the page's)
  *                 (ignored by the two ds layouts, may then be NULL).
  *   q_latent      device BF16 [B][H][512] output.
  *   q_pe          device BF16 [B][H][64] output.
@@ -380,6 +389,196 @@ MLA_API int mla_qkv_a_get_error(mla_qkv_a_t h, unsigned* device_flags, void* str
 /* mla_qkv_a_destroy - free the handle (NULL is a no-op).  No call on it may
  * still be in flight. */
 MLA_API void mla_qkv_a_destroy(mla_qkv_a_t h);
+
+/* ---------------------------------------------------------------------------
+ * The cache side of the step: what reads the paged cache that the decode step
+ * writes, and the tables that tell where its rows lie.  The pages define no
+ * such calls; they have no counterpart there.
+ *
+ *   mla_tables_step    request lengths -> pages, slot map, causal lengths
+ *   mla_query_decode   writes the new tokens' rows (above)
+ *   mla_attn_decode    attention of the query rows over the cache
+ * and, for long contexts, between the last two
+ *   mla_blocks_mean, mla_blocks_score, mla_blocks_select
+ *                      the blocks each query looks at.
+ *
+ * A block table is device int32 [rows][bt_stride]: entry (r, j) is the page
+ * that holds positions j * page_size .. of request r.  A page outside
+ * 0..num_pages - 1 within a request's length counts as absent (its positions
+ * are left out) and raises MLA_DEVERR_BAD_SLOT.  Calls here follow the
+ * conventions above (asynchronous, no allocation, no host synchronisation),
+ * and those that take device_flags OR MLA_DEVERR_* bits into that optional
+ * caller-owned device word.  All of them can be captured into CUDA graphs:
+ * lengths, tables and counts are read on the device.
+ * ------------------------------------------------------------------------- */
+#define MLA_MAX_TABLE_ROWS 4096 /* requests of one mla_tables_step call */
+
+/*
+ * mla_tables_step - one step's block tables, slot map and lengths.
+ *
+ *   rows          requests, 1 <= rows <= MLA_MAX_TABLE_ROWS.
+ *   new_tokens    device int32 [rows]: tokens request r appends now (0: it is
+ *                 idle), or negative: it has ended and gives its pages back.
+ *   lens          device int32 [rows]: positions each request holds.
+ *   lens_out      device int32 [rows]: positions after the step (0 for an
+ *                 ended request); may be lens itself.
+ *   block_table   device int32 [rows][bt_stride], updated: entries of the
+ *                 pages taken now are written, no other.
+ *   free_pages    device int32 [num_pages], a stack of free pages, updated:
+ *                 places 0..*free_count - 1 are free, the last is the top.
+ *                 Ended requests push their pages first, in row order, block
+ *                 after block; then requests take pages from the top, in row
+ *                 order, block after block.
+ *   free_count    device int32 [1]; free_count_out its value after the step,
+ *                 may be free_count itself.
+ *   max_tokens    entries of the three token arrays, >= 1.
+ *   slot_mapping  device int64 [max_tokens]: each new token's cache slot, the
+ *                 requests' tokens one after another in row order; -1 behind
+ *                 the last (the decode step skips such rows).
+ *   token_row     device int32 [max_tokens]: its request, -1 behind the last.
+ *   token_len     device int32 [max_tokens]: positions it looks at, itself
+ *                 the last of them; 0 behind the last.
+ *   cu_tokens     device int32 [rows + 1]: request r's tokens are
+ *                 cu_tokens[r] .. cu_tokens[r + 1] - 1.
+ *
+ * A request whose table row cannot hold its new length, or whose length is
+ * negative or longer than its table row, is left as it is.  From the first
+ * request (in row order) on that finds too few free pages or too little room
+ * in the token arrays, no request appends anything.  Both raise
+ * MLA_DEVERR_REFUSED.  The arrays must not overlap but for the two pairs
+ * named above.  Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.
+ */
+MLA_API int mla_tables_step(int rows, const int32_t* new_tokens, const int32_t* lens,
+                            int32_t* lens_out, int32_t* block_table, int64_t bt_stride,
+                            int32_t* free_pages, const int32_t* free_count,
+                            int32_t* free_count_out, int64_t num_pages, int page_size,
+                            int max_tokens, int64_t* slot_mapping, int32_t* token_row,
+                            int32_t* token_len, int32_t* cu_tokens, unsigned* device_flags,
+                            void* stream);
+
+typedef struct mla_attn* mla_attn_t;
+
+/*
+ * mla_attn_create - the workspace of latent attention for up to max_batch
+ * tokens (1..MLA_MAX_BATCH) of `heads` heads (1..MLA_MAX_ROW_HEADS, the local
+ * heads or all heads of gathered query rows).  Allocates, on the current
+ * device, room for the partial results of the workers that share a context:
+ * at most 2 * SMs * 64 rows of 512 FP32 (38 MiB on 152 SMs), whatever
+ * the batch and the heads.  Synchronises the legacy default stream; the
+ * handle may only be used on that device.
+ * Returns MLA_OK, MLA_EINVAL, MLA_EUNSUPPORTED, MLA_ENOMEM or MLA_ECUDA.
+ */
+MLA_API int mla_attn_create(mla_attn_t* out, int max_batch, int heads);
+
+/*
+ * mla_attn_decode - attention of `batch` query tokens over the paged cache:
+ *   out[t][h] = sum_i p_i c_i[0..511],
+ *   p = softmax_i(softmax_scale * q[t][h] . c_i),
+ * c_i the 576 values of the cache row of position i (512 latent, 64 rope),
+ * i over the first lens[t] positions of request token_row[t], or over those of
+ * them that lie in its selected blocks.
+ *
+ *   q_latent, q_pe  the decode step's outputs: BF16 [batch][heads][512] and
+ *                 [batch][heads][64], or with q_scale_inv (device FP32 [1])
+ *                 the E4M3 codes of mla_query_decode_fp8q.  Element (t, h, i)
+ *                 lies at t * token_stride + h * head_stride + i (elements; 0
+ *                 means contiguous; multiples of 8, for E4M3 of 16).  Gathered
+ *                 rows [batch][q_heads][576] are q_latent = rows, q_pe = rows +
+ *                 512 elements, strides q_heads * 576 and 576 for both.
+ *   kv_cache .. k_scale  as mla_query_decode, the cache read only.
+ *   block_table   device int32 [table_rows][bt_stride].
+ *   token_row     device int32 [batch], or NULL: token t reads table row t.
+ *   lens          device int32 [batch]; at most bt_stride * page_size count.
+ *   sel           device int32 [batch][sel_stride], or NULL for all blocks:
+ *                 the first sel_count[t] entries are blocks of the request's
+ *                 table row, in any order (one named twice counts twice);
+ *                 blocks outside the row and positions from lens[t] on are
+ *                 left out.
+ *   softmax_scale >= 0, finite.
+ *   out           device BF16 [batch][heads][512] (strides as above, multiples
+ *                 of 8).
+ *   lse           device FP32 [batch][heads], natural logarithm of the sum of
+ *                 exponentials, or NULL.
+ *
+ * A token that looks at no position (lens[t] <= 0, a padded token, no block
+ * selected) gets zeros and an lse of -infinity.  Cache bytes of positions
+ * that do not count are never used as values, whatever they hold.  A
+ * token_row outside the table counts as no position and raises
+ * MLA_DEVERR_BAD_SLOT, as do lengths beyond the row.
+ * Results do not depend on the order in which the GPU runs the work.  Calls
+ * sharing a handle, captured or not, must be ordered on one stream: they share
+ * its workspace.  Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.
+ */
+MLA_API int mla_attn_decode(mla_attn_t h, int batch, const void* q_latent, int64_t ql_token_stride,
+                            int64_t ql_head_stride, const void* q_pe, int64_t qp_token_stride,
+                            int64_t qp_head_stride, const float* q_scale_inv, const void* kv_cache,
+                            int64_t num_pages, int page_size, int layout, const float* k_scale,
+                            const int32_t* block_table, int64_t bt_stride, int table_rows,
+                            const int32_t* token_row, const int32_t* lens, const int32_t* sel,
+                            int64_t sel_stride, const int32_t* sel_count, float softmax_scale,
+                            void* out, int64_t out_token_stride, int64_t out_head_stride,
+                            float* lse, void* stream);
+
+/* mla_attn_get_error - read and clear the handle's device error word
+ * (MLA_DEVERR_*); synchronises `stream`. */
+MLA_API int mla_attn_get_error(mla_attn_t h, unsigned* device_flags, void* stream);
+
+/* mla_attn_destroy - free the handle (NULL is a no-op).  No call on it may
+ * still be in flight. */
+MLA_API void mla_attn_destroy(mla_attn_t h);
+
+/*
+ * mla_blocks_mean - the mean key of every block that a step's tokens touched:
+ * mean[p][c] = bf16(sum of value c of the page's filled rows / their number),
+ * for the pages of blocks lens_from[r] / page_size .. of each request r up to
+ * position lens_to[r] (positions from lens_to[r] on are not filled).  Other
+ * pages' means are left as they are.
+ *
+ *   lens_from, lens_to  device int32 [rows]: lens and lens_out of
+ *                 mla_tables_step.  lens_from 0 recomputes a request whole.
+ *   mean          device BF16 [num_pages][576].
+ *   rows          <= MLA_MAX_TABLE_ROWS; the rest as above.
+ * Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.
+ */
+MLA_API int mla_blocks_mean(const void* kv_cache, int64_t num_pages, int page_size, int layout,
+                            const float* k_scale, const int32_t* block_table, int64_t bt_stride,
+                            int rows, const int32_t* lens_from, const int32_t* lens_to, void* mean,
+                            unsigned* device_flags, void* stream);
+
+/*
+ * mla_blocks_score - a score of every block for every query token:
+ * scores[t][j] = max_h (q[t][h] . mean[page of block j]), -infinity for blocks
+ * from lens[t] on and absent pages; all bt_stride columns are written.
+ *
+ *   heads         1 <= heads <= MLA_MAX_ROW_HEADS; queries as mla_attn_decode.
+ *   scores        device FP32 [batch][scores_stride], scores_stride >= bt_stride.
+ * Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.
+ */
+MLA_API int mla_blocks_score(int batch, int heads, const void* q_latent, int64_t ql_token_stride,
+                             int64_t ql_head_stride, const void* q_pe, int64_t qp_token_stride,
+                             int64_t qp_head_stride, const float* q_scale_inv, const void* mean,
+                             int64_t num_pages, int page_size, const int32_t* block_table,
+                             int64_t bt_stride, int table_rows, const int32_t* token_row,
+                             const int32_t* lens, float* scores, int64_t scores_stride,
+                             unsigned* device_flags, void* stream);
+
+/*
+ * mla_blocks_select - the blocks each query token looks at.  Of its
+ * n = ceil(lens[t] / page_size) blocks (at most max_blocks), the first
+ * keep_first and the last keep_last rank as if scored +infinity; the
+ * min(k, n) best are written to sel[t] in ascending order, -1 behind them, and
+ * their number to sel_count[t].  Equal scores: the lowest block first.  NaN
+ * ranks with -infinity.
+ *
+ *   scores        device FP32 [batch][scores_stride], scores_stride >= max_blocks.
+ *   sel           device int32 [batch][sel_stride], sel_stride >= k; the first
+ *                 k entries of a row are written.
+ * Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.
+ */
+MLA_API int mla_blocks_select(int batch, const float* scores, int64_t scores_stride, int max_blocks,
+                              const int32_t* lens, int page_size, int keep_first, int keep_last,
+                              int k, int32_t* sel, int64_t sel_stride, int32_t* sel_count,
+                              void* stream);
 
 #ifdef __cplusplus
 }

@@ -8,15 +8,24 @@ the library; the first binding call does, and fails loudly if it is missing.
 
 from .binding import (  # noqa: F401
     MLA_DEVERR_BAD_SLOT,
+    MLA_DEVERR_REFUSED,
     MLA_DEVERR_TIMEOUT,
     MLA_KV_FP8_DS_MLA,
     MLA_KV_FP8_E4M3,
+    MLA_KV_FP8_E4M3_PAGE,
     MLA_KV_NVFP4_DS_MLA,
     MLA_OK,
     MLA_PATH_AUTO,
     MLA_PATH_FMA,
     MLA_PATH_MMA,
     MlaError,
+    mla_attn_create,
+    mla_attn_decode,
+    mla_attn_destroy,
+    mla_attn_get_error,
+    mla_blocks_mean,
+    mla_blocks_score,
+    mla_blocks_select,
     mla_query_create,
     mla_query_decode,
     mla_query_decode_fp8q,
@@ -32,4 +41,5 @@ from .binding import (  # noqa: F401
     mla_qkv_a_destroy,
     mla_qkv_a_get_error,
     mla_qkv_a_run,
+    mla_tables_step,
 )

@@ -22,9 +22,11 @@ MLA_EUNSUPPORTED = -4
 MLA_KV_FP8_E4M3 = 0
 MLA_KV_FP8_DS_MLA = 1
 MLA_KV_NVFP4_DS_MLA = 2
+MLA_KV_FP8_E4M3_PAGE = 3
 MLA_DEVERR_BAD_SLOT = 1
 MLA_DEVERR_TIMEOUT = 2
 MLA_DEVERR_CHECK = 4  # checks builds only: a bounds check failed (bit 8 + site names it)
+MLA_DEVERR_REFUSED = 8
 MLA_PATH_AUTO = 0
 MLA_PATH_FMA = 1
 MLA_PATH_MMA = 2
@@ -33,6 +35,7 @@ MLA_MAX_HEADS = 128
 MLA_NOALLOC_MAX_BATCH = 64
 MLA_MAX_ROW_HEADS = 1024
 MLA_ROWS_WAIT_MAX_NS = 2000000000
+MLA_MAX_TABLE_ROWS = 4096
 
 _lib = None
 
@@ -102,6 +105,34 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.mla_qkv_a_get_error.restype = i32
     lib.mla_qkv_a_destroy.argtypes = [vp]
     lib.mla_qkv_a_destroy.restype = None
+    lib.mla_tables_step.argtypes = [
+        i32, vp, vp, vp, vp, i64, vp, vp, vp, i64, i32, i32, vp, vp, vp, vp, vp, vp,
+    ]
+    lib.mla_tables_step.restype = i32
+    lib.mla_attn_create.argtypes = [ctypes.POINTER(vp), i32, i32]
+    lib.mla_attn_create.restype = i32
+    lib.mla_attn_decode.argtypes = [
+        vp, i32, vp, i64, i64, vp, i64, i64, vp, vp, i64, i32, i32, vp, vp, i64, i32, vp, vp, vp,
+        i64, vp, f32, vp, i64, i64, vp, vp,
+    ]
+    lib.mla_attn_decode.restype = i32
+    lib.mla_attn_get_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint), vp]
+    lib.mla_attn_get_error.restype = i32
+    lib.mla_attn_destroy.argtypes = [vp]
+    lib.mla_attn_destroy.restype = None
+    lib.mla_blocks_mean.argtypes = [
+        vp, i64, i32, i32, vp, vp, i64, i32, vp, vp, vp, vp, vp,
+    ]
+    lib.mla_blocks_mean.restype = i32
+    lib.mla_blocks_score.argtypes = [
+        i32, i32, vp, i64, i64, vp, i64, i64, vp, vp, i64, i32, vp, i64, i32, vp, vp, vp, i64, vp,
+        vp,
+    ]
+    lib.mla_blocks_score.restype = i32
+    lib.mla_blocks_select.argtypes = [
+        i32, vp, i64, i32, vp, i32, i32, i32, i32, vp, i64, vp, vp,
+    ]
+    lib.mla_blocks_select.restype = i32
     _lib = lib
     return lib
 
@@ -261,6 +292,93 @@ def mla_qkv_a_destroy(handle) -> None:
     load().mla_qkv_a_destroy(handle)
 
 
+def mla_tables_step(
+    rows, new_tokens, lens, lens_out, block_table, bt_stride, free_pages, free_count,
+    free_count_out, num_pages, page_size, max_tokens, slot_mapping, token_row, token_len,
+    cu_tokens, device_flags, stream,
+) -> int:
+    """One step's block tables, slot map and lengths; returns the C return code."""
+    return load().mla_tables_step(
+        rows, _ptr(new_tokens), _ptr(lens), _ptr(lens_out), _ptr(block_table), bt_stride,
+        _ptr(free_pages), _ptr(free_count), _ptr(free_count_out), num_pages, page_size,
+        max_tokens, _ptr(slot_mapping), _ptr(token_row), _ptr(token_len), _ptr(cu_tokens),
+        _ptr(device_flags), _stream(stream),
+    )
+
+
+def mla_attn_create(max_batch, heads) -> int:
+    """Handle of latent attention over the paged cache; raises MlaError on failure."""
+    h = ctypes.c_void_p()
+    rc = load().mla_attn_create(ctypes.byref(h), int(max_batch), int(heads))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_attn_create")
+    return h.value
+
+
+def mla_attn_decode(
+    handle, batch, q_latent, ql_token_stride, ql_head_stride, q_pe, qp_token_stride,
+    qp_head_stride, q_scale_inv, kv_cache, num_pages, page_size, layout, k_scale, block_table,
+    bt_stride, table_rows, token_row, lens, sel, sel_stride, sel_count, softmax_scale, out,
+    out_token_stride, out_head_stride, lse, stream,
+) -> int:
+    """Attention of the query tokens over the paged cache; returns the C return code."""
+    return load().mla_attn_decode(
+        handle, batch, _ptr(q_latent), ql_token_stride, ql_head_stride, _ptr(q_pe),
+        qp_token_stride, qp_head_stride, _ptr(q_scale_inv), _ptr(kv_cache), num_pages, page_size,
+        layout, _ptr(k_scale), _ptr(block_table), bt_stride, table_rows, _ptr(token_row),
+        _ptr(lens), _ptr(sel), sel_stride, _ptr(sel_count), softmax_scale, _ptr(out),
+        out_token_stride, out_head_stride, _ptr(lse), _stream(stream),
+    )
+
+
+def mla_attn_get_error(handle, stream=None) -> int:
+    v = ctypes.c_uint(0)
+    rc = load().mla_attn_get_error(handle, ctypes.byref(v), _stream(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_attn_get_error")
+    return v.value
+
+
+def mla_attn_destroy(handle) -> None:
+    load().mla_attn_destroy(handle)
+
+
+def mla_blocks_mean(
+    kv_cache, num_pages, page_size, layout, k_scale, block_table, bt_stride, rows, lens_from,
+    lens_to, mean, device_flags, stream,
+) -> int:
+    """Mean keys of the blocks touched between two lengths; returns the C return code."""
+    return load().mla_blocks_mean(
+        _ptr(kv_cache), num_pages, page_size, layout, _ptr(k_scale), _ptr(block_table), bt_stride,
+        rows, _ptr(lens_from), _ptr(lens_to), _ptr(mean), _ptr(device_flags), _stream(stream),
+    )
+
+
+def mla_blocks_score(
+    batch, heads, q_latent, ql_token_stride, ql_head_stride, q_pe, qp_token_stride,
+    qp_head_stride, q_scale_inv, mean, num_pages, page_size, block_table, bt_stride, table_rows,
+    token_row, lens, scores, scores_stride, device_flags, stream,
+) -> int:
+    """Scores of every block for every query token; returns the C return code."""
+    return load().mla_blocks_score(
+        batch, heads, _ptr(q_latent), ql_token_stride, ql_head_stride, _ptr(q_pe),
+        qp_token_stride, qp_head_stride, _ptr(q_scale_inv), _ptr(mean), num_pages, page_size,
+        _ptr(block_table), bt_stride, table_rows, _ptr(token_row), _ptr(lens), _ptr(scores),
+        scores_stride, _ptr(device_flags), _stream(stream),
+    )
+
+
+def mla_blocks_select(
+    batch, scores, scores_stride, max_blocks, lens, page_size, keep_first, keep_last, k, sel,
+    sel_stride, sel_count, stream,
+) -> int:
+    """The best-scored blocks of every query token; returns the C return code."""
+    return load().mla_blocks_select(
+        batch, _ptr(scores), scores_stride, max_blocks, _ptr(lens), page_size, keep_first,
+        keep_last, k, _ptr(sel), sel_stride, _ptr(sel_count), _stream(stream),
+    )
+
+
 def exported_symbols() -> list[str]:
     """Function names the public header declares."""
     import re
@@ -268,4 +386,4 @@ def exported_symbols() -> list[str]:
     hdr = os.path.join(os.path.dirname(HERE), "include", "mla_query.h")
     with open(hdr) as f:
         text = f.read()
-    return sorted(set(re.findall(r"\b(mla_(?:query|qkv_a)_[a-z_0-9]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(mla_(?:query|qkv_a|attn|tables|blocks)_[a-z_0-9]+)\s*\(", text)))

@@ -1,0 +1,688 @@
+// mla_attn.cu - latent attention over the paged cache: the C entry points, the
+// mma.sync kernel that serves every layout, and the kernel that joins the
+// parts of a context that several workers read.
+//
+//   o[t][h] = sum_i p_i c_i[0..511],  p = softmax_i(scale * q[t][h] . c_i),
+//   lse[t][h] = log sum_i exp(scale * q[t][h] . c_i)
+//
+// over the cache rows c_i (512 latent and 64 rope values) of the token's
+// context.  The sums run once over the data: with m the running maximum (in
+// base 2), l = sum 2^(x_i - m) and o = sum 2^(x_i - m) c_i are rescaled by
+// 2^(m_old - m_new) whenever m grows.
+#include <stdlib.h>
+
+#include "../../include/mla_query.h"
+#include "mla_attn.cuh"
+#include "mla_device.cuh"
+#include "mla_internal.h"
+
+struct mla_attn {
+  int device;
+  int num_sms;
+  int heads;
+  int max_batch;
+  uint32_t* err;
+  float* part_o;   // partial sums [workers * 2][heads padded][512]
+  float* part_ml;  // their maxima and denominators [..][2]
+};
+
+namespace mla {
+namespace {
+
+// ------------------------------------------------- mma.sync kernel, any layout
+//
+// One CTA takes 16 * MT heads of one token at a time and its tiles of 64
+// cache rows: the rows are widened to BF16 in shared memory (exact for every
+// layout: at most 8 significant bits; a row's FP32 scale goes to the logits
+// and the weights instead), S = Q K^T and O += P V run as m16n8k16 tiles with
+// FP32 accumulators (O in registers: 16 heads x 64 MT columns a warp), and P
+// is rounded to BF16 (half a step: 2^-8 of each weight, below the output's
+// own rounding once weighted and summed).
+
+constexpr int kTile = 64;
+constexpr int kKPitch = kRowElems + 8;   // BF16 elements; 1168 B: ldmatrix without conflicts
+constexpr int kPPitch = kTile + 8;
+constexpr int kSPitch = kTile + 4;
+
+template <int MT>
+struct MmaSmem {
+  static constexpr int kHeads = 16 * MT;
+  static constexpr int oK = 0;
+  static constexpr int oQ = oK + kTile * kKPitch * 2;
+  static constexpr int oP = oQ + kHeads * kKPitch * 2;
+  static constexpr int oS = oP + kHeads * kPPitch * 2;
+  static constexpr int oStat = oS + kHeads * kSPitch * 4;  // alpha[heads], l[heads], m[heads]
+  static constexpr int oRow = oStat + 3 * kHeads * 4;      // int64 row[64]
+  static constexpr int oScale = oRow + kTile * 8;          // float scale[64]
+  static constexpr int oPlan = oScale + kTile * 4;
+  static constexpr int oRed = oPlan + (int)sizeof(AttnPlan) + 8;
+  static constexpr int kBytes = oRed + 64 * 8;
+};
+
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x2(uint32_t& r0, uint32_t& r1, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
+               : "=r"(r0), "=r"(r1)
+               : "r"(addr));
+}
+
+template <int MT, int LAYOUT>
+__global__ void __launch_bounds__(256, 1) mla_attn_mma_kernel(const AttnArgs a) {
+  using S = MmaSmem<MT>;
+  using R = RowChunks<LAYOUT>;
+  constexpr int kHeads = S::kHeads;
+  constexpr int kNQ = MT;        // n8 tiles of S a warp computes
+  constexpr int kNO = 8 * MT;    // n8 tiles of O a warp holds
+  constexpr int kTph = 256 / kHeads;  // threads a head in the softmax
+  constexpr int kCols = kTile / kTph; // positions a thread
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint16_t* sk = reinterpret_cast<uint16_t*>(smem + S::oK);
+  uint16_t* sq = reinterpret_cast<uint16_t*>(smem + S::oQ);
+  uint16_t* sp = reinterpret_cast<uint16_t*>(smem + S::oP);
+  float* ss = reinterpret_cast<float*>(smem + S::oS);
+  float* alpha = reinterpret_cast<float*>(smem + S::oStat);
+  float* sl = alpha + kHeads;
+  float* sm = sl + kHeads;
+  int64_t* srow = reinterpret_cast<int64_t*>(smem + S::oRow);
+  float* sscale = reinterpret_cast<float*>(smem + S::oScale);
+  AttnPlan* plan = reinterpret_cast<AttnPlan*>(smem + S::oPlan);
+  int64_t* red = reinterpret_cast<int64_t*>(smem + S::oRed);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, q4 = lane & 3;
+  const int wm = warp % MT, wn = warp / MT;
+  const int group = blockIdx.x % a.groups, worker = blockIdx.x / a.groups;
+  const int h0 = group * kHeads;
+  pdl_launch_dependents();
+  pdl_wait();
+  attn_make_plan(a, plan, red, blockIdx.x == 0);
+  const int64_t total = plan->start[a.batch];
+  const int workers = attn_workers(a, total);
+  if (worker >= workers) return;
+  const int64_t first = attn_worker_start(total, workers, worker);
+  const int64_t end = attn_worker_start(total, workers, worker + 1);
+  const float qinv = a.q_scale_inv != nullptr ? *a.q_scale_inv : 1.0f;
+  // logits in base 2: x = acc * row scale * (softmax scale / q_scale_inv * log2 e)
+  const float xs = a.scale / qinv * 1.4426950408889634f;
+
+  int64_t x = first;
+  while (x < end) {
+    const int t = attn_token_of(plan, a.batch, x);
+    const int64_t t0 = plan->start[t], t1 = plan->start[t + 1];
+    const int64_t seg_end = min(t1, end);
+    const int row = a.token_row != nullptr ? a.token_row[t] : t;
+    const int64_t len = a.lens[t], nv = attn_positions(a, t, false);
+    // ---- queries
+    __syncthreads();
+    for (int c = tid; c < kHeads * (kRowElems / 8); c += 256) {
+      const int h = c / (kRowElems / 8), k = 8 * (c % (kRowElems / 8));
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (h0 + h < a.heads) {
+        const int64_t e = k < kKvLora ? (int64_t)t * a.ql_ts + (int64_t)(h0 + h) * a.ql_hs + k
+                                      : (int64_t)t * a.qp_ts + (int64_t)(h0 + h) * a.qp_hs + k - kKvLora;
+        const uint8_t* base = k < kKvLora ? a.q_latent : a.q_pe;
+        if (a.q_scale_inv == nullptr) {
+          v = *reinterpret_cast<const uint4*>(base + 2 * e);
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(base + e);
+          float f[8];
+          e4m3x4_values(w.x, f);
+          e4m3x4_values(w.y, f + 4);
+          v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                         pack_bf16x2(f[6], f[7]));
+        }
+      }
+      *reinterpret_cast<uint4*>(sq + h * kKPitch + k) = v;
+    }
+    if (tid < kHeads) {
+      sl[tid] = 0.f;
+      sm[tid] = -INFINITY;
+    }
+    float o[kNO][4];
+#pragma unroll
+    for (int n = 0; n < kNO; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+
+    for (int64_t tile = x; tile < seg_end; ++tile) {
+      const int64_t v0 = (tile - t0) * kTile;
+      __syncthreads();  // the previous tile's K and P are read
+      if (tid < kTile) {
+        int64_t page = 0;
+        const int64_t r = attn_row(a, t, row, nv, len, v0 + tid, &page);
+        srow[tid] = r;
+        sscale[tid] = r >= 0 ? page_scale(a.k_scale, LAYOUT, page) : 1.0f;
+      }
+      __syncthreads();
+      for (int c = tid; c < kTile * R::kChunks; c += 256) {
+        const int i = c / R::kChunks, k = c % R::kChunks;
+        const int64_t r = srow[i];
+        float v[R::kMax];
+#pragma unroll
+        for (int e = 0; e < R::kMax; ++e) v[e] = 0.f;
+        if (r >= 0) {
+          const uint8_t* p = a.cache + r * R::kBytes;
+          R::decode(p, k, *reinterpret_cast<const uint4*>(p + R::offset(k)), v);
+        }
+        uint16_t* d = sk + i * kKPitch + R::col(k);
+        const int width = R::width(k);
+#pragma unroll
+        for (int e = 0; e < R::kMax; e += 8)
+          if (e < width)
+            *reinterpret_cast<uint4*>(d + e) =
+                make_uint4(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]),
+                           pack_bf16x2(v[e + 4], v[e + 5]), pack_bf16x2(v[e + 6], v[e + 7]));
+      }
+      __syncthreads();
+      // ---- S
+      {
+        float c[kNQ][4];
+#pragma unroll
+        for (int n = 0; n < kNQ; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+        const uint32_t qa = smem_u32(sq + (16 * wm + (lane & 15)) * kKPitch + 8 * (lane >> 4));
+        const uint32_t kb = smem_u32(sk + (8 * MT * wn + (lane & 7)) * kKPitch + 8 * ((lane >> 3) & 1));
+#pragma unroll 4
+        for (int k = 0; k < kRowElems / 16; ++k) {
+          uint32_t ra[4];
+          ldsm_x4(ra, qa + 32 * k);
+#pragma unroll
+          for (int n = 0; n < kNQ; ++n) {
+            uint32_t b0, b1;
+            ldsm_x2(b0, b1, kb + 8 * n * kKPitch * 2 + 32 * k);
+            mma_bf16_16816(c[n], ra[0], ra[1], ra[2], ra[3], b0, b1);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < kNQ; ++n) {
+          float* d = ss + (16 * wm + g) * kSPitch + 8 * MT * wn + 8 * n + 2 * q4;
+          d[0] = c[n][0];
+          d[1] = c[n][1];
+          d[8 * kSPitch] = c[n][2];
+          d[8 * kSPitch + 1] = c[n][3];
+        }
+      }
+      __syncthreads();
+      // ---- softmax: kTph threads a head
+      {
+        const int h = tid / kTph, part = tid % kTph;
+        float v[kCols], mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) {
+          const int p = part + kTph * i;
+          v[i] = srow[p] >= 0 ? ss[h * kSPitch + p] * (sscale[p] * xs) : -INFINITY;
+          mx = fmaxf(mx, v[i]);
+        }
+#pragma unroll
+        for (int s = 1; s < kTph; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, s));
+        const float m_old = sm[h], m_new = fmaxf(m_old, mx);
+        const float m_use = m_new == -INFINITY ? 0.f : m_new;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) {
+          const int p = part + kTph * i;
+          const float e = exp2f(v[i] - m_use);
+          sum += e;
+          sp[h * kPPitch + p] = f2bf_bits(e * sscale[p]);
+        }
+#pragma unroll
+        for (int s = 1; s < kTph; s <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
+        __syncwarp();
+        if (part == 0) {
+          const float al = m_old == -INFINITY ? 0.f : exp2f(m_old - m_use);
+          alpha[h] = al;
+          sl[h] = sl[h] * al + sum;
+          sm[h] = m_new;
+        }
+      }
+      __syncthreads();
+      // ---- O
+      {
+        const float a0 = alpha[16 * wm + g], a1 = alpha[16 * wm + g + 8];
+#pragma unroll
+        for (int n = 0; n < kNO; ++n) {
+          o[n][0] *= a0;
+          o[n][1] *= a0;
+          o[n][2] *= a1;
+          o[n][3] *= a1;
+        }
+        const uint32_t pa = smem_u32(sp + (16 * wm + (lane & 15)) * kPPitch + 8 * (lane >> 4));
+        const uint32_t vb = smem_u32(sk + (lane & 15) * kKPitch + 64 * MT * wn + 8 * (lane >> 4));
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k) {
+          uint32_t ra[4];
+          ldsm_x4(ra, pa + 32 * k);
+#pragma unroll
+          for (int n = 0; n < kNO; n += 2) {
+            uint32_t rb[4];
+            ldmatrix_x4_trans(rb, vb + (16 * k * kKPitch + 8 * n) * 2);
+            mma_bf16_16816(o[n], ra[0], ra[1], ra[2], ra[3], rb[0], rb[1]);
+            mma_bf16_16816(o[n + 1], ra[0], ra[1], ra[2], ra[3], rb[2], rb[3]);
+          }
+        }
+      }
+    }
+    // ---- the stretch is done: the output, or a partial
+    const bool whole = x == t0 && seg_end == t1;
+    const int slot = 2 * worker + (x == first ? 0 : 1);
+    const int ha = 16 * wm + g, hb = ha + 8;
+    if (whole) {
+      const float la = sl[ha], lb = sl[hb];
+      const float ra = la == 0.f ? 0.f : 1.0f / la, rb = lb == 0.f ? 0.f : 1.0f / lb;
+#pragma unroll
+      for (int n = 0; n < kNO; ++n) {
+        const int c = 64 * MT * wn + 8 * n + 2 * q4;
+        if (h0 + ha < a.heads)
+          *reinterpret_cast<uint32_t*>(a.out + (int64_t)t * a.o_ts + (int64_t)(h0 + ha) * a.o_hs + c) =
+              pack_bf16x2(o[n][0] * ra, o[n][1] * ra);
+        if (h0 + hb < a.heads)
+          *reinterpret_cast<uint32_t*>(a.out + (int64_t)t * a.o_ts + (int64_t)(h0 + hb) * a.o_hs + c) =
+              pack_bf16x2(o[n][2] * rb, o[n][3] * rb);
+      }
+      if (tid < kHeads && h0 + tid < a.heads && a.lse != nullptr)
+        a.lse[(int64_t)t * a.heads + h0 + tid] = attn_lse(sm[tid], sl[tid]);
+    } else {
+      float* po = a.part_o + ((int64_t)slot * a.heads_pad + h0) * kKvLora;
+#pragma unroll
+      for (int n = 0; n < kNO; ++n) {
+        const int c = 64 * MT * wn + 8 * n + 2 * q4;
+        *reinterpret_cast<float2*>(po + (int64_t)ha * kKvLora + c) = make_float2(o[n][0], o[n][1]);
+        *reinterpret_cast<float2*>(po + (int64_t)hb * kKvLora + c) = make_float2(o[n][2], o[n][3]);
+      }
+      if (tid < kHeads) {
+        float* ml = a.part_ml + ((int64_t)slot * a.heads_pad + h0 + tid) * 2;
+        ml[0] = sm[tid];
+        ml[1] = sl[tid];
+      }
+    }
+    x = seg_end;
+  }
+}
+
+// --------------------------------------------------------------- joining
+//
+// One CTA a (token, head): with M the largest maximum of the parts,
+// o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  Tokens whose context one
+// worker read whole are done already; those that look at nothing get zeros
+// and an lse of -infinity.  Bound by the parts' bytes (L2).
+
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads) mla_attn_join_kernel(const AttnArgs a) {
+  __shared__ AttnPlan plan;
+  __shared__ int64_t red[kJoinThreads / 32];
+  __shared__ float weight[2 * kMaxCtas];
+  __shared__ float4 half[kKvLora / 4];
+  const int tid = threadIdx.x, t = blockIdx.y, h = blockIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
+  attn_make_plan(a, &plan, red, false);
+  const int64_t t0 = plan.start[t], t1 = plan.start[t + 1], total = plan.start[a.batch];
+  uint16_t* out = a.out + (int64_t)t * a.o_ts + (int64_t)h * a.o_hs;
+  if (t0 == t1) {
+    for (int c = 2 * tid; c < kKvLora; c += 2 * kJoinThreads) *reinterpret_cast<uint32_t*>(out + c) = 0u;
+    if (tid == 0 && a.lse != nullptr) a.lse[(int64_t)t * a.heads + h] = -INFINITY;
+    return;
+  }
+  const int workers = attn_workers(a, total);
+  const int w0 = attn_worker_of(total, workers, t0), w1 = attn_worker_of(total, workers, t1 - 1);
+  if (w0 == w1) return;
+  const int n = w1 - w0 + 1;
+  // part i is worker w0 + i's; the first lies in slot 1 where that worker
+  // began with another token
+  const int slot0 = 2 * w0 + (attn_worker_start(total, workers, w0) < t0 ? 1 : 0);
+  auto slot_of = [&](int i) { return i == 0 ? slot0 : 2 * (w0 + i); };
+  float M = -INFINITY;
+  for (int i = 0; i < n; ++i)
+    M = fmaxf(M, a.part_ml[((int64_t)slot_of(i) * a.heads_pad + h) * 2]);
+  const float m_use = M == -INFINITY ? 0.f : M;
+  float l = 0.f;
+  for (int i = 0; i < n; ++i) {
+    const float* ml = a.part_ml + ((int64_t)slot_of(i) * a.heads_pad + h) * 2;
+    const float w = ml[0] == -INFINITY ? 0.f : exp2f(ml[0] - m_use);
+    if (tid == 0) weight[i] = w;
+    l += w * ml[1];
+  }
+  __syncthreads();
+  // threads 0..127 take the even parts, 128..255 the odd ones
+  const int c = tid & 127, odd = tid >> 7;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = odd; i < n; i += 2) {
+    const float4 v = *reinterpret_cast<const float4*>(
+        a.part_o + ((int64_t)slot_of(i) * a.heads_pad + h) * kKvLora + 4 * c);
+    const float w = weight[i];
+    if (w != 0.f) {
+      acc.x += w * v.x;
+      acc.y += w * v.y;
+      acc.z += w * v.z;
+      acc.w += w * v.w;
+    }
+  }
+  if (odd) half[c] = acc;
+  __syncthreads();
+  if (!odd) {
+    const float4 b = half[c];
+    const float r = l == 0.f ? 0.f : 1.0f / l;
+    uint2 v;
+    v.x = pack_bf16x2((acc.x + b.x) * r, (acc.y + b.y) * r);
+    v.y = pack_bf16x2((acc.z + b.z) * r, (acc.w + b.w) * r);
+    *reinterpret_cast<uint2*>(out + 4 * c) = v;
+    if (tid == 0 && a.lse != nullptr) a.lse[(int64_t)t * a.heads + h] = attn_lse(M, l);
+  }
+}
+
+template <int MT>
+cudaError_t launch_mma(const AttnArgs& a, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.workers * a.groups));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = MmaSmem<MT>::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  switch (a.layout) {
+    case MLA_KV_FP8_E4M3: return cudaLaunchKernelEx(&cfg, mla_attn_mma_kernel<MT, MLA_KV_FP8_E4M3>, a);
+    case MLA_KV_FP8_E4M3_PAGE:
+      return cudaLaunchKernelEx(&cfg, mla_attn_mma_kernel<MT, MLA_KV_FP8_E4M3_PAGE>, a);
+    case MLA_KV_FP8_DS_MLA: return cudaLaunchKernelEx(&cfg, mla_attn_mma_kernel<MT, MLA_KV_FP8_DS_MLA>, a);
+    default: return cudaLaunchKernelEx(&cfg, mla_attn_mma_kernel<MT, MLA_KV_NVFP4_DS_MLA>, a);
+  }
+}
+
+template <int MT, int LAYOUT>
+cudaError_t prepare_mma() {
+  static_assert(MmaSmem<MT>::kBytes <= 232448, "shared memory budget");
+  return cudaFuncSetAttribute(mla_attn_mma_kernel<MT, LAYOUT>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, MmaSmem<MT>::kBytes);
+}
+template <int MT>
+cudaError_t prepare_mma_all() {
+  cudaError_t e = prepare_mma<MT, MLA_KV_FP8_E4M3>();
+  if (e == cudaSuccess) e = prepare_mma<MT, MLA_KV_FP8_E4M3_PAGE>();
+  if (e == cudaSuccess) e = prepare_mma<MT, MLA_KV_FP8_DS_MLA>();
+  if (e == cudaSuccess) e = prepare_mma<MT, MLA_KV_NVFP4_DS_MLA>();
+  return e;
+}
+
+// Heads a CTA of the mma.sync kernel takes: 16 or 32 where that covers all of
+// them (less padding, and more workers of the same tiles), 64 otherwise.
+int mma_tiles(int heads) { return heads <= 16 ? 1 : heads <= 32 ? 2 : 4; }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool known_layout(int layout) { return layout >= MLA_KV_FP8_E4M3 && layout <= MLA_KV_FP8_E4M3_PAGE; }
+
+int sm_count(int* num_sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ECUDA;
+  }
+  return MLA_OK;
+}
+
+int launched(cudaError_t e) {
+  if (e == cudaSuccess) return MLA_OK;
+  cudaGetLastError();
+  return MLA_ECUDA;
+}
+
+// Strides of a [batch][heads][width] operand; 0 means contiguous.
+bool fill_strides(int heads, int width, int unit, int64_t* ts, int64_t* hs) {
+  if (*hs == 0) *hs = width;
+  if (*ts == 0) *ts = (int64_t)heads * *hs;
+  return *hs >= width && *ts >= width && *hs % unit == 0 && *ts % unit == 0;
+}
+
+}  // namespace
+}  // namespace mla
+
+extern "C" {
+
+int mla_attn_create(mla_attn_t* out, int max_batch, int heads) {
+  if (out == nullptr) return MLA_EINVAL;
+  *out = nullptr;
+  if (max_batch < 1 || max_batch > MLA_MAX_BATCH || heads < 1 || heads > MLA_MAX_ROW_HEADS)
+    return MLA_EINVAL;
+  mla_attn* h = static_cast<mla_attn*>(calloc(1, sizeof(mla_attn)));
+  if (h == nullptr) return MLA_ENOMEM;
+  h->heads = heads;
+  h->max_batch = max_batch;
+  int rc = MLA_ECUDA;
+  const int gh = 16 * mla::mma_tiles(heads);
+  const int groups = (heads + gh - 1) / gh;
+  size_t slots = 0;
+  if (cudaGetDevice(&h->device) != cudaSuccess) goto fail;
+  if (cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess)
+    goto fail;
+  if (h->num_sms > mla::kMaxCtas || groups > h->num_sms) {
+    rc = MLA_EUNSUPPORTED;
+    goto fail;
+  }
+  if (mla::prepare_mma_all<1>() != cudaSuccess || mla::prepare_mma_all<2>() != cudaSuccess ||
+      mla::prepare_mma_all<4>() != cudaSuccess)
+    goto fail;
+  slots = (size_t)(h->num_sms / groups) * 2 * groups * gh;
+  rc = MLA_ENOMEM;
+  if (cudaMalloc(&h->err, 256) != cudaSuccess ||
+      cudaMalloc(&h->part_o, slots * mla::kKvLora * sizeof(float)) != cudaSuccess ||
+      cudaMalloc(&h->part_ml, slots * 2 * sizeof(float)) != cudaSuccess)
+    goto fail;
+  rc = MLA_ECUDA;
+  if (cudaMemset(h->err, 0, 256) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess) goto fail;
+  *out = h;
+  return MLA_OK;
+fail:
+  mla_attn_destroy(h);
+  cudaGetLastError();
+  return rc;
+}
+
+int mla_attn_decode(mla_attn_t h, int batch, const void* q_latent, int64_t ql_token_stride,
+                    int64_t ql_head_stride, const void* q_pe, int64_t qp_token_stride,
+                    int64_t qp_head_stride, const float* q_scale_inv, const void* kv_cache,
+                    int64_t num_pages, int page_size, int layout, const float* k_scale,
+                    const int32_t* block_table, int64_t bt_stride, int table_rows,
+                    const int32_t* token_row, const int32_t* lens, const int32_t* sel,
+                    int64_t sel_stride, const int32_t* sel_count, float softmax_scale, void* out,
+                    int64_t out_token_stride, int64_t out_head_stride, float* lse, void* stream) {
+  if (h == nullptr || batch < 1 || batch > h->max_batch) return MLA_EINVAL;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return mla::launched(cudaErrorInvalidDevice);
+  if (dev != h->device) return MLA_EINVAL;  // its workspace lies elsewhere
+  if (q_latent == nullptr || q_pe == nullptr || kv_cache == nullptr || block_table == nullptr ||
+      lens == nullptr || out == nullptr)
+    return MLA_EINVAL;
+  if (!mla::known_layout(layout) || (mla::row_scaled(layout) && k_scale == nullptr)) return MLA_EINVAL;
+  if (num_pages < 1 || page_size < 1 || bt_stride < 1 || table_rows < 1) return MLA_EINVAL;
+  if (token_row == nullptr && table_rows < batch) return MLA_EINVAL;
+  if ((sel == nullptr) != (sel_count == nullptr) || (sel != nullptr && sel_stride < 1)) return MLA_EINVAL;
+  if (!(softmax_scale >= 0.0f) || softmax_scale > 3.0e38f) return MLA_EINVAL;
+  const int unit = q_scale_inv != nullptr ? 16 : 8;
+  if (!mla::fill_strides(h->heads, mla::kKvLora, unit, &ql_token_stride, &ql_head_stride) ||
+      !mla::fill_strides(h->heads, mla::kRope, unit, &qp_token_stride, &qp_head_stride) ||
+      !mla::fill_strides(h->heads, mla::kKvLora, 8, &out_token_stride, &out_head_stride))
+    return MLA_EINVAL;
+  if (!mla::aligned16(q_latent) || !mla::aligned16(q_pe) || !mla::aligned16(kv_cache) ||
+      !mla::aligned16(out) || !mla::aligned4(q_scale_inv) || !mla::aligned4(k_scale) ||
+      !mla::aligned4(block_table) || !mla::aligned4(token_row) || !mla::aligned4(lens) ||
+      !mla::aligned4(sel) || !mla::aligned4(sel_count) || !mla::aligned4(lse))
+    return MLA_EINVAL;
+
+  const int mt = mla::mma_tiles(h->heads);
+  mla::AttnArgs a = {};
+  a.q_latent = static_cast<const uint8_t*>(q_latent);
+  a.q_pe = static_cast<const uint8_t*>(q_pe);
+  a.ql_ts = ql_token_stride;
+  a.ql_hs = ql_head_stride;
+  a.qp_ts = qp_token_stride;
+  a.qp_hs = qp_head_stride;
+  a.q_scale_inv = q_scale_inv;
+  a.cache = static_cast<const uint8_t*>(kv_cache);
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.layout = layout;
+  a.k_scale = k_scale;
+  a.table = block_table;
+  a.bt_stride = bt_stride;
+  a.table_rows = table_rows;
+  a.token_row = token_row;
+  a.lens = lens;
+  a.sel = sel;
+  a.sel_stride = sel_stride;
+  a.sel_count = sel_count;
+  a.scale = softmax_scale;
+  a.out = static_cast<uint16_t*>(out);
+  a.o_ts = out_token_stride;
+  a.o_hs = out_head_stride;
+  a.lse = lse;
+  a.part_o = h->part_o;
+  a.part_ml = h->part_ml;
+  a.err = h->err;
+  a.heads = h->heads;
+  a.batch = batch;
+  a.groups = (h->heads + 16 * mt - 1) / (16 * mt);
+  a.heads_pad = a.groups * 16 * mt;
+  a.workers = h->num_sms / a.groups;
+  a.tile = mla::kTile;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int rc = mla::launched(mt == 1   ? mla::launch_mma<1>(a, st)
+                         : mt == 2 ? mla::launch_mma<2>(a, st)
+                                   : mla::launch_mma<4>(a, st));
+  if (rc != MLA_OK) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)h->heads, (unsigned)batch);
+  cfg.blockDim = dim3(mla::kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return mla::launched(cudaLaunchKernelEx(&cfg, mla::mla_attn_join_kernel, a));
+}
+
+int mla_attn_get_error(mla_attn_t h, unsigned* device_flags, void* stream) {
+  if (h == nullptr || device_flags == nullptr) return MLA_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint32_t v = 0;
+  if (cudaMemcpyAsync(&v, h->err, sizeof(v), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess ||
+      cudaMemsetAsync(h->err, 0, sizeof(uint32_t), s) != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ECUDA;
+  }
+  *device_flags = v;
+  return MLA_OK;
+}
+
+void mla_attn_destroy(mla_attn_t h) {
+  if (h == nullptr) return;
+  if (h->err) cudaFree(h->err);
+  if (h->part_o) cudaFree(h->part_o);
+  if (h->part_ml) cudaFree(h->part_ml);
+  free(h);
+}
+
+int mla_tables_step(int rows, const int32_t* new_tokens, const int32_t* lens, int32_t* lens_out,
+                    int32_t* block_table, int64_t bt_stride, int32_t* free_pages,
+                    const int32_t* free_count, int32_t* free_count_out, int64_t num_pages,
+                    int page_size, int max_tokens, int64_t* slot_mapping, int32_t* token_row,
+                    int32_t* token_len, int32_t* cu_tokens, unsigned* device_flags, void* stream) {
+  if (rows < 1 || rows > MLA_MAX_TABLE_ROWS || bt_stride < 1 || num_pages < 1 ||
+      num_pages > 0x7FFFFFFF || page_size < 1 || max_tokens < 1)
+    return MLA_EINVAL;
+  if (new_tokens == nullptr || lens == nullptr || lens_out == nullptr || block_table == nullptr ||
+      free_pages == nullptr || free_count == nullptr || free_count_out == nullptr ||
+      slot_mapping == nullptr || token_row == nullptr || token_len == nullptr || cu_tokens == nullptr)
+    return MLA_EINVAL;
+  if (!mla::aligned4(new_tokens) || !mla::aligned4(lens) || !mla::aligned4(lens_out) ||
+      !mla::aligned4(block_table) || !mla::aligned4(free_pages) || !mla::aligned4(free_count) ||
+      !mla::aligned4(free_count_out) || !mla::aligned4(token_row) || !mla::aligned4(token_len) ||
+      !mla::aligned4(cu_tokens) || !mla::aligned4(device_flags) ||
+      (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+    return MLA_EINVAL;
+  const mla::TableArgs t{rows,          new_tokens, lens,           lens_out,  block_table,
+                         bt_stride,     free_pages, free_count,     free_count_out, num_pages,
+                         page_size,     max_tokens, slot_mapping,   token_row, token_len,
+                         cu_tokens,     device_flags};
+  return mla::launched(mla::launch_tables(t, static_cast<cudaStream_t>(stream)));
+}
+
+int mla_blocks_mean(const void* kv_cache, int64_t num_pages, int page_size, int layout,
+                    const float* k_scale, const int32_t* block_table, int64_t bt_stride, int rows,
+                    const int32_t* lens_from, const int32_t* lens_to, void* mean,
+                    unsigned* device_flags, void* stream) {
+  if (kv_cache == nullptr || block_table == nullptr || lens_from == nullptr || lens_to == nullptr ||
+      mean == nullptr)
+    return MLA_EINVAL;
+  if (!mla::known_layout(layout) || (mla::row_scaled(layout) && k_scale == nullptr)) return MLA_EINVAL;
+  if (num_pages < 1 || page_size < 1 || bt_stride < 1 || rows < 1 || rows > MLA_MAX_TABLE_ROWS)
+    return MLA_EINVAL;
+  if (!mla::aligned16(kv_cache) || !mla::aligned16(mean) || !mla::aligned4(k_scale) ||
+      !mla::aligned4(block_table) || !mla::aligned4(lens_from) || !mla::aligned4(lens_to) ||
+      !mla::aligned4(device_flags))
+    return MLA_EINVAL;
+  int sms = 0;
+  if (mla::sm_count(&sms) != MLA_OK) return MLA_ECUDA;
+  const mla::MeanArgs m{static_cast<const uint8_t*>(kv_cache), num_pages, page_size, layout, k_scale,
+                        block_table, bt_stride, rows, lens_from, lens_to,
+                        static_cast<uint16_t*>(mean), device_flags};
+  return mla::launched(mla::launch_blocks_mean(m, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int mla_blocks_score(int batch, int heads, const void* q_latent, int64_t ql_token_stride,
+                     int64_t ql_head_stride, const void* q_pe, int64_t qp_token_stride,
+                     int64_t qp_head_stride, const float* q_scale_inv, const void* mean,
+                     int64_t num_pages, int page_size, const int32_t* block_table,
+                     int64_t bt_stride, int table_rows, const int32_t* token_row,
+                     const int32_t* lens, float* scores, int64_t scores_stride,
+                     unsigned* device_flags, void* stream) {
+  if (batch < 1 || batch > MLA_MAX_BATCH || heads < 1 || heads > MLA_MAX_ROW_HEADS) return MLA_EINVAL;
+  if (q_latent == nullptr || q_pe == nullptr || mean == nullptr || block_table == nullptr ||
+      lens == nullptr || scores == nullptr)
+    return MLA_EINVAL;
+  if (num_pages < 1 || page_size < 1 || bt_stride < 1 || bt_stride > 0x7FFFFFFF || table_rows < 1 ||
+      (token_row == nullptr && table_rows < batch) || scores_stride < bt_stride)
+    return MLA_EINVAL;
+  const int unit = q_scale_inv != nullptr ? 16 : 8;
+  if (!mla::fill_strides(heads, mla::kKvLora, unit, &ql_token_stride, &ql_head_stride) ||
+      !mla::fill_strides(heads, mla::kRope, unit, &qp_token_stride, &qp_head_stride))
+    return MLA_EINVAL;
+  if (!mla::aligned16(q_latent) || !mla::aligned16(q_pe) || !mla::aligned16(mean) ||
+      !mla::aligned4(q_scale_inv) || !mla::aligned4(block_table) || !mla::aligned4(token_row) ||
+      !mla::aligned4(lens) || !mla::aligned4(scores) || !mla::aligned4(device_flags))
+    return MLA_EINVAL;
+  int sms = 0;
+  if (mla::sm_count(&sms) != MLA_OK) return MLA_ECUDA;
+  const mla::ScoreArgs s{batch, heads, static_cast<const uint8_t*>(q_latent),
+                         static_cast<const uint8_t*>(q_pe), ql_token_stride, ql_head_stride,
+                         qp_token_stride, qp_head_stride, q_scale_inv,
+                         static_cast<const uint16_t*>(mean), num_pages, page_size, block_table,
+                         bt_stride, table_rows, token_row, lens, scores, scores_stride, device_flags};
+  return mla::launched(mla::launch_blocks_score(s, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int mla_blocks_select(int batch, const float* scores, int64_t scores_stride, int max_blocks,
+                      const int32_t* lens, int page_size, int keep_first, int keep_last, int k,
+                      int32_t* sel, int64_t sel_stride, int32_t* sel_count, void* stream) {
+  if (batch < 1 || batch > MLA_MAX_BATCH || scores == nullptr || lens == nullptr || sel == nullptr ||
+      sel_count == nullptr)
+    return MLA_EINVAL;
+  if (max_blocks < 1 || scores_stride < max_blocks || page_size < 1 || keep_first < 0 ||
+      keep_last < 0 || k < 1 || sel_stride < k)
+    return MLA_EINVAL;
+  if (!mla::aligned4(scores) || !mla::aligned4(lens) || !mla::aligned4(sel) || !mla::aligned4(sel_count))
+    return MLA_EINVAL;
+  const mla::SelectArgs s{batch, scores, scores_stride, max_blocks, lens, page_size, keep_first,
+                          keep_last, k, sel, sel_stride, sel_count};
+  return mla::launched(mla::launch_blocks_select(s, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

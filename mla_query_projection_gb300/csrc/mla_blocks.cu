@@ -1,0 +1,397 @@
+// mla_blocks.cu - the selection of cache blocks (pages) for sparse attention:
+// the mean key of a block (mla_blocks_mean), the score of every block for
+// every query (mla_blocks_score) and the best-scored blocks of a query
+// (mla_blocks_select).
+#include <cuda_bf16.h>
+
+#include "../../include/mla_query.h"
+#include "mla_device.cuh"
+#include "mla_internal.h"
+#include "mla_rows.cuh"
+
+namespace mla {
+namespace {
+
+// ------------------------------------------------------------------- means
+//
+// mean[p][c] = bf16((sum over the page's filled rows of key[c]) / rows), the
+// sum in FP32.  It reads each filled row once and writes 1152 bytes a page:
+// bound by HBM.  One CTA a page: chunk c of the row (16 bytes) belongs to one
+// thread of each of kGroups row groups, so a warp reads consecutive bytes of
+// a row, and the groups' sums meet in shared memory in a fixed order.
+
+template <int LAYOUT>
+struct MeanShape {
+  static constexpr int kChunks = RowChunks<LAYOUT>::kChunks;
+  static constexpr int kGroups = kChunks > 20 ? 8 : 14;
+  static constexpr int kThreads = kChunks * kGroups;
+};
+
+template <int LAYOUT>
+__global__ void __launch_bounds__(MeanShape<LAYOUT>::kThreads)
+    mla_blocks_mean_kernel(const MeanArgs m) {
+  using R = RowChunks<LAYOUT>;
+  using M = MeanShape<LAYOUT>;
+  __shared__ float sums[M::kGroups][kRowElems];
+  const int tid = threadIdx.x, chunk = tid % M::kChunks, group = tid / M::kChunks;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int r = blockIdx.y;
+  const int64_t ps = m.page_size;
+  const int64_t cap = m.bt_stride * ps;
+  const int64_t from = max(0, m.lens_from[r]), to = min((int64_t)m.lens_to[r], cap);
+  for (int64_t j = from / ps + blockIdx.x; j * ps < to; j += gridDim.x) {
+    const int64_t page = m.block_table[(int64_t)r * m.bt_stride + j];
+    if (page < 0 || page >= m.num_pages) {
+      if (tid == 0 && m.flags != nullptr) atomicOr(m.flags, MLA_DEVERR_BAD_SLOT);
+      continue;  // the same for the whole CTA
+    }
+    const int filled = (int)min(ps, to - j * ps);
+    const uint8_t* base = m.cache + page * ps * R::kBytes;
+    float acc[R::kMax];
+#pragma unroll
+    for (int i = 0; i < R::kMax; ++i) acc[i] = 0.f;
+#pragma unroll 4
+    for (int t = group; t < filled; t += M::kGroups) {
+      const uint8_t* row = base + (int64_t)t * R::kBytes;
+      const uint4 w = *reinterpret_cast<const uint4*>(row + R::offset(chunk));
+      float v[R::kMax];
+      R::decode(row, chunk, w, v);
+#pragma unroll
+      for (int i = 0; i < R::kMax; ++i) acc[i] += v[i];
+    }
+    const int col = R::col(chunk), width = R::width(chunk);
+#pragma unroll
+    for (int i = 0; i < R::kMax; ++i)
+      if (i < width) sums[group][col + i] = acc[i];
+    __syncthreads();
+    const float mul = page_scale(m.k_scale, LAYOUT, page) / (float)filled;
+    for (int c = 2 * tid; c < kRowElems; c += 2 * M::kThreads) {
+      float a = 0.f, b = 0.f;
+#pragma unroll
+      for (int g = 0; g < M::kGroups; ++g) {
+        a += sums[g][c];
+        b += sums[g][c + 1];
+      }
+      *reinterpret_cast<uint32_t*>(m.mean + page * kRowElems + c) = pack_bf16x2(a * mul, b * mul);
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ scores
+//
+// score[t][j] = max over heads h of q[t][h] . mean[page of block j], FP32
+// accumulation of exact BF16 products (FP8 queries are exact in BF16; their
+// scale divides the result).  One CTA takes kTile blocks of one token: their
+// means go to shared memory once, and its eight warps take 16 heads at a time
+// straight from global memory (mma.sync m16n8k16).  The order of k inside a
+// 32-column step is permuted the same way on both sides, so that each lane's
+// share of a row is 16 contiguous bytes: two k16 steps a 16-byte load.
+
+constexpr int kScorePitch = kRowElems * 2 + 64;  // 1216: 16-byte loads of 8 rows x 4 free of conflicts
+
+template <int NT, bool FP8Q>
+__global__ void __launch_bounds__(256) mla_blocks_score_kernel(const ScoreArgs s) {
+  constexpr int kTile = 8 * NT;
+  __shared__ __align__(16) uint8_t keys[kTile * kScorePitch];
+  __shared__ float best[8][kTile];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, q4 = lane & 3;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int t = blockIdx.y;
+  const int64_t ps = s.page_size;
+  const int row = s.token_row != nullptr ? s.token_row[t] : t;
+  int64_t nb = (max(0, s.lens[t]) + ps - 1) / ps;
+  nb = min(nb, s.bt_stride);
+  if (row < 0 || row >= s.table_rows) {
+    if (nb > 0 && tid == 0 && s.flags != nullptr) atomicOr(s.flags, MLA_DEVERR_BAD_SLOT);
+    nb = 0;
+  }
+  const int64_t j0 = (int64_t)blockIdx.x * kTile;
+  float* out = s.scores + (int64_t)t * s.scores_stride;
+  if (j0 >= nb) {
+    for (int j = tid; j < kTile; j += 256)
+      if (j0 + j < s.bt_stride) out[j0 + j] = -INFINITY;
+    return;
+  }
+  for (int c = tid; c < kTile * (kRowElems / 8); c += 256) {
+    const int b = c / (kRowElems / 8), k = c % (kRowElems / 8);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (j0 + b < nb) {
+      const int64_t page = s.block_table[(int64_t)row * s.bt_stride + j0 + b];
+      if (page >= 0 && page < s.num_pages)
+        v = *reinterpret_cast<const uint4*>(s.mean + page * kRowElems + 8 * k);
+      else if (k == 0 && s.flags != nullptr)
+        atomicOr(s.flags, MLA_DEVERR_BAD_SLOT);
+    }
+    *reinterpret_cast<uint4*>(keys + b * kScorePitch + 16 * k) = v;
+  }
+  __syncthreads();
+  float mx[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY;
+  constexpr int kB = FP8Q ? 1 : 2;  // bytes per query element
+  for (int h0 = 16 * warp; h0 < s.heads; h0 += 128) {
+    // rows h0 + g and h0 + g + 8; heads past the last repeat the last
+    const int ha = min(h0 + g, s.heads - 1), hb = min(h0 + g + 8, s.heads - 1);
+    const uint8_t* la = s.q_latent + ((int64_t)t * s.ql_ts + (int64_t)ha * s.ql_hs) * kB;
+    const uint8_t* lb = s.q_latent + ((int64_t)t * s.ql_ts + (int64_t)hb * s.ql_hs) * kB;
+    const uint8_t* pa = s.q_pe + ((int64_t)t * s.qp_ts + (int64_t)ha * s.qp_hs) * kB;
+    const uint8_t* pb = s.q_pe + ((int64_t)t * s.qp_ts + (int64_t)hb * s.qp_hs) * kB;
+    float acc[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+#pragma unroll 6
+    for (int k = 0; k < kRowElems / 32; ++k) {
+      const uint8_t* a = k < 16 ? la + 32 * k * kB : pa + 32 * (k - 16) * kB;
+      const uint8_t* b = k < 16 ? lb + 32 * k * kB : pb + 32 * (k - 16) * kB;
+      uint4 va, vb;
+      if constexpr (FP8Q) {
+        const uint2 wa = *reinterpret_cast<const uint2*>(a + 8 * q4);
+        const uint2 wb = *reinterpret_cast<const uint2*>(b + 8 * q4);
+        float f[8], h[8];
+        e4m3x4_values(wa.x, f);
+        e4m3x4_values(wa.y, f + 4);
+        e4m3x4_values(wb.x, h);
+        e4m3x4_values(wb.y, h + 4);
+        va = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                        pack_bf16x2(f[6], f[7]));
+        vb = make_uint4(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]), pack_bf16x2(h[4], h[5]),
+                        pack_bf16x2(h[6], h[7]));
+      } else {
+        va = *reinterpret_cast<const uint4*>(a + 16 * q4);
+        vb = *reinterpret_cast<const uint4*>(b + 16 * q4);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint4 kv =
+            *reinterpret_cast<const uint4*>(keys + (8 * n + g) * kScorePitch + 64 * k + 16 * q4);
+        mma_bf16_16816(acc[n], va.x, vb.x, va.y, vb.y, kv.x, kv.y);
+        mma_bf16_16816(acc[n], va.z, vb.z, va.w, vb.w, kv.z, kv.w);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      // NaN wins, as it does in a maximum over the heads
+      const float x = acc[n][0], y = acc[n][2], z = acc[n][1], w = acc[n][3];
+      const float c0 = isnan(x) || isnan(y) ? NAN : fmaxf(x, y);
+      const float c1 = isnan(z) || isnan(w) ? NAN : fmaxf(z, w);
+      mx[n][0] = isnan(mx[n][0]) || isnan(c0) ? NAN : fmaxf(mx[n][0], c0);
+      mx[n][1] = isnan(mx[n][1]) || isnan(c1) ? NAN : fmaxf(mx[n][1], c1);
+    }
+  }
+  // the maximum over the 8 rows a column has in the warp, then over the warps
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float v = mx[n][e];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        const float u = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        v = isnan(u) || isnan(v) ? NAN : fmaxf(u, v);
+      }
+      if (g == 0) best[warp][8 * n + 2 * q4 + e] = v;
+    }
+  __syncthreads();
+  const float inv = FP8Q ? *s.q_scale_inv : 1.0f;
+  for (int j = tid; j < kTile; j += 256) {
+    if (j0 + j >= s.bt_stride) continue;
+    float v = best[0][j];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) {
+      const float u = best[w][j];
+      v = isnan(u) || isnan(v) ? NAN : fmaxf(u, v);
+    }
+    if (FP8Q) v = v / inv;
+    bool in = j0 + j < nb;
+    if (in) {
+      const int64_t page = s.block_table[(int64_t)row * s.bt_stride + j0 + j];
+      in = page >= 0 && page < s.num_pages;
+    }
+    out[j0 + j] = in ? v : -INFINITY;
+  }
+}
+
+// --------------------------------------------------------------- selection
+//
+// The k blocks with the highest scores, ascending.  A score becomes a 32-bit
+// key that orders like it; four histogram passes over 8 bits each, from the
+// top, narrow the k-th key down; then one pass in block order keeps every key
+// above it and, of those equal, the first ones.  All sums are counts, so the
+// result does not depend on the order of the atomics.
+
+constexpr int kSelThreads = 512;
+
+__device__ __forceinline__ uint32_t score_key(float v, bool forced) {
+  if (forced) v = INFINITY;
+  if (isnan(v)) v = -INFINITY;
+  uint32_t u = __float_as_uint(v);
+  if (u == 0x80000000u) u = 0;  // -0 ties with +0
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(kSelThreads) mla_blocks_select_kernel(const SelectArgs s) {
+  __shared__ uint32_t hist[256];
+  __shared__ uint32_t wsum[2][kSelThreads / 32];
+  __shared__ uint32_t pick_digit, pick_above;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int t = blockIdx.x;
+  const float* sc = s.scores + (int64_t)t * s.scores_stride;
+  int32_t* out = s.sel + (int64_t)t * s.sel_stride;
+  const int64_t ps = s.page_size;
+  const int n = (int)min((max((int64_t)s.lens[t], (int64_t)0) + ps - 1) / ps, (int64_t)s.max_blocks);
+  const int k = min(s.k, n);
+  for (int j = k + tid; j < s.k; j += kSelThreads) out[j] = -1;
+  if (tid == 0) s.sel_count[t] = k;
+  if (k == n) {
+    for (int j = tid; j < n; j += kSelThreads) out[j] = j;
+    return;
+  }
+  const int last0 = n - s.keep_last;
+  auto key_at = [&](int j) { return score_key(sc[j], j < s.keep_first || j >= last0); };
+  uint32_t prefix = 0, need = (uint32_t)k;  // `need` of the keys that share the prefix
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int b = tid; b < 256; b += kSelThreads) hist[b] = 0;
+    __syncthreads();
+    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+    for (int j0 = 0; j0 < n; j0 += kSelThreads) {
+      const int j = j0 + tid;
+      const uint32_t key = j < n ? key_at(j) : 0u;
+      const bool in = j < n && (key & mask) == prefix;
+      const uint32_t digit = in ? (key >> shift) & 255u : 256u;
+      // one atomic for the lanes of a warp that share a digit
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, digit);
+      if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], (uint32_t)__popc(same));
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // lane l holds digits 255 - 8 l .. 248 - 8 l: counts from the top
+      uint32_t c[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        c[i] = hist[255 - 8 * lane - i];
+        sum += c[i];
+      }
+      uint32_t inc = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      uint32_t above = inc - sum;
+      if (above < need && inc >= need) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (above < need && above + c[i] >= need) {
+            pick_digit = 255 - 8 * lane - i;
+            pick_above = above;
+            break;
+          }
+          above += c[i];
+        }
+      }
+    }
+    __syncthreads();
+    prefix |= pick_digit << shift;
+    need -= pick_above;
+    __syncthreads();
+  }
+  // keys above `prefix` are all in; of those equal to it the first `need`
+  uint32_t base = 0, ties = 0;
+  for (int j0 = 0; j0 < n; j0 += kSelThreads) {
+    const int j = j0 + tid;
+    const uint32_t key = j < n ? key_at(j) : 0u;
+    const bool gt = j < n && key > prefix, eq = j < n && key == prefix;
+    const uint32_t bg = __ballot_sync(0xFFFFFFFFu, gt), be = __ballot_sync(0xFFFFFFFFu, eq);
+    if (lane == 0) {
+      wsum[0][warp] = __popc(bg);
+      wsum[1][warp] = __popc(be);
+    }
+    __syncthreads();
+    uint32_t g0 = 0, e0 = 0, gt_all = 0, eq_all = 0;
+#pragma unroll
+    for (int w = 0; w < kSelThreads / 32; ++w) {
+      if (w == warp) {
+        g0 = gt_all;
+        e0 = eq_all;
+      }
+      gt_all += wsum[0][w];
+      eq_all += wsum[1][w];
+    }
+    const uint32_t below = (1u << lane) - 1u;
+    g0 += __popc(bg & below);
+    e0 += ties + __popc(be & below);
+    if (gt) out[base + g0 + min(e0, need)] = j;
+    if (eq && e0 < need) out[base + g0 + e0] = j;
+    base += gt_all;
+    ties += eq_all;
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_blocks_mean(const MeanArgs& m, int num_sms, cudaStream_t stream) {
+  // four CTAs an SM in all, but no more a row than it can have blocks
+  int64_t gx = (4 * (int64_t)num_sms + m.rows - 1) / m.rows;
+  if (gx > m.bt_stride) gx = m.bt_stride;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)gx, (unsigned)m.rows, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  switch (m.layout) {
+    case MLA_KV_FP8_E4M3:
+      cfg.blockDim = dim3(MeanShape<MLA_KV_FP8_E4M3>::kThreads);
+      return cudaLaunchKernelEx(&cfg, mla_blocks_mean_kernel<MLA_KV_FP8_E4M3>, m);
+    case MLA_KV_FP8_E4M3_PAGE:
+      cfg.blockDim = dim3(MeanShape<MLA_KV_FP8_E4M3_PAGE>::kThreads);
+      return cudaLaunchKernelEx(&cfg, mla_blocks_mean_kernel<MLA_KV_FP8_E4M3_PAGE>, m);
+    case MLA_KV_FP8_DS_MLA:
+      cfg.blockDim = dim3(MeanShape<MLA_KV_FP8_DS_MLA>::kThreads);
+      return cudaLaunchKernelEx(&cfg, mla_blocks_mean_kernel<MLA_KV_FP8_DS_MLA>, m);
+    default:
+      cfg.blockDim = dim3(MeanShape<MLA_KV_NVFP4_DS_MLA>::kThreads);
+      return cudaLaunchKernelEx(&cfg, mla_blocks_mean_kernel<MLA_KV_NVFP4_DS_MLA>, m);
+  }
+}
+
+cudaError_t launch_blocks_score(const ScoreArgs& s, int num_sms, cudaStream_t stream) {
+  // 16 blocks a CTA: their means are 18 KiB, and several CTAs share an SM
+  constexpr int NT = 2;
+  (void)num_sms;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((s.bt_stride + 8 * NT - 1) / (8 * NT)), (unsigned)s.batch, 1);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return s.q_scale_inv != nullptr ? cudaLaunchKernelEx(&cfg, mla_blocks_score_kernel<NT, true>, s)
+                                  : cudaLaunchKernelEx(&cfg, mla_blocks_score_kernel<NT, false>, s);
+}
+
+cudaError_t launch_blocks_select(const SelectArgs& s, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)s.batch);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, mla_blocks_select_kernel, s);
+}
+
+}  // namespace mla

@@ -220,6 +220,12 @@ __device__ __forceinline__ float kv_group_ss(uint4 v, float (&x)[8]) {
   return ss;
 }
 
+// The divisor of a per-tensor row: k_scale[0], or with a scale for each page
+// the one of the slot's page (a valid slot: kv_row returned its row).
+__device__ __forceinline__ float kv_divisor(const DecodeArgs& a, float tensor_scale, int64_t slot) {
+  return a.layout == MLA_KV_FP8_E4M3_PAGE ? a.k_scale[slot / a.page_size] : tensor_scale;
+}
+
 // The cache row of a slot, or null (a negative slot skips the row; a slot
 // beyond the cache skips it and sets MLA_DEVERR_BAD_SLOT).
 __device__ __forceinline__ uint8_t* kv_row(const DecodeArgs& a, int64_t slot, bool flag) {
@@ -284,7 +290,7 @@ __device__ void kv_insert_loaded(const DecodeArgs& a, int lt, float* red2, const
   const float rr = __frsqrt_rn(__fadd_rn(__fmul_rn(total, 1.0f / 512.0f), a.eps));
   float n[8];
   kv_group_norm(x, gv, rr, n);
-  kv_store_group(a, row, n, pe, lt, ds, nv, ks);
+  kv_store_group(a, row, n, pe, lt, ds, nv, kv_divisor(a, ks, slot));
 }
 
 __device__ void kv_insert(const DecodeArgs& a, int b, int lt, float* red2) {
@@ -328,11 +334,12 @@ __device__ void kv_insert_warp_loaded(const DecodeArgs& a, int lane, const KvWar
   uint8_t* row = kv_row(a, slot, lane == 0);
   if (row == nullptr) return;
   const float rr = __frsqrt_rn(__fadd_rn(__fmul_rn(s0 + s1, 1.0f / 512.0f), a.eps));
+  const float kd = kv_divisor(a, ks, slot);
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     float n[8];
     kv_group_norm(x[g], gv[g], rr, n);
-    kv_store_group(a, row, n, g == 0 ? pe : make_uint4(0, 0, 0, 0), lane + 32 * g, ds, nv, ks);
+    kv_store_group(a, row, n, g == 0 ? pe : make_uint4(0, 0, 0, 0), lane + 32 * g, ds, nv, kd);
   }
 }
 

@@ -212,4 +212,110 @@ cudaError_t repack_w_uk(const uint16_t* w_uk, uint8_t* dst, int heads, cudaStrea
 
 int tokens_per_cta(int batch, bool mma);
 
+// ---- the operators on the cache the decode step writes
+
+// Latent attention (mla_attn.cu).  Strides in elements; out [batch][heads][512]
+// BF16, lse [batch][heads].
+struct AttnArgs {
+  const uint8_t* q_latent;
+  const uint8_t* q_pe;
+  int64_t ql_ts, ql_hs, qp_ts, qp_hs;
+  const float* q_scale_inv;  // null: BF16 queries, else E4M3 codes of q * *q_scale_inv
+  const uint8_t* cache;
+  int64_t num_pages;
+  int page_size;
+  int layout;
+  const float* k_scale;
+  const int32_t* table;  // [table_rows][bt_stride] page of each block
+  int64_t bt_stride;
+  int table_rows;
+  const int32_t* token_row;  // [batch] or null: token t reads table row t
+  const int32_t* lens;       // [batch] positions each token looks at
+  const int32_t* sel;        // [batch][sel_stride] selected blocks, or null: all
+  int64_t sel_stride;
+  const int32_t* sel_count;  // [batch]
+  float scale;
+  uint16_t* out;
+  int64_t o_ts, o_hs;
+  float* lse;      // or null
+  float* part_o;   // [2 * workers][heads_pad][512]
+  float* part_ml;  // [2 * workers][heads_pad][2]
+  uint32_t* err;
+  int heads, heads_pad, groups, batch;
+  int workers;  // per head group
+  int tile;     // positions a tile
+};
+
+// Block tables and slot map of a step (mla_tables.cu).
+struct TableArgs {
+  int rows;
+  const int32_t* new_tokens;
+  const int32_t* lens;
+  int32_t* lens_out;
+  int32_t* block_table;
+  int64_t bt_stride;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* free_count_out;
+  int64_t num_pages;
+  int page_size;
+  int max_tokens;
+  int64_t* slot_mapping;
+  int32_t* token_row;
+  int32_t* token_len;
+  int32_t* cu_tokens;
+  unsigned* flags;
+};
+cudaError_t launch_tables(const TableArgs& t, cudaStream_t stream);
+
+// Block means, scores and selection (mla_blocks.cu).
+struct MeanArgs {
+  const uint8_t* cache;
+  int64_t num_pages;
+  int page_size;
+  int layout;
+  const float* k_scale;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int rows;
+  const int32_t* lens_from;
+  const int32_t* lens_to;
+  uint16_t* mean;  // [num_pages][576]
+  unsigned* flags;
+};
+cudaError_t launch_blocks_mean(const MeanArgs& m, int num_sms, cudaStream_t stream);
+
+struct ScoreArgs {
+  int batch, heads;
+  const uint8_t* q_latent;
+  const uint8_t* q_pe;
+  int64_t ql_ts, ql_hs, qp_ts, qp_hs;
+  const float* q_scale_inv;
+  const uint16_t* mean;
+  int64_t num_pages;
+  int page_size;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int table_rows;
+  const int32_t* token_row;
+  const int32_t* lens;
+  float* scores;
+  int64_t scores_stride;
+  unsigned* flags;
+};
+cudaError_t launch_blocks_score(const ScoreArgs& s, int num_sms, cudaStream_t stream);
+
+struct SelectArgs {
+  int batch;
+  const float* scores;
+  int64_t scores_stride;
+  int max_blocks;
+  const int32_t* lens;
+  int page_size, keep_first, keep_last, k;
+  int32_t* sel;
+  int64_t sel_stride;
+  int32_t* sel_count;
+};
+cudaError_t launch_blocks_select(const SelectArgs& s, cudaStream_t stream);
+
 }  // namespace mla
