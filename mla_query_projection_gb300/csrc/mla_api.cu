@@ -43,9 +43,7 @@ struct mla_query {
   int small_ctas;               // its grid, 0 if it cannot run on this device
 };
 
-namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+namespace mla {
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -60,10 +58,16 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
+}  // namespace mla
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
 // W_UK [H*128 rows][512 columns] BF16, boxes of 128 rows x 64 columns (128 B
 // rows, 128 B swizzle).
 int encode_uk_map(CUtensorMap* map, const void* w_uk, int heads) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  PFN_cuTensorMapEncodeTiled_v12000 enc = mla::tensor_map_encoder();
   if (enc == nullptr) return MLA_ECUDA;
   cuuint64_t dims[2] = {(cuuint64_t)mla::kKvLora, (cuuint64_t)heads * mla::kNope};
   cuuint64_t strides[1] = {(cuuint64_t)mla::kKvLora * 2};

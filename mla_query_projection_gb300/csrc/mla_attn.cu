@@ -411,7 +411,7 @@ cudaError_t prepare_mma_all() {
 
 // Heads a CTA of the mma.sync kernel takes: 16 or 32 where that covers all of
 // them (less padding, and more workers of the same tiles), 64 otherwise.
-int mma_tiles(int heads) { return heads <= 16 ? 1 : heads <= 32 ? 2 : 4; }
+int mma_tiles(int heads) { return attn_tc_heads(heads) / 16; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -466,7 +466,7 @@ int mla_attn_create(mla_attn_t* out, int max_batch, int heads) {
     goto fail;
   }
   if (mla::prepare_mma_all<1>() != cudaSuccess || mla::prepare_mma_all<2>() != cudaSuccess ||
-      mla::prepare_mma_all<4>() != cudaSuccess)
+      mla::prepare_mma_all<4>() != cudaSuccess || mla::prepare_attn_tc() != cudaSuccess)
     goto fail;
   slots = (size_t)(h->num_sms / groups) * 2 * groups * gh;
   rc = MLA_ENOMEM;
@@ -547,14 +547,22 @@ int mla_attn_decode(mla_attn_t h, int batch, const void* q_latent, int64_t ql_to
   a.err = h->err;
   a.heads = h->heads;
   a.batch = batch;
+  // Both kernels take 16, 32 or 64 heads a CTA by the same rule.
   a.groups = (h->heads + 16 * mt - 1) / (16 * mt);
   a.heads_pad = a.groups * 16 * mt;
   a.workers = h->num_sms / a.groups;
-  a.tile = mla::kTile;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int rc = mla::launched(mt == 1   ? mla::launch_mma<1>(a, st)
-                         : mt == 2 ? mla::launch_mma<2>(a, st)
-                                   : mla::launch_mma<4>(a, st));
+  cudaError_t e;
+  if (mla::attn_tc_serves(a)) {
+    a.tile = mla::attn_tc_tile();
+    e = mla::launch_attn_tc(a, st);
+  } else {
+    a.tile = mla::kTile;
+    e = mt == 1   ? mla::launch_mma<1>(a, st)
+        : mt == 2 ? mla::launch_mma<2>(a, st)
+                  : mla::launch_mma<4>(a, st);
+  }
+  int rc = mla::launched(e);
   if (rc != MLA_OK) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)h->heads, (unsigned)batch);
