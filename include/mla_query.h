@@ -488,7 +488,8 @@ MLA_API int mla_attn_create(mla_attn_t* out, int max_batch, int heads);
  *   kv_cache .. k_scale  as mla_query_decode, the cache read only.
  *   block_table   device int32 [table_rows][bt_stride].
  *   token_row     device int32 [batch], or NULL: token t reads table row t.
- *   lens          device int32 [batch]; at most bt_stride * page_size count.
+ *   lens          device int32 [batch]; at most bt_stride * page_size count, and
+ *                 at most 2^29.
  *   sel           device int32 [batch][sel_stride], or NULL for all blocks:
  *                 the first sel_count[t] entries are blocks of the request's
  *                 table row, in any order (one named twice counts twice);

@@ -24,6 +24,7 @@ struct mla_attn {
   uint32_t* err;
   float* part_o;   // partial sums [workers * 2][heads padded][512]
   float* part_ml;  // their maxima and denominators [..][2]
+  uint32_t* plan;  // the tiles up to and with each token's [MLA_MAX_BATCH]
 };
 
 namespace mla {
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(256, 1) mla_attn_mma_kernel(const AttnArgs a) 
   int64_t* srow = reinterpret_cast<int64_t*>(smem + S::oRow);
   float* sscale = reinterpret_cast<float*>(smem + S::oScale);
   AttnPlan* plan = reinterpret_cast<AttnPlan*>(smem + S::oPlan);
-  int64_t* red = reinterpret_cast<int64_t*>(smem + S::oRed);
+  uint32_t* red = reinterpret_cast<uint32_t*>(smem + S::oRed);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q4 = lane & 3;
@@ -100,22 +101,20 @@ __global__ void __launch_bounds__(256, 1) mla_attn_mma_kernel(const AttnArgs a) 
   pdl_launch_dependents();
   pdl_wait();
   attn_make_plan(a, plan, red, blockIdx.x == 0);
-  const int64_t total = plan->start[a.batch];
+  const uint32_t total = plan->end[a.batch - 1];
   const int workers = attn_workers(a, total);
   if (worker >= workers) return;
-  const int64_t first = attn_worker_start(total, workers, worker);
-  const int64_t end = attn_worker_start(total, workers, worker + 1);
+  const uint32_t first = attn_worker_start(total, workers, worker);
+  const uint32_t end = attn_worker_start(total, workers, worker + 1);
   const float qinv = a.q_scale_inv != nullptr ? *a.q_scale_inv : 1.0f;
   // logits in base 2: x = acc * row scale * (softmax scale / q_scale_inv * log2 e)
   const float xs = a.scale / qinv * 1.4426950408889634f;
 
-  int64_t x = first;
+  uint32_t x = first;
   while (x < end) {
-    const int t = attn_token_of(plan, a.batch, x);
-    const int64_t t0 = plan->start[t], t1 = plan->start[t + 1];
-    const int64_t seg_end = min(t1, end);
-    const int row = a.token_row != nullptr ? a.token_row[t] : t;
-    const int64_t len = a.lens[t], nv = attn_positions(a, t, false);
+    const AttnToken tok = attn_token(a, plan, x);
+    const int t = tok.t;
+    const uint32_t seg_end = min(tok.end, end);
     // ---- queries
     __syncthreads();
     for (int c = tid; c < kHeads * (kRowElems / 8); c += 256) {
@@ -146,12 +145,12 @@ __global__ void __launch_bounds__(256, 1) mla_attn_mma_kernel(const AttnArgs a) 
 #pragma unroll
     for (int n = 0; n < kNO; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
 
-    for (int64_t tile = x; tile < seg_end; ++tile) {
-      const int64_t v0 = (tile - t0) * kTile;
+    for (uint32_t tile = x; tile < seg_end; ++tile) {
+      const uint32_t v0 = (tile - tok.start) * kTile;
       __syncthreads();  // the previous tile's K and P are read
       if (tid < kTile) {
         int64_t page = 0;
-        const int64_t r = attn_row(a, t, row, nv, len, v0 + tid, &page);
+        const int64_t r = attn_row(a, tok, v0 + tid, &page);
         srow[tid] = r;
         sscale[tid] = r >= 0 ? page_scale(a.k_scale, LAYOUT, page) : 1.0f;
       }
@@ -264,7 +263,7 @@ __global__ void __launch_bounds__(256, 1) mla_attn_mma_kernel(const AttnArgs a) 
       }
     }
     // ---- the stretch is done: the output, or a partial
-    const bool whole = x == t0 && seg_end == t1;
+    const bool whole = x == tok.start && seg_end == tok.end;
     const int slot = 2 * worker + (x == first ? 0 : 1);
     const int ha = 16 * wm + g, hb = ha + 8;
     if (whole) {
@@ -303,22 +302,39 @@ __global__ void __launch_bounds__(256, 1) mla_attn_mma_kernel(const AttnArgs a) 
 // --------------------------------------------------------------- joining
 //
 // One CTA a (token, head): with M the largest maximum of the parts,
-// o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  Tokens whose context one
-// worker read whole are done already; those that look at nothing get zeros
-// and an lse of -infinity.  Bound by the parts' bytes (L2).
+// o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i, each part's factor found by a
+// thread of its own, the parts' rows summed in kJoinGroups interleaved groups
+// of 128 threads and then group after group (always the same order).  Tokens
+// whose context one worker read whole are done already; those that look at
+// nothing get zeros and an lse of -infinity.  Bound by the parts' bytes (L2).
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinGroups = 4;
+constexpr int kJoinThreads = 128 * kJoinGroups;
+
+__device__ __forceinline__ float join_reduce(float v, bool is_max, float* red) {
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float u = __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    v = is_max ? fmaxf(v, u) : v + u;
+  }
+  if ((tid & 31) == 0) red[tid >> 5] = v;
+  __syncthreads();
+  v = red[0];
+#pragma unroll
+  for (int w = 1; w < kJoinThreads / 32; ++w) v = is_max ? fmaxf(v, red[w]) : v + red[w];
+  __syncthreads();
+  return v;
+}
 
 __global__ void __launch_bounds__(kJoinThreads) mla_attn_join_kernel(const AttnArgs a) {
-  __shared__ AttnPlan plan;
-  __shared__ int64_t red[kJoinThreads / 32];
-  __shared__ float weight[2 * kMaxCtas];
-  __shared__ float4 half[kKvLora / 4];
+  __shared__ float weight[kMaxCtas];
+  __shared__ float red[kJoinThreads / 32];
+  __shared__ float4 sums[kJoinGroups - 1][kKvLora / 4];
   const int tid = threadIdx.x, t = blockIdx.y, h = blockIdx.x;
   pdl_launch_dependents();
   pdl_wait();
-  attn_make_plan(a, &plan, red, false);
-  const int64_t t0 = plan.start[t], t1 = plan.start[t + 1], total = plan.start[a.batch];
+  const uint32_t t0 = t > 0 ? a.plan[t - 1] : 0u, t1 = a.plan[t], total = a.plan[a.batch - 1];
   uint16_t* out = a.out + (int64_t)t * a.o_ts + (int64_t)h * a.o_hs;
   if (t0 == t1) {
     for (int c = 2 * tid; c < kKvLora; c += 2 * kJoinThreads) *reinterpret_cast<uint32_t*>(out + c) = 0u;
@@ -328,46 +344,47 @@ __global__ void __launch_bounds__(kJoinThreads) mla_attn_join_kernel(const AttnA
   const int workers = attn_workers(a, total);
   const int w0 = attn_worker_of(total, workers, t0), w1 = attn_worker_of(total, workers, t1 - 1);
   if (w0 == w1) return;
-  const int n = w1 - w0 + 1;
+  const int n = w1 - w0 + 1;  // at most kMaxCtas, and no more than there are threads
   // part i is worker w0 + i's; the first lies in slot 1 where that worker
   // began with another token
   const int slot0 = 2 * w0 + (attn_worker_start(total, workers, w0) < t0 ? 1 : 0);
   auto slot_of = [&](int i) { return i == 0 ? slot0 : 2 * (w0 + i); };
-  float M = -INFINITY;
-  for (int i = 0; i < n; ++i)
-    M = fmaxf(M, a.part_ml[((int64_t)slot_of(i) * a.heads_pad + h) * 2]);
-  const float m_use = M == -INFINITY ? 0.f : M;
-  float l = 0.f;
-  for (int i = 0; i < n; ++i) {
-    const float* ml = a.part_ml + ((int64_t)slot_of(i) * a.heads_pad + h) * 2;
-    const float w = ml[0] == -INFINITY ? 0.f : exp2f(ml[0] - m_use);
-    if (tid == 0) weight[i] = w;
-    l += w * ml[1];
-  }
-  __syncthreads();
-  // threads 0..127 take the even parts, 128..255 the odd ones
-  const int c = tid & 127, odd = tid >> 7;
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (tid < n)
+    ml = *reinterpret_cast<const float2*>(a.part_ml + ((int64_t)slot_of(tid) * a.heads_pad + h) * 2);
+  const float M = join_reduce(ml.x, true, red);
+  const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - (M == -INFINITY ? 0.f : M));
+  if (tid < n) weight[tid] = w;
+  const float l = join_reduce(tid < n ? w * ml.y : 0.f, false, red);  // (its barriers order weight)
+  const int c = tid & 127, group = tid >> 7;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = odd; i < n; i += 2) {
+#pragma unroll 8
+  for (int i = group; i < n; i += kJoinGroups) {
     const float4 v = *reinterpret_cast<const float4*>(
         a.part_o + ((int64_t)slot_of(i) * a.heads_pad + h) * kKvLora + 4 * c);
-    const float w = weight[i];
-    if (w != 0.f) {
-      acc.x += w * v.x;
-      acc.y += w * v.y;
-      acc.z += w * v.z;
-      acc.w += w * v.w;
+    const float f = weight[i];
+    if (f != 0.f) {
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
     }
   }
-  if (odd) half[c] = acc;
+  if (group > 0) sums[group - 1][c] = acc;
   __syncthreads();
-  if (!odd) {
-    const float4 b = half[c];
+  if (group == 0) {
+#pragma unroll
+    for (int g = 0; g < kJoinGroups - 1; ++g) {
+      const float4 b = sums[g][c];
+      acc.x += b.x;
+      acc.y += b.y;
+      acc.z += b.z;
+      acc.w += b.w;
+    }
     const float r = l == 0.f ? 0.f : 1.0f / l;
     uint2 v;
-    v.x = pack_bf16x2((acc.x + b.x) * r, (acc.y + b.y) * r);
-    v.y = pack_bf16x2((acc.z + b.z) * r, (acc.w + b.w) * r);
+    v.x = pack_bf16x2(acc.x * r, acc.y * r);
+    v.y = pack_bf16x2(acc.z * r, acc.w * r);
     *reinterpret_cast<uint2*>(out + 4 * c) = v;
     if (tid == 0 && a.lse != nullptr) a.lse[(int64_t)t * a.heads + h] = attn_lse(M, l);
   }
@@ -470,12 +487,13 @@ int mla_attn_create(mla_attn_t* out, int max_batch, int heads) {
     goto fail;
   slots = (size_t)(h->num_sms / groups) * 2 * groups * gh;
   rc = MLA_ENOMEM;
-  if (cudaMalloc(&h->err, 256) != cudaSuccess ||
+  if (cudaMalloc(&h->err, 2048) != cudaSuccess ||
       cudaMalloc(&h->part_o, slots * mla::kKvLora * sizeof(float)) != cudaSuccess ||
       cudaMalloc(&h->part_ml, slots * 2 * sizeof(float)) != cudaSuccess)
     goto fail;
   rc = MLA_ECUDA;
-  if (cudaMemset(h->err, 0, 256) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess) goto fail;
+  h->plan = h->err + 64;
+  if (cudaMemset(h->err, 0, 2048) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess) goto fail;
   *out = h;
   return MLA_OK;
 fail:
@@ -545,6 +563,7 @@ int mla_attn_decode(mla_attn_t h, int batch, const void* q_latent, int64_t ql_to
   a.part_o = h->part_o;
   a.part_ml = h->part_ml;
   a.err = h->err;
+  a.plan = h->plan;
   a.heads = h->heads;
   a.batch = batch;
   // Both kernels take 16, 32 or 64 heads a CTA by the same rule.

@@ -11,53 +11,75 @@ constexpr int kAttnMaxBatch = MLA_MAX_BATCH;
 
 // Tiles of the batch, spread evenly.  Token t's context is a list of virtual
 // positions 0 .. nv_t - 1 (its first len_t positions, or the positions of its
-// selected blocks, block after block), cut into tiles; start[t] is the number
-// of tiles before it.  Worker w of a head group takes tiles
+// selected blocks, block after block), cut into tiles; end[t] is the number of
+// tiles up to and with its own.  Worker w of a head group takes tiles
 // [w * total / workers, (w + 1) * total / workers), whatever requests they
 // belong to.  A stretch of one token's tiles that is not all of them leaves
 // the worker as a partial: its first stretch in slot 0, any other (then its
 // last) in slot 1.
 struct AttnPlan {
-  int64_t start[kAttnMaxBatch + 1];
+  uint32_t end[kAttnMaxBatch];
+  __device__ uint32_t start(int t) const { return t > 0 ? end[t - 1] : 0u; }
+};
+// Positions of one token beyond this are left out (and flagged): 256 tokens'
+// tiles stay within 31 bits.
+constexpr int64_t kAttnMaxPositions = (int64_t)1 << 29;
+
+// What a token looks at.
+struct AttnToken {
+  int t, row;
+  uint32_t start, end;  // its tiles
+  uint32_t nv;          // virtual positions
+  int32_t len;
 };
 
-// Virtual positions of token t, 0 for a token that looks at nothing.
-__device__ __forceinline__ int64_t attn_positions(const AttnArgs& a, int t, bool flag) {
-  const int64_t len = a.lens[t];
+// Virtual positions of a token, 0 for one that looks at nothing.
+__device__ __forceinline__ uint32_t attn_positions(const AttnArgs& a, int t, int32_t len, int row,
+                                                   bool flag) {
   if (len <= 0) return 0;
-  const int row = a.token_row != nullptr ? a.token_row[t] : t;
-  if (row < 0 || row >= a.table_rows) {
-    if (flag) atomicOr(a.err, MLA_DEVERR_BAD_SLOT);
-    return 0;
+  bool bad = row < 0 || row >= a.table_rows;
+  int64_t n = 0;
+  if (!bad) {
+    const int64_t cap = a.bt_stride * a.page_size;
+    if (a.sel != nullptr) {
+      n = min((int64_t)max(a.sel_count[t], 0), a.sel_stride) * a.page_size;
+    } else {
+      n = min((int64_t)len, cap);
+      bad = len > cap;
+    }
+    if (n > kAttnMaxPositions) {
+      n = kAttnMaxPositions;
+      bad = true;
+    }
   }
-  if (a.sel != nullptr) {
-    const int64_t n = min((int64_t)max(a.sel_count[t], 0), a.sel_stride);
-    return n * a.page_size;
-  }
-  const int64_t cap = a.bt_stride * a.page_size;
-  if (len > cap && flag) atomicOr(a.err, MLA_DEVERR_BAD_SLOT);
-  return min(len, cap);
+  if (bad && flag) atomicOr(a.err, MLA_DEVERR_BAD_SLOT);
+  return (uint32_t)n;
 }
 
 // Fills the plan; all threads of the block call it (at least 256 of them, a
-// multiple of 32), and may read it after the closing barrier.
-__device__ __forceinline__ void attn_make_plan(const AttnArgs& a, AttnPlan* p, int64_t* red,
+// multiple of 32), and may read it after the closing barrier.  red: 8 words.
+__device__ __forceinline__ void attn_make_plan(const AttnArgs& a, AttnPlan* p, uint32_t* red,
                                                bool flag) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t n = 0;
-  if (tid < a.batch) n = (attn_positions(a, tid, flag) + a.tile - 1) / a.tile;
-  int64_t inc = n;
+  uint32_t n = 0;
+  if (tid < a.batch) {
+    const int32_t len = a.lens[tid];
+    const int row = a.token_row != nullptr ? a.token_row[tid] : tid;
+    n = (attn_positions(a, tid, len, row, flag) + a.tile - 1) / a.tile;
+  }
+  uint32_t inc = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
     if (lane >= o) inc += x;
   }
   if (lane == 31 && warp < kAttnMaxBatch / 32) red[warp] = inc;
   __syncthreads();
   if (tid < kAttnMaxBatch) {
     for (int w = 0; w < warp; ++w) inc += red[w];
-    if (tid < a.batch) p->start[tid + 1] = inc;
-    if (tid == 0) p->start[0] = 0;
+    p->end[tid] = inc;
+    // one CTA leaves the plan for the kernel that joins the parts
+    if (flag) a.plan[tid] = inc;
   }
   __syncthreads();
 }
@@ -65,43 +87,53 @@ __device__ __forceinline__ void attn_make_plan(const AttnArgs& a, AttnPlan* p, i
 // Workers with work: no more than there are tiles, so that every one of them
 // has a tile, and every worker between the first and the last of a token
 // leaves a part of it.
-__device__ __forceinline__ int attn_workers(const AttnArgs& a, int64_t total) {
-  return (int)min((int64_t)a.workers, total);
+__device__ __forceinline__ int attn_workers(const AttnArgs& a, uint32_t total) {
+  return (int)min((uint32_t)a.workers, total);
 }
-__device__ __forceinline__ int64_t attn_worker_start(int64_t total, int workers, int w) {
-  return total * w / workers;
+__device__ __forceinline__ uint32_t attn_worker_start(uint32_t total, int workers, int w) {
+  return (uint32_t)((uint64_t)total * w / workers);
 }
 // The worker whose range holds tile x: the largest w with start(w) <= x.
-__device__ __forceinline__ int attn_worker_of(int64_t total, int workers, int64_t x) {
-  return (int)(((x + 1) * workers - 1) / total);
+__device__ __forceinline__ int attn_worker_of(uint32_t total, int workers, uint32_t x) {
+  return (int)((((uint64_t)x + 1) * workers - 1) / total);
 }
 
-// The token of tile x: the last t with start[t] <= x (tokens without tiles
-// are passed over).
-__device__ __forceinline__ int attn_token_of(const AttnPlan* p, int batch, int64_t x) {
-  int lo = 0, hi = batch;
-  while (hi - lo > 1) {
+// The token of tile x: the first t with end[t] > x.
+__device__ __forceinline__ int attn_token_of(const AttnPlan* p, int batch, uint32_t x) {
+  int lo = 0, hi = batch - 1;
+  while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (p->start[mid] <= x)
-      lo = mid;
-    else
+    if (p->end[mid] > x)
       hi = mid;
+    else
+      lo = mid + 1;
   }
   return lo;
 }
+__device__ __forceinline__ AttnToken attn_token(const AttnArgs& a, const AttnPlan* p, uint32_t x) {
+  AttnToken k;
+  k.t = attn_token_of(p, a.batch, x);
+  k.start = p->start(k.t);
+  k.end = p->end[k.t];
+  k.row = a.token_row != nullptr ? a.token_row[k.t] : k.t;
+  k.len = a.lens[k.t];
+  k.nv = attn_positions(a, k.t, k.len, k.row, false);
+  return k;
+}
 
-// The cache row (page * page_size + offset) of virtual position v of token t,
-// or -1 where the position does not count; *page receives the page.
-__device__ __forceinline__ int64_t attn_row(const AttnArgs& a, int t, int row, int64_t nv, int64_t len,
-                                            int64_t v, int64_t* page) {
-  if (v >= nv) return -1;
-  int64_t j = v / a.page_size;
-  const int off = (int)(v - j * a.page_size);
+// The cache row (page * page_size + offset) of virtual position v, or -1 where
+// the position does not count; *page receives the page.
+__device__ __forceinline__ int64_t attn_row(const AttnArgs& a, const AttnToken& k, uint32_t v,
+                                            int64_t* page) {
+  if (v >= k.nv) return -1;
+  const uint32_t b = v / (uint32_t)a.page_size;
+  const int off = (int)(v - b * (uint32_t)a.page_size);
+  int64_t j = b;
   if (a.sel != nullptr) {
-    j = a.sel[(int64_t)t * a.sel_stride + j];
-    if (j < 0 || j >= a.bt_stride || j * a.page_size + off >= len) return -1;
+    j = a.sel[(int64_t)k.t * a.sel_stride + b];
+    if (j < 0 || j >= a.bt_stride || j * a.page_size + off >= k.len) return -1;
   }
-  const int64_t p = a.table[(int64_t)row * a.bt_stride + j];
+  const int64_t p = a.table[(int64_t)k.row * a.bt_stride + j];
   if (p < 0 || p >= a.num_pages) {
     atomicOr(a.err, MLA_DEVERR_BAD_SLOT);
     return -1;

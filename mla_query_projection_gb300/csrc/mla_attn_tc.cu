@@ -25,9 +25,11 @@
 // only when a weight would leave E4M3's range, so most tiles need no
 // reduction across lanes at all.
 //
-// Shared-memory reads of the tensor core bound a tile (N = 64 heads: 18 MMAs of
-// 8 KiB for S, 32 of 6 KiB for O, at 128 B a cycle), next to HBM's share of
-// 73.7 KiB a tile.
+// Two tiles' planes are in shared memory: while one tile's softmax runs, the
+// tensor core works on the O of the tile before and the S of the one behind.
+// Shared-memory reads of the tensor core bound a tile (64 heads: 18 MMAs of
+// 8 KiB for S and 32 of 6 KiB for O at 128 B a cycle, 2700 cycles), next to
+// HBM's share of 73.7 KiB a tile.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -48,35 +50,31 @@ constexpr long long kTcWait = 2000000000LL;  // ~1 s of SM clock
 // Weights are kept times 2^7, and the reference moves when a logit (base 2)
 // passes it by more than 1.75: 2^8.75 = 430 < 448, E4M3's largest.
 constexpr float kPShift = 7.0f, kPRoom = 1.75f;
-constexpr float kNoMax = -1.0e30f;         // the reference before any key
 
 template <int NH, bool FP8Q>
 struct TcSmem {
   static constexpr int kQRows = FP8Q ? NH : 2 * NH;  // MMA N of S^T
   static constexpr int kQPlane = kQRows * 128;
-  static constexpr int oQ = 0;                        // 4 latent planes
-  static constexpr int oQr = oQ + 4 * kQPlane;        // rope plane, 64-byte rows
-  static constexpr int oP = ((oQr + kQRows * 64 + 1023) / 1024) * 1024;  // [row][hi | lo] 128 B
-  static constexpr int oRing = oP + kPlane;
-  static constexpr int kSlots = (232448 - 1024 - 6144 - oRing) / kPlane > 11 ? 11 : (232448 - 1024 - 6144 - oRing) / kPlane;
-  static constexpr int oBar = oRing + kSlots * kPlane;
-  // full[slots] empty[slots] s_full[2] s_free[2] p_full pv_done q_full drain
-  static constexpr int kBars = 2 * kSlots + 8;
-  static constexpr int oMax = (oBar + kBars * 8 + 15) & ~15;  // reference [NH], read as float4
-  static constexpr int oAlpha = oMax + NH * 4;        // its rescale factors [NH]
-  static constexpr int oXs = oAlpha + NH * 4;         // logit scale of a head's accumulators [NH]
-  static constexpr int oRed = oXs + NH * 4;           // [4][NH] across the quadrants
-  static constexpr int oRef = oRed + 4 * NH * 4;      // value scale: [0] reference, [1] its ratio, [4..7] warp maxima
-  static constexpr int oPlan = (oRef + 48 + 7) & ~7;
-  static constexpr int oScan = oPlan + (int)sizeof(AttnPlan);
-  static constexpr int oTmem = oScan + 64;
-  static constexpr int kBytes = oTmem + 16;
-  static constexpr int kAlloc = kBytes + 1024;        // the base is aligned up to 1 KiB
-  static_assert(kAlloc <= 232448, "shared memory budget");
-  static_assert(kSlots >= 8, "a tile's planes beside the previous tile's");
-  static_assert(oP % 1024 == 0 && oRing % 1024 == 0 && oQr % 512 == 0 && kQPlane % 1024 == 0 &&
-                    oBar % 8 == 0 && oMax % 16 == 0 && oAlpha % 16 == 0 && oXs % 16 == 0 &&
-                    oRed % 16 == 0 && oPlan % 8 == 0 && oScan % 8 == 0 && oTmem % 4 == 0,
+  static constexpr int oRing = 0;                      // [2 tiles][4 latent planes]
+  static constexpr int oRope = oRing + 8 * kPlane;     // one rope plane, 64-byte rows
+  static constexpr int oP = oRope + kPlane / 2;        // [row][hi | lo] 128 B
+  static constexpr int oQ = oP + kPlane;               // 4 latent planes
+  static constexpr int oQr = oQ + 4 * kQPlane;         // rope plane, 64-byte rows
+  static constexpr int oRef = oQr + kQRows * 64;       // reference less 7, base 2 [NH]
+  static constexpr int oXs = oRef + NH * 4;            // logit scale of a head's accumulators [NH]
+  static constexpr int oRed = oXs + NH * 4;            // [4][NH] across the quadrants; [0][.] factors
+  static constexpr int oVref = oRed + 4 * NH * 4;      // value scale: reference, its ratio, [4..7] warp maxima
+  static constexpr int oBar = oVref + 32;
+  // full[8] empty[8] rope_full rope_empty s_full[2] s_free[2] p_full pv_done q_full drain
+  static constexpr int kBars = 26;
+  static constexpr int oPlan = oBar + kBars * 8;
+  static constexpr int oScan = oRed;                   // before the first tile
+  static constexpr int oTmem = oPlan + (int)sizeof(AttnPlan);
+  static constexpr int kBytes = oTmem + 8;
+  static_assert(kBytes <= 232448, "shared memory budget");
+  static_assert(oP % 1024 == 0 && oQ % 1024 == 0 && oRope % 1024 == 0 && oQr % 512 == 0 &&
+                    kQPlane % 1024 == 0 && oRef % 16 == 0 && oXs % 16 == 0 && oRed % 16 == 0 &&
+                    oBar % 8 == 0 && oPlan % 8 == 0 && oTmem % 4 == 0,
                 "alignment");
 };
 
@@ -100,19 +98,25 @@ __host__ __device__ constexpr uint32_t tc_idesc(int m, int n, int btype, bool a_
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+// One elected lane of a converged warp issues; the warp runs the code around it
+// together, so that descriptors are computed in uniform registers (issued from
+// a single lane's branch, an MMA cost about 100 cycles to issue against the
+// 48 to 64 that it takes to run).
 __device__ __forceinline__ void tc_mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                           uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xFFFFFFFF;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_u32(bar))
-               : "memory");
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
 }
 __device__ __forceinline__ void tc_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -127,40 +131,91 @@ __device__ __forceinline__ void tc_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// This warp's 32 lanes x 8 columns.  The loads need tc_wait_ld before use.
-__device__ __forceinline__ void tc_ld8(uint32_t addr, float* v) {
-  uint32_t r[8];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                 "=r"(r[6]), "=r"(r[7])
-               : "r"(addr));
+// This warp's 32 lanes x 8, 16 or 32 columns.  A load's values may be used
+// after tc_wait_ld and tc_landed (the compiler sees no other tie between the
+// wait and the registers that the loads fill).
+#define TC_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), \
+                    "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+#define TC_I8(v, i) "r"(__float_as_uint(v[i])), "r"(__float_as_uint(v[i + 1])), \
+                    "r"(__float_as_uint(v[i + 2])), "r"(__float_as_uint(v[i + 3])), \
+                    "r"(__float_as_uint(v[i + 4])), "r"(__float_as_uint(v[i + 5])), \
+                    "r"(__float_as_uint(v[i + 6])), "r"(__float_as_uint(v[i + 7]))
+template <int N>
+__device__ __forceinline__ void tc_ld(uint32_t addr, float (&v)[N]) {
+  uint32_t r[N];
+  if constexpr (N == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : TC_R8(r, 0)
+                 : "r"(addr));
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : TC_R8(r, 0), TC_R8(r, 8)
+        : "r"(addr));
+  } else {
+    static_assert(N == 32, "columns");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : TC_R8(r, 0), TC_R8(r, 8), TC_R8(r, 16), TC_R8(r, 24)
+        : "r"(addr));
+  }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tc_st8(uint32_t addr, const float* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
-               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-               "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-               "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
-               : "memory");
+__device__ __forceinline__ void tc_st32(uint32_t addr, const float (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      TC_I8(v, 0), TC_I8(v, 8), TC_I8(v, 16), TC_I8(v, 24)
+      : "memory");
 }
-// After tc_wait_ld: the values may be used from here on (the compiler sees no
-// other tie between the wait and the registers that the loads fill).
 template <int N>
 __device__ __forceinline__ void tc_landed(float (&v)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
-template <int N>
-__device__ __forceinline__ void tc_ld(uint32_t addr, float (&v)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; i += 8) tc_ld8(addr + i, v + i);
+
+// Packed FP32 pairs (one instruction for two sums or products).
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mov.b64 rc, {%6, %7};\n\tfma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+// 2^x by the hardware's approximation (2 ulp), subnormal results flushed.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// Two FP32 -> two E5M2 codes, round to nearest even, saturating.
-__device__ __forceinline__ uint16_t e5m2x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+// A weight pair as the sum of two terms: E4M3 codes in the low half of the
+// result, E5M2 codes of the rest in the high half.  The pair is rounded to
+// FP16 first (2^-11, below the terms' 2^-7; FP16 reaches down to 2^-24, further
+// than E5M2).
+__device__ __forceinline__ uint32_t split_weights(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 p, g, d;\n\t.reg .b16 c, e;\n\t"
+      "cvt.rn.f16x2.f32 p, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 c, p;\n\t"
+      "cvt.rn.f16x2.e4m3x2 g, c;\n\t"
+      "sub.rn.f16x2 d, p, g;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 e, d;\n\t"
+      "mov.b32 %0, {c, e};\n\t}"
+      : "=r"(r)
+      : "f"(lo), "f"(hi));
   return r;
 }
 
@@ -218,55 +273,162 @@ __device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, bool& de
   if (!dead && !mbar_wait_bounded(bar, parity, kTcWait)) dead = true;
 }
 
+// The same by a converged warp: its lanes go on together.
+__device__ __forceinline__ void tc_wait_warp(uint64_t* bar, uint32_t parity, bool& dead) {
+  tc_wait(bar, parity, dead);
+  dead = __any_sync(0xFFFFFFFFu, dead);
+}
+
 struct TcMaps {
   CUtensorMap latent;  // boxes of box_rows x 128 bytes, 128-byte swizzle
   CUtensorMap rope;    // boxes of box_rows x 64 bytes, 64-byte swizzle
   int box_rows;        // a power of two that divides the page, 8..128
 };
 
+// One token's queries of NH heads into shared memory as E4M3 terms (B of S^T):
+// warp w takes heads w, w + 8, ..; a lane holds 16 latent columns of each, and
+// lane 4 r + c the rope columns 16 c .. of the warp's r-th head.  Every load is
+// issued before the first is used.  xs[h] turns head h's accumulators into
+// logits in base 2 (`logit` times the inverse of its power of two).
+template <int NH, bool FP8Q>
+__device__ __forceinline__ void tc_queries(const AttnArgs& a, uint8_t* smem, int t, int h0, int warp,
+                                           int lane, float logit, float* xs) {
+  using S = TcSmem<NH, FP8Q>;
+  constexpr int kN = NH / 8;  // heads a warp
+  constexpr int kV = FP8Q ? 1 : 2;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 lat[kN][kV], rope[kV];
+#pragma unroll
+  for (int r = 0; r < kN; ++r) {
+    const int h = h0 + warp + 8 * r;
+    const int64_t e = (int64_t)t * a.ql_ts + (int64_t)h * a.ql_hs + 16 * lane;
+    const uint4* p = reinterpret_cast<const uint4*>(a.q_latent + e * (FP8Q ? 1 : 2));
+#pragma unroll
+    for (int v = 0; v < kV; ++v) lat[r][v] = h < a.heads ? p[v] : zero;
+  }
+  {
+    const int r = lane >> 2, h = h0 + warp + 8 * r;
+    const int64_t e = (int64_t)t * a.qp_ts + (int64_t)h * a.qp_hs + 16 * (lane & 3);
+    const uint4* p = reinterpret_cast<const uint4*>(a.q_pe + e * (FP8Q ? 1 : 2));
+#pragma unroll
+    for (int v = 0; v < kV; ++v) rope[v] = r < kN && h < a.heads ? p[v] : zero;
+  }
+  auto put = [&](int row, uint4 w) {  // latent chunk `lane` of a B row
+    *reinterpret_cast<uint4*>(smem + S::oQ + (lane >> 3) * S::kQPlane + row * 128 +
+                              (((lane ^ row) & 7) << 4)) = w;
+  };
+  auto put_rope = [&](int row, uint4 w) {  // rope chunk lane % 4
+    *reinterpret_cast<uint4*>(smem + S::oQr + row * 64 + ((((lane & 3) ^ (row >> 1)) & 3) << 4)) = w;
+  };
+  const int rr = lane >> 2, rh = warp + 8 * rr;  // the head whose rope this lane holds
+  if constexpr (FP8Q) {
+#pragma unroll
+    for (int r = 0; r < kN; ++r) put(warp + 8 * r, lat[r][0]);
+    if (rr < kN) put_rope(rh, rope[0]);
+    if (lane < kN) xs[warp + 8 * lane] = logit;
+  } else {
+    // magnitudes as bits order like the values (NaN above infinity)
+    auto magnitude = [](uint4 w) {
+      uint32_t m = 0;
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m = max(m, max(ww[k] & 0x7FFFu, (ww[k] >> 16) & 0x7FFFu));
+      return m;
+    };
+    // 16 columns as their two E4M3 terms, scaled by a power of two
+    auto split = [](const uint4* w, float up, uint4* hi, uint4* lo) {
+      uint32_t c[4], d[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint4 q = w[e >> 1];
+        const uint32_t x = e & 1 ? q.z : q.x, y = e & 1 ? q.w : q.y;
+        const float f0 = bf16lo(x) * up, f1 = bf16hi(x) * up, f2 = bf16lo(y) * up, f3 = bf16hi(y) * up;
+        const uint16_t a0 = e4m3x2(f0, f1), a1 = e4m3x2(f2, f3);
+        const float2 g0 = e4m3x2_value(a0), g1 = e4m3x2_value(a1);
+        c[e] = (uint32_t)a0 | ((uint32_t)a1 << 16);
+        d[e] = (uint32_t)e4m3x2(f0 - g0.x, f1 - g0.y) | ((uint32_t)e4m3x2(f2 - g1.x, f3 - g1.y) << 16);
+      }
+      *hi = make_uint4(c[0], c[1], c[2], c[3]);
+      *lo = make_uint4(d[0], d[1], d[2], d[3]);
+    };
+    const uint32_t rope_mag = max(magnitude(rope[0]), magnitude(rope[kV - 1]));
+    float rope_up = 0.f;
+#pragma unroll
+    for (int r = 0; r < kN; ++r) {
+      uint32_t m = max(magnitude(lat[r][0]), magnitude(lat[r][kV - 1]));
+      if (rr == r) m = max(m, rope_mag);
+      m = __reduce_max_sync(0xFFFFFFFFu, m);
+      // the power of two that brings the largest into (224, 448]: from its
+      // exponent field, kept where both it and its inverse are normal
+      int ex = (int)(m >> 7) - 127;
+      ex = max(-100, min(ex, 126));
+      if ((m & 0x7Fu) <= 0x60u) --ex;
+      const float up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
+      float x = logit * __uint_as_float((uint32_t)(127 - 7 + ex) << 23);
+      // an infinite query: no finite logits (E4M3 has no infinity)
+      if (m >= 0x7F80u) x = __int_as_float(0x7FC00000);
+      uint4 hi, lo;
+      split(lat[r], up, &hi, &lo);
+      put(warp + 8 * r, hi);
+      put(NH + warp + 8 * r, lo);
+      if (lane == 0) xs[warp + 8 * r] = x;
+      if (rr == r) rope_up = up;
+    }
+    if (rr < kN) {
+      uint4 hi, lo;
+      split(rope, rope_up, &hi, &lo);
+      put_rope(rh, hi);
+      put_rope(NH + rh, lo);
+    }
+  }
+}
+
 template <int NH, bool FP8Q, int LAYOUT>
 __global__ void __launch_bounds__(kTcThreads, 1)
     mla_attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
   using S = TcSmem<NH, FP8Q>;
-  constexpr int kSlots = S::kSlots;
   constexpr int kHalf = NH / 2;  // heads a softmax thread handles
   constexpr bool kPaged = LAYOUT == MLA_KV_FP8_E4M3_PAGE;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::oBar);
-  uint64_t* empty = full + kSlots;
-  uint64_t* s_full = empty + kSlots;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::oBar);  // [2][4]
+  uint64_t* empty = full + 8;
+  uint64_t* rope_full = empty + 8;
+  uint64_t* rope_empty = rope_full + 1;
+  uint64_t* s_full = rope_empty + 1;
   uint64_t* s_free = s_full + 2;
   uint64_t* p_full = s_free + 2;
   uint64_t* pv_done = p_full + 1;
   uint64_t* q_full = pv_done + 1;
   uint64_t* drain = q_full + 1;
-  float* ref_max = reinterpret_cast<float*>(smem + S::oMax);
-  float* alpha = reinterpret_cast<float*>(smem + S::oAlpha);
+  float* ref = reinterpret_cast<float*>(smem + S::oRef);
   float* xs = reinterpret_cast<float*>(smem + S::oXs);
   float* red = reinterpret_cast<float*>(smem + S::oRed);
-  float* vref = reinterpret_cast<float*>(smem + S::oRef);
+  float* vref = reinterpret_cast<float*>(smem + S::oVref);
   AttnPlan* plan = reinterpret_cast<AttnPlan*>(smem + S::oPlan);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + S::oTmem);
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const int group = blockIdx.x % a.groups, worker = blockIdx.x / a.groups;
   const int h0 = group * NH;
   if (tid == 0) {
-    for (int s = 0; s < kSlots; ++s) {
+    for (int s = 0; s < 8; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
+    mbar_init(rope_full, 1);
+    mbar_init(rope_empty, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&s_full[b], 1);
-      mbar_init(&s_free[b], kTcSoft);
+      mbar_init(&s_free[b], kTcSoft / 32);
     }
-    mbar_init(p_full, kTcSoft);
+    mbar_init(p_full, kTcSoft / 32);
     mbar_init(pv_done, 1);
-    mbar_init(q_full, kTcSoft);
+    mbar_init(q_full, kTcSoft / 32);
     mbar_init(drain, 1);
     mbar_fence_init();
+    // the swizzles go by address bits: the base is a multiple of 1 KiB
+    if (smem_u32(smem) & 1023u) atomicOr(a.err, MLA_DEVERR_CHECK);
   }
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -283,156 +445,136 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   pdl_wait();
   tc_before();
   // (the plan's barriers order the set-up above)
-  attn_make_plan(a, plan, reinterpret_cast<int64_t*>(smem + S::oScan), blockIdx.x == 0);
+  attn_make_plan(a, plan, reinterpret_cast<uint32_t*>(smem + S::oScan), blockIdx.x == 0);
   tc_after();
   const uint32_t tmem = *tslot;  // S^T buffers at columns 0 and 128, O^T planes from 256
-  const int64_t total = plan->start[a.batch];
+  const uint32_t total = plan->end[a.batch - 1];
   const int workers = attn_workers(a, total);
-  const int64_t first = worker < workers ? attn_worker_start(total, workers, worker) : 0;
-  const int64_t end = worker < workers ? attn_worker_start(total, workers, worker + 1) : 0;
+  const uint32_t first = worker < workers ? attn_worker_start(total, workers, worker) : 0;
+  const uint32_t end = worker < workers ? attn_worker_start(total, workers, worker + 1) : 0;
   bool dead = false;
 
   if (warp == 8) {
     // ================= TMA: a tile's planes in the order rope, 0, 1, 2, 3
     const int boxes = kTcTile / maps.box_rows;
     const int32_t no_row = (int32_t)(a.num_pages * a.page_size);  // past the end: zeros
-    int n = 0;  // planes so far
-    int64_t x = first;
+    int i = 0, issued = 0;  // tiles, planes
+    uint32_t x = first;
     while (x < end && !dead) {
-      const int t = attn_token_of(plan, a.batch, x);
-      const int64_t t0 = plan->start[t], seg_end = min(plan->start[t + 1], end);
-      const int row = a.token_row != nullptr ? a.token_row[t] : t;
-      const int64_t len = a.lens[t], nv = attn_positions(a, t, false);
-      for (int64_t tile = x; tile < seg_end && !dead; ++tile) {
+      const AttnToken k = attn_token(a, plan, x);
+      const uint32_t seg_end = min(k.end, end);
+      for (; x < seg_end && !dead; ++x, ++i) {
         int32_t y = no_row;
         if (lane < boxes) {
           int64_t page;
-          const int64_t r =
-              attn_row(a, t, row, nv, len, (tile - t0) * kTcTile + lane * maps.box_rows, &page);
+          const int64_t r = attn_row(a, k, (x - k.start) * kTcTile + lane * maps.box_rows, &page);
           if (r >= 0) y = (int32_t)r;
         }
-        for (int p = 0; p < 5; ++p, ++n) {
-          const int slot = n % kSlots;
-          if (n >= kSlots) tc_wait(&empty[slot], (uint32_t)((n / kSlots - 1) & 1), dead);
-          dead = __any_sync(0xFFFFFFFFu, dead);
+        const int b = i & 1;
+#pragma unroll 1
+        for (int p = 0; p < 5; ++p) {
+          uint64_t* f = p == 0 ? rope_full : &full[4 * b + p - 1];
+          uint64_t* e = p == 0 ? rope_empty : &empty[4 * b + p - 1];
+          if (p == 0 ? i >= 1 : i >= 2)
+            tc_wait_warp(e, (uint32_t)((p == 0 ? i - 1 : i / 2 - 1) & 1), dead);
           if (dead) break;
-          if (lane == 0) mbar_arrive_expect_tx(&full[slot], p == 0 ? kPlane / 2 : kPlane);
+          ++issued;
+          if (lane == 0) mbar_arrive_expect_tx(f, p == 0 ? kPlane / 2 : kPlane);
           __syncwarp();
-          uint8_t* dst = smem + S::oRing + slot * kPlane;
           if (lane < boxes) {
             if (p == 0)
-              tma_g2s_2d(dst + lane * maps.box_rows * 64, &maps.rope, kKvLora, y, &full[slot]);
+              tma_g2s_2d(smem + S::oRope + lane * maps.box_rows * 64, &maps.rope, kKvLora, y, f);
             else
-              tma_g2s_2d(dst + lane * maps.box_rows * 128, &maps.latent, 128 * (p - 1), y, &full[slot]);
+              tma_g2s_2d(smem + S::oRing + (4 * b + p - 1) * kPlane + lane * maps.box_rows * 128,
+                         &maps.latent, 128 * (p - 1), y, f);
           }
         }
       }
-      x = seg_end;
     }
-    // every copy has landed before the CTA may leave
-    for (int k = n > kSlots ? n - kSlots : 0; k < n; ++k)
-      (void)mbar_wait_bounded(&full[k % kSlots], (uint32_t)((k / kSlots) & 1), kTcWait);
+    // A wait ran out: the planes issued last land before the CTA leaves.
+    // (Otherwise the MMAs have read them all.)
+    if (dead && issued > 0) {
+      (void)mbar_wait_bounded(rope_full, (uint32_t)(((issued - 1) / 5) & 1), kTcWait);
+      for (int s = 0; s < 8; ++s) {
+        const int b = s >> 2, n = issued - 2 - (s & 3);  // planes up to this one of some tile
+        int last = n >= 0 ? n / 5 : -1;
+        if (last >= 0 && (last & 1) != b) --last;
+        if (last >= 0) (void)mbar_wait_bounded(&full[s], (uint32_t)((last >> 1) & 1), kTcWait);
+      }
+    }
   } else if (warp == 9) {
-    // ================= MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id_s = tc_idesc(128, S::kQRows, 0, false, false);
-      constexpr uint32_t id_hi = tc_idesc(128, NH, 0, true, true);
-      constexpr uint32_t id_lo = tc_idesc(128, NH, 1, true, true);
-      const uint64_t dk = tc_desc(smem_u32(smem + S::oRing), 1024, 2);   // planes, K- or M-major
-      const uint64_t dkr = tc_desc(smem_u32(smem + S::oRing), 512, 4);   // rope planes
-      const uint64_t dq = tc_desc(smem_u32(smem + S::oQ), 1024, 2);
-      const uint64_t dqr = tc_desc(smem_u32(smem + S::oQr), 512, 4);
-      const uint64_t dp = tc_desc(smem_u32(smem + S::oP), 1024, 2);
-      int i = 0;        // tiles so far
-      int segs = 0;
-      int prev_n = -1;  // first plane of the tile whose PV is still due
-      bool prev_first = false;
-      // S^T of a tile, planes [p0, p1) of rope, 0, 1, 2, 3
-      auto qk = [&](int n, int b, int p0, int p1) {
-        for (int p = p0; p < p1; ++p) {
-          const int slot = (n + p) % kSlots;
-          tc_wait(&full[slot], (uint32_t)(((n + p) / kSlots) & 1), dead);
-          if (dead) return;
-          tc_after();
-          const uint32_t d = tmem + 128 * b;
-          if (p == 0) {
-            const uint64_t da = dkr + (uint64_t)(slot * (kPlane >> 4));
-            tc_mma_f8(d, da, dqr, id_s, 0u);
-            tc_mma_f8(d, da + 2, dqr + 2, id_s, 1u);
-            tc_commit(&empty[slot]);
-          } else {
-            const uint64_t da = dk + (uint64_t)(slot * (kPlane >> 4));
-            const uint64_t db = dq + (uint64_t)((p - 1) * (S::kQPlane >> 4));
+    // ================= MMA issuer (the warp together, one elected lane issues)
+    constexpr uint32_t id_s = tc_idesc(128, S::kQRows, 0, false, false);
+    constexpr uint32_t id_hi = tc_idesc(128, NH, 0, true, true);
+    constexpr uint32_t id_lo = tc_idesc(128, NH, 1, true, true);
+    const uint64_t dk = tc_desc(smem_u32(smem + S::oRing), 1024, 2);  // planes, K- or M-major
+    const uint64_t dkr = tc_desc(smem_u32(smem + S::oRope), 512, 4);  // rope plane
+    const uint64_t dq = tc_desc(smem_u32(smem + S::oQ), 1024, 2);
+    const uint64_t dqr = tc_desc(smem_u32(smem + S::oQr), 512, 4);
+    const uint64_t dp = tc_desc(smem_u32(smem + S::oP), 1024, 2);
+    constexpr uint64_t kPl = kPlane >> 4, kQPl = S::kQPlane >> 4;
+    // O^T += V^T P^T of tile n, the first of its stretch or not
+    auto pv = [&](int n, bool fresh) {
+      tc_wait_warp(p_full, (uint32_t)(n & 1), dead);
+      tc_after();
+      if (dead) return;
+      const int b = n & 1;
+      const uint64_t da = dk + (uint64_t)b * 4 * kPl;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) tc_mma_f8(d, da + 2 * k, db + 2 * k, id_s, 1u);
-          }
-        }
-      };
-      // O^T planes [j0, j1) of the previous tile
-      auto pv = [&](int j0, int j1) {
-        if (j0 == 0) {
-          tc_wait(p_full, (uint32_t)((i - 1) & 1), dead);
-          tc_after();
-        }
-        if (dead) return;
-        for (int j = j0; j < j1; ++j) {
-          const int slot = (prev_n + 1 + j) % kSlots;
-          const uint64_t da = dk + (uint64_t)(slot * (kPlane >> 4));
-          const uint32_t d = tmem + 256 + NH * j;
+      for (int j = 0; j < 4; ++j) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            // 32 rows a step: 4096 bytes of V and of P; P's second term 64 bytes on
-            tc_mma_f8(d, da + 256 * k, dp + 256 * k, id_hi, (k > 0 || !prev_first) ? 1u : 0u);
-            tc_mma_f8(d, da + 256 * k, dp + 256 * k + 4, id_lo, 1u);
-          }
-          tc_commit(&empty[slot]);
+        for (int k = 0; k < 4; ++k) {
+          // 32 rows a step: 4096 bytes of V and of P; P's second term 64 bytes on
+          tc_mma_f8(tmem + 256 + NH * j, da + j * kPl + 256 * k, dp + 256 * k, id_hi,
+                    k > 0 ? 1u : (uint32_t)!fresh);
+          tc_mma_f8(tmem + 256 + NH * j, da + j * kPl + 256 * k, dp + 256 * k + 4, id_lo, 1u);
         }
-        if (j1 == 4) {
-          tc_commit(pv_done);
-          prev_n = -1;
-        }
-      };
-      int64_t x = first;
-      while (x < end && !dead) {
-        const int t = attn_token_of(plan, a.batch, x);
-        const int64_t seg_end = min(plan->start[t + 1], end);
-        for (int64_t tile = x; tile < seg_end && !dead; ++tile, ++i) {
-          const int n = 5 * i, b = i & 1;
-          const bool first_tile = tile == x;
-          if (first_tile) {
-            if (prev_n >= 0) pv(0, 4);  // its softmax must finish before the queries change
-            tc_wait(q_full, (uint32_t)(segs & 1), dead);
-            tc_after();
-          }
-          if (i >= 2) {
-            tc_wait(&s_free[b], (uint32_t)((i / 2 - 1) & 1), dead);
-            tc_after();
-          }
-          if (dead) break;
-          // With eight slots the previous tile's four latent planes leave room
-          // for four of this tile's: its last comes once PV has freed one.
-          if (prev_n >= 0 && kSlots < 9) {
-            qk(n, b, 0, 4);
-            pv(0, 1);
-            qk(n, b, 4, 5);
-            if (!dead) tc_commit(&s_full[b]);
-            pv(1, 4);
-          } else {
-            qk(n, b, 0, 5);
-            if (!dead) tc_commit(&s_full[b]);
-            if (prev_n >= 0) pv(0, 4);
-          }
-          prev_n = n;
-          prev_first = first_tile;
-        }
-        ++segs;
-        x = seg_end;
+        tc_commit(&empty[4 * b + j]);
       }
-      if (prev_n >= 0 && !dead) pv(0, 4);
-      if (dead) {  // let what was issued finish before TMEM is freed
-        tc_commit(drain);
-        (void)mbar_wait_bounded(drain, 0u, kTcWait);
+      tc_commit(pv_done);
+    };
+    int i = 0, segs = 0;
+    bool due = false, due_fresh = false;  // the previous tile's PV
+    uint32_t x = first;
+    while (x < end && !dead) {
+      const uint32_t seg_end = min(plan->end[attn_token_of(plan, a.batch, x)], end);
+      bool fresh = true;
+      for (; x < seg_end && !dead; ++x, ++i) {
+        const int b = i & 1;
+        if (fresh) {
+          if (due) pv(i - 1, due_fresh);  // its softmax must finish before the queries change
+          due = false;
+          tc_wait_warp(q_full, (uint32_t)(segs & 1), dead);
+        }
+        if (i >= 2) tc_wait_warp(&s_free[b], (uint32_t)((i / 2 - 1) & 1), dead);
+        tc_wait_warp(rope_full, (uint32_t)(i & 1), dead);
+        tc_after();
+        if (dead) break;
+        const uint32_t d = tmem + 128 * b;
+        tc_mma_f8(d, dkr, dqr, id_s, 0u);
+        tc_mma_f8(d, dkr + 2, dqr + 2, id_s, 1u);
+        tc_commit(rope_empty);
+        const uint64_t da = dk + (uint64_t)b * 4 * kPl;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          tc_wait_warp(&full[4 * b + j], (uint32_t)((i >> 1) & 1), dead);
+          tc_after();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma_f8(d, da + j * kPl + 2 * k, dq + j * kQPl + 2 * k, id_s, 1u);
+        }
+        tc_commit(&s_full[b]);
+        if (due) pv(i - 1, due_fresh);
+        due = true;
+        due_fresh = fresh;
+        fresh = false;
       }
+      ++segs;
+    }
+    if (due && !dead) pv(i - 1, due_fresh);
+    if (dead) {  // let what was issued finish before TMEM is freed
+      tc_commit(drain);
+      (void)mbar_wait_bounded(drain, 0u, kTcWait);
     }
   } else {
     // ================= softmax, rescaling, epilogue (warps 0-7)
@@ -441,111 +583,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int pos = 32 * quad + lane;    // this thread's row of a tile
     const int hb = half * kHalf;         // its heads
     const float qinv = a.q_scale_inv != nullptr ? *a.q_scale_inv : 1.0f;
-    const float logit = a.scale / qinv * 1.4426950408889634f;
     const float tensor_scale = kPaged ? 1.0f : *a.k_scale;
+    const float logit = a.scale / qinv * 1.4426950408889634f * tensor_scale;
     int i = 0;
-    int64_t x = first;
+    uint32_t x = first;
     // A thread whose wait has run out goes on without waiting: all of them
     // pass the same barriers to the end.
     while (x < end) {
-      const int t = attn_token_of(plan, a.batch, x);
-      const int64_t t0 = plan->start[t], t1 = plan->start[t + 1], seg_end = min(t1, end);
-      const int row = a.token_row != nullptr ? a.token_row[t] : t;
-      const int64_t len = a.lens[t], nv = attn_positions(a, t, false);
+      const AttnToken k = attn_token(a, plan, x);
+      const uint32_t seg0 = x, seg_end = min(k.end, end);
       int64_t page = 0;
-      int64_t crow = attn_row(a, t, row, nv, len, (x - t0) * kTcTile + pos, &page);
+      int64_t crow = attn_row(a, k, (x - k.start) * kTcTile + pos, &page);
       float rscale = crow >= 0 && kPaged ? a.k_scale[page] : 1.0f;
-      // ---- queries: a warp a head, 16 latent columns a lane, 16 rope columns
-      // for lanes 0-3 (every MMA on the previous queries has completed: its S
-      // has been read)
-      for (int h = warp; h < NH; h += 8) {
-        uint4 hi = make_uint4(0, 0, 0, 0), hr = hi;
-        float xscale = 0.f;
-        if (h0 + h < a.heads) {
-          const int64_t el = (int64_t)t * a.ql_ts + (int64_t)(h0 + h) * a.ql_hs + 16 * lane;
-          const int64_t ep = (int64_t)t * a.qp_ts + (int64_t)(h0 + h) * a.qp_hs + 16 * lane;
-          if constexpr (FP8Q) {
-            hi = *reinterpret_cast<const uint4*>(a.q_latent + el);
-            if (lane < 4) hr = *reinterpret_cast<const uint4*>(a.q_pe + ep);
-            xscale = logit;
-          } else {
-            const uint4* l = reinterpret_cast<const uint4*>(a.q_latent + 2 * el);
-            const uint4* r = reinterpret_cast<const uint4*>(a.q_pe + 2 * ep);
-            const uint4 z = make_uint4(0, 0, 0, 0);
-            const uint4 w[4] = {l[0], l[1], lane < 4 ? r[0] : z, lane < 4 ? r[1] : z};
-            float v[32], mx = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t ww[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                v[8 * e + 2 * k] = bf16lo(ww[k]);
-                v[8 * e + 2 * k + 1] = bf16hi(ww[k]);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, fabsf(v[e]));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-            // the power of two that brings the largest into (224, 448]: from
-            // its exponent field, kept where both it and its inverse are normal
-            int ex = (int)((__float_as_uint(mx) >> 23) & 255u) - 127;
-            ex = max(-100, min(ex, 126));
-            if ((__float_as_uint(mx) & 0x007FFFFFu) <= 0x00600000u) --ex;
-            const float up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
-            xscale = logit * __uint_as_float((uint32_t)(127 - 7 + ex) << 23);
-            // an infinite query: no finite logits (E4M3 has no infinity)
-            if (mx == INFINITY) xscale = __int_as_float(0x7FC00000);
-            uint32_t c[8], d[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float f0 = v[4 * e] * up, f1 = v[4 * e + 1] * up, f2 = v[4 * e + 2] * up,
-                          f3 = v[4 * e + 3] * up;
-              const uint16_t a0 = e4m3x2(f0, f1), a1 = e4m3x2(f2, f3);
-              const float2 g0 = e4m3x2_value(a0), g1 = e4m3x2_value(a1);
-              c[e] = (uint32_t)a0 | ((uint32_t)a1 << 16);
-              d[e] = (uint32_t)e4m3x2(f0 - g0.x, f1 - g0.y) |
-                     ((uint32_t)e4m3x2(f2 - g1.x, f3 - g1.y) << 16);
-            }
-            hi = make_uint4(c[0], c[1], c[2], c[3]);
-            hr = make_uint4(c[4], c[5], c[6], c[7]);
-            const int rl = NH + h;  // the second terms' row
-            *reinterpret_cast<uint4*>(smem + S::oQ + (lane >> 3) * S::kQPlane + rl * 128 +
-                                      (((lane ^ rl) & 7) << 4)) = make_uint4(d[0], d[1], d[2], d[3]);
-            if (lane < 4)
-              *reinterpret_cast<uint4*>(smem + S::oQr + rl * 64 + ((lane ^ ((rl >> 1) & 3)) << 4)) =
-                  make_uint4(d[4], d[5], d[6], d[7]);
-          }
-        } else if constexpr (!FP8Q) {
-          const int rl = NH + h;
-          *reinterpret_cast<uint4*>(smem + S::oQ + (lane >> 3) * S::kQPlane + rl * 128 +
-                                    (((lane ^ rl) & 7) << 4)) = hi;
-          if (lane < 4)
-            *reinterpret_cast<uint4*>(smem + S::oQr + rl * 64 + ((lane ^ ((rl >> 1) & 3)) << 4)) = hr;
-        }
-        *reinterpret_cast<uint4*>(smem + S::oQ + (lane >> 3) * S::kQPlane + h * 128 +
-                                  (((lane ^ h) & 7) << 4)) = hi;
-        if (lane < 4)
-          *reinterpret_cast<uint4*>(smem + S::oQr + h * 64 + ((lane ^ ((h >> 1) & 3)) << 4)) = hr;
-        if (lane == 0) {
-          xs[h] = xscale;
-          ref_max[h] = kNoMax;
-        }
-      }
+      tc_queries<NH, FP8Q>(a, smem, k.t, h0, warp, lane, logit, xs);
+      for (int h = tid; h < NH; h += kTcSoft) ref[h] = 0.f;
       if (tid == 0) vref[0] = kPaged ? 0.f : tensor_scale;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(q_full);
       tc_barrier();
-      float l[kHalf];
+      if (lane == 0) mbar_arrive(q_full);
+      bool started = false;  // a row that counts has been met
+      float2 l[kHalf / 2];
 #pragma unroll
-      for (int h = 0; h < kHalf; ++h) l[h] = 0.f;
+      for (int h = 0; h < kHalf / 2; ++h) l[h] = make_float2(0.f, 0.f);
 
-      for (int64_t tile = x; tile < seg_end; ++tile, ++i) {
+      for (; x < seg_end; ++x, ++i) {
         const int b = i & 1;
         const bool valid = crow >= 0;
-        const float rs = kPaged ? rscale : tensor_scale;
-        // a row that is loaded but does not count holds anything, NaN codes too
-        const bool wipe = !valid;
         tc_wait(&s_full[b], (uint32_t)((i >> 1) & 1), dead);
         tc_after();
         float s[kHalf];
@@ -557,29 +620,47 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc_landed(s);
           tc_landed(lo);
 #pragma unroll
-          for (int h = 0; h < kHalf; ++h) s[h] += lo[h];
+          for (int h = 0; h < kHalf; h += 2) {
+            const float2 v = add2(make_float2(s[h], s[h + 1]), make_float2(lo[h], lo[h + 1]));
+            s[h] = v.x;
+            s[h + 1] = v.y;
+          }
         } else {
           tc_wait_ld();
           tc_landed(s);
         }
         tc_before();
-        mbar_arrive(&s_free[b]);
-        // logits in base 2, and how far they pass the reference
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[b]);
+        // exponents: logits in base 2 less the reference, plus 7
         float over = -INFINITY;
+        const float rs = kPaged ? rscale : 1.0f;
 #pragma unroll
         for (int h = 0; h < kHalf; h += 4) {
           const float4 sc = *reinterpret_cast<const float4*>(xs + hb + h);
-          const float4 m = *reinterpret_cast<const float4*>(ref_max + hb + h);
-          const float scv[4] = {sc.x, sc.y, sc.z, sc.w}, mv[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[h + e] = valid ? s[h + e] * (scv[e] * rs) : -INFINITY;
-            over = fmaxf(over, s[h + e] - mv[e]);
+          const float4 m = *reinterpret_cast<const float4*>(ref + hb + h);
+          float2 c0 = make_float2(sc.x, sc.y), c1 = make_float2(sc.z, sc.w);
+          if (kPaged) {
+            c0 = fmul2_rn(c0, make_float2(rs, rs));
+            c1 = fmul2_rn(c1, make_float2(rs, rs));
           }
+          const float2 v0 = fma2(make_float2(s[h], s[h + 1]), c0, make_float2(-m.x, -m.y));
+          const float2 v1 = fma2(make_float2(s[h + 2], s[h + 3]), c1, make_float2(-m.z, -m.w));
+          s[h] = v0.x;
+          s[h + 1] = v0.y;
+          s[h + 2] = v1.x;
+          s[h + 3] = v1.y;
+          over = fmaxf(over, fmaxf(fmaxf(v0.x, v0.y), fmaxf(v1.x, v1.y)));
         }
-        bool move = over > kPRoom;
+        if (!valid) {
+#pragma unroll
+          for (int h = 0; h < kHalf; ++h) s[h] = -INFINITY;
+        }
+        bool move = valid && (!started || over > kPShift + kPRoom);
         if (kPaged) move |= valid && fabsf(rscale) > vref[0];
         if (barrier_any(kTcBar, kTcSoft, move)) {
+          // the reference moves to the tile's maximum where that passes it by
+          // too much (for the first rows that count, everywhere)
           const float mx = lanes_reduce<kHalf, OpMax>(s);
           if ((lane * kHalf) % 32 == 0) red[quad * NH + hb + lane * kHalf / 32] = mx;
           if (kPaged) {
@@ -590,11 +671,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           tc_barrier();
           if (tid < NH) {
-            const float old = ref_max[tid];
             const float m = fmaxf(fmaxf(red[tid], red[NH + tid]), fmaxf(red[2 * NH + tid], red[3 * NH + tid]));
-            const bool grow = m - old > kPRoom;
-            alpha[tid] = grow ? exp2f(old - m) : 1.0f;
-            if (grow) ref_max[tid] = m;
+            const bool grow = started ? m > kPShift + kPRoom : m > -INFINITY;
+            red[tid] = grow ? kPShift - m : 0.f;
+            if (grow) ref[tid] += m - kPShift;
           }
           if (kPaged && tid == NH) {
             const float old = vref[0];
@@ -605,52 +685,57 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           tc_barrier();
           const float ratio = kPaged ? vref[1] : 1.0f;
 #pragma unroll
-          for (int h = 0; h < kHalf; ++h) l[h] *= alpha[hb + h];
-          if (tile > x) {
+          for (int h = 0; h < kHalf; ++h) {
+            const float d = red[hb + h];
+            s[h] += d;
+            float& lh = h & 1 ? l[h / 2].y : l[h / 2].x;
+            if (started) lh *= ex2(d);
+          }
+          if (started && x > seg0) {
             tc_wait(pv_done, (uint32_t)((i - 1) & 1), dead);
             tc_after();
 #pragma unroll 1
-            for (int c = 0; c < 2 * NH; c += 8) {
+            for (int c = 0; c < 2 * NH; c += 32) {
               // planes 2 half and 2 half + 1 of O^T: columns are heads
-              float v[8];
+              float v[32];
               const uint32_t at = tmem + lanes + 256 + 2 * half * NH + c;
-              tc_ld8(at, v);
+              tc_ld(at, v);
               tc_wait_ld();
               tc_landed(v);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] *= alpha[(c + e) % NH] * ratio;
-              tc_st8(at, v);
+              for (int e = 0; e < 32; ++e) v[e] *= ex2(red[(c + e) % NH]) * ratio;
+              tc_st32(at, v);
             }
             tc_wait_st();
           }
+          started = true;
+          tc_barrier();  // red is read
         }
         // ---- weights
         const float vs = kPaged ? (valid && vref[0] > 0.f ? rscale / vref[0] : 0.f) : 1.0f;
         uint32_t phi[kHalf / 4], plo[kHalf / 4];
 #pragma unroll
         for (int h = 0; h < kHalf; h += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(ref_max + hb + h);
-          const float mv[4] = {m.x, m.y, m.z, m.w};
-          float p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = exp2f(s[h + e] - (mv[e] - kPShift));
-            l[h + e] += p[e];
-            if (kPaged) p[e] *= vs;
+          float2 p0 = make_float2(ex2(s[h]), ex2(s[h + 1]));
+          float2 p1 = make_float2(ex2(s[h + 2]), ex2(s[h + 3]));
+          l[h / 2] = add2(l[h / 2], p0);
+          l[h / 2 + 1] = add2(l[h / 2 + 1], p1);
+          if (kPaged) {
+            p0 = fmul2_rn(p0, make_float2(vs, vs));
+            p1 = fmul2_rn(p1, make_float2(vs, vs));
           }
-          const uint16_t a0 = e4m3x2(p[0], p[1]), a1 = e4m3x2(p[2], p[3]);
-          const float2 g0 = e4m3x2_value(a0), g1 = e4m3x2_value(a1);
-          phi[h / 4] = (uint32_t)a0 | ((uint32_t)a1 << 16);
-          plo[h / 4] = (uint32_t)e5m2x2(p[0] - g0.x, p[1] - g0.y) |
-                       ((uint32_t)e5m2x2(p[2] - g1.x, p[3] - g1.y) << 16);
+          const uint32_t w0 = split_weights(p0.x, p0.y), w1 = split_weights(p1.x, p1.y);
+          phi[h / 4] = __byte_perm(w0, w1, 0x5410);
+          plo[h / 4] = __byte_perm(w0, w1, 0x7632);
         }
-        // the previous tile's PV has read P (and the planes that `wipe` touches
-        // belong to this tile, whose S is done)
+        // the previous tile's PV has read P
         if (i > 0) tc_wait(pv_done, (uint32_t)((i - 1) & 1), dead);
-        if (wipe && half == 0) {
+        if (!valid && half == 0) {
+          // a row that is loaded but does not count holds anything, NaN codes
+          // too: no value of it may meet a weight of zero
 #pragma unroll 1
           for (int j = 0; j < 4; ++j) {
-            uint4* d = reinterpret_cast<uint4*>(smem + S::oRing + ((5 * i + 1 + j) % kSlots) * kPlane + pos * 128);
+            uint4* d = reinterpret_cast<uint4*>(smem + S::oRing + (4 * b + j) * kPlane + pos * 128);
 #pragma unroll
             for (int c = 0; c < 8; ++c) d[c] = make_uint4(0, 0, 0, 0);
           }
@@ -671,61 +756,61 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_before();
-        mbar_arrive(p_full);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
         // the next tile's row
-        if (tile + 1 < seg_end) {
-          crow = attn_row(a, t, row, nv, len, (tile + 1 - t0) * kTcTile + pos, &page);
+        if (x + 1 < seg_end) {
+          crow = attn_row(a, k, (x + 1 - k.start) * kTcTile + pos, &page);
           if (kPaged) rscale = crow >= 0 ? a.k_scale[page] : 1.0f;
         }
       }
       // ---- the stretch is done
       {
-        const float sum = lanes_reduce<kHalf, OpSum>(l);
+        float lv[kHalf];
+#pragma unroll
+        for (int h = 0; h < kHalf; ++h) lv[h] = h & 1 ? l[h / 2].y : l[h / 2].x;
+        const float sum = lanes_reduce<kHalf, OpSum>(lv);
         if ((lane * kHalf) % 32 == 0) red[quad * NH + hb + lane * kHalf / 32] = sum;
       }
       tc_barrier();
-      const bool whole = x == t0 && seg_end == t1;
-      const int slot = 2 * worker + (x == first ? 0 : 1);
+      const bool whole = seg0 == k.start && seg_end == k.end;
+      const int slot = 2 * worker + (seg0 == first ? 0 : 1);
       if (tid < NH) {
         const float sum = (red[tid] + red[NH + tid]) + (red[2 * NH + tid] + red[3 * NH + tid]);
-        const float m = ref_max[tid];
-        const bool none = m == kNoMax && sum == 0.f;
-        const float mm = none ? -INFINITY : m - kPShift;
+        const float m = sum == 0.f ? -INFINITY : ref[tid];
         if (whole) {
-          alpha[tid] = none ? 0.f : vref[0] / sum;
+          red[tid] = sum == 0.f ? 0.f : vref[0] / sum;
           if (a.lse != nullptr && h0 + tid < a.heads)
-            a.lse[(int64_t)t * a.heads + h0 + tid] = attn_lse(mm, sum);
+            a.lse[(int64_t)k.t * a.heads + h0 + tid] = attn_lse(m, sum);
         } else {
-          alpha[tid] = none ? 0.f : vref[0];
-          float* ml = a.part_ml + ((int64_t)slot * a.heads_pad + h0 + tid) * 2;
-          ml[0] = mm;
-          ml[1] = sum;
+          red[tid] = sum == 0.f ? 0.f : vref[0];
+          *reinterpret_cast<float2*>(a.part_ml + ((int64_t)slot * a.heads_pad + h0 + tid) * 2) =
+              make_float2(m, sum);
         }
       }
       tc_barrier();
       tc_wait(pv_done, (uint32_t)((i - 1) & 1), dead);
       tc_after();
 #pragma unroll 1
-      for (int c = 0; c < 2 * NH; c += 8) {
-        float v[8];
-        tc_ld8(tmem + lanes + 256 + 2 * half * NH + c, v);
+      for (int c = 0; c < 2 * NH; c += 32) {
+        float v[32];
+        tc_ld(tmem + lanes + 256 + 2 * half * NH + c, v);
         tc_wait_ld();
         tc_landed(v);
-        const int col = 128 * (2 * half + c / NH) + pos;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int h = (c + e) % NH;
+        for (int e = 0; e < 32; ++e) {
+          const int h = (c + e) % NH, col = 128 * (2 * half + (c + e) / NH) + pos;
+          const float r = v[e] * red[h];
           if (whole) {
             if (h0 + h < a.heads)
-              a.out[(int64_t)t * a.o_ts + (int64_t)(h0 + h) * a.o_hs + col] = f2bf_bits(v[e] * alpha[h]);
+              a.out[(int64_t)k.t * a.o_ts + (int64_t)(h0 + h) * a.o_hs + col] = f2bf_bits(r);
           } else {
-            a.part_o[((int64_t)slot * a.heads_pad + h0 + h) * kKvLora + col] = v[e] * alpha[h];
+            a.part_o[((int64_t)slot * a.heads_pad + h0 + h) * kKvLora + col] = r;
           }
         }
       }
       tc_before();
-      tc_barrier();  // alpha and red are read
-      x = seg_end;
+      tc_barrier();  // red is read
     }
   }
   if (dead) atomicOr(a.err, MLA_DEVERR_TIMEOUT);
@@ -744,7 +829,7 @@ cudaError_t launch_tc(const AttnArgs& a, const TcMaps& maps, cudaStream_t stream
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.workers * a.groups));
   cfg.blockDim = dim3(kTcThreads);
-  cfg.dynamicSmemBytes = TcSmem<NH, FP8Q>::kAlloc;
+  cfg.dynamicSmemBytes = TcSmem<NH, FP8Q>::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -767,7 +852,7 @@ cudaError_t launch_tc_heads(const AttnArgs& a, const TcMaps& maps, cudaStream_t 
 template <int NH, bool FP8Q, int LAYOUT>
 cudaError_t prepare_tc() {
   return cudaFuncSetAttribute(mla_attn_tc_kernel<NH, FP8Q, LAYOUT>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<NH, FP8Q>::kAlloc);
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<NH, FP8Q>::kBytes);
 }
 template <int NH>
 cudaError_t prepare_tc_heads() {

@@ -241,6 +241,7 @@ struct AttnArgs {
   float* lse;      // or null
   float* part_o;   // [2 * workers][heads_pad][512]
   float* part_ml;  // [2 * workers][heads_pad][2]
+  uint32_t* plan;  // [MLA_MAX_BATCH] for the joining kernel (mla_attn.cuh, AttnPlan)
   uint32_t* err;
   int heads, heads_pad, groups, batch;
   int workers;  // per head group
