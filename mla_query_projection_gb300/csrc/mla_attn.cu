@@ -22,8 +22,8 @@ struct mla_attn {
   int heads;
   int max_batch;
   uint32_t* err;
-  float* part_o;   // partial sums [workers * 2][heads padded][512]
-  float* part_ml;  // their maxima and denominators [..][2]
+  float4* part_o;   // partial sums of the workers (mla_attn.cuh, attn_part)
+  float2* part_ml;  // their maxima and denominators
   uint32_t* plan;  // the tiles up to and with each token's [MLA_MAX_BATCH]
 };
 
@@ -282,18 +282,15 @@ __global__ void __launch_bounds__(256, 1) mla_attn_mma_kernel(const AttnArgs a) 
       if (tid < kHeads && h0 + tid < a.heads && a.lse != nullptr)
         a.lse[(int64_t)t * a.heads + h0 + tid] = attn_lse(sm[tid], sl[tid]);
     } else {
-      float* po = a.part_o + ((int64_t)slot * a.heads_pad + h0) * kKvLora;
 #pragma unroll
       for (int n = 0; n < kNO; ++n) {
         const int c = 64 * MT * wn + 8 * n + 2 * q4;
-        *reinterpret_cast<float2*>(po + (int64_t)ha * kKvLora + c) = make_float2(o[n][0], o[n][1]);
-        *reinterpret_cast<float2*>(po + (int64_t)hb * kKvLora + c) = make_float2(o[n][2], o[n][3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          reinterpret_cast<float*>(&attn_part(a, slot, (h0 + (e < 2 ? ha : hb)) >> 2, c + (e & 1)))
+              [(e < 2 ? ha : hb) & 3] = o[n][e];
       }
-      if (tid < kHeads) {
-        float* ml = a.part_ml + ((int64_t)slot * a.heads_pad + h0 + tid) * 2;
-        ml[0] = sm[tid];
-        ml[1] = sl[tid];
-      }
+      if (tid < kHeads) attn_part_ml(a, h0 + tid)[slot] = make_float2(sm[tid], sl[tid]);
     }
     x = seg_end;
   }
@@ -301,92 +298,106 @@ __global__ void __launch_bounds__(256, 1) mla_attn_mma_kernel(const AttnArgs a) 
 
 // --------------------------------------------------------------- joining
 //
-// One CTA a (token, head): with M the largest maximum of the parts,
-// o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i, each part's factor found by a
-// thread of its own, the parts' rows summed in kJoinGroups interleaved groups
-// of 128 threads and then group after group (always the same order).  Tokens
-// whose context one worker read whole are done already; those that look at
-// nothing get zeros and an lse of -infinity.  Bound by the parts' bytes (L2).
+// With M the largest maximum of a (token, head)'s parts,
+// o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  Tokens whose context one
+// worker read whole are done already; those that look at nothing get zeros
+// and an lse of -infinity.  Bound by the parts' bytes (L2), and by latency
+// where there are few.  A CTA takes four heads, which lie side by side in the
+// parts (attn_part), in one of two shapes by the parts a token has on average:
+//  * many (one or a few long contexts): 32 columns a CTA, its eight warps every
+//    eighth part each, their shares summed in order;
+//  * few: all columns, 128 a warp.
+// (One CTA a head in both cases spent its time on CTAs with two or three
+// parts: 7,936 of them for 62 tokens of 128 heads.)
 
-constexpr int kJoinGroups = 4;
-constexpr int kJoinThreads = 128 * kJoinGroups;
-
-__device__ __forceinline__ float join_reduce(float v, bool is_max, float* red) {
-  const int tid = threadIdx.x;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float u = __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    v = is_max ? fmaxf(v, u) : v + u;
-  }
-  if ((tid & 31) == 0) red[tid >> 5] = v;
-  __syncthreads();
-  v = red[0];
-#pragma unroll
-  for (int w = 1; w < kJoinThreads / 32; ++w) v = is_max ? fmaxf(v, red[w]) : v + red[w];
-  __syncthreads();
-  return v;
-}
-
-__global__ void __launch_bounds__(kJoinThreads) mla_attn_join_kernel(const AttnArgs a) {
-  __shared__ float weight[kMaxCtas];
-  __shared__ float red[kJoinThreads / 32];
-  __shared__ float4 sums[kJoinGroups - 1][kKvLora / 4];
-  const int tid = threadIdx.x, t = blockIdx.y, h = blockIdx.x;
+template <bool WIDE>
+__global__ void __launch_bounds__(WIDE ? 256 : 128) mla_attn_join_kernel(const AttnArgs a) {
+  __shared__ float4 weight[kMaxCtas];  // a part's factors for the four heads
+  __shared__ float4 scale4, sums[WIDE ? 8 : 1][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = blockIdx.y;
+  const int quad = WIDE ? (int)blockIdx.x >> 4 : (int)blockIdx.x, h0 = 4 * quad;
   pdl_launch_dependents();
   pdl_wait();
   const uint32_t t0 = t > 0 ? a.plan[t - 1] : 0u, t1 = a.plan[t], total = a.plan[a.batch - 1];
-  uint16_t* out = a.out + (int64_t)t * a.o_ts + (int64_t)h * a.o_hs;
-  if (t0 == t1) {
-    for (int c = 2 * tid; c < kKvLora; c += 2 * kJoinThreads) *reinterpret_cast<uint32_t*>(out + c) = 0u;
-    if (tid == 0 && a.lse != nullptr) a.lse[(int64_t)t * a.heads + h] = -INFINITY;
-    return;
-  }
   const int workers = attn_workers(a, total);
-  const int w0 = attn_worker_of(total, workers, t0), w1 = attn_worker_of(total, workers, t1 - 1);
-  if (w0 == w1) return;
-  const int n = w1 - w0 + 1;  // at most kMaxCtas, and no more than there are threads
+  int w0 = 0, n = 0;
+  if (t1 > t0) {
+    w0 = attn_worker_of(total, workers, t0);
+    n = attn_worker_of(total, workers, t1 - 1) - w0 + 1;  // parts, at most kMaxCtas
+    if (n == 1) return;
+  }
   // part i is worker w0 + i's; the first lies in slot 1 where that worker
   // began with another token
-  const int slot0 = 2 * w0 + (attn_worker_start(total, workers, w0) < t0 ? 1 : 0);
+  const int slot0 = 2 * w0 + (n > 0 && attn_worker_start(total, workers, w0) < t0 ? 1 : 0);
   auto slot_of = [&](int i) { return i == 0 ? slot0 : 2 * (w0 + i); };
-  float2 ml = make_float2(-INFINITY, 0.f);
-  if (tid < n)
-    ml = *reinterpret_cast<const float2*>(a.part_ml + ((int64_t)slot_of(tid) * a.heads_pad + h) * 2);
-  const float M = join_reduce(ml.x, true, red);
-  const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - (M == -INFINITY ? 0.f : M));
-  if (tid < n) weight[tid] = w;
-  const float l = join_reduce(tid < n ? w * ml.y : 0.f, false, red);  // (its barriers order weight)
-  const int c = tid & 127, group = tid >> 7;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = group; i < n; i += kJoinGroups) {
-    const float4 v = *reinterpret_cast<const float4*>(
-        a.part_o + ((int64_t)slot_of(i) * a.heads_pad + h) * kKvLora + 4 * c);
-    const float f = weight[i];
-    if (f != 0.f) {
-      acc.x += f * v.x;
-      acc.y += f * v.y;
-      acc.z += f * v.z;
-      acc.w += f * v.w;
+  if (warp < 4) {  // warp e: the factors of head h0 + e
+    const float2* ml = attn_part_ml(a, h0 + warp);
+    float M = -INFINITY, l = 0.f;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, ml[slot_of(i)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+    const float m_use = M == -INFINITY ? 0.f : M;
+    for (int i = lane; i < n; i += 32) {
+      const float2 v = ml[slot_of(i)];
+      const float f = v.x == -INFINITY ? 0.f : exp2f(v.x - m_use);
+      l += f * v.y;
+      reinterpret_cast<float*>(&weight[i])[warp] = f;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+    if (lane == 0) {
+      reinterpret_cast<float*>(&scale4)[warp] = l == 0.f ? 0.f : 1.0f / l;
+      if (a.lse != nullptr && h0 + warp < a.heads && (!WIDE || (blockIdx.x & 15) == 0))
+        a.lse[(int64_t)t * a.heads + h0 + warp] = attn_lse(M, l);
     }
   }
-  if (group > 0) sums[group - 1][c] = acc;
   __syncthreads();
-  if (group == 0) {
+  const float4 r = scale4;
+  auto add = [](float4& acc, float4 f, float4 v) {
+    // (a part that saw nothing holds zeros, so its factor of zero needs no test)
+    acc.x = fmaf(f.x, v.x, acc.x);
+    acc.y = fmaf(f.y, v.y, acc.y);
+    acc.z = fmaf(f.z, v.z, acc.z);
+    acc.w = fmaf(f.w, v.w, acc.w);
+  };
+  auto put = [&](int col, float4 v) {
+    uint16_t* o = a.out + (int64_t)t * a.o_ts + (int64_t)h0 * a.o_hs + col;
+    const float w[4] = {v.x * r.x, v.y * r.y, v.z * r.z, v.w * r.w};
 #pragma unroll
-    for (int g = 0; g < kJoinGroups - 1; ++g) {
-      const float4 b = sums[g][c];
-      acc.x += b.x;
-      acc.y += b.y;
-      acc.z += b.z;
-      acc.w += b.w;
+    for (int e = 0; e < 4; ++e)
+      if (h0 + e < a.heads) o[e * a.o_hs] = f2bf_bits(w[e]);
+  };
+  if constexpr (WIDE) {
+    const int col = 32 * (blockIdx.x & 15) + lane;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = warp; i < n; i += 8) add(acc, weight[i], attn_part(a, slot_of(i), quad, col));
+    sums[warp][lane] = acc;
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int g = 1; g < 8; ++g) {
+        const float4 b = sums[g][lane];
+        acc.x += b.x;
+        acc.y += b.y;
+        acc.z += b.z;
+        acc.w += b.w;
+      }
+      put(col, acc);
     }
-    const float r = l == 0.f ? 0.f : 1.0f / l;
-    uint2 v;
-    v.x = pack_bf16x2(acc.x * r, acc.y * r);
-    v.y = pack_bf16x2(acc.z * r, acc.w * r);
-    *reinterpret_cast<uint2*>(out + 4 * c) = v;
-    if (tid == 0 && a.lse != nullptr) a.lse[(int64_t)t * a.heads + h] = attn_lse(M, l);
+  } else {
+    const int c0 = 128 * warp + lane;
+    float4 acc[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const int slot = slot_of(i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) add(acc[e], weight[i], attn_part(a, slot, quad, c0 + 32 * e));
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) put(c0 + 32 * e, acc[e]);
   }
 }
 
@@ -489,7 +500,7 @@ int mla_attn_create(mla_attn_t* out, int max_batch, int heads) {
   rc = MLA_ENOMEM;
   if (cudaMalloc(&h->err, 2048) != cudaSuccess ||
       cudaMalloc(&h->part_o, slots * mla::kKvLora * sizeof(float)) != cudaSuccess ||
-      cudaMalloc(&h->part_ml, slots * 2 * sizeof(float)) != cudaSuccess)
+      cudaMalloc(&h->part_ml, slots * sizeof(float2)) != cudaSuccess)
     goto fail;
   rc = MLA_ECUDA;
   h->plan = h->err + 64;
@@ -583,16 +594,19 @@ int mla_attn_decode(mla_attn_t h, int batch, const void* q_latent, int64_t ql_to
   }
   int rc = mla::launched(e);
   if (rc != MLA_OK) return rc;
+  // parts a token has on average: workers / batch
+  const bool wide = a.workers >= 16 * batch;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)h->heads, (unsigned)batch);
-  cfg.blockDim = dim3(mla::kJoinThreads);
+  cfg.gridDim = dim3((unsigned)((h->heads + 3) / 4 * (wide ? 16 : 1)), (unsigned)batch);
+  cfg.blockDim = dim3(wide ? 256 : 128);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return mla::launched(cudaLaunchKernelEx(&cfg, mla::mla_attn_join_kernel, a));
+  return mla::launched(wide ? cudaLaunchKernelEx(&cfg, mla::mla_attn_join_kernel<true>, a)
+                            : cudaLaunchKernelEx(&cfg, mla::mla_attn_join_kernel<false>, a));
 }
 
 int mla_attn_get_error(mla_attn_t h, unsigned* device_flags, void* stream) {

@@ -56,16 +56,30 @@ __device__ __forceinline__ uint32_t attn_positions(const AttnArgs& a, int t, int
   return (uint32_t)n;
 }
 
+// The tokens' lengths, rows and positions as the plan read them, kept where
+// there is room until the first tile: a worker's first token needs no second
+// trip to memory.
+struct AttnSeen {
+  int32_t len[kAttnMaxBatch], row[kAttnMaxBatch];
+  uint32_t nv[kAttnMaxBatch];
+};
+
 // Fills the plan; all threads of the block call it (at least 256 of them, a
 // multiple of 32), and may read it after the closing barrier.  red: 8 words.
 __device__ __forceinline__ void attn_make_plan(const AttnArgs& a, AttnPlan* p, uint32_t* red,
-                                               bool flag) {
+                                               bool flag, AttnSeen* seen = nullptr) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t n = 0;
   if (tid < a.batch) {
     const int32_t len = a.lens[tid];
     const int row = a.token_row != nullptr ? a.token_row[tid] : tid;
-    n = (attn_positions(a, tid, len, row, flag) + a.tile - 1) / a.tile;
+    const uint32_t nv = attn_positions(a, tid, len, row, flag);
+    n = (nv + a.tile - 1) / a.tile;
+    if (seen != nullptr) {
+      seen->len[tid] = len;
+      seen->row[tid] = row;
+      seen->nv[tid] = nv;
+    }
   }
   uint32_t inc = n;
 #pragma unroll
@@ -84,11 +98,14 @@ __device__ __forceinline__ void attn_make_plan(const AttnArgs& a, AttnPlan* p, u
   __syncthreads();
 }
 
-// Workers with work: no more than there are tiles, so that every one of them
-// has a tile, and every worker between the first and the last of a token
-// leaves a part of it.
+// Workers with work: the fewest for which the busiest has no more tiles than
+// it would have if all took part (every part less is one that need not be
+// written and joined); so every one of them has a tile, and every worker
+// between the first and the last of a token leaves a part of it.
 __device__ __forceinline__ int attn_workers(const AttnArgs& a, uint32_t total) {
-  return (int)min((uint32_t)a.workers, total);
+  if (total == 0) return 0;
+  const uint32_t most = (total + a.workers - 1) / a.workers;
+  return (int)((total + most - 1) / most);
 }
 __device__ __forceinline__ uint32_t attn_worker_start(uint32_t total, int workers, int w) {
   return (uint32_t)((uint64_t)total * w / workers);
@@ -110,11 +127,18 @@ __device__ __forceinline__ int attn_token_of(const AttnPlan* p, int batch, uint3
   }
   return lo;
 }
-__device__ __forceinline__ AttnToken attn_token(const AttnArgs& a, const AttnPlan* p, uint32_t x) {
+__device__ __forceinline__ AttnToken attn_token(const AttnArgs& a, const AttnPlan* p, uint32_t x,
+                                                const AttnSeen* seen = nullptr) {
   AttnToken k;
   k.t = attn_token_of(p, a.batch, x);
   k.start = p->start(k.t);
   k.end = p->end[k.t];
+  if (seen != nullptr) {
+    k.row = seen->row[k.t];
+    k.len = seen->len[k.t];
+    k.nv = seen->nv[k.t];
+    return k;
+  }
   k.row = a.token_row != nullptr ? a.token_row[k.t] : k.t;
   k.len = a.lens[k.t];
   k.nv = attn_positions(a, k.t, k.len, k.row, false);
@@ -140,6 +164,17 @@ __device__ __forceinline__ int64_t attn_row(const AttnArgs& a, const AttnToken& 
   }
   *page = p;
   return p * a.page_size + off;
+}
+
+// A part's sums: slot, then the head's group of four, then the column, four
+// heads side by side, so that a thread that holds one column of several heads
+// (a lane of O^T) writes 16 bytes, and a warp 512 bytes in a row.
+__device__ __forceinline__ float4& attn_part(const AttnArgs& a, int slot, int quad, int col) {
+  return a.part_o[((int64_t)slot * (a.heads_pad >> 2) + quad) * kKvLora + col];
+}
+// A head's (maximum in base 2, denominator), by slot.
+__device__ __forceinline__ float2* attn_part_ml(const AttnArgs& a, int head) {
+  return a.part_ml + (int64_t)head * 2 * a.workers;
 }
 
 // Natural logarithm of the sum of exponentials, from the maximum in base 2 and

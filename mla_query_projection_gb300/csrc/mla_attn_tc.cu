@@ -15,7 +15,7 @@
 //    same plane read transposed (M-major), so no value is moved or converted.
 //    P is the sum of an E4M3 and an E5M2 term (4 + 3 bits: 2^-7 of each
 //    weight), two MMAs into one accumulator.  The second term in E5M2 keeps
-//    weights down to 2^-23 of the largest: a context with one dominant key and
+//    weights down to 2^-21 of the largest: a context with one dominant key and
 //    thousands of small ones needs their sum.
 //
 // Tokens lie on TMEM lanes in S^T: a softmax thread owns one cache row and
@@ -47,9 +47,11 @@ constexpr int kTcSoft = 256;               // softmax threads (warps 0-7)
 constexpr int kTcThreads = kTcSoft + 64;   // + a TMA warp, an MMA warp
 constexpr int kTcBar = 1;                  // named barrier of the softmax threads
 constexpr long long kTcWait = 2000000000LL;  // ~1 s of SM clock
-// Weights are kept times 2^7, and the reference moves when a logit (base 2)
-// passes it by more than 1.75: 2^8.75 = 430 < 448, E4M3's largest.
-constexpr float kPShift = 7.0f, kPRoom = 1.75f;
+// Weights are kept times 2^5, and the reference moves when a logit (base 2)
+// passes it by more than 3.75: 2^8.75 = 430 < 448, E4M3's largest.  (With 2^7
+// and 1.75 a sixth of the tiles of normally distributed logits moved it, at
+// 7,000 cycles each.)
+constexpr float kPShift = 5.0f, kPRoom = 3.75f;
 
 template <int NH, bool FP8Q>
 struct TcSmem {
@@ -60,14 +62,15 @@ struct TcSmem {
   static constexpr int oP = oRope + kPlane / 2;        // [row][hi | lo] 128 B
   static constexpr int oQ = oP + kPlane;               // 4 latent planes
   static constexpr int oQr = oQ + 4 * kQPlane;         // rope plane, 64-byte rows
-  static constexpr int oRef = oQr + kQRows * 64;       // reference less 7, base 2 [NH]
+  static constexpr int oRef = oQr + kQRows * 64;       // reference less kPShift, base 2 [NH]
   static constexpr int oXs = oRef + NH * 4;            // logit scale of a head's accumulators [NH]
   static constexpr int oRed = oXs + NH * 4;            // [4][NH] across the quadrants; [0][.] factors
   static constexpr int oVref = oRed + 4 * NH * 4;      // value scale: reference, its ratio, [4..7] warp maxima
   static constexpr int oBar = oVref + 32;
-  // full[8] empty[8] rope_full rope_empty s_full[2] s_free[2] p_full pv_done q_full drain
-  static constexpr int kBars = 26;
-  static constexpr int oPlan = oBar + kBars * 8;
+  // full[8] empty[8] rope_full rope_empty s_full[2] s_free[2] p_full pv_done q_full drain voted
+  static constexpr int kBars = 27;
+  static constexpr int oMoved = oBar + kBars * 8;      // [2] 1 + the last tile that moved the reference
+  static constexpr int oPlan = oMoved + 8;
   static constexpr int oScan = oRed;                   // before the first tile
   static constexpr int oTmem = oPlan + (int)sizeof(AttnPlan);
   static constexpr int kBytes = oTmem + 8;
@@ -111,6 +114,51 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d, uint64_t a, uint64_t b, ui
       : "memory");
 }
 
+// S^T of one latent plane: four steps of 32 codes.
+__device__ __forceinline__ void tc_qk_plane(uint32_t d, uint64_t a, uint64_t b, uint32_t id0, uint32_t id1,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q, t;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, %5, %5;\n\t"
+      "elect.sync _|q, 0xFFFFFFFF;\n\t"
+      "add.u64 x, %1, 0;\n\tadd.u64 y, %2, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n\t"
+      "add.u64 x, %1, 2;\n\tadd.u64 y, %2, 2;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, t;\n\t"
+      "add.u64 x, %1, 4;\n\tadd.u64 y, %2, 4;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, t;\n\t"
+      "add.u64 x, %1, 6;\n\tadd.u64 y, %2, 6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, t;\n\t"
+      "}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id0), "r"(id1), "r"(accumulate)
+      : "memory");
+}
+// O^T of one plane: four steps of 32 rows (4096 bytes of V and of P), each with
+// both terms of P (the second 64 bytes on).
+__device__ __forceinline__ void tc_pv_plane(uint32_t d, uint64_t a, uint64_t b, uint32_t id0, uint32_t id1,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q, t;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, %5, %5;\n\t"
+      "elect.sync _|q, 0xFFFFFFFF;\n\t"
+      "add.u64 x, %1, 0;\n\tadd.u64 y, %2, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n\t"
+      "add.u64 x, %1, 0;\n\tadd.u64 y, %2, 4;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %4, t;\n\t"
+      "add.u64 x, %1, 256;\n\tadd.u64 y, %2, 256;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, t;\n\t"
+      "add.u64 x, %1, 256;\n\tadd.u64 y, %2, 260;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %4, t;\n\t"
+      "add.u64 x, %1, 512;\n\tadd.u64 y, %2, 512;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, t;\n\t"
+      "add.u64 x, %1, 512;\n\tadd.u64 y, %2, 516;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %4, t;\n\t"
+      "add.u64 x, %1, 768;\n\tadd.u64 y, %2, 768;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, t;\n\t"
+      "add.u64 x, %1, 768;\n\tadd.u64 y, %2, 772;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %4, t;\n\t"
+      "}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id0), "r"(id1), "r"(accumulate)
+      : "memory");
+}
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\t"
@@ -252,17 +300,6 @@ __device__ __forceinline__ float lanes_reduce(const float (&in)[N]) {
   return v[0];
 }
 
-// Whether any of the `count` threads on named barrier `id` says so.
-__device__ __forceinline__ bool barrier_any(int id, int count, bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)p), "r"(id), "r"(count)
-      : "memory");
-  return r != 0;
-}
 __device__ __forceinline__ void tc_barrier() {
   asm volatile("bar.sync %0, %1;" ::"r"(kTcBar), "r"(kTcSoft) : "memory");
 }
@@ -277,6 +314,20 @@ __device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, bool& de
 __device__ __forceinline__ void tc_wait_warp(uint64_t* bar, uint32_t parity, bool& dead) {
   tc_wait(bar, parity, dead);
   dead = __any_sync(0xFFFFFFFFu, dead);
+}
+
+// Whether the phase is over, the same answer for the whole warp, at once (a
+// try_wait may hold the thread for a while).
+__device__ __forceinline__ bool tc_ready(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return __all_sync(0xFFFFFFFFu, ok != 0);
 }
 
 struct TcMaps {
@@ -329,35 +380,45 @@ __device__ __forceinline__ void tc_queries(const AttnArgs& a, uint8_t* smem, int
   } else {
     // magnitudes as bits order like the values (NaN above infinity)
     auto magnitude = [](uint4 w) {
-      uint32_t m = 0;
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) m = max(m, max(ww[k] & 0x7FFFu, (ww[k] >> 16) & 0x7FFFu));
-      return m;
+      const uint32_t s = 0x7FFF7FFFu;
+      return __vmaxu2(__vmaxu2(w.x & s, w.y & s), __vmaxu2(w.z & s, w.w & s));
     };
-    // 16 columns as their two E4M3 terms, scaled by a power of two
-    auto split = [](const uint4* w, float up, uint4* hi, uint4* lo) {
+    // A pair of columns times a power of two as two E4M3 terms: the first's
+    // codes in the low half of the result, the rest's in the high half (FP16
+    // holds the scaled values, at most 448, exactly down to 2^-17).
+    auto split2 = [](uint32_t w, float up) {
+      const float2 v = fmul2_rn(make_float2(bf16lo(w), bf16hi(w)), make_float2(up, up));
+      uint32_t r;
+      asm("{\n\t.reg .b32 p, g, d;\n\t.reg .b16 c, e;\n\t"
+          "cvt.rn.f16x2.f32 p, %2, %1;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f16x2 c, p;\n\t"
+          "cvt.rn.f16x2.e4m3x2 g, c;\n\t"
+          "sub.rn.f16x2 d, p, g;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f16x2 e, d;\n\t"
+          "mov.b32 %0, {c, e};\n\t}"
+          : "=r"(r)
+          : "f"(v.x), "f"(v.y));
+      return r;
+    };
+    auto split = [&](const uint4* w, float up, uint4* hi, uint4* lo) {
       uint32_t c[4], d[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint4 q = w[e >> 1];
-        const uint32_t x = e & 1 ? q.z : q.x, y = e & 1 ? q.w : q.y;
-        const float f0 = bf16lo(x) * up, f1 = bf16hi(x) * up, f2 = bf16lo(y) * up, f3 = bf16hi(y) * up;
-        const uint16_t a0 = e4m3x2(f0, f1), a1 = e4m3x2(f2, f3);
-        const float2 g0 = e4m3x2_value(a0), g1 = e4m3x2_value(a1);
-        c[e] = (uint32_t)a0 | ((uint32_t)a1 << 16);
-        d[e] = (uint32_t)e4m3x2(f0 - g0.x, f1 - g0.y) | ((uint32_t)e4m3x2(f2 - g1.x, f3 - g1.y) << 16);
+        const uint32_t x = split2(e & 1 ? q.z : q.x, up), y = split2(e & 1 ? q.w : q.y, up);
+        c[e] = __byte_perm(x, y, 0x5410);
+        d[e] = __byte_perm(x, y, 0x7632);
       }
       *hi = make_uint4(c[0], c[1], c[2], c[3]);
       *lo = make_uint4(d[0], d[1], d[2], d[3]);
     };
-    const uint32_t rope_mag = max(magnitude(rope[0]), magnitude(rope[kV - 1]));
+    const uint32_t rope_mag = __vmaxu2(magnitude(rope[0]), magnitude(rope[kV - 1]));
     float rope_up = 0.f;
 #pragma unroll
     for (int r = 0; r < kN; ++r) {
-      uint32_t m = max(magnitude(lat[r][0]), magnitude(lat[r][kV - 1]));
-      if (rr == r) m = max(m, rope_mag);
-      m = __reduce_max_sync(0xFFFFFFFFu, m);
+      uint32_t m = __vmaxu2(magnitude(lat[r][0]), magnitude(lat[r][kV - 1]));
+      if (rr == r) m = __vmaxu2(m, rope_mag);
+      m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
       // the power of two that brings the largest into (224, 448]: from its
       // exponent field, kept where both it and its inverse are normal
       int ex = (int)(m >> 7) - 127;
@@ -400,6 +461,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* pv_done = p_full + 1;
   uint64_t* q_full = pv_done + 1;
   uint64_t* drain = q_full + 1;
+  uint64_t* voted = drain + 1;
+  uint32_t* moved = reinterpret_cast<uint32_t*>(smem + S::oMoved);
   float* ref = reinterpret_cast<float*>(smem + S::oRef);
   float* xs = reinterpret_cast<float*>(smem + S::oXs);
   float* red = reinterpret_cast<float*>(smem + S::oRed);
@@ -426,6 +489,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(pv_done, 1);
     mbar_init(q_full, kTcSoft / 32);
     mbar_init(drain, 1);
+    mbar_init(voted, kTcSoft / 32);
+    moved[0] = moved[1] = 0;
     mbar_fence_init();
     // the swizzles go by address bits: the base is a multiple of 1 KiB
     if (smem_u32(smem) & 1023u) atomicOr(a.err, MLA_DEVERR_CHECK);
@@ -445,9 +510,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   pdl_wait();
   tc_before();
   // (the plan's barriers order the set-up above)
-  attn_make_plan(a, plan, reinterpret_cast<uint32_t*>(smem + S::oScan), blockIdx.x == 0);
+  AttnSeen* seen = reinterpret_cast<AttnSeen*>(smem + S::oP);  // until the first weights
+  attn_make_plan(a, plan, reinterpret_cast<uint32_t*>(smem + S::oScan), blockIdx.x == 0, seen);
   tc_after();
-  const uint32_t tmem = *tslot;  // S^T buffers at columns 0 and 128, O^T planes from 256
+  const uint32_t tmem = __reduce_max_sync(0xFFFFFFFFu, *tslot);  // S^T buffers at columns 0 and 128, O^T planes from 256
   const uint32_t total = plan->end[a.batch - 1];
   const int workers = attn_workers(a, total);
   const uint32_t first = worker < workers ? attn_worker_start(total, workers, worker) : 0;
@@ -461,7 +527,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int i = 0, issued = 0;  // tiles, planes
     uint32_t x = first;
     while (x < end && !dead) {
-      const AttnToken k = attn_token(a, plan, x);
+      // (the first token's weights come after its queries and a tile of its
+      // rows: this warp has read `seen` by then)
+      const AttnToken k = attn_token(a, plan, x, i == 0 ? seen : nullptr);
       const uint32_t seg_end = min(k.end, end);
       for (; x < seg_end && !dead; ++x, ++i) {
         int32_t y = no_row;
@@ -513,65 +581,69 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint64_t dqr = tc_desc(smem_u32(smem + S::oQr), 512, 4);
     const uint64_t dp = tc_desc(smem_u32(smem + S::oP), 1024, 2);
     constexpr uint64_t kPl = kPlane >> 4, kQPl = S::kQPlane >> 4;
-    // O^T += V^T P^T of tile n, the first of its stretch or not
-    auto pv = [&](int n, bool fresh) {
+    // O^T += V^T P^T of tile n (`add`: to what its stretch has so far)
+    auto pv = [&](int n, uint32_t add) {
       tc_wait_warp(p_full, (uint32_t)(n & 1), dead);
       tc_after();
-      if (dead) return;
       const int b = n & 1;
       const uint64_t da = dk + (uint64_t)b * 4 * kPl;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          // 32 rows a step: 4096 bytes of V and of P; P's second term 64 bytes on
-          tc_mma_f8(tmem + 256 + NH * j, da + j * kPl + 256 * k, dp + 256 * k, id_hi,
-                    k > 0 ? 1u : (uint32_t)!fresh);
-          tc_mma_f8(tmem + 256 + NH * j, da + j * kPl + 256 * k, dp + 256 * k + 4, id_lo, 1u);
-        }
+        tc_pv_plane(tmem + 256 + NH * j, da + j * kPl, dp, id_hi, id_lo, add);
         tc_commit(&empty[4 * b + j]);
       }
       tc_commit(pv_done);
     };
-    int i = 0, segs = 0;
-    bool due = false, due_fresh = false;  // the previous tile's PV
-    uint32_t x = first;
-    while (x < end && !dead) {
-      const uint32_t seg_end = min(plan->end[attn_token_of(plan, a.batch, x)], end);
-      bool fresh = true;
-      for (; x < seg_end && !dead; ++x, ++i) {
-        const int b = i & 1;
-        if (fresh) {
-          if (due) pv(i - 1, due_fresh);  // its softmax must finish before the queries change
-          due = false;
-          tc_wait_warp(q_full, (uint32_t)(segs & 1), dead);
-        }
-        if (i >= 2) tc_wait_warp(&s_free[b], (uint32_t)((i / 2 - 1) & 1), dead);
-        tc_wait_warp(rope_full, (uint32_t)(i & 1), dead);
-        tc_after();
-        if (dead) break;
-        const uint32_t d = tmem + 128 * b;
-        tc_mma_f8(d, dkr, dqr, id_s, 0u);
-        tc_mma_f8(d, dkr + 2, dqr + 2, id_s, 1u);
-        tc_commit(rope_empty);
-        const uint64_t da = dk + (uint64_t)b * 4 * kPl;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          tc_wait_warp(&full[4 * b + j], (uint32_t)((i >> 1) & 1), dead);
-          tc_after();
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_f8(d, da + j * kPl + 2 * k, dq + j * kQPl + 2 * k, id_s, 1u);
-        }
-        tc_commit(&s_full[b]);
-        if (due) pv(i - 1, due_fresh);
-        due = true;
-        due_fresh = fresh;
-        fresh = false;
+    // A wait that ran out ends no loop here (the loops are then the warp's, and
+    // the descriptors stay in uniform registers): the MMAs go on over whatever
+    // the planes hold, and the results do not count.
+    const int tiles = (int)__reduce_max_sync(0xFFFFFFFFu, end - first);
+    const uint32_t x0 = __reduce_max_sync(0xFFFFFFFFu, first);
+    uint32_t seg_end = x0;
+    int segs = 0;
+    uint32_t add = 0;  // whether the tile before added to its O^T
+    bool due = false;  // its PV is still to be issued
+    for (int i = 0; i < tiles; ++i) {
+      const int b = i & 1;
+      const bool fresh = x0 + i == seg_end;
+      if (fresh) {
+        seg_end = __reduce_max_sync(0xFFFFFFFFu, plan->end[attn_token_of(plan, a.batch, x0 + i)]);
+        if (due) pv(i - 1, add);  // its softmax must finish before the queries change
+        due = false;
+        tc_wait_warp(q_full, (uint32_t)(segs & 1), dead);
+        ++segs;
       }
-      ++segs;
+      if (i >= 2) tc_wait_warp(&s_free[b], (uint32_t)((i / 2 - 1) & 1), dead);
+      tc_wait_warp(rope_full, (uint32_t)(i & 1), dead);
+      tc_after();
+      const uint32_t d = tmem + 128 * b;
+      tc_mma_f8(d, dkr, dqr, id_s, 0u);
+      tc_mma_f8(d, dkr + 2, dqr + 2, id_s, 1u);
+      tc_commit(rope_empty);
+      const uint64_t da = dk + (uint64_t)b * 4 * kPl;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // While a plane has not landed, weights may come: PV first then, which
+        // is what frees the planes of the tile after this one.
+        if (due) {
+          const long long since = clock64();
+          while (!tc_ready(&full[4 * b + j], (uint32_t)((i >> 1) & 1)) && clock64() - since < kTcWait)
+            if (tc_ready(p_full, (uint32_t)((i - 1) & 1))) {
+              pv(i - 1, add);
+              due = false;
+              break;
+            }
+        }
+        tc_wait_warp(&full[4 * b + j], (uint32_t)((i >> 1) & 1), dead);
+        tc_after();
+        tc_qk_plane(d, da + j * kPl, dq + j * kQPl, id_s, id_s, 1u);
+      }
+      tc_commit(&s_full[b]);
+      if (due) pv(i - 1, add);
+      due = true;
+      add = fresh ? 0u : 1u;
     }
-    if (due && !dead) pv(i - 1, due_fresh);
+    if (due) pv(tiles - 1, add);
     if (dead) {  // let what was issued finish before TMEM is freed
       tc_commit(drain);
       (void)mbar_wait_bounded(drain, 0u, kTcWait);
@@ -590,17 +662,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // A thread whose wait has run out goes on without waiting: all of them
     // pass the same barriers to the end.
     while (x < end) {
-      const AttnToken k = attn_token(a, plan, x);
+      const AttnToken k = attn_token(a, plan, x, i == 0 ? seen : nullptr);
       const uint32_t seg0 = x, seg_end = min(k.end, end);
-      int64_t page = 0;
-      int64_t crow = attn_row(a, k, (x - k.start) * kTcTile + pos, &page);
-      float rscale = crow >= 0 && kPaged ? a.k_scale[page] : 1.0f;
       tc_queries<NH, FP8Q>(a, smem, k.t, h0, warp, lane, logit, xs);
       for (int h = tid; h < NH; h += kTcSoft) ref[h] = 0.f;
       if (tid == 0) vref[0] = kPaged ? 0.f : tensor_scale;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tc_barrier();
       if (lane == 0) mbar_arrive(q_full);
+      int64_t page = 0;
+      int64_t crow = attn_row(a, k, (x - k.start) * kTcTile + pos, &page);
+      float rscale = crow >= 0 && kPaged ? a.k_scale[page] : 1.0f;
       bool started = false;  // a row that counts has been met
       float2 l[kHalf / 2];
 #pragma unroll
@@ -612,55 +684,84 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_wait(&s_full[b], (uint32_t)((i >> 1) & 1), dead);
         tc_after();
         float s[kHalf];
-        tc_ld(tmem + lanes + 128 * b + hb, s);
-        if constexpr (!FP8Q) {
-          float lo[kHalf];
-          tc_ld(tmem + lanes + 128 * b + NH + hb, lo);
-          tc_wait_ld();
-          tc_landed(s);
-          tc_landed(lo);
+        // exponents: logits in base 2 less the reference, plus kPShift
+        auto exponents = [&]() {
+          tc_ld(tmem + lanes + 128 * b + hb, s);
+          if constexpr (!FP8Q) {
+            float lo[kHalf];
+            tc_ld(tmem + lanes + 128 * b + NH + hb, lo);
+            tc_wait_ld();
+            tc_landed(s);
+            tc_landed(lo);
 #pragma unroll
-          for (int h = 0; h < kHalf; h += 2) {
-            const float2 v = add2(make_float2(s[h], s[h + 1]), make_float2(lo[h], lo[h + 1]));
-            s[h] = v.x;
-            s[h + 1] = v.y;
+            for (int h = 0; h < kHalf; h += 2) {
+              const float2 v = add2(make_float2(s[h], s[h + 1]), make_float2(lo[h], lo[h + 1]));
+              s[h] = v.x;
+              s[h + 1] = v.y;
+            }
+          } else {
+            tc_wait_ld();
+            tc_landed(s);
           }
-        } else {
-          tc_wait_ld();
-          tc_landed(s);
-        }
-        tc_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[b]);
-        // exponents: logits in base 2 less the reference, plus 7
-        float over = -INFINITY;
-        const float rs = kPaged ? rscale : 1.0f;
+          const float rs = kPaged ? rscale : 1.0f;
 #pragma unroll
-        for (int h = 0; h < kHalf; h += 4) {
-          const float4 sc = *reinterpret_cast<const float4*>(xs + hb + h);
-          const float4 m = *reinterpret_cast<const float4*>(ref + hb + h);
-          float2 c0 = make_float2(sc.x, sc.y), c1 = make_float2(sc.z, sc.w);
-          if (kPaged) {
-            c0 = fmul2_rn(c0, make_float2(rs, rs));
-            c1 = fmul2_rn(c1, make_float2(rs, rs));
+          for (int h = 0; h < kHalf; h += 4) {
+            const float4 sc = *reinterpret_cast<const float4*>(xs + hb + h);
+            const float4 m = *reinterpret_cast<const float4*>(ref + hb + h);
+            float2 c0 = make_float2(sc.x, sc.y), c1 = make_float2(sc.z, sc.w);
+            if (kPaged) {
+              c0 = fmul2_rn(c0, make_float2(rs, rs));
+              c1 = fmul2_rn(c1, make_float2(rs, rs));
+            }
+            const float2 v0 = fma2(make_float2(s[h], s[h + 1]), c0, make_float2(-m.x, -m.y));
+            const float2 v1 = fma2(make_float2(s[h + 2], s[h + 3]), c1, make_float2(-m.z, -m.w));
+            s[h] = v0.x;
+            s[h + 1] = v0.y;
+            s[h + 2] = v1.x;
+            s[h + 3] = v1.y;
           }
-          const float2 v0 = fma2(make_float2(s[h], s[h + 1]), c0, make_float2(-m.x, -m.y));
-          const float2 v1 = fma2(make_float2(s[h + 2], s[h + 3]), c1, make_float2(-m.z, -m.w));
-          s[h] = v0.x;
-          s[h + 1] = v0.y;
-          s[h + 2] = v1.x;
-          s[h + 3] = v1.y;
-          over = fmaxf(over, fmaxf(fmaxf(v0.x, v0.y), fmaxf(v1.x, v1.y)));
-        }
-        if (!valid) {
+          if (!valid) {
 #pragma unroll
-          for (int h = 0; h < kHalf; ++h) s[h] = -INFINITY;
-        }
+            for (int h = 0; h < kHalf; ++h) s[h] = -INFINITY;
+          }
+        };
+        // weights from the exponents, and their two terms
+        uint32_t phi[kHalf / 4], plo[kHalf / 4];
+        auto weights = [&]() {
+          const float vs = kPaged ? (valid && vref[0] > 0.f ? rscale / vref[0] : 0.f) : 1.0f;
+#pragma unroll
+          for (int h = 0; h < kHalf; h += 4) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[h + e] = ex2(s[h + e]);
+            float2 p0 = make_float2(s[h], s[h + 1]), p1 = make_float2(s[h + 2], s[h + 3]);
+            if (kPaged) {
+              p0 = fmul2_rn(p0, make_float2(vs, vs));
+              p1 = fmul2_rn(p1, make_float2(vs, vs));
+            }
+            const uint32_t w0 = split_weights(p0.x, p0.y), w1 = split_weights(p1.x, p1.y);
+            phi[h / 4] = __byte_perm(w0, w1, 0x5410);
+            plo[h / 4] = __byte_perm(w0, w1, 0x7632);
+          }
+        };
+        exponents();
+        float over = fmaxf(s[0], s[1]);
+#pragma unroll
+        for (int h = 2; h < kHalf; h += 2) over = fmaxf(over, fmaxf(s[h], s[h + 1]));
+        // Does the reference have to move?  The warps' answers meet while the
+        // weights are computed as if not.
         bool move = valid && (!started || over > kPShift + kPRoom);
         if (kPaged) move |= valid && fabsf(rscale) > vref[0];
-        if (barrier_any(kTcBar, kTcSoft, move)) {
+        move = __any_sync(0xFFFFFFFFu, move);
+        if (lane == 0) {
+          if (move) *reinterpret_cast<volatile uint32_t*>(&moved[b]) = (uint32_t)i + 1;
+          mbar_arrive(voted);
+        }
+        weights();
+        tc_wait(voted, (uint32_t)(i & 1), dead);
+        if (*reinterpret_cast<volatile uint32_t*>(&moved[b]) == (uint32_t)i + 1) {
           // the reference moves to the tile's maximum where that passes it by
           // too much (for the first rows that count, everywhere)
+          exponents();
           const float mx = lanes_reduce<kHalf, OpMax>(s);
           if ((lane * kHalf) % 32 == 0) red[quad * NH + hb + lane * kHalf / 32] = mx;
           if (kPaged) {
@@ -709,25 +810,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc_wait_st();
           }
           started = true;
+          weights();
           tc_barrier();  // red is read
         }
-        // ---- weights
-        const float vs = kPaged ? (valid && vref[0] > 0.f ? rscale / vref[0] : 0.f) : 1.0f;
-        uint32_t phi[kHalf / 4], plo[kHalf / 4];
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[b]);
 #pragma unroll
-        for (int h = 0; h < kHalf; h += 4) {
-          float2 p0 = make_float2(ex2(s[h]), ex2(s[h + 1]));
-          float2 p1 = make_float2(ex2(s[h + 2]), ex2(s[h + 3]));
-          l[h / 2] = add2(l[h / 2], p0);
-          l[h / 2 + 1] = add2(l[h / 2 + 1], p1);
-          if (kPaged) {
-            p0 = fmul2_rn(p0, make_float2(vs, vs));
-            p1 = fmul2_rn(p1, make_float2(vs, vs));
-          }
-          const uint32_t w0 = split_weights(p0.x, p0.y), w1 = split_weights(p1.x, p1.y);
-          phi[h / 4] = __byte_perm(w0, w1, 0x5410);
-          plo[h / 4] = __byte_perm(w0, w1, 0x7632);
-        }
+        for (int h = 0; h < kHalf; h += 2) l[h / 2] = add2(l[h / 2], make_float2(s[h], s[h + 1]));
         // the previous tile's PV has read P
         if (i > 0) tc_wait(pv_done, (uint32_t)((i - 1) & 1), dead);
         if (!valid && half == 0) {
@@ -784,8 +874,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             a.lse[(int64_t)k.t * a.heads + h0 + tid] = attn_lse(m, sum);
         } else {
           red[tid] = sum == 0.f ? 0.f : vref[0];
-          *reinterpret_cast<float2*>(a.part_ml + ((int64_t)slot * a.heads_pad + h0 + tid) * 2) =
-              make_float2(m, sum);
+          attn_part_ml(a, h0 + tid)[slot] = make_float2(m, sum);
         }
       }
       tc_barrier();
@@ -798,14 +887,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_wait_ld();
         tc_landed(v);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int h = (c + e) % NH, col = 128 * (2 * half + (c + e) / NH) + pos;
-          const float r = v[e] * red[h];
+        for (int e = 0; e < 32; e += 4) {
+          const int h = (c + e) % NH, j = 2 * half + (c + e) / NH;
+          const float4 f = *reinterpret_cast<const float4*>(red + h);
+          const float v0 = v[e] * f.x, v1 = v[e + 1] * f.y, v2 = v[e + 2] * f.z, v3 = v[e + 3] * f.w;
           if (whole) {
-            if (h0 + h < a.heads)
-              a.out[(int64_t)k.t * a.o_ts + (int64_t)(h0 + h) * a.o_hs + col] = f2bf_bits(r);
+            // neighbouring lanes trade heads, so that each stores two columns
+            const bool odd = lane & 1;
+            const float g0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
+            const float g1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? v2 : v3, 1);
+            const int h1 = h0 + h + odd;
+            uint16_t* o = a.out + (int64_t)k.t * a.o_ts + (int64_t)h1 * a.o_hs + 128 * j + (pos & ~1);
+            if (h1 < a.heads) *reinterpret_cast<uint32_t*>(o) = odd ? pack_bf16x2(g0, v1) : pack_bf16x2(v0, g0);
+            if (h1 + 2 < a.heads)
+              *reinterpret_cast<uint32_t*>(o + 2 * a.o_hs) = odd ? pack_bf16x2(g1, v3) : pack_bf16x2(v2, g1);
           } else {
-            a.part_o[((int64_t)slot * a.heads_pad + h0 + h) * kKvLora + col] = r;
+            attn_part(a, slot, (h0 + h) >> 2, 128 * j + pos) = make_float4(v0, v1, v2, v3);
           }
         }
       }

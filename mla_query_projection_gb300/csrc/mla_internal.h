@@ -239,8 +239,8 @@ struct AttnArgs {
   uint16_t* out;
   int64_t o_ts, o_hs;
   float* lse;      // or null
-  float* part_o;   // [2 * workers][heads_pad][512]
-  float* part_ml;  // [2 * workers][heads_pad][2]
+  float4* part_o;   // partial sums, see attn_part in mla_attn.cuh
+  float2* part_ml;  // [heads_pad][2 * workers] their maxima and denominators
   uint32_t* plan;  // [MLA_MAX_BATCH] for the joining kernel (mla_attn.cuh, AttnPlan)
   uint32_t* err;
   int heads, heads_pad, groups, batch;
