@@ -494,7 +494,8 @@ int mla_attn_create(mla_attn_t* out, int max_batch, int heads) {
     goto fail;
   }
   if (mla::prepare_mma_all<1>() != cudaSuccess || mla::prepare_mma_all<2>() != cudaSuccess ||
-      mla::prepare_mma_all<4>() != cudaSuccess || mla::prepare_attn_tc() != cudaSuccess)
+      mla::prepare_mma_all<4>() != cudaSuccess || mla::prepare_attn_tc() != cudaSuccess ||
+      mla::prepare_attn_ds() != cudaSuccess)
     goto fail;
   slots = (size_t)(h->num_sms / groups) * 2 * groups * gh;
   rc = MLA_ENOMEM;
@@ -585,7 +586,7 @@ int mla_attn_decode(mla_attn_t h, int batch, const void* q_latent, int64_t ql_to
   cudaError_t e;
   if (mla::attn_tc_serves(a)) {
     a.tile = mla::attn_tc_tile();
-    e = mla::launch_attn_tc(a, st);
+    e = layout == MLA_KV_FP8_DS_MLA ? mla::launch_attn_ds(a, st) : mla::launch_attn_tc(a, st);
   } else {
     a.tile = mla::kTile;
     e = mt == 1   ? mla::launch_mma<1>(a, st)

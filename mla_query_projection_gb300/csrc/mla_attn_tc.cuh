@@ -1,0 +1,487 @@
+// mla_attn_tc.cuh - what the two tcgen05 attention kernels share: descriptors,
+// MMA issue, TMEM access, the two-term weights and queries, bounded waits.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "mla_attn.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kTcTile = 128;               // cache rows a tile: MMA M of S^T, K of O^T
+constexpr int kPlane = kTcTile * 128;      // a 128-byte column plane of a tile
+constexpr int kTcSoft = 256;               // softmax threads (warps 0-7)
+constexpr int kTcThreads = kTcSoft + 64;   // + a TMA warp, an MMA warp
+constexpr int kTcBar = 1;                  // named barrier of the softmax threads
+constexpr long long kTcWait = 2000000000LL;  // ~1 s of SM clock
+// Weights are kept times 2^5, and the reference moves when a logit (base 2)
+// passes it by more than 3.75: 2^8.75 = 430 < 448, E4M3's largest.  (With 2^7
+// and 1.75 a sixth of the tiles of normally distributed logits moved it, at
+// 7,000 cycles each.)
+constexpr float kPShift = 5.0f, kPRoom = 3.75f;
+
+// Shared-memory matrix descriptors (tcgen05), version 1.  K-major, 128- or
+// 64-byte swizzle: 8-row groups `sbo` bytes apart.  M/N-major with 128-byte
+// swizzle: rows are K, 128 bytes of M or N each, groups of 8 K rows 1024 bytes
+// apart (`sbo`); one atom covers M or N, so the leading offset is unused.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t saddr, uint32_t sbo, uint32_t swizzle) {
+  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)1 << 16;
+  d |= (uint64_t)(sbo >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)swizzle << 61;  // 2: 128 B, 4: 64 B
+  return d;
+}
+
+// Instruction descriptor, FP32 accumulators: operand types (0 E4M3, 1 E5M2),
+// and whether A and B are M/N-major.
+__host__ __device__ constexpr uint32_t tc_idesc(int m, int n, int btype, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((uint32_t)btype << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// One elected lane of a converged warp issues; the warp runs the code around it
+// together, so that descriptors are computed in uniform registers (issued from
+// a single lane's branch, an MMA cost about 100 cycles to issue against the
+// 48 to 64 that it takes to run).
+__device__ __forceinline__ void tc_mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xFFFFFFFF;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Several MMAs into one accumulator by one elected lane: step k multiplies the
+// operands at a + k * AS and b + k * BS (16-byte units); tc_mma4x2 follows each
+// by the same A with B at BL more (its second term, idesc id1).
+#define TC_MMA_ENTER                                                     \
+  "{\n\t.reg .pred p, q, t;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t" \
+  "setp.eq.b32 t, %4, %4;\n\telect.sync _|q, 0xFFFFFFFF;\n\t"
+#define TC_MMA_NEXT(da, db) "add.s64 x, x, " da ";\n\tadd.s64 y, y, " db ";\n\t"
+#define TC_MMA_F8(id, pred) "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, " id ", " pred ";\n\t"
+#define TC_MMA_F16(id, pred) "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, " id ", " pred ";\n\t"
+template <int AS, int BS>
+__device__ __forceinline__ void tc_mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+                                        uint32_t accumulate) {
+  asm volatile(TC_MMA_ENTER "mov.b64 x, %1;\n\tmov.b64 y, %2;\n\t" TC_MMA_F8("%3", "p")
+               TC_MMA_NEXT("%5", "%6") TC_MMA_F8("%3", "t")
+               TC_MMA_NEXT("%5", "%6") TC_MMA_F8("%3", "t")
+               TC_MMA_NEXT("%5", "%6") TC_MMA_F8("%3", "t") "}" ::"r"(d),
+               "l"(a), "l"(b), "r"(id), "r"(accumulate), "n"(AS), "n"(BS)
+               : "memory");
+}
+template <int AS, int BS>
+__device__ __forceinline__ void tc_mma4_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+                                             uint32_t accumulate) {
+  asm volatile(TC_MMA_ENTER "mov.b64 x, %1;\n\tmov.b64 y, %2;\n\t" TC_MMA_F16("%3", "p")
+               TC_MMA_NEXT("%5", "%6") TC_MMA_F16("%3", "t")
+               TC_MMA_NEXT("%5", "%6") TC_MMA_F16("%3", "t")
+               TC_MMA_NEXT("%5", "%6") TC_MMA_F16("%3", "t") "}" ::"r"(d),
+               "l"(a), "l"(b), "r"(id), "r"(accumulate), "n"(AS), "n"(BS)
+               : "memory");
+}
+template <int AS, int BS, int BL>
+__device__ __forceinline__ void tc_mma4x2(uint32_t d, uint64_t a, uint64_t b, uint32_t id0,
+                                          uint32_t id1, uint32_t accumulate) {
+  asm volatile(TC_MMA_ENTER "mov.b64 x, %1;\n\tmov.b64 y, %2;\n\t"
+               TC_MMA_F8("%3", "p") TC_MMA_NEXT("0", "%7") TC_MMA_F8("%8", "t")
+               TC_MMA_NEXT("%5", "%6") TC_MMA_F8("%3", "t") TC_MMA_NEXT("0", "%7") TC_MMA_F8("%8", "t")
+               TC_MMA_NEXT("%5", "%6") TC_MMA_F8("%3", "t") TC_MMA_NEXT("0", "%7") TC_MMA_F8("%8", "t")
+               TC_MMA_NEXT("%5", "%6") TC_MMA_F8("%3", "t") TC_MMA_NEXT("0", "%7") TC_MMA_F8("%8", "t")
+               "}" ::"r"(d),
+               "l"(a), "l"(b), "r"(id0), "r"(accumulate), "n"(AS), "n"(BS - BL), "n"(BL), "r"(id1)
+               : "memory");
+}
+
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tc_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// This warp's 32 lanes x 8, 16 or 32 columns.  A load's values may be used
+// after tc_wait_ld and tc_landed (the compiler sees no other tie between the
+// wait and the registers that the loads fill).
+#define TC_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), \
+                    "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+#define TC_I8(v, i) "r"(__float_as_uint(v[i])), "r"(__float_as_uint(v[i + 1])), \
+                    "r"(__float_as_uint(v[i + 2])), "r"(__float_as_uint(v[i + 3])), \
+                    "r"(__float_as_uint(v[i + 4])), "r"(__float_as_uint(v[i + 5])), \
+                    "r"(__float_as_uint(v[i + 6])), "r"(__float_as_uint(v[i + 7]))
+template <int N>
+__device__ __forceinline__ void tc_ld(uint32_t addr, float (&v)[N]) {
+  uint32_t r[N];
+  if constexpr (N == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : TC_R8(r, 0)
+                 : "r"(addr));
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : TC_R8(r, 0), TC_R8(r, 8)
+        : "r"(addr));
+  } else {
+    static_assert(N == 32, "columns");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : TC_R8(r, 0), TC_R8(r, 8), TC_R8(r, 16), TC_R8(r, 24)
+        : "r"(addr));
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const float (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      TC_I8(v, 0), TC_I8(v, 8), TC_I8(v, 16), TC_I8(v, 24)
+      : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tc_landed(float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+
+// Packed FP32 pairs (one instruction for two sums or products).
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mov.b64 rc, {%6, %7};\n\tfma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+// 2^x by the hardware's approximation (2 ulp), subnormal results flushed.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A weight pair as the sum of two terms: E4M3 codes in the low half of the
+// result, E5M2 codes of the rest in the high half.  The pair is rounded to
+// FP16 first (2^-11, below the terms' 2^-7; FP16 reaches down to 2^-24, further
+// than E5M2).
+__device__ __forceinline__ uint32_t split_weights(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 p, g, d;\n\t.reg .b16 c, e;\n\t"
+      "cvt.rn.f16x2.f32 p, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 c, p;\n\t"
+      "cvt.rn.f16x2.e4m3x2 g, c;\n\t"
+      "sub.rn.f16x2 d, p, g;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 e, d;\n\t"
+      "mov.b32 %0, {c, e};\n\t}"
+      : "=r"(r)
+      : "f"(lo), "f"(hi));
+  return r;
+}
+
+// The same of an FP16 pair times an FP16 pair of factors.
+__device__ __forceinline__ uint32_t split_weights16(uint32_t p, uint32_t f) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 q, g, d;\n\t.reg .b16 c, e;\n\t"
+      "mul.rn.f16x2 q, %1, %2;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 c, q;\n\t"
+      "cvt.rn.f16x2.e4m3x2 g, c;\n\t"
+      "sub.rn.f16x2 d, q, g;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 e, d;\n\t"
+      "mov.b32 %0, {c, e};\n\t}"
+      : "=r"(r)
+      : "r"(p), "r"(f));
+  return r;
+}
+
+struct OpMax {
+  __device__ static float f(float a, float b) { return fmaxf(a, b); }
+};
+struct OpSum {
+  __device__ static float f(float a, float b) { return a + b; }
+};
+// Reduces N values (8, 16 or 32) over the 32 lanes of a warp, halving what a
+// lane carries at each step: lane l ends with the result of value l * N / 32.
+template <int N, class Op>
+__device__ __forceinline__ float lanes_reduce(const float (&in)[N]) {
+  const int lane = threadIdx.x & 31;
+  float v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = in[i];
+  int n = N;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = (lane & o) != 0;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i)
+        if (i < n) {
+          const float keep = up ? v[i + n] : v[i], send = up ? v[i] : v[i + n];
+          v[i] = Op::f(keep, __shfl_xor_sync(0xFFFFFFFFu, send, o));
+        }
+    } else {
+      v[0] = Op::f(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], o));
+    }
+  }
+  return v[0];
+}
+
+__device__ __forceinline__ void tc_barrier() {
+  asm volatile("bar.sync %0, %1;" ::"r"(kTcBar), "r"(kTcSoft) : "memory");
+}
+
+// A bounded wait that gives up for good: once one has run out, the thread
+// waits no more (its results do not count) and leaves.
+__device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, bool& dead) {
+  if (!dead && !mbar_wait_bounded(bar, parity, kTcWait)) dead = true;
+}
+
+// The same by a converged warp: its lanes go on together.
+__device__ __forceinline__ void tc_wait_warp(uint64_t* bar, uint32_t parity, bool& dead) {
+  tc_wait(bar, parity, dead);
+  dead = __any_sync(0xFFFFFFFFu, dead);
+}
+
+// Whether the phase is over, the same answer for the whole warp, at once (a
+// try_wait may hold the thread for a while).
+__device__ __forceinline__ bool tc_ready(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return __all_sync(0xFFFFFFFFu, ok != 0);
+}
+
+struct TcMaps {
+  CUtensorMap latent;  // boxes of box_rows x 128 bytes, 128-byte swizzle
+  CUtensorMap rope;    // boxes of box_rows x 64 bytes, 64-byte swizzle
+  int box_rows;        // a power of two that divides the page, 8..128
+};
+
+// This thread's column of planes 2 half and 2 half + 1 of O^T (at `ot`, NH
+// columns a plane), times factor[h] and the plane's f0 or f1: the output, or
+// the worker's part.
+template <int NH>
+__device__ __forceinline__ void tc_store_out(const AttnArgs& a, const AttnToken& k, uint32_t ot,
+                                             int half, int pos, int h0, int slot, bool whole,
+                                             const float* factor, float f0, float f1) {
+  const int lane = pos & 31;
+#pragma unroll 1
+  for (int c = 0; c < 2 * NH; c += 32) {
+    float v[32];
+    tc_ld(ot + 2 * half * NH + c, v);
+    tc_wait_ld();
+    tc_landed(v);
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      const int h = (c + e) % NH, j = 2 * half + (c + e) / NH;
+      const float4 f = *reinterpret_cast<const float4*>(factor + h);
+      const float fp = (c + e) / NH ? f1 : f0;
+      const float v0 = v[e] * (f.x * fp), v1 = v[e + 1] * (f.y * fp), v2 = v[e + 2] * (f.z * fp),
+                  v3 = v[e + 3] * (f.w * fp);
+      if (whole) {
+        // neighbouring lanes trade heads, so that each stores two columns
+        const bool odd = lane & 1;
+        const float g0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
+        const float g1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? v2 : v3, 1);
+        const int h1 = h0 + h + odd;
+        uint16_t* o = a.out + (int64_t)k.t * a.o_ts + (int64_t)h1 * a.o_hs + 128 * j + (pos & ~1);
+        if (h1 < a.heads) *reinterpret_cast<uint32_t*>(o) = odd ? pack_bf16x2(g0, v1) : pack_bf16x2(v0, g0);
+        if (h1 + 2 < a.heads)
+          *reinterpret_cast<uint32_t*>(o + 2 * a.o_hs) = odd ? pack_bf16x2(g1, v3) : pack_bf16x2(v2, g1);
+      } else {
+        attn_part(a, slot, (h0 + h) >> 2, 128 * j + pos) = make_float4(v0, v1, v2, v3);
+      }
+    }
+  }
+}
+
+// One token's queries of NH heads into shared memory as E4M3 terms (B of S^T):
+// warp w takes heads w, w + 8, ..; a lane holds 16 latent columns of each, and
+// lane 4 r + c the rope columns 16 c .. of the warp's r-th head.  Every load is
+// issued before the first is used.  xs[h] turns head h's accumulators into
+// logits in base 2 (`logit` times the inverse of its power of two).  Latent
+// planes at sq, rope rows at sr: E4M3 terms in 64-byte rows, or with ROPE16
+// BF16 times the same power of two in 128-byte rows.
+template <int NH, bool FP8Q, bool ROPE16>
+__device__ __forceinline__ void tc_queries(const AttnArgs& a, uint8_t* sq, uint8_t* sr, int t, int h0,
+                                           int warp, int lane, float logit, float* xs) {
+  constexpr int kQPlane = (FP8Q ? NH : 2 * NH) * 128;
+  constexpr int kN = NH / 8;  // heads a warp
+  constexpr int kV = FP8Q ? 1 : 2;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint4 lat[kN][kV], rope[kV];
+#pragma unroll
+  for (int r = 0; r < kN; ++r) {
+    const int h = h0 + warp + 8 * r;
+    const int64_t e = (int64_t)t * a.ql_ts + (int64_t)h * a.ql_hs + 16 * lane;
+    const uint4* p = reinterpret_cast<const uint4*>(a.q_latent + e * (FP8Q ? 1 : 2));
+#pragma unroll
+    for (int v = 0; v < kV; ++v) lat[r][v] = h < a.heads ? p[v] : zero;
+  }
+  {
+    const int r = lane >> 2, h = h0 + warp + 8 * r;
+    const int64_t e = (int64_t)t * a.qp_ts + (int64_t)h * a.qp_hs + 16 * (lane & 3);
+    const uint4* p = reinterpret_cast<const uint4*>(a.q_pe + e * (FP8Q ? 1 : 2));
+#pragma unroll
+    for (int v = 0; v < kV; ++v) rope[v] = r < kN && h < a.heads ? p[v] : zero;
+  }
+  auto put = [&](int row, uint4 w) {  // latent chunk `lane` of a B row
+    *reinterpret_cast<uint4*>(sq + (lane >> 3) * kQPlane + row * 128 +
+                              (((lane ^ row) & 7) << 4)) = w;
+  };
+  auto put_rope = [&](int row, uint4 w) {  // rope chunk lane % 4
+    *reinterpret_cast<uint4*>(sr + row * 64 + ((((lane & 3) ^ (row >> 1)) & 3) << 4)) = w;
+  };
+  auto put_rope16 = [&](int row, int c, uint4 w) {  // half c of rope columns 16 (lane % 4) ..
+    *reinterpret_cast<uint4*>(sr + row * 128 + (((2 * (lane & 3) + c) ^ row) & 7) * 16) = w;
+  };
+  const int rr = lane >> 2, rh = warp + 8 * rr;  // the head whose rope this lane holds
+  if constexpr (FP8Q) {
+#pragma unroll
+    for (int r = 0; r < kN; ++r) put(warp + 8 * r, lat[r][0]);
+    if (rr < kN) {
+      if constexpr (ROPE16) {
+        const uint32_t w[4] = {rope[0].x, rope[0].y, rope[0].z, rope[0].w};
+        uint32_t c[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float v[4];
+          e4m3x4_values(w[e], v);
+          c[2 * e] = pack_bf16x2(v[0], v[1]);
+          c[2 * e + 1] = pack_bf16x2(v[2], v[3]);
+        }
+        put_rope16(rh, 0, make_uint4(c[0], c[1], c[2], c[3]));
+        put_rope16(rh, 1, make_uint4(c[4], c[5], c[6], c[7]));
+      } else {
+        put_rope(rh, rope[0]);
+      }
+    }
+    if (lane < kN) xs[warp + 8 * lane] = logit;
+  } else {
+    // magnitudes as bits order like the values (NaN above infinity)
+    auto magnitude = [](uint4 w) {
+      const uint32_t s = 0x7FFF7FFFu;
+      return __vmaxu2(__vmaxu2(w.x & s, w.y & s), __vmaxu2(w.z & s, w.w & s));
+    };
+    // A pair of columns times a power of two as two E4M3 terms: the first's
+    // codes in the low half of the result, the rest's in the high half (FP16
+    // holds the scaled values, at most 448, exactly down to 2^-17).
+    auto split2 = [](uint32_t w, float up) {
+      const float2 v = fmul2_rn(make_float2(bf16lo(w), bf16hi(w)), make_float2(up, up));
+      uint32_t r;
+      asm("{\n\t.reg .b32 p, g, d;\n\t.reg .b16 c, e;\n\t"
+          "cvt.rn.f16x2.f32 p, %2, %1;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f16x2 c, p;\n\t"
+          "cvt.rn.f16x2.e4m3x2 g, c;\n\t"
+          "sub.rn.f16x2 d, p, g;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f16x2 e, d;\n\t"
+          "mov.b32 %0, {c, e};\n\t}"
+          : "=r"(r)
+          : "f"(v.x), "f"(v.y));
+      return r;
+    };
+    auto split = [&](const uint4* w, float up, uint4* hi, uint4* lo) {
+      uint32_t c[4], d[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint4 q = w[e >> 1];
+        const uint32_t x = split2(e & 1 ? q.z : q.x, up), y = split2(e & 1 ? q.w : q.y, up);
+        c[e] = __byte_perm(x, y, 0x5410);
+        d[e] = __byte_perm(x, y, 0x7632);
+      }
+      *hi = make_uint4(c[0], c[1], c[2], c[3]);
+      *lo = make_uint4(d[0], d[1], d[2], d[3]);
+    };
+    const uint32_t rope_mag = __vmaxu2(magnitude(rope[0]), magnitude(rope[kV - 1]));
+    float rope_up = 0.f;
+#pragma unroll
+    for (int r = 0; r < kN; ++r) {
+      uint32_t m = __vmaxu2(magnitude(lat[r][0]), magnitude(lat[r][kV - 1]));
+      if (!ROPE16 && rr == r) m = __vmaxu2(m, rope_mag);
+      m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+      // the power of two that brings the largest into (224, 448]: from its
+      // exponent field, kept where both it and its inverse are normal
+      int ex = (int)(m >> 7) - 127;
+      ex = max(-100, min(ex, 126));
+      if ((m & 0x7Fu) <= 0x60u) --ex;
+      const float up = __uint_as_float((uint32_t)(127 + 7 - ex) << 23);
+      float x = logit * __uint_as_float((uint32_t)(127 - 7 + ex) << 23);
+      // an infinite query: no finite logits (E4M3 has no infinity)
+      if (m >= 0x7F80u) x = __int_as_float(0x7FC00000);
+      uint4 hi, lo;
+      split(lat[r], up, &hi, &lo);
+      put(warp + 8 * r, hi);
+      put(NH + warp + 8 * r, lo);
+      if (lane == 0) xs[warp + 8 * r] = x;
+      if (rr == r) rope_up = up;
+    }
+    if (rr < kN) {
+      if constexpr (ROPE16) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t w[4] = {rope[e].x, rope[e].y, rope[e].z, rope[e].w};
+          uint32_t c[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) c[k] = pack_bf16x2(bf16lo(w[k]) * rope_up, bf16hi(w[k]) * rope_up);
+          put_rope16(rh, e, make_uint4(c[0], c[1], c[2], c[3]));
+        }
+      } else {
+        uint4 hi, lo;
+        split(rope, rope_up, &hi, &lo);
+        put_rope(rh, hi);
+        put_rope(NH + rh, lo);
+      }
+    }
+  }
+}
+
+// A map of the cache's rows in boxes of box_rows x box_bytes (64 or 128, with the
+// swizzle of that width).
+inline bool encode_plane_map(CUtensorMap* map, const AttnArgs& a, int row_bytes, int box_bytes,
+                      int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)(a.num_pages * a.page_size)};
+  cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  cuuint32_t box[2] = {(cuuint32_t)box_bytes, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(a.cache), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+}  // namespace mla

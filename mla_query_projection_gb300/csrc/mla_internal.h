@@ -251,14 +251,17 @@ struct AttnArgs {
 // The driver's tensor-map encoder (null where it cannot be had).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
-// The tcgen05 kernel (mla_attn_tc.cu): whether it serves a call (an E4M3 row
-// under one scale, pages of a multiple of 8 rows, row numbers within 31
-// bits), its heads a CTA and rows a tile.
+// The tcgen05 kernels (mla_attn_tc.cu, mla_attn_ds.cu): whether they serve a
+// call (E4M3 codes, pages of a multiple of 8 rows, row numbers within 31
+// bits), their heads a CTA and rows a tile.
 bool attn_tc_serves(const AttnArgs& a);
 int attn_tc_heads(int heads);
 int attn_tc_tile();
 cudaError_t prepare_attn_tc();
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t stream);
+// The same for fp8_ds_mla rows (mla_attn_ds.cu).
+cudaError_t prepare_attn_ds();
+cudaError_t launch_attn_ds(const AttnArgs& a, cudaStream_t stream);
 
 // Block tables and slot map of a step (mla_tables.cu).
 struct TableArgs {
