@@ -25,6 +25,7 @@ struct MeanShape {
   static constexpr int kChunks = RowChunks<LAYOUT>::kChunks;
   static constexpr int kGroups = kChunks > 20 ? 8 : 14;
   static constexpr int kThreads = kChunks * kGroups;
+  static constexpr int kDeep = kChunks > 20 ? 8 : 5;  // rows a thread has in flight (a 64-row page)
 };
 
 template <int LAYOUT>
@@ -51,14 +52,24 @@ __global__ void __launch_bounds__(MeanShape<LAYOUT>::kThreads)
     float acc[R::kMax];
 #pragma unroll
     for (int i = 0; i < R::kMax; ++i) acc[i] = 0.f;
-#pragma unroll 4
-    for (int t = group; t < filled; t += M::kGroups) {
-      const uint8_t* row = base + (int64_t)t * R::kBytes;
-      const uint4 w = *reinterpret_cast<const uint4*>(row + R::offset(chunk));
-      float v[R::kMax];
-      R::decode(row, chunk, w, v);
+    for (int t0 = group; t0 < filled; t0 += M::kGroups * M::kDeep) {
+      uint4 w[M::kDeep];
 #pragma unroll
-      for (int i = 0; i < R::kMax; ++i) acc[i] += v[i];
+      for (int d = 0; d < M::kDeep; ++d) {
+        const int t = t0 + d * M::kGroups;
+        if (t < filled)
+          w[d] = *reinterpret_cast<const uint4*>(base + (int64_t)t * R::kBytes + R::offset(chunk));
+      }
+#pragma unroll
+      for (int d = 0; d < M::kDeep; ++d) {
+        const int t = t0 + d * M::kGroups;
+        if (t < filled) {
+          float v[R::kMax];
+          R::decode(base + (int64_t)t * R::kBytes, chunk, w[d], v);
+#pragma unroll
+          for (int i = 0; i < R::kMax; ++i) acc[i] += v[i];
+        }
+      }
     }
     const int col = R::col(chunk), width = R::width(chunk);
 #pragma unroll
@@ -94,8 +105,9 @@ constexpr int kScorePitch = kRowElems * 2 + 64;  // 1216: 16-byte loads of 8 row
 template <int NT, bool FP8Q>
 __global__ void __launch_bounds__(256) mla_blocks_score_kernel(const ScoreArgs s) {
   constexpr int kTile = 8 * NT;
-  __shared__ __align__(16) uint8_t keys[kTile * kScorePitch];
+  extern __shared__ __align__(16) uint8_t keys[];  // [kTile][kScorePitch]
   __shared__ float best[8][kTile];
+  __shared__ int64_t pages[kTile];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q4 = lane & 3;
   pdl_launch_dependents();
@@ -116,18 +128,30 @@ __global__ void __launch_bounds__(256) mla_blocks_score_kernel(const ScoreArgs s
       if (j0 + j < s.bt_stride) out[j0 + j] = -INFINITY;
     return;
   }
+  if (tid < kTile) {
+    int64_t page = -1;
+    if (j0 + tid < nb) {
+      page = s.block_table[(int64_t)row * s.bt_stride + j0 + tid];
+      if (page < 0 || page >= s.num_pages) {
+        page = -1;
+        if (s.flags != nullptr) atomicOr(s.flags, MLA_DEVERR_BAD_SLOT);
+      }
+    }
+    pages[tid] = page;
+  }
+  __syncthreads();
+  // the means by 16-byte asynchronous copies, all in flight at once
   for (int c = tid; c < kTile * (kRowElems / 8); c += 256) {
     const int b = c / (kRowElems / 8), k = c % (kRowElems / 8);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (j0 + b < nb) {
-      const int64_t page = s.block_table[(int64_t)row * s.bt_stride + j0 + b];
-      if (page >= 0 && page < s.num_pages)
-        v = *reinterpret_cast<const uint4*>(s.mean + page * kRowElems + 8 * k);
-      else if (k == 0 && s.flags != nullptr)
-        atomicOr(s.flags, MLA_DEVERR_BAD_SLOT);
-    }
-    *reinterpret_cast<uint4*>(keys + b * kScorePitch + 16 * k) = v;
+    uint8_t* d = keys + b * kScorePitch + 16 * k;
+    if (pages[b] >= 0)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(d)),
+                   "l"(s.mean + pages[b] * kRowElems + 8 * k)
+                   : "memory");
+    else
+      *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
   }
+  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
   __syncthreads();
   float mx[NT][2];
 #pragma unroll
@@ -206,24 +230,26 @@ __global__ void __launch_bounds__(256) mla_blocks_score_kernel(const ScoreArgs s
       v = isnan(u) || isnan(v) ? NAN : fmaxf(u, v);
     }
     if (FP8Q) v = v / inv;
-    bool in = j0 + j < nb;
-    if (in) {
-      const int64_t page = s.block_table[(int64_t)row * s.bt_stride + j0 + j];
-      in = page >= 0 && page < s.num_pages;
-    }
-    out[j0 + j] = in ? v : -INFINITY;
+    out[j0 + j] = pages[j] >= 0 ? v : -INFINITY;
   }
 }
 
 // --------------------------------------------------------------- selection
 //
 // The k blocks with the highest scores, ascending.  A score becomes a 32-bit
-// key that orders like it; four histogram passes over 8 bits each, from the
-// top, narrow the k-th key down; then one pass in block order keeps every key
-// above it and, of those equal, the first ones.  All sums are counts, so the
-// result does not depend on the order of the atomics.
+// key that orders like it; the k-th largest key is found by its leading 11,
+// then 11, then 10 bits, each digit from a histogram of the keys that share
+// the bits so far (2,048 bins: enough that the keys of a warp seldom meet in
+// one); then one pass in block order keeps every key above it and, of those
+// equal, the first ones.  All sums are counts, so the result does not depend
+// on the order of the atomics.  Keys stay in registers (up to 16 a thread;
+// beyond 8,192 blocks they are formed again from the scores in each pass).
+// Bound by latency: the barriers of the passes.
 
 constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelKeys = 16;  // a thread, in registers
+constexpr int kSelBins = 2048;
 
 __device__ __forceinline__ uint32_t score_key(float v, bool forced) {
   if (forced) v = INFINITY;
@@ -233,12 +259,14 @@ __device__ __forceinline__ uint32_t score_key(float v, bool forced) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) mla_blocks_select_kernel(const SelectArgs s) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t wsum[2][kSelThreads / 32];
-  __shared__ uint32_t pick_digit, pick_above;
+template <bool REGS>
+__global__ void __launch_bounds__(kSelThreads, 2) mla_blocks_select_kernel(const SelectArgs s) {
+  __shared__ __align__(16) uint32_t hist[kSelBins];
+  __shared__ uint32_t counts[kSelWarps], pick_bin, pick_above, pick_all;
+  __shared__ uint32_t place[kSelKeys * kSelWarps];  // (chunk, warp): above << 16 | equal
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_launch_dependents();
+  reinterpret_cast<uint4*>(hist)[tid] = make_uint4(0, 0, 0, 0);
   pdl_wait();
   const int t = blockIdx.x;
   const float* sc = s.scores + (int64_t)t * s.scores_stride;
@@ -246,91 +274,132 @@ __global__ void __launch_bounds__(kSelThreads) mla_blocks_select_kernel(const Se
   const int64_t ps = s.page_size;
   const int n = (int)min((max((int64_t)s.lens[t], (int64_t)0) + ps - 1) / ps, (int64_t)s.max_blocks);
   const int k = min(s.k, n);
+  const int last0 = n - s.keep_last;
+  auto key_at = [&](int j) { return score_key(sc[j], j < s.keep_first || j >= last0); };
+  uint32_t keys[REGS ? kSelKeys : 1];
+  if (REGS) {
+#pragma unroll
+    for (int c = 0; c < kSelKeys; ++c) {
+      const int j = c * kSelThreads + tid;
+      keys[REGS ? c : 0] = j < n ? key_at(j) : 0u;
+    }
+  }
   for (int j = k + tid; j < s.k; j += kSelThreads) out[j] = -1;
   if (tid == 0) s.sel_count[t] = k;
   if (k == n) {
     for (int j = tid; j < n; j += kSelThreads) out[j] = j;
     return;
   }
-  const int last0 = n - s.keep_last;
-  auto key_at = [&](int j) { return score_key(sc[j], j < s.keep_first || j >= last0); };
-  uint32_t prefix = 0, need = (uint32_t)k;  // `need` of the keys that share the prefix
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int b = tid; b < 256; b += kSelThreads) hist[b] = 0;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    for (int j0 = 0; j0 < n; j0 += kSelThreads) {
-      const int j = j0 + tid;
-      const uint32_t key = j < n ? key_at(j) : 0u;
-      const bool in = j < n && (key & mask) == prefix;
-      const uint32_t digit = in ? (key >> shift) & 255u : 256u;
-      // one atomic for the lanes of a warp that share a digit
-      const uint32_t same = __match_any_sync(0xFFFFFFFFu, digit);
-      if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], (uint32_t)__popc(same));
+  uint32_t kth = 0, need = (uint32_t)k;  // the bits found; keys needed among those that share them
+  __syncthreads();                       // hist is clear
+  int shift = 21, bits = 11;
+  while (true) {
+    const uint32_t mask = shift == 21 ? 0u : 0xFFFFFFFFu << (shift + bits);
+    auto put = [&](uint32_t key) {
+      if ((key & mask) == kth) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1u)], 1u);
+    };
+    if (REGS) {
+#pragma unroll
+      for (int c = 0; c < kSelKeys; ++c)
+        if (c * kSelThreads + tid < n) put(keys[REGS ? c : 0]);
+    } else {
+      for (int j = tid; j < n; j += kSelThreads) put(key_at(j));
     }
     __syncthreads();
-    if (warp == 0) {
-      // lane l holds digits 255 - 8 l .. 248 - 8 l: counts from the top
-      uint32_t c[8], sum = 0;
+    // this thread's four bins, counted from the top, and cleared for the next pass
+    uint4* mine = reinterpret_cast<uint4*>(hist) + (kSelThreads - 1 - tid);
+    const uint4 h = *mine;
+    *mine = make_uint4(0, 0, 0, 0);
+    const uint32_t c[4] = {h.w, h.z, h.y, h.x};
+    const uint32_t sum = c[0] + c[1] + c[2] + c[3];
+    uint32_t inc = sum;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        c[i] = hist[255 - 8 * lane - i];
-        sum += c[i];
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    if (lane == 31) counts[warp] = inc;
+    __syncthreads();
+    uint32_t before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? counts[lane & (kSelWarps - 1)] : 0u);
+    before += inc - sum;
+    if (before < need && before + sum >= need) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (before < need && before + c[e] >= need) {
+          pick_bin = (uint32_t)(kSelBins - 1 - 4 * tid - e);
+          pick_above = before;
+          pick_all = before + c[e] == need;  // the whole bin is in
+        }
+        before += c[e];
+      }
+    }
+    __syncthreads();
+    kth |= pick_bin << shift;
+    need -= pick_above;
+    if (pick_all || shift == 0) break;
+    if (shift == 21) {
+      shift = 10;
+    } else {
+      shift = 0;
+      bits = 10;
+    }
+  }
+  // Keys above the bits found (those that share them are `equal`, and where the
+  // search stopped early all of them are in) ...
+  const uint32_t low = shift == 0 ? 0u : (1u << shift) - 1u;
+  const uint32_t top = kth | low;
+  // ... and of those equal the first `need`.
+  uint32_t base = 0, ties = 0;
+  const uint32_t below = (1u << lane) - 1u;
+  for (int j00 = 0; j00 < n; j00 += kSelKeys * kSelThreads) {
+    uint32_t bg[kSelKeys], be[kSelKeys];
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < kSelKeys; ++c) {
+      const int j = j00 + c * kSelThreads + tid;
+      const uint32_t key = REGS ? keys[REGS ? c : 0] : j < n ? key_at(j) : 0u;
+      bg[c] = __ballot_sync(0xFFFFFFFFu, j < n && key > top);
+      be[c] = __ballot_sync(0xFFFFFFFFu, j < n && key >= kth && key <= top);
+      if (lane == 0) place[c * kSelWarps + warp] = (uint32_t)__popc(bg[c]) << 16 | __popc(be[c]);
+    }
+    __syncthreads();
+    // exclusive sums over (chunk, warp), by the first warp, eight entries a lane
+    uint32_t sum_all = 0;
+    if (warp == 0) {
+      uint32_t v[8], sum = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e] = place[8 * lane + e];
+        sum += v[e];
       }
       uint32_t inc = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= o) inc += x;
+        const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += u;
       }
-      uint32_t above = inc - sum;
-      if (above < need && inc >= need) {
+      uint32_t ex = inc - sum;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (above < need && above + c[i] >= need) {
-            pick_digit = 255 - 8 * lane - i;
-            pick_above = above;
-            break;
-          }
-          above += c[i];
-        }
+      for (int e = 0; e < 8; ++e) {
+        place[8 * lane + e] = ex;
+        ex += v[e];
       }
+      sum_all = __shfl_sync(0xFFFFFFFFu, inc, 31);
+      if (lane == 0) pick_all = sum_all;
     }
     __syncthreads();
-    prefix |= pick_digit << shift;
-    need -= pick_above;
-    __syncthreads();
-  }
-  // keys above `prefix` are all in; of those equal to it the first `need`
-  uint32_t base = 0, ties = 0;
-  for (int j0 = 0; j0 < n; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    const uint32_t key = j < n ? key_at(j) : 0u;
-    const bool gt = j < n && key > prefix, eq = j < n && key == prefix;
-    const uint32_t bg = __ballot_sync(0xFFFFFFFFu, gt), be = __ballot_sync(0xFFFFFFFFu, eq);
-    if (lane == 0) {
-      wsum[0][warp] = __popc(bg);
-      wsum[1][warp] = __popc(be);
-    }
-    __syncthreads();
-    uint32_t g0 = 0, e0 = 0, gt_all = 0, eq_all = 0;
+    sum_all = pick_all;
 #pragma unroll
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      if (w == warp) {
-        g0 = gt_all;
-        e0 = eq_all;
-      }
-      gt_all += wsum[0][w];
-      eq_all += wsum[1][w];
+    for (int c = 0; c < kSelKeys; ++c) {
+      const int j = j00 + c * kSelThreads + tid;
+      const uint32_t at = place[c * kSelWarps + warp];
+      const uint32_t g = base + (at >> 16) + __popc(bg[c] & below);
+      const uint32_t e = ties + (at & 0xFFFFu) + __popc(be[c] & below);
+      if (bg[c] >> lane & 1u) out[g + min(e, need)] = j;
+      if ((be[c] >> lane & 1u) && e < need) out[g + e] = j;
     }
-    const uint32_t below = (1u << lane) - 1u;
-    g0 += __popc(bg & below);
-    e0 += ties + __popc(be & below);
-    if (gt) out[base + g0 + min(e0, need)] = j;
-    if (eq && e0 < need) out[base + g0 + e0] = j;
-    base += gt_all;
-    ties += eq_all;
-    __syncthreads();
+    base += sum_all >> 16;
+    ties += sum_all & 0xFFFFu;
   }
 }
 
@@ -364,21 +433,38 @@ cudaError_t launch_blocks_mean(const MeanArgs& m, int num_sms, cudaStream_t stre
   }
 }
 
-cudaError_t launch_blocks_score(const ScoreArgs& s, int num_sms, cudaStream_t stream) {
-  // 16 blocks a CTA: their means are 18 KiB, and several CTAs share an SM
-  constexpr int NT = 2;
-  (void)num_sms;
+namespace {
+template <int NT, bool FP8Q>
+cudaError_t launch_score(const ScoreArgs& s, cudaStream_t stream) {
+  constexpr int kBytes = 8 * NT * kScorePitch;
+  auto kernel = mla_blocks_score_kernel<NT, FP8Q>;
+  if constexpr (kBytes > 40 * 1024) {  // beyond the default limit, on the device in use
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((s.bt_stride + 8 * NT - 1) / (8 * NT)), (unsigned)s.batch, 1);
   cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return s.q_scale_inv != nullptr ? cudaLaunchKernelEx(&cfg, mla_blocks_score_kernel<NT, true>, s)
-                                  : cudaLaunchKernelEx(&cfg, mla_blocks_score_kernel<NT, false>, s);
+  return cudaLaunchKernelEx(&cfg, kernel, s);
+}
+}  // namespace
+
+cudaError_t launch_blocks_score(const ScoreArgs& s, int num_sms, cudaStream_t stream) {
+  // A CTA reads its token's queries once (128 heads: 147 KB), whatever its
+  // tile: 64 blocks where that still fills the SMs, 16 blocks for few tokens.
+  // (64 tokens of up to 256 blocks at 128 heads: 17.5 us with 16 blocks, 1,024
+  // CTAs reading 150 MB of queries.)
+  const bool large = (s.bt_stride + 63) / 64 * s.batch >= num_sms;
+  if (s.q_scale_inv != nullptr)
+    return large ? launch_score<8, true>(s, stream) : launch_score<2, true>(s, stream);
+  return large ? launch_score<8, false>(s, stream) : launch_score<2, false>(s, stream);
 }
 
 cudaError_t launch_blocks_select(const SelectArgs& s, cudaStream_t stream) {
@@ -391,7 +477,9 @@ cudaError_t launch_blocks_select(const SelectArgs& s, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mla_blocks_select_kernel, s);
+  return s.max_blocks <= kSelKeys * kSelThreads
+             ? cudaLaunchKernelEx(&cfg, mla_blocks_select_kernel<true>, s)
+             : cudaLaunchKernelEx(&cfg, mla_blocks_select_kernel<false>, s);
 }
 
 }  // namespace mla

@@ -12,7 +12,7 @@
 //
 // What bounds it is latency: a decode step moves a few KiB.  So it is one
 // launch of one thread-block cluster: every CTA scans all requests (at most
-// 4096, four a thread, redundantly: a scan costs less than handing its result
+// 4096, redundantly: a scan costs less than handing its result
 // over), pushes its share of the released pages, and after the one cluster
 // barrier pops pages and writes its share of the outputs.  The barrier is also
 // what lets lens_out and free_count_out alias their inputs: every CTA has read
@@ -25,7 +25,6 @@
 namespace mla {
 namespace {
 
-constexpr int kTabRowsPerThread = 4;
 constexpr int kTabCluster = 8;  // CTAs of a large step (portable cluster size)
 
 constexpr int kGiveNone = -1, kGiveNothing = -2;
@@ -40,43 +39,56 @@ struct TabSmem {  // per request; sized by rows
   int32_t* len;    // length before
 };
 
-// Inclusive block-wide sums of two 64-bit values; returns this thread's
-// inclusive prefix in a, b and the totals in ta, tb.
-__device__ __forceinline__ void block_scan2(int64_t& a, int64_t& b, int64_t& ta, int64_t& tb,
-                                            int64_t* red) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+struct Sum3 {
+  int64_t f, p, t;  // pages given back, pages taken, tokens
+};
+__device__ __forceinline__ Sum3 warp_scan(Sum3 v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, a, o), y = __shfl_up_sync(0xFFFFFFFFu, b, o);
+    const int64_t f = __shfl_up_sync(0xFFFFFFFFu, v.f, o), p = __shfl_up_sync(0xFFFFFFFFu, v.p, o),
+                  t = __shfl_up_sync(0xFFFFFFFFu, v.t, o);
     if (lane >= o) {
-      a += x;
-      b += y;
+      v.f += f;
+      v.p += p;
+      v.t += t;
     }
   }
-  __syncthreads();
-  if (lane == 31) {
-    red[warp] = a;
-    red[32 + warp] = b;
-  }
-  __syncthreads();
-  int64_t pa = 0, pb = 0;
-  ta = 0;
-  tb = 0;
-  for (int w = 0; w < nw; ++w) {
-    if (w == warp) {
-      pa = ta;
-      pb = tb;
-    }
-    ta += red[w];
-    tb += red[32 + w];
-  }
-  a += pa;
-  b += pb;
+  return v;
 }
 
+// Inclusive block-wide sums (the warps' totals are summed by every warp for
+// itself); returns the block's total too.
+__device__ __forceinline__ Sum3 block_scan(Sum3 v, Sum3* total, Sum3* red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  v = warp_scan(v, lane);
+  if (lane == 31) red[warp] = v;
+  __syncthreads();
+  const Sum3 w = warp_scan(lane < nw ? red[lane] : Sum3{0, 0, 0}, lane);
+  const int before = warp > 0 ? warp - 1 : 0;
+  const int64_t f = __shfl_sync(0xFFFFFFFFu, w.f, before), p = __shfl_sync(0xFFFFFFFFu, w.p, before),
+                t = __shfl_sync(0xFFFFFFFFu, w.t, before);
+  if (warp > 0) {
+    v.f += f;
+    v.p += p;
+    v.t += t;
+  }
+  total->f = __shfl_sync(0xFFFFFFFFu, w.f, 31);
+  total->p = __shfl_sync(0xFFFFFFFFu, w.p, 31);
+  total->t = __shfl_sync(0xFFFFFFFFu, w.t, 31);
+  return v;
+}
+
+// Blocks that v positions fill (v up to 2^32 - 2).
+__device__ __forceinline__ uint32_t blocks_of(uint32_t v, uint32_t page_size) {
+  const uint32_t q = v / page_size;
+  return q + (v - q * page_size != 0);
+}
+
+// RPT: consecutive requests a thread has.
+template <int RPT>
 __global__ void __launch_bounds__(1024) mla_tables_kernel(const TableArgs t) {
   extern __shared__ int32_t tab_smem[];
-  __shared__ int64_t red[64];
+  __shared__ Sum3 red[32];
   __shared__ int fail_row;
   const int R = t.rows;
   const TabSmem s{tab_smem, tab_smem + R, tab_smem + 2 * R, tab_smem + 3 * R, tab_smem + 4 * R,
@@ -88,30 +100,32 @@ __global__ void __launch_bounds__(1024) mla_tables_kernel(const TableArgs t) {
   pdl_launch_dependents();
   pdl_wait();
 
-  // ---- this thread's requests 4 tid .. 4 tid + 3
-  const int r0 = tid * kTabRowsPerThread;
-  int64_t have[kTabRowsPerThread], freed[kTabRowsPerThread], take[kTabRowsPerThread],
-      toks[kTabRowsPerThread];
-  bool released[kTabRowsPerThread];
+  // ---- this thread's requests
+  const int r0 = tid * RPT;
+  int32_t len[RPT], have[RPT], take[RPT], toks[RPT];
+  bool released[RPT];
   bool refused = false;
-  int64_t sum_f = 0, sum_p = 0, sum_t = 0, unused = 0;
+  Sum3 sum{0, 0, 0};
+  int32_t count = *t.free_count;
 #pragma unroll
-  for (int i = 0; i < kTabRowsPerThread; ++i) {
-    have[i] = freed[i] = take[i] = toks[i] = 0;
+  for (int i = 0; i < RPT; ++i) {
+    len[i] = have[i] = take[i] = toks[i] = 0;
     released[i] = false;
     const int r = r0 + i;
     if (r < R) {
-      const int64_t len = t.lens[r], nw = t.new_tokens[r];
-      const bool sound = len >= 0 && (len + ps - 1) / ps <= t.bt_stride;
-      if (sound) {
-        have[i] = (len + ps - 1) / ps;
+      const int32_t ln = t.lens[r], nw = t.new_tokens[r];
+      len[i] = ln;
+      const uint32_t held = blocks_of((uint32_t)max(ln, 0), (uint32_t)t.page_size);
+      if (ln >= 0 && held <= t.bt_stride) {
+        have[i] = (int32_t)held;
         if (nw < 0) {
-          freed[i] = have[i];
           released[i] = true;
+          sum.f += held;
         } else if (nw > 0) {
-          const int64_t need = (len + nw + ps - 1) / ps;
-          if (need <= t.bt_stride && len + nw <= 0x7FFFFFFF) {
-            take[i] = need - have[i];
+          const uint32_t after = (uint32_t)ln + (uint32_t)nw;
+          const uint32_t need = blocks_of(after, (uint32_t)t.page_size);
+          if (need <= t.bt_stride && after <= 0x7FFFFFFFu) {
+            take[i] = (int32_t)(need - held);
             toks[i] = nw;
           } else {
             refused = true;  // its row of the block table cannot hold it
@@ -121,29 +135,27 @@ __global__ void __launch_bounds__(1024) mla_tables_kernel(const TableArgs t) {
         refused = true;
       }
     }
-    sum_f += freed[i];
-    sum_p += take[i];
-    sum_t += toks[i];
+    sum.p += take[i];
+    sum.t += toks[i];
   }
-  int64_t in_f = sum_f, in_p = sum_p, in_t = sum_t, tot_f, tot_p, tot_t, zero;
-  block_scan2(in_p, in_t, tot_p, tot_t, red);
-  block_scan2(in_f, unused, tot_f, zero, red);
-  int64_t count = *t.free_count;
+  Sum3 all;
+  const Sum3 in = block_scan(sum, &all, red);
   if (count < 0 || count > t.num_pages) {
     count = 0;
     refused = true;
   }
   // stack places that the array cannot hold are left out (more pages given
   // back than exist)
+  const int64_t tot_f = all.f;
   const int64_t avail = min(count + tot_f, t.num_pages);
   if (count + tot_f > t.num_pages) refused = true;
 
   // ---- who fits; the first that does not
-  int64_t ex_f = in_f - sum_f, ex_p = in_p - sum_p, ex_t = in_t - sum_t;
+  const int64_t ex_f = in.f - sum.f, ex_p = in.p - sum.p, ex_t = in.t - sum.t;
   {
     int64_t p = ex_p, k = ex_t;
 #pragma unroll
-    for (int i = 0; i < kTabRowsPerThread; ++i) {
+    for (int i = 0; i < RPT; ++i) {
       p += take[i];
       k += toks[i];
       if (toks[i] > 0 && (p > avail || k > t.max_tokens)) {
@@ -158,18 +170,18 @@ __global__ void __launch_bounds__(1024) mla_tables_kernel(const TableArgs t) {
   {
     int64_t f = ex_f, p = ex_p, k = ex_t;
 #pragma unroll
-    for (int i = 0; i < kTabRowsPerThread; ++i) {
+    for (int i = 0; i < RPT; ++i) {
       const int r = r0 + i;
       if (r < R) {
-        const bool in = toks[i] > 0 && r < stop;
-        s.len[r] = t.lens[r];
-        s.have[r] = (int32_t)have[i];
-        s.give[r] = !released[i] ? kGiveNone : freed[i] > 0 ? (int32_t)f : kGiveNothing;
-        s.take[r] = in ? (int32_t)take[i] : 0;
+        const bool in_step = toks[i] > 0 && r < stop;
+        s.len[r] = len[i];
+        s.have[r] = have[i];
+        s.give[r] = !released[i] ? kGiveNone : have[i] > 0 ? (int32_t)f : kGiveNothing;
+        s.take[r] = in_step ? take[i] : 0;
         s.first[r] = (int32_t)min(p, (int64_t)0x7FFFFFFF);
         k += toks[i];
-        s.cu[r] = r < stop ? (int32_t)k : -1;  // -1: the admitted total, below
-        f += freed[i];
+        s.cu[r] = (int32_t)min(k, (int64_t)0x7FFFFFFF);  // from `stop` on: the admitted total, below
+        if (released[i]) f += have[i];
         p += take[i];
       }
     }
@@ -179,9 +191,10 @@ __global__ void __launch_bounds__(1024) mla_tables_kernel(const TableArgs t) {
   const int32_t all_tokens = stop > 0 ? s.cu[stop - 1] : 0;
   int64_t taken = 0;
   if (stop > 0) taken = (int64_t)s.first[stop - 1] + s.take[stop - 1];
-  __syncthreads();
-  for (int r = tid; r < R; r += nt)
-    if (r >= stop) s.cu[r] = all_tokens;
+  if (stop < R) {
+    __syncthreads();
+    for (int r = stop + tid; r < R; r += nt) s.cu[r] = all_tokens;
+  }
 
   // ---- released pages onto the stack, a warp a request
   const int lane = tid & 31;
@@ -216,34 +229,51 @@ __global__ void __launch_bounds__(1024) mla_tables_kernel(const TableArgs t) {
     *t.free_count_out = (int32_t)(avail - taken);
   }
 
-  // ---- the tokens, padded behind the last
-  for (int64_t k = (int64_t)rank * nt + tid; k < t.max_tokens; k += (int64_t)ctas * nt) {
-    int64_t slot = -1;
-    int32_t row = -1, len = 0;
-    if (k < all_tokens) {
-      int lo = 0, hi = R - 1;  // the first request whose inclusive offset passes k
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (s.cu[mid] > k)
-          hi = mid;
-        else
-          lo = mid + 1;
+  // ---- the tokens, padded behind the last, four a thread at a time (their
+  // trips to the table and the stack overlap)
+  constexpr int kDeep = 4;
+  const int64_t stride = (int64_t)ctas * nt;
+  for (int64_t k0 = (int64_t)rank * nt + tid; k0 < t.max_tokens; k0 += kDeep * stride) {
+    int32_t row[kDeep], pos[kDeep], page[kDeep];
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      const int64_t k = k0 + d * stride;
+      row[d] = -1;
+      pos[d] = -1;
+      page[d] = -1;
+      if (k < all_tokens) {
+        int lo = 0, hi = R - 1;  // the first request whose inclusive offset passes k
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (s.cu[mid] > k)
+            hi = mid;
+          else
+            lo = mid + 1;
+        }
+        row[d] = lo;
+        pos[d] = s.len[lo] + (int32_t)(k - (lo > 0 ? s.cu[lo - 1] : 0));
+        const int32_t j = pos[d] / t.page_size;
+        const int32_t* from = j >= s.have[lo]
+                                  ? t.free_pages + (avail - 1 - s.first[lo] - (j - s.have[lo]))
+                                  : t.block_table + (int64_t)lo * t.bt_stride + j;
+        page[d] = *from;
       }
-      row = lo;
-      const int32_t pos = s.len[row] + (int32_t)(k - (row > 0 ? s.cu[row - 1] : 0));
-      const int32_t j = pos / t.page_size;
-      const int64_t page =
-          j >= s.have[row] ? t.free_pages[avail - 1 - s.first[row] - (j - s.have[row])]
-                           : t.block_table[(int64_t)row * t.bt_stride + j];
-      if (page >= 0 && page < t.num_pages)
-        slot = page * ps + pos % t.page_size;
-      else if (t.flags != nullptr)
-        atomicOr(t.flags, MLA_DEVERR_BAD_SLOT);
-      len = pos + 1;
     }
-    t.slot_mapping[k] = slot;
-    t.token_row[k] = row;
-    t.token_len[k] = len;
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      const int64_t k = k0 + d * stride;
+      if (k >= t.max_tokens) break;
+      int64_t slot = -1;
+      if (row[d] >= 0) {
+        if (page[d] >= 0 && page[d] < t.num_pages)
+          slot = page[d] * ps + pos[d] % t.page_size;
+        else if (t.flags != nullptr)
+          atomicOr(t.flags, MLA_DEVERR_BAD_SLOT);
+      }
+      t.slot_mapping[k] = slot;
+      t.token_row[k] = row[d];
+      t.token_len[k] = pos[d] + 1;
+    }
   }
 }
 
@@ -251,16 +281,16 @@ __global__ void __launch_bounds__(1024) mla_tables_kernel(const TableArgs t) {
 
 cudaError_t launch_tables(const TableArgs& t, cudaStream_t stream) {
   // One CTA of 256 threads serves a decode step; a step with many requests or
-  // tokens takes a cluster of eight CTAs of 1024.
-  const bool large = t.rows > 512 || t.max_tokens > 2048;
+  // tokens takes a cluster of eight CTAs of 1024 threads.
+  const bool large = t.rows > 256 || t.max_tokens > 2048;
+  auto kernel = t.rows > 1024 ? mla_tables_kernel<4> : mla_tables_kernel<1>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(large ? kTabCluster : 1, 1, 1);
   cfg.blockDim = dim3(large ? 1024 : 256, 1, 1);
   cfg.dynamicSmemBytes = 6 * (size_t)t.rows * sizeof(int32_t);
   if (cfg.dynamicSmemBytes > 40 * 1024) {  // beyond the default limit, on the device in use
-    const cudaError_t e =
-        cudaFuncSetAttribute(mla_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             6 * MLA_MAX_TABLE_ROWS * (int)sizeof(int32_t));
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               6 * MLA_MAX_TABLE_ROWS * (int)sizeof(int32_t));
     if (e != cudaSuccess) return e;
   }
   cfg.stream = stream;
@@ -273,7 +303,7 @@ cudaError_t launch_tables(const TableArgs& t, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, mla_tables_kernel, t);
+  return cudaLaunchKernelEx(&cfg, kernel, t);
 }
 
 }  // namespace mla

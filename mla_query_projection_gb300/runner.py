@@ -129,11 +129,20 @@ class DecodeStep:
 # ---- the cache side of the step -------------------------------------------
 #
 # Thin calls over the C ABI for torch tensors: sizes and strides come from the
-# tensors, what would be misread (a wrong type, an inner stride) is refused
-# here, and a return code that is not MLA_OK raises MlaError.
+# tensors, what would be misread (a wrong type, an inner stride, a tensor that
+# is too short) is refused here, and a return code that is not MLA_OK raises
+# MlaError.  A small step's call takes longer on the host than on the GPU, so
+# these functions hand plain integers to the library and ask each tensor only
+# for what they check.
 
 _ROW_BYTES = {B.MLA_KV_FP8_E4M3: 576, B.MLA_KV_FP8_DS_MLA: 656, B.MLA_KV_NVFP4_DS_MLA: 352,
               B.MLA_KV_FP8_E4M3_PAGE: 576}
+_I32, _I64, _F32, _U8, _BF16 = torch.int32, torch.int64, torch.float32, torch.uint8, torch.bfloat16
+_FP8 = torch.float8_e4m3fn
+
+
+def _refuse(what: str):
+    raise B.MlaError(B.MLA_EINVAL, what)
 
 
 def _check(rc: int, what: str) -> None:
@@ -141,43 +150,52 @@ def _check(rc: int, what: str) -> None:
         raise B.MlaError(rc, what)
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise B.MlaError(B.MLA_EINVAL, what)
+def _flat(x, dtype, n: int, what: str) -> int:
+    """Address of a contiguous tensor of `dtype` with at least n elements; 0 for None."""
+    if x is None:
+        return 0
+    if x.dtype is not dtype or not x.is_contiguous() or x.numel() < n:
+        _refuse(what)
+    return x.data_ptr()
 
 
-def _flat(x, dtype, n: int | None, what: str) -> None:
-    """`x` is None or a contiguous tensor of `dtype` with at least n elements."""
-    if x is not None:
-        _need(x.dtype == dtype and x.is_contiguous() and (n is None or x.numel() >= n), what)
+def _stream_of(x: torch.Tensor, stream) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(x.get_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _stream_of(t: torch.Tensor, stream):
-    return torch.cuda.current_stream(t.device) if stream is None else stream
+def _query_args(q_latent, q_pe, q_scale_inv, what: str):
+    """(tokens, heads, the C arguments q_latent .. q_scale_inv)."""
+    tokens, heads, width = q_latent.shape
+    dtype = q_latent.dtype
+    if q_pe.dtype is not dtype or (dtype is not _BF16 if q_scale_inv is None
+                                   else dtype is not _U8 and dtype is not _FP8):
+        _refuse(what + ": query type")
+    lt, lh, l1 = q_latent.stride()
+    pt, ph, p1 = q_pe.stride()
+    if width != 512 or q_pe.shape != (tokens, heads, 64) or l1 != 1 or p1 != 1:
+        _refuse(what + ": query shape")
+    return tokens, heads, (q_latent.data_ptr(), lt, lh, q_pe.data_ptr(), pt, ph,
+                           _flat(q_scale_inv, _F32, 1, what + ": q_scale_inv"))
 
 
-def _queries(q_latent, q_pe, q_scale_inv, what: str):
-    tokens, heads = q_latent.shape[0], q_latent.shape[1]
-    dtypes = (torch.bfloat16,) if q_scale_inv is None else (torch.uint8, torch.float8_e4m3fn)
-    _need(q_latent.dtype in dtypes and q_pe.dtype in dtypes, what + ": query type")
-    _need(q_latent.shape[2] == 512 and tuple(q_pe.shape) == (tokens, heads, 64)
-          and q_latent.stride(2) == 1 and q_pe.stride(2) == 1, what + ": query shape")
-    _flat(q_scale_inv, torch.float32, 1, what + ": q_scale_inv")
-    return tokens, heads
+def _cache_args(cache, layout, k_scale, what: str):
+    """The C arguments kv_cache .. k_scale."""
+    pages, page, row = cache.shape
+    if cache.dtype is not _U8 or row != _ROW_BYTES.get(layout) or not cache.is_contiguous():
+        _refuse(what + ": cache")
+    return (cache.data_ptr(), pages, page, layout,
+            _flat(k_scale, _F32, pages if layout == B.MLA_KV_FP8_E4M3_PAGE else 1, what + ": k_scale"))
 
 
-def _paged(cache, layout, k_scale, table, what: str):
-    _need(cache.dtype == torch.uint8 and cache.is_contiguous() and cache.dim() == 3
-          and cache.shape[2] == _ROW_BYTES.get(layout), what + ": cache")
-    _flat(k_scale, torch.float32, cache.shape[0] if layout == B.MLA_KV_FP8_E4M3_PAGE else 1,
-          what + ": k_scale")
-    _need(table.dtype == torch.int32 and table.dim() == 2 and table.stride(1) == 1
-          and (table.shape[0] == 1 or table.stride(0) >= table.shape[1]), what + ": block table")
-
-
-def _wide(table: torch.Tensor) -> int:
-    """Entries between two rows of a [rows][blocks] table."""
-    return table.stride(0) if table.shape[0] > 1 else table.shape[1]
+def _rows2d(x, dtype, what: str):
+    """(address, entries between rows, rows, columns) of a [rows, columns] tensor with unit inner stride."""
+    rows, cols = x.shape
+    st, s1 = x.stride()
+    if x.dtype is not dtype or (s1 != 1 and cols > 1) or (rows > 1 and st < cols):
+        _refuse(what)
+    return x.data_ptr(), (st if rows > 1 else cols), rows, cols
 
 
 def tables_step(new_tokens, lens, block_table, free_pages, free_count, page_size, lens_out,
@@ -187,63 +205,63 @@ def tables_step(new_tokens, lens, block_table, free_pages, free_count, page_size
 
     ``block_table`` and ``free_pages`` are updated; ``lens_out`` and
     ``free_count_out`` may be ``lens`` and ``free_count`` themselves."""
-    rows, tokens, i32 = lens.shape[0], slot_mapping.shape[0], torch.int32
-    for x, n in ((new_tokens, rows), (lens, rows), (lens_out, rows), (free_pages, None),
-                 (free_count, 1), (free_count_out, 1), (token_row, tokens), (token_len, tokens),
-                 (cu_tokens, rows + 1), (block_table, None), (flags, 1)):
-        _flat(x, i32, n, "tables_step: int32 arrays")
-    _flat(slot_mapping, torch.int64, tokens, "tables_step: slot_mapping")
-    _need(block_table.dim() == 2 and block_table.shape[0] == rows, "tables_step: block table")
-    _check(B.mla_tables_step(
-        rows, new_tokens, lens, lens_out, block_table, block_table.shape[1], free_pages, free_count,
-        free_count_out, free_pages.shape[0], page_size, tokens, slot_mapping, token_row, token_len,
-        cu_tokens, flags, _stream_of(lens, stream)), "mla_tables_step")
+    what = "tables_step: arrays"
+    rows, tokens, pages = lens.numel(), slot_mapping.numel(), free_pages.numel()
+    table_rows, width = block_table.shape
+    if table_rows != rows:
+        _refuse("tables_step: block table")
+    _check(B.load().mla_tables_step(
+        rows, _flat(new_tokens, _I32, rows, what), _flat(lens, _I32, rows, what),
+        _flat(lens_out, _I32, rows, what), _flat(block_table, _I32, 1, what), width,
+        _flat(free_pages, _I32, 1, what), _flat(free_count, _I32, 1, what),
+        _flat(free_count_out, _I32, 1, what), pages, page_size, tokens,
+        _flat(slot_mapping, _I64, 1, what), _flat(token_row, _I32, tokens, what),
+        _flat(token_len, _I32, tokens, what), _flat(cu_tokens, _I32, rows + 1, what),
+        _flat(flags, _I32, 1, what), _stream_of(lens, stream)), "mla_tables_step")
 
 
 def blocks_mean(cache, layout, k_scale, block_table, lens_from, lens_to, mean, flags=None,
                 stream=None) -> None:
     """Mean keys ``mean`` [pages, 576] of the blocks between two lengths (``mla_blocks_mean``)."""
-    _paged(cache, layout, k_scale, block_table, "blocks_mean")
-    rows = lens_to.shape[0]
-    _flat(lens_from, torch.int32, rows, "blocks_mean: lengths")
-    _flat(lens_to, torch.int32, rows, "blocks_mean: lengths")
-    _flat(flags, torch.int32, 1, "blocks_mean: flags")
-    _flat(mean, torch.bfloat16, cache.shape[0] * 576, "blocks_mean: mean")
-    _need(block_table.shape[0] >= rows, "blocks_mean: block table")
-    _check(B.mla_blocks_mean(
-        cache, cache.shape[0], cache.shape[1], layout, k_scale, block_table, _wide(block_table), rows,
-        lens_from, lens_to, mean, flags, _stream_of(cache, stream)), "mla_blocks_mean")
+    args = _cache_args(cache, layout, k_scale, "blocks_mean")
+    table, bt_stride, table_rows, _ = _rows2d(block_table, _I32, "blocks_mean: block table")
+    rows = lens_to.numel()
+    if table_rows < rows:
+        _refuse("blocks_mean: block table")
+    _check(B.load().mla_blocks_mean(
+        *args, table, bt_stride, rows, _flat(lens_from, _I32, rows, "blocks_mean: lengths"),
+        _flat(lens_to, _I32, rows, "blocks_mean: lengths"),
+        _flat(mean, _BF16, args[1] * 576, "blocks_mean: mean"),
+        _flat(flags, _I32, 1, "blocks_mean: flags"), _stream_of(cache, stream)), "mla_blocks_mean")
 
 
 def blocks_score(q_latent, q_pe, mean, page_size, block_table, lens, scores, q_scale_inv=None,
                  token_row=None, flags=None, stream=None) -> None:
     """Scores [tokens, blocks] of every block for every query (``mla_blocks_score``)."""
-    tokens, heads = _queries(q_latent, q_pe, q_scale_inv, "blocks_score")
-    _flat(mean, torch.bfloat16, None, "blocks_score: mean")
-    _flat(lens, torch.int32, tokens, "blocks_score: lengths")
-    _flat(token_row, torch.int32, tokens, "blocks_score: token_row")
-    _flat(flags, torch.int32, 1, "blocks_score: flags")
-    _need(block_table.dtype == torch.int32 and block_table.is_contiguous()
-          and scores.dtype == torch.float32 and scores.stride(1) == 1 and scores.shape[0] >= tokens
-          and scores.shape[1] >= block_table.shape[1], "blocks_score: block table or scores")
-    _check(B.mla_blocks_score(
-        tokens, heads, q_latent, q_latent.stride(0), q_latent.stride(1), q_pe, q_pe.stride(0),
-        q_pe.stride(1), q_scale_inv, mean, mean.shape[0], page_size, block_table,
-        block_table.shape[1], block_table.shape[0], token_row, lens, scores, _wide(scores), flags,
-        _stream_of(q_latent, stream)), "mla_blocks_score")
+    tokens, heads, query = _query_args(q_latent, q_pe, q_scale_inv, "blocks_score")
+    table_rows, width = block_table.shape
+    out, out_stride, out_rows, out_cols = _rows2d(scores, _F32, "blocks_score: scores")
+    if out_rows < tokens or out_cols < width:
+        _refuse("blocks_score: scores")
+    _check(B.load().mla_blocks_score(
+        tokens, heads, *query, _flat(mean, _BF16, 576, "blocks_score: mean"), mean.shape[0], page_size,
+        _flat(block_table, _I32, 1, "blocks_score: block table"), width, table_rows,
+        _flat(token_row, _I32, tokens, "blocks_score: token_row"),
+        _flat(lens, _I32, tokens, "blocks_score: lengths"), out, out_stride,
+        _flat(flags, _I32, 1, "blocks_score: flags"), _stream_of(q_latent, stream)), "mla_blocks_score")
 
 
 def blocks_select(scores, lens, page_size, keep_first, keep_last, sel, sel_count, stream=None) -> None:
     """The best-scored blocks ``sel`` [tokens, k] of every query (``mla_blocks_select``)."""
-    tokens, k = sel.shape
-    _need(scores.dtype == torch.float32 and scores.stride(1) == 1 and scores.shape[0] >= tokens,
-          "blocks_select: scores")
-    _need(sel.dtype == torch.int32 and sel.stride(1) == 1, "blocks_select: sel")
-    _flat(lens, torch.int32, tokens, "blocks_select: lengths")
-    _flat(sel_count, torch.int32, tokens, "blocks_select: sel_count")
-    _check(B.mla_blocks_select(
-        tokens, scores, _wide(scores), scores.shape[1], lens, page_size, keep_first, keep_last, k,
-        sel, _wide(sel), sel_count, _stream_of(scores, stream)), "mla_blocks_select")
+    out, out_stride, tokens, k = _rows2d(sel, _I32, "blocks_select: sel")
+    sc, sc_stride, sc_rows, blocks = _rows2d(scores, _F32, "blocks_select: scores")
+    if sc_rows < tokens:
+        _refuse("blocks_select: scores")
+    _check(B.load().mla_blocks_select(
+        tokens, sc, sc_stride, blocks, _flat(lens, _I32, tokens, "blocks_select: lengths"), page_size,
+        keep_first, keep_last, k, out, out_stride,
+        _flat(sel_count, _I32, tokens, "blocks_select: sel_count"), _stream_of(scores, stream)),
+        "mla_blocks_select")
 
 
 class PagedAttention:
@@ -253,6 +271,7 @@ class PagedAttention:
     must be ordered on one stream."""
 
     def __init__(self, max_batch: int, heads: int, device="cuda:0"):
+        self.handle = None
         self.device = torch.device(device)
         self.heads = heads
         with torch.cuda.device(self.device):
@@ -267,28 +286,28 @@ class PagedAttention:
         be strided (views of gathered rows); ``out`` BF16 [tokens, heads, 512]
         is allocated where it is not given, ``lse`` FP32 [tokens, heads] is
         written where it is."""
-        tokens, heads = _queries(q_latent, q_pe, q_scale_inv, "attention")
-        _paged(cache, layout, k_scale, block_table, "attention")
-        _need(heads == self.heads, "attention: heads")
-        _flat(lens, torch.int32, tokens, "attention: lengths")
-        _flat(token_row, torch.int32, tokens, "attention: token_row")
-        _flat(sel_count, torch.int32, tokens, "attention: sel_count")
-        _flat(lse, torch.float32, tokens * heads, "attention: lse")
-        sel_stride = 0
+        tokens, heads, query = _query_args(q_latent, q_pe, q_scale_inv, "attention")
+        paged = _cache_args(cache, layout, k_scale, "attention")
+        table, bt_stride, table_rows, _ = _rows2d(block_table, _I32, "attention: block table")
+        if heads != self.heads:
+            _refuse("attention: heads")
+        sel_ptr = sel_stride = 0
         if sel is not None:
-            _need(sel.dtype == torch.int32 and sel.stride(1) == 1 and sel.shape[0] >= tokens,
-                  "attention: sel")
-            sel_stride = _wide(sel)
+            sel_ptr, sel_stride, sel_rows, _ = _rows2d(sel, _I32, "attention: sel")
+            if sel_rows < tokens:
+                _refuse("attention: sel")
         if out is None:
-            out = torch.empty((tokens, heads, 512), dtype=torch.bfloat16, device=q_latent.device)
-        _need(out.dtype == torch.bfloat16 and tuple(out.shape) == (tokens, heads, 512)
-              and out.stride(2) == 1, "attention: out")
-        _check(B.mla_attn_decode(
-            self.handle, tokens, q_latent, q_latent.stride(0), q_latent.stride(1), q_pe,
-            q_pe.stride(0), q_pe.stride(1), q_scale_inv, cache, cache.shape[0], cache.shape[1], layout,
-            k_scale, block_table, _wide(block_table), block_table.shape[0], token_row, lens, sel,
-            sel_stride, sel_count, softmax_scale, out, out.stride(0), out.stride(1), lse,
-            _stream_of(q_latent, stream)), "mla_attn_decode")
+            out = torch.empty((tokens, heads, 512), dtype=_BF16, device=q_latent.device)
+        ot, oh, o1 = out.stride()
+        if out.dtype is not _BF16 or out.shape != (tokens, heads, 512) or o1 != 1:
+            _refuse("attention: out")
+        _check(B.load().mla_attn_decode(
+            self.handle, tokens, *query, *paged, table, bt_stride, table_rows,
+            _flat(token_row, _I32, tokens, "attention: token_row"),
+            _flat(lens, _I32, tokens, "attention: lengths"), sel_ptr, sel_stride,
+            _flat(sel_count, _I32, tokens, "attention: sel_count"), softmax_scale, out.data_ptr(), ot, oh,
+            _flat(lse, _F32, tokens * heads, "attention: lse"), _stream_of(q_latent, stream)),
+            "mla_attn_decode")
         return out, lse
 
     def error_flags(self) -> int:
