@@ -16,17 +16,27 @@
 // product and plane 3 share one, in turn), and O^T's four planes.
 //
 // Six latent planes, one rope plane and two weight tiles are in shared memory.
-// The MMA warp issues whatever is ready, O before S: the planes that O frees
-// are what S of the next tile waits for.
-// What bounds a tile (64 heads): shared-memory reads of the tensor core (36
-// MMAs for S and 32 for O, 48 cycles each: 3264), with the softmax warps'
-// conversions (64 term pairs a thread) close behind.
+// The MMA warp issues in a fixed order, the first products of a tile's S before
+// the O of the tile before it, the last ones behind: with loops and barriers
+// known to the compiler the descriptors are uniform, and the planes with one
+// copy are asked for last.  (Issuing whatever was ready, by test_wait, took
+// 104 us at 62 tokens, 128 heads and up to 4,096 rows; this order 98 us.)
+// What bounds a tile (64 heads): the chain of its steps, about 6,500 cycles.
+// The tensor core's share, shared-memory reads (36 MMAs for S and 32 for O, 48
+// cycles each), is 3264; the softmax warps' conversions (64 term pairs a
+// thread) do not overlap it fully, since TMEM has room for one tile's S only.
+// Sixteen softmax warps (97.7 us, with spills) or weights split once and
+// shifted by exponent for each plane (109 us) gained nothing.
 #include "mla_attn_tc.cuh"
 
 namespace mla {
 namespace {
 
-constexpr int kDsSlots = 6;  // latent planes in shared memory
+// Latent planes in shared memory: two copies of planes 0 and 1 (slots 0-3, by
+// the tile's parity), one of planes 2 and 3 (slots 4 and 5); a slot's n-th use.
+constexpr int kDsSlots = 6;
+__device__ __forceinline__ int ds_slot(int tile, int j) { return j < 2 ? 2 * (tile & 1) + j : 2 + j; }
+__device__ __forceinline__ uint32_t ds_use(int tile, int j) { return j < 2 ? tile >> 1 : tile; }
 
 template <int NH, bool FP8Q>
 struct DsSmem {
@@ -73,6 +83,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* drain = q_full + 1;
   uint64_t* voted = drain + 1;
   uint32_t* moved = reinterpret_cast<uint32_t*>(smem + S::oMoved);
+  uint32_t* gave_up = reinterpret_cast<uint32_t*>(smem + S::oTmem + 4);  // a softmax wait ran out
   float* ref = reinterpret_cast<float*>(smem + S::oRef);
   float* xs = reinterpret_cast<float*>(smem + S::oXs);
   float* red = reinterpret_cast<float*>(smem + S::oRed);
@@ -104,6 +115,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(drain, 1);
     mbar_init(voted, kTcSoft / 32);
     moved[0] = moved[1] = 0;
+    *gave_up = 0;
     mbar_fence_init();
     // the swizzles go by address bits: the base is a multiple of 1 KiB
     if (smem_u32(smem) & 1023u) atomicOr(a.err, MLA_DEVERR_CHECK);
@@ -124,7 +136,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_after();
   // S^T accumulators at columns NH * b: rope and plane 3 in 0, planes 0-2 in
   // 1-3; O^T planes from 256
-  const uint32_t tmem = __reduce_max_sync(0xFFFFFFFFu, *tslot);
+  const uint32_t tmem = uniform(*tslot);
   const uint32_t total = plan->end[a.batch - 1];
   const int workers = attn_workers(a, total);
   const uint32_t first = worker < workers ? attn_worker_start(total, workers, worker) : 0;
@@ -149,11 +161,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
 #pragma unroll 1
         for (int p = 0; p < 5; ++p) {
-          const int n = 4 * i + p - 1, slot = p == 0 ? 0 : n % kDsSlots, use = n / kDsSlots;
+          const int slot = p == 0 ? 0 : ds_slot(i, p - 1);
+          const uint32_t use = p == 0 ? i : ds_use(i, p - 1);
           uint64_t* f = p == 0 ? rope_full : &full[slot];
-          if (p == 0 ? i >= 1 : use >= 1)
-            tc_wait_warp(p == 0 ? rope_empty : &empty[slot], (uint32_t)((p == 0 ? i - 1 : use - 1) & 1),
-                         dead);
+          if (use >= 1) tc_wait_warp(p == 0 ? rope_empty : &empty[slot], (use - 1) & 1u, dead);
           if (dead) break;
           ++issued;
           if (lane == 0) mbar_arrive_expect_tx(f, kPlane);
@@ -168,9 +179,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // (Otherwise the MMAs have read them all.)
     if (dead && issued > 0) {
       (void)mbar_wait_bounded(rope_full, (uint32_t)(((issued - 1) / 5) & 1), kTcWait);
-      const int planes = issued - (issued + 4) / 5;  // latent planes among them
-      for (int n = max(0, planes - kDsSlots); n < planes; ++n)
-        (void)mbar_wait_bounded(&full[n % kDsSlots], (uint32_t)((n / kDsSlots) & 1), kTcWait);
+      for (int s = 0; s < kDsSlots; ++s) {
+        const int j = s < 4 ? s & 1 : s - 2, n = issued - 2 - j;  // planes up to this one of some tile
+        int last = n >= 0 ? n / 5 : -1;
+        if (s < 4 && last >= 0 && (last & 1) != s >> 1) --last;
+        if (last >= 0) (void)mbar_wait_bounded(&full[s], ds_use(last, j) & 1u, kTcWait);
+      }
     }
   } else if (warp == 9) {
     // ================= MMA issuer (the warp together, one elected lane issues)
@@ -184,79 +198,74 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint64_t dqr = tc_desc(smem_u32(smem + S::oQr), 1024, 2);
     const uint64_t dp = tc_desc(smem_u32(smem + S::oP), 1024, 2);
     constexpr uint64_t kPl = kPlane >> 4, kQPl = S::kQPlane >> 4;
-    // Two cursors: the next product of S^T (tile qi, step qs: rope, planes 0..3)
-    // and the next plane of O^T (tile vi, plane vj).  A barrier is tested for a
-    // phase only once the phase before it is known to be over.  (The counts are
-    // broadcast through a reduction, which lands in a uniform register.)
-    const int tiles = (int)__reduce_max_sync(0xFFFFFFFFu, end - first);
-    const uint32_t x0 = __reduce_max_sync(0xFFFFFFFFu, first);
-    int qi = 0, qs = 0, vi = 0, vj = 0, segs = 0;
-    uint32_t q_next = x0, v_next = x0;  // the first tile of the next stretch
-    uint32_t add = 0;                   // whether tile vi adds to its stretch's O^T
-    long long since = clock64();
-    while (vi < tiles && !dead) {
-      bool issued = false;
-      if (vi < qi && tc_ready(&p_full[vj & 1], (uint32_t)(vj >> 1))) {
-        tc_after();
-        if (vj == 0) {
-          add = x0 + vi != v_next;
-          if (!add)
-            v_next = __reduce_max_sync(0xFFFFFFFFu, plan->end[attn_token_of(plan, a.batch, x0 + vi)]);
-        }
-        const int slot = (4 * vi + vj) % kDsSlots;
-        tc_mma4x2<256, 256, 4>(tmem + 256 + NH * vj, dk + (uint64_t)slot * kPl,
-                               dp + (uint64_t)(vj & 1) * kPl, id_hi, id_lo, add);
-        tc_commit(&empty[slot]);
-        tc_commit(&pv_done[vj & 1]);
-        if (++vj == 4) {
-          vj = 0;
-          ++vi;
-        }
-        issued = true;
-      } else if (qi < tiles) {
-        if (qs == 0) {
-          // queries of a new stretch, the rope rows, the accumulator that plane
-          // 3 of the tile before had
-          const bool fresh = x0 + qi == q_next;
-          if ((!fresh || tc_ready(q_full, (uint32_t)(segs & 1))) && tc_ready(rope_full, (uint32_t)(qi & 1)) &&
-              (qi == 0 || tc_ready(&d_free[0], 1u))) {
-            tc_after();
-            if (fresh) {
-              ++segs;
-              q_next = __reduce_max_sync(0xFFFFFFFFu, plan->end[attn_token_of(plan, a.batch, x0 + qi)]);
-            }
-            tc_mma4_bf16<2, 2>(tmem, dkr, dqr, id_r, 0u);
-            tc_commit(rope_empty);
-            tc_commit(&d_full[0]);
-            qs = 1;
-            issued = true;
-          }
-        } else {
-          const int j = qs - 1, n = 4 * qi + j, slot = n % kDsSlots, b = qs & 3;
-          // accumulator 0 was read once in this tile (rope), the others in the one before
-          const bool free = b == 0 ? tc_ready(&d_free[0], 0u)
-                                   : qi == 0 || tc_ready(&d_free[b], (uint32_t)((qi - 1) & 1));
-          if (free && tc_ready(&full[slot], (uint32_t)((n / kDsSlots) & 1))) {
-            tc_after();
-            const uint64_t da = dk + (uint64_t)slot * kPl, db = dq + (uint64_t)j * kQPl;
-            if constexpr (FP8Q)
-              tc_mma4<2, 2>(tmem + NH * b, da, db, id_s, 0u);
-            else
-              tc_mma4x2<2, 2, NH * 8>(tmem + NH * b, da, db, id_s, id_s, 0u);
-            tc_commit(&d_full[b]);
-            if (++qs == 5) {
-              qs = 0;
-              ++qi;
-            }
-            issued = true;
-          }
-        }
-      }
-      const long long now = clock64();
-      if (issued)
-        since = now;
+    // (A wait that ran out ends no loop here: the loops are then the warp's, and
+    // the descriptors stay in uniform registers.  The MMAs go on over whatever
+    // the planes hold, and the results do not count.)
+    const int tiles = (int)uniform(end - first);
+    const uint32_t x0 = uniform(first);
+    // O^T of plane j of tile n, the q-th in order (`add`: to what its stretch has)
+    auto pv = [&](int n, int q, int j, uint32_t add) {
+      tc_wait_warp(&p_full[q & 1], (uint32_t)(q >> 1), dead);
+      tc_after();
+      tc_mma4x2<256, 256, 4>(tmem + 256 + NH * j, dk + ds_slot(n, j) * kPl, dp + (q & 1) * kPl, id_hi,
+                             id_lo, add);
+      tc_commit(&empty[ds_slot(n, j)]);
+      tc_commit(&pv_done[q & 1]);
+    };
+    // S^T: the rope product of tile n, and plane j's
+    auto qk_rope = [&](int n) {
+      if (n > 0) tc_wait_warp(&d_free[0], 1u, dead);  // plane 3 of the tile before has been read
+      tc_wait_warp(rope_full, (uint32_t)(n & 1), dead);
+      tc_after();
+      tc_mma4_bf16<2, 2>(tmem, dkr, dqr, id_r, 0u);
+      tc_commit(rope_empty);
+      tc_commit(&d_full[0]);
+    };
+    auto qk = [&](int n, int j) {
+      const int d = (j + 1) & 3;
+      if (d == 0)
+        tc_wait_warp(&d_free[0], 0u, dead);  // the rope product has been read
+      else if (n > 0)
+        tc_wait_warp(&d_free[d], (uint32_t)((n - 1) & 1), dead);
+      tc_wait_warp(&full[ds_slot(n, j)], ds_use(n, j) & 1u, dead);
+      tc_after();
+      const uint64_t da = dk + ds_slot(n, j) * kPl, db = dq + j * kQPl;
+      if constexpr (FP8Q)
+        tc_mma4<2, 2>(tmem + NH * d, da, db, id_s, 0u);
       else
-        dead = __any_sync(0xFFFFFFFFu, now - since > kTcWait);
+        tc_mma4x2<2, 2, NH * 8>(tmem + NH * d, da, db, id_s, id_s, 0u);
+      tc_commit(&d_full[d]);
+    };
+    uint32_t seg_end = x0, add = 0;  // add: whether the tile before added to its O^T
+    int segs = 0;
+    for (int i = 0; i <= tiles; ++i) {
+      // S of tile i around the O of tile i - 1: planes 2 and 3, of which there
+      // is one copy, are freed first and asked for last
+      const bool more = i < tiles, fresh = more && x0 + i == seg_end, due = i > 0;
+      if (more && !fresh) {
+        qk_rope(i);
+        qk(i, 0);
+        qk(i, 1);
+      }
+      if (due) {
+        pv(i - 1, 0, 2, add);
+        pv(i - 1, 1, 3, add);
+        pv(i - 1, 2, 0, add);
+        pv(i - 1, 3, 1, add);
+      }
+      if (fresh) {  // new queries: they come when the stretch before is stored
+        seg_end = uniform(plan->end[attn_token_of(plan, a.batch, x0 + i)]);
+        tc_wait_warp(q_full, (uint32_t)(segs & 1), dead);
+        ++segs;
+        qk_rope(i);
+        qk(i, 0);
+        qk(i, 1);
+      }
+      if (more) {
+        qk(i, 2);
+        qk(i, 3);
+      }
+      add = fresh ? 0u : 1u;
     }
     if (dead) {  // let what was issued finish before TMEM is freed
       tc_commit(drain);
@@ -277,7 +286,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int i = 0;
     uint32_t x = first;
     // A thread whose wait has run out goes on without waiting: all of them
-    // pass the same barriers to the end.
+    // pass the same barriers to the end.  (It says so, and from then on none takes
+    // the path that only some votes take.)
     while (x < end) {
       const AttnToken k = attn_token(a, plan, x, i == 0 ? seen : nullptr);
       const uint32_t seg0 = x, seg_end = min(k.end, end);
@@ -299,32 +309,49 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int b = i & 1;
         const bool valid = crow >= 0;
         const float sc[4] = {rscale.x, rscale.y, rscale.z, rscale.w};
+        const bool more = x + 1 < seg_end;
         // ---- S: R + sum_j scale_j D_j
         float s[kHalf];
-#pragma unroll
-        for (int step = 0; step < 5; ++step) {
-          const int d = step & 3;
-          tc_wait(&d_full[d], (uint32_t)(d == 0 ? step >> 2 : i & 1), dead);
+        auto read = [&](float (&v)[kHalf], int d, uint32_t parity) {
+          tc_wait(&d_full[d], parity, dead, gave_up);
           tc_after();
-          float v[kHalf];
           tc_ld(tmem + lanes + NH * d + hb, v);
-          tc_wait_ld();
+        };
+        auto scaled = [&](float (&v)[kHalf], float f) {
           tc_landed(v);
+          const float2 f2 = make_float2(f, f);
+#pragma unroll
+          for (int h = 0; h < kHalf; h += 2) {
+            const float2 w = fma2(make_float2(v[h], v[h + 1]), f2, make_float2(s[h], s[h + 1]));
+            s[h] = w.x;
+            s[h + 1] = w.y;
+          }
+        };
+        auto freed = [&](int d) {
           tc_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&d_free[d]);
-          if (step == 0) {
-#pragma unroll
-            for (int h = 0; h < kHalf; ++h) s[h] = v[h];
-          } else {
-            const float2 f = make_float2(sc[step - 1], sc[step - 1]);
-#pragma unroll
-            for (int h = 0; h < kHalf; h += 2) {
-              const float2 w = fma2(make_float2(v[h], v[h + 1]), f, make_float2(s[h], s[h + 1]));
-              s[h] = w.x;
-              s[h + 1] = w.y;
-            }
-          }
+        };
+        {
+          float v[kHalf], w[kHalf];
+          read(s, 0, 0u);
+          tc_wait_ld();
+          tc_landed(s);
+          freed(0);
+          read(v, 1, (uint32_t)(i & 1));
+          read(w, 2, (uint32_t)(i & 1));
+          tc_wait_ld();
+          scaled(v, sc[0]);
+          scaled(w, sc[1]);
+          freed(1);
+          if (lane == 0) mbar_arrive(&d_free[2]);
+          read(v, 3, (uint32_t)(i & 1));
+          read(w, 0, 1u);
+          tc_wait_ld();
+          scaled(v, sc[2]);
+          scaled(w, sc[3]);
+          freed(3);
+          if (lane == 0) mbar_arrive(&d_free[0]);
         }
         // exponents (logits in base 2 less the reference, plus kPShift), weights
         float p[kHalf];
@@ -360,8 +387,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // (the weights as if nothing moved, while the warps' answers meet)
 #pragma unroll
         for (int h = 0; h < kHalf; ++h) p[h] = ex2(p[h]);
-        tc_wait(voted, (uint32_t)(i & 1), dead);
-        if (*reinterpret_cast<volatile uint32_t*>(&moved[b]) == (uint32_t)i + 1) {
+        tc_wait(voted, (uint32_t)(i & 1), dead, gave_up);
+        if (*reinterpret_cast<volatile uint32_t*>(&moved[b]) == (uint32_t)i + 1 &&
+            *reinterpret_cast<volatile uint32_t*>(gave_up) == 0u) {
           // the reference moves to the tile's maximum where that passes it by
           // too much (for the first rows that count, everywhere), the planes'
           // references to the tile's largest scales
@@ -398,8 +426,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (started) lh *= ex2(d);
           }
           if (started && x > seg0) {
-            tc_wait(&pv_done[0], 1u, dead);  // both tiles of weights of the tile before
-            tc_wait(&pv_done[1], 1u, dead);
+            tc_wait(&pv_done[0], 1u, dead, gave_up);  // both tiles of weights of the tile before
+            tc_wait(&pv_done[1], 1u, dead, gave_up);
             tc_after();
 #pragma unroll 1
             for (int c = 0; c < 2 * NH; c += 32) {
@@ -427,7 +455,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int h = 0; h < kHalf; h += 2)
           asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(p16[h / 2]) : "f"(p[h]), "f"(p[h + 1]));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int q = 0; q < 4; ++q) {
+          const int j = (q + 2) & 3;  // planes 2, 3, 0, 1
           const float vj = vref[j];
           const float f = valid && vj > 0.f ? __fdividef(sc[j], vj) : 0.f;
           uint32_t f2;
@@ -439,16 +468,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             phi[h / 4] = __byte_perm(w0, w1, 0x5410);
             plo[h / 4] = __byte_perm(w0, w1, 0x7632);
           }
-          // use 2 i + j / 2 of this weight tile: the one before it has been read
-          if (i > 0 || j >= 2) tc_wait(&pv_done[j & 1], (uint32_t)(j >= 2 ? 0 : 1), dead);
-          if (!valid && half == 0) {
+          // use 2 i + q / 2 of this weight tile: the one before it has been read
+          if (i > 0 || q >= 2) tc_wait(&pv_done[q & 1], (uint32_t)(q >= 2 ? 0 : 1), dead, gave_up);
+          if (!valid && half == (j & 1)) {
             // a row that is loaded but does not count holds anything, NaN codes
             // too: no value of it may meet a weight of zero
-            uint4* d = reinterpret_cast<uint4*>(smem + S::oRing + ((4 * i + j) % kDsSlots) * kPlane + pos * 128);
+            uint4* d = reinterpret_cast<uint4*>(smem + S::oRing + ds_slot(i, j) * kPlane + pos * 128);
 #pragma unroll
             for (int c = 0; c < 8; ++c) d[c] = make_uint4(0, 0, 0, 0);
           }
-          uint8_t* prow = smem + S::oP + (j & 1) * kPlane + pos * 128;
+          uint8_t* prow = smem + S::oP + (q & 1) * kPlane + pos * 128;
           if constexpr (kHalf >= 16) {
 #pragma unroll
             for (int c = 0; c < kHalf / 16; ++c) {
@@ -465,10 +494,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           tc_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[j & 1]);
+          if (lane == 0) mbar_arrive(&p_full[q & 1]);
         }
-        // the next tile's row
-        if (x + 1 < seg_end) {
+        if (more) {  // the next tile's row
           crow = attn_row(a, k, (x + 1 - k.start) * kTcTile + pos, &page);
           rscale = row_scales(crow);
         }
@@ -494,8 +522,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           a.lse[(int64_t)k.t * a.heads + h0 + tid] = attn_lse(m, sum);
       }
       tc_barrier();
-      tc_wait(&pv_done[0], 1u, dead);
-      tc_wait(&pv_done[1], 1u, dead);
+      tc_wait(&pv_done[0], 1u, dead, gave_up);
+      tc_wait(&pv_done[1], 1u, dead, gave_up);
       tc_after();
       tc_store_out<NH>(a, k, tmem + lanes + 256, half, pos, h0, slot, whole, red, vref[2 * half],
                        vref[2 * half + 1]);

@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t* drain = q_full + 1;
   uint64_t* voted = drain + 1;
   uint32_t* moved = reinterpret_cast<uint32_t*>(smem + S::oMoved);
+  uint32_t* gave_up = reinterpret_cast<uint32_t*>(smem + S::oTmem + 4);  // a softmax wait ran out
   float* ref = reinterpret_cast<float*>(smem + S::oRef);
   float* xs = reinterpret_cast<float*>(smem + S::oXs);
   float* red = reinterpret_cast<float*>(smem + S::oRed);
@@ -110,6 +111,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     mbar_init(drain, 1);
     mbar_init(voted, kTcSoft / 32);
     moved[0] = moved[1] = 0;
+    *gave_up = 0;
     mbar_fence_init();
     // the swizzles go by address bits: the base is a multiple of 1 KiB
     if (smem_u32(smem) & 1023u) atomicOr(a.err, MLA_DEVERR_CHECK);
@@ -132,7 +134,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   AttnSeen* seen = reinterpret_cast<AttnSeen*>(smem + S::oP);  // until the first weights
   attn_make_plan(a, plan, reinterpret_cast<uint32_t*>(smem + S::oScan), blockIdx.x == 0, seen);
   tc_after();
-  const uint32_t tmem = __reduce_max_sync(0xFFFFFFFFu, *tslot);  // S^T buffers at columns 0 and 128, O^T planes from 256
+  const uint32_t tmem = uniform(*tslot);  // S^T buffers at columns 0 and 128, O^T planes from 256
   const uint32_t total = plan->end[a.batch - 1];
   const int workers = attn_workers(a, total);
   const uint32_t first = worker < workers ? attn_worker_start(total, workers, worker) : 0;
@@ -217,8 +219,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // A wait that ran out ends no loop here (the loops are then the warp's, and
     // the descriptors stay in uniform registers): the MMAs go on over whatever
     // the planes hold, and the results do not count.
-    const int tiles = (int)__reduce_max_sync(0xFFFFFFFFu, end - first);
-    const uint32_t x0 = __reduce_max_sync(0xFFFFFFFFu, first);
+    const int tiles = (int)uniform(end - first);
+    const uint32_t x0 = uniform(first);
     uint32_t seg_end = x0;
     int segs = 0;
     uint32_t add = 0;  // whether the tile before added to its O^T
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int b = i & 1;
       const bool fresh = x0 + i == seg_end;
       if (fresh) {
-        seg_end = __reduce_max_sync(0xFFFFFFFFu, plan->end[attn_token_of(plan, a.batch, x0 + i)]);
+        seg_end = uniform(plan->end[attn_token_of(plan, a.batch, x0 + i)]);
         if (due) pv(i - 1, add);  // its softmax must finish before the queries change
         due = false;
         tc_wait_warp(q_full, (uint32_t)(segs & 1), dead);
@@ -280,7 +282,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int i = 0;
     uint32_t x = first;
     // A thread whose wait has run out goes on without waiting: all of them
-    // pass the same barriers to the end.
+    // pass the same barriers to the end.  (It says so, and from then on none takes
+    // the path that only some votes take.)
     while (x < end) {
       const AttnToken k = attn_token(a, plan, x, i == 0 ? seen : nullptr);
       const uint32_t seg0 = x, seg_end = min(k.end, end);
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (; x < seg_end; ++x, ++i) {
         const int b = i & 1;
         const bool valid = crow >= 0;
-        tc_wait(&s_full[b], (uint32_t)((i >> 1) & 1), dead);
+        tc_wait(&s_full[b], (uint32_t)((i >> 1) & 1), dead, gave_up);
         tc_after();
         float s[kHalf];
         // exponents: logits in base 2 less the reference, plus kPShift
@@ -377,8 +380,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           mbar_arrive(voted);
         }
         weights();
-        tc_wait(voted, (uint32_t)(i & 1), dead);
-        if (*reinterpret_cast<volatile uint32_t*>(&moved[b]) == (uint32_t)i + 1) {
+        tc_wait(voted, (uint32_t)(i & 1), dead, gave_up);
+        if (*reinterpret_cast<volatile uint32_t*>(&moved[b]) == (uint32_t)i + 1 &&
+            *reinterpret_cast<volatile uint32_t*>(gave_up) == 0u) {
           // the reference moves to the tile's maximum where that passes it by
           // too much (for the first rows that count, everywhere)
           exponents();
@@ -413,7 +417,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (started) lh *= ex2(d);
           }
           if (started && x > seg0) {
-            tc_wait(pv_done, (uint32_t)((i - 1) & 1), dead);
+            tc_wait(pv_done, (uint32_t)((i - 1) & 1), dead, gave_up);
             tc_after();
 #pragma unroll 1
             for (int c = 0; c < 2 * NH; c += 32) {
@@ -439,7 +443,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int h = 0; h < kHalf; h += 2) l[h / 2] = add2(l[h / 2], make_float2(s[h], s[h + 1]));
         // the previous tile's PV has read P
-        if (i > 0) tc_wait(pv_done, (uint32_t)((i - 1) & 1), dead);
+        if (i > 0) tc_wait(pv_done, (uint32_t)((i - 1) & 1), dead, gave_up);
         if (!valid && half == 0) {
           // a row that is loaded but does not count holds anything, NaN codes
           // too: no value of it may meet a weight of zero
@@ -498,7 +502,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
       tc_barrier();
-      tc_wait(pv_done, (uint32_t)((i - 1) & 1), dead);
+      tc_wait(pv_done, (uint32_t)((i - 1) & 1), dead, gave_up);
       tc_after();
       tc_store_out<NH>(a, k, tmem + lanes + 256, half, pos, h0, slot, whole, red, vref[0], vref[0]);
       tc_before();
