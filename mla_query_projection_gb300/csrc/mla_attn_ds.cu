@@ -65,7 +65,7 @@ struct DsSmem {
                 "alignment");
 };
 
-template <int NH, bool FP8Q>
+template <int NH, bool FP8Q, bool COPY>
 __global__ void __launch_bounds__(kTcThreads, 1)
     mla_attn_ds_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
   using S = DsSmem<NH, FP8Q>;
@@ -145,45 +145,54 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp == 8) {
     // ================= TMA: a tile's planes in the order rope, 0, 1, 2, 3
-    const int boxes = kTcTile / maps.box_rows;
-    const int32_t no_row = (int32_t)(a.num_pages * a.page_size);  // past the end: zeros
-    int i = 0, issued = 0;  // tiles, planes
-    uint32_t x = first;
-    while (x < end && !dead) {
-      const AttnToken k = attn_token(a, plan, x, i == 0 ? seen : nullptr);
-      const uint32_t seg_end = min(k.end, end);
-      for (; x < seg_end && !dead; ++x, ++i) {
-        int32_t y = no_row;
-        if (lane < boxes) {
-          int64_t page;
-          const int64_t r = attn_row(a, k, (x - k.start) * kTcTile + lane * maps.box_rows, &page);
-          if (r >= 0) y = (int32_t)r;
-        }
+    if constexpr (COPY) {
+      auto place = [&](int n, int p) {
+        if (p == 0) return TcSlot{rope_full, rope_empty, (uint32_t)n, smem + S::oRope};
+        const int s = ds_slot(n, p - 1);
+        return TcSlot{&full[s], &empty[s], ds_use(n, p - 1), smem + S::oRing + s * kPlane};
+      };
+      tc_copy_tiles<kRowDs, 128, kDsRope>(a, plan, seen, first, end, lane, dead, place);
+    } else {
+      const int boxes = kTcTile / maps.box_rows;
+      const int32_t no_row = (int32_t)(a.num_pages * a.page_size);  // past the end: zeros
+      int i = 0, issued = 0;  // tiles, planes
+      uint32_t x = first;
+      while (x < end && !dead) {
+        const AttnToken k = attn_token(a, plan, x, i == 0 ? seen : nullptr);
+        const uint32_t seg_end = min(k.end, end);
+        for (; x < seg_end && !dead; ++x, ++i) {
+          int32_t y = no_row;
+          if (lane < boxes) {
+            int64_t page;
+            const int64_t r = attn_row(a, k, (x - k.start) * kTcTile + lane * maps.box_rows, &page);
+            if (r >= 0) y = (int32_t)r;
+          }
 #pragma unroll 1
-        for (int p = 0; p < 5; ++p) {
-          const int slot = p == 0 ? 0 : ds_slot(i, p - 1);
-          const uint32_t use = p == 0 ? i : ds_use(i, p - 1);
-          uint64_t* f = p == 0 ? rope_full : &full[slot];
-          if (use >= 1) tc_wait_warp(p == 0 ? rope_empty : &empty[slot], (use - 1) & 1u, dead);
-          if (dead) break;
-          ++issued;
-          if (lane == 0) mbar_arrive_expect_tx(f, kPlane);
-          __syncwarp();
-          if (lane < boxes)
-            tma_g2s_2d(smem + (p == 0 ? S::oRope : S::oRing + slot * kPlane) + lane * maps.box_rows * 128,
-                       &maps.latent, p == 0 ? kDsRope : 128 * (p - 1), y, f);
+          for (int p = 0; p < 5; ++p) {
+            const int slot = p == 0 ? 0 : ds_slot(i, p - 1);
+            const uint32_t use = p == 0 ? i : ds_use(i, p - 1);
+            uint64_t* f = p == 0 ? rope_full : &full[slot];
+            if (use >= 1) tc_wait_warp(p == 0 ? rope_empty : &empty[slot], (use - 1) & 1u, dead);
+            if (dead) break;
+            ++issued;
+            if (lane == 0) mbar_arrive_expect_tx(f, kPlane);
+            __syncwarp();
+            if (lane < boxes)
+              tma_g2s_2d(smem + (p == 0 ? S::oRope : S::oRing + slot * kPlane) + lane * maps.box_rows * 128,
+                         &maps.latent, p == 0 ? kDsRope : 128 * (p - 1), y, f);
+          }
         }
       }
-    }
-    // A wait ran out: the planes issued last land before the CTA leaves.
-    // (Otherwise the MMAs have read them all.)
-    if (dead && issued > 0) {
-      (void)mbar_wait_bounded(rope_full, (uint32_t)(((issued - 1) / 5) & 1), kTcWait);
-      for (int s = 0; s < kDsSlots; ++s) {
-        const int j = s < 4 ? s & 1 : s - 2, n = issued - 2 - j;  // planes up to this one of some tile
-        int last = n >= 0 ? n / 5 : -1;
-        if (s < 4 && last >= 0 && (last & 1) != s >> 1) --last;
-        if (last >= 0) (void)mbar_wait_bounded(&full[s], ds_use(last, j) & 1u, kTcWait);
+      // A wait ran out: the planes issued last land before the CTA leaves.
+      // (Otherwise the MMAs have read them all.)
+      if (dead && issued > 0) {
+        (void)mbar_wait_bounded(rope_full, (uint32_t)(((issued - 1) / 5) & 1), kTcWait);
+        for (int s = 0; s < kDsSlots; ++s) {
+          const int j = s < 4 ? s & 1 : s - 2, n = issued - 2 - j;  // planes up to this one of some tile
+          int last = n >= 0 ? n / 5 : -1;
+          if (s < 4 && last >= 0 && (last & 1) != s >> 1) --last;
+          if (last >= 0) (void)mbar_wait_bounded(&full[s], ds_use(last, j) & 1u, kTcWait);
+        }
       }
     }
   } else if (warp == 9) {
@@ -543,7 +552,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-template <int NH, bool FP8Q>
+template <int NH, bool FP8Q, bool COPY>
 cudaError_t launch_ds(const AttnArgs& a, const TcMaps& maps, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.workers * a.groups));
@@ -555,24 +564,30 @@ cudaError_t launch_ds(const AttnArgs& a, const TcMaps& maps, cudaStream_t stream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mla_attn_ds_kernel<NH, FP8Q>, a, maps);
+  return cudaLaunchKernelEx(&cfg, mla_attn_ds_kernel<NH, FP8Q, COPY>, a, maps);
 }
 
 template <int NH>
 cudaError_t launch_ds_heads(const AttnArgs& a, const TcMaps& maps, cudaStream_t stream) {
-  return a.q_scale_inv != nullptr ? launch_ds<NH, true>(a, maps, stream)
-                                  : launch_ds<NH, false>(a, maps, stream);
+  const bool copy = maps.box_rows == 0;
+  if (a.q_scale_inv != nullptr)
+    return copy ? launch_ds<NH, true, true>(a, maps, stream) : launch_ds<NH, true, false>(a, maps, stream);
+  return copy ? launch_ds<NH, false, true>(a, maps, stream) : launch_ds<NH, false, false>(a, maps, stream);
 }
 
+template <int NH, bool FP8Q>
+cudaError_t prepare_ds() {
+  cudaError_t e = cudaFuncSetAttribute(mla_attn_ds_kernel<NH, FP8Q, false>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, DsSmem<NH, FP8Q>::kBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(mla_attn_ds_kernel<NH, FP8Q, true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, DsSmem<NH, FP8Q>::kBytes);
+  return e;
+}
 template <int NH>
 cudaError_t prepare_ds_heads() {
-  cudaError_t e = cudaFuncSetAttribute(mla_attn_ds_kernel<NH, false>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       DsSmem<NH, false>::kBytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(mla_attn_ds_kernel<NH, true>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, DsSmem<NH, true>::kBytes);
-  return e;
+  cudaError_t e = prepare_ds<NH, false>();
+  return e == cudaSuccess ? prepare_ds<NH, true>() : e;
 }
 
 }  // namespace
@@ -585,11 +600,10 @@ cudaError_t prepare_attn_ds() {
 }
 
 cudaError_t launch_attn_ds(const AttnArgs& a, cudaStream_t stream) {
-  TcMaps maps;
-  int r = a.page_size & -a.page_size;
-  maps.box_rows = r < kTcTile ? r : kTcTile;
+  TcMaps maps = {};
+  maps.box_rows = plane_box_rows(a);
   // one map: the four latent planes and the rope values are 128-byte boxes
-  if (!encode_plane_map(&maps.latent, a, kRowDs, 128, maps.box_rows)) return cudaErrorInvalidValue;
+  if (maps.box_rows > 0 && !encode_plane_map(&maps.latent, a, kRowDs, 128, maps.box_rows)) return cudaErrorInvalidValue;
   maps.rope = maps.latent;
   switch (attn_tc_heads(a.heads)) {
     case 16: return launch_ds_heads<16>(a, maps, stream);

@@ -63,7 +63,7 @@ struct TcSmem {
                 "alignment");
 };
 
-template <int NH, bool FP8Q, int LAYOUT>
+template <int NH, bool FP8Q, int LAYOUT, bool COPY>
 __global__ void __launch_bounds__(kTcThreads, 1)
     mla_attn_tc_kernel(const AttnArgs a, const __grid_constant__ TcMaps maps) {
   using S = TcSmem<NH, FP8Q>;
@@ -143,52 +143,61 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp == 8) {
     // ================= TMA: a tile's planes in the order rope, 0, 1, 2, 3
-    const int boxes = kTcTile / maps.box_rows;
-    const int32_t no_row = (int32_t)(a.num_pages * a.page_size);  // past the end: zeros
-    int i = 0, issued = 0;  // tiles, planes
-    uint32_t x = first;
-    while (x < end && !dead) {
-      // (the first token's weights come after its queries and a tile of its
-      // rows: this warp has read `seen` by then)
-      const AttnToken k = attn_token(a, plan, x, i == 0 ? seen : nullptr);
-      const uint32_t seg_end = min(k.end, end);
-      for (; x < seg_end && !dead; ++x, ++i) {
-        int32_t y = no_row;
-        if (lane < boxes) {
-          int64_t page;
-          const int64_t r = attn_row(a, k, (x - k.start) * kTcTile + lane * maps.box_rows, &page);
-          if (r >= 0) y = (int32_t)r;
-        }
-        const int b = i & 1;
-#pragma unroll 1
-        for (int p = 0; p < 5; ++p) {
-          uint64_t* f = p == 0 ? rope_full : &full[4 * b + p - 1];
-          uint64_t* e = p == 0 ? rope_empty : &empty[4 * b + p - 1];
-          if (p == 0 ? i >= 1 : i >= 2)
-            tc_wait_warp(e, (uint32_t)((p == 0 ? i - 1 : i / 2 - 1) & 1), dead);
-          if (dead) break;
-          ++issued;
-          if (lane == 0) mbar_arrive_expect_tx(f, p == 0 ? kPlane / 2 : kPlane);
-          __syncwarp();
+    if constexpr (COPY) {
+      auto place = [&](int n, int p) {
+        const int s = 4 * (n & 1) + p - 1;
+        return p == 0 ? TcSlot{rope_full, rope_empty, (uint32_t)n, smem + S::oRope}
+                      : TcSlot{&full[s], &empty[s], (uint32_t)n >> 1, smem + S::oRing + s * kPlane};
+      };
+      tc_copy_tiles<kRowE4m3, 64, kKvLora>(a, plan, seen, first, end, lane, dead, place);
+    } else {
+      const int boxes = kTcTile / maps.box_rows;
+      const int32_t no_row = (int32_t)(a.num_pages * a.page_size);  // past the end: zeros
+      int i = 0, issued = 0;  // tiles, planes
+      uint32_t x = first;
+      while (x < end && !dead) {
+        // (the first token's weights come after its queries and a tile of its
+        // rows: this warp has read `seen` by then)
+        const AttnToken k = attn_token(a, plan, x, i == 0 ? seen : nullptr);
+        const uint32_t seg_end = min(k.end, end);
+        for (; x < seg_end && !dead; ++x, ++i) {
+          int32_t y = no_row;
           if (lane < boxes) {
-            if (p == 0)
-              tma_g2s_2d(smem + S::oRope + lane * maps.box_rows * 64, &maps.rope, kKvLora, y, f);
-            else
-              tma_g2s_2d(smem + S::oRing + (4 * b + p - 1) * kPlane + lane * maps.box_rows * 128,
-                         &maps.latent, 128 * (p - 1), y, f);
+            int64_t page;
+            const int64_t r = attn_row(a, k, (x - k.start) * kTcTile + lane * maps.box_rows, &page);
+            if (r >= 0) y = (int32_t)r;
+          }
+          const int b = i & 1;
+#pragma unroll 1
+          for (int p = 0; p < 5; ++p) {
+            uint64_t* f = p == 0 ? rope_full : &full[4 * b + p - 1];
+            uint64_t* e = p == 0 ? rope_empty : &empty[4 * b + p - 1];
+            if (p == 0 ? i >= 1 : i >= 2)
+              tc_wait_warp(e, (uint32_t)((p == 0 ? i - 1 : i / 2 - 1) & 1), dead);
+            if (dead) break;
+            ++issued;
+            if (lane == 0) mbar_arrive_expect_tx(f, p == 0 ? kPlane / 2 : kPlane);
+            __syncwarp();
+            if (lane < boxes) {
+              if (p == 0)
+                tma_g2s_2d(smem + S::oRope + lane * maps.box_rows * 64, &maps.rope, kKvLora, y, f);
+              else
+                tma_g2s_2d(smem + S::oRing + (4 * b + p - 1) * kPlane + lane * maps.box_rows * 128,
+                           &maps.latent, 128 * (p - 1), y, f);
+            }
           }
         }
       }
-    }
-    // A wait ran out: the planes issued last land before the CTA leaves.
-    // (Otherwise the MMAs have read them all.)
-    if (dead && issued > 0) {
-      (void)mbar_wait_bounded(rope_full, (uint32_t)(((issued - 1) / 5) & 1), kTcWait);
-      for (int s = 0; s < 8; ++s) {
-        const int b = s >> 2, n = issued - 2 - (s & 3);  // planes up to this one of some tile
-        int last = n >= 0 ? n / 5 : -1;
-        if (last >= 0 && (last & 1) != b) --last;
-        if (last >= 0) (void)mbar_wait_bounded(&full[s], (uint32_t)((last >> 1) & 1), kTcWait);
+      // A wait ran out: the planes issued last land before the CTA leaves.
+      // (Otherwise the MMAs have read them all.)
+      if (dead && issued > 0) {
+        (void)mbar_wait_bounded(rope_full, (uint32_t)(((issued - 1) / 5) & 1), kTcWait);
+        for (int s = 0; s < 8; ++s) {
+          const int b = s >> 2, n = issued - 2 - (s & 3);  // planes up to this one of some tile
+          int last = n >= 0 ? n / 5 : -1;
+          if (last >= 0 && (last & 1) != b) --last;
+          if (last >= 0) (void)mbar_wait_bounded(&full[s], (uint32_t)((last >> 1) & 1), kTcWait);
+        }
       }
     }
   } else if (warp == 9) {
@@ -520,8 +529,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-template <int NH, bool FP8Q, int LAYOUT>
-cudaError_t launch_tc(const AttnArgs& a, const TcMaps& maps, cudaStream_t stream) {
+template <int NH, bool FP8Q, int LAYOUT, bool COPY>
+cudaError_t launch_tc_kernel(const AttnArgs& a, const TcMaps& maps, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.workers * a.groups));
   cfg.blockDim = dim3(kTcThreads);
@@ -532,7 +541,13 @@ cudaError_t launch_tc(const AttnArgs& a, const TcMaps& maps, cudaStream_t stream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mla_attn_tc_kernel<NH, FP8Q, LAYOUT>, a, maps);
+  return cudaLaunchKernelEx(&cfg, mla_attn_tc_kernel<NH, FP8Q, LAYOUT, COPY>, a, maps);
+}
+
+template <int NH, bool FP8Q, int LAYOUT>
+cudaError_t launch_tc(const AttnArgs& a, const TcMaps& maps, cudaStream_t stream) {
+  return maps.box_rows == 0 ? launch_tc_kernel<NH, FP8Q, LAYOUT, true>(a, maps, stream)
+                            : launch_tc_kernel<NH, FP8Q, LAYOUT, false>(a, maps, stream);
 }
 
 template <int NH>
@@ -547,8 +562,12 @@ cudaError_t launch_tc_heads(const AttnArgs& a, const TcMaps& maps, cudaStream_t 
 
 template <int NH, bool FP8Q, int LAYOUT>
 cudaError_t prepare_tc() {
-  return cudaFuncSetAttribute(mla_attn_tc_kernel<NH, FP8Q, LAYOUT>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<NH, FP8Q>::kBytes);
+  cudaError_t e = cudaFuncSetAttribute(mla_attn_tc_kernel<NH, FP8Q, LAYOUT, false>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<NH, FP8Q>::kBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(mla_attn_tc_kernel<NH, FP8Q, LAYOUT, true>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem<NH, FP8Q>::kBytes);
+  return e;
 }
 template <int NH>
 cudaError_t prepare_tc_heads() {
@@ -565,8 +584,7 @@ int attn_tc_heads(int heads) { return heads <= 16 ? 16 : heads <= 32 ? 32 : 64; 
 int attn_tc_tile() { return kTcTile; }
 
 bool attn_tc_serves(const AttnArgs& a) {
-  return a.layout != MLA_KV_NVFP4_DS_MLA && a.page_size % 8 == 0 &&
-         a.num_pages <= (int64_t)0x7FFFFFFF / a.page_size;
+  return a.layout != MLA_KV_NVFP4_DS_MLA;
 }
 
 cudaError_t prepare_attn_tc() {
@@ -577,11 +595,10 @@ cudaError_t prepare_attn_tc() {
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t stream) {
-  TcMaps maps;
-  int r = a.page_size & -a.page_size;
-  maps.box_rows = r < kTcTile ? r : kTcTile;
-  if (!encode_plane_map(&maps.latent, a, kRowE4m3, 128, maps.box_rows) ||
-      !encode_plane_map(&maps.rope, a, kRowE4m3, 64, maps.box_rows))
+  TcMaps maps = {};
+  maps.box_rows = plane_box_rows(a);
+  if (maps.box_rows > 0 && (!encode_plane_map(&maps.latent, a, kRowE4m3, 128, maps.box_rows) ||
+                            !encode_plane_map(&maps.rope, a, kRowE4m3, 64, maps.box_rows)))
     return cudaErrorInvalidValue;
   switch (attn_tc_heads(a.heads)) {
     case 16: return launch_tc_heads<16>(a, maps, stream);

@@ -299,8 +299,90 @@ __device__ __forceinline__ bool tc_ready(uint64_t* bar, uint32_t parity) {
 struct TcMaps {
   CUtensorMap latent;  // boxes of box_rows x 128 bytes, 128-byte swizzle
   CUtensorMap rope;    // boxes of box_rows x 64 bytes, 64-byte swizzle
-  int box_rows;        // a power of two that divides the page, 8..128
+  int box_rows;        // a power of two that divides the page, 8..128; 0: rows are copied
 };
+
+// Where plane p of a tile goes (0: rope, then the latent ones), the slot's
+// barriers, and how often it was used before.
+struct TcSlot {
+  uint64_t *full, *empty;
+  uint32_t use;
+  uint8_t* dst;
+};
+
+// One plane of a tile by 16-byte copies, swizzled as TMA does it: 128 rows of
+// WIDTH bytes, from byte `col` of the cache rows (lane l holds those of rows l,
+// l + 32, ..; -1: zeros).
+template <int WIDTH>
+__device__ __forceinline__ void tc_copy_plane(const AttnArgs& a, int row_bytes, uint8_t* dst, int col,
+                                              const int64_t (&rows)[4], int lane) {
+  constexpr int kChunks = WIDTH / 16, kRows = 32 / kChunks;  // a row's chunks, rows an instruction
+  const int c = lane % kChunks;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+#pragma unroll
+    for (int it = 0; it < kChunks; ++it) {
+      const int rl = it * kRows + lane / kChunks, r = 32 * g + rl;
+      const int64_t row = __shfl_sync(0xFFFFFFFFu, rows[g], rl);
+      const uint32_t d = smem_u32(dst) + r * WIDTH + ((WIDTH == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+      const uint8_t* s = a.cache + (row >= 0 ? row : 0) * row_bytes + col + 16 * c;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(s), "r"(row >= 0 ? 16 : 0)
+                   : "memory");
+    }
+  }
+}
+
+// The producer warp where TMA boxes would be too low (8 does not divide the
+// page: pages of one token would need 640 boxes a tile).  Up to three planes
+// are under way while a fourth is asked for; a plane is told of when its copies
+// have landed and are fenced for the tensor core.  32 requests of 4,096 E4M3
+// rows, 64 heads: 73 us with pages of 1 (the mma.sync kernel: 183); with pages
+// of 64 these copies take 64 us, TMA 45.
+template <int ROW_BYTES, int ROPE_BYTES, int ROPE_COL, class Place>
+__device__ __forceinline__ void tc_copy_tiles(const AttnArgs& a, const AttnPlan* plan, const AttnSeen* seen,
+                                              uint32_t first, uint32_t end, int lane, bool& dead,
+                                              Place place) {
+  int i = 0, sent = 0, told = 0;  // tiles; planes
+  auto tell = [&]() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) mbar_arrive(place(told / 5, told % 5).full);
+    ++told;
+  };
+  uint32_t x = first;
+  while (x < end && !dead) {
+    const AttnToken k = attn_token(a, plan, x, i == 0 ? seen : nullptr);
+    const uint32_t seg_end = min(k.end, end);
+    for (; x < seg_end && !dead; ++x, ++i) {
+      int64_t rows[4], page;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) rows[g] = attn_row(a, k, (x - k.start) * kTcTile + 32 * g + lane, &page);
+#pragma unroll 1
+      for (int p = 0; p < 5; ++p) {
+        const TcSlot s = place(i, p);
+        if (s.use >= 1) {
+          if (!tc_ready(s.empty, (s.use - 1) & 1u)) {  // what frees it may need the planes under way
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            while (told < sent) tell();
+          }
+          tc_wait_warp(s.empty, (s.use - 1) & 1u, dead);
+        }
+        if (dead) break;
+        if (p == 0)
+          tc_copy_plane<ROPE_BYTES>(a, ROW_BYTES, s.dst, ROPE_COL, rows, lane);
+        else
+          tc_copy_plane<128>(a, ROW_BYTES, s.dst, 128 * (p - 1), rows, lane);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (++sent - told > 3) {
+          asm volatile("cp.async.wait_group 3;" ::: "memory");
+          tell();
+        }
+      }
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  while (told < sent) tell();
+}
 
 // This thread's column of planes 2 half and 2 half + 1 of O^T (at `ot`, NH
 // columns a plane), times factor[h] and the plane's f0 or f1: the output, or
@@ -482,6 +564,15 @@ __device__ __forceinline__ void tc_queries(const AttnArgs& a, uint8_t* sq, uint8
 
 // A map of the cache's rows in boxes of box_rows x box_bytes (64 or 128, with the
 // swizzle of that width).
+// Rows a box has: the largest power of two that divides the page, up to a
+// tile.  0, to copy the rows instead, for fewer than 8 (a box starts on a
+// swizzle's 8 rows) and where a row's number passes a TMA coordinate.
+inline int plane_box_rows(const AttnArgs& a) {
+  const int r = a.page_size & -a.page_size;
+  if (r < 8 || a.num_pages > (int64_t)0x7FFFFFFF / a.page_size) return 0;
+  return r < kTcTile ? r : kTcTile;
+}
+
 inline bool encode_plane_map(CUtensorMap* map, const AttnArgs& a, int row_bytes, int box_bytes,
                       int box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
