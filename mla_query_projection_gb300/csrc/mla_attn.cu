@@ -1,6 +1,7 @@
-// mla_attn.cu - latent attention over the paged cache: the C entry points, the
-// mma.sync kernel that serves every layout, and the kernel that joins the
-// parts of a context that several workers read.
+// mla_attn.cu - latent attention over the paged cache: the C entry points and
+// the kernel that joins the parts of a context that several workers read.
+// (What reads the cache is in mla_attn_tc.cu, mla_attn_ds.cu and mla_attn_nv.cu,
+// by layout.)
 //
 //   o[t][h] = sum_i p_i c_i[0..511],  p = softmax_i(scale * q[t][h] . c_i),
 //   lse[t][h] = log sum_i exp(scale * q[t][h] . c_i)
@@ -29,272 +30,6 @@ struct mla_attn {
 
 namespace mla {
 namespace {
-
-// ------------------------------------------------- mma.sync kernel, any layout
-//
-// One CTA takes 16 * MT heads of one token at a time and its tiles of 64
-// cache rows: the rows are widened to BF16 in shared memory (exact for every
-// layout: at most 8 significant bits; a row's FP32 scale goes to the logits
-// and the weights instead), S = Q K^T and O += P V run as m16n8k16 tiles with
-// FP32 accumulators (O in registers: 16 heads x 64 MT columns a warp), and P
-// is rounded to BF16 (half a step: 2^-8 of each weight, below the output's
-// own rounding once weighted and summed).
-
-constexpr int kTile = 64;
-constexpr int kKPitch = kRowElems + 8;   // BF16 elements; 1168 B: ldmatrix without conflicts
-constexpr int kPPitch = kTile + 8;
-constexpr int kSPitch = kTile + 4;
-
-template <int MT>
-struct MmaSmem {
-  static constexpr int kHeads = 16 * MT;
-  static constexpr int oK = 0;
-  static constexpr int oQ = oK + kTile * kKPitch * 2;
-  static constexpr int oP = oQ + kHeads * kKPitch * 2;
-  static constexpr int oS = oP + kHeads * kPPitch * 2;
-  static constexpr int oStat = oS + kHeads * kSPitch * 4;  // alpha[heads], l[heads], m[heads]
-  static constexpr int oRow = oStat + 3 * kHeads * 4;      // int64 row[64]
-  static constexpr int oScale = oRow + kTile * 8;          // float scale[64]
-  static constexpr int oPlan = oScale + kTile * 4;
-  static constexpr int oRed = oPlan + (int)sizeof(AttnPlan) + 8;
-  static constexpr int kBytes = oRed + 64 * 8;
-};
-
-__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-__device__ __forceinline__ void ldsm_x2(uint32_t& r0, uint32_t& r1, uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
-               : "=r"(r0), "=r"(r1)
-               : "r"(addr));
-}
-
-template <int MT, int LAYOUT>
-__global__ void __launch_bounds__(256, 1) mla_attn_mma_kernel(const AttnArgs a) {
-  using S = MmaSmem<MT>;
-  using R = RowChunks<LAYOUT>;
-  constexpr int kHeads = S::kHeads;
-  constexpr int kNQ = MT;        // n8 tiles of S a warp computes
-  constexpr int kNO = 8 * MT;    // n8 tiles of O a warp holds
-  constexpr int kTph = 256 / kHeads;  // threads a head in the softmax
-  constexpr int kCols = kTile / kTph; // positions a thread
-  extern __shared__ __align__(16) uint8_t smem[];
-  uint16_t* sk = reinterpret_cast<uint16_t*>(smem + S::oK);
-  uint16_t* sq = reinterpret_cast<uint16_t*>(smem + S::oQ);
-  uint16_t* sp = reinterpret_cast<uint16_t*>(smem + S::oP);
-  float* ss = reinterpret_cast<float*>(smem + S::oS);
-  float* alpha = reinterpret_cast<float*>(smem + S::oStat);
-  float* sl = alpha + kHeads;
-  float* sm = sl + kHeads;
-  int64_t* srow = reinterpret_cast<int64_t*>(smem + S::oRow);
-  float* sscale = reinterpret_cast<float*>(smem + S::oScale);
-  AttnPlan* plan = reinterpret_cast<AttnPlan*>(smem + S::oPlan);
-  uint32_t* red = reinterpret_cast<uint32_t*>(smem + S::oRed);
-
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, q4 = lane & 3;
-  const int wm = warp % MT, wn = warp / MT;
-  const int group = blockIdx.x % a.groups, worker = blockIdx.x / a.groups;
-  const int h0 = group * kHeads;
-  pdl_launch_dependents();
-  pdl_wait();
-  attn_make_plan(a, plan, red, blockIdx.x == 0);
-  const uint32_t total = plan->end[a.batch - 1];
-  const int workers = attn_workers(a, total);
-  if (worker >= workers) return;
-  const uint32_t first = attn_worker_start(total, workers, worker);
-  const uint32_t end = attn_worker_start(total, workers, worker + 1);
-  const float qinv = a.q_scale_inv != nullptr ? *a.q_scale_inv : 1.0f;
-  // logits in base 2: x = acc * row scale * (softmax scale / q_scale_inv * log2 e)
-  const float xs = a.scale / qinv * 1.4426950408889634f;
-
-  uint32_t x = first;
-  while (x < end) {
-    const AttnToken tok = attn_token(a, plan, x);
-    const int t = tok.t;
-    const uint32_t seg_end = min(tok.end, end);
-    // ---- queries
-    __syncthreads();
-    for (int c = tid; c < kHeads * (kRowElems / 8); c += 256) {
-      const int h = c / (kRowElems / 8), k = 8 * (c % (kRowElems / 8));
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (h0 + h < a.heads) {
-        const int64_t e = k < kKvLora ? (int64_t)t * a.ql_ts + (int64_t)(h0 + h) * a.ql_hs + k
-                                      : (int64_t)t * a.qp_ts + (int64_t)(h0 + h) * a.qp_hs + k - kKvLora;
-        const uint8_t* base = k < kKvLora ? a.q_latent : a.q_pe;
-        if (a.q_scale_inv == nullptr) {
-          v = *reinterpret_cast<const uint4*>(base + 2 * e);
-        } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(base + e);
-          float f[8];
-          e4m3x4_values(w.x, f);
-          e4m3x4_values(w.y, f + 4);
-          v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                         pack_bf16x2(f[6], f[7]));
-        }
-      }
-      *reinterpret_cast<uint4*>(sq + h * kKPitch + k) = v;
-    }
-    if (tid < kHeads) {
-      sl[tid] = 0.f;
-      sm[tid] = -INFINITY;
-    }
-    float o[kNO][4];
-#pragma unroll
-    for (int n = 0; n < kNO; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-
-    for (uint32_t tile = x; tile < seg_end; ++tile) {
-      const uint32_t v0 = (tile - tok.start) * kTile;
-      __syncthreads();  // the previous tile's K and P are read
-      if (tid < kTile) {
-        int64_t page = 0;
-        const int64_t r = attn_row(a, tok, v0 + tid, &page);
-        srow[tid] = r;
-        sscale[tid] = r >= 0 ? page_scale(a.k_scale, LAYOUT, page) : 1.0f;
-      }
-      __syncthreads();
-      for (int c = tid; c < kTile * R::kChunks; c += 256) {
-        const int i = c / R::kChunks, k = c % R::kChunks;
-        const int64_t r = srow[i];
-        float v[R::kMax];
-#pragma unroll
-        for (int e = 0; e < R::kMax; ++e) v[e] = 0.f;
-        if (r >= 0) {
-          const uint8_t* p = a.cache + r * R::kBytes;
-          R::decode(p, k, *reinterpret_cast<const uint4*>(p + R::offset(k)), v);
-        }
-        uint16_t* d = sk + i * kKPitch + R::col(k);
-        const int width = R::width(k);
-#pragma unroll
-        for (int e = 0; e < R::kMax; e += 8)
-          if (e < width)
-            *reinterpret_cast<uint4*>(d + e) =
-                make_uint4(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]),
-                           pack_bf16x2(v[e + 4], v[e + 5]), pack_bf16x2(v[e + 6], v[e + 7]));
-      }
-      __syncthreads();
-      // ---- S
-      {
-        float c[kNQ][4];
-#pragma unroll
-        for (int n = 0; n < kNQ; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
-        const uint32_t qa = smem_u32(sq + (16 * wm + (lane & 15)) * kKPitch + 8 * (lane >> 4));
-        const uint32_t kb = smem_u32(sk + (8 * MT * wn + (lane & 7)) * kKPitch + 8 * ((lane >> 3) & 1));
-#pragma unroll 4
-        for (int k = 0; k < kRowElems / 16; ++k) {
-          uint32_t ra[4];
-          ldsm_x4(ra, qa + 32 * k);
-#pragma unroll
-          for (int n = 0; n < kNQ; ++n) {
-            uint32_t b0, b1;
-            ldsm_x2(b0, b1, kb + 8 * n * kKPitch * 2 + 32 * k);
-            mma_bf16_16816(c[n], ra[0], ra[1], ra[2], ra[3], b0, b1);
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < kNQ; ++n) {
-          float* d = ss + (16 * wm + g) * kSPitch + 8 * MT * wn + 8 * n + 2 * q4;
-          d[0] = c[n][0];
-          d[1] = c[n][1];
-          d[8 * kSPitch] = c[n][2];
-          d[8 * kSPitch + 1] = c[n][3];
-        }
-      }
-      __syncthreads();
-      // ---- softmax: kTph threads a head
-      {
-        const int h = tid / kTph, part = tid % kTph;
-        float v[kCols], mx = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kCols; ++i) {
-          const int p = part + kTph * i;
-          v[i] = srow[p] >= 0 ? ss[h * kSPitch + p] * (sscale[p] * xs) : -INFINITY;
-          mx = fmaxf(mx, v[i]);
-        }
-#pragma unroll
-        for (int s = 1; s < kTph; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, s));
-        const float m_old = sm[h], m_new = fmaxf(m_old, mx);
-        const float m_use = m_new == -INFINITY ? 0.f : m_new;
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kCols; ++i) {
-          const int p = part + kTph * i;
-          const float e = exp2f(v[i] - m_use);
-          sum += e;
-          sp[h * kPPitch + p] = f2bf_bits(e * sscale[p]);
-        }
-#pragma unroll
-        for (int s = 1; s < kTph; s <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
-        __syncwarp();
-        if (part == 0) {
-          const float al = m_old == -INFINITY ? 0.f : exp2f(m_old - m_use);
-          alpha[h] = al;
-          sl[h] = sl[h] * al + sum;
-          sm[h] = m_new;
-        }
-      }
-      __syncthreads();
-      // ---- O
-      {
-        const float a0 = alpha[16 * wm + g], a1 = alpha[16 * wm + g + 8];
-#pragma unroll
-        for (int n = 0; n < kNO; ++n) {
-          o[n][0] *= a0;
-          o[n][1] *= a0;
-          o[n][2] *= a1;
-          o[n][3] *= a1;
-        }
-        const uint32_t pa = smem_u32(sp + (16 * wm + (lane & 15)) * kPPitch + 8 * (lane >> 4));
-        const uint32_t vb = smem_u32(sk + (lane & 15) * kKPitch + 64 * MT * wn + 8 * (lane >> 4));
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k) {
-          uint32_t ra[4];
-          ldsm_x4(ra, pa + 32 * k);
-#pragma unroll
-          for (int n = 0; n < kNO; n += 2) {
-            uint32_t rb[4];
-            ldmatrix_x4_trans(rb, vb + (16 * k * kKPitch + 8 * n) * 2);
-            mma_bf16_16816(o[n], ra[0], ra[1], ra[2], ra[3], rb[0], rb[1]);
-            mma_bf16_16816(o[n + 1], ra[0], ra[1], ra[2], ra[3], rb[2], rb[3]);
-          }
-        }
-      }
-    }
-    // ---- the stretch is done: the output, or a partial
-    const bool whole = x == tok.start && seg_end == tok.end;
-    const int slot = 2 * worker + (x == first ? 0 : 1);
-    const int ha = 16 * wm + g, hb = ha + 8;
-    if (whole) {
-      const float la = sl[ha], lb = sl[hb];
-      const float ra = la == 0.f ? 0.f : 1.0f / la, rb = lb == 0.f ? 0.f : 1.0f / lb;
-#pragma unroll
-      for (int n = 0; n < kNO; ++n) {
-        const int c = 64 * MT * wn + 8 * n + 2 * q4;
-        if (h0 + ha < a.heads)
-          *reinterpret_cast<uint32_t*>(a.out + (int64_t)t * a.o_ts + (int64_t)(h0 + ha) * a.o_hs + c) =
-              pack_bf16x2(o[n][0] * ra, o[n][1] * ra);
-        if (h0 + hb < a.heads)
-          *reinterpret_cast<uint32_t*>(a.out + (int64_t)t * a.o_ts + (int64_t)(h0 + hb) * a.o_hs + c) =
-              pack_bf16x2(o[n][2] * rb, o[n][3] * rb);
-      }
-      if (tid < kHeads && h0 + tid < a.heads && a.lse != nullptr)
-        a.lse[(int64_t)t * a.heads + h0 + tid] = attn_lse(sm[tid], sl[tid]);
-    } else {
-#pragma unroll
-      for (int n = 0; n < kNO; ++n) {
-        const int c = 64 * MT * wn + 8 * n + 2 * q4;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          reinterpret_cast<float*>(&attn_part(a, slot, (h0 + (e < 2 ? ha : hb)) >> 2, c + (e & 1)))
-              [(e < 2 ? ha : hb) & 3] = o[n][e];
-      }
-      if (tid < kHeads) attn_part_ml(a, h0 + tid)[slot] = make_float2(sm[tid], sl[tid]);
-    }
-    x = seg_end;
-  }
-}
 
 // --------------------------------------------------------------- joining
 //
@@ -401,46 +136,6 @@ __global__ void __launch_bounds__(WIDE ? 256 : 128) mla_attn_join_kernel(const A
   }
 }
 
-template <int MT>
-cudaError_t launch_mma(const AttnArgs& a, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.workers * a.groups));
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = MmaSmem<MT>::kBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  switch (a.layout) {
-    case MLA_KV_FP8_E4M3: return cudaLaunchKernelEx(&cfg, mla_attn_mma_kernel<MT, MLA_KV_FP8_E4M3>, a);
-    case MLA_KV_FP8_E4M3_PAGE:
-      return cudaLaunchKernelEx(&cfg, mla_attn_mma_kernel<MT, MLA_KV_FP8_E4M3_PAGE>, a);
-    case MLA_KV_FP8_DS_MLA: return cudaLaunchKernelEx(&cfg, mla_attn_mma_kernel<MT, MLA_KV_FP8_DS_MLA>, a);
-    default: return cudaLaunchKernelEx(&cfg, mla_attn_mma_kernel<MT, MLA_KV_NVFP4_DS_MLA>, a);
-  }
-}
-
-template <int MT, int LAYOUT>
-cudaError_t prepare_mma() {
-  static_assert(MmaSmem<MT>::kBytes <= 232448, "shared memory budget");
-  return cudaFuncSetAttribute(mla_attn_mma_kernel<MT, LAYOUT>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, MmaSmem<MT>::kBytes);
-}
-template <int MT>
-cudaError_t prepare_mma_all() {
-  cudaError_t e = prepare_mma<MT, MLA_KV_FP8_E4M3>();
-  if (e == cudaSuccess) e = prepare_mma<MT, MLA_KV_FP8_E4M3_PAGE>();
-  if (e == cudaSuccess) e = prepare_mma<MT, MLA_KV_FP8_DS_MLA>();
-  if (e == cudaSuccess) e = prepare_mma<MT, MLA_KV_NVFP4_DS_MLA>();
-  return e;
-}
-
-// Heads a CTA of the mma.sync kernel takes: 16 or 32 where that covers all of
-// them (less padding, and more workers of the same tiles), 64 otherwise.
-int mma_tiles(int heads) { return attn_tc_heads(heads) / 16; }
-
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool known_layout(int layout) { return layout >= MLA_KV_FP8_E4M3 && layout <= MLA_KV_FP8_E4M3_PAGE; }
@@ -483,7 +178,7 @@ int mla_attn_create(mla_attn_t* out, int max_batch, int heads) {
   h->heads = heads;
   h->max_batch = max_batch;
   int rc = MLA_ECUDA;
-  const int gh = 16 * mla::mma_tiles(heads);
+  const int gh = mla::attn_tc_heads(heads);
   const int groups = (heads + gh - 1) / gh;
   size_t slots = 0;
   if (cudaGetDevice(&h->device) != cudaSuccess) goto fail;
@@ -493,9 +188,8 @@ int mla_attn_create(mla_attn_t* out, int max_batch, int heads) {
     rc = MLA_EUNSUPPORTED;
     goto fail;
   }
-  if (mla::prepare_mma_all<1>() != cudaSuccess || mla::prepare_mma_all<2>() != cudaSuccess ||
-      mla::prepare_mma_all<4>() != cudaSuccess || mla::prepare_attn_tc() != cudaSuccess ||
-      mla::prepare_attn_ds() != cudaSuccess)
+  if (mla::prepare_attn_tc() != cudaSuccess || mla::prepare_attn_ds() != cudaSuccess ||
+      mla::prepare_attn_nv() != cudaSuccess)
     goto fail;
   slots = (size_t)(h->num_sms / groups) * 2 * groups * gh;
   rc = MLA_ENOMEM;
@@ -545,7 +239,7 @@ int mla_attn_decode(mla_attn_t h, int batch, const void* q_latent, int64_t ql_to
       !mla::aligned4(sel) || !mla::aligned4(sel_count) || !mla::aligned4(lse))
     return MLA_EINVAL;
 
-  const int mt = mla::mma_tiles(h->heads);
+  const int gh = mla::attn_tc_heads(h->heads);
   mla::AttnArgs a = {};
   a.q_latent = static_cast<const uint8_t*>(q_latent);
   a.q_pe = static_cast<const uint8_t*>(q_pe);
@@ -578,20 +272,15 @@ int mla_attn_decode(mla_attn_t h, int batch, const void* q_latent, int64_t ql_to
   a.plan = h->plan;
   a.heads = h->heads;
   a.batch = batch;
-  // Both kernels take 16, 32 or 64 heads a CTA by the same rule.
-  a.groups = (h->heads + 16 * mt - 1) / (16 * mt);
-  a.heads_pad = a.groups * 16 * mt;
+  a.groups = (h->heads + gh - 1) / gh;
+  a.heads_pad = a.groups * gh;
   a.workers = h->num_sms / a.groups;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (mla::attn_tc_serves(a)) {
-    a.tile = mla::attn_tc_tile();
-    e = layout == MLA_KV_FP8_DS_MLA ? mla::launch_attn_ds(a, st) : mla::launch_attn_tc(a, st);
-  } else {
-    a.tile = mla::kTile;
-    e = mt == 1   ? mla::launch_mma<1>(a, st)
-        : mt == 2 ? mla::launch_mma<2>(a, st)
-                  : mla::launch_mma<4>(a, st);
+  switch (layout) {
+    case MLA_KV_FP8_DS_MLA: e = mla::launch_attn_ds(a, st); break;
+    case MLA_KV_NVFP4_DS_MLA: e = mla::launch_attn_nv(a, st); break;
+    default: e = mla::launch_attn_tc(a, st);
   }
   int rc = mla::launched(e);
   if (rc != MLA_OK) return rc;

@@ -8,6 +8,7 @@ namespace mla {
 namespace {
 
 constexpr int kAttnMaxBatch = MLA_MAX_BATCH;
+constexpr uint32_t kAttnTile = 128;  // positions a tile
 
 // Tiles of the batch, spread evenly.  Token t's context is a list of virtual
 // positions 0 .. nv_t - 1 (its first len_t positions, or the positions of its
@@ -74,7 +75,7 @@ __device__ __forceinline__ void attn_make_plan(const AttnArgs& a, AttnPlan* p, u
     const int32_t len = a.lens[tid];
     const int row = a.token_row != nullptr ? a.token_row[tid] : tid;
     const uint32_t nv = attn_positions(a, tid, len, row, flag);
-    n = (nv + a.tile - 1) / a.tile;
+    n = (nv + kAttnTile - 1) / kAttnTile;
     if (seen != nullptr) {
       seen->len[tid] = len;
       seen->row[tid] = row;

@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (n > 0) tc_wait_warp(&d_free[0], 1u, dead);  // plane 3 of the tile before has been read
       tc_wait_warp(rope_full, (uint32_t)(n & 1), dead);
       tc_after();
-      tc_mma4_bf16<2, 2>(tmem, dkr, dqr, id_r, 0u);
+      tc_mma4_f16<2, 2>(tmem, dkr, dqr, id_r, 0u);
       tc_commit(rope_empty);
       tc_commit(&d_full[0]);
     };

@@ -580,12 +580,9 @@ cudaError_t prepare_tc_heads() {
 
 }  // namespace
 
+// Heads a CTA takes: 16 or 32 where that covers all of them (less padding, and
+// more workers of the same tiles), 64 otherwise.
 int attn_tc_heads(int heads) { return heads <= 16 ? 16 : heads <= 32 ? 32 : 64; }
-int attn_tc_tile() { return kTcTile; }
-
-bool attn_tc_serves(const AttnArgs& a) {
-  return a.layout != MLA_KV_NVFP4_DS_MLA;
-}
 
 cudaError_t prepare_attn_tc() {
   cudaError_t e = prepare_tc_heads<16>();

@@ -1,4 +1,4 @@
-// mla_attn_tc.cuh - what the two tcgen05 attention kernels share: descriptors,
+// mla_attn_tc.cuh - what the tcgen05 attention kernels share: descriptors,
 // MMA issue, TMEM access, the two-term weights and queries, bounded waits.
 #pragma once
 
@@ -10,7 +10,7 @@
 namespace mla {
 namespace {
 
-constexpr int kTcTile = 128;               // cache rows a tile: MMA M of S^T, K of O^T
+constexpr int kTcTile = kAttnTile;         // cache rows a tile: MMA M of S^T, K of O^T
 constexpr int kPlane = kTcTile * 128;      // a 128-byte column plane of a tile
 constexpr int kTcSoft = 256;               // softmax threads (warps 0-7)
 constexpr int kTcThreads = kTcSoft + 64;   // + a TMA warp, an MMA warp
@@ -35,7 +35,13 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t saddr, uint32_t sbo, uint32
   return d;
 }
 
-// Instruction descriptor, FP32 accumulators: operand types (0 E4M3, 1 E5M2),
+// M-major over more than one atom: the atoms of 128 bytes of M `lbo` apart.
+__device__ __forceinline__ uint64_t tc_desc_wide(uint32_t saddr, uint32_t sbo, uint32_t lbo) {
+  return (tc_desc(saddr, sbo, 2) & ~((uint64_t)0x3FFF << 16)) | (uint64_t)(lbo >> 4) << 16;
+}
+
+// Instruction descriptor, FP32 accumulators: operand types (0 E4M3, 1 E5M2; of
+// kind::f16, 0 FP16, 1 BF16),
 // and whether A and B are M/N-major.
 __host__ __device__ constexpr uint32_t tc_idesc(int m, int n, int btype, bool a_mn, bool b_mn) {
   return (1u << 4) | ((uint32_t)btype << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
@@ -75,7 +81,7 @@ __device__ __forceinline__ void tc_mma4(uint32_t d, uint64_t a, uint64_t b, uint
                : "memory");
 }
 template <int AS, int BS>
-__device__ __forceinline__ void tc_mma4_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+__device__ __forceinline__ void tc_mma4_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
                                              uint32_t accumulate) {
   asm volatile(TC_MMA_ENTER "mov.b64 x, %1;\n\tmov.b64 y, %2;\n\t" TC_MMA_F16("%3", "p")
                TC_MMA_NEXT("%5", "%6") TC_MMA_F16("%3", "t")

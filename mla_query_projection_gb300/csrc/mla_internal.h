@@ -245,23 +245,21 @@ struct AttnArgs {
   uint32_t* err;
   int heads, heads_pad, groups, batch;
   int workers;  // per head group
-  int tile;     // positions a tile
 };
 
 // The driver's tensor-map encoder (null where it cannot be had).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
-// The tcgen05 kernels (mla_attn_tc.cu, mla_attn_ds.cu): whether they serve a
-// call (E4M3 codes, pages of a multiple of 8 rows, row numbers within 31
-// bits), their heads a CTA and rows a tile.
-bool attn_tc_serves(const AttnArgs& a);
+// The attention kernels, by layout: E4M3 rows under one scale or a page's
+// (mla_attn_tc.cu), fp8_ds_mla (mla_attn_ds.cu), nvfp4_ds_mla (mla_attn_nv.cu);
+// and the heads that a CTA of theirs takes.
 int attn_tc_heads(int heads);
-int attn_tc_tile();
 cudaError_t prepare_attn_tc();
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t stream);
-// The same for fp8_ds_mla rows (mla_attn_ds.cu).
 cudaError_t prepare_attn_ds();
 cudaError_t launch_attn_ds(const AttnArgs& a, cudaStream_t stream);
+cudaError_t prepare_attn_nv();
+cudaError_t launch_attn_nv(const AttnArgs& a, cudaStream_t stream);
 
 // Block tables and slot map of a step (mla_tables.cu).
 struct TableArgs {
