@@ -506,6 +506,12 @@ MLA_API int mla_attn_create(mla_attn_t* out, int max_batch, int heads);
  * that do not count are never used as values, whatever they hold.  A
  * token_row outside the table counts as no position and raises
  * MLA_DEVERR_BAD_SLOT, as do lengths beyond the row.
+ * Sums, maxima and denominators are FP32.  The weights p meet the values with
+ * a relative error of at most 2^-7 (2^-11 for nvfp4_ds_mla rows); with
+ * fp8_ds_mla rows, whose scales are positive, this holds for rows whose scale
+ * is at least 2^-14 of the largest scale that the same 128 columns have in the
+ * context.  A NaN or an infinity in a head's query, or a NaN in a row that
+ * counts, makes the head's results NaN.
  * Results do not depend on the order in which the GPU runs the work.  Calls
  * sharing a handle, captured or not, must be ordered on one stream: they share
  * its workspace.  Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.
@@ -533,7 +539,8 @@ MLA_API void mla_attn_destroy(mla_attn_t h);
  * mean[p][c] = bf16(sum of value c of the page's filled rows / their number),
  * for the pages of blocks lens_from[r] / page_size .. of each request r up to
  * position lens_to[r] (positions from lens_to[r] on are not filled).  Other
- * pages' means are left as they are.
+ * pages' means are left as they are.  A page that several requests of the call
+ * hold should be filled alike by them: each of them writes its mean.
  *
  *   lens_from, lens_to  device int32 [rows]: lens and lens_out of
  *                 mla_tables_step.  lens_from 0 recomputes a request whole.

@@ -9,9 +9,10 @@
 //    queries times the same power of two as the codes' queries) another; the
 //    softmax thread, which owns one row, adds R + sum_j scale_j D_j.
 //  * O^T: plane j's weights are P times scale_j / ref_j, split into an E4M3 and
-//    an E5M2 term each, ref_j the largest scale so far (a power of two, like
-//    the scales, so the factors are exact); O_j is multiplied by ref_j at the
-//    end.
+//    an E5M2 term each, ref_j the largest scale so far; O_j is multiplied by
+//    ref_j at the end.  The factor and P go to FP16 first (2^-11 each, and the
+//    factor exact where the scales are powers of two, as the decode step writes
+//    them): half the conversions of FP32 pairs, small next to the terms' 2^-7.
 // TMEM: four 64-column accumulators for the five products of a tile (the rope
 // product and plane 3 share one, in turn), and O^T's four planes.
 //

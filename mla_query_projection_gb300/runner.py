@@ -150,22 +150,25 @@ def _check(rc: int, what: str) -> None:
         raise B.MlaError(rc, what)
 
 
-def _flat(x, dtype, n: int, what: str) -> int:
-    """Address of a contiguous tensor of `dtype` with at least n elements; 0 for None."""
+def _flat(x, dtype, n: int, dev: int, what: str) -> int:
+    """Address of a contiguous tensor of `dtype` on device `dev` with at least n elements; 0 for None."""
     if x is None:
         return 0
-    if x.dtype is not dtype or not x.is_contiguous() or x.numel() < n:
+    if x.dtype is not dtype or not x.is_contiguous() or x.numel() < n or x.get_device() != dev:
         _refuse(what)
     return x.data_ptr()
 
 
-def _stream_of(x: torch.Tensor, stream) -> int:
+def _stream_of(dev: int, stream, what: str) -> int:
+    """The stream's handle; the tensors' device has to be the current one, on which the library launches."""
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        _refuse(what + ": tensors that are not on the current device")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(x.get_device())
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _query_args(q_latent, q_pe, q_scale_inv, what: str):
+def _query_args(q_latent, q_pe, q_scale_inv, dev: int, what: str):
     """(tokens, heads, the C arguments q_latent .. q_scale_inv)."""
     tokens, heads, width = q_latent.shape
     dtype = q_latent.dtype
@@ -174,26 +177,28 @@ def _query_args(q_latent, q_pe, q_scale_inv, what: str):
         _refuse(what + ": query type")
     lt, lh, l1 = q_latent.stride()
     pt, ph, p1 = q_pe.stride()
-    if width != 512 or q_pe.shape != (tokens, heads, 64) or l1 != 1 or p1 != 1:
+    if (width != 512 or q_pe.shape != (tokens, heads, 64) or l1 != 1 or p1 != 1
+            or q_latent.get_device() != dev or q_pe.get_device() != dev):
         _refuse(what + ": query shape")
     return tokens, heads, (q_latent.data_ptr(), lt, lh, q_pe.data_ptr(), pt, ph,
-                           _flat(q_scale_inv, _F32, 1, what + ": q_scale_inv"))
+                           _flat(q_scale_inv, _F32, 1, dev, what + ": q_scale_inv"))
 
 
-def _cache_args(cache, layout, k_scale, what: str):
+def _cache_args(cache, layout, k_scale, dev: int, what: str):
     """The C arguments kv_cache .. k_scale."""
     pages, page, row = cache.shape
-    if cache.dtype is not _U8 or row != _ROW_BYTES.get(layout) or not cache.is_contiguous():
+    if (cache.dtype is not _U8 or row != _ROW_BYTES.get(layout) or not cache.is_contiguous()
+            or cache.get_device() != dev):
         _refuse(what + ": cache")
     return (cache.data_ptr(), pages, page, layout,
-            _flat(k_scale, _F32, pages if layout == B.MLA_KV_FP8_E4M3_PAGE else 1, what + ": k_scale"))
+            _flat(k_scale, _F32, pages if layout == B.MLA_KV_FP8_E4M3_PAGE else 1, dev, what + ": k_scale"))
 
 
-def _rows2d(x, dtype, what: str):
+def _rows2d(x, dtype, dev: int, what: str):
     """(address, entries between rows, rows, columns) of a [rows, columns] tensor with unit inner stride."""
     rows, cols = x.shape
     st, s1 = x.stride()
-    if x.dtype is not dtype or (s1 != 1 and cols > 1) or (rows > 1 and st < cols):
+    if x.dtype is not dtype or (s1 != 1 and cols > 1) or (rows > 1 and st < cols) or x.get_device() != dev:
         _refuse(what)
     return x.data_ptr(), (st if rows > 1 else cols), rows, cols
 
@@ -206,62 +211,71 @@ def tables_step(new_tokens, lens, block_table, free_pages, free_count, page_size
     ``block_table`` and ``free_pages`` are updated; ``lens_out`` and
     ``free_count_out`` may be ``lens`` and ``free_count`` themselves."""
     what = "tables_step: arrays"
+    dev = lens.get_device()
     rows, tokens, pages = lens.numel(), slot_mapping.numel(), free_pages.numel()
     table_rows, width = block_table.shape
     if table_rows != rows:
         _refuse("tables_step: block table")
     _check(B.load().mla_tables_step(
-        rows, _flat(new_tokens, _I32, rows, what), _flat(lens, _I32, rows, what),
-        _flat(lens_out, _I32, rows, what), _flat(block_table, _I32, 1, what), width,
-        _flat(free_pages, _I32, 1, what), _flat(free_count, _I32, 1, what),
-        _flat(free_count_out, _I32, 1, what), pages, page_size, tokens,
-        _flat(slot_mapping, _I64, 1, what), _flat(token_row, _I32, tokens, what),
-        _flat(token_len, _I32, tokens, what), _flat(cu_tokens, _I32, rows + 1, what),
-        _flat(flags, _I32, 1, what), _stream_of(lens, stream)), "mla_tables_step")
+        rows, _flat(new_tokens, _I32, rows, dev, what), _flat(lens, _I32, rows, dev, what),
+        _flat(lens_out, _I32, rows, dev, what), _flat(block_table, _I32, 1, dev, what), width,
+        _flat(free_pages, _I32, 1, dev, what), _flat(free_count, _I32, 1, dev, what),
+        _flat(free_count_out, _I32, 1, dev, what), pages, page_size, tokens,
+        _flat(slot_mapping, _I64, 1, dev, what), _flat(token_row, _I32, tokens, dev, what),
+        _flat(token_len, _I32, tokens, dev, what), _flat(cu_tokens, _I32, rows + 1, dev, what),
+        _flat(flags, _I32, 1, dev, what), _stream_of(dev, stream, "tables_step")), "mla_tables_step")
 
 
 def blocks_mean(cache, layout, k_scale, block_table, lens_from, lens_to, mean, flags=None,
                 stream=None) -> None:
     """Mean keys ``mean`` [pages, 576] of the blocks between two lengths (``mla_blocks_mean``)."""
-    args = _cache_args(cache, layout, k_scale, "blocks_mean")
-    table, bt_stride, table_rows, _ = _rows2d(block_table, _I32, "blocks_mean: block table")
+    dev = cache.get_device()
+    args = _cache_args(cache, layout, k_scale, dev, "blocks_mean")
+    table, bt_stride, table_rows, _ = _rows2d(block_table, _I32, dev, "blocks_mean: block table")
     rows = lens_to.numel()
     if table_rows < rows:
         _refuse("blocks_mean: block table")
     _check(B.load().mla_blocks_mean(
-        *args, table, bt_stride, rows, _flat(lens_from, _I32, rows, "blocks_mean: lengths"),
-        _flat(lens_to, _I32, rows, "blocks_mean: lengths"),
-        _flat(mean, _BF16, args[1] * 576, "blocks_mean: mean"),
-        _flat(flags, _I32, 1, "blocks_mean: flags"), _stream_of(cache, stream)), "mla_blocks_mean")
+        *args, table, bt_stride, rows, _flat(lens_from, _I32, rows, dev, "blocks_mean: lengths"),
+        _flat(lens_to, _I32, rows, dev, "blocks_mean: lengths"),
+        _flat(mean, _BF16, args[1] * 576, dev, "blocks_mean: mean"),
+        _flat(flags, _I32, 1, dev, "blocks_mean: flags"), _stream_of(dev, stream, "blocks_mean")),
+        "mla_blocks_mean")
 
 
 def blocks_score(q_latent, q_pe, mean, page_size, block_table, lens, scores, q_scale_inv=None,
                  token_row=None, flags=None, stream=None) -> None:
     """Scores [tokens, blocks] of every block for every query (``mla_blocks_score``)."""
-    tokens, heads, query = _query_args(q_latent, q_pe, q_scale_inv, "blocks_score")
+    dev = q_latent.get_device()
+    tokens, heads, query = _query_args(q_latent, q_pe, q_scale_inv, dev, "blocks_score")
     table_rows, width = block_table.shape
-    out, out_stride, out_rows, out_cols = _rows2d(scores, _F32, "blocks_score: scores")
+    out, out_stride, out_rows, out_cols = _rows2d(scores, _F32, dev, "blocks_score: scores")
     if out_rows < tokens or out_cols < width:
         _refuse("blocks_score: scores")
+    pages, columns = mean.shape
+    if columns != 576:
+        _refuse("blocks_score: mean")
     _check(B.load().mla_blocks_score(
-        tokens, heads, *query, _flat(mean, _BF16, 576, "blocks_score: mean"), mean.shape[0], page_size,
-        _flat(block_table, _I32, 1, "blocks_score: block table"), width, table_rows,
-        _flat(token_row, _I32, tokens, "blocks_score: token_row"),
-        _flat(lens, _I32, tokens, "blocks_score: lengths"), out, out_stride,
-        _flat(flags, _I32, 1, "blocks_score: flags"), _stream_of(q_latent, stream)), "mla_blocks_score")
+        tokens, heads, *query, _flat(mean, _BF16, 1, dev, "blocks_score: mean"), pages, page_size,
+        _flat(block_table, _I32, 1, dev, "blocks_score: block table"), width, table_rows,
+        _flat(token_row, _I32, tokens, dev, "blocks_score: token_row"),
+        _flat(lens, _I32, tokens, dev, "blocks_score: lengths"), out, out_stride,
+        _flat(flags, _I32, 1, dev, "blocks_score: flags"), _stream_of(dev, stream, "blocks_score")),
+        "mla_blocks_score")
 
 
 def blocks_select(scores, lens, page_size, keep_first, keep_last, sel, sel_count, stream=None) -> None:
     """The best-scored blocks ``sel`` [tokens, k] of every query (``mla_blocks_select``)."""
-    out, out_stride, tokens, k = _rows2d(sel, _I32, "blocks_select: sel")
-    sc, sc_stride, sc_rows, blocks = _rows2d(scores, _F32, "blocks_select: scores")
+    dev = scores.get_device()
+    out, out_stride, tokens, k = _rows2d(sel, _I32, dev, "blocks_select: sel")
+    sc, sc_stride, sc_rows, blocks = _rows2d(scores, _F32, dev, "blocks_select: scores")
     if sc_rows < tokens:
         _refuse("blocks_select: scores")
     _check(B.load().mla_blocks_select(
-        tokens, sc, sc_stride, blocks, _flat(lens, _I32, tokens, "blocks_select: lengths"), page_size,
+        tokens, sc, sc_stride, blocks, _flat(lens, _I32, tokens, dev, "blocks_select: lengths"), page_size,
         keep_first, keep_last, k, out, out_stride,
-        _flat(sel_count, _I32, tokens, "blocks_select: sel_count"), _stream_of(scores, stream)),
-        "mla_blocks_select")
+        _flat(sel_count, _I32, tokens, dev, "blocks_select: sel_count"),
+        _stream_of(dev, stream, "blocks_select")), "mla_blocks_select")
 
 
 class PagedAttention:
@@ -286,27 +300,28 @@ class PagedAttention:
         be strided (views of gathered rows); ``out`` BF16 [tokens, heads, 512]
         is allocated where it is not given, ``lse`` FP32 [tokens, heads] is
         written where it is."""
-        tokens, heads, query = _query_args(q_latent, q_pe, q_scale_inv, "attention")
-        paged = _cache_args(cache, layout, k_scale, "attention")
-        table, bt_stride, table_rows, _ = _rows2d(block_table, _I32, "attention: block table")
+        dev = q_latent.get_device()
+        tokens, heads, query = _query_args(q_latent, q_pe, q_scale_inv, dev, "attention")
+        paged = _cache_args(cache, layout, k_scale, dev, "attention")
+        table, bt_stride, table_rows, _ = _rows2d(block_table, _I32, dev, "attention: block table")
         if heads != self.heads:
             _refuse("attention: heads")
         sel_ptr = sel_stride = 0
         if sel is not None:
-            sel_ptr, sel_stride, sel_rows, _ = _rows2d(sel, _I32, "attention: sel")
+            sel_ptr, sel_stride, sel_rows, _ = _rows2d(sel, _I32, dev, "attention: sel")
             if sel_rows < tokens:
                 _refuse("attention: sel")
         if out is None:
             out = torch.empty((tokens, heads, 512), dtype=_BF16, device=q_latent.device)
         ot, oh, o1 = out.stride()
-        if out.dtype is not _BF16 or out.shape != (tokens, heads, 512) or o1 != 1:
+        if out.dtype is not _BF16 or out.shape != (tokens, heads, 512) or o1 != 1 or out.get_device() != dev:
             _refuse("attention: out")
         _check(B.load().mla_attn_decode(
             self.handle, tokens, *query, *paged, table, bt_stride, table_rows,
-            _flat(token_row, _I32, tokens, "attention: token_row"),
-            _flat(lens, _I32, tokens, "attention: lengths"), sel_ptr, sel_stride,
-            _flat(sel_count, _I32, tokens, "attention: sel_count"), softmax_scale, out.data_ptr(), ot, oh,
-            _flat(lse, _F32, tokens * heads, "attention: lse"), _stream_of(q_latent, stream)),
+            _flat(token_row, _I32, tokens, dev, "attention: token_row"),
+            _flat(lens, _I32, tokens, dev, "attention: lengths"), sel_ptr, sel_stride,
+            _flat(sel_count, _I32, tokens, dev, "attention: sel_count"), softmax_scale, out.data_ptr(), ot, oh,
+            _flat(lse, _F32, tokens * heads, dev, "attention: lse"), _stream_of(dev, stream, "attention")),
             "mla_attn_decode")
         return out, lse
 

@@ -248,13 +248,13 @@ def test_attention_offsets_beyond_32_bits(layout):
     attn.close()
 
 
-@pytest.mark.parametrize("layout", [0, 1, 3])
-def test_attention_growing_maximum_and_a_sink(layout):
+@pytest.mark.parametrize("layout,page", [(0, 64), (1, 64), (2, 64), (3, 64), (0, 7), (1, 12), (2, 1), (3, 100)])
+def test_attention_growing_maximum_and_a_sink(layout, page):
     """The largest logit comes late, and one key (a sink) outweighs thousands of others: the running
     maximum has to grow, and small weights have to keep their sum."""
     rng = np.random.default_rng(16 + layout)
-    page, n, heads = 64, 6000, 64
-    pages = 94
+    n, heads = 6000, 64
+    pages = -(-n // page)
     cache, k_scale = C.make_cache(rng, pages, page, layout)
     table = C.make_table(rng, [n], page, pages)
     q64 = np.zeros((1, heads, 576))
@@ -265,7 +265,9 @@ def test_attention_growing_maximum_and_a_sink(layout):
     # rope value 0 of a key: grows with the position, the last key far above all
     for i, (p, o) in enumerate(where):
         v = 8.0 * i / n + (64.0 if i == n - 5 else 0.0)
-        if layout == 1:
+        if layout == 2:
+            cache[p, o, 288] = int(torch.tensor([v]).to(torch.float8_e4m3fn).view(torch.uint8))
+        elif layout == 1:
             cache[p, o, 528:530] = torch.tensor([v]).to(torch.bfloat16).view(torch.uint8).numpy()
         else:
             sc = float(k_scale[p] if layout == 3 else k_scale[0])
@@ -278,6 +280,99 @@ def test_attention_growing_maximum_and_a_sink(layout):
                          SCALE, k_scale=dev(k_scale), lse=lse)
     check_attention(out[0], lse[0], q64[0], keys64(cache, k_scale, layout, where), SCALE, layout)
     attn.close()
+
+
+@pytest.mark.parametrize("layout", [0, 1, 2, 3])
+@pytest.mark.parametrize("page", [1, 64])
+def test_attention_full_batch(layout, page):
+    """As many tokens as a call takes, most of them short, empty ones among them."""
+    rng = np.random.default_rng(40 + layout)
+    lens = [int(n) for n in rng.integers(0, 40, B.MLA_MAX_BATCH)]
+    lens[0], lens[17], lens[100], lens[255] = 1, 1500, 0, 129
+    assert run_attention(rng, lens, 16, layout, page) == 0
+
+
+@pytest.mark.parametrize("ratio", [1.0, 1.3, 0.0])
+def test_attention_scales_that_differ(ratio):
+    """fp8_ds_mla scales a row apart by up to 2^12, by no power of two, and zero in some rows.
+
+    (Scaled weights go through FP16 twice, 2^-11 each: 2^-7 + 2^-10 of a weight at
+    most, and 2^-24 of a plane's largest row for what falls below FP16's steps.)"""
+    rng = np.random.default_rng(45)
+    n, heads, page = 700, 64, 64
+    cache, k_scale = C.make_cache(rng, 12, page, 1)
+    table = C.make_table(rng, [n], page, 12)
+    sc = np.exp2(-rng.integers(0, 13, (12, page, 4))).astype(np.float32) * np.float32(0.02 * max(ratio, 1.0))
+    if ratio == 0.0:
+        sc[rng.random(sc.shape) < 0.2] = 0.0
+    cache[:, :, 512:528] = sc.view(np.uint8).reshape(12, page, 16)
+    ql, qp, inv, q64 = queries(rng, 1, heads)
+    where = C.positions(n, page, table.shape[1], 12, table[0])
+    keys = keys64(cache, k_scale, 1, where)
+    attn = R.PagedAttention(1, heads)
+    lse = torch.empty(1, heads, device="cuda")
+    out, _ = attn.decode(ql, qp, dev(cache), 1, dev(table), dev(np.array([n], dtype=np.int32)), SCALE, lse=lse)
+    assert attn.error_flags() == 0
+    attn.close()
+    o, want_lse, mass, mag = C.attend64(q64[0], keys, SCALE)
+    slack = 2.0 ** -14.8 * mag + 2.0 ** -17.8 * np.abs(q64[0]).max(1) * np.abs(keys).sum(1).max() * SCALE \
+        + (n / 256 + 16) * 2.0 ** -24
+    assert (np.abs(lse[0].double().cpu().numpy() - want_lse) <= slack + 2.0 ** -23 * np.abs(want_lse)).all()
+    err = np.abs(out[0].double().cpu().numpy() - o)
+    floor = n * 2.0 ** -24 * 448 * float(sc.max())
+    assert (err <= (2.0 ** -7 + 2.0 ** -10 + 2 * slack)[:, None] * mass + 2.0 ** -8 * np.abs(o) + floor).all(), err.max()
+
+
+def test_attention_of_a_nan_row():
+    """A NaN in a row that counts reaches the heads' results, in that token only."""
+    rng = np.random.default_rng(46)
+    for layout in (0, 1, 2, 3):
+        cache, k_scale = C.make_cache(rng, 4, 64, layout)
+        table = np.array([[0, 1], [2, 3]], dtype=np.int32)
+        cache[1, 5] = 0x7F if layout != 1 else 0xFF
+        ql, qp, inv, q64 = queries(rng, 2, 16)
+        attn = R.PagedAttention(2, 16)
+        out, _ = attn.decode(ql, qp, dev(cache), layout, dev(table), dev(np.array([100, 100], dtype=np.int32)), SCALE,
+                             k_scale=dev(k_scale))
+        assert out[0].isnan().all(), layout
+        assert not out[1].isnan().any(), layout
+        attn.close()
+
+
+def test_attention_two_handles_at_once():
+    """Calls of two handles run side by side on two streams; graphs of one handle follow one another."""
+    rng = np.random.default_rng(47)
+    cache, k_scale = C.make_cache(rng, 200, 64, 3)
+    table = dev(C.make_table(rng, [6000, 6100], 64, 200))
+    cache, k_scale = dev(cache), dev(k_scale)
+    lens = [dev(np.array(x, dtype=np.int32)) for x in ([6000, 6100], [3001, 17])]
+    ql, qp, inv, q64 = queries(rng, 2, 128)
+    attn = [R.PagedAttention(2, 128) for _ in range(2)]
+    want = []
+    for a, n in zip(attn, lens):
+        want.append(a.decode(ql, qp, cache, 3, table, n, SCALE, k_scale=k_scale)[0])
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], [torch.zeros_like(want[0]) for _ in range(2)]
+    for _ in range(20):
+        for a, n, s, o in zip(attn, lens, streams, outs):
+            with torch.cuda.stream(s):
+                a.decode(ql, qp, cache, 3, table, n, SCALE, k_scale=k_scale, out=o)
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert torch.equal(w, o)
+        o.zero_()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g, n, o in zip(graphs, lens, outs):  # both on the first handle's workspace
+        with torch.cuda.graph(g):
+            attn[0].decode(ql, qp, cache, 3, table, n, SCALE, k_scale=k_scale, out=o)
+    for _ in range(3):
+        graphs[0].replay()
+        graphs[1].replay()
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert torch.equal(w, o)
+    for a in attn:
+        a.close()
 
 
 def test_attention_repeats_and_streams():
@@ -318,6 +413,9 @@ def test_attention_refuses_more_tokens_than_its_workspace():
     ql, qp, _, _ = queries(np.random.default_rng(1), 2, 16)
     cache, table = torch.zeros(2, 64, 576, dtype=torch.uint8).cuda(), torch.zeros(2, 1, dtype=torch.int32).cuda()
     lens = torch.ones(2, dtype=torch.int32).cuda()
+    host = torch.ones(2, dtype=torch.int32)  # lengths in host memory
+    with pytest.raises(B.MlaError):
+        attn.decode(ql[:1], qp[:1], cache, 0, table, host, SCALE, k_scale=torch.ones(1).cuda())
     for kw in (dict(), dict(sel=table)):  # too many tokens; a selection without its counts
         with pytest.raises(B.MlaError):
             attn.decode(ql, qp, cache, 0, table, lens, SCALE, k_scale=torch.ones(1).cuda(), **kw)

@@ -119,6 +119,22 @@ def test_runner_refuses_what_would_be_misread():
             R.blocks_mean(a["cache"], a["layout"], a["k_scale"], a["table"], lens, lens, a["mean"], stream=0)
 
 
+def test_runner_refuses_tensors_off_the_device():
+    """What would pass every other check, but lies in host memory, is refused before a launch."""
+    i32 = torch.int32
+    scores, lens, sel = torch.zeros(2, 8), torch.ones(2, dtype=i32), torch.zeros(2, 4, dtype=i32)
+    cache, table = torch.zeros(4, 64, 576, dtype=torch.uint8), torch.zeros(2, 8, dtype=i32)
+    mean, k_scale = torch.zeros(4, 576, dtype=torch.bfloat16), torch.ones(1)
+    ql, qp = torch.zeros(2, 16, 512, dtype=torch.bfloat16), torch.zeros(2, 16, 64, dtype=torch.bfloat16)
+    for call in (lambda: R.blocks_select(scores, lens, 64, 0, 0, sel, lens.clone(), stream=0),
+                 lambda: R.blocks_mean(cache, 0, k_scale, table, lens, lens, mean, stream=0),
+                 lambda: R.blocks_score(ql, qp, mean, 64, table, lens, scores, stream=0)):
+        with pytest.raises(B.MlaError, match="device"):
+            call()
+    with pytest.raises(B.MlaError, match="mean"):  # rows of another width
+        R.blocks_score(ql, qp, mean.reshape(-1, 64), 64, table, lens, scores, stream=0)
+
+
 def test_decode_takes_the_page_scaled_layout_only_with_scales():
     # a null handle is refused before the layout is looked at; the noalloc entry checks its layout itself
     args = [16, P, P, P, P, 1e-6, 1, P, 0, P, 0, P, 0, P, P, 4, 64, 3, None, P, P, None, None, None]
