@@ -3,22 +3,28 @@
 Each ``csrc/*.cu`` is compiled to an object in parallel, then linked into one
 shared library next to this file.  The CUDA runtime is linked statically, so
 the library loads on a machine without a GPU (every call then returns
-MLA_ECUDA).  Usage: ``python -m mla_query_projection_gb300.build``.
+MLA_ECUDA).  ``csrc/torch/tensor_calls.cpp``, the module through which torch
+tensors reach the cache-side operators, is compiled by the host compiler into
+``_tensor_calls.so`` beside it.  Usage: ``python -m mla_query_projection_gb300.build``.
 """
 
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmla_query.so")
 BUILD = os.path.join(HERE, "_build")
+CALLS_SRC = os.path.join(CSRC, "torch", "tensor_calls.cpp")
+CALLS = os.path.join(HERE, "_tensor_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
@@ -51,6 +57,20 @@ def _compile(src: str, build_dir: str = BUILD, extra: tuple = ()) -> tuple[str, 
     return obj, p.stderr
 
 
+def _compile_calls() -> None:
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    include = [os.path.join(torch, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = CALLS + ".tmp"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", *("-I" + i for i in include),
+           CALLS_SRC, "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           "-o", tmp]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"g++ failed for {CALLS_SRC}:\n{p.stdout}\n{p.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(verbose: bool = False, out_dir: str | None = None, extra: tuple = ()) -> str:
     """Compile and link; returns the path of the shared library.  With
     `out_dir` and `extra` nvcc flags, a variant of the same sources goes into
@@ -60,8 +80,11 @@ def build(verbose: bool = False, out_dir: str | None = None, extra: tuple = ()) 
     lib = LIB if out_dir is None else os.path.join(out_dir, "libmla_query.so")
     os.makedirs(build_dir, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        calls = ex.submit(_compile_calls) if out_dir is None else None
         results = list(ex.map(lambda src: _compile(src, build_dir, tuple(extra)), srcs))
+        if calls is not None:
+            calls.result()
     objs = [o for o, _ in results]
     if verbose:
         for _, log in results:

@@ -131,6 +131,14 @@ def test_runner_refuses_tensors_off_the_device():
                  lambda: R.blocks_score(ql, qp, mean, 64, table, lens, scores, stream=0)):
         with pytest.raises(B.MlaError, match="device"):
             call()
+    for bad in (lambda: R.blocks_select(None, lens, 64, 0, 0, sel, lens.clone(), stream=0),
+                lambda: R.blocks_select(scores, [1, 1], 64, 0, 0, sel, lens.clone(), stream=0),
+                lambda: R.blocks_select(scores, lens, "64", 0, 0, sel, lens.clone(), stream=0),
+                lambda: R.blocks_select(scores, lens, 1 << 40, 0, 0, sel, lens.clone(), stream=0),
+                lambda: R.blocks_score(ql[0], qp, mean, 64, table, lens, scores, stream=0),
+                lambda: R.blocks_score(ql, qp.float(), mean, 64, table, lens, scores, stream=0)):
+        with pytest.raises(B.MlaError):
+            bad()
     with pytest.raises(B.MlaError, match="mean"):  # rows of another width
         R.blocks_score(ql, qp, mean.reshape(-1, 64), 64, table, lens, scores, stream=0)
 
