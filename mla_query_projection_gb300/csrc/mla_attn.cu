@@ -65,6 +65,23 @@ __global__ void __launch_bounds__(WIDE ? 256 : 128) mla_attn_join_kernel(const A
   // began with another token
   const int slot0 = 2 * w0 + (n > 0 && attn_worker_start(total, workers, w0) < t0 ? 1 : 0);
   auto slot_of = [&](int i) { return i == 0 ? slot0 : 2 * (w0 + i); };
+  // The first parts are on their way while the factors are worked out: warp w's
+  // parts w, w + 8, .. of one column, or 0 and 1 of four.
+  constexpr int kPre = WIDE ? 4 : 2;
+  const int c0 = WIDE ? 32 * ((int)blockIdx.x & 15) + lane : 128 * warp + lane;
+  float4 pre[WIDE ? kPre : 4 * kPre];
+#pragma unroll
+  for (int u = 0; u < kPre; ++u) {
+    const int i = WIDE ? warp + 8 * u : u;
+    if (i < n) {
+      if constexpr (WIDE) {
+        pre[u] = attn_part(a, slot_of(i), quad, c0);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pre[4 * u + e] = attn_part(a, slot_of(i), quad, c0 + 32 * e);
+      }
+    }
+  }
   if (warp < 4) {  // warp e: the factors of head h0 + e
     const float2* ml = attn_part_ml(a, h0 + warp);
     float M = -INFINITY, l = 0.f;
@@ -103,10 +120,12 @@ __global__ void __launch_bounds__(WIDE ? 256 : 128) mla_attn_join_kernel(const A
       if (h0 + e < a.heads) o[e * a.o_hs] = f2bf_bits(w[e]);
   };
   if constexpr (WIDE) {
-    const int col = 32 * (blockIdx.x & 15) + lane;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < kPre; ++u)
+      if (warp + 8 * u < n) add(acc, weight[warp + 8 * u], pre[u]);
 #pragma unroll 8
-    for (int i = warp; i < n; i += 8) add(acc, weight[i], attn_part(a, slot_of(i), quad, col));
+    for (int i = warp + 8 * kPre; i < n; i += 8) add(acc, weight[i], attn_part(a, slot_of(i), quad, c0));
     sums[warp][lane] = acc;
     __syncthreads();
     if (warp == 0) {
@@ -118,15 +137,20 @@ __global__ void __launch_bounds__(WIDE ? 256 : 128) mla_attn_join_kernel(const A
         acc.z += b.z;
         acc.w += b.w;
       }
-      put(col, acc);
+      put(c0, acc);
     }
   } else {
-    const int c0 = 128 * warp + lane;
     float4 acc[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < kPre; ++u) {
+      if (u >= n) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) add(acc[e], weight[u], pre[4 * u + e]);
+    }
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
+    for (int i = kPre; i < n; ++i) {
       const int slot = slot_of(i);
 #pragma unroll
       for (int e = 0; e < 4; ++e) add(acc[e], weight[i], attn_part(a, slot, quad, c0 + 32 * e));

@@ -376,25 +376,35 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         };
         exponents();
+        // A page's scale relative to the one that values are kept over, base 2:
+        // a weight times it must stay in E4M3's range.  (That scale is the
+        // first tile's largest, and stays.  While it grew with every larger page
+        // scale, O was rescaled as often: 8 tokens, 128 heads, 32 pages of 64
+        // selected, scales within a factor of 8 took 25.6 us, so 21.0.)
+        const bool first_rows = !started || (kPaged && vref[0] == 0.f);
+        // (At least -32: the denominators' terms stay far from FP32's limits.)
+        const float up = kPaged && !first_rows ? fmaxf(__log2f(fabsf(rscale) / vref[0]), -32.0f) : 0.f;
         float over = fmaxf(s[0], s[1]);
 #pragma unroll
         for (int h = 2; h < kHalf; h += 2) over = fmaxf(over, fmaxf(s[h], s[h + 1]));
         // Does the reference have to move?  The warps' answers meet while the
-        // weights are computed as if not.
-        bool move = valid && (!started || over > kPShift + kPRoom);
-        if (kPaged) move |= valid && fabsf(rscale) > vref[0];
-        move = __any_sync(0xFFFFFFFFu, move);
+        // weights are computed as if not (unless there is no reference yet).
+        const bool move = __any_sync(0xFFFFFFFFu, valid && (first_rows || over + up > kPShift + kPRoom));
         if (lane == 0) {
           if (move) *reinterpret_cast<volatile uint32_t*>(&moved[b]) = (uint32_t)i + 1;
           mbar_arrive(voted);
         }
-        weights();
+        if (started) weights();
         tc_wait(voted, (uint32_t)(i & 1), dead, gave_up);
         if (*reinterpret_cast<volatile uint32_t*>(&moved[b]) == (uint32_t)i + 1 &&
             *reinterpret_cast<volatile uint32_t*>(gave_up) == 0u) {
           // the reference moves to the tile's maximum where that passes it by
           // too much (for the first rows that count, everywhere)
-          exponents();
+          if (started) exponents();
+          if (kPaged && !first_rows) {
+#pragma unroll
+            for (int h = 0; h < kHalf; ++h) s[h] += up;
+          }
           const float mx = lanes_reduce<kHalf, OpMax>(s);
           if ((lane * kHalf) % 32 == 0) red[quad * NH + hb + lane * kHalf / 32] = mx;
           if (kPaged) {
@@ -410,14 +420,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             red[tid] = grow ? kPShift - m : 0.f;
             if (grow) ref[tid] += m - kPShift;
           }
-          if (kPaged && tid == NH) {
-            const float old = vref[0];
-            const float v = fmaxf(fmaxf(vref[4], vref[5]), fmaxf(vref[6], vref[7]));
-            vref[1] = v > old ? old / v : 1.0f;
-            if (v > old) vref[0] = v;
-          }
+          if (kPaged && tid == NH && first_rows)  // (O is zero so far)
+            vref[0] = fmaxf(fmaxf(vref[4], vref[5]), fmaxf(vref[6], vref[7]));
           tc_barrier();
-          const float ratio = kPaged ? vref[1] : 1.0f;
 #pragma unroll
           for (int h = 0; h < kHalf; ++h) {
             const float d = red[hb + h];
@@ -425,6 +430,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float& lh = h & 1 ? l[h / 2].y : l[h / 2].x;
             if (started) lh *= ex2(d);
           }
+          if (kPaged && !first_rows) exponents();  // s has `up` in it
           if (started && x > seg0) {
             tc_wait(pv_done, (uint32_t)((i - 1) & 1), dead, gave_up);
             tc_after();
@@ -437,7 +443,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               tc_wait_ld();
               tc_landed(v);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] *= ex2(red[(c + e) % NH]) * ratio;
+              for (int e = 0; e < 32; ++e) v[e] *= ex2(red[(c + e) % NH]);
               tc_st32(at, v);
             }
             tc_wait_st();
@@ -445,6 +451,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           started = true;
           weights();
           tc_barrier();  // red is read
+        } else if (!started) {
+          weights();
         }
         tc_before();
         __syncwarp();

@@ -323,6 +323,42 @@ def test_attention_scales_that_differ(ratio):
     assert (err <= (2.0 ** -7 + 2.0 ** -10 + 2 * slack)[:, None] * mass + 2.0 ** -8 * np.abs(o) + floor).all(), err.max()
 
 
+@pytest.mark.parametrize("order", ["up", "down", "zeros"])
+def test_attention_page_scales_that_differ(order):
+    """Page scales apart by 2^12, the larger ones later or earlier, or zero on most pages, the first ones too.
+
+    (Weights are kept over the largest scale of a worker's first tile, to steps of
+    2^-16 at a largest weight of 2^5 or more: n * 2^-22 of the largest value.)"""
+    rng = np.random.default_rng(48)
+    n, heads, page = 1500, 64, 16
+    pages = -(-n // page) + 2
+    cache, k_scale = C.make_cache(rng, pages, page, 3)
+    table = C.make_table(rng, [n], page, pages)
+    blocks = -(-n // page)
+    sc = 0.03 * np.exp2(12.0 * np.arange(blocks) / blocks - 12.0)
+    if order == "down":
+        sc = sc[::-1]
+    if order == "zeros":
+        sc = np.where((np.arange(blocks) < 40) | (rng.random(blocks) < 0.5), 0.0, 0.03)
+    k_scale[table[0, :blocks]] = sc.astype(np.float32)
+    ql, qp, inv, q64 = queries(rng, 1, heads)
+    where = C.positions(n, page, table.shape[1], pages, table[0])
+    keys = keys64(cache, k_scale, 3, where)
+    attn = R.PagedAttention(1, heads)
+    lse = torch.empty(1, heads, device="cuda")
+    out, _ = attn.decode(ql, qp, dev(cache), 3, dev(table), dev(np.array([n], dtype=np.int32)), SCALE,
+                         k_scale=dev(k_scale), lse=lse)
+    assert attn.error_flags() == 0
+    attn.close()
+    o, want_lse, mass, mag = C.attend64(q64[0], keys, SCALE)
+    slack = 2.0 ** -14.8 * mag + 2.0 ** -17.8 * np.abs(q64[0]).max(1) * np.abs(keys).sum(1).max() * SCALE \
+        + (n / 256 + 16) * 2.0 ** -24
+    assert (np.abs(lse[0].double().cpu().numpy() - want_lse) <= slack + 2.0 ** -23 * np.abs(want_lse)).all()
+    err = np.abs(out[0].double().cpu().numpy() - o)
+    floor = n * 2.0 ** -22 * 448 * float(k_scale.max())
+    assert (err <= (2.0 ** -7 + 2 * slack)[:, None] * mass + 2.0 ** -8 * np.abs(o) + floor).all(), err.max()
+
+
 def test_attention_of_a_nan_row():
     """A NaN in a row that counts reaches the heads' results, in that token only."""
     rng = np.random.default_rng(46)
