@@ -25,7 +25,7 @@ struct mla_attn {
   uint32_t* err;
   float4* part_o;   // partial sums of the workers (mla_attn.cuh, attn_part)
   float2* part_ml;  // their maxima and denominators
-  uint32_t* plan;  // the tiles up to and with each token's [MLA_MAX_BATCH]
+  uint32_t* plan;  // for the join: the axis up to and with each token, its lead [MLA_MAX_BATCH + 1]
 };
 
 namespace mla {
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(WIDE ? 256 : 128) mla_attn_join_kernel(const A
   const int workers = attn_workers(a, total);
   int w0 = 0, n = 0;
   if (t1 > t0) {
-    w0 = attn_worker_of(total, workers, t0);
+    w0 = attn_worker_of(total, workers, t0 + a.plan[kAttnMaxBatch]);  // its first tile
     n = attn_worker_of(total, workers, t1 - 1) - w0 + 1;  // parts, at most kMaxCtas
     if (n == 1) return;
   }
@@ -180,6 +180,18 @@ int launched(cudaError_t e) {
   return MLA_ECUDA;
 }
 
+// What a worker's going on from one token to the next costs, in tiles: 5 where
+// a tile is quick against it (E4M3 rows, 64 heads a CTA), else 3.  Us without a
+// lead and with leads of 2, 3 and 5:
+//   E4M3, 8 tokens of 16,384 rows, 128 heads      54.5  52.1  49.4  47.8
+//   E4M3, 32 tokens of 4,096 rows, 64 heads       41.7  39.3  37.2  35.5
+//   E4M3, 60 tokens of 300 to 2,000, 16 heads     25.1  22.3  22.5  23.5
+//   fp8_ds_mla, 62 tokens of 700 to 4,096, 128    92.7  85.4  81.1  83.6
+//   nvfp4_ds_mla, 32 tokens of 4,096 rows, 64     57.3  54.6  54.3  54.6
+uint32_t attn_lead(int layout, int heads) {
+  return row_scaled(layout) && attn_tc_heads(heads) == 64 ? 5u : 3u;
+}
+
 // Strides of a [batch][heads][width] operand; 0 means contiguous.
 bool fill_strides(int heads, int width, int unit, int64_t* ts, int64_t* hs) {
   if (*hs == 0) *hs = width;
@@ -299,6 +311,7 @@ int mla_attn_decode(mla_attn_t h, int batch, const void* q_latent, int64_t ql_to
   a.groups = (h->heads + gh - 1) / gh;
   a.heads_pad = a.groups * gh;
   a.workers = h->num_sms / a.groups;
+  a.lead = mla::attn_lead(layout, h->heads);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   switch (layout) {

@@ -12,14 +12,21 @@ constexpr uint32_t kAttnTile = 128;  // positions a tile
 
 // Tiles of the batch, spread evenly.  Token t's context is a list of virtual
 // positions 0 .. nv_t - 1 (its first len_t positions, or the positions of its
-// selected blocks, block after block), cut into tiles; end[t] is the number of
-// tiles up to and with its own.  Worker w of a head group takes tiles
-// [w * total / workers, (w + 1) * total / workers), whatever requests they
-// belong to.  A stretch of one token's tiles that is not all of them leaves
-// the worker as a partial: its first stretch in slot 0, any other (then its
-// last) in slot 1.
+// selected blocks, block after block), cut into tiles.  On the axis that is
+// shared out, a token with tiles has `lead` units without work and then a unit
+// a tile; end[t] is the axis up to and with token t.  Worker w of a head group
+// takes what lies in [w * total / workers, (w + 1) * total / workers), whatever
+// requests it belongs to.  A stretch of one token's tiles that is not all of
+// them leaves the worker as a partial: its first stretch in slot 0, any other
+// (then its last) in slot 1.
+//
+// The lead stands for what a worker pays when it goes on from one token to the
+// next: the sums are written, new queries come in and the reference is set
+// anew, 5 to 8 us or a few tiles.  Without it a call waits for the few workers
+// whose share spans two tokens (attn_lead has what it measured).
 struct AttnPlan {
   uint32_t end[kAttnMaxBatch];
+  uint32_t lead, pad;
   __device__ uint32_t start(int t) const { return t > 0 ? end[t - 1] : 0u; }
 };
 // Positions of one token beyond this are left out (and flagged): 256 tokens'
@@ -29,7 +36,7 @@ constexpr int64_t kAttnMaxPositions = (int64_t)1 << 29;
 // What a token looks at.
 struct AttnToken {
   int t, row;
-  uint32_t start, end;  // its tiles
+  uint32_t start, end;  // its tiles on the axis
   uint32_t nv;          // virtual positions
   int32_t len;
 };
@@ -66,7 +73,7 @@ struct AttnSeen {
 };
 
 // Fills the plan; all threads of the block call it (at least 256 of them, a
-// multiple of 32), and may read it after the closing barrier.  red: 8 words.
+// multiple of 32), and may read it after the closing barrier.  red: 16 words.
 __device__ __forceinline__ void attn_make_plan(const AttnArgs& a, AttnPlan* p, uint32_t* red,
                                                bool flag, AttnSeen* seen = nullptr) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -82,27 +89,48 @@ __device__ __forceinline__ void attn_make_plan(const AttnArgs& a, AttnPlan* p, u
       seen->nv[tid] = nv;
     }
   }
+  const uint32_t some = __ballot_sync(0xFFFFFFFFu, n > 0);
   uint32_t inc = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
     if (lane >= o) inc += x;
   }
-  if (lane == 31 && warp < kAttnMaxBatch / 32) red[warp] = inc;
+  constexpr int kWarps = kAttnMaxBatch / 32;
+  if (lane == 31 && warp < kWarps) {
+    red[warp] = inc;
+    red[kWarps + warp] = __popc(some);
+  }
   __syncthreads();
   if (tid < kAttnMaxBatch) {
-    for (int w = 0; w < warp; ++w) inc += red[w];
+    uint32_t count = __popc(some & (0xFFFFFFFFu >> (31 - lane))), tiles = 0, tokens = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) {
+        inc += red[w];
+        count += red[kWarps + w];
+      }
+      tiles += red[w];
+      tokens += red[kWarps + w];
+    }
+    // (A share below a lead and a tile has nothing to even out.)
+    const uint32_t lead = tokens > 1 && tiles >= (a.lead + 1) * a.workers ? a.lead : 0u;
+    inc += lead * count;
     p->end[tid] = inc;
     // one CTA leaves the plan for the kernel that joins the parts
     if (flag) a.plan[tid] = inc;
+    if (tid == 0) {
+      p->lead = lead;
+      if (flag) a.plan[kAttnMaxBatch] = lead;
+    }
   }
   __syncthreads();
 }
 
-// Workers with work: the fewest for which the busiest has no more tiles than
-// it would have if all took part (every part less is one that need not be
-// written and joined); so every one of them has a tile, and every worker
-// between the first and the last of a token leaves a part of it.
+// Workers with work: the fewest for which the busiest has no more than it would
+// have if all took part (every part less is one that need not be written and
+// joined).  Every worker from the one that holds a token's first tile to the one
+// that holds its last has a tile of it, and leaves a part.
 __device__ __forceinline__ int attn_workers(const AttnArgs& a, uint32_t total) {
   if (total == 0) return 0;
   const uint32_t most = (total + a.workers - 1) / a.workers;
@@ -111,12 +139,12 @@ __device__ __forceinline__ int attn_workers(const AttnArgs& a, uint32_t total) {
 __device__ __forceinline__ uint32_t attn_worker_start(uint32_t total, int workers, int w) {
   return (uint32_t)((uint64_t)total * w / workers);
 }
-// The worker whose range holds tile x: the largest w with start(w) <= x.
+// The worker whose range holds the tile at x: the largest w with start(w) <= x.
 __device__ __forceinline__ int attn_worker_of(uint32_t total, int workers, uint32_t x) {
   return (int)((((uint64_t)x + 1) * workers - 1) / total);
 }
 
-// The token of tile x: the first t with end[t] > x.
+// The token at x: the first t with end[t] > x.
 __device__ __forceinline__ int attn_token_of(const AttnPlan* p, int batch, uint32_t x) {
   int lo = 0, hi = batch - 1;
   while (lo < hi) {
@@ -132,7 +160,7 @@ __device__ __forceinline__ AttnToken attn_token(const AttnArgs& a, const AttnPla
                                                 const AttnSeen* seen = nullptr) {
   AttnToken k;
   k.t = attn_token_of(p, a.batch, x);
-  k.start = p->start(k.t);
+  k.start = p->start(k.t) + p->lead;
   k.end = p->end[k.t];
   if (seen != nullptr) {
     k.row = seen->row[k.t];
@@ -144,6 +172,24 @@ __device__ __forceinline__ AttnToken attn_token(const AttnArgs& a, const AttnPla
   k.len = a.lens[k.t];
   k.nv = attn_positions(a, k.t, k.len, k.row, false);
   return k;
+}
+
+// A worker's part of the axis, from a tile to behind a tile (nothing where
+// first >= end).
+__device__ __forceinline__ void attn_range(const AttnArgs& a, const AttnPlan* p, int worker, uint32_t* first,
+                                           uint32_t* end) {
+  const uint32_t total = p->end[a.batch - 1];
+  const int workers = attn_workers(a, total);
+  *first = *end = 0;
+  if (worker >= workers) return;
+  *first = attn_worker_start(total, workers, worker);
+  *end = attn_worker_start(total, workers, worker + 1);
+  if (p->lead == 0) return;
+  *first = max(*first, p->start(attn_token_of(p, a.batch, *first)) + p->lead);
+  if (*end < total) {  // not into the next token's lead
+    const uint32_t s = p->start(attn_token_of(p, a.batch, *end));
+    if (*end <= s + p->lead) *end = s;
+  }
 }
 
 // The cache row (page * page_size + offset) of virtual position v, or -1 where

@@ -138,10 +138,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // S^T accumulators at columns NH * b: rope and plane 3 in 0, planes 0-2 in
   // 1-3; O^T planes from 256
   const uint32_t tmem = uniform(*tslot);
-  const uint32_t total = plan->end[a.batch - 1];
-  const int workers = attn_workers(a, total);
-  const uint32_t first = worker < workers ? attn_worker_start(total, workers, worker) : 0;
-  const uint32_t end = worker < workers ? attn_worker_start(total, workers, worker + 1) : 0;
+  uint32_t first, end;
+  attn_range(a, plan, worker, &first, &end);
   bool dead = false;
 
   if (warp == 8) {
@@ -160,6 +158,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       uint32_t x = first;
       while (x < end && !dead) {
         const AttnToken k = attn_token(a, plan, x, i == 0 ? seen : nullptr);
+        x = max(x, k.start);
         const uint32_t seg_end = min(k.end, end);
         for (; x < seg_end && !dead; ++x, ++i) {
           int32_t y = no_row;
@@ -211,8 +210,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // (A wait that ran out ends no loop here: the loops are then the warp's, and
     // the descriptors stay in uniform registers.  The MMAs go on over whatever
     // the planes hold, and the results do not count.)
-    const int tiles = (int)uniform(end - first);
-    const uint32_t x0 = uniform(first);
+    const uint32_t x1 = uniform(end), lead = uniform(plan->lead);
     // O^T of plane j of tile n, the q-th in order (`add`: to what its stretch has)
     auto pv = [&](int n, int q, int j, uint32_t add) {
       tc_wait_warp(&p_full[q & 1], (uint32_t)(q >> 1), dead);
@@ -246,12 +244,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_mma4x2<2, 2, NH * 8>(tmem + NH * d, da, db, id_s, id_s, 0u);
       tc_commit(&d_full[d]);
     };
-    uint32_t seg_end = x0, add = 0;  // add: whether the tile before added to its O^T
+    uint32_t x = uniform(first), seg_end = x, add = 0;  // add: whether the tile before added to its O^T
     int segs = 0;
-    for (int i = 0; i <= tiles; ++i) {
+    for (int i = 0;; ++i, ++x) {
       // S of tile i around the O of tile i - 1: planes 2 and 3, of which there
       // is one copy, are freed first and asked for last
-      const bool more = i < tiles, fresh = more && x0 + i == seg_end, due = i > 0;
+      const bool more = x < x1, fresh = more && x == seg_end, due = i > 0;
       if (more && !fresh) {
         qk_rope(i);
         qk(i, 0);
@@ -264,7 +262,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         pv(i - 1, 3, 1, add);
       }
       if (fresh) {  // new queries: they come when the stretch before is stored
-        seg_end = uniform(plan->end[attn_token_of(plan, a.batch, x0 + i)]);
+        const int t = attn_token_of(plan, a.batch, x);
+        if (due) x += lead;
+        seg_end = uniform(plan->end[t]);
         tc_wait_warp(q_full, (uint32_t)(segs & 1), dead);
         ++segs;
         qk_rope(i);
@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         qk(i, 2);
         qk(i, 3);
       }
+      if (!more) break;
       add = fresh ? 0u : 1u;
     }
     if (dead) {  // let what was issued finish before TMEM is freed
@@ -300,6 +301,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // the path that only some votes take.)
     while (x < end) {
       const AttnToken k = attn_token(a, plan, x, i == 0 ? seen : nullptr);
+      x = max(x, k.start);
       const uint32_t seg0 = x, seg_end = min(k.end, end);
       tc_queries<NH, FP8Q, true>(a, smem + S::oQ, smem + S::oQr, k.t, h0, warp, lane, logit, xs);
       for (int h = tid; h < NH; h += kTcSoft) ref[h] = 0.f;

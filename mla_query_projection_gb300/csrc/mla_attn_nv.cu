@@ -25,7 +25,7 @@
 // What bounds a tile (64 heads) is that chain: 36 MMAs for S and 32 for O at 48
 // cycles are 3264 cycles, the conversions (8 lanes a cycle) about 1000, the
 // stores of the planes 1150, and they overlap in part.  32 tokens of 4,096 rows,
-// 64 heads: 62 us (the rows' bytes at 6.77 TB/s: 7.5; an mma.sync kernel that
+// 64 heads: 54 us (the rows' bytes at 6.77 TB/s: 7.5; an mma.sync kernel that
 // widened to BF16 in the same way: 149).
 #include "mla_attn_tc.cuh"
 
@@ -245,10 +245,8 @@ __global__ void __launch_bounds__(kNvThreads, 1) mla_attn_nv_kernel(const AttnAr
   tc_after();
   // S^T at column 0, O^T planes (128 columns of the latent each) from 256
   const uint32_t tmem = uniform(*tslot);
-  const uint32_t total = plan->end[a.batch - 1];
-  const int workers = attn_workers(a, total);
-  const uint32_t first = worker < workers ? attn_worker_start(total, workers, worker) : 0;
-  const uint32_t end = worker < workers ? attn_worker_start(total, workers, worker + 1) : 0;
+  uint32_t first, end;
+  attn_range(a, plan, worker, &first, &end);
   bool dead = false;
 
   if (warp == kNvWarpMma) {
@@ -263,15 +261,16 @@ __global__ void __launch_bounds__(kNvThreads, 1) mla_attn_nv_kernel(const AttnAr
     // (A wait that ran out ends no loop here: the loops are then the warp's, and
     // the descriptors stay in uniform registers.  The MMAs go on over whatever
     // the planes hold, and the results do not count.)
-    const int tiles = (int)uniform(end - first);
-    const uint32_t x0 = uniform(first);
-    uint32_t seg_end = x0;
+    const uint32_t x1 = uniform(end), lead = uniform(plan->lead);
+    uint32_t x = uniform(first), seg_end = x;
     int segs = 0;
-    for (int i = 0; i < tiles; ++i) {
+    for (int i = 0; x < x1; ++i, ++x) {
       const uint32_t par = (uint32_t)(i & 1);
-      const bool fresh = x0 + i == seg_end;
+      const bool fresh = x == seg_end;
       if (fresh) {
-        seg_end = uniform(plan->end[attn_token_of(plan, a.batch, x0 + i)]);
+        const int t = attn_token_of(plan, a.batch, x);
+        if (i > 0) x += lead;
+        seg_end = uniform(plan->end[t]);
         tc_wait_warp(q_full, (uint32_t)(segs & 1), dead);
         ++segs;
       }
@@ -315,6 +314,7 @@ __global__ void __launch_bounds__(kNvThreads, 1) mla_attn_nv_kernel(const AttnAr
     // the path that only some votes take.)
     while (x < end) {
       const AttnToken k = attn_token(a, plan, x, i == 0 ? seen : nullptr);
+      x = max(x, k.start);
       const uint32_t seg0 = x, seg_end = min(k.end, end);
       int64_t page;
       NvRow raw;

@@ -135,10 +135,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   attn_make_plan(a, plan, reinterpret_cast<uint32_t*>(smem + S::oScan), blockIdx.x == 0, seen);
   tc_after();
   const uint32_t tmem = uniform(*tslot);  // S^T buffers at columns 0 and 128, O^T planes from 256
-  const uint32_t total = plan->end[a.batch - 1];
-  const int workers = attn_workers(a, total);
-  const uint32_t first = worker < workers ? attn_worker_start(total, workers, worker) : 0;
-  const uint32_t end = worker < workers ? attn_worker_start(total, workers, worker + 1) : 0;
+  uint32_t first, end;
+  attn_range(a, plan, worker, &first, &end);
   bool dead = false;
 
   if (warp == 8) {
@@ -159,6 +157,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // (the first token's weights come after its queries and a tile of its
         // rows: this warp has read `seen` by then)
         const AttnToken k = attn_token(a, plan, x, i == 0 ? seen : nullptr);
+        x = max(x, k.start);
         const uint32_t seg_end = min(k.end, end);
         for (; x < seg_end && !dead; ++x, ++i) {
           int32_t y = no_row;
@@ -228,17 +227,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // A wait that ran out ends no loop here (the loops are then the warp's, and
     // the descriptors stay in uniform registers): the MMAs go on over whatever
     // the planes hold, and the results do not count.
-    const int tiles = (int)uniform(end - first);
-    const uint32_t x0 = uniform(first);
-    uint32_t seg_end = x0;
+    const uint32_t x1 = uniform(end), lead = uniform(plan->lead);
+    uint32_t x = uniform(first), seg_end = x;
     int segs = 0;
     uint32_t add = 0;  // whether the tile before added to its O^T
     bool due = false;  // its PV is still to be issued
-    for (int i = 0; i < tiles; ++i) {
+    int i = 0;
+    for (; x < x1; ++i, ++x) {
       const int b = i & 1;
-      const bool fresh = x0 + i == seg_end;
+      const bool fresh = x == seg_end;
       if (fresh) {
-        seg_end = uniform(plan->end[attn_token_of(plan, a.batch, x0 + i)]);
+        const int t = attn_token_of(plan, a.batch, x);
+        if (i > 0) x += lead;
+        seg_end = uniform(plan->end[t]);
         if (due) pv(i - 1, add);  // its softmax must finish before the queries change
         due = false;
         tc_wait_warp(q_full, (uint32_t)(segs & 1), dead);
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       due = true;
       add = fresh ? 0u : 1u;
     }
-    if (due) pv(tiles - 1, add);
+    if (due) pv(i - 1, add);
     if (dead) {  // let what was issued finish before TMEM is freed
       tc_commit(drain);
       (void)mbar_wait_bounded(drain, 0u, kTcWait);
@@ -295,6 +296,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // the path that only some votes take.)
     while (x < end) {
       const AttnToken k = attn_token(a, plan, x, i == 0 ? seen : nullptr);
+      x = max(x, k.start);
       const uint32_t seg0 = x, seg_end = min(k.end, end);
       tc_queries<NH, FP8Q, false>(a, smem + S::oQ, smem + S::oQr, k.t, h0, warp, lane, logit, xs);
       for (int h = tid; h < NH; h += kTcSoft) ref[h] = 0.f;

@@ -358,6 +358,7 @@ __device__ __forceinline__ void tc_copy_tiles(const AttnArgs& a, const AttnPlan*
   uint32_t x = first;
   while (x < end && !dead) {
     const AttnToken k = attn_token(a, plan, x, i == 0 ? seen : nullptr);
+    x = max(x, k.start);
     const uint32_t seg_end = min(k.end, end);
     for (; x < seg_end && !dead; ++x, ++i) {
       int64_t rows[4], page;

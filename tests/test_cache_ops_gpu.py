@@ -283,6 +283,15 @@ def test_attention_growing_maximum_and_a_sink(layout, page):
 
 
 @pytest.mark.parametrize("layout", [0, 1, 2, 3])
+@pytest.mark.parametrize("page", [16, 100])
+def test_attention_workers_with_several_tokens(layout, page):
+    """Many tiles a worker (ten groups of heads leave each 15 workers), and tokens that end inside their shares."""
+    rng = np.random.default_rng(60 + layout)
+    lens = [1, 0, 900, 128, 129, 2000, 5, 640, 0, 1300, 127, 1025, 3, 3000, 2100]
+    assert run_attention(rng, lens, 640, layout, page) == 0
+
+
+@pytest.mark.parametrize("layout", [0, 1, 2, 3])
 @pytest.mark.parametrize("page", [1, 64])
 def test_attention_full_batch(layout, page):
     """As many tokens as a call takes, most of them short, empty ones among them."""
