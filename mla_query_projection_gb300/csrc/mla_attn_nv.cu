@@ -58,23 +58,6 @@ struct NvSmem {
                 "alignment");
 };
 
-// Eight E2M1 codes times a scale (twice in `sc`), FP16.
-__device__ __forceinline__ uint4 nv_widen(uint32_t w, uint32_t sc) {
-  uint32_t h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .b32 v;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 v, b0;\n\tmul.rn.f16x2 %0, v, %2;\n\t}"
-        : "=r"(h[i])
-        : "r"(w >> (8 * i)), "r"(sc));
-  return make_uint4(h[0], h[1], h[2], h[3]);
-}
-__device__ __forceinline__ uint32_t nv_e4m3x2(uint32_t w) {  // its two low codes, FP16
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
-  return h;
-}
-
 // A thread's share of one cache row on its way from memory to the planes: row
 // 16 warp + lane / 2 of a tile, its half `side` = lane % 2 of each 64 columns
 // (so a warp's 16-byte stores of swizzled rows meet no bank twice, and a pair
@@ -100,12 +83,15 @@ struct NvRow {
   __device__ __forceinline__ void put(uint8_t* row, int r, int side, int j) const {
     // blocks 4 j + 2 side and the next: byte j of the scales' 8-byte words 2 side, 2 side + 1
     const uint32_t s0 = j < 4 ? scale.x : scale.y, s1 = j < 4 ? scale.z : scale.w;
-    const uint32_t f0 = nv_e4m3x2(__byte_perm(s0, 0, 0x11u * (j & 3)));
-    const uint32_t f1 = nv_e4m3x2(__byte_perm(s1, 0, 0x11u * (j & 3)));
+    const uint32_t f0 = e4m3x2_f16(__byte_perm(s0, 0, 0x11u * (j & 3)));
+    const uint32_t f1 = e4m3x2_f16(__byte_perm(s1, 0, 0x11u * (j & 3)));
     const uint32_t w[4] = {code[j].x, code[j].y, code[j].z, code[j].w};
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<uint4*>(row + ((((4 * side + c) ^ r) & 7) << 4)) = nv_widen(w[c], c < 2 ? f0 : f1);
+    for (int c = 0; c < 4; ++c) {
+      uint32_t h[4];
+      e2m1x8_scaled(w[c], c < 2 ? f0 : f1, h);
+      *reinterpret_cast<uint4*>(row + ((((4 * side + c) ^ r) & 7) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
   }
   __device__ __forceinline__ void put_rope(uint8_t* row, int r, int side) const {
     const uint32_t w[8] = {rope[0].x, rope[0].y, rope[0].z, rope[0].w,
@@ -113,8 +99,8 @@ struct NvRow {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       *reinterpret_cast<uint4*>(row + ((((4 * side + c) ^ r) & 7) << 4)) =
-          make_uint4(nv_e4m3x2(w[2 * c]), nv_e4m3x2(w[2 * c] >> 16), nv_e4m3x2(w[2 * c + 1]),
-                     nv_e4m3x2(w[2 * c + 1] >> 16));
+          make_uint4(e4m3x2_f16(w[2 * c]), e4m3x2_f16(w[2 * c] >> 16), e4m3x2_f16(w[2 * c + 1]),
+                     e4m3x2_f16(w[2 * c + 1] >> 16));
   }
 };
 
@@ -151,7 +137,7 @@ __device__ __forceinline__ void nv_queries(const AttnArgs& a, uint8_t* sq, int t
     for (int e = 0; e < 8; ++e) {
       if constexpr (FP8Q) {
         const uint32_t c = e < 4 ? (e < 2 ? w[0].x : w[0].y) : (e < 6 ? w[0].z : w[0].w);
-        h[e] = nv_e4m3x2(e & 1 ? c >> 16 : c);
+        h[e] = e4m3x2_f16(e & 1 ? c >> 16 : c);
       } else {
         const uint4 q = w[e >> 2];
         const uint32_t c = (e & 3) < 2 ? (e & 1 ? q.y : q.x) : (e & 1 ? q.w : q.z);

@@ -18,7 +18,10 @@ namespace {
 // sum in FP32.  It reads each filled row once and writes 1152 bytes a page:
 // bound by HBM.  One CTA a page: chunk c of the row (16 bytes) belongs to one
 // thread of each of kGroups row groups, so a warp reads consecutive bytes of
-// a row, and the groups' sums meet in shared memory in a fixed order.
+// a row, and the groups' sums meet in shared memory in a fixed order.  FP16
+// values (E4M3 codes, E2M1 times its scale) are added to FP32 sums as they are:
+// conversions to FP32 of their own made 17.6 us of the 16.6 that four CTAs an SM
+// take for 8 prompts of 9,001 to 16,384 tokens (15.5 now; their bytes 8.9).
 
 template <int LAYOUT>
 struct MeanShape {
@@ -63,12 +66,7 @@ __global__ void __launch_bounds__(MeanShape<LAYOUT>::kThreads)
 #pragma unroll
       for (int d = 0; d < M::kDeep; ++d) {
         const int t = t0 + d * M::kGroups;
-        if (t < filled) {
-          float v[R::kMax];
-          R::decode(base + (int64_t)t * R::kBytes, chunk, w[d], v);
-#pragma unroll
-          for (int i = 0; i < R::kMax; ++i) acc[i] += v[i];
-        }
+        if (t < filled) R::add(base + (int64_t)t * R::kBytes, chunk, w[d], acc);
       }
     }
     const int col = R::col(chunk), width = R::width(chunk);
@@ -140,24 +138,36 @@ __global__ void __launch_bounds__(256) mla_blocks_score_kernel(const ScoreArgs s
     pages[tid] = page;
   }
   __syncthreads();
-  // the means by 16-byte asynchronous copies, all in flight at once
-  for (int c = tid; c < kTile * (kRowElems / 8); c += 256) {
-    const int b = c / (kRowElems / 8), k = c % (kRowElems / 8);
-    uint8_t* d = keys + b * kScorePitch + 16 * k;
-    if (pages[b] >= 0)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(d)),
-                   "l"(s.mean + pages[b] * kRowElems + 8 * k)
-                   : "memory");
-    else
-      *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
+  // the means by 16-byte asynchronous copies, all in flight at once; with 16
+  // blocks a CTA, where the call is a chain of latencies, the first third of
+  // their columns is used while the others come (1,024 blocks, 64 heads: 5.6 us,
+  // so 4.9; with 64 blocks a CTA 13.4 became 14.4)
+  constexpr int kParts = NT == 2 ? 3 : 1;
+  constexpr int kPart = kRowElems / 8 / kParts, kSteps = kRowElems / 32 / kParts;
+#pragma unroll 1
+  for (int part = 0; part < kParts; ++part) {
+    for (int c = tid; c < kTile * kPart; c += 256) {
+      const int b = c / kPart, k = part * kPart + c % kPart;
+      uint8_t* d = keys + b * kScorePitch + 16 * k;
+      if (pages[b] >= 0)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(d)),
+                     "l"(s.mean + pages[b] * kRowElems + 8 * k)
+                     : "memory");
+      else
+        *reinterpret_cast<uint4*>(d) = make_uint4(0, 0, 0, 0);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-  __syncthreads();
   float mx[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY;
   constexpr int kB = FP8Q ? 1 : 2;  // bytes per query element
-  for (int h0 = 16 * warp; h0 < s.heads; h0 += 128) {
+  if constexpr (kParts == 1) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+  }
+  // (with parts, every warp passes the barriers of the first 16 heads, whether it has them or not)
+  for (int h0 = 16 * warp; h0 < s.heads || (kParts > 1 && h0 < 128); h0 += 128) {
     // rows h0 + g and h0 + g + 8; heads past the last repeat the last
     const int ha = min(h0 + g, s.heads - 1), hb = min(h0 + g + 8, s.heads - 1);
     const uint8_t* la = s.q_latent + ((int64_t)t * s.ql_ts + (int64_t)ha * s.ql_hs) * kB;
@@ -169,6 +179,15 @@ __global__ void __launch_bounds__(256) mla_blocks_score_kernel(const ScoreArgs s
     for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 #pragma unroll 6
     for (int k = 0; k < kRowElems / 32; ++k) {
+      if (kParts > 1 && h0 < 128 && k % kSteps == 0) {
+        if (k == 0)
+          asm volatile("cp.async.wait_group 2;" ::: "memory");
+        else if (k == kSteps)
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+      }
       const uint8_t* a = k < 16 ? la + 32 * k * kB : pa + 32 * (k - 16) * kB;
       const uint8_t* b = k < 16 ? lb + 32 * k * kB : pb + 32 * (k - 16) * kB;
       uint4 va, vb;
@@ -406,8 +425,12 @@ __global__ void __launch_bounds__(kSelThreads, 2) mla_blocks_select_kernel(const
 }  // namespace
 
 cudaError_t launch_blocks_mean(const MeanArgs& m, int num_sms, cudaStream_t stream) {
-  // four CTAs an SM in all, but no more a row than it can have blocks
-  int64_t gx = (4 * (int64_t)num_sms + m.rows - 1) / m.rows;
+  // Four CTAs an SM in all, but no more a row than it can have blocks; six for
+  // few rows, which then have many blocks each, in unequal numbers (8 prompts of
+  // 9,001 to 16,384 tokens: 16.6 us with four, 15.5 with six or eight; 64 rows
+  // of one new token: 4.0 and 4.2).
+  const int64_t per_sm = m.rows <= 16 ? 6 : 4;
+  int64_t gx = (per_sm * num_sms + m.rows - 1) / m.rows;
   if (gx > m.bt_stride) gx = m.bt_stride;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)gx, (unsigned)m.rows, 1);

@@ -27,26 +27,39 @@ __device__ __forceinline__ void e4m3x4_values(uint32_t w, float* v) {
   v[3] = b.y;
 }
 
-// Eight E2M1 codes, value 2k in the low half of byte k.
-__device__ __forceinline__ void e2m1x8_values(uint32_t w, float* v) {
+// Eight E2M1 codes times a scale (twice in `sc`) as four FP16 pairs: exact, at
+// most 2 + 4 significant bits.
+__device__ __forceinline__ void e2m1x8_scaled(uint32_t w, uint32_t sc, uint32_t (&h)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t h;
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
-        : "=r"(h)
-        : "r"(w >> (8 * i)));
-    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
-        : "=f"(v[2 * i]), "=f"(v[2 * i + 1])
-        : "r"(h));
-  }
+  for (int i = 0; i < 4; ++i)
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .b32 v;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 v, b0;\n\tmul.rn.f16x2 %0, v, %2;\n\t}"
+        : "=r"(h[i])
+        : "r"(w >> (8 * i)), "r"(sc));
+}
+// Two E4M3 codes (the low ones of w) as an FP16 pair.
+__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t w) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
+  return h;
 }
 
-// A row as 16-byte chunks (chunk c at byte kFirst(c)), each with its columns
-// [col(c), col(c) + width(c)).  decode() gives their values: the codes
+// acc[0..1] += an FP16 pair, in FP32 (one instruction each: no conversion).
+__device__ __forceinline__ void add_f16x2(uint32_t h, float* acc) {
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tadd.f32.f16 %0, l, %0;\n\t"
+      "add.f32.f16 %1, u, %1;\n\t}"
+      : "+f"(acc[0]), "+f"(acc[1])
+      : "r"(h));
+}
+__device__ __forceinline__ void add_e4m3x4(uint32_t w, float* acc) {
+  add_f16x2(e4m3x2_f16(w), acc);
+  add_f16x2(e4m3x2_f16(w >> 16), acc + 2);
+}
+
+// A row as 16-byte chunks (chunk c at byte offset(c)), each with its columns
+// [col(c), col(c) + width(c)).  add() adds their values to FP32 sums: the codes
 // themselves for the layouts whose scale is one FP32 for the row (the caller
-// applies it), the exact products of code and scale for the two ds layouts
-// (at most 4 + 4 significant bits: exact in BF16 too).
+// applies it), code times scale for the two ds layouts.
 template <int LAYOUT>
 struct RowChunks;
 
@@ -56,11 +69,11 @@ struct RowChunks<MLA_KV_FP8_E4M3> {
   __device__ static int offset(int c) { return 16 * c; }
   __device__ static int col(int c) { return 16 * c; }
   __device__ static int width(int) { return 16; }
-  __device__ static void decode(const uint8_t*, int, uint4 w, float (&v)[kMax]) {
-    e4m3x4_values(w.x, v);
-    e4m3x4_values(w.y, v + 4);
-    e4m3x4_values(w.z, v + 8);
-    e4m3x4_values(w.w, v + 12);
+  __device__ static void add(const uint8_t*, int, uint4 w, float (&acc)[kMax]) {
+    add_e4m3x4(w.x, acc);
+    add_e4m3x4(w.y, acc + 4);
+    add_e4m3x4(w.z, acc + 8);
+    add_e4m3x4(w.w, acc + 12);
   }
 };
 
@@ -70,20 +83,22 @@ struct RowChunks<MLA_KV_FP8_DS_MLA> {
   __device__ static int offset(int c) { return c < 32 ? 16 * c : kDsRope + 16 * (c - 32); }
   __device__ static int col(int c) { return c < 32 ? 16 * c : kKvLora + 8 * (c - 32); }
   __device__ static int width(int c) { return c < 32 ? 16 : 8; }
-  __device__ static void decode(const uint8_t* row, int c, uint4 w, float (&v)[kMax]) {
+  __device__ static void add(const uint8_t* row, int c, uint4 w, float (&acc)[kMax]) {
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
     if (c < 32) {
-      RowChunks<MLA_KV_FP8_E4M3>::decode(row, c, w, v);
       const float s = *reinterpret_cast<const float*>(row + kDsScales + 4 * (c >> 3));
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] *= s;
+      for (int i = 0; i < 4; ++i) {
+        float v[4];
+        e4m3x4_values(ww[i], v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[4 * i + e] = fmaf(v[e], s, acc[4 * i + e]);
+      }
     } else {
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16lo(ww[i]);
-        v[2 * i + 1] = bf16hi(ww[i]);
-        v[8 + 2 * i] = 0.f;
-        v[9 + 2 * i] = 0.f;
+        acc[2 * i] += bf16lo(ww[i]);
+        acc[2 * i + 1] += bf16hi(ww[i]);
       }
     }
   }
@@ -95,24 +110,20 @@ struct RowChunks<MLA_KV_NVFP4_DS_MLA> {
   __device__ static int offset(int c) { return c < 16 ? 16 * c : kNvRope + 16 * (c - 16); }
   __device__ static int col(int c) { return c < 16 ? 32 * c : kKvLora + 16 * (c - 16); }
   __device__ static int width(int c) { return c < 16 ? 32 : 16; }
-  __device__ static void decode(const uint8_t* row, int c, uint4 w, float (&v)[kMax]) {
+  __device__ static void add(const uint8_t* row, int c, uint4 w, float (&acc)[kMax]) {
     const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
     if (c < 16) {
-      // blocks 2c and 2c + 1 of 16 values
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int s = 2 * c + b;
-        const float sc = e4m3x2_value(row[kNvScales + 8 * (s & 3) + (s >> 2)]).x;
-        e2m1x8_values(ww[2 * b], v + 16 * b);
-        e2m1x8_values(ww[2 * b + 1], v + 16 * b + 8);
+      for (int i = 0; i < 4; ++i) {  // words 0, 1 are block 2c, words 2, 3 block 2c + 1
+        const int s = 2 * c + (i >> 1);
+        uint32_t h[4];
+        e2m1x8_scaled(ww[i], e4m3x2_f16(0x0101u * row[kNvScales + 8 * (s & 3) + (s >> 2)]), h);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[16 * b + i] *= sc;
+        for (int e = 0; e < 4; ++e) add_f16x2(h[e], acc + 8 * i + 2 * e);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) e4m3x4_values(ww[i], v + 4 * i);
-#pragma unroll
-      for (int i = 16; i < 32; ++i) v[i] = 0.f;
+      for (int i = 0; i < 4; ++i) add_e4m3x4(ww[i], acc + 4 * i);
     }
   }
 };
