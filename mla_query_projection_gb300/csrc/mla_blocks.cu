@@ -19,9 +19,9 @@ namespace {
 // bound by HBM.  One CTA a page: chunk c of the row (16 bytes) belongs to one
 // thread of each of kGroups row groups, so a warp reads consecutive bytes of
 // a row, and the groups' sums meet in shared memory in a fixed order.  FP16
-// values (E4M3 codes, E2M1 times its scale) are added to FP32 sums as they are:
-// conversions to FP32 of their own made 17.6 us of the 16.6 that four CTAs an SM
-// take for 8 prompts of 9,001 to 16,384 tokens (15.5 now; their bytes 8.9).
+// values (E4M3 codes, E2M1 times its scale) are added to the FP32 sums as they
+// are (converted first, 8 prompts of 9,001 to 16,384 tokens took 17.6 us, not
+// 16.6; with the present grid 15.5, where the rows' bytes are 8.9).
 
 template <int LAYOUT>
 struct MeanShape {
