@@ -508,7 +508,8 @@ def state(rng, lens, page, pages, width):
 @pytest.mark.parametrize("alias", [False, True])
 @pytest.mark.parametrize("rows,page,width,longest,tokens", [
     (1, 64, 4, 1, 1), (5, 1, 9, 3, 64), (64, 64, 12, 1, 64), (64, 16, 40, 200, 4000), (300, 7, 30, 20, 9000),
-    (513, 64, 8, 60, 2048), (1000, 64, 5, 1, 1000), (4096, 16, 6, 9, 4096 * 9),
+    (513, 64, 8, 60, 2048), (1000, 64, 5, 1, 1000), (4096, 16, 6, 9, 4096 * 9), (40, 16, 40, 200, 3003),
+    (7, 48, 30, 300, 257),
 ])
 def test_tables_step(rows, page, width, longest, tokens, alias):
     rng = np.random.default_rng(rows + page)
@@ -519,6 +520,36 @@ def test_tables_step(rows, page, width, longest, tokens, alias):
     table, stack, count = state(rng, lens, page, pages, width)
     d = step(new, lens, table, stack, count, page, tokens, alias)
     check_step(d, C.tables_ref(new, lens, table, stack, count, page, tokens))
+
+
+@pytest.mark.parametrize("tokens", [63, 3001])
+def test_tables_step_into_unaligned_arrays(tokens):
+    """Token arrays that begin one entry into their allocation; what lies around them stays."""
+    rng = np.random.default_rng(70)
+    rows, page, width = 20, 16, 30
+    lens = rng.integers(0, 100, rows).astype(np.int32)
+    new = rng.integers(0, 4 if tokens < 100 else 140, rows).astype(np.int32)
+    pages = 600
+    table = C.make_table(rng, [int(n) for n in lens], page, pages, width)
+    held = set(table[r, j] for r in range(rows) for j in range(-(-int(lens[r]) // page)))
+    stack = np.full(pages, -7, dtype=np.int32)
+    free = [p for p in range(pages) if p not in held]
+    stack[:len(free)] = free
+    want = C.tables_ref(new, lens, table, stack, len(free), page, tokens)
+    d = step(new, lens, table, stack, len(free), page, tokens)
+    check_step(d, want)
+    wide = dict(slots=torch.full((tokens + 9,), 55, dtype=torch.int64, device="cuda"),
+                row=torch.full((tokens + 9,), 55, dtype=torch.int32, device="cuda"),
+                ln=torch.full((tokens + 9,), 55, dtype=torch.int32, device="cuda"))
+    cut = {k: v[1:1 + tokens] for k, v in wide.items()}
+    again = torch.zeros_like(d["lens_out"]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    R.tables_step(dev(new), dev(lens), dev(table), dev(stack), dev(np.array([len(free)], dtype=np.int32)), page,
+                  again[0], again[1], cut["slots"], cut["row"], cut["ln"],
+                  torch.zeros(rows + 1, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    for k, v in cut.items():
+        assert torch.equal(v, d[k]), k
+        assert (wide[k][:1] == 55).all() and (wide[k][1 + tokens:] == 55).all(), k
 
 
 @pytest.mark.parametrize("what", ["pages", "tokens", "row", "length"])
