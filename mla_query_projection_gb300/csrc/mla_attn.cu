@@ -25,7 +25,6 @@ struct mla_attn {
   uint32_t* err;
   float4* part_o;   // partial sums of the workers (mla_attn.cuh, attn_part)
   float2* part_ml;  // their maxima and denominators
-  uint32_t* plan;  // for the join: the axis up to and with each token, its lead [MLA_MAX_BATCH + 1]
 };
 
 namespace mla {
@@ -37,126 +36,174 @@ namespace {
 // o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  Tokens whose context one
 // worker read whole are done already; those that look at nothing get zeros
 // and an lse of -infinity.  Bound by the parts' bytes (L2), and by latency
-// where there are few.  A CTA takes four heads, which lie side by side in the
-// parts (attn_part), in one of two shapes by the parts a token has on average:
-//  * many (one or a few long contexts): 32 columns a CTA, its eight warps every
-//    eighth part each, their shares summed in order;
-//  * few: all columns, 128 a warp.
-// (One CTA a head in both cases spent its time on CTAs with two or three
-// parts: 7,936 of them for 62 tokens of 128 heads.)
+// where there are few.  Before it waits for the parts a CTA works out the plan
+// for itself (the kernel before has waited for what wrote the lengths by the
+// time this one may start), so that the first trip to memory is for the parts.
+// It then takes four heads of a token at a time, which lie side by side in the
+// parts (attn_part), in one of three shapes by the parts a token has on average
+// (attn_join_cols), COLS columns a lane:
+//  1: 32 columns a CTA, the eight warps every eighth part each, their shares
+//     summed in order;
+//  2: all columns, 64 a warp, the parts in order;
+//  4: the same, 128 a warp, so that more CTAs fit.
 
-template <bool WIDE>
-__global__ void __launch_bounds__(WIDE ? 256 : 128) mla_attn_join_kernel(const AttnArgs a) {
+template <int COLS>
+__global__ void __launch_bounds__(COLS == 4 ? 128 : 256) mla_attn_join_kernel(const AttnArgs a) {
+  __shared__ AttnPlan plan;
+  __shared__ uint32_t red[16];
   __shared__ float4 weight[kMaxCtas];  // a part's factors for the four heads
+  constexpr bool WIDE = COLS == 1;
   __shared__ float4 scale4, sums[WIDE ? 8 : 1][32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = blockIdx.y;
-  const int quad = WIDE ? (int)blockIdx.x >> 4 : (int)blockIdx.x, h0 = 4 * quad;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_launch_dependents();
-  pdl_wait();
-  const uint32_t t0 = t > 0 ? a.plan[t - 1] : 0u, t1 = a.plan[t], total = a.plan[a.batch - 1];
+  attn_make_plan<COLS == 4 ? 2 : 1>(a, &plan, red, false);
+  const uint32_t total = plan.end[a.batch - 1];
   const int workers = attn_workers(a, total);
-  int w0 = 0, n = 0;
-  if (t1 > t0) {
-    w0 = attn_worker_of(total, workers, t0 + a.plan[kAttnMaxBatch]);  // its first tile
-    n = attn_worker_of(total, workers, t1 - 1) - w0 + 1;  // parts, at most kMaxCtas
-    if (n == 1) return;
-  }
-  // part i is worker w0 + i's; the first lies in slot 1 where that worker
-  // began with another token
-  const int slot0 = 2 * w0 + (n > 0 && attn_worker_start(total, workers, w0) < t0 ? 1 : 0);
-  auto slot_of = [&](int i) { return i == 0 ? slot0 : 2 * (w0 + i); };
-  // The first parts are on their way while the factors are worked out: warp w's
-  // parts w, w + 8, .. of one column, or 0 and 1 of four.
-  constexpr int kPre = WIDE ? 4 : 2;
-  const int c0 = WIDE ? 32 * ((int)blockIdx.x & 15) + lane : 128 * warp + lane;
-  float4 pre[WIDE ? kPre : 4 * kPre];
-#pragma unroll
-  for (int u = 0; u < kPre; ++u) {
-    const int i = WIDE ? warp + 8 * u : u;
-    if (i < n) {
-      if constexpr (WIDE) {
-        pre[u] = attn_part(a, slot_of(i), quad, c0);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) pre[4 * u + e] = attn_part(a, slot_of(i), quad, c0 + 32 * e);
-      }
+  const int quads = (a.heads + 3) / 4;
+  pdl_wait();
+  for (int item = blockIdx.x; item < a.batch * quads * (WIDE ? 16 : 1); item += gridDim.x) {
+    const int tq = WIDE ? item >> 4 : item, t = tq / quads, quad = tq - t * quads, h0 = 4 * quad;
+    const uint32_t t0 = plan.start(t), t1 = plan.end[t];
+    int w0 = 0, n = 0;
+    if (t1 > t0) {
+      w0 = attn_worker_of(total, workers, t0 + plan.lead);  // its first tile
+      n = attn_worker_of(total, workers, t1 - 1) - w0 + 1;  // parts, at most kMaxCtas
+      if (n == 1) continue;
     }
-  }
-  if (warp < 4) {  // warp e: the factors of head h0 + e
-    const float2* ml = attn_part_ml(a, h0 + warp);
-    float M = -INFINITY, l = 0.f;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, ml[slot_of(i)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-    const float m_use = M == -INFINITY ? 0.f : M;
-    for (int i = lane; i < n; i += 32) {
-      const float2 v = ml[slot_of(i)];
-      const float f = v.x == -INFINITY ? 0.f : exp2f(v.x - m_use);
-      l += f * v.y;
-      reinterpret_cast<float*>(&weight[i])[warp] = f;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-    if (lane == 0) {
-      reinterpret_cast<float*>(&scale4)[warp] = l == 0.f ? 0.f : 1.0f / l;
-      if (a.lse != nullptr && h0 + warp < a.heads && (!WIDE || (blockIdx.x & 15) == 0))
-        a.lse[(int64_t)t * a.heads + h0 + warp] = attn_lse(M, l);
-    }
-  }
-  __syncthreads();
-  const float4 r = scale4;
-  auto add = [](float4& acc, float4 f, float4 v) {
-    // (a part that saw nothing holds zeros, so its factor of zero needs no test)
-    acc.x = fmaf(f.x, v.x, acc.x);
-    acc.y = fmaf(f.y, v.y, acc.y);
-    acc.z = fmaf(f.z, v.z, acc.z);
-    acc.w = fmaf(f.w, v.w, acc.w);
-  };
-  auto put = [&](int col, float4 v) {
-    uint16_t* o = a.out + (int64_t)t * a.o_ts + (int64_t)h0 * a.o_hs + col;
-    const float w[4] = {v.x * r.x, v.y * r.y, v.z * r.z, v.w * r.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (h0 + e < a.heads) o[e * a.o_hs] = f2bf_bits(w[e]);
-  };
-  if constexpr (WIDE) {
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int u = 0; u < kPre; ++u)
-      if (warp + 8 * u < n) add(acc, weight[warp + 8 * u], pre[u]);
-#pragma unroll 8
-    for (int i = warp + 8 * kPre; i < n; i += 8) add(acc, weight[i], attn_part(a, slot_of(i), quad, c0));
-    sums[warp][lane] = acc;
-    __syncthreads();
-    if (warp == 0) {
-#pragma unroll
-      for (int g = 1; g < 8; ++g) {
-        const float4 b = sums[g][lane];
-        acc.x += b.x;
-        acc.y += b.y;
-        acc.z += b.z;
-        acc.w += b.w;
-      }
-      put(c0, acc);
-    }
-  } else {
-    float4 acc[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    // part i is worker w0 + i's; the first lies in slot 1 where that worker
+    // began with another token
+    const int slot0 = 2 * w0 + (n > 0 && attn_worker_start(total, workers, w0) < t0 ? 1 : 0);
+    auto slot_of = [&](int i) { return i == 0 ? slot0 : 2 * (w0 + i); };
+    // The first parts are on their way while the factors are worked out: warp w's
+    // parts w, w + 8, .. of one column, or the first parts of two or four.
+    constexpr int kPre = COLS == 4 ? 2 : 4;
+    const int c0 = WIDE ? 32 * (item & 15) + lane : 32 * COLS * warp + lane;
+    float4 pre[COLS * kPre];
 #pragma unroll
     for (int u = 0; u < kPre; ++u) {
-      if (u >= n) continue;
+      const int i = WIDE ? warp + 8 * u : u;
+      if (i < n) {
+        if constexpr (WIDE) {
+          pre[u] = attn_part(a, slot_of(i), quad, c0);
+        } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) add(acc[e], weight[u], pre[4 * u + e]);
+          for (int e = 0; e < COLS; ++e) pre[COLS * u + e] = attn_part(a, slot_of(i), quad, c0 + 32 * e);
+        }
+      }
     }
-#pragma unroll 4
-    for (int i = kPre; i < n; ++i) {
-      const int slot = slot_of(i);
+    if (warp < 4) {  // warp e: the factors of head h0 + e
+      const float2* ml = attn_part_ml(a, h0 + warp);
+      float M = -INFINITY, l = 0.f;
+      for (int i = lane; i < n; i += 32) M = fmaxf(M, ml[slot_of(i)].x);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) add(acc[e], weight[i], attn_part(a, slot, quad, c0 + 32 * e));
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+      const float m_use = M == -INFINITY ? 0.f : M;
+      for (int i = lane; i < n; i += 32) {
+        const float2 v = ml[slot_of(i)];
+        const float f = v.x == -INFINITY ? 0.f : exp2f(v.x - m_use);
+        l += f * v.y;
+        reinterpret_cast<float*>(&weight[i])[warp] = f;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+      if (lane == 0) {
+        reinterpret_cast<float*>(&scale4)[warp] = l == 0.f ? 0.f : 1.0f / l;
+        if (a.lse != nullptr && h0 + warp < a.heads && (!WIDE || (item & 15) == 0))
+          a.lse[(int64_t)t * a.heads + h0 + warp] = attn_lse(M, l);
+      }
     }
+    __syncthreads();
+    const float4 r = scale4;
+    auto add = [](float4& acc, float4 f, float4 v) {
+      // (a part that saw nothing holds zeros, so its factor of zero needs no test)
+      acc.x = fmaf(f.x, v.x, acc.x);
+      acc.y = fmaf(f.y, v.y, acc.y);
+      acc.z = fmaf(f.z, v.z, acc.z);
+      acc.w = fmaf(f.w, v.w, acc.w);
+    };
+    auto put = [&](int col, float4 v) {
+      uint16_t* o = a.out + (int64_t)t * a.o_ts + (int64_t)h0 * a.o_hs + col;
+      const float w[4] = {v.x * r.x, v.y * r.y, v.z * r.z, v.w * r.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) put(c0 + 32 * e, acc[e]);
+      for (int e = 0; e < 4; ++e)
+        if (h0 + e < a.heads) o[e * a.o_hs] = f2bf_bits(w[e]);
+    };
+    if constexpr (WIDE) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < kPre; ++u)
+        if (warp + 8 * u < n) add(acc, weight[warp + 8 * u], pre[u]);
+#pragma unroll 8
+      for (int i = warp + 8 * kPre; i < n; i += 8) add(acc, weight[i], attn_part(a, slot_of(i), quad, c0));
+      sums[warp][lane] = acc;
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int g = 1; g < 8; ++g) {
+          const float4 b = sums[g][lane];
+          acc.x += b.x;
+          acc.y += b.y;
+          acc.z += b.z;
+          acc.w += b.w;
+        }
+        put(c0, acc);
+      }
+    } else {
+      float4 acc[COLS];
+#pragma unroll
+      for (int e = 0; e < COLS; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < kPre; ++u) {
+        if (u >= n) continue;
+#pragma unroll
+        for (int e = 0; e < COLS; ++e) add(acc[e], weight[u], pre[COLS * u + e]);
+      }
+#pragma unroll COLS == 4 ? 2 : 4
+      for (int i = kPre; i < n; ++i) {
+        const int slot = slot_of(i);
+#pragma unroll
+        for (int e = 0; e < COLS; ++e) add(acc[e], weight[i], attn_part(a, slot, quad, c0 + 32 * e));
+      }
+#pragma unroll
+      for (int e = 0; e < COLS; ++e) put(c0 + 32 * e, acc[e]);
+    }
+    __syncthreads();  // weight, scale4 and sums are read
+  }
+}
+
+// The shape by the parts a token has on average, workers / batch; with few parts
+// and many fours of heads the smallest CTAs.  Us a call with 1, 2 and 4 columns:
+//   1 token of 65,536 E4M3 rows, 64 heads         25.3   51.6  77.4
+//   8 tokens of 16,384 rows, 128 heads            59.4   43.4  45.6
+//   60 tokens of 300 to 2,000 rows, 16 heads      37.9   21.0  22.0
+//   32 tokens of 4,096 rows, 64 heads             69.8   35.9  34.0
+//   62 tokens, 128 heads, fp8_ds_mla             210     84.7  83.1
+int attn_join_cols(const AttnArgs& a, int num_sms) {
+  if (a.workers >= 16 * a.batch) return 1;
+  return a.workers >= 6 * a.batch || (a.heads + 3) / 4 * a.batch <= 3 * num_sms ? 2 : 4;
+}
+
+template <int COLS>
+cudaError_t launch_join_cols(const AttnArgs& a, int num_sms, cudaStream_t stream) {
+  const int64_t items = (int64_t)a.batch * ((a.heads + 3) / 4) * (COLS == 1 ? 16 : 1);
+  const int64_t most = (COLS == 4 ? 6 : 3) * (int64_t)num_sms;  // about what fits at once
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items < most ? items : most));
+  cfg.blockDim = dim3(COLS == 4 ? 128 : 256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, mla_attn_join_kernel<COLS>, a);
+}
+
+cudaError_t launch_join(const AttnArgs& a, int num_sms, cudaStream_t stream) {
+  switch (attn_join_cols(a, num_sms)) {
+    case 1: return launch_join_cols<1>(a, num_sms, stream);
+    case 2: return launch_join_cols<2>(a, num_sms, stream);
+    default: return launch_join_cols<4>(a, num_sms, stream);
   }
 }
 
@@ -229,13 +276,12 @@ int mla_attn_create(mla_attn_t* out, int max_batch, int heads) {
     goto fail;
   slots = (size_t)(h->num_sms / groups) * 2 * groups * gh;
   rc = MLA_ENOMEM;
-  if (cudaMalloc(&h->err, 2048) != cudaSuccess ||
+  if (cudaMalloc(&h->err, 256) != cudaSuccess ||
       cudaMalloc(&h->part_o, slots * mla::kKvLora * sizeof(float)) != cudaSuccess ||
       cudaMalloc(&h->part_ml, slots * sizeof(float2)) != cudaSuccess)
     goto fail;
   rc = MLA_ECUDA;
-  h->plan = h->err + 64;
-  if (cudaMemset(h->err, 0, 2048) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess) goto fail;
+  if (cudaMemset(h->err, 0, 256) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess) goto fail;
   *out = h;
   return MLA_OK;
 fail:
@@ -305,7 +351,6 @@ int mla_attn_decode(mla_attn_t h, int batch, const void* q_latent, int64_t ql_to
   a.part_o = h->part_o;
   a.part_ml = h->part_ml;
   a.err = h->err;
-  a.plan = h->plan;
   a.heads = h->heads;
   a.batch = batch;
   a.groups = (h->heads + gh - 1) / gh;
@@ -321,19 +366,7 @@ int mla_attn_decode(mla_attn_t h, int batch, const void* q_latent, int64_t ql_to
   }
   int rc = mla::launched(e);
   if (rc != MLA_OK) return rc;
-  // parts a token has on average: workers / batch
-  const bool wide = a.workers >= 16 * batch;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((h->heads + 3) / 4 * (wide ? 16 : 1)), (unsigned)batch);
-  cfg.blockDim = dim3(wide ? 256 : 128);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return mla::launched(wide ? cudaLaunchKernelEx(&cfg, mla::mla_attn_join_kernel<true>, a)
-                            : cudaLaunchKernelEx(&cfg, mla::mla_attn_join_kernel<false>, a));
+  return mla::launched(mla::launch_join(a, h->num_sms, st));
 }
 
 int mla_attn_get_error(mla_attn_t h, unsigned* device_flags, void* stream) {

@@ -72,42 +72,52 @@ struct AttnSeen {
   uint32_t nv[kAttnMaxBatch];
 };
 
-// Fills the plan; all threads of the block call it (at least 256 of them, a
-// multiple of 32), and may read it after the closing barrier.  red: 16 words.
+// Fills the plan; all threads of the block call it (at least 256 / TPT of them, a
+// multiple of 32; TPT tokens a thread), and may read it after the closing
+// barrier.  red: 16 words.
+template <int TPT = 1>
 __device__ __forceinline__ void attn_make_plan(const AttnArgs& a, AttnPlan* p, uint32_t* red,
                                                bool flag, AttnSeen* seen = nullptr) {
+  constexpr int kWarps = kAttnMaxBatch / (32 * TPT);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t n = 0;
-  if (tid < a.batch) {
-    const int32_t len = a.lens[tid];
-    const int row = a.token_row != nullptr ? a.token_row[tid] : tid;
-    const uint32_t nv = attn_positions(a, tid, len, row, flag);
-    n = (nv + kAttnTile - 1) / kAttnTile;
-    if (seen != nullptr) {
-      seen->len[tid] = len;
-      seen->row[tid] = row;
-      seen->nv[tid] = nv;
+  uint32_t n[TPT], sum = 0, below = 0, some = 0;  // tiles; tokens with tiles, in lower lanes and in the warp
+#pragma unroll
+  for (int i = 0; i < TPT; ++i) {
+    const int t = TPT * tid + i;
+    n[i] = 0;
+    if (t < a.batch) {
+      const int32_t len = a.lens[t];
+      const int row = a.token_row != nullptr ? a.token_row[t] : t;
+      const uint32_t nv = attn_positions(a, t, len, row, flag);
+      n[i] = (nv + kAttnTile - 1) / kAttnTile;
+      if (seen != nullptr) {
+        seen->len[t] = len;
+        seen->row[t] = row;
+        seen->nv[t] = nv;
+      }
     }
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, n[i] > 0);
+    below += __popc(mask & ((1u << lane) - 1u));
+    some += __popc(mask);
+    sum += n[i];
   }
-  const uint32_t some = __ballot_sync(0xFFFFFFFFu, n > 0);
-  uint32_t inc = n;
+  uint32_t inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
     if (lane >= o) inc += x;
   }
-  constexpr int kWarps = kAttnMaxBatch / 32;
   if (lane == 31 && warp < kWarps) {
     red[warp] = inc;
-    red[kWarps + warp] = __popc(some);
+    red[kWarps + warp] = some;
   }
   __syncthreads();
-  if (tid < kAttnMaxBatch) {
-    uint32_t count = __popc(some & (0xFFFFFFFFu >> (31 - lane))), tiles = 0, tokens = 0;
+  if (warp < kWarps) {
+    uint32_t at = inc - sum, count = below, tiles = 0, tokens = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) {
-        inc += red[w];
+        at += red[w];
         count += red[kWarps + w];
       }
       tiles += red[w];
@@ -115,14 +125,13 @@ __device__ __forceinline__ void attn_make_plan(const AttnArgs& a, AttnPlan* p, u
     }
     // (A share below a lead and a tile has nothing to even out.)
     const uint32_t lead = tokens > 1 && tiles >= (a.lead + 1) * a.workers ? a.lead : 0u;
-    inc += lead * count;
-    p->end[tid] = inc;
-    // one CTA leaves the plan for the kernel that joins the parts
-    if (flag) a.plan[tid] = inc;
-    if (tid == 0) {
-      p->lead = lead;
-      if (flag) a.plan[kAttnMaxBatch] = lead;
+#pragma unroll
+    for (int i = 0; i < TPT; ++i) {
+      at += n[i];
+      count += n[i] > 0;
+      p->end[TPT * tid + i] = at + lead * count;
     }
+    if (tid == 0) p->lead = lead;
   }
   __syncthreads();
 }

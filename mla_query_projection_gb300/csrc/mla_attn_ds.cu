@@ -129,8 +129,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == kTcSoft) prefetch_tensormap(&maps.latent);
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // (after the wait: the join reads the lengths before its own)
   tc_before();
   // (the plan's barriers order the set-up above)
   attn_make_plan(a, plan, reinterpret_cast<uint32_t*>(red), blockIdx.x == 0, seen);

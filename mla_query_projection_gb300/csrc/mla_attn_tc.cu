@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     prefetch_tensormap(&maps.latent);
     prefetch_tensormap(&maps.rope);
   }
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // (after the wait: the join reads the lengths before its own)
   tc_before();
   // (the plan's barriers order the set-up above)
   AttnSeen* seen = reinterpret_cast<AttnSeen*>(smem + S::oP);  // until the first weights

@@ -241,7 +241,6 @@ struct AttnArgs {
   float* lse;      // or null
   float4* part_o;   // partial sums, see attn_part in mla_attn.cuh
   float2* part_ml;  // [heads_pad][2 * workers] their maxima and denominators
-  uint32_t* plan;  // [MLA_MAX_BATCH + 1] for the joining kernel (mla_attn.cuh, AttnPlan)
   uint32_t* err;
   int heads, heads_pad, groups, batch;
   int workers;  // per head group
