@@ -179,8 +179,9 @@ __global__ void __launch_bounds__(COLS == 4 ? 128 : 256) mla_attn_join_kernel(co
 //   32 tokens of 4,096 rows, 64 heads             69.8   35.9  34.0
 //   62 tokens, 128 heads, fp8_ds_mla             210     84.7  83.1
 int attn_join_cols(const AttnArgs& a, int num_sms) {
-  if (a.workers >= 16 * a.batch) return 1;
-  return a.workers >= 6 * a.batch || (a.heads + 3) / 4 * a.batch <= 3 * num_sms ? 2 : 4;
+  const int items = (a.heads + 3) / 4 * a.batch;
+  if (a.workers >= 16 * a.batch && 16 * items <= 8 * num_sms) return 1;
+  return a.workers >= 6 * a.batch || items <= 3 * num_sms ? 2 : 4;
 }
 
 template <int COLS>
@@ -227,6 +228,42 @@ int launched(cudaError_t e) {
   return MLA_ECUDA;
 }
 
+// Heads a CTA takes at most: 16 or 32 where that covers all of them (less
+// padding, and more workers of the same tiles), 64 otherwise.
+int attn_most_heads(int heads) { return heads <= 16 ? 16 : heads <= 32 ? 32 : 64; }
+
+// Heads a CTA takes, by the most tiles that the call's tables or selections can
+// hold (the lengths are known on the GPU only).  With half the heads a CTA has
+// half the queries to load, half the softmax, half the sums to write and join;
+// it has twice the tiles, and each costs more than half (the rows' bytes and,
+// with nvfp4_ds_mla rows, the widening stay).  So: while every CTA still has one
+// tile at most; and for 8-bit rows from 64 to 32 between three and seven tiles
+// (at one to three the tiles are too coarse to share out).  Us with 64, 32 and 16
+// heads a CTA, and tiles a CTA at 32:
+//   1 x 64 heads, 512 E4M3 rows       0.05   13.8  10.7   9.5
+//   1 x 128, 2,048 E4M3 rows          0.4    16.3  13.7  12.5
+//   4 x 64, 2,000 fp8_ds_mla rows     0.8    21.7  18.5  17.2
+//   2 x 64, 2,048 nvfp4_ds_mla rows   0.4    17.5  14.8  13.5
+//   16 x 128, 500 E4M3 rows           1.7    18.1  20.0  19.9
+//   6 x 96, 4,096 E4M3 rows           3.8    29.6  18.7
+//   1 x 64, 65,536 E4M3 rows          6.7    25.4  23.9  30.3
+//   2 x 128, 16,384 E4M3 rows         6.7    28.8  26.0  30.6
+//   2 x 128, 16,384 fp8_ds_mla rows   6.7    33.5  32.1
+//   1 x 128, 32,768 nvfp4_ds_mla rows 6.7    31.7  34.3  50.2
+//   4 x 128, 16,384 E4M3 rows         13     34.5  35.2  50.8
+//   32 x 64, 4,096 E4M3 rows          13     33.8  37.5  54.2
+int attn_cta_heads(const AttnArgs& a, int num_sms) {
+  const int64_t blocks = a.sel != nullptr ? (a.sel_stride < a.bt_stride ? a.sel_stride : a.bt_stride) : a.bt_stride;
+  const int64_t tiles = a.batch * ((blocks * a.page_size + kAttnTile - 1) / kAttnTile);
+  int n = attn_most_heads(a.heads);
+  for (; n > 16; n /= 2) {
+    const int64_t all = tiles * ((a.heads + n / 2 - 1) / (n / 2));
+    const bool few = n == 64 && a.layout != MLA_KV_NVFP4_DS_MLA && all >= 3 * num_sms && all <= 7 * num_sms;
+    if (all > num_sms && !few) break;
+  }
+  return n;
+}
+
 // What a worker's going on from one token to the next costs, in tiles: 5 where
 // a tile is quick against it (E4M3 rows, 64 heads a CTA), else 3.  Us without a
 // lead and with leads of 2, 3 and 5:
@@ -235,9 +272,7 @@ int launched(cudaError_t e) {
 //   E4M3, 60 tokens of 300 to 2,000, 16 heads     25.1  22.3  22.5  23.5
 //   fp8_ds_mla, 62 tokens of 700 to 4,096, 128    92.7  85.4  81.1  83.6
 //   nvfp4_ds_mla, 32 tokens of 4,096 rows, 64     57.3  54.6  54.3  54.6
-uint32_t attn_lead(int layout, int heads) {
-  return row_scaled(layout) && attn_tc_heads(heads) == 64 ? 5u : 3u;
-}
+uint32_t attn_lead(const AttnArgs& a) { return row_scaled(a.layout) && a.cta_heads == 64 ? 5u : 3u; }
 
 // Strides of a [batch][heads][width] operand; 0 means contiguous.
 bool fill_strides(int heads, int width, int unit, int64_t* ts, int64_t* hs) {
@@ -261,7 +296,7 @@ int mla_attn_create(mla_attn_t* out, int max_batch, int heads) {
   h->heads = heads;
   h->max_batch = max_batch;
   int rc = MLA_ECUDA;
-  const int gh = mla::attn_tc_heads(heads);
+  const int gh = mla::attn_most_heads(heads);
   const int groups = (heads + gh - 1) / gh;
   size_t slots = 0;
   if (cudaGetDevice(&h->device) != cudaSuccess) goto fail;
@@ -321,7 +356,6 @@ int mla_attn_decode(mla_attn_t h, int batch, const void* q_latent, int64_t ql_to
       !mla::aligned4(sel) || !mla::aligned4(sel_count) || !mla::aligned4(lse))
     return MLA_EINVAL;
 
-  const int gh = mla::attn_tc_heads(h->heads);
   mla::AttnArgs a = {};
   a.q_latent = static_cast<const uint8_t*>(q_latent);
   a.q_pe = static_cast<const uint8_t*>(q_pe);
@@ -353,10 +387,11 @@ int mla_attn_decode(mla_attn_t h, int batch, const void* q_latent, int64_t ql_to
   a.err = h->err;
   a.heads = h->heads;
   a.batch = batch;
+  const int gh = a.cta_heads = mla::attn_cta_heads(a, h->num_sms);
   a.groups = (h->heads + gh - 1) / gh;
   a.heads_pad = a.groups * gh;
   a.workers = h->num_sms / a.groups;
-  a.lead = mla::attn_lead(layout, h->heads);
+  a.lead = mla::attn_lead(a);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   switch (layout) {

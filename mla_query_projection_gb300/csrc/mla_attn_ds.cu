@@ -608,7 +608,7 @@ cudaError_t launch_attn_ds(const AttnArgs& a, cudaStream_t stream) {
   // one map: the four latent planes and the rope values are 128-byte boxes
   if (maps.box_rows > 0 && !encode_plane_map(&maps.latent, a, kRowDs, 128, maps.box_rows)) return cudaErrorInvalidValue;
   maps.rope = maps.latent;
-  switch (attn_tc_heads(a.heads)) {
+  switch (a.cta_heads) {
     case 16: return launch_ds_heads<16>(a, maps, stream);
     case 32: return launch_ds_heads<32>(a, maps, stream);
     default: return launch_ds_heads<64>(a, maps, stream);

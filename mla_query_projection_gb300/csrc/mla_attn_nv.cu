@@ -518,7 +518,7 @@ cudaError_t prepare_attn_nv() {
 }
 
 cudaError_t launch_attn_nv(const AttnArgs& a, cudaStream_t stream) {
-  switch (attn_tc_heads(a.heads)) {
+  switch (a.cta_heads) {
     case 16: return launch_nv_heads<16>(a, stream);
     case 32: return launch_nv_heads<32>(a, stream);
     default: return launch_nv_heads<64>(a, stream);

@@ -590,10 +590,6 @@ cudaError_t prepare_tc_heads() {
 
 }  // namespace
 
-// Heads a CTA takes: 16 or 32 where that covers all of them (less padding, and
-// more workers of the same tiles), 64 otherwise.
-int attn_tc_heads(int heads) { return heads <= 16 ? 16 : heads <= 32 ? 32 : 64; }
-
 cudaError_t prepare_attn_tc() {
   cudaError_t e = prepare_tc_heads<16>();
   if (e == cudaSuccess) e = prepare_tc_heads<32>();
@@ -607,7 +603,7 @@ cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t stream) {
   if (maps.box_rows > 0 && (!encode_plane_map(&maps.latent, a, kRowE4m3, 128, maps.box_rows) ||
                             !encode_plane_map(&maps.rope, a, kRowE4m3, 64, maps.box_rows)))
     return cudaErrorInvalidValue;
-  switch (attn_tc_heads(a.heads)) {
+  switch (a.cta_heads) {
     case 16: return launch_tc_heads<16>(a, maps, stream);
     case 32: return launch_tc_heads<32>(a, maps, stream);
     default: return launch_tc_heads<64>(a, maps, stream);

@@ -243,6 +243,7 @@ struct AttnArgs {
   float2* part_ml;  // [heads_pad][2 * workers] their maxima and denominators
   uint32_t* err;
   int heads, heads_pad, groups, batch;
+  int cta_heads;  // 16, 32 or 64
   int workers;  // per head group
   uint32_t lead;  // units of a worker's share that a token costs beside its tiles (AttnPlan)
 };
@@ -251,9 +252,7 @@ struct AttnArgs {
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // The attention kernels, by layout: E4M3 rows under one scale or a page's
-// (mla_attn_tc.cu), fp8_ds_mla (mla_attn_ds.cu), nvfp4_ds_mla (mla_attn_nv.cu);
-// and the heads that a CTA of theirs takes.
-int attn_tc_heads(int heads);
+// (mla_attn_tc.cu), fp8_ds_mla (mla_attn_ds.cu), nvfp4_ds_mla (mla_attn_nv.cu).
 cudaError_t prepare_attn_tc();
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t stream);
 cudaError_t prepare_attn_ds();
