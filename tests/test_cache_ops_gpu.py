@@ -283,6 +283,15 @@ def test_attention_growing_maximum_and_a_sink(layout, page):
 
 
 @pytest.mark.parametrize("layout", [0, 1, 2, 3])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page,width", [(64, 4000), (64, 400), (7, 20000)])
+def test_attention_tables_far_wider_than_the_requests(layout, kind, page, width):
+    """What a table could hold decides on the heads a CTA takes; the lengths stay short."""
+    rng = np.random.default_rng(50 + layout)
+    assert run_attention(rng, [300, 0, 77, 1, 513], 100, layout, page, kind, width=width) == 0
+
+
+@pytest.mark.parametrize("layout", [0, 1, 2, 3])
 @pytest.mark.parametrize("page", [16, 100])
 def test_attention_workers_with_several_tokens(layout, page):
     """Many tiles a worker (ten groups of heads leave each 15 workers), and tokens that end inside their shares."""
