@@ -98,9 +98,22 @@ __global__ void __launch_bounds__(MeanShape<LAYOUT>::kThreads)
 // 32-column step is permuted the same way on both sides, so that each lane's
 // share of a row is 16 contiguous bytes: two k16 steps a 16-byte load.
 
+template <bool FP8Q>
+struct ScoreWords {
+  using type = uint4;
+};
+template <>
+struct ScoreWords<true> {
+  using type = uint2;
+};
+
 constexpr int kScorePitch = kRowElems * 2 + 64;  // 1216: 16-byte loads of 8 rows x 4 free of conflicts
 
-template <int NT, bool FP8Q>
+// EARLY (one CTA an SM): a warp's first queries are loaded whole before the
+// blocks' pages are looked up, and wait in registers (one query over 1,024
+// blocks, 64 heads, call after call: 7.8 us, so 4.8).
+
+template <int NT, bool FP8Q, bool EARLY>
 __global__ void __launch_bounds__(256) mla_blocks_score_kernel(const ScoreArgs s) {
   constexpr int kTile = 8 * NT;
   extern __shared__ __align__(16) uint8_t keys[];  // [kTile][kScorePitch]
@@ -118,6 +131,23 @@ __global__ void __launch_bounds__(256) mla_blocks_score_kernel(const ScoreArgs s
   if (row < 0 || row >= s.table_rows) {
     if (nb > 0 && tid == 0 && s.flags != nullptr) atomicOr(s.flags, MLA_DEVERR_BAD_SLOT);
     nb = 0;
+  }
+  constexpr int kB = FP8Q ? 1 : 2;  // bytes per query element
+  using Words = typename ScoreWords<FP8Q>::type;  // a lane's share of a row's 32 columns
+  // heads h0 + g and h0 + g + 8, columns 32 k ..; heads past the last repeat the last
+  auto query = [&](int h0, int k, Words* wa, Words* wb) {
+    const int ha = min(h0 + g, s.heads - 1), hb = min(h0 + g + 8, s.heads - 1);
+    const uint8_t* base = k < 16 ? s.q_latent : s.q_pe;
+    const int64_t ts = k < 16 ? s.ql_ts : s.qp_ts, hs = k < 16 ? s.ql_hs : s.qp_hs;
+    const int64_t at = (int64_t)t * ts + 32 * (k < 16 ? k : k - 16) + 8 * q4;
+    *wa = *reinterpret_cast<const Words*>(base + (at + ha * hs) * kB);
+    *wb = *reinterpret_cast<const Words*>(base + (at + hb * hs) * kB);
+  };
+  constexpr int kAll = kRowElems / 32;
+  Words qa[EARLY ? kAll : 1], qb[EARLY ? kAll : 1];
+  if constexpr (EARLY) {
+#pragma unroll
+    for (int k = 0; k < kAll; ++k) query(16 * warp, k, &qa[k], &qb[k]);
   }
   const int64_t j0 = (int64_t)blockIdx.x * kTile;
   float* out = s.scores + (int64_t)t * s.scores_stride;
@@ -161,23 +191,16 @@ __global__ void __launch_bounds__(256) mla_blocks_score_kernel(const ScoreArgs s
   float mx[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) mx[n][0] = mx[n][1] = -INFINITY;
-  constexpr int kB = FP8Q ? 1 : 2;  // bytes per query element
   if constexpr (kParts == 1) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
   }
   // (with parts, every warp passes the barriers of the first 16 heads, whether it has them or not)
   for (int h0 = 16 * warp; h0 < s.heads || (kParts > 1 && h0 < 128); h0 += 128) {
-    // rows h0 + g and h0 + g + 8; heads past the last repeat the last
-    const int ha = min(h0 + g, s.heads - 1), hb = min(h0 + g + 8, s.heads - 1);
-    const uint8_t* la = s.q_latent + ((int64_t)t * s.ql_ts + (int64_t)ha * s.ql_hs) * kB;
-    const uint8_t* lb = s.q_latent + ((int64_t)t * s.ql_ts + (int64_t)hb * s.ql_hs) * kB;
-    const uint8_t* pa = s.q_pe + ((int64_t)t * s.qp_ts + (int64_t)ha * s.qp_hs) * kB;
-    const uint8_t* pb = s.q_pe + ((int64_t)t * s.qp_ts + (int64_t)hb * s.qp_hs) * kB;
     float acc[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-#pragma unroll 6
+#pragma unroll NT == 2 && !EARLY ? 6 : kAll
     for (int k = 0; k < kRowElems / 32; ++k) {
       if (kParts > 1 && h0 < 128 && k % kSteps == 0) {
         if (k == 0)
@@ -188,12 +211,15 @@ __global__ void __launch_bounds__(256) mla_blocks_score_kernel(const ScoreArgs s
           asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
       }
-      const uint8_t* a = k < 16 ? la + 32 * k * kB : pa + 32 * (k - 16) * kB;
-      const uint8_t* b = k < 16 ? lb + 32 * k * kB : pb + 32 * (k - 16) * kB;
+      Words wa, wb;
+      if (EARLY && h0 < 128) {
+        wa = qa[EARLY ? k : 0];
+        wb = qb[EARLY ? k : 0];
+      } else {
+        query(h0, k, &wa, &wb);
+      }
       uint4 va, vb;
       if constexpr (FP8Q) {
-        const uint2 wa = *reinterpret_cast<const uint2*>(a + 8 * q4);
-        const uint2 wb = *reinterpret_cast<const uint2*>(b + 8 * q4);
         float f[8], h[8];
         e4m3x4_values(wa.x, f);
         e4m3x4_values(wa.y, f + 4);
@@ -204,8 +230,8 @@ __global__ void __launch_bounds__(256) mla_blocks_score_kernel(const ScoreArgs s
         vb = make_uint4(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]), pack_bf16x2(h[4], h[5]),
                         pack_bf16x2(h[6], h[7]));
       } else {
-        va = *reinterpret_cast<const uint4*>(a + 16 * q4);
-        vb = *reinterpret_cast<const uint4*>(b + 16 * q4);
+        va = wa;
+        vb = wb;
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -457,10 +483,10 @@ cudaError_t launch_blocks_mean(const MeanArgs& m, int num_sms, cudaStream_t stre
 }
 
 namespace {
-template <int NT, bool FP8Q>
+template <int NT, bool FP8Q, bool EARLY>
 cudaError_t launch_score(const ScoreArgs& s, cudaStream_t stream) {
   constexpr int kBytes = 8 * NT * kScorePitch;
-  auto kernel = mla_blocks_score_kernel<NT, FP8Q>;
+  auto kernel = mla_blocks_score_kernel<NT, FP8Q, EARLY>;
   if constexpr (kBytes > 40 * 1024) {  // beyond the default limit, on the device in use
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
@@ -485,9 +511,14 @@ cudaError_t launch_blocks_score(const ScoreArgs& s, int num_sms, cudaStream_t st
   // (64 tokens of up to 256 blocks at 128 heads: 17.5 us with 16 blocks, 1,024
   // CTAs reading 150 MB of queries.)
   const bool large = (s.bt_stride + 63) / 64 * s.batch >= num_sms;
+  const bool early = (s.bt_stride + 15) / 16 * s.batch <= num_sms;  // CTAs of 16 blocks
   if (s.q_scale_inv != nullptr)
-    return large ? launch_score<8, true>(s, stream) : launch_score<2, true>(s, stream);
-  return large ? launch_score<8, false>(s, stream) : launch_score<2, false>(s, stream);
+    return large ? launch_score<8, true, false>(s, stream)
+           : early ? launch_score<2, true, true>(s, stream)
+                   : launch_score<2, true, false>(s, stream);
+  return large ? launch_score<8, false, false>(s, stream)
+         : early ? launch_score<2, false, true>(s, stream)
+                 : launch_score<2, false, false>(s, stream);
 }
 
 cudaError_t launch_blocks_select(const SelectArgs& s, cudaStream_t stream) {
