@@ -127,15 +127,13 @@ class Call {
       return nullptr;
     }
     if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev_).stream();
-    if (PyLong_Check(o)) return PyLong_AsVoidPtr(o);
-    PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
-    if (h == nullptr) {
+    PyObject* h = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
+    void* p = h != nullptr ? PyLong_AsVoidPtr(h) : nullptr;
+    Py_XDECREF(h);
+    if (PyErr_Occurred()) {
       PyErr_Clear();
       wrong("stream");
-      return nullptr;
     }
-    void* p = PyLong_AsVoidPtr(h);
-    Py_DECREF(h);
     return p;
   }
   void wrong(const char* what) {
@@ -300,7 +298,9 @@ PyObject* blocks_select(PyObject* const* a) {
 
 PyObject* attn_decode(PyObject* const* a) {
   Call c(a[2]);
-  auto handle = static_cast<mla_attn_t>(PyLong_AsVoidPtr(a[0]));
+  c.need(a[0] != Py_None, "handle is closed");
+  auto handle = a[0] != Py_None ? static_cast<mla_attn_t>(PyLong_AsVoidPtr(a[0])) : nullptr;
+  if (PyErr_Occurred()) return nullptr;
   const Query q(c, a[2], a[3], a[10]);
   c.need(q.heads == c.number(a[1], INT_MAX, "heads"), "heads");
   const Cache k(c, a[4], a[5], a[9]);
@@ -309,6 +309,7 @@ PyObject* attn_decode(PyObject* const* a) {
   c.need(table_rows <= INT_MAX, "block table");
   auto* lens = c.flat<const int32_t>(a[7], at::kInt, q.tokens, "lengths");
   const double scale = PyFloat_AsDouble(a[8]);
+  if (PyErr_Occurred()) return nullptr;
   auto* token_row = c.flat<const int32_t>(a[11], at::kInt, q.tokens, "token_row");
   const int32_t* sel = nullptr;
   if (a[12] != Py_None) {
@@ -321,7 +322,6 @@ PyObject* attn_decode(PyObject* const* a) {
   c.need(type == at::kBFloat16, "out");
   auto* lse = c.flat<float>(a[15], at::kFloat, q.tokens * q.heads, "lse");
   void* stream = c.stream(a[16]);
-  if (PyErr_Occurred()) return nullptr;
   if (!c.ok()) return c.refusal();
   return run([&] { return attn_decode_c(handle, (int)q.tokens, q.latent, q.lt, q.lh, q.pe, q.pt, q.ph, q.inv, k.rows,
                               k.pages, k.page, k.layout, k.scale, table, stride, (int)table_rows, token_row,

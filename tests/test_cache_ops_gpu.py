@@ -475,7 +475,11 @@ def test_attention_refuses_more_tokens_than_its_workspace():
             attn.decode(ql, qp, cache, 0, table, lens, SCALE, k_scale=torch.ones(1).cuda(), **kw)
     with pytest.raises(B.MlaError):  # one token, but a scale that is not finite
         attn.decode(ql[:1], qp[:1], cache, 0, table, lens[:1], float("nan"), k_scale=torch.ones(1).cuda())
+    with pytest.raises(B.MlaError):  # no stream
+        attn.decode(ql[:1], qp[:1], cache, 0, table, lens[:1], SCALE, k_scale=torch.ones(1).cuda(), stream="1")
     attn.close()
+    with pytest.raises(B.MlaError):
+        attn.decode(ql[:1], qp[:1], cache, 0, table, lens[:1], SCALE, k_scale=torch.ones(1).cuda())
 
 
 # ------------------------------------------------------------------- tables
