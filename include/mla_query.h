@@ -499,7 +499,7 @@ MLA_API int mla_attn_create(mla_attn_t* out, int max_batch, int heads);
  *   out           device BF16 [batch][heads][512] (strides as above, multiples
  *                 of 8).
  *   lse           device FP32 [batch][heads], natural logarithm of the sum of
- *                 exponentials, or NULL.
+ *                 exponentials, or NULL.  Neither it nor out may overlap an input.
  *
  * A token that looks at no position (lens[t] <= 0, a padded token, no block
  * selected) gets zeros and an lse of -infinity.  Cache bytes of positions
