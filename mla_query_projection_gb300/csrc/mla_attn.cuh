@@ -50,7 +50,7 @@ __device__ __forceinline__ uint32_t attn_positions(const AttnArgs& a, int t, int
   if (!bad) {
     const int64_t cap = a.bt_stride * a.page_size;
     if (a.sel != nullptr) {
-      n = min((int64_t)max(a.sel_count[t], 0), a.sel_stride) * a.page_size;
+      n = min((int64_t)max(__ldcg(a.sel_count + t), 0), a.sel_stride) * a.page_size;
     } else {
       n = min((int64_t)len, cap);
       bad = len > cap;
@@ -86,8 +86,10 @@ __device__ __forceinline__ void attn_make_plan(const AttnArgs& a, AttnPlan* p, u
     const int t = TPT * tid + i;
     n[i] = 0;
     if (t < a.batch) {
-      const int32_t len = a.lens[t];
-      const int row = a.token_row != nullptr ? a.token_row[t] : t;
+      // (from L2: the join asks before its own wait, when only the kernel before
+      // has waited for what wrote these)
+      const int32_t len = __ldcg(a.lens + t);
+      const int row = a.token_row != nullptr ? __ldcg(a.token_row + t) : t;
       const uint32_t nv = attn_positions(a, t, len, row, flag);
       n[i] = (nv + kAttnTile - 1) / kAttnTile;
       if (seen != nullptr) {

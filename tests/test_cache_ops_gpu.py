@@ -462,6 +462,50 @@ def test_attention_repeats_and_streams():
     attn.close()
 
 
+def test_attention_right_behind_what_writes_its_lengths():
+    """Lengths that the call before wrote, a step after another in one graph: every step sees its own."""
+    rng = np.random.default_rng(49)
+    rows, page, pages = 3, 16, 300
+    cache, k_scale = C.make_cache(rng, pages, page, 0)
+    ql, qp, inv, q64 = queries(rng, rows, 16)
+    cache_d, scale_d = dev(cache), dev(k_scale)
+    lens = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    table = torch.full((rows, 90), -1, dtype=torch.int32, device="cuda")
+    free, count = torch.arange(pages, dtype=torch.int32, device="cuda"), dev(np.array([pages], dtype=np.int32))
+    news = [[900, 5, 0], [1, 1, 300], [1, 500, 1], [200, 1, 1]]
+    steps = [dict(new=dev(np.array(n, dtype=np.int32)), slots=torch.zeros(1500, dtype=torch.int64, device="cuda"),
+                  row=torch.zeros(1500, dtype=torch.int32, device="cuda"),
+                  ln=torch.zeros(1500, dtype=torch.int32, device="cuda"),
+                  out=torch.zeros(rows, 16, 512, dtype=torch.bfloat16, device="cuda"),
+                  lse=torch.zeros(rows, 16, device="cuda")) for n in news]
+    cu = torch.zeros(rows + 1, dtype=torch.int32, device="cuda")
+    attn = R.PagedAttention(rows, 16)
+
+    def go():
+        for s in steps:
+            R.tables_step(s["new"], lens, table, free, count, page, lens, count, s["slots"], s["row"], s["ln"], cu)
+            attn.decode(ql, qp, cache_d, 0, table, lens, SCALE, k_scale=scale_d, out=s["out"], lse=s["lse"])
+
+    go()  # (and once more below, from a graph)
+    lens.zero_()
+    table.fill_(-1)
+    free.copy_(torch.arange(pages, dtype=torch.int32))
+    count.fill_(pages)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert attn.error_flags() == 0
+    final, held = table.cpu().numpy(), np.zeros(rows, dtype=int)
+    for s, n in zip(steps, news):
+        held += n
+        for r in range(rows):
+            where = C.positions(int(held[r]), page, 90, pages, final[r])
+            check_attention(s["out"][r], s["lse"][r], q64[r], keys64(cache, k_scale, 0, where), SCALE, (n, r))
+    attn.close()
+
+
 def test_attention_refuses_more_tokens_than_its_workspace():
     attn = R.PagedAttention(1, 16)
     ql, qp, _, _ = queries(np.random.default_rng(1), 2, 16)
