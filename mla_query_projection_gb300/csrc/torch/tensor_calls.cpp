@@ -91,17 +91,21 @@ class Call {
     return static_cast<T*>(t->data_ptr());
   }
   // Address and strides of a [tokens, heads, width] tensor with unit inner stride.
+  // A stride of 0 is one row for all to torch (an expanded tensor) and contiguous
+  // rows to the library: refused, and what the library gets where there is one
+  // token or head, whose stride in torch may be anything.
   void* heads(PyObject* o, int64_t tokens, int64_t heads, int64_t width, int64_t* ts, int64_t* hs,
               at::ScalarType* type, const char* what) {
     const at::Tensor* t = tensor(o, what);
     if (t == nullptr) return nullptr;
     if (t->dim() != 3 || t->size(0) != tokens || t->size(1) != heads || t->size(2) != width ||
-        t->stride(2) != 1 || t->get_device() != dev_) {
+        t->stride(2) != 1 || (tokens > 1 && t->stride(0) == 0) || (heads > 1 && t->stride(1) == 0) ||
+        t->get_device() != dev_) {
       wrong(what);
       return nullptr;
     }
-    *ts = t->stride(0);
-    *hs = t->stride(1);
+    *ts = tokens > 1 ? t->stride(0) : 0;
+    *hs = heads > 1 ? t->stride(1) : 0;
     *type = t->scalar_type();
     return t->data_ptr();
   }

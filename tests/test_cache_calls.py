@@ -1,0 +1,66 @@
+"""Host checks of the cache-side calls for torch tensors that have the right
+sizes and types, but would be read or written elsewhere than they lie (CPU only:
+every call here is refused before a launch, by the text that is matched)."""
+
+import os
+
+import pytest
+import torch
+
+from mla_query_projection_gb300 import binding as B
+from mla_query_projection_gb300 import runner as R
+
+BF16, I32 = torch.bfloat16, torch.int32
+HERE = "tensors that are not on the current device"  # the last check: all else was taken
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not os.path.exists(B.LIB_PATH):
+        from mla_query_projection_gb300 import build
+
+        build.build()
+    return B.load()
+
+
+def attend(tokens=3, heads=4, width=8, **change):
+    """What the attention call says to these tensors in host memory; its handle is never followed."""
+    a = dict(handle=4096, heads=heads, q_latent=torch.zeros(tokens, heads, 512, dtype=BF16),
+             q_pe=torch.zeros(tokens, heads, 64, dtype=BF16), cache=torch.zeros(9, 16, 576, dtype=torch.uint8),
+             layout=0, table=torch.zeros(tokens, width, dtype=I32), lens=torch.ones(tokens, dtype=I32), scale=0.1,
+             k_scale=torch.ones(1), inv=None, token_row=None, sel=None, sel_count=None,
+             out=torch.zeros(tokens, heads, 512, dtype=BF16), lse=None, stream=0)
+    return R._native().attn_decode(*(a | change).values())
+
+
+def score(tokens=3, heads=4, width=8, **change):
+    a = dict(q_latent=torch.zeros(tokens, heads, 512, dtype=BF16), q_pe=torch.zeros(tokens, heads, 64, dtype=BF16),
+             mean=torch.zeros(9, 576, dtype=BF16), page=16, table=torch.zeros(tokens, width, dtype=I32),
+             lens=torch.ones(tokens, dtype=I32), scores=torch.zeros(tokens, width), inv=None, token_row=None, flags=None,
+             stream=0)
+    return R._native().blocks_score(*(a | change).values())
+
+
+@pytest.mark.parametrize("call", [attend, score])
+def test_broadcast_queries_are_refused(call):
+    """An expanded tensor holds one token's or one head's rows: not what a row stride of 0 means to the library."""
+    assert call() == HERE
+    for name, width in (("q_latent", 512), ("q_pe", 64)):
+        for shape in ((1, 4, width), (3, 1, width), (1, 1, width)):
+            t = torch.zeros(shape, dtype=BF16).expand(3, 4, width)
+            assert call(**{name: t}) == "query shape", (name, shape)
+        # a single token or head is no broadcast, whatever its stride
+        assert call(tokens=1, **{name: torch.zeros(1, 4, width, dtype=BF16).expand(1, 4, width)}) == HERE
+        assert call(heads=1, **{name: torch.zeros(3, 1, width, dtype=BF16)}) == HERE
+        odd = torch.zeros(8, 4, width, dtype=BF16).as_strided((1, 4, width), (7, width, 1))
+        assert call(tokens=1, **{name: odd}) == HERE
+    with pytest.raises(B.MlaError, match="query shape"):
+        R.blocks_score(torch.zeros(1, 4, 512, dtype=BF16).expand(3, 4, 512), torch.zeros(3, 4, 64, dtype=BF16),
+                       torch.zeros(9, 576, dtype=BF16), 16, torch.zeros(3, 8, dtype=I32), torch.ones(3, dtype=I32),
+                       torch.zeros(3, 8), stream=0)
+
+
+def test_broadcast_output_is_refused():
+    assert attend(out=torch.zeros(1, 4, 512, dtype=BF16).expand(3, 4, 512)) == "out"
+    assert attend(out=torch.zeros(3, 1, 512, dtype=BF16).expand(3, 4, 512)) == "out"
+    assert attend(out=torch.zeros(4, 3, 512, dtype=BF16).transpose(0, 1)) == HERE  # head-major
