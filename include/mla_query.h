@@ -497,7 +497,7 @@ MLA_API int mla_attn_create(mla_attn_t* out, int max_batch, int heads);
  *                 left out.
  *   softmax_scale >= 0, finite.
  *   out           device BF16 [batch][heads][512] (strides as above, multiples
- *                 of 8).
+ *                 of 8), rows that do not overlap.
  *   lse           device FP32 [batch][heads], natural logarithm of the sum of
  *                 exponentials, or NULL.  Neither it nor out may overlap an input.
  *

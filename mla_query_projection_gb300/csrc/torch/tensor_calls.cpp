@@ -324,6 +324,10 @@ PyObject* attn_decode(PyObject* const* a) {
   at::ScalarType type = at::kFloat;
   void* out = c.heads(a[14], q.tokens, q.heads, 512, &ot, &oh, &type, "out");
   c.need(type == at::kBFloat16, "out");
+  // rows that do not lie over one another: the closer ones in between the others
+  const int64_t near = ot < oh ? ot : oh, far = ot < oh ? oh : ot;
+  const int64_t count = ot < oh ? q.tokens : q.heads;
+  c.need(q.tokens <= 1 || q.heads <= 1 || (near >= 512 && (far - 512) / near >= count - 1), "out");
   auto* lse = c.flat<float>(a[15], at::kFloat, q.tokens * q.heads, "lse");
   void* stream = c.stream(a[16]);
   if (!c.ok()) return c.refusal();

@@ -64,3 +64,12 @@ def test_broadcast_output_is_refused():
     assert attend(out=torch.zeros(1, 4, 512, dtype=BF16).expand(3, 4, 512)) == "out"
     assert attend(out=torch.zeros(3, 1, 512, dtype=BF16).expand(3, 4, 512)) == "out"
     assert attend(out=torch.zeros(4, 3, 512, dtype=BF16).transpose(0, 1)) == HERE  # head-major
+
+
+def test_output_rows_that_overlap_are_refused():
+    """Two heads or tokens written to the same place have no result."""
+    room = torch.zeros(16 * 512, dtype=BF16)
+    for strides in ((512, 512), (1024, 1024), (512, 1024), (3 * 512, 512), (512, 2 * 512)):
+        assert attend(out=room.as_strided((3, 4, 512), (*strides, 1))) == "out", strides
+    for strides in ((4 * 512, 512), (512, 3 * 512), (5 * 512, 512), (520, 3 * 520)):  # rows side by side, gaps
+        assert attend(out=room.as_strided((3, 4, 512), (*strides, 1))) == HERE, strides
