@@ -526,6 +526,28 @@ MLA_API int mla_attn_decode(mla_attn_t h, int batch, const void* q_latent, int64
                             void* out, int64_t out_token_stride, int64_t out_head_stride,
                             float* lse, void* stream);
 
+/*
+ * mla_attn_decode_cols - mla_attn_decode for a table, or selections, that are
+ * the first columns of wider ones: rows of bt_cols blocks (1..bt_stride) that
+ * lie bt_stride apart, selections of at most sel_cols entries (1..sel_stride)
+ * that lie sel_stride apart.  What lies behind those columns is not read, and
+ * bt_cols * page_size is what lens may count.  mla_attn_decode itself takes
+ * all columns.  How the call spreads its work goes by the columns: a table
+ * that is wider than this step's longest request is best passed with the
+ * columns that the step needs.
+ */
+MLA_API int mla_attn_decode_cols(mla_attn_t h, int batch, const void* q_latent,
+                                 int64_t ql_token_stride, int64_t ql_head_stride, const void* q_pe,
+                                 int64_t qp_token_stride, int64_t qp_head_stride,
+                                 const float* q_scale_inv, const void* kv_cache, int64_t num_pages,
+                                 int page_size, int layout, const float* k_scale,
+                                 const int32_t* block_table, int64_t bt_stride, int64_t bt_cols,
+                                 int table_rows, const int32_t* token_row, const int32_t* lens,
+                                 const int32_t* sel, int64_t sel_stride, int64_t sel_cols,
+                                 const int32_t* sel_count, float softmax_scale, void* out,
+                                 int64_t out_token_stride, int64_t out_head_stride, float* lse,
+                                 void* stream);
+
 /* mla_attn_get_error - read and clear the handle's device error word
  * (MLA_DEVERR_*); synchronises `stream`. */
 MLA_API int mla_attn_get_error(mla_attn_t h, unsigned* device_flags, void* stream);
@@ -552,6 +574,16 @@ MLA_API int mla_blocks_mean(const void* kv_cache, int64_t num_pages, int page_si
                             const float* k_scale, const int32_t* block_table, int64_t bt_stride,
                             int rows, const int32_t* lens_from, const int32_t* lens_to, void* mean,
                             unsigned* device_flags, void* stream);
+
+/*
+ * mla_blocks_mean_cols - mla_blocks_mean for a table that is the first columns
+ * of a wider one: rows of bt_cols blocks (1..bt_stride), bt_stride apart.
+ */
+MLA_API int mla_blocks_mean_cols(const void* kv_cache, int64_t num_pages, int page_size, int layout,
+                                 const float* k_scale, const int32_t* block_table,
+                                 int64_t bt_stride, int64_t bt_cols, int rows,
+                                 const int32_t* lens_from, const int32_t* lens_to, void* mean,
+                                 unsigned* device_flags, void* stream);
 
 /*
  * mla_blocks_score - a score of every block for every query token:

@@ -21,9 +21,11 @@ from .binding import (  # noqa: F401
     MlaError,
     mla_attn_create,
     mla_attn_decode,
+    mla_attn_decode_cols,
     mla_attn_destroy,
     mla_attn_get_error,
     mla_blocks_mean,
+    mla_blocks_mean_cols,
     mla_blocks_score,
     mla_blocks_select,
     mla_query_create,

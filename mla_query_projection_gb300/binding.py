@@ -116,6 +116,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
         i64, vp, f32, vp, i64, i64, vp, vp,
     ]
     lib.mla_attn_decode.restype = i32
+    lib.mla_attn_decode_cols.argtypes = [
+        vp, i32, vp, i64, i64, vp, i64, i64, vp, vp, i64, i32, i32, vp, vp, i64, i64, i32, vp, vp,
+        vp, i64, i64, vp, f32, vp, i64, i64, vp, vp,
+    ]
+    lib.mla_attn_decode_cols.restype = i32
     lib.mla_attn_get_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint), vp]
     lib.mla_attn_get_error.restype = i32
     lib.mla_attn_destroy.argtypes = [vp]
@@ -124,6 +129,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
         vp, i64, i32, i32, vp, vp, i64, i32, vp, vp, vp, vp, vp,
     ]
     lib.mla_blocks_mean.restype = i32
+    lib.mla_blocks_mean_cols.argtypes = [
+        vp, i64, i32, i32, vp, vp, i64, i64, i32, vp, vp, vp, vp, vp,
+    ]
+    lib.mla_blocks_mean_cols.restype = i32
     lib.mla_blocks_score.argtypes = [
         i32, i32, vp, i64, i64, vp, i64, i64, vp, vp, i64, i32, vp, i64, i32, vp, vp, vp, i64, vp,
         vp,
@@ -331,6 +340,22 @@ def mla_attn_decode(
     )
 
 
+def mla_attn_decode_cols(
+    handle, batch, q_latent, ql_token_stride, ql_head_stride, q_pe, qp_token_stride,
+    qp_head_stride, q_scale_inv, kv_cache, num_pages, page_size, layout, k_scale, block_table,
+    bt_stride, bt_cols, table_rows, token_row, lens, sel, sel_stride, sel_cols, sel_count,
+    softmax_scale, out, out_token_stride, out_head_stride, lse, stream,
+) -> int:
+    """The same with a table or selections that are the first columns of wider ones."""
+    return load().mla_attn_decode_cols(
+        handle, batch, _ptr(q_latent), ql_token_stride, ql_head_stride, _ptr(q_pe),
+        qp_token_stride, qp_head_stride, _ptr(q_scale_inv), _ptr(kv_cache), num_pages, page_size,
+        layout, _ptr(k_scale), _ptr(block_table), bt_stride, bt_cols, table_rows, _ptr(token_row),
+        _ptr(lens), _ptr(sel), sel_stride, sel_cols, _ptr(sel_count), softmax_scale, _ptr(out),
+        out_token_stride, out_head_stride, _ptr(lse), _stream(stream),
+    )
+
+
 def mla_attn_get_error(handle, stream=None) -> int:
     v = ctypes.c_uint(0)
     rc = load().mla_attn_get_error(handle, ctypes.byref(v), _stream(stream))
@@ -351,6 +376,18 @@ def mla_blocks_mean(
     return load().mla_blocks_mean(
         _ptr(kv_cache), num_pages, page_size, layout, _ptr(k_scale), _ptr(block_table), bt_stride,
         rows, _ptr(lens_from), _ptr(lens_to), _ptr(mean), _ptr(device_flags), _stream(stream),
+    )
+
+
+def mla_blocks_mean_cols(
+    kv_cache, num_pages, page_size, layout, k_scale, block_table, bt_stride, bt_cols, rows,
+    lens_from, lens_to, mean, device_flags, stream,
+) -> int:
+    """The same with a table that is the first columns of a wider one."""
+    return load().mla_blocks_mean_cols(
+        _ptr(kv_cache), num_pages, page_size, layout, _ptr(k_scale), _ptr(block_table), bt_stride,
+        bt_cols, rows, _ptr(lens_from), _ptr(lens_to), _ptr(mean), _ptr(device_flags),
+        _stream(stream),
     )
 
 

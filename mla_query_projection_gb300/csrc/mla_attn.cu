@@ -253,7 +253,7 @@ int attn_most_heads(int heads) { return heads <= 16 ? 16 : heads <= 32 ? 32 : 64
 //   4 x 128, 16,384 E4M3 rows         13     34.5  35.2  50.8
 //   32 x 64, 4,096 E4M3 rows          13     33.8  37.5  54.2
 int attn_cta_heads(const AttnArgs& a, int num_sms) {
-  const int64_t blocks = a.sel != nullptr ? (a.sel_stride < a.bt_stride ? a.sel_stride : a.bt_stride) : a.bt_stride;
+  const int64_t blocks = a.sel != nullptr ? (a.sel_cols < a.bt_cols ? a.sel_cols : a.bt_cols) : a.bt_cols;
   const int64_t tiles = a.batch * ((blocks * a.page_size + kAttnTile - 1) / kAttnTile);
   int n = attn_most_heads(a.heads);
   for (; n > 16; n /= 2) {
@@ -333,6 +333,22 @@ int mla_attn_decode(mla_attn_t h, int batch, const void* q_latent, int64_t ql_to
                     const int32_t* token_row, const int32_t* lens, const int32_t* sel,
                     int64_t sel_stride, const int32_t* sel_count, float softmax_scale, void* out,
                     int64_t out_token_stride, int64_t out_head_stride, float* lse, void* stream) {
+  return mla_attn_decode_cols(h, batch, q_latent, ql_token_stride, ql_head_stride, q_pe, qp_token_stride,
+                              qp_head_stride, q_scale_inv, kv_cache, num_pages, page_size, layout, k_scale,
+                              block_table, bt_stride, bt_stride, table_rows, token_row, lens, sel, sel_stride,
+                              sel_stride, sel_count, softmax_scale, out, out_token_stride, out_head_stride, lse,
+                              stream);
+}
+
+int mla_attn_decode_cols(mla_attn_t h, int batch, const void* q_latent, int64_t ql_token_stride,
+                         int64_t ql_head_stride, const void* q_pe, int64_t qp_token_stride,
+                         int64_t qp_head_stride, const float* q_scale_inv, const void* kv_cache,
+                         int64_t num_pages, int page_size, int layout, const float* k_scale,
+                         const int32_t* block_table, int64_t bt_stride, int64_t bt_cols, int table_rows,
+                         const int32_t* token_row, const int32_t* lens, const int32_t* sel,
+                         int64_t sel_stride, int64_t sel_cols, const int32_t* sel_count,
+                         float softmax_scale, void* out, int64_t out_token_stride,
+                         int64_t out_head_stride, float* lse, void* stream) {
   if (h == nullptr || batch < 1 || batch > h->max_batch) return MLA_EINVAL;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return mla::launched(cudaErrorInvalidDevice);
@@ -341,9 +357,10 @@ int mla_attn_decode(mla_attn_t h, int batch, const void* q_latent, int64_t ql_to
       lens == nullptr || out == nullptr)
     return MLA_EINVAL;
   if (!mla::known_layout(layout) || (mla::row_scaled(layout) && k_scale == nullptr)) return MLA_EINVAL;
-  if (num_pages < 1 || page_size < 1 || bt_stride < 1 || table_rows < 1) return MLA_EINVAL;
+  if (num_pages < 1 || page_size < 1 || bt_cols < 1 || bt_stride < bt_cols || table_rows < 1) return MLA_EINVAL;
   if (token_row == nullptr && table_rows < batch) return MLA_EINVAL;
-  if ((sel == nullptr) != (sel_count == nullptr) || (sel != nullptr && sel_stride < 1)) return MLA_EINVAL;
+  if ((sel == nullptr) != (sel_count == nullptr)) return MLA_EINVAL;
+  if (sel != nullptr && (sel_cols < 1 || sel_stride < sel_cols)) return MLA_EINVAL;
   if (!(softmax_scale >= 0.0f) || softmax_scale > 3.0e38f) return MLA_EINVAL;
   const int unit = q_scale_inv != nullptr ? 16 : 8;
   if (!mla::fill_strides(h->heads, mla::kKvLora, unit, &ql_token_stride, &ql_head_stride) ||
@@ -371,11 +388,13 @@ int mla_attn_decode(mla_attn_t h, int batch, const void* q_latent, int64_t ql_to
   a.k_scale = k_scale;
   a.table = block_table;
   a.bt_stride = bt_stride;
+  a.bt_cols = bt_cols;
   a.table_rows = table_rows;
   a.token_row = token_row;
   a.lens = lens;
   a.sel = sel;
   a.sel_stride = sel_stride;
+  a.sel_cols = sel_cols;
   a.sel_count = sel_count;
   a.scale = softmax_scale;
   a.out = static_cast<uint16_t*>(out);
@@ -455,11 +474,20 @@ int mla_blocks_mean(const void* kv_cache, int64_t num_pages, int page_size, int 
                     const float* k_scale, const int32_t* block_table, int64_t bt_stride, int rows,
                     const int32_t* lens_from, const int32_t* lens_to, void* mean,
                     unsigned* device_flags, void* stream) {
+  return mla_blocks_mean_cols(kv_cache, num_pages, page_size, layout, k_scale, block_table, bt_stride, bt_stride,
+                              rows, lens_from, lens_to, mean, device_flags, stream);
+}
+
+int mla_blocks_mean_cols(const void* kv_cache, int64_t num_pages, int page_size, int layout,
+                         const float* k_scale, const int32_t* block_table, int64_t bt_stride,
+                         int64_t bt_cols, int rows, const int32_t* lens_from, const int32_t* lens_to,
+                         void* mean, unsigned* device_flags, void* stream) {
   if (kv_cache == nullptr || block_table == nullptr || lens_from == nullptr || lens_to == nullptr ||
       mean == nullptr)
     return MLA_EINVAL;
   if (!mla::known_layout(layout) || (mla::row_scaled(layout) && k_scale == nullptr)) return MLA_EINVAL;
-  if (num_pages < 1 || page_size < 1 || bt_stride < 1 || rows < 1 || rows > MLA_MAX_TABLE_ROWS)
+  if (num_pages < 1 || page_size < 1 || bt_cols < 1 || bt_stride < bt_cols || rows < 1 ||
+      rows > MLA_MAX_TABLE_ROWS)
     return MLA_EINVAL;
   if (!mla::aligned16(kv_cache) || !mla::aligned16(mean) || !mla::aligned4(k_scale) ||
       !mla::aligned4(block_table) || !mla::aligned4(lens_from) || !mla::aligned4(lens_to) ||
@@ -468,7 +496,7 @@ int mla_blocks_mean(const void* kv_cache, int64_t num_pages, int page_size, int 
   int sms = 0;
   if (mla::sm_count(&sms) != MLA_OK) return MLA_ECUDA;
   const mla::MeanArgs m{static_cast<const uint8_t*>(kv_cache), num_pages, page_size, layout, k_scale,
-                        block_table, bt_stride, rows, lens_from, lens_to,
+                        block_table, bt_stride, bt_cols, rows, lens_from, lens_to,
                         static_cast<uint16_t*>(mean), device_flags};
   return mla::launched(mla::launch_blocks_mean(m, sms, static_cast<cudaStream_t>(stream)));
 }

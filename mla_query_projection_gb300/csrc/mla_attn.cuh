@@ -48,9 +48,9 @@ __device__ __forceinline__ uint32_t attn_positions(const AttnArgs& a, int t, int
   bool bad = row < 0 || row >= a.table_rows;
   int64_t n = 0;
   if (!bad) {
-    const int64_t cap = a.bt_stride * a.page_size;
+    const int64_t cap = a.bt_cols * a.page_size;
     if (a.sel != nullptr) {
-      n = min((int64_t)max(__ldcg(a.sel_count + t), 0), a.sel_stride) * a.page_size;
+      n = min((int64_t)max(__ldcg(a.sel_count + t), 0), a.sel_cols) * a.page_size;
     } else {
       n = min((int64_t)len, cap);
       bad = len > cap;
@@ -213,7 +213,7 @@ __device__ __forceinline__ int64_t attn_row(const AttnArgs& a, const AttnToken& 
   int64_t j = b;
   if (a.sel != nullptr) {
     j = a.sel[(int64_t)k.t * a.sel_stride + b];
-    if (j < 0 || j >= a.bt_stride || j * a.page_size + off >= k.len) return -1;
+    if (j < 0 || j >= a.bt_cols || j * a.page_size + off >= k.len) return -1;
   }
   const int64_t p = a.table[(int64_t)k.row * a.bt_stride + j];
   if (p < 0 || p >= a.num_pages) {

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(MeanShape<LAYOUT>::kThreads)
   pdl_wait();
   const int r = blockIdx.y;
   const int64_t ps = m.page_size;
-  const int64_t cap = m.bt_stride * ps;
+  const int64_t cap = m.bt_cols * ps;
   const int64_t from = max(0, m.lens_from[r]), to = min((int64_t)m.lens_to[r], cap);
   for (int64_t j = from / ps + blockIdx.x; j * ps < to; j += gridDim.x) {
     const int64_t page = m.block_table[(int64_t)r * m.bt_stride + j];
@@ -457,7 +457,7 @@ cudaError_t launch_blocks_mean(const MeanArgs& m, int num_sms, cudaStream_t stre
   // of one new token: 4.0 and 4.2).
   const int64_t per_sm = m.rows <= 16 ? 6 : 4;
   int64_t gx = (per_sm * num_sms + m.rows - 1) / m.rows;
-  if (gx > m.bt_stride) gx = m.bt_stride;
+  if (gx > m.bt_cols) gx = m.bt_cols;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)gx, (unsigned)m.rows, 1);
   cfg.stream = stream;

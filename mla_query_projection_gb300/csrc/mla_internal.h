@@ -227,13 +227,13 @@ struct AttnArgs {
   int page_size;
   int layout;
   const float* k_scale;
-  const int32_t* table;  // [table_rows][bt_stride] page of each block
-  int64_t bt_stride;
+  const int32_t* table;  // [table_rows][bt_cols] page of each block, rows bt_stride apart
+  int64_t bt_stride, bt_cols;
   int table_rows;
   const int32_t* token_row;  // [batch] or null: token t reads table row t
   const int32_t* lens;       // [batch] positions each token looks at
-  const int32_t* sel;        // [batch][sel_stride] selected blocks, or null: all
-  int64_t sel_stride;
+  const int32_t* sel;        // [batch][sel_cols] selected blocks, rows sel_stride apart, or null: all
+  int64_t sel_stride, sel_cols;
   const int32_t* sel_count;  // [batch]
   float scale;
   uint16_t* out;
@@ -290,7 +290,7 @@ struct MeanArgs {
   int layout;
   const float* k_scale;
   const int32_t* block_table;
-  int64_t bt_stride;
+  int64_t bt_stride, bt_cols;
   int rows;
   const int32_t* lens_from;
   const int32_t* lens_to;

@@ -25,10 +25,10 @@
 namespace {
 
 decltype(&mla_tables_step) tables_step_c = nullptr;
-decltype(&mla_blocks_mean) blocks_mean_c = nullptr;
+decltype(&mla_blocks_mean_cols) blocks_mean_c = nullptr;
 decltype(&mla_blocks_score) blocks_score_c = nullptr;
 decltype(&mla_blocks_select) blocks_select_c = nullptr;
-decltype(&mla_attn_decode) attn_decode_c = nullptr;
+decltype(&mla_attn_decode_cols) attn_decode_c = nullptr;
 
 // What a call asks of its tensors; the first thing that is wrong stays.
 class Call {
@@ -258,7 +258,7 @@ PyObject* blocks_mean(PyObject* const* a) {
   auto* flags = c.flat<unsigned>(a[7], at::kInt, 1, "flags");
   void* stream = c.stream(a[8]);
   if (!c.ok()) return c.refusal();
-  return run([&] { return blocks_mean_c(k.rows, k.pages, k.page, k.layout, k.scale, table, stride, (int)rows, from, to,
+  return run([&] { return blocks_mean_c(k.rows, k.pages, k.page, k.layout, k.scale, table, stride, width, (int)rows, from, to,
                               mean, flags, stream); });
 }
 
@@ -308,7 +308,7 @@ PyObject* attn_decode(PyObject* const* a) {
   const Query q(c, a[2], a[3], a[10]);
   c.need(q.heads == c.number(a[1], INT_MAX, "heads"), "heads");
   const Cache k(c, a[4], a[5], a[9]);
-  int64_t stride, table_rows, width, sel_stride = 0, sel_rows = 0, sel_cols, ot = 0, oh = 0;
+  int64_t stride, table_rows, width, sel_stride = 0, sel_rows = 0, sel_cols = 0, ot = 0, oh = 0;
   auto* table = c.rows<const int32_t>(a[6], at::kInt, &stride, &table_rows, &width, "block table");
   c.need(table_rows <= INT_MAX, "block table");
   auto* lens = c.flat<const int32_t>(a[7], at::kInt, q.tokens, "lengths");
@@ -332,8 +332,8 @@ PyObject* attn_decode(PyObject* const* a) {
   void* stream = c.stream(a[16]);
   if (!c.ok()) return c.refusal();
   return run([&] { return attn_decode_c(handle, (int)q.tokens, q.latent, q.lt, q.lh, q.pe, q.pt, q.ph, q.inv, k.rows,
-                              k.pages, k.page, k.layout, k.scale, table, stride, (int)table_rows, token_row,
-                              lens, sel, sel_stride, sel_count, (float)scale, out, ot, oh, lse, stream); });
+                              k.pages, k.page, k.layout, k.scale, table, stride, width, (int)table_rows, token_row,
+                              lens, sel, sel_stride, sel_cols, sel_count, (float)scale, out, ot, oh, lse, stream); });
 }
 
 PyObject* bind(PyObject* const* a) {

@@ -151,8 +151,8 @@ def _native():
             raise RuntimeError("mla_query_projection_gb300/_tensor_calls.so is not built: build it with "
                                "`python -m mla_query_projection_gb300.build`") from e
         _tensor_calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-            lib.mla_tables_step, lib.mla_blocks_mean, lib.mla_blocks_score, lib.mla_blocks_select,
-            lib.mla_attn_decode)))
+            lib.mla_tables_step, lib.mla_blocks_mean_cols, lib.mla_blocks_score, lib.mla_blocks_select,
+            lib.mla_attn_decode_cols)))
         _calls = _tensor_calls
     return _calls
 
@@ -223,7 +223,8 @@ class PagedAttention:
         """Attention of the query tokens (``mla_attn_decode``); returns ``(out, lse)``.
 
         ``q_latent`` [tokens, heads, 512] and ``q_pe`` [tokens, heads, 64] may
-        be strided (views of gathered rows); ``out`` BF16 [tokens, heads, 512]
+        be strided (views of gathered rows), and so may ``block_table`` and
+        ``sel`` (the first columns of wider tables: only those count); ``out`` BF16 [tokens, heads, 512]
         is allocated where it is not given, ``lse`` FP32 [tokens, heads] is
         written where it is."""
         if out is None:

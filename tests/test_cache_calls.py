@@ -73,3 +73,14 @@ def test_output_rows_that_overlap_are_refused():
         assert attend(out=room.as_strided((3, 4, 512), (*strides, 1))) == "out", strides
     for strides in ((4 * 512, 512), (512, 3 * 512), (5 * 512, 512), (520, 3 * 520)):  # rows side by side, gaps
         assert attend(out=room.as_strided((3, 4, 512), (*strides, 1))) == HERE, strides
+
+
+def test_columns_of_wider_tables():
+    """The C calls take the columns apart from the stride: at least one, no more than the stride."""
+    p = 4096
+    mean = dict(kv_cache=p, num_pages=16, page_size=64, layout=0, k_scale=p, block_table=p, bt_stride=8, bt_cols=4,
+                rows=2, lens_from=p, lens_to=p, mean=p, device_flags=None, stream=None)
+    for bad in (dict(bt_cols=0), dict(bt_cols=9), dict(bt_cols=-1), dict(bt_stride=0, bt_cols=0), dict(mean=None)):
+        assert B.mla_blocks_mean_cols(**(mean | bad)) == B.MLA_EINVAL
+    assert B.mla_attn_decode_cols(None, 1, p, 0, 0, p, 0, 0, None, p, 4, 64, 0, p, p, 4, 2, 1, None, p, None, 0, 0, None,
+                                  0.1, p, 0, 0, None, None) == B.MLA_EINVAL
