@@ -6,6 +6,7 @@ one ``mla_query_decode`` call into the CUDA library.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import numpy as np
@@ -204,6 +205,19 @@ def blocks_select(scores, lens, page_size, keep_first, keep_last, sel, sel_count
         _refuse(wrong, "mla_blocks_select")
 
 
+def _allocating_on(stream, device):
+    """A context whose allocations belong to the stream that a call is given, in any of its
+    forms: memory of another stream may still be in use there, or be handed out there again,
+    while this call's kernels run."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = getattr(stream, "cuda_stream", stream)
+        if not isinstance(handle, int):  # None: the current one (anything else is refused by the call)
+            return contextlib.nullcontext()
+        # (0 and 1: the legacy default stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle > 1 else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 class PagedAttention:
     """Latent attention over the paged cache, with its workspace.
 
@@ -224,11 +238,13 @@ class PagedAttention:
 
         ``q_latent`` [tokens, heads, 512] and ``q_pe`` [tokens, heads, 64] may
         be strided (views of gathered rows), and so may ``block_table`` and
-        ``sel`` (the first columns of wider tables: only those count); ``out`` BF16 [tokens, heads, 512]
-        is allocated where it is not given, ``lse`` FP32 [tokens, heads] is
+        ``sel`` (the first columns of wider tables: only those count).
+        ``out`` BF16 [tokens, heads, 512] is allocated, as memory of the
+        call's stream, where it is not given; ``lse`` FP32 [tokens, heads] is
         written where it is."""
-        if out is None:
-            out = torch.empty((*q_latent.shape[:2], 512), dtype=torch.bfloat16, device=q_latent.device)
+        if out is None and isinstance(q_latent, torch.Tensor) and q_latent.is_cuda:
+            with _allocating_on(stream, q_latent.device):
+                out = torch.empty((*q_latent.shape[:2], 512), dtype=torch.bfloat16, device=q_latent.device)
         wrong = (_calls or _native()).attn_decode(
             self.handle, self.heads, q_latent, q_pe, cache, layout, block_table, lens, softmax_scale, k_scale,
             q_scale_inv, token_row, sel, sel_count, out, lse, stream)

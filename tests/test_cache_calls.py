@@ -84,3 +84,12 @@ def test_columns_of_wider_tables():
         assert B.mla_blocks_mean_cols(**(mean | bad)) == B.MLA_EINVAL
     assert B.mla_attn_decode_cols(None, 1, p, 0, 0, p, 0, 0, None, p, 4, 64, 0, p, p, 4, 2, 1, None, p, None, 0, 0, None,
                                   0.1, p, 0, 0, None, None) == B.MLA_EINVAL
+
+
+def test_attention_without_an_output_refuses_what_is_no_query():
+    attn = R.PagedAttention.__new__(R.PagedAttention)
+    attn.handle, attn.heads = None, 4
+    for q in (None, 3, torch.zeros(3, 4, 512, dtype=BF16)):
+        with pytest.raises(B.MlaError):
+            attn.decode(q, torch.zeros(3, 4, 64, dtype=BF16), torch.zeros(9, 16, 576, dtype=torch.uint8), 0,
+                        torch.zeros(3, 8, dtype=I32), torch.ones(3, dtype=I32), 0.1, k_scale=torch.ones(1))

@@ -76,3 +76,36 @@ def test_blocks_mean_over_columns_of_a_wider_table(layout):
                 k = keys64(cache, k_scale, layout, [(p, o) for o in range(fill)])
                 want[p], slack[p] = k.mean(0), (page + 2) * 2.0 ** -24 * np.abs(k).mean(0)
     assert (np.abs(got - want) <= slack + 2.0 ** -8 * np.abs(want) + 1e-30).all()
+
+
+@pytest.mark.parametrize("form", ["stream", "handle", "default"])
+def test_attention_output_belongs_to_the_calls_stream(form):
+    """An output that the call allocates is memory of the stream that it runs on: not a block that the
+    current stream has given back, whose work there may not be done."""
+    rng = np.random.default_rng(220)
+    cache, k_scale = C.make_cache(rng, 8, 64, 0)
+    table = C.make_table(rng, [400, 30], 64, 8)
+    ql, qp, _, q64 = queries(rng, 2, 64)
+    args = (ql, qp, dev(cache), 0, dev(table), i32([400, 30]), SCALE)
+    lse, scale = torch.empty(2, 64, device="cuda"), dev(k_scale)
+    attn = R.PagedAttention(2, 64)
+    other, current = torch.cuda.Stream(), torch.cuda.Stream()
+    given = {"stream": other, "handle": other.cuda_stream, "default": 0}[form]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(current):
+        free = torch.empty(2, 64, 512, dtype=torch.bfloat16, device="cuda")  # given back to the current stream
+        at = free.data_ptr()
+        del free
+        out, _ = attn.decode(*args, k_scale=scale, lse=lse, stream=given)
+        assert out.data_ptr() != at
+        again = torch.empty(2, 64, 512, dtype=torch.bfloat16, device="cuda")
+        assert again.data_ptr() == at
+    torch.cuda.synchronize()
+    assert attn.error_flags() == 0
+    for t, n in enumerate((400, 30)):
+        where = C.positions(n, 64, table.shape[1], 8, table[t])
+        check_attention(out[t], lse[t], q64[t], keys64(cache, k_scale, 0, where), SCALE, (t, form))
+    with torch.cuda.stream(current):  # without one, the current stream's
+        assert attn.decode(*args, k_scale=scale, lse=lse)[0].data_ptr() not in (at, out.data_ptr())
+    torch.cuda.synchronize()
+    attn.close()
