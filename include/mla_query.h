@@ -507,11 +507,22 @@ MLA_API int mla_attn_create(mla_attn_t* out, int max_batch, int heads);
  * token_row outside the table counts as no position and raises
  * MLA_DEVERR_BAD_SLOT, as do lengths beyond the row.
  * Sums, maxima and denominators are FP32.  The weights p meet the values with
- * a relative error of at most 2^-7 (2^-11 for nvfp4_ds_mla rows); with
- * fp8_ds_mla rows, whose scales are positive, this holds for rows whose scale
- * is at least 2^-14 of the largest scale that the same 128 columns have in the
- * context.  A NaN or an infinity in a head's query, or a NaN in a row that
- * counts, makes the head's results NaN.
+ * fewer bits, off by at most
+ *   2^-7 of a weight that is at least 2^-10 of the head's largest, and 2^-17 of
+ *   the largest for smaller ones (E4M3 rows, fp8_ds_mla rows);
+ *   2^-11 of a weight, or 2^-30 of the largest (nvfp4_ds_mla rows).
+ * Those small weights are rounded up or down by their row's place, so that many
+ * that are alike keep their sum: 128 neighbouring ones to 2^-8 of it, or to
+ * 2^-20 of the largest weight.  Where rows have scales of their own (a page's,
+ * or fp8_ds_mla's for 128 columns; positive), all this is said of a weight
+ * times its row's scale, against the largest weight times the largest scale
+ * that the same columns have in the context, and for fp8_ds_mla with 2^-6.5 in
+ * place of 2^-7 (the product is formed in FP16).  A query element of BF16 that
+ * is below 2^-10 of its head's largest may be off by 2^-17 of that largest
+ * (2^-33 for nvfp4_ds_mla rows); with fp8_ds_mla rows the largest is that of
+ * the latent elements, and rope elements are exact.
+ * A NaN or an infinity in a head's query, or a NaN in a row that counts, makes
+ * the head's results NaN.
  * Results do not depend on the order in which the GPU runs the work.  Calls
  * sharing a handle, captured or not, must be ordered on one stream: they share
  * its workspace.  Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.

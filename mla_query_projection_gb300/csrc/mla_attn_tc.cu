@@ -13,10 +13,10 @@
 //    then the lo rows, one MMA forms both halves, and the softmax adds them.
 //  * O^T += V^T P^T (M = 128 latent columns, N = heads, K = 128 rows): A is the
 //    same plane read transposed (M-major), so no value is moved or converted.
-//    P is the sum of an E4M3 and an E5M2 term (4 + 3 bits: 2^-7 of each
-//    weight), two MMAs into one accumulator.  The second term in E5M2 keeps
-//    weights down to 2^-21 of the largest: a context with one dominant key and
-//    thousands of small ones needs their sum.
+//    P is the sum of an E4M3 and an E5M2 term, two MMAs into one accumulator:
+//    4 + 3 bits, 2^-7 of a weight, down to 2^-10 of the largest; below, 2^-17 of
+//    the largest, rounded so that thousands of alike small weights beside a
+//    dominant one keep their sum (split_weights).
 //
 // Tokens lie on TMEM lanes in S^T: a softmax thread owns one cache row and
 // half the heads, so a row's scale, mask and page are its scalars, and the
@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (; x < seg_end; ++x, ++i) {
         const int b = i & 1;
         const bool valid = crow >= 0;
+        const uint32_t dither = weight_dither(pos, x - k.start);
         tc_wait(&s_full[b], (uint32_t)((i >> 1) & 1), dead, gave_up);
         tc_after();
         float s[kHalf];
@@ -374,9 +375,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               p0 = fmul2_rn(p0, make_float2(vs, vs));
               p1 = fmul2_rn(p1, make_float2(vs, vs));
             }
-            const uint32_t w0 = split_weights(p0.x, p0.y), w1 = split_weights(p1.x, p1.y);
-            phi[h / 4] = __byte_perm(w0, w1, 0x5410);
-            plo[h / 4] = __byte_perm(w0, w1, 0x7632);
+            const uint32_t w0 = f16x2_of(p0.x, p0.y), w1 = f16x2_of(p1.x, p1.y);
+            split_weights(w0, w1, weight_round(w0, kSmallWeight16, dither), weight_round(w1, kSmallWeight16, dither),
+                          &phi[h / 4], &plo[h / 4]);
           }
         };
         exponents();

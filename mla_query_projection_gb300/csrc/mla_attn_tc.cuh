@@ -193,37 +193,64 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// A weight pair as the sum of two terms: E4M3 codes in the low half of the
-// result, E5M2 codes of the rest in the high half.  The pair is rounded to
-// FP16 first (2^-11, below the terms' 2^-7; FP16 reaches down to 2^-24, further
-// than E5M2).
-__device__ __forceinline__ uint32_t split_weights(float lo, float hi) {
-  uint32_t r;
-  asm("{\n\t.reg .b32 p, g, d;\n\t.reg .b16 c, e;\n\t"
-      "cvt.rn.f16x2.f32 p, %2, %1;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 c, p;\n\t"
-      "cvt.rn.f16x2.e4m3x2 g, c;\n\t"
-      "sub.rn.f16x2 d, p, g;\n\t"
-      "cvt.rn.satfinite.e5m2x2.f16x2 e, d;\n\t"
-      "mov.b32 %0, {c, e};\n\t}"
-      : "=r"(r)
-      : "f"(lo), "f"(hi));
-  return r;
+// Four weights as the sum of two terms, E4M3 codes and E5M2 codes of the rest;
+// they come as FP16 pairs (2^-11, below the terms' own errors; FP16 reaches down
+// to 2^-24, further than E5M2).
+//
+// An E5M2 code is the upper byte of an FP16 value, so the rest is rounded by an
+// addition to its bits: half a step (0x80) for weights of 2^-5 or more, which
+// keeps 2^-8 of them.  E4M3's steps of 2^-9 hold smaller ones badly and from
+// 2^-10 down not at all: a bare E5M2 value has three bits, and a context may
+// have thousands of such weights, all alike, beside a large one.  Rounded to
+// nearest they are off by the same 2^-3 of themselves, and their sum is too
+// (65,535 of 2^-16 beside a weight of 1: 10 % of it; below 2^-22 nothing was
+// left).  So these are rounded up or down by the place of their row: the 128
+// rows of a tile have the 128 odd ones of a step's 256 thresholds, in
+// bit-reversed order, and the sum of alike weights is off by a step in a tile.
+// One weight is then off by up to a step of its rest: at most 2^-13, 2^-18 of
+// the largest weight (which is 2^5 or more).  The choice costs two instructions
+// a pair (8 tokens of 16,384 E4M3 rows, 128 heads: 43.4 us, so 43.9), and the
+// rest's conversion is one less.
+//
+// weight_dither: the threshold of row `pos` of a token's tile n, for a pair.
+// (Tiles differ in which rows have the low ones, so that values that alternate
+// from row to row meet no rounding that does too.)
+__device__ __forceinline__ uint32_t weight_dither(int pos, uint32_t n) {
+  return 0x00010001u * (2u * ((__brev((uint32_t)pos) ^ (n * 0x9E3779B1u)) >> 25) + 1u);
 }
-
-// The same of an FP16 pair times an FP16 pair of factors.
-__device__ __forceinline__ uint32_t split_weights16(uint32_t p, uint32_t f) {
-  uint32_t r;
-  asm("{\n\t.reg .b32 q, g, d;\n\t.reg .b16 c, e;\n\t"
-      "mul.rn.f16x2 q, %1, %2;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 c, q;\n\t"
-      "cvt.rn.f16x2.e4m3x2 g, c;\n\t"
-      "sub.rn.f16x2 d, q, g;\n\t"
-      "cvt.rn.satfinite.e5m2x2.f16x2 e, d;\n\t"
-      "mov.b32 %0, {c, e};\n\t}"
-      : "=r"(r)
-      : "r"(p), "r"(f));
-  return r;
+// What a pair's rests are rounded by: the threshold for weights below `limit`.
+// (A NaN is not below it, and half a step does not carry out of its half.)
+__device__ __forceinline__ uint32_t weight_round(uint32_t w, uint32_t limit, uint32_t dither) {
+  uint32_t small;
+  asm("set.lt.u32.f16x2 %0, %1, %2;" : "=r"(small) : "r"(w), "r"(limit));
+  return (small & dither) | (~small & 0x00800080u);
+}
+constexpr float kSmallWeight = 0.03125f;       // 2^-5
+constexpr uint32_t kSmallWeight16 = 0x28002800u;  // the same as an FP16 pair
+__device__ __forceinline__ void split_weights(uint32_t w0, uint32_t w1, uint32_t round0, uint32_t round1,
+                                              uint32_t* hi, uint32_t* lo) {
+  uint32_t d0, d1;
+  asm("{\n\t.reg .b32 g;\n\t.reg .b16 c0, c1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 c0, %3;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 c1, %4;\n\t"
+      "cvt.rn.f16x2.e4m3x2 g, c0;\n\t"
+      "sub.rn.f16x2 %1, %3, g;\n\t"
+      "cvt.rn.f16x2.e4m3x2 g, c1;\n\t"
+      "sub.rn.f16x2 %2, %4, g;\n\t"
+      "mov.b32 %0, {c0, c1};\n\t}"
+      : "=&r"(*hi), "=&r"(d0), "=&r"(d1)
+      : "r"(w0), "r"(w1));
+  *lo = __byte_perm(d0 + round0, d1 + round1, 0x7531);
+}
+__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
+  uint32_t p;
+  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(p) : "f"(lo), "f"(hi));
+  return p;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t p;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(p) : "r"(a), "r"(b));
+  return p;
 }
 
 struct OpMax {

@@ -109,3 +109,74 @@ def test_attention_output_belongs_to_the_calls_stream(form):
         assert attn.decode(*args, k_scale=scale, lse=lse)[0].data_ptr() not in (at, out.data_ptr())
     torch.cuda.synchronize()
     attn.close()
+
+
+@pytest.mark.parametrize("layout,down", [(0, 0), (1, 0), (2, 0), (3, 0), (1, 8), (3, 8)])
+def test_attention_keeps_the_sum_of_many_small_weights(layout, down):
+    """One key beside 65,535 alike ones whose weights are 2^-11 to 2^-26 of its own (a range over the heads),
+    in contexts that a worker reads whole; or weights 2^down times as large on rows of scales that much smaller.
+
+    With w = 32 p a small weight as the kernel holds it (p of the large one), FP16 is off by 2^-11 w or
+    2^-25, and the second term by a step of at most 2^-2 w, 2^-13 and at least 2^-16, once in 128 rows:
+    they have the thresholds of that many parts of a step.  The large weight keeps 2^-7, the output 2^-8."""
+    rng = np.random.default_rng(230 + layout)
+    n, heads, tokens, page = 65536, 64, 152, 64
+    pages = n // page
+    row = np.zeros((n, C.ROW_BYTES[layout]), dtype=np.uint8)
+    # latent values: one row for all, another for the sink; column 0 is zero
+    code = lambda: (rng.integers(0, 2, 512) << 7 | rng.integers(4, 9, 512) << 3 | rng.integers(0, 8, 512)).astype(np.uint8)
+    k_scale = np.full(pages if layout == 3 else 1, 0.125, dtype=np.float32)
+    ratio = 2.0 ** -down
+    for at, v in ((slice(None), 0.0), (5, 32.0)):
+        if layout == 2:
+            row[at, :256] = rng.integers(0, 256, 256)
+            row[at, 0] &= 0xF0
+            row[at, 256:288] = 7 << 3
+            row[at, 288] = int(torch.tensor([v]).to(torch.float8_e4m3fn).view(torch.uint8))
+        else:
+            row[at, :512] = code()
+            row[at, 0] = 0
+            if layout == 1:
+                row[at, 512:528] = np.full(4, 0.125 * (1.0 if v else ratio), dtype=np.float32).view(np.uint8)
+                row[at, 528:530] = torch.tensor([v]).to(torch.bfloat16).view(torch.uint8).numpy()
+            else:
+                row[at, 512] = int(torch.tensor([v / 0.125]).to(torch.float8_e4m3fn).view(torch.uint8))
+    cache = row.reshape(pages, page, -1)
+    table = rng.permutation(pages).astype(np.int32)[None]
+    if layout == 3:  # the sink's page keeps its scale
+        k_scale[table[0, 1:]] *= np.float32(ratio)
+    stored = np.empty_like(cache)
+    stored[table[0]] = cache
+    # logits: rope column 0 alone, 32 against 0; head h's small weights are 2^-bits[h]
+    bits = np.linspace(11.0, 26.0, heads) - down
+    ql, qp = torch.zeros(1, heads, 512, dtype=torch.bfloat16), torch.zeros(1, heads, 64, dtype=torch.bfloat16)
+    ql[:, :, 0] = 1.0
+    qp[0, :, 0] = torch.from_numpy(bits * np.log(2.0) / (SCALE * 32.0)).to(torch.bfloat16)
+    q64 = torch.cat([ql, qp], 2).double().numpy()[0]
+    keys = C.rows64(row[[100, 5]], layout, [0.125 * (ratio if layout == 3 else 1.0), 0.125])
+    x = (q64 @ keys.T) * SCALE
+    p = np.exp(x[:, 0] - x[:, 1])[:, None]
+    total = 1.0 + (n - 1) * p
+    count = n - 1.0  # of the small rows, in values of the ordinary one (those of the sink's page are larger)
+    if layout == 3:
+        count += (page - 1) * (1.0 / ratio - 1.0)
+    want = (count * p * keys[0, :512] + keys[1, :512]) / total
+    mass = (count * p * np.abs(keys[0, :512]) + np.abs(keys[1, :512])) / total
+    attn = R.PagedAttention(tokens, heads)
+    out, _ = attn.decode(ql.cuda().repeat(tokens, 1, 1), qp.cuda().repeat(tokens, 1, 1), dev(stored), layout, dev(table),
+                         torch.full((tokens,), n, dtype=torch.int32, device="cuda"), SCALE, k_scale=dev(k_scale),
+                         token_row=torch.zeros(tokens, dtype=torch.int32, device="cuda"))
+    assert attn.error_flags() == 0
+    attn.close()
+    w = 32.0 * p * ratio
+    each = 2.0 ** -11 * w + 2.0 ** -25
+    if layout != 2:
+        each = each + np.maximum(np.minimum(2.0 ** -2 * w, 2.0 ** -13), 2.0 ** -16) / 128
+    each = n * each
+    if down and layout == 3:  # the sink's page, each of its rows for itself
+        each = each + page * (2.0 ** -13 + 2.0 ** -7 * w / ratio)
+    slack = (2.0 ** -14.8 + 2.0 ** -17.8) * np.abs(x).max(1)[:, None] + (n / 256 + 16) * 2.0 ** -24
+    bound = (each / 32.0 * np.abs(keys[0, :512]) / ratio + 2.0 ** -7 * np.abs(keys[1, :512])) / total \
+        + 2 * slack * mass + 2.0 ** -8 * np.abs(want)
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert (err <= bound).all(), (err.max(), (err / bound).max(), bits[np.argmax((err / bound).max((0, 2)))])
