@@ -169,6 +169,9 @@ __device__ __forceinline__ void nv_queries(const AttnArgs& a, uint8_t* sq, int t
       ex = max(-100, min(ex, 126));
       up = __uint_as_float((uint32_t)(127 + 8 - ex) << 23);
       x = logit * __uint_as_float((uint32_t)(127 - 8 + ex) << 23);
+      // an infinite query: no finite logits (the products alone would give -infinity
+      // for rows of one sign, and a context of those would look empty)
+      if (m >= 0x7F80u) x = __int_as_float(0x7FC00000);
     }
     put(lane >> 2, warp + 8 * r, lat[r], up);
     if (lane == 0) xs[warp + 8 * r] = x;

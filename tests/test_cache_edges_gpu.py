@@ -180,3 +180,39 @@ def test_attention_keeps_the_sum_of_many_small_weights(layout, down):
         + 2 * slack * mass + 2.0 ** -8 * np.abs(want)
     err = np.abs(out.double().cpu().numpy() - want)
     assert (err <= bound).all(), (err.max(), (err / bound).max(), bits[np.argmax((err / bound).max((0, 2)))])
+
+
+@pytest.mark.parametrize("layout", [0, 1, 2, 3])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("column", [0, 131, 511, 512, 575])
+def test_attention_of_a_query_that_is_not_finite(layout, value, column):
+    """It makes its head's results NaN, whatever the sign of the keys in its column, and no other's."""
+    rng = np.random.default_rng(240 + column)
+    heads, page = 33, 16
+    cache, k_scale = C.make_cache(rng, 8, page, layout)
+    where = [(p, o) for p in range(8) for o in range(page)]
+    k = keys64(cache, k_scale, layout, where)[:, column]
+    order = [int(np.argmax(k)), int(np.argmin(k))]  # a row of either sign in that column
+    assert k[order[0]] > 0 > k[order[1]]
+    # one request for each sign, of that row alone; one with all rows
+    first = cache.reshape(128, -1)[order].copy()
+    cache[6, 0], cache[7, 0] = first
+    if layout == 3:
+        k_scale[6], k_scale[7] = k_scale[[where[order[0]][0], where[order[1]][0]]]
+    table = i32([[6, 0], [7, 0], [0, 1]])
+    lens = i32([1, 1, 2 * page])
+    ql, qp, _, _ = queries(rng, 3, heads)
+    for t in range(3):
+        if column < 512:
+            ql[t, 17, column] = value
+        else:
+            qp[t, 17, column - 512] = value
+    lse = torch.zeros(3, heads, device="cuda")
+    attn = R.PagedAttention(3, heads)
+    out, _ = attn.decode(ql, qp, dev(cache), layout, table, lens, SCALE, k_scale=dev(k_scale), lse=lse)
+    assert attn.error_flags() == 0
+    attn.close()
+    others = [h for h in range(heads) if h != 17]
+    for t in range(3):
+        assert out[t, 17].isnan().all() and lse[t, 17].isnan(), t
+        assert out[t, others].isfinite().all() and lse[t, others].isfinite().all(), t
