@@ -554,13 +554,19 @@ __device__ __forceinline__ void tc_queries(const AttnArgs& a, uint8_t* sq, uint8
       *lo = make_uint4(d[0], d[1], d[2], d[3]);
     };
     const uint32_t rope_mag = __vmaxu2(magnitude(rope[0]), magnitude(rope[kV - 1]));
-    // (BF16 rope values need no power of two, but an infinity or a NaN has to be met)
-    const bool rope_odd = max(rope_mag & 0xFFFFu, rope_mag >> 16) >= 0x7F80u;
+    // BF16 rope values need no power of two: what they ask for is an exponent that
+    // keeps their products in FP32's range where the latent part is far smaller
+    // (or zero), 2^60 below their own.  An infinity or a NaN counts as it is.
+    uint32_t rope_bits = rope_mag;
+    if constexpr (ROPE16) {
+      rope_bits = max(rope_mag & 0xFFFFu, rope_mag >> 16);
+      if (rope_bits < 0x7F80u) rope_bits = max(rope_bits, 60u << 7) - (60u << 7);
+    }
     float rope_up = 0.f;
 #pragma unroll
     for (int r = 0; r < kN; ++r) {
       uint32_t m = __vmaxu2(magnitude(lat[r][0]), magnitude(lat[r][kV - 1]));
-      if (rr == r && (!ROPE16 || rope_odd)) m = __vmaxu2(m, rope_mag);
+      if (rr == r) m = __vmaxu2(m, rope_bits);
       m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
       // the power of two that brings the largest into (224, 448]: from its
       // exponent field, kept where both it and its inverse are normal

@@ -216,3 +216,28 @@ def test_attention_of_a_query_that_is_not_finite(layout, value, column):
     for t in range(3):
         assert out[t, 17].isnan().all() and lse[t, 17].isnan(), t
         assert out[t, others].isfinite().all() and lse[t, others].isfinite().all(), t
+
+
+@pytest.mark.parametrize("layout", [0, 1, 2, 3])
+@pytest.mark.parametrize("latent", [0.0, 2.0 ** -40, 2.0 ** -12])
+def test_attention_of_queries_whose_rope_part_is_far_larger(layout, latent):
+    """Latent queries of zero, or far below the rope part: no product leaves FP32's range."""
+    rng = np.random.default_rng(250)
+    heads, page, n = 20, 16, 300
+    pages = -(-n // page)
+    cache, k_scale = C.make_cache(rng, pages, page, layout)
+    if layout == 1:
+        pe = torch.from_numpy(rng.standard_normal((pages, page, 64), dtype=np.float32) * 3000.0).to(torch.bfloat16)
+        cache[:, :, 528:] = pe.view(torch.uint8).numpy().reshape(pages, page, 128)
+    table = C.make_table(rng, [n], page, pages)
+    ql, qp, _, _ = queries(rng, 1, heads)
+    ql, qp = (ql.float() * latent).to(torch.bfloat16), (qp.float() * 3000.0).to(torch.bfloat16)
+    q64 = torch.cat([ql, qp], 2).double().cpu().numpy()
+    where = C.positions(n, page, table.shape[1], pages, table[0])
+    keys = keys64(cache, k_scale, layout, where)
+    scale = float(np.float32(1.0 / np.abs(q64[0] @ keys.T).mean()))
+    lse = torch.empty(1, heads, device="cuda")
+    attn = R.PagedAttention(1, heads)
+    out, _ = attn.decode(ql, qp, dev(cache), layout, dev(table), i32([n]), scale, k_scale=dev(k_scale), lse=lse)
+    attn.close()
+    check_attention(out[0], lse[0], q64[0], keys, scale, (layout, latent))
