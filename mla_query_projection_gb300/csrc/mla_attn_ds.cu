@@ -395,6 +395,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool move = valid && (!started || over > kPShift + kPRoom || sc[0] > vr.x || sc[1] > vr.y ||
                               sc[2] > vr.z || sc[3] > vr.w);
         move = __any_sync(0xFFFFFFFFu, move);
+        __syncwarp();  // (what a lane has said by gave_up goes before the arrival)
         if (lane == 0) {
           if (move) *reinterpret_cast<volatile uint32_t*>(&moved[b]) = (uint32_t)i + 1;
           mbar_arrive(voted);
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // (the weights as if nothing moved, while the warps' answers meet)
 #pragma unroll
         for (int h = 0; h < kHalf; ++h) p[h] = ex2(p[h]);
-        tc_wait(voted, (uint32_t)(i & 1), dead, gave_up);
+        tc_wait_votes(voted, (uint32_t)(i & 1), dead, gave_up);
         if (*reinterpret_cast<volatile uint32_t*>(&moved[b]) == (uint32_t)i + 1 &&
             *reinterpret_cast<volatile uint32_t*>(gave_up) == 0u) {
           // the reference moves to the tile's maximum where that passes it by

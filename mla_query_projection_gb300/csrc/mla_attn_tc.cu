@@ -395,12 +395,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // Does the reference have to move?  The warps' answers meet while the
         // weights are computed as if not (unless there is no reference yet).
         const bool move = __any_sync(0xFFFFFFFFu, valid && (first_rows || over + up > kPShift + kPRoom));
+        __syncwarp();  // (what a lane has said by gave_up goes before the arrival)
         if (lane == 0) {
           if (move) *reinterpret_cast<volatile uint32_t*>(&moved[b]) = (uint32_t)i + 1;
           mbar_arrive(voted);
         }
         if (started) weights();
-        tc_wait(voted, (uint32_t)(i & 1), dead, gave_up);
+        tc_wait_votes(voted, (uint32_t)(i & 1), dead, gave_up);
         if (*reinterpret_cast<volatile uint32_t*>(&moved[b]) == (uint32_t)i + 1 &&
             *reinterpret_cast<volatile uint32_t*>(gave_up) == 0u) {
           // the reference moves to the tile's maximum where that passes it by

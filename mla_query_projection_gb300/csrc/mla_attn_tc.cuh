@@ -6,6 +6,7 @@
 #include <cudaTypedefs.h>
 
 #include "mla_attn.cuh"
+#include "mla_wait.h"
 
 namespace mla {
 namespace {
@@ -304,6 +305,19 @@ __device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, bool& de
 // The same, and says so to the other softmax threads.
 __device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, bool& dead, uint32_t* gave_up) {
   if (!dead && !mbar_wait_bounded(bar, parity, kTcWait)) {
+    dead = true;
+    *reinterpret_cast<volatile uint32_t*>(gave_up) = 1u;
+  }
+}
+
+// The wait for the softmax warps' votes.  A warp's waits before its vote are
+// bounded, and it votes whether they ran out or not, so every vote comes; what
+// must not happen is that one thread gives this wait up and another, a poll
+// later, does not: the threads that saw the vote alike go through barriers
+// together.  Hence more time than the other waits have, and polls beyond it.
+__device__ __forceinline__ void tc_wait_votes(uint64_t* bar, uint32_t parity, bool& dead, uint32_t* gave_up) {
+  if (!dead && !wait_for_all([&] { return mbar_try_wait(bar, parity); }, [] { return clock64(); }, 4 * kTcWait,
+                             1u << 20)) {
     dead = true;
     *reinterpret_cast<volatile uint32_t*>(gave_up) = 1u;
   }
