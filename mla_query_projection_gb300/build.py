@@ -5,7 +5,8 @@ shared library next to this file.  The CUDA runtime is linked statically, so
 the library loads on a machine without a GPU (every call then returns
 MLA_ECUDA).  ``csrc/torch/tensor_calls.cpp``, the module through which torch
 tensors reach the cache-side operators, is compiled by the host compiler into
-``_tensor_calls.so`` beside it.  Usage: ``python -m mla_query_projection_gb300.build``.
+``_tensor_calls.so`` beside it (where that fails, the library is built all the
+same, and the failure raised).  Usage: ``python -m mla_query_projection_gb300.build``.
 """
 
 from __future__ import annotations
@@ -58,7 +59,10 @@ def _compile(src: str, build_dir: str = BUILD, extra: tuple = ()) -> tuple[str, 
 
 
 def _compile_calls() -> None:
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch is not installed: _tensor_calls.so, which it needs, is not built")
+    torch = os.path.dirname(spec.origin)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     include = [os.path.join(torch, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     tmp = CALLS + ".tmp"
@@ -83,8 +87,6 @@ def build(verbose: bool = False, out_dir: str | None = None, extra: tuple = ()) 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
         calls = ex.submit(_compile_calls) if out_dir is None else None
         results = list(ex.map(lambda src: _compile(src, build_dir, tuple(extra)), srcs))
-        if calls is not None:
-            calls.result()
     objs = [o for o, _ in results]
     if verbose:
         for _, log in results:
@@ -98,6 +100,8 @@ def build(verbose: bool = False, out_dir: str | None = None, extra: tuple = ()) 
     with open(os.path.join(build_dir, "ptxas.log"), "w") as f:
         for _, log in results:
             f.write(log)
+    if calls is not None:
+        calls.result()  # (a failure is raised here: the C library stands without the module)
     return lib
 
 
