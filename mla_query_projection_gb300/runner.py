@@ -73,7 +73,8 @@ class DecodeStep:
         self.slots = torch.from_numpy(np.asarray(inp["slots"], dtype=np.int64)).to(dev)
         self.cache = torch.from_numpy(np.ascontiguousarray(inp["cache"])).to(dev)
         self.num_pages, self.page_size = int(self.cache.shape[0]), int(self.cache.shape[1])
-        self.k_scale = torch.tensor([inp["k_scale"]], dtype=torch.float32, device=dev)
+        # one scale, or one for each page (MLA_KV_FP8_E4M3_PAGE)
+        self.k_scale = torch.tensor(np.atleast_1d(inp["k_scale"]), dtype=torch.float32, device=dev)
         self.eps = float(inp["eps"])
         self.q_latent = torch.empty((Bn, H, 512), dtype=torch.bfloat16, device=dev)
         self.q_pe = torch.empty((Bn, H, 64), dtype=torch.bfloat16, device=dev)
@@ -81,6 +82,9 @@ class DecodeStep:
         self.handle = B.mla_query_create(H, self.w_qb, self.w_uk, self.gamma_q, self.gamma_kv, self.eps)
 
     def decode(self, stream=None, batch=None) -> int:
+        if self.layout == B.MLA_KV_FP8_E4M3_PAGE and (
+                self.k_scale.numel() < self.num_pages or not self.k_scale.is_contiguous()):
+            return B.MLA_EINVAL  # the kernel would read behind the scales
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
         if self.qkv_a is not None:
             rc = B.mla_qkv_a_run(self.qkv_a, self.batch if batch is None else batch, self.hidden, 0,

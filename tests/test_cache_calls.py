@@ -93,3 +93,23 @@ def test_attention_without_an_output_refuses_what_is_no_query():
         with pytest.raises(B.MlaError):
             attn.decode(q, torch.zeros(3, 4, 64, dtype=BF16), torch.zeros(9, 16, 576, dtype=torch.uint8), 0,
                         torch.zeros(3, 8, dtype=I32), torch.ones(3, dtype=I32), 0.1, k_scale=torch.ones(1))
+
+
+def test_decode_step_has_a_scale_for_every_page(monkeypatch):
+    """With a scale a page, a step whose scales are fewer than its pages would have the kernel read behind them."""
+    asked = []
+    monkeypatch.setattr(B, "mla_query_decode", lambda *a: asked.append(a) or B.MLA_OK)
+    step = R.DecodeStep.__new__(R.DecodeStep)
+    step.handle = step.qkv_a = None
+    step.batch, step.strides, step.layout = 1, (0, 0, 0), B.MLA_KV_FP8_E4M3_PAGE
+    step.q_a = step.kv_c = step.k_pe = step.slots = step.cache = step.q_latent = step.q_pe = step.q_c = None
+    step.num_pages, step.page_size = 8, 64
+    for few in (torch.ones(1), torch.ones(7)):
+        step.k_scale = few
+        assert step.decode(stream=0) == B.MLA_EINVAL and not asked
+    step.k_scale = torch.ones(16)[::2]  # eight, but not side by side
+    assert step.decode(stream=0) == B.MLA_EINVAL and not asked
+    step.k_scale = torch.ones(8)
+    assert step.decode(stream=0) == B.MLA_OK and len(asked) == 1
+    step.layout, step.k_scale = B.MLA_KV_FP8_E4M3, torch.ones(1)
+    assert step.decode(stream=0) == B.MLA_OK and len(asked) == 2
