@@ -254,7 +254,8 @@ int attn_most_heads(int heads) { return heads <= 16 ? 16 : heads <= 32 ? 32 : 64
 //   32 x 64, 4,096 E4M3 rows          13     33.8  37.5  54.2
 int attn_cta_heads(const AttnArgs& a, int num_sms) {
   const int64_t blocks = a.sel != nullptr ? (a.sel_cols < a.bt_cols ? a.sel_cols : a.bt_cols) : a.bt_cols;
-  const int64_t tiles = a.batch * ((blocks * a.page_size + kAttnTile - 1) / kAttnTile);
+  const int64_t most = blocks * a.page_size;
+  const int64_t tiles = a.batch * (((most < kAttnMaxPositions ? most : kAttnMaxPositions) + kAttnTile - 1) / kAttnTile);
   int n = attn_most_heads(a.heads);
   for (; n > 16; n /= 2) {
     const int64_t all = tiles * ((a.heads + n / 2 - 1) / (n / 2));
@@ -273,6 +274,10 @@ int attn_cta_heads(const AttnArgs& a, int num_sms) {
 //   fp8_ds_mla, 62 tokens of 700 to 4,096, 128    92.7  85.4  81.1  83.6
 //   nvfp4_ds_mla, 32 tokens of 4,096 rows, 64     57.3  54.6  54.3  54.6
 uint32_t attn_lead(const AttnArgs& a) { return row_scaled(a.layout) && a.cta_heads == 64 ? 5u : 3u; }
+
+// Columns that a length or a count of 32 bits can reach: their product with the
+// page size fits 64 bits (a single row's stride may be any number).
+int64_t counted_cols(int64_t cols) { return cols < 0x7FFFFFFF ? cols : 0x7FFFFFFF; }
 
 // Strides of a [batch][heads][width] operand; 0 means contiguous.
 bool fill_strides(int heads, int width, int unit, int64_t* ts, int64_t* hs) {
@@ -388,13 +393,13 @@ int mla_attn_decode_cols(mla_attn_t h, int batch, const void* q_latent, int64_t 
   a.k_scale = k_scale;
   a.table = block_table;
   a.bt_stride = bt_stride;
-  a.bt_cols = bt_cols;
+  a.bt_cols = mla::counted_cols(bt_cols);
   a.table_rows = table_rows;
   a.token_row = token_row;
   a.lens = lens;
   a.sel = sel;
   a.sel_stride = sel_stride;
-  a.sel_cols = sel_cols;
+  a.sel_cols = mla::counted_cols(sel_cols);
   a.sel_count = sel_count;
   a.scale = softmax_scale;
   a.out = static_cast<uint16_t*>(out);
@@ -496,7 +501,7 @@ int mla_blocks_mean_cols(const void* kv_cache, int64_t num_pages, int page_size,
   int sms = 0;
   if (mla::sm_count(&sms) != MLA_OK) return MLA_ECUDA;
   const mla::MeanArgs m{static_cast<const uint8_t*>(kv_cache), num_pages, page_size, layout, k_scale,
-                        block_table, bt_stride, bt_cols, rows, lens_from, lens_to,
+                        block_table, bt_stride, mla::counted_cols(bt_cols), rows, lens_from, lens_to,
                         static_cast<uint16_t*>(mean), device_flags};
   return mla::launched(mla::launch_blocks_mean(m, sms, static_cast<cudaStream_t>(stream)));
 }

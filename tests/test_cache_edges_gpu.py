@@ -241,3 +241,36 @@ def test_attention_of_queries_whose_rope_part_is_far_larger(layout, latent):
     out, _ = attn.decode(ql, qp, dev(cache), layout, dev(table), i32([n]), scale, k_scale=dev(k_scale), lse=lse)
     attn.close()
     check_attention(out[0], lse[0], q64[0], keys, scale, (layout, latent))
+
+
+@pytest.mark.parametrize("stride", [1 << 33, 1 << 57, 1 << 62])
+def test_a_single_row_may_have_any_stride(stride):
+    """One request's table row: its stride leads nowhere, and stride * page_size does not fit 64 bits."""
+    rng = np.random.default_rng(260)
+    page, pages, heads, n = 64, 8, 16, 300
+    cache, k_scale = C.make_cache(rng, pages, page, 0)
+    table = C.make_table(rng, [n], page, pages)
+    ql, qp, _, q64 = queries(rng, 1, heads)
+    out = torch.zeros(1, heads, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(1, heads, device="cuda")
+    mean = torch.full((pages, 576), 9.0, dtype=torch.bfloat16, device="cuda")
+    d = [dev(cache), dev(k_scale), dev(table), i32([n]), i32([0])]
+    attn = R.PagedAttention(1, heads)
+    stream = torch.cuda.current_stream()
+    sel, count = i32([[4, 0]]), i32([2])
+    where = C.positions(n, page, table.shape[1], pages, table[0])
+    for s, sel_stride, c, w in ((None, 0, None, where),
+                                (sel, stride, count, C.positions(n, page, table.shape[1], pages, table[0], [4, 0]))):
+        rc = B.mla_attn_decode(attn.handle, 1, ql, 0, 0, qp, 0, 0, None, d[0], pages, page, 0, d[1], d[2], stride, 1, None,
+                               d[3], s, sel_stride, c, SCALE, out, 0, 0, lse, stream)
+        assert rc == B.MLA_OK and attn.error_flags() == 0
+        check_attention(out[0], lse[0], q64[0], keys64(cache, k_scale, 0, w), SCALE, stride)
+    rc = B.mla_blocks_mean(d[0], pages, page, 0, d[1], d[2], stride, 1, d[4], d[3], mean, None, stream)
+    assert rc == B.MLA_OK
+    torch.cuda.synchronize()
+    got = mean.double().cpu().numpy()
+    for j in range(-(-n // page)):
+        k = keys64(cache, k_scale, 0, [(table[0, j], o) for o in range(min(page, n - j * page))])
+        want, slack = k.mean(0), (page + 2) * 2.0 ** -24 * np.abs(k).mean(0)
+        assert (np.abs(got[table[0, j]] - want) <= slack + 2.0 ** -8 * np.abs(want)).all()
+    attn.close()
