@@ -49,11 +49,11 @@ __device__ __forceinline__ uint32_t attn_positions(const AttnArgs& a, int t, int
   int64_t n = 0;
   if (!bad) {
     const int64_t cap = a.bt_cols * a.page_size;
+    bad = len > cap;
     if (a.sel != nullptr) {
       n = min((int64_t)max(__ldcg(a.sel_count + t), 0), a.sel_cols) * a.page_size;
     } else {
       n = min((int64_t)len, cap);
-      bad = len > cap;
     }
     if (n > kAttnMaxPositions) {
       n = kAttnMaxPositions;

@@ -274,3 +274,23 @@ def test_a_single_row_may_have_any_stride(stride):
         want, slack = k.mean(0), (page + 2) * 2.0 ** -24 * np.abs(k).mean(0)
         assert (np.abs(got[table[0, j]] - want) <= slack + 2.0 ** -8 * np.abs(want)).all()
     attn.close()
+
+
+def test_attention_over_selected_blocks_flags_lengths_beyond_the_row():
+    """As over the whole context: what the row holds is used, and the length flagged."""
+    rng = np.random.default_rng(270)
+    page, pages, heads, width = 16, 20, 16, 4
+    cache, k_scale = C.make_cache(rng, pages, page, 0)
+    table = rng.permutation(pages)[:3 * width].reshape(3, width).astype(np.int32)
+    ql, qp, _, q64 = queries(rng, 3, heads)
+    sel = [[3, 0], [1], []]
+    lse = torch.zeros(3, heads, device="cuda")
+    attn = R.PagedAttention(3, heads)
+    for lens, flags in (([64, 20, 64], 0), ([65, 20, 64], B.MLA_DEVERR_BAD_SLOT), ([64, 20, 1000], B.MLA_DEVERR_BAD_SLOT)):
+        out, _ = attn.decode(ql, qp, dev(cache), 0, dev(table), i32(lens), SCALE, k_scale=dev(k_scale), lse=lse,
+                             sel=i32([[3, 0], [1, -1], [-1, -1]]), sel_count=i32([2, 1, 0]))
+        assert attn.error_flags() == flags, lens
+        for t, n in enumerate(lens):
+            where = C.positions(n, page, width, pages, table[t], sel[t])
+            check_attention(out[t], lse[t], q64[t], keys64(cache, k_scale, 0, where), SCALE, (t, n))
+    attn.close()
