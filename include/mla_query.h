@@ -444,8 +444,9 @@ MLA_API void mla_qkv_a_destroy(mla_qkv_a_t h);
  * A request whose table row cannot hold its new length, or whose length is
  * negative or longer than its table row, is left as it is.  From the first
  * request (in row order) on that finds too few free pages or too little room
- * in the token arrays, no request appends anything.  Both raise
- * MLA_DEVERR_REFUSED.  The arrays must not overlap but for the two pairs
+ * in the token arrays, no request appends anything.  A *free_count outside
+ * 0..num_pages counts as 0, and pages given back beyond the num_pages places
+ * of the stack are dropped.  All of these raise MLA_DEVERR_REFUSED.  The arrays must not overlap but for the two pairs
  * named above.  Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.
  */
 MLA_API int mla_tables_step(int rows, const int32_t* new_tokens, const int32_t* lens,

@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(1024) mla_tables_kernel(const TableArgs t) {
         const bool in_step = toks[i] > 0 && r < stop;
         s.len[r] = len[i];
         s.have[r] = have[i];
-        s.give[r] = !released[i] ? kGiveNone : have[i] > 0 ? (int32_t)f : kGiveNothing;
+        // (a place that 32 bits do not hold lies behind the stack's end)
+        s.give[r] = !released[i] ? kGiveNone : have[i] > 0 ? (int32_t)min(f, (int64_t)0x7FFFFFFF) : kGiveNothing;
         s.take[r] = in_step ? take[i] : 0;
         s.first[r] = (int32_t)min(p, (int64_t)0x7FFFFFFF);
         k += toks[i];
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(1024) mla_tables_kernel(const TableArgs t) {
     for (int r = gw; r < R; r += warps)
       if (s.give[r] >= 0)
         for (int j = lane; j < s.have[r]; j += 32) {
-          const int64_t at = count + s.give[r] + j;
+          const int64_t at = (int64_t)count + s.give[r] + j;
           if (at < t.num_pages) t.free_pages[at] = t.block_table[(int64_t)r * t.bt_stride + j];
         }
   if (refused && rank == 0 && t.flags != nullptr) atomicOr(t.flags, MLA_DEVERR_REFUSED);

@@ -294,3 +294,26 @@ def test_attention_over_selected_blocks_flags_lengths_beyond_the_row():
             where = C.positions(n, page, width, pages, table[t], sel[t])
             check_attention(out[t], lse[t], q64[t], keys64(cache, k_scale, 0, where), SCALE, (t, n))
     attn.close()
+
+
+def test_tables_step_given_back_more_pages_than_32_bits_count():
+    """Requests that end with more pages in all than 2^32 (the same ones many times over): what the stack can
+    hold, in row order, and no entry twice."""
+    rows, page, pages, held = 4096, 1, 10000, (1 << 20) + 257  # those before the last one: 2^32 + 3839
+    table = torch.arange(rows, dtype=torch.int32, device="cuda")[:, None].expand(rows, held).contiguous()
+    lens = torch.full((rows,), held, dtype=torch.int32, device="cuda")
+    new = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    stack = torch.full((pages,), -7, dtype=torch.int32, device="cuda")
+    stack[:5] = torch.arange(9000, 9005)
+    count, flags = i32([5]), i32([0])
+    slots = torch.zeros(3, dtype=torch.int64, device="cuda")
+    token = [torch.zeros(3, dtype=torch.int32, device="cuda") for _ in range(2)]
+    cu = torch.full((rows + 1,), 9, dtype=torch.int32, device="cuda")
+    R.tables_step(new, lens, table, stack, count, page, lens, count, slots, *token, cu, flags)
+    assert int(count.item()) == pages and (lens == 0).all() and (cu == 0).all()
+    assert stack[:5].tolist() == [9000, 9001, 9002, 9003, 9004]
+    assert (stack[5:] == 0).all()  # the first request's, of which there are enough
+    assert int(flags.item()) == B.MLA_DEVERR_REFUSED
+    assert (slots == -1).all() and (token[0] == -1).all() and (token[1] == 0).all()
+    del table
+    torch.cuda.empty_cache()
