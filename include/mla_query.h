@@ -572,7 +572,8 @@ MLA_API void mla_attn_destroy(mla_attn_t h);
  * mla_blocks_mean - the mean key of every block that a step's tokens touched:
  * mean[p][c] = bf16(sum of value c of the page's filled rows / their number),
  * for the pages of blocks lens_from[r] / page_size .. of each request r up to
- * position lens_to[r] (positions from lens_to[r] on are not filled).  Other
+ * position lens_to[r] (positions from lens_to[r] on are not filled; where both
+ * lie in the same partly filled block, that block, also if they are equal).  Other
  * pages' means are left as they are.  A page that several requests of the call
  * hold should be filled alike by them: each of them writes its mean.
  *

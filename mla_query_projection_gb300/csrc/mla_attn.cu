@@ -232,8 +232,8 @@ int launched(cudaError_t e) {
 // padding, and more workers of the same tiles), 64 otherwise.
 int attn_most_heads(int heads) { return heads <= 16 ? 16 : heads <= 32 ? 32 : 64; }
 
-// Heads a CTA takes, by the most tiles that the call's tables or selections can
-// hold (the lengths are known on the GPU only).  With half the heads a CTA has
+// Heads a CTA takes, by the most tiles that the columns of the call's tables or
+// selections can hold (the lengths are known on the GPU only).  With half the heads a CTA has
 // half the queries to load, half the softmax, half the sums to write and join;
 // it has twice the tiles, and each costs more than half (the rows' bytes and,
 // with nvfp4_ds_mla rows, the widening stay).  So: while every CTA still has one
@@ -252,6 +252,17 @@ int attn_most_heads(int heads) { return heads <= 16 ? 16 : heads <= 32 ? 32 : 64
 //   1 x 128, 32,768 nvfp4_ds_mla rows 6.7    31.7  34.3  50.2
 //   4 x 128, 16,384 E4M3 rows         13     34.5  35.2  50.8
 //   32 x 64, 4,096 E4M3 rows          13     33.8  37.5  54.2
+// Between 7 and 13 tiles neither is better throughout (64 and 32 heads a CTA):
+//   2 x 128, 20,480 E4M3 rows         8.4    26.4  27.9
+//   20 x 64, 4,096 E4M3 rows          8.4    31.7  25.3
+//   20 x 64, 4,096 fp8_ds_mla rows    8.4    30.5  34.0
+//   8 x 64, 12,288 E4M3 rows          10     28.6  28.1
+//   2 x 128, 24,576 fp8_ds_mla rows   10     36.9  39.8
+//   2 x 128, 28,672 E4M3 rows         12     35.3  32.1
+// Columns that no request reaches count too: 1 x 64 heads over 512 E4M3 rows
+// take 9.4 us with a table of 8 or 32 blocks, 10.6 with 128 and 10.8 with 1,024;
+// 4 x 64 over 2,000 fp8_ds_mla rows 17.8 with 32 blocks, 21.2 with 512 (and 17.8
+// with the first 32 columns of those 512: mla_attn_decode_cols).
 int attn_cta_heads(const AttnArgs& a, int num_sms) {
   const int64_t blocks = a.sel != nullptr ? (a.sel_cols < a.bt_cols ? a.sel_cols : a.bt_cols) : a.bt_cols;
   const int64_t most = blocks * a.page_size;

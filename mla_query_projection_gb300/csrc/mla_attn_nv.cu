@@ -25,7 +25,7 @@
 // What bounds a tile (64 heads) is that chain: 36 MMAs for S and 32 for O at 48
 // cycles are 3264 cycles, the conversions (8 lanes a cycle) about 1000, the
 // stores of the planes 1150, and they overlap in part.  32 tokens of 4,096 rows,
-// 64 heads: 54 us (the rows' bytes at 6.77 TB/s: 7.5; an mma.sync kernel that
+// 64 heads: 53 us (the rows' bytes at 6.77 TB/s: 7.5; an mma.sync kernel that
 // widened to BF16 in the same way: 149).
 #include "mla_attn_tc.cuh"
 

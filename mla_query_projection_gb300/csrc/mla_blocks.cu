@@ -284,8 +284,9 @@ __global__ void __launch_bounds__(256) mla_blocks_score_kernel(const ScoreArgs s
 // The k blocks with the highest scores, ascending.  A score becomes a 32-bit
 // key that orders like it; the k-th largest key is found by its leading 11,
 // then 11, then 10 bits, each digit from a histogram of the keys that share
-// the bits so far (2,048 bins: enough that the keys of a warp seldom meet in
-// one); then one pass in block order keeps every key above it and, of those
+// the bits so far (2,048 bins: in the two later digits the keys of a warp seldom
+// meet in one; the first is the sign, the exponent and two bits, of which alike
+// scores fill few); then one pass in block order keeps every key above it and, of those
 // equal, the first ones.  All sums are counts, so the result does not depend
 // on the order of the atomics.  Keys stay in registers (up to 16 a thread;
 // beyond 8,192 blocks they are formed again from the scores in each pass).
