@@ -30,7 +30,7 @@
 // Shared-memory reads of the tensor core bound a tile (64 heads: 18 MMAs of
 // 8 KiB for S and 32 of 6 KiB for O at 128 B a cycle, 2700 cycles), next to
 // HBM's share of 73.7 KiB a tile; measured, 3,650 cycles a tile, and 44 us for 8
-// tokens of 16,384 rows at 128 heads (the tensor pipe 40 % active, plan, queries,
+// tokens of 16,384 rows at 128 heads (the tensor pipe 39 % active, plan, queries,
 // first tiles, sums and their joining included).
 #include "mla_attn_tc.cuh"
 
