@@ -633,6 +633,199 @@ MLA_API int mla_blocks_select(int batch, const float* scores, int64_t scores_str
                               int k, int32_t* sel, int64_t sel_stride, int32_t* sel_count,
                               void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The prompt's side of the layer: what a prompt, or a chunk of one, needs before
+ * its requests decode.  The pages define no such calls; they have no counterpart
+ * there.
+ *
+ *   mla_rope_apply     rotary positions of query rows (or of k_pe rows)
+ *   mla_cache_write    norm, rotation and quantisation of many tokens' rows
+ *   mla_cache_read     cached rows as BF16 rows, one request after another
+ *   mla_prompt_attn    attention of packed documents over expanded keys
+ *
+ * A chunk of a prompt goes: mla_tables_step (slots, positions), mla_cache_write,
+ * mla_cache_read where the request has a context in the cache, the caller's
+ * up-projection of the rows to k_nope and v, mla_prompt_attn.  Conventions as
+ * above: asynchronous, no allocation, no host synchronisation, all can be
+ * captured into CUDA graphs (lengths and positions are read on the device).
+ * ------------------------------------------------------------------------- */
+#define MLA_MAX_ROPE_AXES 8            /* axes of positions (time, height, ..) */
+#define MLA_MAX_PROMPT_TOKENS 268435456 /* tokens of one mla_prompt_attn call  */
+#define MLA_MAX_SOFTCAP 1000           /* largest softcap of mla_prompt_attn   */
+
+typedef struct mla_rope* mla_rope_t;
+
+/*
+ * mla_rope_create - a rotation of 64-wide rows in 32 pairs.
+ *
+ *   inv_freq     host double [32]: radians pair p turns for each position, at
+ *                most 1e6 in magnitude (0: the pair is not turned).
+ *   axis         host int32 [32], or NULL for one axis: which axis' position
+ *                turns pair p, 0 .. MLA_MAX_ROPE_AXES - 1.
+ *   interleaved  1: pair p is values 2p and 2p + 1; 0: values p and p + 32.
+ *   scale        finite; multiplies cosine and sine.
+ *
+ * The handle holds host memory only and serves every device and stream.
+ * Returns MLA_OK, MLA_EINVAL or MLA_ENOMEM.
+ */
+MLA_API int mla_rope_create(mla_rope_t* out, const double* inv_freq, const int32_t* axis,
+                            int interleaved, float scale);
+
+/* mla_rope_axes - how many axes of positions the rotation reads (1 + the
+ * largest of `axis`), or MLA_EINVAL. */
+MLA_API int mla_rope_axes(mla_rope_t h);
+
+/* mla_rope_destroy - free the handle (NULL is a no-op); calls under way keep
+ * what they need. */
+MLA_API void mla_rope_destroy(mla_rope_t h);
+
+/*
+ * mla_rope_apply - out[t][h] = x[t][h] with pair p turned by
+ * a = (positions[axis[p]][t] + pos_offset) * inv_freq[p]:
+ *   y0 = scale (x0 cos a - x1 sin a), y1 = scale (x1 cos a + x0 sin a).
+ * Angles are exact to about 2^-24 of a turn for every 32-bit position; products
+ * and sums are FP32, rounded once to BF16.  Negative positions turn back.
+ *
+ *   tokens        >= 0; heads 1..MLA_MAX_ROW_HEADS.
+ *   x, out        device BF16 [tokens][heads][64]: element (t, h, i) at t *
+ *                 token_stride + h * head_stride + i (elements; 0 means
+ *                 contiguous; multiples of 8, 64 at least).  Gathered rows
+ *                 [tokens][q_heads][576] are rows + 512, strides q_heads * 576
+ *                 and 576.  out may be x itself (with its strides), and must
+ *                 overlap it in no other way; its own rows must not overlap.
+ *   positions     device int32 [axes][pos_stride], pos_stride >= tokens (0 means
+ *                 tokens); axes as mla_rope_axes.
+ *   pos_offset    in 32 bits; -1 takes token_len of mla_tables_step as it is.
+ * Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.
+ */
+MLA_API int mla_rope_apply(mla_rope_t h, int64_t tokens, int heads, const void* x,
+                           int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions,
+                           int64_t pos_stride, int64_t pos_offset, void* out,
+                           int64_t out_token_stride, int64_t out_head_stride, void* stream);
+
+/*
+ * mla_cache_write - the cache rows of many tokens: step 5 of mla_query_decode
+ * (the same bytes), for any number of tokens and without the query path.
+ *
+ *   tokens        >= 0.
+ *   kv_c, k_pe    device BF16 [tokens][stride] (first 512 and 64 used; strides
+ *                 as mla_query_decode, multiples of 8).
+ *   gamma_kv      device BF16 [512], or NULL: kv_c is normalised already (and
+ *                 eps is not used; eps >= 0).
+ *   rope, positions, pos_stride, pos_offset  the rotation of k_pe as
+ *                 mla_rope_apply (rounded to BF16 before it is quantised), or
+ *                 both handles NULL: k_pe is written as it is.
+ *   slot_mapping .. k_scale  as mla_query_decode; the slots >= 0 of one call are
+ *                 distinct.
+ *   rows          device BF16 [tokens][rows_stride] (0 means 576; a multiple of
+ *                 8), or NULL: the normalised row and the rotated k_pe, for every
+ *                 token whatever its slot.  May be the input row itself (kv_c =
+ *                 rows, k_pe = rows + 512, all strides alike); overlaps the
+ *                 inputs in no other way.
+ * Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.
+ */
+MLA_API int mla_cache_write(int64_t tokens, const void* kv_c, int64_t kv_c_stride, const void* k_pe,
+                            int64_t k_pe_stride, const void* gamma_kv, float eps, mla_rope_t rope,
+                            const int32_t* positions, int64_t pos_stride, int64_t pos_offset,
+                            const int64_t* slot_mapping, void* kv_cache, int64_t num_pages,
+                            int page_size, int layout, const float* k_scale, void* rows,
+                            int64_t rows_stride, unsigned* device_flags, void* stream);
+
+/*
+ * mla_cache_read - cached rows as BF16 rows of 512 latent and 64 rope values (each
+ * value times its scale, rounded once): rows[i], cu_rows[r] <= i < cu_rows[r + 1],
+ * is position first[r] + i - cu_rows[r] of request r.
+ *
+ *   kv_cache .. k_scale  as mla_query_decode, read only.
+ *   block_table   device int32 [requests][bt_stride], the first bt_cols columns
+ *                 count; requests <= MLA_MAX_TABLE_ROWS.
+ *   cu_rows       device int32 [requests + 1], ascending.
+ *   first         device int32 [requests], or NULL: from position 0.
+ *   rows          device BF16 [max_rows][rows_stride] (0 means 576; a multiple of
+ *                 8); max_rows at most 2^31 - 1.  Rows before cu_rows[0] and from
+ *                 cu_rows[requests] on are left as they are, and rows from
+ *                 max_rows on are not written.
+ * A position outside the table's columns or on an absent page gives zeros and
+ * raises MLA_DEVERR_BAD_SLOT.  Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.
+ */
+MLA_API int mla_cache_read(const void* kv_cache, int64_t num_pages, int page_size, int layout,
+                           const float* k_scale, const int32_t* block_table, int64_t bt_stride,
+                           int64_t bt_cols, int requests, const int32_t* cu_rows,
+                           const int32_t* first, int64_t max_rows, void* rows, int64_t rows_stride,
+                           unsigned* device_flags, void* stream);
+
+typedef struct mla_prompt* mla_prompt_t;
+
+/*
+ * mla_prompt_create - the workspace of prompt attention for `heads` heads
+ * (1..MLA_MAX_ROW_HEADS).  Allocates, on the current device, room for the sums of
+ * query rows whose keys several workers share: 3 * SMs * 256 rows of 128 FP32 (59
+ * MiB on 152 SMs).  Synchronises the legacy default stream; the handle may only be
+ * used on that device.
+ * Returns MLA_OK, MLA_EINVAL, MLA_ENOMEM or MLA_ECUDA.
+ */
+MLA_API int mla_prompt_create(mla_prompt_t* out, int heads);
+
+/*
+ * mla_prompt_attn - attention of packed documents:
+ *   out[i][h] = sum_j p_j v[j][h],  p = softmax_j(x_j),
+ *   x_j = cap(softmax_scale * (q_nope[i][h] . k_nope[j][h] + q_pe[i][h] . k_pe[j]))
+ *         - slopes[h] * |place_i - j|,
+ * with cap(x) = softcap * tanh(x / softcap), over the keys j of row i's own
+ * document that it sees.
+ *
+ *   docs          1..MLA_MAX_TABLE_ROWS.  Document d has query rows cu_q[d] ..
+ *                 cu_q[d + 1] - 1 and keys cu_k[d] .. cu_k[d + 1] - 1 (device
+ *                 int32 [docs + 1], ascending, within q_tokens and k_tokens; what
+ *                 lies beyond is cut off and raises MLA_DEVERR_BAD_SLOT, as does
+ *                 an array that descends, whose rows are then not all written).
+ *                 Its nq query rows are its last ones: row i lies at place i + nk
+ *                 - nq among its nk keys (nk < nq: the first rows lie before all
+ *                 keys).
+ *   causal        0: a row sees all keys of its document.  1: those up to its own
+ *                 place, and the first prefix[d] (device int32 [docs], or NULL:
+ *                 none), which all rows of the document see.
+ *   q_nope, q_pe  device BF16 [q_tokens][heads][128] and [q_tokens][heads][64],
+ *   k_nope, v     device BF16 [k_tokens][heads][128] each,
+ *   k_pe          device BF16 [k_tokens][64], shared by the heads: element (t, h,
+ *                 i) at t * token_stride + h * head_stride + i (elements; 0 means
+ *                 contiguous; multiples of 8, below 2^38).  Views of [..][192]
+ *                 queries and of [..][256] up-projected rows are fine.
+ *   softmax_scale >= 0, finite.  softcap: 0 for none, at most MLA_MAX_SOFTCAP.
+ *   slopes        device FP32 [heads], finite, or NULL for no bias.
+ *   out           device BF16 [q_tokens][heads][128], strides alike; rows that do
+ *                 not overlap one another or an input.
+ *   lse           device FP32 [q_tokens][heads], natural logarithm of the sum of
+ *                 exponentials, or NULL.
+ *
+ * A row that sees no key gets zeros and an lse of -infinity.  Query rows of no
+ * document are left as they are.  What a row does not see is never used as a value,
+ * infinities and NaN included.  Scores, sums, references and denominators are
+ * FP32; the weights meet the values as BF16 (2^-8 of a weight at most); capped
+ * scores are off by at most 2^-20 of the softcap more.  Results do not depend on
+ * the order in which the GPU runs the work.  Calls sharing a handle, captured or
+ * not, must be ordered on one stream: they share its workspace.
+ * Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.
+ */
+MLA_API int mla_prompt_attn(mla_prompt_t h, int docs, int64_t q_tokens, int64_t k_tokens,
+                            const void* q_nope, int64_t qn_token_stride, int64_t qn_head_stride,
+                            const void* q_pe, int64_t qp_token_stride, int64_t qp_head_stride,
+                            const void* k_nope, int64_t kn_token_stride, int64_t kn_head_stride,
+                            const void* k_pe, int64_t kp_token_stride, const void* v,
+                            int64_t v_token_stride, int64_t v_head_stride, const int32_t* cu_q,
+                            const int32_t* cu_k, int causal, const int32_t* prefix,
+                            float softmax_scale, float softcap, const float* slopes, void* out,
+                            int64_t out_token_stride, int64_t out_head_stride, float* lse,
+                            void* stream);
+
+/* mla_prompt_get_error - read and clear the handle's device error word
+ * (MLA_DEVERR_*); synchronises `stream`. */
+MLA_API int mla_prompt_get_error(mla_prompt_t h, unsigned* device_flags, void* stream);
+
+/* mla_prompt_destroy - free the handle (NULL is a no-op).  No call on it may
+ * still be in flight. */
+MLA_API void mla_prompt_destroy(mla_prompt_t h);
+
 #ifdef __cplusplus
 }
 #endif

@@ -36,6 +36,9 @@ MLA_NOALLOC_MAX_BATCH = 64
 MLA_MAX_ROW_HEADS = 1024
 MLA_ROWS_WAIT_MAX_NS = 2000000000
 MLA_MAX_TABLE_ROWS = 4096
+MLA_MAX_ROPE_AXES = 8
+MLA_MAX_PROMPT_TOKENS = 268435456
+MLA_MAX_SOFTCAP = 1000
 
 _lib = None
 
@@ -142,6 +145,33 @@ def load(path: str | None = None) -> ctypes.CDLL:
         i32, vp, i64, i32, vp, i32, i32, i32, i32, vp, i64, vp, vp,
     ]
     lib.mla_blocks_select.restype = i32
+    lib.mla_rope_create.argtypes = [ctypes.POINTER(vp), vp, vp, i32, f32]
+    lib.mla_rope_create.restype = i32
+    lib.mla_rope_axes.argtypes = [vp]
+    lib.mla_rope_axes.restype = i32
+    lib.mla_rope_destroy.argtypes = [vp]
+    lib.mla_rope_destroy.restype = None
+    lib.mla_rope_apply.argtypes = [vp, i64, i32, vp, i64, i64, vp, i64, i64, vp, i64, i64, vp]
+    lib.mla_rope_apply.restype = i32
+    lib.mla_cache_write.argtypes = [
+        i64, vp, i64, vp, i64, vp, f32, vp, vp, i64, i64, vp, vp, i64, i32, i32, vp, vp, i64, vp, vp,
+    ]
+    lib.mla_cache_write.restype = i32
+    lib.mla_cache_read.argtypes = [
+        vp, i64, i32, i32, vp, vp, i64, i64, i32, vp, vp, i64, vp, i64, vp, vp,
+    ]
+    lib.mla_cache_read.restype = i32
+    lib.mla_prompt_create.argtypes = [ctypes.POINTER(vp), i32]
+    lib.mla_prompt_create.restype = i32
+    lib.mla_prompt_attn.argtypes = [
+        vp, i32, i64, i64, vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp,
+        i32, vp, f32, f32, vp, vp, i64, i64, vp, vp,
+    ]
+    lib.mla_prompt_attn.restype = i32
+    lib.mla_prompt_get_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint), vp]
+    lib.mla_prompt_get_error.restype = i32
+    lib.mla_prompt_destroy.argtypes = [vp]
+    lib.mla_prompt_destroy.restype = None
     _lib = lib
     return lib
 
@@ -416,6 +446,106 @@ def mla_blocks_select(
     )
 
 
+def mla_rope_create(inv_freq, axis=None, interleaved=True, scale=1.0) -> int:
+    """Handle of a rotation: 32 frequencies (radians a position) and, where there is
+    more than one, their axes; raises MlaError on failure."""
+    inv = [float(f) for f in inv_freq]
+    ax = None if axis is None else [int(a) for a in axis]
+    if len(inv) != 32 or (ax is not None and len(ax) != 32):
+        raise MlaError(MLA_EINVAL, "mla_rope_create")
+    h = ctypes.c_void_p()
+    rc = load().mla_rope_create(
+        ctypes.byref(h), (ctypes.c_double * 32)(*inv),
+        None if ax is None else (ctypes.c_int32 * 32)(*(max(-1, min(a, 1 << 20)) for a in ax)),
+        int(bool(interleaved)), float(scale),
+    )
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_rope_create")
+    return h.value
+
+
+def mla_rope_axes(handle) -> int:
+    return load().mla_rope_axes(handle)
+
+
+def mla_rope_destroy(handle) -> None:
+    load().mla_rope_destroy(handle)
+
+
+def mla_rope_apply(
+    handle, tokens, heads, x, x_token_stride, x_head_stride, positions, pos_stride, pos_offset, out,
+    out_token_stride, out_head_stride, stream,
+) -> int:
+    """Rotary positions of rows [tokens][heads][64]; returns the C return code."""
+    return load().mla_rope_apply(
+        handle, tokens, heads, _ptr(x), x_token_stride, x_head_stride, _ptr(positions), pos_stride,
+        pos_offset, _ptr(out), out_token_stride, out_head_stride, _stream(stream),
+    )
+
+
+def mla_cache_write(
+    tokens, kv_c, kv_c_stride, k_pe, k_pe_stride, gamma_kv, eps, rope, positions, pos_stride,
+    pos_offset, slot_mapping, kv_cache, num_pages, page_size, layout, k_scale, rows, rows_stride,
+    device_flags, stream,
+) -> int:
+    """Cache rows of many tokens; returns the C return code."""
+    return load().mla_cache_write(
+        tokens, _ptr(kv_c), kv_c_stride, _ptr(k_pe), k_pe_stride, _ptr(gamma_kv), eps, rope,
+        _ptr(positions), pos_stride, pos_offset, _ptr(slot_mapping), _ptr(kv_cache), num_pages,
+        page_size, layout, _ptr(k_scale), _ptr(rows), rows_stride, _ptr(device_flags),
+        _stream(stream),
+    )
+
+
+def mla_cache_read(
+    kv_cache, num_pages, page_size, layout, k_scale, block_table, bt_stride, bt_cols, requests,
+    cu_rows, first, max_rows, rows, rows_stride, device_flags, stream,
+) -> int:
+    """Cached rows as BF16 rows; returns the C return code."""
+    return load().mla_cache_read(
+        _ptr(kv_cache), num_pages, page_size, layout, _ptr(k_scale), _ptr(block_table), bt_stride,
+        bt_cols, requests, _ptr(cu_rows), _ptr(first), max_rows, _ptr(rows), rows_stride,
+        _ptr(device_flags), _stream(stream),
+    )
+
+
+def mla_prompt_create(heads) -> int:
+    """Handle of prompt attention; raises MlaError on failure."""
+    h = ctypes.c_void_p()
+    rc = load().mla_prompt_create(ctypes.byref(h), int(heads))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_prompt_create")
+    return h.value
+
+
+def mla_prompt_attn(
+    handle, docs, q_tokens, k_tokens, q_nope, qn_token_stride, qn_head_stride, q_pe,
+    qp_token_stride, qp_head_stride, k_nope, kn_token_stride, kn_head_stride, k_pe,
+    kp_token_stride, v, v_token_stride, v_head_stride, cu_q, cu_k, causal, prefix, softmax_scale,
+    softcap, slopes, out, out_token_stride, out_head_stride, lse, stream,
+) -> int:
+    """Attention of packed documents; returns the C return code."""
+    return load().mla_prompt_attn(
+        handle, docs, q_tokens, k_tokens, _ptr(q_nope), qn_token_stride, qn_head_stride, _ptr(q_pe),
+        qp_token_stride, qp_head_stride, _ptr(k_nope), kn_token_stride, kn_head_stride, _ptr(k_pe),
+        kp_token_stride, _ptr(v), v_token_stride, v_head_stride, _ptr(cu_q), _ptr(cu_k), causal,
+        _ptr(prefix), softmax_scale, softcap, _ptr(slopes), _ptr(out), out_token_stride,
+        out_head_stride, _ptr(lse), _stream(stream),
+    )
+
+
+def mla_prompt_get_error(handle, stream=None) -> int:
+    v = ctypes.c_uint(0)
+    rc = load().mla_prompt_get_error(handle, ctypes.byref(v), _stream(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_prompt_get_error")
+    return v.value
+
+
+def mla_prompt_destroy(handle) -> None:
+    load().mla_prompt_destroy(handle)
+
+
 def exported_symbols() -> list[str]:
     """Function names the public header declares."""
     import re
@@ -423,4 +553,4 @@ def exported_symbols() -> list[str]:
     hdr = os.path.join(os.path.dirname(HERE), "include", "mla_query.h")
     with open(hdr) as f:
         text = f.read()
-    return sorted(set(re.findall(r"\b(mla_(?:query|qkv_a|attn|tables|blocks)_[a-z_0-9]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(mla_(?:query|qkv_a|attn|tables|blocks|rope|cache|prompt)_[a-z_0-9]+)\s*\(", text)))

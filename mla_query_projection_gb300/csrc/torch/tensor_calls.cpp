@@ -1,4 +1,4 @@
-// tensor_calls.cpp - the cache-side operators of libmla_query for torch tensors:
+// tensor_calls.cpp - the cache-side and prompt operators of libmla_query for torch tensors:
 // a CPython module that checks the tensors of a call and hands their addresses,
 // sizes and strides to the C ABI.
 //
@@ -29,6 +29,10 @@ decltype(&mla_blocks_mean_cols) blocks_mean_c = nullptr;
 decltype(&mla_blocks_score) blocks_score_c = nullptr;
 decltype(&mla_blocks_select) blocks_select_c = nullptr;
 decltype(&mla_attn_decode_cols) attn_decode_c = nullptr;
+decltype(&mla_rope_apply) rope_apply_c = nullptr;
+decltype(&mla_cache_write) cache_write_c = nullptr;
+decltype(&mla_cache_read) cache_read_c = nullptr;
+decltype(&mla_prompt_attn) prompt_attn_c = nullptr;
 
 // What a call asks of its tensors; the first thing that is wrong stays.
 class Call {
@@ -118,6 +122,54 @@ class Call {
       wrong(what);
     }
     return v;
+  }
+  // A handle of the library: an address, which None is not.
+  template <class T>
+  T handle(PyObject* o) {
+    void* p = o != Py_None ? PyLong_AsVoidPtr(o) : nullptr;
+    if (PyErr_Occurred()) PyErr_Clear();
+    if (p == nullptr) wrong("handle is closed");
+    return static_cast<T>(p);
+  }
+  float real(PyObject* o, const char* what) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) {
+      PyErr_Clear();
+      wrong(what);
+    }
+    return (float)v;
+  }
+  // Positions int32 of `axes` axes for n tokens: [n] or more for one, else [axes, n or
+  // more]; the distance between axes.
+  const int32_t* positions(PyObject* o, int64_t axes, int64_t n, int64_t* stride) {
+    *stride = 0;
+    const at::Tensor* t = tensor(o, "positions");
+    if (t == nullptr) return nullptr;
+    const int64_t dim = t->dim();
+    const bool one = dim == 1 && axes == 1;
+    if (t->scalar_type() != at::kInt || t->get_device() != dev_ || !(one || (dim == 2 && t->size(0) >= axes)) ||
+        t->size(dim - 1) < n || (t->size(dim - 1) > 1 && t->stride(dim - 1) != 1) ||
+        (axes > 1 && t->stride(0) < n)) {
+      wrong("positions");
+      return nullptr;
+    }
+    *stride = axes > 1 ? t->stride(0) : 0;
+    return static_cast<const int32_t*>(t->data_ptr());
+  }
+  // Address and strides of BF16 heads; rows that do not lie over one another are
+  // asked for where they are written.
+  void* bf16_heads(PyObject* o, int64_t tokens, int64_t heads, int64_t width, int64_t* ts, int64_t* hs, bool written,
+                   const char* what) {
+    at::ScalarType type = at::kFloat;
+    void* p = this->heads(o, tokens, heads, width, ts, hs, &type, what);
+    need(type == at::kBFloat16, what);
+    if (written && tokens > 1 && heads > 1) {  // the closer ones in between the others
+      const int64_t near = *ts < *hs ? *ts : *hs, far = *ts < *hs ? *hs : *ts, count = *ts < *hs ? tokens : heads;
+      need(near >= width && (far - width) / near >= count - 1, what);
+    } else if (written) {
+      need((tokens <= 1 || *ts >= width) && (heads <= 1 || *hs >= width), what);
+    }
+    return p;
   }
   int integer(PyObject* o, const char* what) { return (int)number(o, INT_MAX, what); }
   void need(bool ok, const char* what) {
@@ -336,9 +388,110 @@ PyObject* attn_decode(PyObject* const* a) {
                               lens, sel, sel_stride, sel_cols, sel_count, (float)scale, out, ot, oh, lse, stream); });
 }
 
+PyObject* rope_apply(PyObject* const* a) {
+  Call c(a[2]);
+  auto rope = c.handle<mla_rope_t>(a[0]);
+  const at::Tensor* t = c.tensor(a[2], "x");
+  c.need(t != nullptr && t->dim() == 3, "x");
+  if (!c.ok()) return c.refusal();
+  const int64_t tokens = t->size(0), heads = t->size(1);
+  int64_t xt, xh, ot, oh, ps;
+  void* x = c.bf16_heads(a[2], tokens, heads, 64, &xt, &xh, false, "x");
+  void* out = c.bf16_heads(a[5], tokens, heads, 64, &ot, &oh, true, "out");
+  c.need(heads <= INT_MAX, "x");
+  auto* pos = c.positions(a[3], c.number(a[1], INT_MAX, "axes"), tokens, &ps);
+  const int64_t offset = c.number(a[4], INT_MAX, "offset");
+  void* stream = c.stream(a[6]);
+  if (!c.ok()) return c.refusal();
+  return run([&] { return rope_apply_c(rope, tokens, (int)heads, x, xt, xh, pos, ps, offset, out, ot, oh, stream); });
+}
+
+PyObject* cache_write(PyObject* const* a) {
+  Call c(a[0]);
+  int64_t ks, kr, kc, ps, pr, pc, slots_n[1], pos_stride = 0, rs = 0, rr, rc;
+  void* kv = c.rows(a[0], at::kBFloat16, &ks, &kr, &kc, "kv_c");
+  void* pe = c.rows(a[1], at::kBFloat16, &ps, &pr, &pc, "k_pe");
+  auto* slots = c.whole<const int64_t>(a[2], at::kLong, 1, slots_n, "slots");
+  const int64_t tokens = slots_n[0];
+  c.need(kc == 512 && kr >= tokens, "kv_c");
+  c.need(pc == 64 && pr >= tokens, "k_pe");
+  const Cache k(c, a[3], a[4], a[5]);
+  void* gamma = c.flat(a[6], at::kBFloat16, 512, "gamma");
+  const float eps = c.real(a[7], "eps");
+  mla_rope_t rope = nullptr;
+  const int32_t* pos = nullptr;
+  if (a[8] != Py_None || a[10] != Py_None) {
+    rope = c.handle<mla_rope_t>(a[8]);
+    pos = c.positions(a[10], c.number(a[9], INT_MAX, "axes"), tokens, &pos_stride);
+  }
+  const int64_t offset = c.number(a[11], INT_MAX, "offset");
+  void* rows = nullptr;
+  if (a[12] != Py_None) {
+    rows = c.rows(a[12], at::kBFloat16, &rs, &rr, &rc, "rows");
+    c.need(rc == 576 && rr >= tokens, "rows");
+  }
+  auto* flags = c.flat<unsigned>(a[13], at::kInt, 1, "flags");
+  void* stream = c.stream(a[14]);
+  if (!c.ok()) return c.refusal();
+  return run([&] { return cache_write_c(tokens, kv, ks, pe, ps, gamma, eps, rope, pos, pos_stride, offset, slots,
+                              const_cast<void*>(k.rows), k.pages, k.page, k.layout, k.scale, rows, rs, flags, stream); });
+}
+
+PyObject* cache_read(PyObject* const* a) {
+  Call c(a[0]);
+  const Cache k(c, a[0], a[1], a[2]);
+  int64_t stride, table_rows, width, cu_n[1], rs, rr, rc;
+  auto* table = c.rows<const int32_t>(a[3], at::kInt, &stride, &table_rows, &width, "block table");
+  auto* cu = c.whole<const int32_t>(a[4], at::kInt, 1, cu_n, "cu_rows");
+  const int64_t requests = cu_n[0] - 1;
+  c.need(requests >= 1 && requests <= INT_MAX, "cu_rows");
+  c.need(table_rows >= requests, "block table");
+  void* rows = c.rows(a[5], at::kBFloat16, &rs, &rr, &rc, "rows");
+  c.need(rc == 576, "rows");
+  auto* first = c.flat<const int32_t>(a[6], at::kInt, requests, "first");
+  auto* flags = c.flat<unsigned>(a[7], at::kInt, 1, "flags");
+  void* stream = c.stream(a[8]);
+  if (!c.ok()) return c.refusal();
+  return run([&] { return cache_read_c(k.rows, k.pages, k.page, k.layout, k.scale, table, stride, width, (int)requests, cu,
+                             first, rr, rows, rs, flags, stream); });
+}
+
+PyObject* prompt_attn(PyObject* const* a) {
+  Call c(a[2]);
+  auto handle = c.handle<mla_prompt_t>(a[0]);
+  const int64_t heads = c.number(a[1], INT_MAX, "heads");
+  const at::Tensor *q = c.tensor(a[2], "queries"), *key = c.tensor(a[4], "keys");
+  c.need(q != nullptr && q->dim() == 3, "queries");
+  c.need(key != nullptr && key->dim() == 3, "keys");
+  if (!c.ok()) return c.refusal();
+  const int64_t tq = q->size(0), tk = key->size(0);
+  int64_t qnt, qnh, qpt, qph, knt, knh, vt, vh, ot, oh, pes, per, pec, cu_n[1];
+  void* qn = c.bf16_heads(a[2], tq, heads, 128, &qnt, &qnh, false, "queries");
+  void* qp = c.bf16_heads(a[3], tq, heads, 64, &qpt, &qph, false, "queries");
+  void* kn = c.bf16_heads(a[4], tk, heads, 128, &knt, &knh, false, "keys");
+  void* kp = c.rows(a[5], at::kBFloat16, &pes, &per, &pec, "k_pe");
+  c.need(pec == 64 && per == tk, "k_pe");
+  void* v = c.bf16_heads(a[6], tk, heads, 128, &vt, &vh, false, "values");
+  auto* cu_q = c.whole<const int32_t>(a[7], at::kInt, 1, cu_n, "cu_q");
+  const int64_t docs = cu_n[0] - 1;
+  c.need(docs >= 1 && docs <= INT_MAX, "cu_q");
+  auto* cu_k = a[8] == Py_None ? cu_q : c.flat<const int32_t>(a[8], at::kInt, docs + 1, "cu_k");
+  const int causal = PyObject_IsTrue(a[9]);
+  if (causal < 0) return nullptr;
+  auto* prefix = c.flat<const int32_t>(a[10], at::kInt, docs, "prefix");
+  const float scale = c.real(a[11], "softmax_scale"), cap = c.real(a[12], "softcap");
+  auto* slopes = c.flat<const float>(a[13], at::kFloat, heads, "slopes");
+  void* out = c.bf16_heads(a[14], tq, heads, 128, &ot, &oh, true, "out");
+  auto* lse = c.flat<float>(a[15], at::kFloat, tq * heads, "lse");
+  void* stream = c.stream(a[16]);
+  if (!c.ok()) return c.refusal();
+  return run([&] { return prompt_attn_c(handle, (int)docs, tq, tk, qn, qnt, qnh, qp, qpt, qph, kn, knt, knh, kp, pes, v, vt,
+                              vh, cu_q, cu_k, causal, prefix, scale, cap, slopes, out, ot, oh, lse, stream); });
+}
+
 PyObject* bind(PyObject* const* a) {
-  void* p[5];
-  for (int i = 0; i < 5; ++i) {
+  void* p[9];
+  for (int i = 0; i < 9; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -347,6 +500,10 @@ PyObject* bind(PyObject* const* a) {
   blocks_score_c = reinterpret_cast<decltype(blocks_score_c)>(p[2]);
   blocks_select_c = reinterpret_cast<decltype(blocks_select_c)>(p[3]);
   attn_decode_c = reinterpret_cast<decltype(attn_decode_c)>(p[4]);
+  rope_apply_c = reinterpret_cast<decltype(rope_apply_c)>(p[5]);
+  cache_write_c = reinterpret_cast<decltype(cache_write_c)>(p[6]);
+  cache_read_c = reinterpret_cast<decltype(cache_read_c)>(p[7]);
+  prompt_attn_c = reinterpret_cast<decltype(prompt_attn_c)>(p[8]);
   Py_RETURN_NONE;
 }
 
@@ -357,12 +514,16 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef methods[] = {
-    method<5, bind>("bind"),
+    method<9, bind>("bind"),
     method<14, tables_step>("tables_step"),
     method<9, blocks_mean>("blocks_mean"),
     method<11, blocks_score>("blocks_score"),
     method<8, blocks_select>("blocks_select"),
     method<17, attn_decode>("attn_decode"),
+    method<7, rope_apply>("rope_apply"),
+    method<15, cache_write>("cache_write"),
+    method<9, cache_read>("cache_read"),
+    method<17, prompt_attn>("prompt_attn"),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_calls", nullptr, -1, methods};

@@ -157,7 +157,8 @@ def _native():
                                "`python -m mla_query_projection_gb300.build`") from e
         _tensor_calls.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.mla_tables_step, lib.mla_blocks_mean_cols, lib.mla_blocks_score, lib.mla_blocks_select,
-            lib.mla_attn_decode_cols)))
+            lib.mla_attn_decode_cols, lib.mla_rope_apply, lib.mla_cache_write, lib.mla_cache_read,
+            lib.mla_prompt_attn)))
         _calls = _tensor_calls
     return _calls
 
@@ -263,6 +264,118 @@ class PagedAttention:
         if self.handle:
             torch.cuda.synchronize(self.device)
             B.mla_attn_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ---- the prompt's side of the layer ----------------------------------------
+
+
+class Rotary:
+    """Rotary positions of 64-wide rows: 32 pairs, pair p turned by its axis'
+    position times ``inv_freq[p]`` (``mla_rope_create``).
+
+    ``axis`` [32] names each pair's axis where positions have several (time, height,
+    width); ``interleaved`` takes neighbours as pairs, else halves.  The object holds
+    no device memory: it serves every device and stream."""
+
+    def __init__(self, inv_freq, axis=None, interleaved: bool = True, scale: float = 1.0):
+        self.handle = None
+        self.handle = B.mla_rope_create(inv_freq, axis, interleaved, scale)
+        self.axes = B.mla_rope_axes(self.handle)
+
+    def apply(self, x, positions, out=None, offset: int = 0, stream=None):
+        """``x`` [tokens, heads, 64] BF16 turned (``mla_rope_apply``); returns ``out``.
+
+        ``positions`` int32 [tokens], or [axes, tokens]; ``offset`` is added to each
+        (-1 takes the ``token_len`` of ``tables_step``).  ``out`` is allocated, as
+        memory of the call's stream, where it is not given, and may be ``x``."""
+        if out is None and isinstance(x, torch.Tensor) and x.is_cuda:
+            with _allocating_on(stream, x.device):
+                out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        wrong = (_calls or _native()).rope_apply(self.handle, self.axes, x, positions, offset, out, stream)
+        if wrong is not None:
+            _refuse(wrong, "mla_rope_apply")
+        return out
+
+    def close(self):
+        if self.handle:
+            B.mla_rope_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def cache_write(kv_c, k_pe, slot_mapping, cache, layout, k_scale=None, gamma=None, eps=1e-6, rotary=None,
+                positions=None, offset=0, rows=None, flags=None, stream=None) -> None:
+    """Cache rows of many tokens (``mla_cache_write``): the RMSNorm of ``kv_c`` [tokens, 512]
+    with ``gamma`` (None: it is normalised), the rotation of ``k_pe`` [tokens, 64] with
+    ``rotary`` (None: as it is), quantised into the slots; ``rows`` [tokens, 576] receives
+    the same row in BF16."""
+    handle, axes = (None, 1) if rotary is None else (rotary.handle or 0, rotary.axes)
+    wrong = (_calls or _native()).cache_write(kv_c, k_pe, slot_mapping, cache, layout, k_scale, gamma, eps, handle,
+                                              axes, positions, offset, rows, flags, stream)
+    if wrong is not None:
+        _refuse(wrong, "mla_cache_write")
+
+
+def cache_read(cache, layout, k_scale, block_table, cu_rows, rows, first=None, flags=None, stream=None) -> None:
+    """Cached rows as BF16 ``rows`` [rows, 576] (``mla_cache_read``): request r's positions
+    from ``first[r]`` (None: 0) on in rows ``cu_rows[r]`` .. ``cu_rows[r + 1] - 1``."""
+    wrong = (_calls or _native()).cache_read(cache, layout, k_scale, block_table, cu_rows, rows, first, flags, stream)
+    if wrong is not None:
+        _refuse(wrong, "mla_cache_read")
+
+
+class PromptAttention:
+    """Attention of packed documents over expanded keys, with its workspace.
+
+    One object serves calls of ``heads`` heads; they must be ordered on one stream."""
+
+    def __init__(self, heads: int, device="cuda:0"):
+        self.handle = None
+        self.device = torch.device(device)
+        self.heads = heads
+        with torch.cuda.device(self.device):
+            self.handle = B.mla_prompt_create(heads)
+
+    def attend(self, q_nope, q_pe, k_nope, k_pe, v, cu_q, softmax_scale, cu_k=None, causal=True, prefix=None,
+               softcap=0.0, slopes=None, out=None, lse=None, stream=None):
+        """Attention of the documents' rows (``mla_prompt_attn``); returns ``(out, lse)``.
+
+        ``q_nope`` [tokens, heads, 128], ``q_pe`` [tokens, heads, 64], ``k_nope`` and
+        ``v`` [keys, heads, 128] may be strided (views of 192-wide queries and 256-wide
+        up-projected rows), ``k_pe`` [keys, 64] too.  ``cu_q`` and ``cu_k`` int32
+        [documents + 1] say where the documents lie (``cu_k`` None: where the queries
+        do).  ``out`` BF16 [tokens, heads, 128] is allocated, as memory of the call's
+        stream, where it is not given; ``lse`` FP32 [tokens, heads] is written where it
+        is."""
+        if out is None and isinstance(q_nope, torch.Tensor) and q_nope.is_cuda:
+            with _allocating_on(stream, q_nope.device):
+                out = torch.empty(q_nope.shape, dtype=torch.bfloat16, device=q_nope.device)
+        wrong = (_calls or _native()).prompt_attn(
+            self.handle, self.heads, q_nope, q_pe, k_nope, k_pe, v, cu_q, cu_k, causal, prefix, softmax_scale,
+            softcap, slopes, out, lse, stream)
+        if wrong is not None:
+            _refuse(wrong, "mla_prompt_attn")
+        return out, lse
+
+    def error_flags(self) -> int:
+        return B.mla_prompt_get_error(self.handle, torch.cuda.current_stream(self.device))
+
+    def close(self):
+        if self.handle:
+            torch.cuda.synchronize(self.device)
+            B.mla_prompt_destroy(self.handle)
             self.handle = None
 
     def __del__(self):
