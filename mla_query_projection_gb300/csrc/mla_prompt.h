@@ -81,13 +81,16 @@ struct PromptArgs {
   int splits;
   float* part_o;    // [splits][heads][q_tokens][128]
   float2* part_ml;  // [splits][heads][q_tokens] reference in base 2, sum
+  const uint16_t* v;
+  int64_t v_ts, v_hs;
+  int group;       // heads that are handed out together
+  uint32_t* next;  // items handed out beside each CTA's first, CTAs that are done; zero between calls
   uint32_t* err;
 };
 struct PromptMaps {
   CUtensorMap q_nope, q_pe, k_nope, k_pe, v;
 };
 cudaError_t prepare_prompt();
-// `tiles`: at least the documents' tiles of 256 query rows, taken together.
-cudaError_t launch_prompt(const PromptArgs& a, const PromptInputs& in, int tiles, cudaStream_t stream);
+cudaError_t launch_prompt(const PromptArgs& a, const PromptInputs& in, int ctas, cudaStream_t stream);
 
 }  // namespace mla

@@ -5,13 +5,14 @@
 //   x_ij = cap(scale q_i . k_j) - slope |place_i - j|,  cap(x) = c tanh(x / c)
 //   out_i = sum_j p_ij v_j,  p_i = softmax over the keys that row i sees
 //
-// A CTA takes 256 query rows of one head and document as two tiles of 128, and
-// goes through the keys in tiles of 128 that both share.  S = Q K^T (M = 128
-// rows, N = 128 keys, K = 192) and O += P V (K = 128 keys, N = 128 columns) are
-// tcgen05 products with FP32 accumulators in TMEM; P goes back to TMEM as BF16
+// A CTA takes an item of work after another: 256 query rows of a head and document,
+// as two tiles of 128, through the keys in tiles of 128 that both share.  S = Q K^T
+// (M = 128 rows, N = 128 keys, K = 192) and O += P V (K = 128 keys, N = 128 columns)
+// are tcgen05 products with FP32 accumulators in TMEM; P goes back to TMEM as BF16
 // in the place of its S, and is read from there.  While the softmax of one tile
 // runs, the tensor core works for the other: O0 += P0 V, S0 of the next keys,
-// O1 += P1 V, S1.
+// O1 += P1 V, S1.  The next item's queries and keys are loaded, and its first
+// scores formed, while the last item's sums are written.
 //
 //  * A softmax thread owns one query row: its maximum, its sum and its mask need
 //    no other lane.  The row's reference (what exponents are taken relative to)
@@ -20,13 +21,16 @@
 //  * What a row sees are the first `bound` keys of its document: its own place
 //    and all before it, or its document's two-way prefix, or all.  Tiles that no
 //    row of theirs needs are not touched, and only those on an edge are masked.
+//  * An item of 128 rows or fewer has one query tile: its key tiles go to the two
+//    softmax warpgroups in turn, each with its own sums, which are added at the end.
 //  * Keys and values come by TMA in units of 16 KiB through a ring of eight: 64
 //    columns of 128 keys, or 64 keys of 128 values.
 //  * A value that a row does not see may be an infinity or a NaN, and zero times
 //    it is not zero.  So on the tiles with an edge the softmax threads look their
 //    values over first: rows behind the document are zeroed; an infinity or a NaN
-//    inside it is replaced by zero and noted for its column with its place, and
-//    the rows that see it get it at the end.
+//    inside it is replaced by zero and added at the end to the rows that see it.
+//  * Items are handed out on the GPU as CTAs become free, the longest first: their
+//    lengths are known there alone.
 //  * Few query rows: the keys are split over several CTAs, whose sums a second
 //    kernel joins.
 #include <stdlib.h>
@@ -38,7 +42,7 @@ struct mla_prompt {
   int device;
   int num_sms;
   int heads;
-  uint32_t* err;
+  uint32_t* err;    // flags, then (at 2 and 3) items handed out and CTAs done with them
   float* part_o;    // sums of split rows
   float2* part_ml;  // their references and denominators
 };
@@ -46,26 +50,44 @@ struct mla_prompt {
 namespace mla {
 namespace {
 
-constexpr int kPrTile = 128;                  // query rows and keys of a tile
-constexpr int kPrUnit = 16384;                // bytes of a ring unit
+constexpr int kPrTile = 128;     // query rows and keys of a tile
+constexpr int kPrUnit = 16384;   // bytes of a ring slot
 constexpr int kPrRing = 8;
-constexpr int kPrThreads = 320;               // two softmax warpgroups, a TMA warp, an MMA warp
-constexpr int kPrQ = 3 * kPrUnit;             // a query tile: planes of 64 columns
-constexpr float kPrRoom = 8.0f;               // base 2
+constexpr int kPrThreads = 384;  // two softmax warpgroups; warps that load, multiply, hand out work (and one idle)
+constexpr int kPrQ = 3 * kPrUnit;  // a query tile: planes of 64 columns
+constexpr float kPrRoom = 8.0f;  // base 2
+constexpr int kPrChunks = 96;    // sums of the documents' tiles
+constexpr int kPrItems = 4;      // items of work in flight
+constexpr int kPrReaders = 10;   // warps that read them
+
+// One item of work: up to 256 query rows of a head and document, and the tiles
+// of its keys that this CTA goes through.
+struct PrItem {
+  int valid;         // 0: there is no more
+  int head, split;
+  int q0, nq;        // the document's query rows
+  int k0, nk;        // and keys
+  int prefix;
+  int r0;            // first row, in the document
+  int j0, n[2];      // query tile q: key tiles j0 .. n[q] - 1
+  int safe[2];       // tiles below are seen whole by every row of query tile q
+  int solo;          // one query tile only: its keys are shared out, 1 + who begins
+  uint32_t odd;      // values that are not finite were met
+};
 
 struct PrSmem {
   static constexpr int oQ = 0;
   static constexpr int oRing = 2 * kPrQ;
   static constexpr int oBar = oRing + kPrRing * kPrUnit;
-  // full[8] empty[8] q_full[2] s_full[2] p_full[2] o_full[2] drain
-  static constexpr int kBars = 25;
-  static constexpr int oBad = oBar + kBars * 8;  // [3][128] first NaN, infinity, -infinity of a column
-  static constexpr int oAny = oBad + 3 * 128 * 4;
-  static constexpr int oPlan = oAny + 4;         // document, tile, total
-  static constexpr int oScan = oPlan + 12;       // [10]
-  static constexpr int oTmem = oScan + 40;
+  // full[8] empty[8] q_full[2] q_free[2] s_full[2] p_full[4] o_full[2] o_free[2] ml_full[2] item_full[4]
+  // item_free[4] drain
+  static constexpr int kBars = 41;
+  static constexpr int oItem = oBar + kBars * 8;
+  static constexpr int oMl = oItem + kPrItems * (int)sizeof(PrItem);  // [2][128] reference and sum of a shared row
+  static constexpr int oScan = oMl + 2 * 128 * 8;                     // [96]
+  static constexpr int oTmem = oScan + kPrChunks * 4;
   static constexpr int kBytes = oTmem + 8;
-  static_assert(kBytes <= 232448 && oBar % 8 == 0 && oBad % 4 == 0, "shared memory budget");
+  static_assert(kBytes <= 232448 && oBar % 8 == 0 && oItem % 8 == 0 && oMl % 8 == 0, "shared memory budget");
 };
 
 // O += P V, four steps of 16 keys: P in TMEM (8 columns a step), V's steps 2 KiB apart.
@@ -97,16 +119,93 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// The smaller, or NaN.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 
-struct PrDoc {
-  int q0, nq, k0, nk, prefix, tile;
-  // keys that query row i (of the document) sees
-  __device__ __forceinline__ int bound(int i, bool causal) const {
-    if (!causal) return nk;
-    const int own = i + (nk - nq) + 1;
-    return max(min(prefix, nk), max(0, min(own, nk)));
+// Keys that query row i of a document sees: the first so many.
+__device__ __forceinline__ int pr_bound(int i, int nq, int nk, int prefix, bool causal) {
+  if (!causal) return nk;
+  return max(min(prefix, nk), max(0, min(i + (nk - nq) + 1, nk)));
+}
+__device__ __forceinline__ bool pr_edge(const PrItem& k, int j) {
+  return (j < k.n[0] && j >= k.safe[0]) || (j < k.n[1] && j >= k.safe[1]);
+}
+
+// A document's rows, cut to the tensor.
+__device__ __forceinline__ int pr_place(const int32_t* cu, int d, int most, int* n, bool* cut) {
+  const int lo = cu[d], hi = cu[d + 1];
+  const int c0 = max(0, min(lo, most)), c1 = max(c0, min(hi, most));
+  *n = c1 - c0;
+  *cut = c0 != lo || c1 != hi;
+  return c0;
+}
+__device__ __forceinline__ int pr_tiles(const PromptArgs& a, int d) {
+  int n;
+  bool cut;
+  pr_place(a.cu_q, d, a.q_tokens, &n, &cut);
+  return (n + 2 * kPrTile - 1) / (2 * kPrTile);
+}
+
+// A key's row of values in a ring unit (two halves of 128 bytes): zeros where the
+// key lies behind its document; else what is not finite becomes zero.  Whether
+// there was any.
+__device__ __noinline__ bool pr_look_over(uint8_t* base, int lane, bool behind) {
+  if (behind) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      *reinterpret_cast<uint4*>(base + (c >> 3) * (kPrUnit / 2) + (((c + lane) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+    return false;
   }
-};
+  uint32_t mag = 0;
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    const uint4 w = *reinterpret_cast<const uint4*>(base + (c >> 3) * (kPrUnit / 2) + (((c + lane) & 7) << 4));
+    const uint32_t g = 0x7FFF7FFFu;
+    mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(w.x & g, w.y & g), __vmaxu2(w.z & g, w.w & g)));
+  }
+  if ((mag & 0xFFFFu) < 0x7F80u && (mag >> 16) < 0x7F80u) return false;
+#pragma unroll 1
+  for (int c = 0; c < 64; ++c) {
+    uint16_t* e = reinterpret_cast<uint16_t*>(base) + c;
+    if ((*e & 0x7F80u) == 0x7F80u) *e = 0;
+    e += kPrUnit / 4;
+    if ((*e & 0x7F80u) == 0x7F80u) *e = 0;
+  }
+  return true;
+}
+
+// Values that are not finite and lie in the tiles that were looked over (where they
+// count as zero in the products): added to a stored row that sees the first `bound`
+// keys, its sums (`part`) or its output.  Slow, and rare.
+__device__ __noinline__ void pr_add_odd(const PromptArgs& a, const PrItem& k, int j0, int end, int bound, float* part,
+                                        uint16_t* out) {
+  for (int c = 0; c < 128; c += 4) {
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int j = j0; j < end; ++j) {
+      if (!pr_edge(k, j)) continue;
+      for (int key = j * kPrTile, e = min(min(key + kPrTile, bound), k.nk); key < e; ++key) {
+        const uint2 w =
+            *reinterpret_cast<const uint2*>(a.v + (int64_t)(k.k0 + key) * a.v_ts + (int64_t)k.head * a.v_hs + c);
+        const uint32_t x[4] = {w.x << 16, w.x & 0xFFFF0000u, w.y << 16, w.y & 0xFFFF0000u};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((x[i] & 0x7F800000u) == 0x7F800000u) sum[i] += __uint_as_float(x[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (sum[i] == 0.f) continue;
+      if (part != nullptr)
+        part[c + i] += sum[i];
+      else
+        out[c + i] = f2bf_bits(__uint_as_float((uint32_t)out[c + i] << 16) + sum[i]);
+    }
+  }
+}
 
 // CAP: scores are capped; BIAS: they lose by distance.
 template <bool CAP, bool BIAS>
@@ -117,114 +216,65 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::oBar);
   uint64_t* empty = full + kPrRing;
   uint64_t* q_full = empty + kPrRing;
-  uint64_t* s_full = q_full + 2;
+  uint64_t* q_free = q_full + 2;
+  uint64_t* s_full = q_free + 2;
   uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = p_full + 2;
-  uint64_t* drain = o_full + 2;
-  int* bad = reinterpret_cast<int*>(smem + S::oBad);
-  volatile uint32_t* any_bad = reinterpret_cast<uint32_t*>(smem + S::oAny);
-  int* plan = reinterpret_cast<int*>(smem + S::oPlan);
+  uint64_t* o_full = p_full + 4;  // (p_full: two halves a buffer)
+  uint64_t* o_free = o_full + 2;
+  uint64_t* ml_full = o_free + 2;
+  uint64_t* item_full = ml_full + 2;
+  uint64_t* item_free = item_full + kPrItems;
+  uint64_t* drain = item_free + kPrItems;
+  PrItem* items = reinterpret_cast<PrItem*>(smem + S::oItem);
+  volatile float2* ml = reinterpret_cast<float2*>(smem + S::oMl);
   int* scan = reinterpret_cast<int*>(smem + S::oScan);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + S::oTmem);
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
-  const int head = blockIdx.y;
-  pdl_wait();
-  pdl_launch_dependents();
-
-  // ---- which document and tile: the prefix sum of the documents' tiles, the
-  // last tiles first (with causal masks they are the longest)
-  const int each = (a.docs + kPrThreads - 1) / kPrThreads;
-  const int d0 = min(a.docs, tid * each), d1 = min(a.docs, d0 + each);
-  auto place = [&](const int32_t* cu, int d, int most, int* n) {
-    const int lo = cu[d], hi = cu[d + 1];
-    const int c0 = max(0, min(lo, most)), c1 = max(c0, min(hi, most));
-    *n = c1 - c0;
-    if ((c0 != lo || c1 != hi) && blockIdx.x == 0 && head == 0 && blockIdx.z == 0) atomicOr(a.err, MLA_DEVERR_BAD_SLOT);
-    return c0;
-  };
-  int mine = 0;
-  for (int d = d0; d < d1; ++d) {
-    int n;
-    place(a.cu_q, d, a.q_tokens, &n);
-    mine += (n + 2 * kPrTile - 1) / (2 * kPrTile);
-  }
-  int sum = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-    if (lane >= o) sum += v;
-  }
-  if (lane == 31) scan[warp] = sum;
-  if (tid == 0) plan[0] = -1;
-  __syncthreads();
-  int before = sum - mine, total = 0;
-  for (int w = 0; w < kPrThreads / 32; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
-  }
-  const int x = total - 1 - (int)blockIdx.x;
-  if (x >= before && x < before + mine) {
-    int at = before;
-    for (int d = d0; d < d1; ++d) {
-      int n;
-      place(a.cu_q, d, a.q_tokens, &n);
-      const int t = (n + 2 * kPrTile - 1) / (2 * kPrTile);
-      if (x < at + t) {
-        plan[0] = d;
-        plan[1] = x - at;
-        break;
-      }
-      at += t;
-    }
-  }
-  for (int c = tid; c < 3 * 128; c += kPrThreads) bad[c] = 0x7FFFFFFF;
+  const bool causal = a.causal != 0;
+  const int each = (a.docs + kPrChunks - 1) / kPrChunks;  // documents a sum
   if (tid == 0) {
-    *any_bad = 0;
     for (int s = 0; s < kPrRing; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int q = 0; q < 2; ++q) {
       mbar_init(&q_full[q], 1);
+      mbar_init(&q_free[q], 1);
       mbar_init(&s_full[q], 1);
-      mbar_init(&p_full[q], 4);
+      mbar_init(&p_full[2 * q], 4);
+      mbar_init(&p_full[2 * q + 1], 4);
       mbar_init(&o_full[q], 1);
+      mbar_init(&o_free[q], 4);
+      mbar_init(&ml_full[q], 4);
+    }
+    for (int i = 0; i < kPrItems; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_free[i], kPrReaders);
     }
     mbar_init(drain, 1);
     mbar_fence_init();
     if (smem_u32(smem) & 1023u) atomicOr(a.err, MLA_DEVERR_CHECK);
   }
-  __syncthreads();
-  const int d = plan[0];
-  if (d < 0) return;  // (the grid is an upper bound of the tiles)
-  PrDoc k;
-  k.tile = plan[1];
-  k.q0 = place(a.cu_q, d, a.q_tokens, &k.nq);
-  k.k0 = place(a.cu_k, d, a.k_tokens, &k.nk);
-  k.prefix = a.prefix != nullptr ? a.prefix[d] : 0;
-  const bool causal = a.causal != 0;
-  // query tile q: rows first[q] .. of the document, key tiles [j0, n[q])
-  const int r0 = k.tile * 2 * kPrTile;
-  int n[2], safe[2];  // key tiles below safe[q] are seen whole by every row
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int lo = r0 + q * kPrTile, hi = min(lo + kPrTile, k.nq);
-    n[q] = hi > lo ? (k.bound(hi - 1, causal) + kPrTile - 1) / kPrTile : 0;
-    safe[q] = hi > lo ? k.bound(lo, causal) / kPrTile : 0;
-  }
-  // this CTA's share of the key tiles
-  const int all = max(n[0], n[1]);
-  const int j0 = (int)((int64_t)all * blockIdx.z / a.splits), j1 = (int)((int64_t)all * (blockIdx.z + 1) / a.splits);
-  n[0] = min(n[0], j1);
-  n[1] = min(n[1], j1);
-  const int end = max(n[0], n[1]);  // == j1, or none where j1 <= j0
-
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 32 * 8) {
+    prefetch_tensormap(&maps.k_nope);
+    prefetch_tensormap(&maps.k_pe);
+    prefetch_tensormap(&maps.q_nope);
+    prefetch_tensormap(&maps.q_pe);
+    prefetch_tensormap(&maps.v);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (tid < kPrChunks) {
+    int sum = 0;
+    for (int d = tid * each, e = min(a.docs, d + each); d < e; ++d) sum += pr_tiles(a, d);
+    scan[tid] = sum;
   }
   tc_before();
   __syncthreads();
@@ -232,299 +282,617 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   const uint32_t tmem = uniform(*tslot);  // S at columns 0 and 128, O at 256 and 384
   bool dead = false;
 
-  if (warp == 8) {
-    // ================= TMA: queries, then units in the order K, V of tile after tile
-    if (lane == 0 && j0 < end) {
-      int use = 0;  // units so far
-      auto next = [&]() -> int {
-        const int s = use % kPrRing;
-        if (use >= kPrRing) tc_wait(&empty[s], (uint32_t)((use / kPrRing - 1) & 1), dead);
-        return s;
-      };
-      auto query = [&](int q) {
-        if (n[q] <= j0) return;
-        mbar_arrive_expect_tx(&q_full[q], kPrQ);
-        const uint32_t dst = smem_u32(smem + S::oQ) + q * kPrQ;
-        const int row = k.q0 + r0 + q * kPrTile;
-        tma_g2s_3d(dst, &maps.q_nope, 0, head, row, &q_full[q]);
-        tma_g2s_3d(dst + kPrUnit, &maps.q_nope, 64, head, row, &q_full[q]);
-        tma_g2s_3d(dst + 2 * kPrUnit, &maps.q_pe, 0, head, row, &q_full[q]);
-      };
-      query(0);
-      for (int j = j0; j < end && !dead; ++j) {
-        const int row = k.k0 + j * kPrTile;
-        for (int u = 0; u < 3 && !dead; ++u) {
-          const int s = next();
-          if (dead) break;
-          const uint32_t dst = smem_u32(smem + S::oRing) + s * kPrUnit;
-          mbar_arrive_expect_tx(&full[s], kPrUnit);
-          if (u < 2)
-            tma_g2s_3d(dst, &maps.k_nope, 64 * u, head, row, &full[s]);
-          else
-            tma_g2s_3d(dst, &maps.k_pe, 0, 0, row, &full[s]);
-          ++use;
+  // What each reader of the items does: the next one, and that it is done with one.
+  auto item_wait = [&](uint32_t i) -> const PrItem& {
+    tc_wait_warp(&item_full[i % kPrItems], (i / kPrItems) & 1u, dead);
+    return items[i % kPrItems];
+  };
+  auto item_done = [&](uint32_t i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_free[i % kPrItems]);
+  };
+
+  // Registers: 168 a thread at the launch; the softmax takes 208, the others keep 88.
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 10) {
+    // ================= work: the items in order, each CTA the next one that is free
+    constexpr int kOwn = kPrChunks / 32;  // sums a lane
+    int mine = 0;
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) mine += scan[lane * kOwn + e];
+    int before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, before, o);
+      if (lane >= o) before += v;
+    }
+    const int tiles = __shfl_sync(0xFFFFFFFFu, before, 31);
+    before -= mine;
+    const uint32_t total = (uint32_t)tiles * (uint32_t)a.heads * (uint32_t)a.splits;
+    uint32_t u = blockIdx.x;
+    int at = -1, doc = 0, tile = 0, last_q = 1;
+    for (uint32_t i = 0;; ++i) {
+      // ahead: the answer is there by the time it is needed
+      uint32_t ahead = 0;
+      if (lane == 0 && u < total) ahead = atomicAdd(a.next, 1u) + gridDim.x;
+      if (i >= kPrItems) tc_wait_warp(&item_free[i % kPrItems], (i / kPrItems - 1) & 1u, dead);
+      PrItem& k = items[i % kPrItems];
+      if (u >= total || dead) {
+        if (lane == 0) {
+          k.valid = 0;
+          mbar_arrive(&item_full[i % kPrItems]);
         }
-        if (j == j0) query(1);
-        for (int u = 0; u < 2 && !dead; ++u) {  // 64 keys, both halves of their columns
-          const int s = next();
-          if (dead) break;
-          const uint32_t dst = smem_u32(smem + S::oRing) + s * kPrUnit;
-          mbar_arrive_expect_tx(&full[s], kPrUnit);
-          tma_g2s_3d(dst, &maps.v, 0, head, row + 64 * u, &full[s]);
-          tma_g2s_3d(dst + kPrUnit / 2, &maps.v, 64, head, row + 64 * u, &full[s]);
-          ++use;
+        break;
+      }
+      // groups of heads; of a group the last tiles first (the longest where rows see
+      // what lies before them), head after head
+      const uint32_t per_group = (uint32_t)a.group * (uint32_t)tiles * (uint32_t)a.splits;
+      const uint32_t g = u / per_group, r = u - g * per_group;
+      const int heads = min(a.group, a.heads - (int)g * a.group);
+      const uint32_t row = (uint32_t)(heads * a.splits);
+      const int x = tiles - 1 - (int)(r / row);
+      const int in = (int)(r % row);
+      if (x != at) {
+        at = x;
+        // the lane whose sums hold x, its sum, then the document
+        const unsigned who = __ballot_sync(0xFFFFFFFFu, x >= before && x < before + mine);
+        const int src = __ffs(who) - 1;
+        int b = before, c = lane * kOwn;
+        while (lane == src && x >= b + scan[c]) b += scan[c++];
+        b = __shfl_sync(0xFFFFFFFFu, b, src);
+        c = __shfl_sync(0xFFFFFFFFu, c, src);
+        for (int d0 = c * each;; d0 += 32) {
+          const int d = d0 + lane;
+          int n = d < min(a.docs, (c + 1) * each) ? pr_tiles(a, d) : 0;
+          const int own = n;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, n, o);
+            if (lane >= o) n += v;
+          }
+          const unsigned hit = __ballot_sync(0xFFFFFFFFu, x >= b + n - own && x < b + n);
+          if (hit != 0) {
+            const int w = __ffs(hit) - 1;
+            doc = d0 + w;
+            tile = x - (b + __shfl_sync(0xFFFFFFFFu, n - own, w));
+            break;
+          }
+          b += __shfl_sync(0xFFFFFFFFu, n, 31);
+          if (d0 >= a.docs) break;  // (documents that another program moves meanwhile)
         }
       }
-      if (dead) {  // the copies under way land before the CTA leaves
-        for (int q = 0; q < 2; ++q)
-          if (n[q] > j0) (void)mbar_wait_bounded(&q_full[q], 0u, kTcWait);
-        for (int s = 0; s < kPrRing; ++s)
-          if (use > s) (void)mbar_wait_bounded(&full[s], (uint32_t)(((use - 1 - s) / kPrRing) & 1), kTcWait);
+      if (lane == 0) {
+        bool cut_q, cut_k;
+        k.q0 = pr_place(a.cu_q, doc, a.q_tokens, &k.nq, &cut_q);
+        k.k0 = pr_place(a.cu_k, doc, a.k_tokens, &k.nk, &cut_k);
+        k.prefix = a.prefix != nullptr ? a.prefix[doc] : 0;
+        k.head = (int)g * a.group + in / a.splits;
+        k.split = in % a.splits;
+        k.r0 = tile * 2 * kPrTile;
+        int n[2], safe[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int lo = k.r0 + q * kPrTile, hi = min(lo + kPrTile, k.nq);
+          n[q] = hi > lo ? (pr_bound(hi - 1, k.nq, k.nk, k.prefix, causal) + kPrTile - 1) / kPrTile : 0;
+          safe[q] = hi > lo ? pr_bound(lo, k.nq, k.nk, k.prefix, causal) / kPrTile : 0;
+        }
+        // this item's share of the key tiles
+        const int all = max(n[0], n[1]);
+        const int j0 = (int)((int64_t)all * k.split / a.splits), j1 = (int)((int64_t)all * (k.split + 1) / a.splits);
+        k.j0 = j0;
+        k.n[0] = min(n[0], j1);
+        k.n[1] = min(n[1], j1);
+        k.safe[0] = safe[0];
+        k.safe[1] = safe[1];
+        const int jobs = max(0, k.n[0] - j0);
+        k.solo = 0;
+        if (k.r0 + kPrTile >= k.nq) {
+          k.solo = 2 - last_q;  // whoever did not end the item before begins
+          if (jobs > 0) last_q = (k.solo - 1) ^ ((jobs - 1) & 1);
+        } else if (k.n[1] > j0) {
+          last_q = 1;
+        }
+        k.odd = 0;
+        k.valid = 1;
+        mbar_arrive(&item_full[i % kPrItems]);
       }
+      u = __shfl_sync(0xFFFFFFFFu, ahead, 0);
+    }
+    // the last CTA to come here leaves the count of items as it was
+    if (lane == 0) {
+      __threadfence();
+      if (atomicAdd(a.next + 1, 1u) == gridDim.x - 1) a.next[0] = a.next[1] = 0;
+    }
+    if (blockIdx.x == 0) {
+      bool bad = false;
+      for (int d = lane; d < a.docs; d += 32) {
+        int n;
+        bool cut_q, cut_k;
+        pr_place(a.cu_q, d, a.q_tokens, &n, &cut_q);
+        pr_place(a.cu_k, d, a.k_tokens, &n, &cut_k);
+        bad = bad || cut_q || cut_k;
+      }
+      if (bad) atomicOr(a.err, MLA_DEVERR_BAD_SLOT);
+    }
+  } else if (warp == 8) {
+    // ================= TMA: K, V of key tile after key tile, the queries behind the first K
+    uint32_t use = 0, loads[2] = {0, 0};  // ring slots, query tiles so far
+    for (uint32_t i = 0; !dead; ++i) {
+      const PrItem& k = item_wait(i);
+      if (dead || !k.valid) break;
+      const int end = max(k.n[0], k.n[1]);
+      if (lane == 0 && k.j0 < end) {
+        auto slot = [&]() -> int {
+          const int s = use % kPrRing;
+          if (use >= kPrRing) tc_wait(&empty[s], (use / kPrRing - 1) & 1u, dead);
+          return s;
+        };
+        auto query = [&](int q, int place) {  // query tile q into buffer `place`
+          if (loads[place] > 0) tc_wait(&q_free[place], (loads[place] - 1) & 1u, dead);
+          if (dead) return;
+          ++loads[place];
+          mbar_arrive_expect_tx(&q_full[place], kPrQ);
+          const uint32_t dst = smem_u32(smem + S::oQ) + place * kPrQ;
+          const int row = k.q0 + k.r0 + q * kPrTile;
+          tma_g2s_3d(dst, &maps.q_nope, 0, k.head, row, &q_full[place]);
+          tma_g2s_3d(dst + kPrUnit, &maps.q_nope, 64, k.head, row, &q_full[place]);
+          tma_g2s_3d(dst + 2 * kPrUnit, &maps.q_pe, 0, k.head, row, &q_full[place]);
+        };
+        for (int j = k.j0; j < end && !dead; ++j) {
+          const int row = k.k0 + j * kPrTile;
+          for (int u = 0; u < 3 && !dead; ++u) {
+            const int s = slot();
+            if (dead) break;
+            const uint32_t dst = smem_u32(smem + S::oRing) + s * kPrUnit;
+            mbar_arrive_expect_tx(&full[s], kPrUnit);
+            if (u < 2)
+              tma_g2s_3d(dst, &maps.k_nope, 64 * u, k.head, row, &full[s]);
+            else
+              tma_g2s_3d(dst, &maps.k_pe, 0, 0, row, &full[s]);
+            ++use;
+          }
+          if (j == k.j0) {  // (their buffers come free later than the ring's slots)
+            if (k.n[0] > j && !dead) query(0, k.solo ? k.solo - 1 : 0);
+            if (k.n[1] > j && !dead) query(1, 1);
+          }
+          for (int u = 0; u < 2 && !dead; ++u) {  // 64 keys, both halves of their columns
+            const int s = slot();
+            if (dead) break;
+            const uint32_t dst = smem_u32(smem + S::oRing) + s * kPrUnit;
+            mbar_arrive_expect_tx(&full[s], kPrUnit);
+            tma_g2s_3d(dst, &maps.v, 0, k.head, row + 64 * u, &full[s]);
+            tma_g2s_3d(dst + kPrUnit / 2, &maps.v, 64, k.head, row + 64 * u, &full[s]);
+            ++use;
+          }
+        }
+      }
+      dead = __any_sync(0xFFFFFFFFu, dead);
+      item_done(i);
+    }
+    if (dead && lane == 0) {  // the copies under way land before the CTA leaves
+      for (int q = 0; q < 2; ++q)
+        if (loads[q] > 0) (void)mbar_wait_bounded(&q_full[q], (loads[q] - 1) & 1u, kTcWait);
+      for (uint32_t s = 0; s < kPrRing; ++s)
+        if (use > s) (void)mbar_wait_bounded(&full[s], ((use - 1 - s) / kPrRing) & 1u, kTcWait);
     }
   } else if (warp == 9) {
     // ================= MMA issuer (the warp together, one elected lane issues)
+    //
+    // A job is a key tile for a softmax warpgroup.  The jobs of an item, in order: key
+    // tile after key tile for both query tiles, or shared out in turn; the buffers
+    // take turns throughout (a job may be missing).  Each step forms O += P V of the
+    // job two steps before and then S of its own job, in the same buffer: the tensor
+    // core keeps the order.
     constexpr uint32_t kBf16 = 1u << 7;
     constexpr uint32_t id_s = tc_idesc(128, 128, 1, false, false) | kBf16;
     constexpr uint32_t id_o = tc_idesc(128, 128, 1, false, true) | kBf16;
     const uint64_t dq = tc_desc(smem_u32(smem + S::oQ), 1024, 2);
     const uint64_t dk = tc_desc(smem_u32(smem + S::oRing), 1024, 2);
     const uint64_t dv = tc_desc_wide(smem_u32(smem + S::oRing), 1024, kPrUnit / 2);
-    const int n0 = (int)uniform((uint32_t)n[0]), n1 = (int)uniform((uint32_t)n[1]);
-    const int jb = (int)uniform((uint32_t)j0), je = max(n0, n1);
-    // unit u of key tile j: 0..2 keys, 3, 4 values
-    auto unit = [&](int j, int u) { return 5 * (j - jb) + u; };
-    auto wait_unit = [&](int i) { tc_wait_warp(&full[i % kPrRing], (uint32_t)((i / kPrRing) & 1), dead); };
-    auto scores = [&](int q, int j, bool last) {
-      if (j == jb) tc_wait_warp(&q_full[q], 0u, dead);
-#pragma unroll 1
-      for (int u = 0; u < 3; ++u) {
-        const int i = unit(j, u);
-        wait_unit(i);
-        tc_after();
-        tc_mma4_f16<2, 2>(tmem + 128 * q, dq + (uint64_t)((q * kPrQ + u * kPrUnit) >> 4),
-                          dk + (uint64_t)((i % kPrRing) * (kPrUnit >> 4)), id_s, u > 0);
-        if (last) tc_commit(&empty[i % kPrRing]);
-      }
-      tc_commit(&s_full[q]);
-    };
-    auto values = [&](int q, int j, bool last) {
-      tc_wait_warp(&p_full[q], (uint32_t)((j - jb) & 1), dead);
-#pragma unroll 1
-      for (int u = 0; u < 2; ++u) {
-        const int i = unit(j, 3 + u);
-        wait_unit(i);
-        tc_after();
-        pr_mma4_pv(tmem + 256 + 128 * q, tmem + 128 * q + 32 * u, dv + (uint64_t)((i % kPrRing) * (kPrUnit >> 4)), id_o,
-                   j > jb || u > 0);
-        if (last) tc_commit(&empty[i % kPrRing]);
-      }
-    };
-    if (jb < je) {
-      if (jb < n0) scores(0, jb, jb >= n1);
-      if (jb < n1) scores(1, jb, true);
-      for (int j = jb; j < je; ++j) {
-        if (j < n0) {
-          values(0, j, j >= n1);
-          if (j + 1 < n0) scores(0, j + 1, j + 1 >= n1);
-          else tc_commit(&o_full[0]);
+    // A job in a word: its key tile's first ring slot modulo 16, and
+    constexpr uint32_t kJob = 16, kFirst = 32, kLast = 64;  // there is one; reads these keys first, last
+    constexpr uint32_t kNew = 128, kEnd = 256;              // its buffer's first of the item, last
+    constexpr uint32_t kQWait = 512, kQFree = 1024, kPlace = 2048;  // queries: wait for, give back, which
+    uint32_t item = 0, slot = 0, mid[2] = {0, 0};
+    int j = 0, j0 = 0, n0 = 0, n1 = 0, solo = 0, fast = 0;
+    bool at_item = false, begun = false, over = false;
+    // The job of a step of buffer q.
+    auto job = [&](int q, bool pending) -> uint32_t {
+      if (fast > 0) {  // the middle of an item
+        --fast;
+        const uint32_t w = slot | (q ? mid[1] : mid[0]);
+        if (solo || q) {
+          ++j;
+          slot = (slot + 5) & 15u;
         }
-        if (j < n1) {
-          values(1, j, true);
-          if (j + 1 < n1) scores(1, j + 1, true);
-          else tc_commit(&o_full[1]);
+        return w;
+      }
+      while (!at_item) {
+        if (over) return 0;
+        // (where work is pending the items behind may wait for it)
+        if (pending && !tc_ready(&item_full[item % kPrItems], (item / kPrItems) & 1u)) return 0;
+        const PrItem& k = item_wait(item);
+        if (dead || !k.valid) {
+          over = true;
+          return 0;
+        }
+        j = j0 = k.j0;
+        n0 = k.n[0];
+        n1 = k.n[1];
+        solo = k.solo;
+        item_done(item);
+        ++item;
+        at_item = j0 < max(n0, n1);
+        begun = false;
+      }
+      const int count = solo ? n0 : n1;  // key tiles up to here
+      if (!begun && q != (solo ? solo - 1 : 0)) return 0;  // the other buffer begins
+      begun = true;
+      uint32_t w = 0;
+      const int mine = solo || q == 0 ? n0 : n1, step = solo ? 2 : 1;
+      if (j < mine) {
+        w = slot | kJob;
+        if (solo || q == 0 || j >= n0) w |= kFirst;
+        if (solo || q == 1) w |= kLast;
+        if (j < j0 + step) w |= kNew;
+        if (j + step >= mine) w |= kEnd;
+        if (j == j0) w |= kQWait;
+        if (j + 1 >= mine) w |= kQFree;
+        if (solo ? solo == 2 : q == 1) w |= kPlace;
+      }
+      if (solo || q) {
+        ++j;
+        slot = (slot + 5) & 15u;
+        at_item = j < count;
+        // jobs in turn that neither begin nor end anything
+        if (at_item && j > j0 + (solo ? 1 : 0)) {
+          fast = solo ? n0 - 2 - j : 2 * (n0 - 1 - j);
+          mid[0] = kJob | kFirst | (solo ? kLast | (solo == 2 ? kPlace : 0) : 0);
+          mid[1] = kJob | kLast | (solo ? kFirst | (solo == 2 ? kPlace : 0) : kPlace);
         }
       }
-      if (dead) {
-        tc_commit(drain);
-        (void)mbar_wait_bounded(drain, 0u, kTcWait);
+      return w;
+    };
+    uint32_t q_uses = 0, p_uses = 0, o_uses = 0, o_first = 0;  // parities and whether O was used, a bit a buffer
+    uint32_t before[2] = {0, 0};  // the jobs of the last two steps
+    for (int step = 0; !dead; ++step) {
+      const int q = step & 1;
+      const uint32_t v = uniform(before[0]), w = uniform(job(q, (before[0] | before[1]) != 0));
+      if (v & kJob) {  // O of buffer q from its P and the values
+        if (v & kNew) {  // (O of the item before has been read)
+          if (o_first >> q & 1u) {
+            tc_wait(&o_free[q], o_uses >> q & 1u, dead);
+            o_uses ^= 1u << q;
+          }
+          o_first |= 1u << q;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t s = (v + 3 + u) & 15u, at = s & 7u;
+          // (A lane's wait that ran out is known to the others at the next vote: until
+          // then products go on over whatever the slots hold, and do not count.)
+          if (v & kFirst) tc_wait(&full[at], s >> 3, dead);
+          tc_wait(&p_full[2 * q + u], p_uses >> q & 1u, dead);
+          tc_after();
+          pr_mma4_pv(tmem + 256 + 128 * q, tmem + 128 * q + 32 * u, dv + (uint64_t)(at * (kPrUnit >> 4)), id_o,
+                     u > 0 || !(v & kNew));
+          if (v & kLast) tc_commit(&empty[at]);
+        }
+        p_uses ^= 1u << q;
+        if (v & kEnd) tc_commit(&o_full[q]);
       }
+      if (w & kJob) {  // S of buffer q from the queries and the keys
+        const int from = w & kPlace ? 1 : 0;
+        if (w & kQWait) {
+          tc_wait(&q_full[from], q_uses >> from & 1u, dead);
+          q_uses ^= 1u << from;
+        }
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+          const uint32_t s = (w + u) & 15u, at = s & 7u;
+          if (w & kFirst) tc_wait(&full[at], s >> 3, dead);
+          tc_after();
+          tc_mma4_f16<2, 2>(tmem + 128 * q, dq + (uint64_t)((from * kPrQ + u * kPrUnit) >> 4),
+                            dk + (uint64_t)(at * (kPrUnit >> 4)), id_s, u > 0);
+          if (w & kLast) tc_commit(&empty[at]);
+        }
+        tc_commit(&s_full[q]);
+        if (w & kQFree) tc_commit(&q_free[from]);
+      }
+      before[0] = before[1];
+      before[1] = w;
+      dead = __any_sync(0xFFFFFFFFu, dead);
+      if (over && !(before[0] & kJob) && !(before[1] & kJob)) break;
+    }
+    if (dead) {
+      tc_commit(drain);
+      (void)mbar_wait_bounded(drain, 0u, kTcWait);
+    }
     }
   } else {
-    // ================= softmax (warps 0-3: query tile 0, 4-7: tile 1)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ================= softmax (warps 0-3: S and O of buffer 0, 4-7: of buffer 1)
     const int q = warp >> 2, quad = warp & 3;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-    const int i = r0 + q * kPrTile + 32 * quad + lane;  // this thread's row of the document
-    const int bound = k.bound(min(i, k.nq - 1), causal);
-    const int nq = n[q];
+    const uint32_t st = tmem + lanes + 128 * q;
     const float scale2 = a.scale * 1.4426950408889634f;
     // capped: x = C - 2 C / (1 + 2^(s e)), e = 2 scale log2(e) / cap, in base 2
     const float capC = CAP ? a.cap * 1.4426950408889634f : 0.f, capE = CAP ? 2.0f * scale2 / a.cap : 0.f;
-    const float slope = BIAS ? -a.slopes[head] * 1.4426950408889634f : 0.f;
-    const float own = (float)(i + k.nk - k.nq);  // its place among the keys
-    float ref = -INFINITY, l = 0.f;
-    for (int j = j0; j < nq; ++j) {
-      const uint32_t st = tmem + lanes + 128 * q;
-      tc_wait(&s_full[q], (uint32_t)((j - j0) & 1), dead);
-      tc_after();
-      float s[128];
+    const float unit2 = CAP || BIAS ? 1.0f : scale2;
+    uint32_t uses = 0;     // jobs of this buffer so far
+    uint32_t o_reads = 0;  // parities of o_full, a bit a buffer
+    uint32_t shares = 0;   // items whose keys were shared out
+    uint32_t ring = 0;     // ring slots of the items before
+    for (uint32_t it = 0; !dead; ++it) {
+      const PrItem& k = item_wait(it);
+      if (dead || !k.valid) break;
+      const int solo = k.solo, qt = solo ? 0 : q;  // its query tile
+      const int j0 = k.j0, nt = k.n[qt], step = solo ? 2 : 1, safe = k.safe[qt];
+      const int jfirst = j0 + (solo && q != solo - 1 ? 1 : 0);
+      const int base_row = k.r0 + qt * kPrTile + 32 * quad;
+      const int i = base_row + lane;  // this thread's row of the document
+      const int bound = pr_bound(min(i, k.nq - 1), k.nq, k.nk, k.prefix, causal);
+      const float slope = BIAS ? -a.slopes[k.head] * 1.4426950408889634f : 0.f;
+      float ref = -INFINITY, l = 0.f;
+      for (int j = jfirst; j < nt; j += step) {
+        // An edge in this tile (for either query tile): its values are looked over by
+        // the first that has it, here, where it would wait for the scores (they do not
+        // wait for the values, nor these for them).  Where keys are shared out the
+        // slot's use before may still be to come, and its parity would be taken for
+        // this one's: there behind the wait, when all units before are known to be in.
+        const bool look = pr_edge(k, j) && (solo || q == 0 || j >= k.n[0]);
+        const auto look_over = [&]() {
+          const int r = 32 * quad + lane;
+          const uint32_t u = ring + 5 * (uint32_t)(j - j0) + 3 + (r >> 6), slot = u % kPrRing;
+          tc_wait(&full[slot], (u / kPrRing) & 1u, dead);
+          if (pr_look_over(smem + S::oRing + slot * kPrUnit + (r & 63) * 128, lane, j * kPrTile + r >= k.nk))
+            *reinterpret_cast<volatile uint32_t*>(const_cast<uint32_t*>(&k.odd)) = 1u;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        };
+        if (look && !solo) look_over();
+        tc_wait(&s_full[q], uses & 1u, dead);
+        ++uses;
+        if (look && solo) look_over();
+        tc_after();
+        float s[128];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tc_ld(st + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
-      tc_wait_ld();
-      tc_landed(s);
-      // Scores to base 2: at once where something is done to them, else with
-      // the subtraction of the reference.
-      if constexpr (CAP) {
-#pragma unroll
-        for (int c = 0; c < 128; ++c) s[c] = fmaf(-2.0f * capC, rcp_approx(1.0f + ex2(s[c] * capE)), capC);
-      }
-      if constexpr (BIAS) {
-        const float base = own - (float)(j * kPrTile);
-#pragma unroll
-        for (int c = 0; c < 128; ++c) {
-          const float x2 = CAP ? s[c] : s[c] * scale2;
-          s[c] = fmaf(slope, fabsf(base - (float)c), x2);
-        }
-      }
-      const float unit2 = CAP || BIAS ? 1.0f : scale2;
-      if (j >= safe[q]) {
+        for (int c = 0; c < 4; ++c) tc_ld(st + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
+        tc_wait_ld();
+        tc_landed(s);
+        const bool edge = j >= safe;
         const int left = bound - j * kPrTile;  // keys of this tile that count
+        // Scores to base 2: at once where something is done to them, else with
+        // the subtraction of the reference.
+        if constexpr (CAP) {
+          if (edge) {  // (neighbours share a reciprocal below)
 #pragma unroll
-        for (int c = 0; c < 128; ++c) s[c] = c < left ? s[c] : -INFINITY;
-      }
-      float m4[4];
+            for (int c = 0; c < 128; ++c) s[c] = c < left ? s[c] : 0.f;
+          }
+          // 1 / (1 + 2^y) for four at a time from one reciprocal of their product:
+          // 2^30 as the largest power keeps that in range (and is 1 - 2^-29 as a tangent)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) m4[e] = fmaxf(s[e], s[e + 4]);
-#pragma unroll
-      for (int c = 8; c < 128; c += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], fmaxf(s[c + e], s[c + e + 4]));
-      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * unit2;
-      // The reference: the first maximum; later only where it is passed by far.
-      const bool grow = mx > ref + kPrRoom || (ref == -INFINITY && mx > -INFINITY);
-      if (__any_sync(0xFFFFFFFFu, grow)) {
-        float f = 1.0f;
-        if (grow) {
-          f = ex2(ref - mx);  // 0 from -infinity
-          ref = mx;
-          l *= f;
+          for (int c = 0; c < 128; c += 4) {
+            const float2 e2 = make_float2(capE, capE), one = make_float2(1.0f, 1.0f);
+            float2 x = fmul2_rn(make_float2(s[c], s[c + 1]), e2), y = fmul2_rn(make_float2(s[c + 2], s[c + 3]), e2);
+            x = add2(make_float2(ex2(min_nan(x.x, 30.0f)), ex2(min_nan(x.y, 30.0f))), one);
+            y = add2(make_float2(ex2(min_nan(y.x, 30.0f)), ex2(min_nan(y.y, 30.0f))), one);
+            const float2 m = fmul2_rn(x, y);  // (x0 y0, x1 y1)
+            const float r = rcp_approx(m.x * m.y);
+            const float2 w = fmul2_rn(make_float2(m.y, m.x), make_float2(r, r));  // 1 / (x0 y0), 1 / (x1 y1)
+            const float2 c2 = make_float2(capC, capC), d2 = make_float2(-2.0f * capC, -2.0f * capC);
+            const float2 t0 = fma2(fmul2_rn(w, y), d2, c2), t1 = fma2(fmul2_rn(w, x), d2, c2);
+            s[c] = t0.x;
+            s[c + 1] = t0.y;
+            s[c + 2] = t1.x;
+            s[c + 3] = t1.y;
+          }
         }
-        if (j > j0) {
-          // (S of this tile was issued after O of the one before: both are done)
+        if constexpr (BIAS) {
+          // distance from this row's place: one sign for the whole warp where the
+          // tile lies on one side of its rows
+          const int near = base_row + (k.nk - k.nq) - j * kPrTile;
+          const float own = (float)(near + lane);
+          const float2 u2 = make_float2(scale2, scale2);
+          if (near >= kPrTile - 1 || near + 31 <= 0) {
+            const float sg = near >= kPrTile - 1 ? slope : -slope;
+            const float2 k0 = make_float2(sg * own, sg * own), k1 = make_float2(-sg, -sg);
+#pragma unroll
+            for (int c = 0; c < 128; c += 2) {
+              const float2 d = fma2(k1, make_float2((float)c, (float)(c + 1)), k0);
+              const float2 x = CAP ? add2(make_float2(s[c], s[c + 1]), d) : fma2(make_float2(s[c], s[c + 1]), u2, d);
+              s[c] = x.x;
+              s[c + 1] = x.y;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) s[c] = fmaf(slope, fabsf(own - (float)c), CAP ? s[c] : s[c] * scale2);
+          }
+        }
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c) s[c] = c < left ? s[c] : -INFINITY;
+        }
+        float m4[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m4[e] = fmaxf(s[e], s[e + 4]);
+#pragma unroll
+        for (int c = 8; c < 128; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], fmaxf(s[c + e], s[c + e + 4]));
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * unit2;
+        // The reference: the first maximum; later only where it is passed by far.
+        const bool grow = mx > ref + kPrRoom || (ref == -INFINITY && mx > -INFINITY);
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+          float f = 1.0f;
+          if (grow) {
+            f = ex2(ref - mx);  // 0 from -infinity
+            ref = mx;
+            l *= f;
+          }
+          if (j > jfirst) {
+            // (S of this tile was issued after O of the one before: both are done)
 #pragma unroll 1
-          for (int c = 0; c < 128; c += 32) {
-            float v[32];
-            const uint32_t at = tmem + lanes + 256 + 128 * q + c;
-            tc_ld(at, v);
+            for (int c = 0; c < 128; c += 32) {
+              float v[32];
+              const uint32_t at = tmem + lanes + 256 + 128 * q + c;
+              tc_ld(at, v);
+              tc_wait_ld();
+              tc_landed(v);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] *= f;
+              tc_st32(at, v);
+            }
+          }
+        }
+        const float minus = ref == -INFINITY ? 0.f : -ref;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float pk[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float2 e = fma2(make_float2(s[64 * half + 2 * c], s[64 * half + 2 * c + 1]), make_float2(unit2, unit2),
+                                  make_float2(minus, minus));
+            const float2 p = make_float2(ex2(e.x), ex2(e.y));
+            sum[c & 1] = add2(sum[c & 1], p);
+            pk[c] = __uint_as_float(pack_bf16x2(p.x, p.y));
+          }
+          tc_st32(st + 32 * half, pk);
+          tc_wait_st();
+          tc_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * q + half]);
+        }
+        const float2 both = add2(sum[0], sum[1]);
+        l += both.x + both.y;
+      }
+      // ---- the sums: of a query tile whose keys were shared out, whoever began
+      // takes both buffers
+      const int end = max(k.n[0], k.n[1]), jobs = max(0, nt - j0);
+      const int lead = solo - 1;  // (of a shared one)
+      const bool shared = solo && jobs > 1;
+      const bool mine = solo ? q == lead : true;
+      const int other = q ^ 1;
+      float f0 = 1.0f, f1 = 0.f;  // what this buffer's and the other's sums are taken times
+      if (shared) {
+        volatile float2* at = ml + 128 * (shares & 1u) + 32 * quad + lane;
+        if (!mine) {
+          at->x = ref;
+          at->y = l;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ml_full[shares & 1u]);
+        } else {
+          tc_wait(&ml_full[shares & 1u], (shares >> 1) & 1u, dead);
+          const float ref1 = at->x, l1 = at->y;
+          const float m = fmaxf(ref, ref1);
+          if (m > -INFINITY) {
+            f0 = ex2(ref - m);
+            f1 = ex2(ref1 - m);
+            l = l * f0 + l1 * f1;
+            ref = m;
+          }
+        }
+        ++shares;
+      }
+      const bool used = solo ? jobs > (mine ? 0 : 1) : nt > j0;  // this buffer
+      const bool used1 = solo ? jobs > (mine ? 1 : 0) : k.n[other] > j0;
+      if (mine) {
+        if (used) tc_wait(&o_full[q], o_reads >> q & 1u, dead);
+        if (shared) tc_wait(&o_full[other], o_reads >> other & 1u, dead);
+        tc_after();
+        const bool have = i < k.nq, part = a.splits > 1;
+        const int64_t row = k.q0 + i;
+        const float inv = part ? 1.0f : l == 0.f ? 0.f : 1.0f / l;
+        f0 *= inv;
+        f1 *= inv;
+        if (have) {
+          if (part)
+            a.part_ml[((int64_t)k.split * a.heads + k.head) * a.q_tokens + row] = make_float2(ref, l);
+          else if (a.lse != nullptr)
+            a.lse[row * a.heads + k.head] = l == 0.f ? -INFINITY : ref * 0.6931471805599453f + logf(l);
+        }
+        // Four neighbouring lanes trade 16-byte pieces, so that they store 64 bytes of
+        // one row after another: 8 rows an instruction, not 32.
+        const int sub = lane & 3;
+        const int left = k.nq - (i - sub);  // rows from the first of the four on
+        float* po = a.part_o + (((int64_t)k.split * a.heads + k.head) * a.q_tokens + row) * 128;
+        uint16_t* o = a.out + (row - sub) * a.o_ts + (int64_t)k.head * a.o_hs + 8 * sub;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          float v[32];
+          if (used) {
+            tc_ld(tmem + lanes + 256 + 128 * q + c, v);
             tc_wait_ld();
             tc_landed(v);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] *= f;
-            tc_st32(at, v);
           }
-        }
-      }
-      const float minus = ref == -INFINITY ? 0.f : -ref;
-      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          if (shared) {
+            float w[32];
+            tc_ld(tmem + lanes + 256 + 128 * other + c, w);
+            tc_wait_ld();
+            tc_landed(w);
+            // (a buffer whose rows saw nothing holds zeros)
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float pk[32];
+            for (int e = 0; e < 32; ++e) v[e] = fmaf(w[e], f1, v[e] * f0);
+          } else {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float2 e = fma2(make_float2(s[64 * half + 2 * c], s[64 * half + 2 * c + 1]), make_float2(unit2, unit2),
-                                make_float2(minus, minus));
-          const float2 p = make_float2(ex2(e.x), ex2(e.y));
-          sum[c & 1] = add2(sum[c & 1], p);
-          pk[c] = __uint_as_float(pack_bf16x2(p.x, p.y));
-        }
-        tc_st32(st + 32 * half, pk);
-      }
-      const float2 both = add2(sum[0], sum[1]);
-      l += both.x + both.y;
-      // An edge in this tile (for either query tile): its values are looked over
-      // by the first of the two that still has it.
-      const bool edge = (j < n[0] && j >= safe[0]) || (j < n[1] && j >= safe[1]);
-      if (edge && (q == 0 || j >= n[0])) {
-        const int r = 32 * quad + lane, u = 5 * (j - j0) + 3 + (r >> 6), slot = u % kPrRing;
-        tc_wait(&full[slot], (uint32_t)((u / kPrRing) & 1), dead);
-        uint8_t* base = smem + S::oRing + slot * kPrUnit + (r & 63) * 128;
-        const int key = j * kPrTile + r;
-        if (key >= k.nk) {
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            *reinterpret_cast<uint4*>(base + (c >> 3) * (kPrUnit / 2) + (((c + lane) & 7) << 4)) = make_uint4(0, 0, 0, 0);
-        } else {
-          uint32_t mag = 0;
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const uint4 w = *reinterpret_cast<const uint4*>(base + (c >> 3) * (kPrUnit / 2) + (((c + lane) & 7) << 4));
-            const uint32_t g = 0x7FFF7FFFu;
-            mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(w.x & g, w.y & g), __vmaxu2(w.z & g, w.w & g)));
+            for (int e = 0; e < 32; ++e) v[e] *= f0;
           }
-          if ((mag & 0xFFFFu) >= 0x7F80u || (mag >> 16) >= 0x7F80u) {
-#pragma unroll 1
-            for (int c = 0; c < 128; ++c) {
-              // chunk c / 8 of the row lies where the 128-byte swizzle puts it
-              uint16_t* e = reinterpret_cast<uint16_t*>(base + (c >> 6) * (kPrUnit / 2) +
-                                                        ((((c >> 3) & 7) ^ (r & 7)) << 4)) + (c & 7);
-              const uint32_t w = *e;
-              if ((w & 0x7F80u) == 0x7F80u) {
-                const int kind = (w & 0x7Fu) != 0 ? 0 : (w & 0x8000u) == 0 ? 1 : 2;
-                atomicMin(&bad[kind * 128 + c], key);
-                *e = 0;
+          if (c == 96) {  // the sums are read: the buffers may be used again
+            tc_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (used) mbar_arrive(&o_free[q]);
+              if (shared) mbar_arrive(&o_free[other]);
+            }
+          }
+          if (!used || l == 0.f) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = 0.f;
+          }
+          if (part) {
+            if (have) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4*>(po + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+            }
+          } else {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+#pragma unroll
+            for (int x = 1; x <= 2; x *= 2) {
+              const bool up = (sub & x) != 0;
+#pragma unroll
+              for (int p = 0; p < 4; ++p) {
+                if (p & x) continue;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {  // piece p + x of the lower lane for piece p of the upper one
+                  const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? w[4 * p + e] : w[4 * (p + x) + e], x);
+                  w[4 * p + e] = up ? got : w[4 * p + e];
+                  w[4 * (p + x) + e] = up ? w[4 * (p + x) + e] : got;
+                }
               }
             }
-            *any_bad = 1;
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+              if (p < left)
+                *reinterpret_cast<uint4*>(o + p * a.o_ts + c) = make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
           }
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-      }
-      tc_wait_st();
-      tc_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[q]);
-    }
-    // ---- the sums
-    if (nq > j0) {
-      tc_wait(&o_full[q], 0u, dead);
-      tc_after();
-    }
-    const bool have = i < k.nq;
-    const int64_t row = k.q0 + i;
-    const bool part = a.splits > 1;
-    const float inv = part ? 1.0f : l == 0.f ? 0.f : 1.0f / l;
-    const bool noted = nq > j0 && *any_bad != 0;
-    if (have) {
-      if (part)
-        a.part_ml[((int64_t)blockIdx.z * a.heads + head) * a.q_tokens + row] = make_float2(ref, l);
-      else if (a.lse != nullptr)
-        a.lse[row * a.heads + head] = l == 0.f ? -INFINITY : ref * 0.6931471805599453f + logf(l);
-    }
-    float* po = a.part_o + (((int64_t)blockIdx.z * a.heads + head) * a.q_tokens + row) * 128;
-    uint16_t* o = a.out + row * a.o_ts + (int64_t)head * a.o_hs;
-#pragma unroll 1
-    for (int c = 0; c < 128; c += 32) {
-      float v[32];
-      if (nq > j0) {
-        tc_ld(tmem + lanes + 256 + 128 * q + c, v);
-        tc_wait_ld();
-        tc_landed(v);
-      }
-#pragma unroll
-      for (int e = 0; e < 32; ++e) v[e] = nq > j0 && l != 0.f ? v[e] * inv : 0.f;
-      if (noted && l != 0.f) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const bool nan = bad[c + e] < bound, up = bad[128 + c + e] < bound, down = bad[256 + c + e] < bound;
-          if (nan || up || down) v[e] = nan || (up && down) ? __int_as_float(0x7FC00000) : v[e] + (up ? INFINITY : -INFINITY);
+        if (*reinterpret_cast<volatile uint32_t*>(const_cast<uint32_t*>(&k.odd)) != 0u) {
+          __syncwarp();  // (the row's pieces are other lanes' stores)
+          __threadfence_block();
+          if (have && l != 0.f) pr_add_odd(a, k, j0, end, bound, part ? po : nullptr, a.out + row * a.o_ts + (int64_t)k.head * a.o_hs);
         }
       }
-      if (have) {
-        if (part) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(po + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(o + c + e) =
-                make_uint4(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]), pack_bf16x2(v[e + 4], v[e + 5]),
-                           pack_bf16x2(v[e + 6], v[e + 7]));
-        }
-      }
+      if (used) o_reads ^= 1u << q;
+      if (used1) o_reads ^= 1u << other;
+      if (j0 < end) ring += 5 * (uint32_t)(end - j0);
+      dead = __any_sync(0xFFFFFFFFu, dead);
+      item_done(it);
     }
-    tc_before();
   }
   if (dead) atomicOr(a.err, MLA_DEVERR_TIMEOUT);
   __syncwarp();
@@ -587,9 +955,9 @@ bool encode_heads_map(CUtensorMap* map, const void* base, int64_t tokens, int he
 }
 
 template <bool CAP, bool BIAS>
-cudaError_t launch_prompt_kernel(const PromptArgs& a, const PromptMaps& maps, int tiles, cudaStream_t stream) {
+cudaError_t launch_prompt_kernel(const PromptArgs& a, const PromptMaps& maps, int ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)tiles, (unsigned)a.heads, (unsigned)a.splits);
+  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kPrThreads);
   cfg.dynamicSmemBytes = PrSmem::kBytes;
   cfg.stream = stream;
@@ -616,7 +984,7 @@ cudaError_t prepare_prompt() {
   return e;
 }
 
-cudaError_t launch_prompt(const PromptArgs& a, const PromptInputs& in, int tiles, cudaStream_t stream) {
+cudaError_t launch_prompt(const PromptArgs& a, const PromptInputs& in, int ctas, cudaStream_t stream) {
   PromptMaps maps = {};
   const int keys = a.k_tokens > 0 ? a.k_tokens : 1;
   if (!encode_heads_map(&maps.q_nope, in.q_nope, a.q_tokens, a.heads, kNope, in.qn_ts, in.qn_hs, kPrTile) ||
@@ -626,10 +994,10 @@ cudaError_t launch_prompt(const PromptArgs& a, const PromptInputs& in, int tiles
       !encode_heads_map(&maps.v, in.v, keys, a.heads, kNope, in.v_ts, in.v_hs, kPrTile / 2))
     return cudaErrorInvalidValue;
   const bool cap = a.cap > 0.f, bias = a.slopes != nullptr;
-  cudaError_t e = cap ? (bias ? launch_prompt_kernel<true, true>(a, maps, tiles, stream)
-                              : launch_prompt_kernel<true, false>(a, maps, tiles, stream))
-                      : (bias ? launch_prompt_kernel<false, true>(a, maps, tiles, stream)
-                              : launch_prompt_kernel<false, false>(a, maps, tiles, stream));
+  cudaError_t e = cap ? (bias ? launch_prompt_kernel<true, true>(a, maps, ctas, stream)
+                              : launch_prompt_kernel<true, false>(a, maps, ctas, stream))
+                      : (bias ? launch_prompt_kernel<false, true>(a, maps, ctas, stream)
+                              : launch_prompt_kernel<false, false>(a, maps, ctas, stream));
   if (e != cudaSuccess || a.splits == 1) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(((int64_t)a.q_tokens * a.heads + 7) / 8));
@@ -780,7 +1148,18 @@ int mla_prompt_attn(mla_prompt_t h, int docs, int64_t q_tokens, int64_t k_tokens
   const int64_t tiles = (q_tokens + (int64_t)(2 * mla::kPrTile - 1) * docs) / (2 * mla::kPrTile);
   a.splits = mla::prompt_splits(tiles * h->heads, q_tokens * h->heads,
                                 (k_tokens / docs + mla::kPrTile - 1) / mla::kPrTile, h->num_sms);
-  return mla::launched(mla::launch_prompt(a, in, (int)tiles, static_cast<cudaStream_t>(stream)));
+  const int64_t items = tiles * h->heads * a.splits;
+  // Heads whose tiles are handed out together, longest first: enough for four items
+  // an SM, so that short ones are left for the end; no more, so that their keys
+  // stay in L2.
+  const int64_t group = (4 * (int64_t)h->num_sms + tiles * a.splits - 1) / (tiles * a.splits);
+  a.group = (int)(group < h->heads ? group : h->heads);
+  a.next = h->err + 2;
+  a.v = static_cast<const uint16_t*>(in.v);
+  a.v_ts = in.v_ts;
+  a.v_hs = in.v_hs;
+  return mla::launched(mla::launch_prompt(a, in, (int)(items < h->num_sms ? items : h->num_sms),
+                                          static_cast<cudaStream_t>(stream)));
 }
 
 int mla_prompt_get_error(mla_prompt_t h, unsigned* device_flags, void* stream) {
