@@ -16,8 +16,9 @@
 //
 //  * A softmax thread owns one query row: its maximum, its sum and its mask need
 //    no other lane.  The row's reference (what exponents are taken relative to)
-//    moves only when a score passes it by more than 2^8, and only then is O
-//    rescaled: P then reaches 256, as exact in BF16 as at 1.
+//    is its first tile's maximum, and moves only when a score passes it by more
+//    than 20 in base 2; only then is O rescaled.  P then reaches 2^20, as exact in
+//    BF16 as at 1, and what is summed stays far below FP32's limits.
 //  * What a row sees are the first `bound` keys of its document: its own place
 //    and all before it, or its document's two-way prefix, or all.  Tiles that no
 //    row of theirs needs are not touched, and only those on an edge are masked.
@@ -55,7 +56,7 @@ constexpr int kPrUnit = 16384;   // bytes of a ring slot
 constexpr int kPrRing = 8;
 constexpr int kPrThreads = 384;  // two softmax warpgroups; warps that load, multiply, hand out work (and one idle)
 constexpr int kPrQ = 3 * kPrUnit;  // a query tile: planes of 64 columns
-constexpr float kPrRoom = 8.0f;  // base 2
+constexpr float kPrRoom = 20.0f;  // base 2
 constexpr int kPrChunks = 96;    // sums of the documents' tiles
 constexpr int kPrItems = 4;      // items of work in flight
 constexpr int kPrReaders = 10;   // warps that read them
@@ -114,9 +115,31 @@ __device__ __forceinline__ void tma_g2s_3d(uint32_t dst, const CUtensorMap* map,
       : "memory");
 }
 
+// The same value, which the compiler does not know: a loop with a branch on it is
+// not made into two loops.
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {
+  asm volatile("" : "+r"(v));
+  return v;
+}
+
+// A bounded wait that gives up for good.
+__device__ __forceinline__ bool pr_wait_long(uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, kTcWait); }
+__device__ __forceinline__ void pr_wait(uint64_t* bar, uint32_t parity, bool& dead) {
+  if (!dead && !pr_wait_long(bar, parity)) dead = true;
+}
+__device__ __forceinline__ void pr_wait_warp(uint64_t* bar, uint32_t parity, bool& dead) {
+  pr_wait(bar, parity, dead);
+  dead = __any_sync(0xFFFFFFFFu, dead);
+}
+
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 // The smaller, or NaN.
@@ -154,25 +177,25 @@ __device__ __forceinline__ int pr_tiles(const PromptArgs& a, int d) {
 // key lies behind its document; else what is not finite becomes zero.  Whether
 // there was any.
 __device__ __noinline__ bool pr_look_over(uint8_t* base, int lane, bool behind) {
-  if (behind) {
-#pragma unroll
-    for (int c = 0; c < 16; ++c)
-      *reinterpret_cast<uint4*>(base + (c >> 3) * (kPrUnit / 2) + (((c + lane) & 7) << 4)) = make_uint4(0, 0, 0, 0);
-    return false;
-  }
-  uint32_t mag = 0;
-#pragma unroll
-  for (int c = 0; c < 16; ++c) {
-    const uint4 w = *reinterpret_cast<const uint4*>(base + (c >> 3) * (kPrUnit / 2) + (((c + lane) & 7) << 4));
-    const uint32_t g = 0x7FFF7FFFu;
-    mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(w.x & g, w.y & g), __vmaxu2(w.z & g, w.w & g)));
-  }
-  if ((mag & 0xFFFFu) < 0x7F80u && (mag >> 16) < 0x7F80u) return false;
+  uint32_t odd = 0;
 #pragma unroll 1
-  for (int c = 0; c < 64; ++c) {
-    uint16_t* e = reinterpret_cast<uint16_t*>(base) + c;
-    if ((*e & 0x7F80u) == 0x7F80u) *e = 0;
-    e += kPrUnit / 4;
+  for (int half = 0; half < kPrUnit; half += kPrUnit / 2) {
+#pragma unroll 4
+    for (int c = 0; c < 8; ++c) {
+      uint4* at = reinterpret_cast<uint4*>(base + half + (((c + lane) & 7) << 4));
+      if (behind) {
+        *at = make_uint4(0, 0, 0, 0);
+      } else {
+        const uint4 w = *at;  // an exponent of all ones carries into the place of its sign
+        const uint32_t g = 0x7F807F80u, one = 0x00800080u;
+        odd |= (((w.x & g) + one) | ((w.y & g) + one)) | (((w.z & g) + one) | ((w.w & g) + one));
+      }
+    }
+  }
+  if ((odd & 0x80008000u) == 0) return false;
+#pragma unroll 1
+  for (int c = 0; c < 128; ++c) {
+    uint16_t* e = reinterpret_cast<uint16_t*>(base + (c >> 6) * (kPrUnit / 2)) + (c & 63);
     if ((*e & 0x7F80u) == 0x7F80u) *e = 0;
   }
   return true;
@@ -183,10 +206,13 @@ __device__ __noinline__ bool pr_look_over(uint8_t* base, int lane, bool behind) 
 // keys, its sums (`part`) or its output.  Slow, and rare.
 __device__ __noinline__ void pr_add_odd(const PromptArgs& a, const PrItem& k, int j0, int end, int bound, float* part,
                                         uint16_t* out) {
+#pragma unroll 1
   for (int c = 0; c < 128; c += 4) {
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
     for (int j = j0; j < end; ++j) {
       if (!pr_edge(k, j)) continue;
+#pragma unroll 1
       for (int key = j * kPrTile, e = min(min(key + kPrTile, bound), k.nk); key < e; ++key) {
         const uint2 w =
             *reinterpret_cast<const uint2*>(a.v + (int64_t)(k.k0 + key) * a.v_ts + (int64_t)k.head * a.v_hs + c);
@@ -273,6 +299,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   pdl_launch_dependents();
   if (tid < kPrChunks) {
     int sum = 0;
+#pragma unroll 1
     for (int d = tid * each, e = min(a.docs, d + each); d < e; ++d) sum += pr_tiles(a, d);
     scan[tid] = sum;
   }
@@ -284,7 +311,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 
   // What each reader of the items does: the next one, and that it is done with one.
   auto item_wait = [&](uint32_t i) -> const PrItem& {
-    tc_wait_warp(&item_full[i % kPrItems], (i / kPrItems) & 1u, dead);
+    pr_wait_warp(&item_full[i % kPrItems], (i / kPrItems) & 1u, dead);
     return items[i % kPrItems];
   };
   auto item_done = [&](uint32_t i) {
@@ -312,11 +339,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const uint32_t total = (uint32_t)tiles * (uint32_t)a.heads * (uint32_t)a.splits;
     uint32_t u = blockIdx.x;
     int at = -1, doc = 0, tile = 0, last_q = 1;
+#pragma unroll 1
     for (uint32_t i = 0;; ++i) {
       // ahead: the answer is there by the time it is needed
       uint32_t ahead = 0;
       if (lane == 0 && u < total) ahead = atomicAdd(a.next, 1u) + gridDim.x;
-      if (i >= kPrItems) tc_wait_warp(&item_free[i % kPrItems], (i / kPrItems - 1) & 1u, dead);
+      if (i >= kPrItems) pr_wait_warp(&item_free[i % kPrItems], (i / kPrItems - 1) & 1u, dead);
       PrItem& k = items[i % kPrItems];
       if (u >= total || dead) {
         if (lane == 0) {
@@ -331,17 +359,19 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const uint32_t g = u / per_group, r = u - g * per_group;
       const int heads = min(a.group, a.heads - (int)g * a.group);
       const uint32_t row = (uint32_t)(heads * a.splits);
-      const int x = tiles - 1 - (int)(r / row);
-      const int in = (int)(r % row);
+      const uint32_t nth = r / row;
+      const int x = tiles - 1 - (int)nth, in = (int)(r - nth * row);
       if (x != at) {
         at = x;
         // the lane whose sums hold x, its sum, then the document
         const unsigned who = __ballot_sync(0xFFFFFFFFu, x >= before && x < before + mine);
         const int src = __ffs(who) - 1;
         int b = before, c = lane * kOwn;
+#pragma unroll 1
         while (lane == src && x >= b + scan[c]) b += scan[c++];
         b = __shfl_sync(0xFFFFFFFFu, b, src);
         c = __shfl_sync(0xFFFFFFFFu, c, src);
+#pragma unroll 1
         for (int d0 = c * each;; d0 += 32) {
           const int d = d0 + lane;
           int n = d < min(a.docs, (c + 1) * each) ? pr_tiles(a, d) : 0;
@@ -367,8 +397,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         k.q0 = pr_place(a.cu_q, doc, a.q_tokens, &k.nq, &cut_q);
         k.k0 = pr_place(a.cu_k, doc, a.k_tokens, &k.nk, &cut_k);
         k.prefix = a.prefix != nullptr ? a.prefix[doc] : 0;
-        k.head = (int)g * a.group + in / a.splits;
-        k.split = in % a.splits;
+        k.head = (int)(g * (uint32_t)a.group + (uint32_t)in / (uint32_t)a.splits);
+        k.split = in - (k.head - (int)g * a.group) * a.splits;
         k.r0 = tile * 2 * kPrTile;
         int n[2], safe[2];
 #pragma unroll
@@ -379,7 +409,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         }
         // this item's share of the key tiles
         const int all = max(n[0], n[1]);
-        const int j0 = (int)((int64_t)all * k.split / a.splits), j1 = (int)((int64_t)all * (k.split + 1) / a.splits);
+        const int j0 = (int)((uint32_t)(all * k.split) / (uint32_t)a.splits);  // (below 2^21 tiles, 64 parts)
+        const int j1 = (int)((uint32_t)(all * (k.split + 1)) / (uint32_t)a.splits);
         k.j0 = j0;
         k.n[0] = min(n[0], j1);
         k.n[1] = min(n[1], j1);
@@ -406,6 +437,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     }
     if (blockIdx.x == 0) {
       bool bad = false;
+#pragma unroll 1
       for (int d = lane; d < a.docs; d += 32) {
         int n;
         bool cut_q, cut_k;
@@ -417,7 +449,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     }
   } else if (warp == 8) {
     // ================= TMA: K, V of key tile after key tile, the queries behind the first K
-    uint32_t use = 0, loads[2] = {0, 0};  // ring slots, query tiles so far
+    uint32_t use = 0;                // ring slots so far
+    uint32_t loads = 0, q_uses = 0;  // query buffers: used, parity of q_free; a bit a buffer
     for (uint32_t i = 0; !dead; ++i) {
       const PrItem& k = item_wait(i);
       if (dead || !k.valid) break;
@@ -425,23 +458,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       if (lane == 0 && k.j0 < end) {
         auto slot = [&]() -> int {
           const int s = use % kPrRing;
-          if (use >= kPrRing) tc_wait(&empty[s], (use / kPrRing - 1) & 1u, dead);
+          if (use >= kPrRing) pr_wait(&empty[s], (use / kPrRing - 1) & 1u, dead);
           return s;
-        };
-        auto query = [&](int q, int place) {  // query tile q into buffer `place`
-          if (loads[place] > 0) tc_wait(&q_free[place], (loads[place] - 1) & 1u, dead);
-          if (dead) return;
-          ++loads[place];
-          mbar_arrive_expect_tx(&q_full[place], kPrQ);
-          const uint32_t dst = smem_u32(smem + S::oQ) + place * kPrQ;
-          const int row = k.q0 + k.r0 + q * kPrTile;
-          tma_g2s_3d(dst, &maps.q_nope, 0, k.head, row, &q_full[place]);
-          tma_g2s_3d(dst + kPrUnit, &maps.q_nope, 64, k.head, row, &q_full[place]);
-          tma_g2s_3d(dst + 2 * kPrUnit, &maps.q_pe, 0, k.head, row, &q_full[place]);
         };
         for (int j = k.j0; j < end && !dead; ++j) {
           const int row = k.k0 + j * kPrTile;
-          for (int u = 0; u < 3 && !dead; ++u) {
+#pragma unroll
+          for (int u = 0; u < 3; ++u) {
             const int s = slot();
             if (dead) break;
             const uint32_t dst = smem_u32(smem + S::oRing) + s * kPrUnit;
@@ -452,11 +475,30 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               tma_g2s_3d(dst, &maps.k_pe, 0, 0, row, &full[s]);
             ++use;
           }
-          if (j == k.j0) {  // (their buffers come free later than the ring's slots)
-            if (k.n[0] > j && !dead) query(0, k.solo ? k.solo - 1 : 0);
-            if (k.n[1] > j && !dead) query(1, 1);
+          if (j == k.j0) {
+            // the queries (their buffers come free later than the ring's slots): tile
+            // q into buffer `place`
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+              if (k.n[q] <= j) continue;
+              const int place = k.solo ? k.solo - 1 : q;
+              if (loads >> place & 1u) {
+                pr_wait(&q_free[place], q_uses >> place & 1u, dead);
+                q_uses ^= 1u << place;
+              }
+              if (dead) break;
+              loads |= 1u << place;
+              mbar_arrive_expect_tx(&q_full[place], kPrQ);
+              const uint32_t dst = smem_u32(smem + S::oQ) + place * kPrQ;
+              const int at = k.q0 + k.r0 + q * kPrTile;
+              tma_g2s_3d(dst, &maps.q_nope, 0, k.head, at, &q_full[place]);
+              tma_g2s_3d(dst + kPrUnit, &maps.q_nope, 64, k.head, at, &q_full[place]);
+              tma_g2s_3d(dst + 2 * kPrUnit, &maps.q_pe, 0, k.head, at, &q_full[place]);
+            }
           }
-          for (int u = 0; u < 2 && !dead; ++u) {  // 64 keys, both halves of their columns
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {  // 64 keys, both halves of their columns
+            if (dead) break;
             const int s = slot();
             if (dead) break;
             const uint32_t dst = smem_u32(smem + S::oRing) + s * kPrUnit;
@@ -471,10 +513,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       item_done(i);
     }
     if (dead && lane == 0) {  // the copies under way land before the CTA leaves
-      for (int q = 0; q < 2; ++q)
-        if (loads[q] > 0) (void)mbar_wait_bounded(&q_full[q], (loads[q] - 1) & 1u, kTcWait);
+      for (int q = 0; q < 2; ++q)  // (as often waited for as loaded, but for the last time)
+        if (loads >> q & 1u) (void)pr_wait_long(&q_full[q], q_uses >> q & 1u);
+#pragma unroll 1
       for (uint32_t s = 0; s < kPrRing; ++s)
-        if (use > s) (void)mbar_wait_bounded(&full[s], ((use - 1 - s) / kPrRing) & 1u, kTcWait);
+        if (use > s) (void)pr_wait_long(&full[s], ((use - 1 - s) / kPrRing) & 1u);
     }
   } else if (warp == 9) {
     // ================= MMA issuer (the warp together, one elected lane issues)
@@ -555,14 +598,15 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       return w;
     };
     uint32_t q_uses = 0, p_uses = 0, o_uses = 0, o_first = 0;  // parities and whether O was used, a bit a buffer
-    uint32_t before[2] = {0, 0};  // the jobs of the last two steps
+    // The jobs of the last two steps and of this one.
+    uint32_t before[2] = {0, 0}, w = uniform(job(0, false));
     for (int step = 0; !dead; ++step) {
       const int q = step & 1;
-      const uint32_t v = uniform(before[0]), w = uniform(job(q, (before[0] | before[1]) != 0));
+      const uint32_t v = before[0];
       if (v & kJob) {  // O of buffer q from its P and the values
         if (v & kNew) {  // (O of the item before has been read)
           if (o_first >> q & 1u) {
-            tc_wait(&o_free[q], o_uses >> q & 1u, dead);
+            pr_wait(&o_free[q], o_uses >> q & 1u, dead);
             o_uses ^= 1u << q;
           }
           o_first |= 1u << q;
@@ -572,8 +616,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           const uint32_t s = (v + 3 + u) & 15u, at = s & 7u;
           // (A lane's wait that ran out is known to the others at the next vote: until
           // then products go on over whatever the slots hold, and do not count.)
-          if (v & kFirst) tc_wait(&full[at], s >> 3, dead);
-          tc_wait(&p_full[2 * q + u], p_uses >> q & 1u, dead);
+          if (v & kFirst) pr_wait(&full[at], s >> 3, dead);
+          pr_wait(&p_full[2 * q + u], p_uses >> q & 1u, dead);
           tc_after();
           pr_mma4_pv(tmem + 256 + 128 * q, tmem + 128 * q + 32 * u, dv + (uint64_t)(at * (kPrUnit >> 4)), id_o,
                      u > 0 || !(v & kNew));
@@ -585,13 +629,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       if (w & kJob) {  // S of buffer q from the queries and the keys
         const int from = w & kPlace ? 1 : 0;
         if (w & kQWait) {
-          tc_wait(&q_full[from], q_uses >> from & 1u, dead);
+          pr_wait(&q_full[from], q_uses >> from & 1u, dead);
           q_uses ^= 1u << from;
         }
 #pragma unroll
         for (int u = 0; u < 3; ++u) {
           const uint32_t s = (w + u) & 15u, at = s & 7u;
-          if (w & kFirst) tc_wait(&full[at], s >> 3, dead);
+          if (w & kFirst) pr_wait(&full[at], s >> 3, dead);
           tc_after();
           tc_mma4_f16<2, 2>(tmem + 128 * q, dq + (uint64_t)((from * kPrQ + u * kPrUnit) >> 4),
                             dk + (uint64_t)(at * (kPrUnit >> 4)), id_s, u > 0);
@@ -603,11 +647,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       before[0] = before[1];
       before[1] = w;
       dead = __any_sync(0xFFFFFFFFu, dead);
-      if (over && !(before[0] & kJob) && !(before[1] & kJob)) break;
+      w = uniform(job(q ^ 1, (before[0] | before[1]) != 0));
+      if (over && !((before[0] | before[1] | w) & kJob)) break;
     }
     if (dead) {
       tc_commit(drain);
-      (void)mbar_wait_bounded(drain, 0u, kTcWait);
+      (void)pr_wait_long(drain, 0u);
     }
     }
   } else {
@@ -642,77 +687,95 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         // slot's use before may still be to come, and its parity would be taken for
         // this one's: there behind the wait, when all units before are known to be in.
         const bool look = pr_edge(k, j) && (solo || q == 0 || j >= k.n[0]);
-        const auto look_over = [&]() {
+        if (solo) pr_wait(&s_full[q], uses & 1u, dead);
+        if (look) {
           const int r = 32 * quad + lane;
           const uint32_t u = ring + 5 * (uint32_t)(j - j0) + 3 + (r >> 6), slot = u % kPrRing;
-          tc_wait(&full[slot], (u / kPrRing) & 1u, dead);
+          pr_wait(&full[slot], (u / kPrRing) & 1u, dead);
           if (pr_look_over(smem + S::oRing + slot * kPrUnit + (r & 63) * 128, lane, j * kPrTile + r >= k.nk))
             *reinterpret_cast<volatile uint32_t*>(const_cast<uint32_t*>(&k.odd)) = 1u;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-        };
-        if (look && !solo) look_over();
-        tc_wait(&s_full[q], uses & 1u, dead);
+        }
+        if (!solo) pr_wait(&s_full[q], uses & 1u, dead);
         ++uses;
-        if (look && solo) look_over();
         tc_after();
+        const uint32_t at_edge = j >= safe;
+        const int left = bound - j * kPrTile;  // keys of this tile that count
+        // What is done to the scores before their maximum where it takes many
+        // instructions (caps, and keys on both sides of a biased row): 32 columns at a
+        // time and back to TMEM, in a loop.  (Its code for all 128 at once drove the rest
+        // out of the instruction cache: 24 documents of 100 to 1,000 rows took 579 us
+        // capped, so 390.)
+        const int near = base_row + (k.nk - k.nq) - j * kPrTile;  // the warp's first row among the tile's keys
+        const bool apart = CAP || (BIAS && (at_edge || !(near >= kPrTile - 1 || near + 31 <= 0)));
+        if (apart) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < 128; c0 += 32) {
+            const int count = left - c0;
+            float s[32];
+            tc_ld(st + c0, s);
+            tc_wait_ld();
+            tc_landed(s);
+            if constexpr (CAP) {
+              if (opaque(at_edge)) {  // (neighbours share a reciprocal below)
+#pragma unroll
+                for (int c = 0; c < 32; ++c) s[c] = c < count ? s[c] : 0.f;
+              }
+              // 1 / (1 + 2^y) for four at a time from one reciprocal of their product:
+              // 2^30 as the largest power keeps that in range (and is 1 - 2^-29 as a tangent)
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                const float2 e2 = make_float2(capE, capE), one = make_float2(1.0f, 1.0f);
+                float2 x = fmul2_rn(make_float2(s[c], s[c + 1]), e2), y = fmul2_rn(make_float2(s[c + 2], s[c + 3]), e2);
+                x = add2(make_float2(ex2(min_nan(x.x, 30.0f)), ex2(min_nan(x.y, 30.0f))), one);
+                y = add2(make_float2(ex2(min_nan(y.x, 30.0f)), ex2(min_nan(y.y, 30.0f))), one);
+                const float2 m = fmul2_rn(x, y);  // (x0 y0, x1 y1)
+                const float r = rcp_approx(m.x * m.y);
+                const float2 w = fmul2_rn(make_float2(m.y, m.x), make_float2(r, r));  // 1 / (x0 y0), 1 / (x1 y1)
+                const float2 c2 = make_float2(capC, capC), d2 = make_float2(-2.0f * capC, -2.0f * capC);
+                const float2 t0 = fma2(fmul2_rn(w, y), d2, c2), t1 = fma2(fmul2_rn(w, x), d2, c2);
+                s[c] = t0.x;
+                s[c + 1] = t0.y;
+                s[c + 2] = t1.x;
+                s[c + 3] = t1.y;
+              }
+            }
+            if constexpr (BIAS) {  // by distance from this row's place
+              const float own = (float)(near - c0 + lane);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) s[c] = fmaf(slope, fabsf(own - (float)c), CAP ? s[c] : s[c] * scale2);
+            }
+            if (opaque(at_edge)) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) s[c] = c < count ? s[c] : -INFINITY;
+            }
+            tc_st32(st + c0, s);
+          }
+          tc_wait_st();
+        }
         float s[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc_ld(st + 32 * c, *reinterpret_cast<float(*)[32]>(s + 32 * c));
         tc_wait_ld();
         tc_landed(s);
-        const bool edge = j >= safe;
-        const int left = bound - j * kPrTile;  // keys of this tile that count
-        // Scores to base 2: at once where something is done to them, else with
-        // the subtraction of the reference.
-        if constexpr (CAP) {
-          if (edge) {  // (neighbours share a reciprocal below)
+        if constexpr (!CAP && !BIAS) {
+          if (at_edge) {
 #pragma unroll
-            for (int c = 0; c < 128; ++c) s[c] = c < left ? s[c] : 0.f;
-          }
-          // 1 / (1 + 2^y) for four at a time from one reciprocal of their product:
-          // 2^30 as the largest power keeps that in range (and is 1 - 2^-29 as a tangent)
-#pragma unroll
-          for (int c = 0; c < 128; c += 4) {
-            const float2 e2 = make_float2(capE, capE), one = make_float2(1.0f, 1.0f);
-            float2 x = fmul2_rn(make_float2(s[c], s[c + 1]), e2), y = fmul2_rn(make_float2(s[c + 2], s[c + 3]), e2);
-            x = add2(make_float2(ex2(min_nan(x.x, 30.0f)), ex2(min_nan(x.y, 30.0f))), one);
-            y = add2(make_float2(ex2(min_nan(y.x, 30.0f)), ex2(min_nan(y.y, 30.0f))), one);
-            const float2 m = fmul2_rn(x, y);  // (x0 y0, x1 y1)
-            const float r = rcp_approx(m.x * m.y);
-            const float2 w = fmul2_rn(make_float2(m.y, m.x), make_float2(r, r));  // 1 / (x0 y0), 1 / (x1 y1)
-            const float2 c2 = make_float2(capC, capC), d2 = make_float2(-2.0f * capC, -2.0f * capC);
-            const float2 t0 = fma2(fmul2_rn(w, y), d2, c2), t1 = fma2(fmul2_rn(w, x), d2, c2);
-            s[c] = t0.x;
-            s[c + 1] = t0.y;
-            s[c + 2] = t1.x;
-            s[c + 3] = t1.y;
+            for (int c = 0; c < 128; ++c) s[c] = c < left ? s[c] : -INFINITY;
           }
         }
-        if constexpr (BIAS) {
-          // distance from this row's place: one sign for the whole warp where the
-          // tile lies on one side of its rows
-          const int near = base_row + (k.nk - k.nq) - j * kPrTile;
-          const float own = (float)(near + lane);
-          const float2 u2 = make_float2(scale2, scale2);
-          if (near >= kPrTile - 1 || near + 31 <= 0) {
-            const float sg = near >= kPrTile - 1 ? slope : -slope;
-            const float2 k0 = make_float2(sg * own, sg * own), k1 = make_float2(-sg, -sg);
+        if constexpr (BIAS && !CAP) {
+          if (!apart) {  // keys on one side of the warp's rows: the distance is linear
+            const float sg = near > 0 ? slope : -slope, own = (float)(near + lane);
+            const float2 k0 = make_float2(sg * own, sg * own), k1 = make_float2(-sg, -sg), u2 = make_float2(scale2, scale2);
 #pragma unroll
             for (int c = 0; c < 128; c += 2) {
-              const float2 d = fma2(k1, make_float2((float)c, (float)(c + 1)), k0);
-              const float2 x = CAP ? add2(make_float2(s[c], s[c + 1]), d) : fma2(make_float2(s[c], s[c + 1]), u2, d);
+              const float2 x = fma2(make_float2(s[c], s[c + 1]), u2, fma2(k1, make_float2((float)c, (float)(c + 1)), k0));
               s[c] = x.x;
               s[c + 1] = x.y;
             }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 128; ++c) s[c] = fmaf(slope, fabsf(own - (float)c), CAP ? s[c] : s[c] * scale2);
           }
-        }
-        if (edge) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c) s[c] = c < left ? s[c] : -INFINITY;
         }
         float m4[4];
 #pragma unroll
@@ -784,7 +847,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&ml_full[shares & 1u]);
         } else {
-          tc_wait(&ml_full[shares & 1u], (shares >> 1) & 1u, dead);
+          pr_wait(&ml_full[shares & 1u], (shares >> 1) & 1u, dead);
           const float ref1 = at->x, l1 = at->y;
           const float m = fmaxf(ref, ref1);
           if (m > -INFINITY) {
@@ -799,19 +862,20 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const bool used = solo ? jobs > (mine ? 0 : 1) : nt > j0;  // this buffer
       const bool used1 = solo ? jobs > (mine ? 1 : 0) : k.n[other] > j0;
       if (mine) {
-        if (used) tc_wait(&o_full[q], o_reads >> q & 1u, dead);
-        if (shared) tc_wait(&o_full[other], o_reads >> other & 1u, dead);
+        if (used) pr_wait(&o_full[q], o_reads >> q & 1u, dead);
+        if (shared) pr_wait(&o_full[other], o_reads >> other & 1u, dead);
         tc_after();
         const bool have = i < k.nq, part = a.splits > 1;
+        const uint32_t used_ = used, shared_ = shared, part_ = part;
         const int64_t row = k.q0 + i;
-        const float inv = part ? 1.0f : l == 0.f ? 0.f : 1.0f / l;
+        const float inv = part ? 1.0f : l == 0.f ? 0.f : rcp_approx(l);
         f0 *= inv;
         f1 *= inv;
         if (have) {
           if (part)
             a.part_ml[((int64_t)k.split * a.heads + k.head) * a.q_tokens + row] = make_float2(ref, l);
           else if (a.lse != nullptr)
-            a.lse[row * a.heads + k.head] = l == 0.f ? -INFINITY : ref * 0.6931471805599453f + logf(l);
+            a.lse[row * a.heads + k.head] = l == 0.f ? -INFINITY : (ref + lg2_approx(l)) * 0.6931471805599453f;
         }
         // Four neighbouring lanes trade 16-byte pieces, so that they store 64 bytes of
         // one row after another: 8 rows an instruction, not 32.
@@ -821,6 +885,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         uint16_t* o = a.out + (row - sub) * a.o_ts + (int64_t)k.head * a.o_hs + 8 * sub;
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32) {
+          const bool used = opaque(used_), shared = opaque(shared_), part = opaque(part_);
           float v[32];
           if (used) {
             tc_ld(tmem + lanes + 256 + 128 * q + c, v);
@@ -919,9 +984,11 @@ __global__ void __launch_bounds__(256) mla_prompt_join_kernel(const __grid_const
   if (row >= a.q_tokens || row < a.cu_q[0] || row >= a.cu_q[a.docs]) return;
   const int64_t step = (int64_t)a.heads * a.q_tokens, at = (int64_t)head * a.q_tokens + row;
   float M = -INFINITY;
+#pragma unroll 4
   for (int s = 0; s < a.splits; ++s) M = fmaxf(M, a.part_ml[s * step + at].x);
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
   for (int s = 0; s < a.splits; ++s) {
     const float2 ml = a.part_ml[s * step + at];
     if (ml.y == 0.f) continue;  // saw nothing
