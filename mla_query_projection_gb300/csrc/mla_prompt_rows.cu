@@ -54,63 +54,82 @@ __device__ __forceinline__ float2 turned(float x0, float x1, float c, float s) {
   return make_float2(fmaf(x0, c, -(x1 * s)), fmaf(x1, c, x0 * s));
 }
 
-// Four lanes a head, eight heads a warp: lane j of four has pairs 8 j .. 8 j + 7,
-// whose values are 32 bytes in a row (neighbours as pairs) or 16 bytes of each
-// half (halves as pairs).  A warp stays with a token for `chunk` heads: one
-// sine and cosine a lane, handed round by shuffles.  A lane reads all it turns
-// before it writes, so the output may be the input.
-template <bool INTERLEAVED>
-__global__ void __launch_bounds__(256) mla_rope_kernel(const __grid_constant__ RopeArgs r, int64_t tokens, int heads,
-                                                       int chunk, const uint16_t* x, int64_t x_ts, int64_t x_hs,
-                                                       uint16_t* out, int64_t o_ts, int64_t o_hs) {
-  const int lane = threadIdx.x & 31, j = lane & 3;
-  const int64_t warps = (int64_t)gridDim.x * 8;
-  const RopeLane rope(r, lane);
-  const int h0 = blockIdx.y * chunk + (lane >> 2), h1 = min(heads, (int)(blockIdx.y + 1) * chunk);
-  // words 0..3 and 4..7 of a lane's share of a row, in values from its start
+// A CTA takes 64 rows (tokens' heads, one after another) after another, four threads
+// each: thread j of four has pairs 8 j .. 8 j + 7, whose values are 32 bytes in a row
+// (neighbours as pairs) or 16 bytes of each half (halves as pairs).  The next rows'
+// values are on their way, and their tokens' sines and cosines worked out once, into
+// shared memory, while these are turned.  A thread reads all it turns before it
+// writes, so the output may be the input.  (Without the next rows under way, 4,096
+// tokens of 128 heads took 35 us.)
+constexpr int kRopeRows = 64;
+
+// MANY: a CTA has more than one round.
+template <bool INTERLEAVED, bool MANY>
+__global__ void __launch_bounds__(256, 5) mla_rope_kernel(const __grid_constant__ RopeArgs r, int64_t tokens, int heads,
+                                                          const uint16_t* x, int64_t x_ts, int64_t x_hs, uint16_t* out,
+                                                          int64_t o_ts, int64_t o_hs) {
+  __shared__ float2 turns[MANY ? 2 : 1][(kRopeRows + 1) * kRopePairs];
+  const int tid = threadIdx.x, j = tid & 3;
+  const int64_t rows = tokens * heads, step = (int64_t)gridDim.x * kRopeRows;
+  // words 0..3 and 4..7 of a thread's share of a row, in values from its start
   const int a0 = INTERLEAVED ? 16 * j : 8 * j, a1 = INTERLEAVED ? 16 * j + 8 : 32 + 8 * j;
+  const RopeLane rope(r, tid & 31);
+  const bool narrow = rows <= 0xFFFFFFFFll;
+  auto token_of = [&](int64_t row) -> int64_t { return narrow ? (uint32_t)row / (uint32_t)heads : row / heads; };
   pdl_wait();
   pdl_launch_dependents();
-  for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < tokens; t += warps) {
-    const uint16_t* xt = x + t * x_ts;
-    uint4 v0 = {}, v1 = {};
-    if (h0 < h1) {
-      v0 = *reinterpret_cast<const uint4*>(xt + (int64_t)h0 * x_hs + a0);
-      v1 = *reinterpret_cast<const uint4*>(xt + (int64_t)h0 * x_hs + a1);
+  struct Part {
+    uint4 v0, v1;
+    int64_t t;
+    int h, n;  // head, the token's place among the CTA's
+  };
+  // a thread's values of the rows from row0 on, and the turns of their tokens
+  auto fetch = [&](int64_t row0, float2* turn) -> Part {
+    Part p = {};
+    const int64_t row = row0 + (tid >> 2), t0 = token_of(row0);
+    if (row < rows) {
+      p.t = token_of(row);
+      p.h = (int)(row - p.t * heads);
+      p.n = (int)(p.t - t0);
+      const uint16_t* at = x + p.t * x_ts + (int64_t)p.h * x_hs;
+      p.v0 = *reinterpret_cast<const uint4*>(at + a0);
+      p.v1 = *reinterpret_cast<const uint4*>(at + a1);
     }
-    const float2 mine = rope.at(t);
-    float c[8], s[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      c[i] = __shfl_sync(0xFFFFFFFFu, mine.x, 8 * j + i);
-      s[i] = __shfl_sync(0xFFFFFFFFu, mine.y, 8 * j + i);
-    }
-    for (int h = h0; h < h1; h += 8) {
-      const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-      if (h + 8 < h1) {
-        v0 = *reinterpret_cast<const uint4*>(xt + (int64_t)(h + 8) * x_hs + a0);
-        v1 = *reinterpret_cast<const uint4*>(xt + (int64_t)(h + 8) * x_hs + a1);
-      }
+    const int count = (int)(token_of((row0 + kRopeRows < rows ? row0 + kRopeRows : rows) - 1) - t0);
+    for (int n = tid >> 5; n <= count; n += 8) turn[n * kRopePairs + (tid & 31)] = rope.at(t0 + n);
+    return p;
+  };
+  int64_t row0 = (int64_t)blockIdx.x * kRopeRows;
+  Part p = fetch(row0, turns[0]);
+  for (int b = 0; row0 < rows; b ^= 1, row0 += step) {
+    __syncthreads();
+    Part next = {};
+    if (MANY && row0 + step < rows) next = fetch(row0 + step, turns[b ^ 1]);
+    if (row0 + (tid >> 2) < rows) {
+      const float4* cs = reinterpret_cast<const float4*>(turns[b] + p.n * kRopePairs + 8 * j);  // two pairs each
+      const uint32_t w[8] = {p.v0.x, p.v0.y, p.v0.z, p.v0.w, p.v1.x, p.v1.y, p.v1.z, p.v1.w};
       uint32_t y[8];
-      if constexpr (INTERLEAVED) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 p = turned(bf16lo(w[i]), bf16hi(w[i]), c[i], s[i]);
-          y[i] = pack_bf16x2(p.x, p.y);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 p = turned(bf16lo(w[i]), bf16lo(w[i + 4]), c[2 * i], s[2 * i]);
-          const float2 q = turned(bf16hi(w[i]), bf16hi(w[i + 4]), c[2 * i + 1], s[2 * i + 1]);
-          y[i] = pack_bf16x2(p.x, q.x);
-          y[i + 4] = pack_bf16x2(p.y, q.y);
+      for (int i = 0; i < 4; ++i) {
+        const float4 f = cs[i];
+        if constexpr (INTERLEAVED) {
+          const float2 u = turned(bf16lo(w[2 * i]), bf16hi(w[2 * i]), f.x, f.y);
+          const float2 v = turned(bf16lo(w[2 * i + 1]), bf16hi(w[2 * i + 1]), f.z, f.w);
+          y[2 * i] = pack_bf16x2(u.x, u.y);
+          y[2 * i + 1] = pack_bf16x2(v.x, v.y);
+        } else {
+          const float2 u = turned(bf16lo(w[i]), bf16lo(w[i + 4]), f.x, f.y);
+          const float2 v = turned(bf16hi(w[i]), bf16hi(w[i + 4]), f.z, f.w);
+          y[i] = pack_bf16x2(u.x, v.x);
+          y[i + 4] = pack_bf16x2(u.y, v.y);
         }
       }
-      uint16_t* o = out + t * o_ts + (int64_t)h * o_hs;
+      uint16_t* o = out + p.t * o_ts + (int64_t)p.h * o_hs;
       *reinterpret_cast<uint4*>(o + a0) = make_uint4(y[0], y[1], y[2], y[3]);
       *reinterpret_cast<uint4*>(o + a1) = make_uint4(y[4], y[5], y[6], y[7]);
     }
+    if (!MANY) break;
+    p = next;
   }
 }
 
@@ -119,9 +138,53 @@ __global__ void __launch_bounds__(256) mla_rope_kernel(const __grid_constant__ R
 // One warp a token: the decode step's insert (the same sums in the same order,
 // so the same bytes), with the norm and the rotation optional, and the row
 // handed on in BF16 where the caller wants it.  A lane has latent columns
-// 8 lane .. and 256 + 8 lane ..; the first eight lanes have the rope part.
+// 8 lane .. and 256 + 8 lane ..; the first eight lanes have the rope part.  The
+// next token's row is on its way while this one is worked on.
+
+__device__ __forceinline__ float2 fma2_rn(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mov.b64 rc, {%6, %7};\n\tfma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// Quotients of a token by one divisor, each correctly rounded, as a division gives
+// them: by P. Markstein's theorem (IBM Journal of Research and Development 34, 1990),
+// with y the rounded reciprocal of b and q = a y rounded, q + (a - b q) y rounded once
+// is the rounded a / b.  Where the quotient is far beyond E4M3's range the product is
+// as good (and may be infinite); divisors near the ends of FP32's range are divided by.
+struct Divisor {
+  float b, y;
+  bool plain;
+  __device__ __forceinline__ explicit Divisor(float divisor) {
+    b = divisor;
+    y = __frcp_rn(divisor);
+    plain = !(fabsf(divisor) >= 0x1p-60f && fabsf(divisor) <= 0x1p60f);
+  }
+  // two, in packed arithmetic
+  __device__ __forceinline__ float2 quotients(float2 a) const {
+    const float2 y2 = make_float2(y, y), q = fmul2_rn(a, y2);
+    const float2 r = fma2_rn(fma2_rn(make_float2(-q.x, -q.y), make_float2(b, b), a), y2, q);
+    return make_float2(fabsf(q.x) < 0x1p20f ? r.x : q.x, fabsf(q.y) < 0x1p20f ? r.y : q.y);
+  }
+  // the E4M3 codes of two pairs of BF16 values
+  __device__ __forceinline__ uint32_t codes(uint32_t w0, uint32_t w1) const {
+    float2 p = make_float2(bf16lo(w0), bf16hi(w0)), q = make_float2(bf16lo(w1), bf16hi(w1));
+    if (plain) {
+      p = make_float2(__fdiv_rn(p.x, b), __fdiv_rn(p.y, b));
+      q = make_float2(__fdiv_rn(q.x, b), __fdiv_rn(q.y, b));
+    } else {
+      p = quotients(p);
+      q = quotients(q);
+    }
+    return (uint32_t)e4m3x2(p.x, p.y) | ((uint32_t)e4m3x2(q.x, q.y) << 16);
+  }
+};
+
 template <int LAYOUT>
-__global__ void __launch_bounds__(256) mla_cache_write_kernel(const __grid_constant__ CacheWriteArgs w) {
+__global__ void __launch_bounds__(256, 4) mla_cache_write_kernel(const __grid_constant__ CacheWriteArgs w) {
   constexpr bool kDs = LAYOUT == MLA_KV_FP8_DS_MLA, kNv = LAYOUT == MLA_KV_NVFP4_DS_MLA;
   constexpr int kBytes = RowChunks<LAYOUT>::kBytes;
   const int lane = threadIdx.x & 31;
@@ -131,32 +194,47 @@ __global__ void __launch_bounds__(256) mla_cache_write_kernel(const __grid_const
   const DecodeArgs none = {};
   pdl_wait();
   pdl_launch_dependents();
-  uint4 gv[2] = {};
-  if (w.gamma != nullptr) {
-    gv[0] = *reinterpret_cast<const uint4*>(w.gamma + 8 * lane);
-    gv[1] = *reinterpret_cast<const uint4*>(w.gamma + 256 + 8 * lane);
-  }
   const float tensor_scale = LAYOUT == MLA_KV_FP8_E4M3 ? *w.k_scale : 1.0f;
-  for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < w.tokens; t += warps) {
+  struct Token {
+    uint4 v[2], pe;
+    int64_t slot;
+    float2 turn;
+    float scale;
+  };
+  auto fetch = [&](int64_t t) -> Token {
+    Token k;
     const uint16_t* kv = w.kv_c + t * w.kv_c_stride;
-    const uint4 v[2] = {*reinterpret_cast<const uint4*>(kv + 8 * lane),
-                        *reinterpret_cast<const uint4*>(kv + 256 + 8 * lane)};
-    uint4 pe = {};
-    if (lane < 8) pe = *reinterpret_cast<const uint4*>(w.k_pe + t * w.k_pe_stride + 8 * lane);
-    int64_t slot = w.slots[t];
-    if (slot >= w.capacity) {
+    k.v[0] = *reinterpret_cast<const uint4*>(kv + 8 * lane);
+    k.v[1] = *reinterpret_cast<const uint4*>(kv + 256 + 8 * lane);
+    k.pe = make_uint4(0, 0, 0, 0);
+    if (lane < 8) k.pe = *reinterpret_cast<const uint4*>(w.k_pe + t * w.k_pe_stride + 8 * lane);
+    k.slot = w.slots[t];
+    if (k.slot >= w.capacity) {
       if (lane == 0 && w.flags != nullptr) atomicOr(w.flags, MLA_DEVERR_BAD_SLOT);
-      slot = -1;
+      k.slot = -1;
     }
+    k.scale = tensor_scale;
+    if (LAYOUT == MLA_KV_FP8_E4M3_PAGE && k.slot >= 0)
+      k.scale = w.k_scale[k.slot <= 0xFFFFFFFFll ? (uint32_t)k.slot / (uint32_t)w.page_size : k.slot / w.page_size];
+    k.turn = rope_on ? rope.at(t) : make_float2(1.f, 0.f);
+    return k;
+  };
+  int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (t >= w.tokens) return;
+  Token k = fetch(t);
+  for (;;) {
+    const int64_t after = t + warps;
+    Token next;
+    if (after < w.tokens) next = fetch(after);
+    uint4 pe = k.pe;
     if (rope_on) {
-      const float2 mine = rope.at(t);
       const uint32_t x[4] = {pe.x, pe.y, pe.z, pe.w};
       uint32_t y[4];
       if (w.rope.spec.interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // pair 4 lane + i
-          const float c = __shfl_sync(0xFFFFFFFFu, mine.x, (4 * lane + i) & 31);
-          const float s = __shfl_sync(0xFFFFFFFFu, mine.y, (4 * lane + i) & 31);
+          const float c = __shfl_sync(0xFFFFFFFFu, k.turn.x, (4 * lane + i) & 31);
+          const float s = __shfl_sync(0xFFFFFFFFu, k.turn.y, (4 * lane + i) & 31);
           const float2 p = turned(bf16lo(x[i]), bf16hi(x[i]), c, s);
           y[i] = pack_bf16x2(p.x, p.y);
         }
@@ -166,8 +244,8 @@ __global__ void __launch_bounds__(256) mla_cache_write_kernel(const __grid_const
         for (int i = 0; i < 4; ++i) {
           const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, x[i], 4);
           const int p0 = 8 * (lane & 3) + 2 * i;
-          const float c0 = __shfl_sync(0xFFFFFFFFu, mine.x, p0), s0 = __shfl_sync(0xFFFFFFFFu, mine.y, p0);
-          const float c1 = __shfl_sync(0xFFFFFFFFu, mine.x, p0 + 1), s1 = __shfl_sync(0xFFFFFFFFu, mine.y, p0 + 1);
+          const float c0 = __shfl_sync(0xFFFFFFFFu, k.turn.x, p0), s0 = __shfl_sync(0xFFFFFFFFu, k.turn.y, p0);
+          const float c1 = __shfl_sync(0xFFFFFFFFu, k.turn.x, p0 + 1), s1 = __shfl_sync(0xFFFFFFFFu, k.turn.y, p0 + 1);
           const uint32_t x0 = second ? other : x[i], x1 = second ? x[i] : other;
           const float2 p = turned(bf16lo(x0), bf16lo(x1), c0, s0), q = turned(bf16hi(x0), bf16hi(x1), c1, s1);
           y[i] = second ? pack_bf16x2(p.y, q.y) : pack_bf16x2(p.x, q.x);
@@ -175,54 +253,150 @@ __global__ void __launch_bounds__(256) mla_cache_write_kernel(const __grid_const
       }
       pe = make_uint4(y[0], y[1], y[2], y[3]);
     }
-    float n[2][8];
-    const float s0 = kv_group_ss(v[0], n[0]), s1 = kv_group_ss(v[1], n[1]);
+    uint32_t n[2][4] = {{k.v[0].x, k.v[0].y, k.v[0].z, k.v[0].w}, {k.v[1].x, k.v[1].y, k.v[1].z, k.v[1].w}};
     if (w.gamma != nullptr) {
+      float x[8];
+      const float s0 = kv_group_ss(k.v[0], x), s1 = kv_group_ss(k.v[1], x);
       const float total = warp_sum(s0) + warp_sum(s1);
       const float rr = __frsqrt_rn(__fadd_rn(__fmul_rn(total, 1.0f / 512.0f), w.eps));
-      kv_group_norm(n[0], gv[0], rr, n[0]);
-      kv_group_norm(n[1], gv[1], rr, n[1]);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const uint4 gv = *reinterpret_cast<const uint4*>(w.gamma + 256 * g + 8 * lane);
+        const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n[g][i] = rms_scale_bf16x2(n[g][i], rr, gw[i]);
+      }
     }
     if (w.rows != nullptr) {
       uint16_t* o = w.rows + t * w.rows_stride;
 #pragma unroll
       for (int g = 0; g < 2; ++g)
-        *reinterpret_cast<uint4*>(o + 256 * g + 8 * lane) =
-            make_uint4(pack_bf16x2(n[g][0], n[g][1]), pack_bf16x2(n[g][2], n[g][3]), pack_bf16x2(n[g][4], n[g][5]),
-                       pack_bf16x2(n[g][6], n[g][7]));
+        *reinterpret_cast<uint4*>(o + 256 * g + 8 * lane) = make_uint4(n[g][0], n[g][1], n[g][2], n[g][3]);
       if (lane < 8) *reinterpret_cast<uint4*>(o + kKvLora + 8 * lane) = pe;
     }
-    if (slot < 0) continue;
-    float ks = tensor_scale;
-    if constexpr (LAYOUT == MLA_KV_FP8_E4M3_PAGE) ks = w.k_scale[slot / w.page_size];
-    uint8_t* row = w.cache + slot * kBytes;
+    if (k.slot >= 0) {
+      uint8_t* row = w.cache + k.slot * kBytes;
+      if constexpr (kDs || kNv) {
 #pragma unroll
-    for (int g = 0; g < 2; ++g)
-      kv_store_group(none, row, n[g], g == 0 ? pe : make_uint4(0, 0, 0, 0), lane + 32 * g, kDs, kNv, ks);
+        for (int g = 0; g < 2; ++g) {
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[2 * i] = bf16lo(n[g][i]);
+            x[2 * i + 1] = bf16hi(n[g][i]);
+          }
+          kv_store_group(none, row, x, g == 0 ? pe : make_uint4(0, 0, 0, 0), lane + 32 * g, kDs, kNv, 1.0f);
+        }
+      } else {
+        const Divisor d(k.scale);
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+          *reinterpret_cast<uint2*>(row + 256 * g + 8 * lane) = make_uint2(d.codes(n[g][0], n[g][1]), d.codes(n[g][2], n[g][3]));
+        if (lane < 8)
+          *reinterpret_cast<uint2*>(row + kKvLora + 8 * lane) = make_uint2(d.codes(pe.x, pe.y), d.codes(pe.z, pe.w));
+      }
+    }
+    if (after >= w.tokens) break;
+    t = after;
+    k = next;
   }
 }
 
 // --------------------------------------------------------------- reading
 //
-// A CTA takes R output rows in a row.  A thread each finds where they lie (the
-// request by bisection, the page from the table); then all threads take 16-byte
-// chunks of the rows, four under way at a time, and store their values.
-constexpr int kReadThreads = 256, kReadMost = 64;
+// A row's 576 values are 72 groups of eight, whatever the layout: a thread turns the 4, 8
+// or 16 bytes of a group into 16 bytes of output, so that a warp's loads and stores
+// both are rows of bytes without gaps.  (16 bytes a load and two stores of 16 took 28 us
+// for 65,536 rows.)  A CTA takes a batch of R rows after another.  Where rows lie is
+// found two batches ahead (the request by bisection, the page from the table, a thread
+// each: three trips to memory), their groups are loaded one batch ahead.
+constexpr int kReadThreads = 256, kReadGroups = kRowElems / 8;
 
 template <int LAYOUT>
-__global__ void __launch_bounds__(kReadThreads) mla_cache_read_kernel(const __grid_constant__ CacheReadArgs a, int R) {
-  using C = RowChunks<LAYOUT>;
-  __shared__ int64_t source[kReadMost];  // byte offset of the cache row; -1: zeros, -2: left as it is
-  __shared__ float scale[kReadMost];
+struct ReadGroup;
+
+template <>
+struct ReadGroup<MLA_KV_FP8_E4M3> {
+  static constexpr int kBytes = kRowE4m3, kAhead = 8;
+  using Raw = uint2;
+  __device__ static Raw load(const uint8_t* row, int g) { return *reinterpret_cast<const uint2*>(row + 8 * g); }
+  __device__ static void values(Raw w, int, float scale, float (&v)[8]) {
+    e4m3x4_values(w.x, v);
+    e4m3x4_values(w.y, v + 4);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float2 p = fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(scale, scale));
+      v[i] = p.x;
+      v[i + 1] = p.y;
+    }
+  }
+};
+template <>
+struct ReadGroup<MLA_KV_FP8_E4M3_PAGE> : ReadGroup<MLA_KV_FP8_E4M3> {};
+template <>
+struct ReadGroup<MLA_KV_FP8_DS_MLA> {
+  static constexpr int kBytes = kRowDs, kAhead = 4;
+  using Raw = uint4;  // codes, scale; or eight BF16
+  __device__ static Raw load(const uint8_t* row, int g) {
+    if (g >= 64) return *reinterpret_cast<const uint4*>(row + kDsRope + 16 * (g - 64));
+    const uint2 c = *reinterpret_cast<const uint2*>(row + 8 * g);
+    return make_uint4(c.x, c.y, *reinterpret_cast<const uint32_t*>(row + kDsScales + 4 * (g >> 4)), 0);
+  }
+  __device__ static void values(Raw w, int g, float, float (&v)[8]) {
+    if (g < 64) {
+      ReadGroup<MLA_KV_FP8_E4M3>::values(make_uint2(w.x, w.y), g, __uint_as_float(w.z), v);
+    } else {
+      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16lo(x[i]);
+        v[2 * i + 1] = bf16hi(x[i]);
+      }
+    }
+  }
+};
+template <>
+struct ReadGroup<MLA_KV_NVFP4_DS_MLA> {
+  static constexpr int kBytes = kRowNvfp4, kAhead = 8;
+  using Raw = uint2;  // codes, scale; or eight E4M3
+  __device__ static Raw load(const uint8_t* row, int g) {
+    if (g >= 64) return *reinterpret_cast<const uint2*>(row + kNvRope + 8 * (g - 64));
+    const int s = g >> 1;
+    return make_uint2(*reinterpret_cast<const uint32_t*>(row + 4 * g), row[kNvScales + 8 * (s & 3) + (s >> 2)]);
+  }
+  __device__ static void values(Raw w, int g, float, float (&v)[8]) {
+    if (g >= 64) {
+      e4m3x4_values(w.x, v);
+      e4m3x4_values(w.y, v + 4);
+      return;
+    }
+    uint32_t h[4];
+    e2m1x8_scaled(w.x, e4m3x2_f16(0x0101u * w.y), h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = v[2 * i + 1] = 0.f;
+      add_f16x2(h[i], v + 2 * i);
+    }
+  }
+};
+
+template <int LAYOUT>
+__global__ void __launch_bounds__(kReadThreads, 4) mla_cache_read_kernel(const __grid_constant__ CacheReadArgs a, int R) {
+  using G = ReadGroup<LAYOUT>;
+  using Raw = typename G::Raw;
+  constexpr int kAhead = G::kAhead, kMost = kAhead * kReadThreads / kReadGroups;
+  __shared__ int64_t source[3][kMost];  // byte offset of the cache row; -1: zeros, -2: left as it is
+  __shared__ float scale[3][kMost];
   const int tid = threadIdx.x;
-  const int64_t row0 = (int64_t)blockIdx.x * R;
   pdl_wait();
   pdl_launch_dependents();
-  if (tid < R) {
+  const int64_t first = a.cu[0], last = min((int64_t)a.cu[a.requests], a.max_rows), step = (int64_t)gridDim.x * R;
+  auto look_up = [&](int64_t row0, int buffer) {
+    if (tid >= R) return;
     const int64_t i = row0 + tid;
     int64_t src = -2;
     float sc = 1.0f;
-    if (i < a.max_rows && i >= a.cu[0] && i < a.cu[a.requests]) {
+    if (i < last && i >= first) {
       int lo = 0, hi = a.requests - 1;  // the last request with cu[r] <= i
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -239,44 +413,54 @@ __global__ void __launch_bounds__(kReadThreads) mla_cache_read_kernel(const __gr
         if (b < a.bt_cols) page = a.table[(int64_t)lo * a.bt_stride + b];
       }
       if (page >= 0 && page < a.num_pages) {
-        src = (page * a.page_size + off) * C::kBytes;
+        src = (page * a.page_size + off) * G::kBytes;
         sc = page_scale(a.k_scale, LAYOUT, page);
       } else {
         src = -1;
         if (a.flags != nullptr) atomicOr(a.flags, MLA_DEVERR_BAD_SLOT);
       }
     }
-    source[tid] = src;
-    scale[tid] = sc;
-  }
+    source[buffer][tid] = src;
+    scale[buffer][tid] = sc;
+  };
+  const int groups = R * kReadGroups;
+  auto load = [&](Raw (&to)[kAhead], int b) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int k = tid + u * kReadThreads, r = k / kReadGroups;
+      to[u] = Raw{};
+      if (k < groups && source[b][r] >= 0) to[u] = G::load(a.cache + source[b][r], k - r * kReadGroups);
+    }
+  };
+  int64_t row0 = (int64_t)blockIdx.x * R;
+  if (row0 >= last) return;
+  Raw w[kAhead];
+  look_up(row0, 0);
+  const bool many = row0 + step < last;
+  if (many) look_up(row0 + step, 1);
   __syncthreads();
-  constexpr int kAhead = 4;
-  for (int base = tid; base < R * C::kChunks; base += kAhead * kReadThreads) {
-    uint4 w[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int k = base + u * kReadThreads, r = k / C::kChunks;
-      w[u] = make_uint4(0, 0, 0, 0);
-      if (k < R * C::kChunks && source[r] >= 0)
-        w[u] = *reinterpret_cast<const uint4*>(a.cache + source[r] + C::offset(k - r * C::kChunks));
+  load(w, 0);
+  for (int b = 0; row0 < last; row0 += step) {
+    const int b1 = b == 2 ? 0 : b + 1, b2 = b1 == 2 ? 0 : b1 + 1;
+    Raw next[kAhead];
+    if (row0 + step < last) {
+      if (row0 + 2 * step < last) look_up(row0 + 2 * step, b2);
+      load(next, b1);
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      const int k = base + u * kReadThreads, r = k / C::kChunks, c = k - r * C::kChunks;
-      if (k >= R * C::kChunks || source[r] == -2) continue;
-      float v[C::kMax];
-#pragma unroll
-      for (int e = 0; e < C::kMax; ++e) v[e] = 0.f;
-      if (source[r] >= 0) C::add(a.cache + source[r], c, w[u], v);
-      const float sc = scale[r];
-      uint16_t* o = a.rows + (row0 + r) * a.rows_stride + C::col(c);
-#pragma unroll
-      for (int e = 0; e < C::kMax; e += 8)
-        if (e < C::width(c))
-          *reinterpret_cast<uint4*>(o + e) =
-              make_uint4(pack_bf16x2(v[e] * sc, v[e + 1] * sc), pack_bf16x2(v[e + 2] * sc, v[e + 3] * sc),
-                         pack_bf16x2(v[e + 4] * sc, v[e + 5] * sc), pack_bf16x2(v[e + 6] * sc, v[e + 7] * sc));
+      const int k = tid + u * kReadThreads, r = k / kReadGroups, g = k - r * kReadGroups;
+      if (k >= groups || source[b][r] == -2) continue;
+      float v[8];
+      G::values(w[u], g, scale[b][r], v);
+      *reinterpret_cast<uint4*>(a.rows + (row0 + r) * a.rows_stride + 8 * g) =
+          make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     }
+    if (!many) break;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) w[u] = next[u];
+    b = b1;
   }
 }
 
@@ -311,6 +495,19 @@ struct Launch {
     cfg.numAttrs = 1;
   }
 };
+
+// Rows a batch: as many as the threads take with all their loads, or fewer where that
+// gives every SM four CTAs (a row alone at the least).
+template <int LAYOUT>
+cudaError_t launch_read(const CacheReadArgs& a, int sms, void* stream) {
+  constexpr int kMost = ReadGroup<LAYOUT>::kAhead * kReadThreads / kReadGroups;
+  const int64_t even = (a.max_rows + 4 * sms - 1) / (4 * sms);
+  const int R = (int)(even < kMost ? even : kMost);
+  int64_t ctas = (a.max_rows + R - 1) / R;
+  if (ctas > 4 * (int64_t)sms) ctas = 4 * (int64_t)sms;
+  Launch l(dim3((unsigned)ctas), kReadThreads, stream);
+  return cudaLaunchKernelEx(&l.cfg, mla_cache_read_kernel<LAYOUT>, a, R);
+}
 
 // A cache's pages and rows that byte offsets of 64 bits reach.
 bool cache_fits(int64_t num_pages, int page_size) {
@@ -369,23 +566,19 @@ int mla_rope_apply(mla_rope_t h, int64_t tokens, int heads, const void* x, int64
       out_token_stride < mla::kRope || (x_head_stride | x_token_stride | out_head_stride | out_token_stride) % 8)
     return MLA_EINVAL;
   if (!mla::aligned16(x) || !mla::aligned16(out) || !mla::aligned4(positions)) return MLA_EINVAL;
+  if (tokens > INT64_MAX / 2048) return MLA_EINVAL;
   int sms = 0;
   if (!mla::sm_count(&sms)) return MLA_ECUDA;
-  // Heads a warp takes of a token: all of them (one sine and cosine for all)
-  // while that makes eight warps an SM, down to one head a lane quad.
-  int chunk = (heads + 7) / 8 * 8;
-  while (chunk > 8 && tokens * ((heads + chunk - 1) / chunk) < 8 * (int64_t)sms) chunk = (chunk / 2 + 7) / 8 * 8;
-  const int groups = (heads + chunk - 1) / chunk;
-  int64_t ctas = (tokens + 7) / 8;
-  const int64_t most = (8 * (int64_t)sms + groups - 1) / groups;  // eight CTAs an SM are resident
-  if (ctas > most) ctas = most;
-  mla::Launch l(dim3((unsigned)ctas, (unsigned)groups), 256, stream);
+  int64_t ctas = (tokens * heads + mla::kRopeRows - 1) / mla::kRopeRows;
+  const bool many = ctas > 5 * (int64_t)sms;  // (five CTAs an SM are resident)
+  if (many) ctas = 5 * (int64_t)sms;
+  mla::Launch l(dim3((unsigned)ctas), 256, stream);
   const mla::RopeArgs r{h->spec, positions, pos_stride, pos_offset};
-  const uint16_t* xp = static_cast<const uint16_t*>(x);
-  uint16_t* op = static_cast<uint16_t*>(out);
-  return mla::launched(cudaLaunchKernelEx(&l.cfg, h->spec.interleaved ? mla::mla_rope_kernel<true> : mla::mla_rope_kernel<false>,
-                                          r, tokens, heads, chunk, xp, x_token_stride, x_head_stride, op,
-                                          out_token_stride, out_head_stride));
+  auto kernel = h->spec.interleaved ? (many ? mla::mla_rope_kernel<true, true> : mla::mla_rope_kernel<true, false>)
+                                    : (many ? mla::mla_rope_kernel<false, true> : mla::mla_rope_kernel<false, false>);
+  return mla::launched(cudaLaunchKernelEx(&l.cfg, kernel, r, tokens, heads, static_cast<const uint16_t*>(x),
+                                          x_token_stride, x_head_stride, static_cast<uint16_t*>(out), out_token_stride,
+                                          out_head_stride));
 }
 
 int mla_cache_write(int64_t tokens, const void* kv_c, int64_t kv_c_stride, const void* k_pe, int64_t k_pe_stride,
@@ -430,7 +623,7 @@ int mla_cache_write(int64_t tokens, const void* kv_c, int64_t kv_c_stride, const
   w.rows_stride = rows_stride;
   w.flags = device_flags;
   int64_t ctas = (tokens + 7) / 8;
-  if (ctas > 8 * (int64_t)sms) ctas = 8 * (int64_t)sms;
+  if (ctas > 4 * (int64_t)sms) ctas = 4 * (int64_t)sms;
   mla::Launch l(dim3((unsigned)ctas), 256, stream);
   cudaError_t e;
   switch (layout) {
@@ -475,15 +668,12 @@ int mla_cache_read(const void* kv_cache, int64_t num_pages, int page_size, int l
   a.rows = static_cast<uint16_t*>(rows);
   a.rows_stride = rows_stride;
   a.flags = device_flags;
-  // Rows a CTA: 8 while all CTAs are resident at once, 32 beyond.
-  const int R = max_rows <= 8 * 8 * (int64_t)sms ? 8 : 32;
-  mla::Launch l(dim3((unsigned)((max_rows + R - 1) / R)), mla::kReadThreads, stream);
   cudaError_t e;
   switch (layout) {
-    case MLA_KV_FP8_DS_MLA: e = cudaLaunchKernelEx(&l.cfg, mla::mla_cache_read_kernel<MLA_KV_FP8_DS_MLA>, a, R); break;
-    case MLA_KV_NVFP4_DS_MLA: e = cudaLaunchKernelEx(&l.cfg, mla::mla_cache_read_kernel<MLA_KV_NVFP4_DS_MLA>, a, R); break;
-    case MLA_KV_FP8_E4M3_PAGE: e = cudaLaunchKernelEx(&l.cfg, mla::mla_cache_read_kernel<MLA_KV_FP8_E4M3_PAGE>, a, R); break;
-    default: e = cudaLaunchKernelEx(&l.cfg, mla::mla_cache_read_kernel<MLA_KV_FP8_E4M3>, a, R);
+    case MLA_KV_FP8_DS_MLA: e = mla::launch_read<MLA_KV_FP8_DS_MLA>(a, sms, stream); break;
+    case MLA_KV_NVFP4_DS_MLA: e = mla::launch_read<MLA_KV_NVFP4_DS_MLA>(a, sms, stream); break;
+    case MLA_KV_FP8_E4M3_PAGE: e = mla::launch_read<MLA_KV_FP8_E4M3_PAGE>(a, sms, stream); break;
+    default: e = mla::launch_read<MLA_KV_FP8_E4M3>(a, sms, stream);
   }
   return mla::launched(e);
 }
