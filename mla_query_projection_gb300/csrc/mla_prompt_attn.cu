@@ -80,9 +80,9 @@ struct PrSmem {
   static constexpr int oQ = 0;
   static constexpr int oRing = 2 * kPrQ;
   static constexpr int oBar = oRing + kPrRing * kPrUnit;
-  // full[8] empty[8] q_full[2] q_free[2] s_full[2] p_full[4] o_full[2] o_free[2] ml_full[2] item_full[4]
-  // item_free[4] drain
-  static constexpr int kBars = 41;
+  // k_full[2] v_full[2] k_free[2] v_free[2] q_full[2] q_free[2] s_full[2] p_full[4] o_full[2] o_free[2] ml_full[2]
+  // item_full[4] item_free[4] drain
+  static constexpr int kBars = 33;
   static constexpr int oItem = oBar + kBars * 8;
   static constexpr int oMl = oItem + kPrItems * (int)sizeof(PrItem);  // [2][128] reference and sum of a shared row
   static constexpr int oScan = oMl + 2 * 128 * 8;                     // [96]
@@ -140,6 +140,12 @@ __device__ __forceinline__ float rcp_approx(float x) {
 __device__ __forceinline__ float lg2_approx(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The largest of three (one instruction).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 // The smaller, or NaN.
@@ -239,9 +245,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     mla_prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ PromptMaps maps) {
   using S = PrSmem;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::oBar);
-  uint64_t* empty = full + kPrRing;
-  uint64_t* q_full = empty + kPrRing;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + S::oBar);  // of a key tile, by its parity
+  uint64_t* v_full = k_full + 2;
+  uint64_t* k_free = v_full + 2;
+  uint64_t* v_free = k_free + 2;
+  uint64_t* q_full = v_free + 2;
   uint64_t* q_free = q_full + 2;
   uint64_t* s_full = q_free + 2;
   uint64_t* p_full = s_full + 2;
@@ -261,11 +269,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   const bool causal = a.causal != 0;
   const int each = (a.docs + kPrChunks - 1) / kPrChunks;  // documents a sum
   if (tid == 0) {
-    for (int s = 0; s < kPrRing; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
     for (int q = 0; q < 2; ++q) {
+      mbar_init(&k_full[q], 1);
+      mbar_init(&v_full[q], 1);
+      mbar_init(&k_free[q], 1);
+      mbar_init(&v_free[q], 1);
       mbar_init(&q_full[q], 1);
       mbar_init(&q_free[q], 1);
       mbar_init(&s_full[q], 1);
@@ -449,32 +457,27 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     }
   } else if (warp == 8) {
     // ================= TMA: K, V of key tile after key tile, the queries behind the first K
-    uint32_t use = 0;                // ring slots so far
+    //
+    // Tile t of all that this CTA goes through has units 5 t .. of the ring: three of K,
+    // two of V.  Its K comes in the place of K's last unit and V of tile t - 2, its V in
+    // that of K's first two of tile t - 1.
+    uint32_t tile = 0;               // key tiles so far
     uint32_t loads = 0, q_uses = 0;  // query buffers: used, parity of q_free; a bit a buffer
     for (uint32_t i = 0; !dead; ++i) {
       const PrItem& k = item_wait(i);
       if (dead || !k.valid) break;
       const int end = max(k.n[0], k.n[1]);
-      if (lane == 0 && k.j0 < end) {
-        auto slot = [&]() -> int {
-          const int s = use % kPrRing;
-          if (use >= kPrRing) pr_wait(&empty[s], (use / kPrRing - 1) & 1u, dead);
-          return s;
-        };
-        for (int j = k.j0; j < end && !dead; ++j) {
+      if (lane == 0) {
+        for (int j = k.j0; j < end && !dead; ++j, ++tile) {
           const int row = k.k0 + j * kPrTile;
-#pragma unroll
-          for (int u = 0; u < 3; ++u) {
-            const int s = slot();
-            if (dead) break;
-            const uint32_t dst = smem_u32(smem + S::oRing) + s * kPrUnit;
-            mbar_arrive_expect_tx(&full[s], kPrUnit);
-            if (u < 2)
-              tma_g2s_3d(dst, &maps.k_nope, 64 * u, k.head, row, &full[s]);
-            else
-              tma_g2s_3d(dst, &maps.k_pe, 0, 0, row, &full[s]);
-            ++use;
-          }
+          const uint32_t b = tile & 1u, ring = smem_u32(smem + S::oRing);
+          auto unit = [&](uint32_t u) { return ring + ((5 * tile + u) % kPrRing) * kPrUnit; };
+          mbar_arrive_expect_tx(&k_full[b], 3 * kPrUnit);
+          tma_g2s_3d(unit(0), &maps.k_nope, 0, k.head, row, &k_full[b]);  // (K of tile t - 2 has been waited for)
+          if (tile >= 2) pr_wait(&v_free[b], ((tile >> 1) - 1) & 1u, dead);
+          if (dead) break;
+          tma_g2s_3d(unit(1), &maps.k_nope, 64, k.head, row, &k_full[b]);
+          tma_g2s_3d(unit(2), &maps.k_pe, 0, 0, row, &k_full[b]);
           if (j == k.j0) {
             // the queries (their buffers come free later than the ring's slots): tile
             // q into buffer `place`
@@ -496,16 +499,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               tma_g2s_3d(dst + 2 * kPrUnit, &maps.q_pe, 0, k.head, at, &q_full[place]);
             }
           }
+          if (tile >= 1 && !dead) pr_wait(&k_free[b ^ 1u], ((tile - 1) >> 1) & 1u, dead);
+          if (dead) break;
+          mbar_arrive_expect_tx(&v_full[b], 2 * kPrUnit);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {  // 64 keys, both halves of their columns
-            if (dead) break;
-            const int s = slot();
-            if (dead) break;
-            const uint32_t dst = smem_u32(smem + S::oRing) + s * kPrUnit;
-            mbar_arrive_expect_tx(&full[s], kPrUnit);
-            tma_g2s_3d(dst, &maps.v, 0, k.head, row + 64 * u, &full[s]);
-            tma_g2s_3d(dst + kPrUnit / 2, &maps.v, 64, k.head, row + 64 * u, &full[s]);
-            ++use;
+            tma_g2s_3d(unit(3 + u), &maps.v, 0, k.head, row + 64 * u, &v_full[b]);
+            tma_g2s_3d(unit(3 + u) + kPrUnit / 2, &maps.v, 64, k.head, row + 64 * u, &v_full[b]);
           }
         }
       }
@@ -515,9 +515,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     if (dead && lane == 0) {  // the copies under way land before the CTA leaves
       for (int q = 0; q < 2; ++q)  // (as often waited for as loaded, but for the last time)
         if (loads >> q & 1u) (void)pr_wait_long(&q_full[q], q_uses >> q & 1u);
-#pragma unroll 1
-      for (uint32_t s = 0; s < kPrRing; ++s)
-        if (use > s) (void)pr_wait_long(&full[s], ((use - 1 - s) / kPrRing) & 1u);
+      for (uint32_t t = tile > 1 ? tile - 1 : 0; t <= tile; ++t) {  // (a tile that was cut short runs the wait out)
+        (void)pr_wait_long(&k_full[t & 1u], (t >> 1) & 1u);
+        (void)pr_wait_long(&v_full[t & 1u], (t >> 1) & 1u);
+      }
     }
   } else if (warp == 9) {
     // ================= MMA issuer (the warp together, one elected lane issues)
@@ -533,21 +534,21 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const uint64_t dq = tc_desc(smem_u32(smem + S::oQ), 1024, 2);
     const uint64_t dk = tc_desc(smem_u32(smem + S::oRing), 1024, 2);
     const uint64_t dv = tc_desc_wide(smem_u32(smem + S::oRing), 1024, kPrUnit / 2);
-    // A job in a word: its key tile's first ring slot modulo 16, and
+    // A job in a word: the number of its key tile modulo 16, and
     constexpr uint32_t kJob = 16, kFirst = 32, kLast = 64;  // there is one; reads these keys first, last
     constexpr uint32_t kNew = 128, kEnd = 256;              // its buffer's first of the item, last
     constexpr uint32_t kQWait = 512, kQFree = 1024, kPlace = 2048;  // queries: wait for, give back, which
-    uint32_t item = 0, slot = 0, mid[2] = {0, 0};
+    uint32_t item = 0, tile = 0, mid[2] = {0, 0};
     int j = 0, j0 = 0, n0 = 0, n1 = 0, solo = 0, fast = 0;
     bool at_item = false, begun = false, over = false;
     // The job of a step of buffer q.
     auto job = [&](int q, bool pending) -> uint32_t {
       if (fast > 0) {  // the middle of an item
         --fast;
-        const uint32_t w = slot | (q ? mid[1] : mid[0]);
+        const uint32_t w = tile | (q ? mid[1] : mid[0]);
         if (solo || q) {
           ++j;
-          slot = (slot + 5) & 15u;
+          tile = (tile + 1) & 15u;
         }
         return w;
       }
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       uint32_t w = 0;
       const int mine = solo || q == 0 ? n0 : n1, step = solo ? 2 : 1;
       if (j < mine) {
-        w = slot | kJob;
+        w = tile | kJob;
         if (solo || q == 0 || j >= n0) w |= kFirst;
         if (solo || q == 1) w |= kLast;
         if (j < j0 + step) w |= kNew;
@@ -586,7 +587,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       }
       if (solo || q) {
         ++j;
-        slot = (slot + 5) & 15u;
+        tile = (tile + 1) & 15u;
         at_item = j < count;
         // jobs in turn that neither begin nor end anything
         if (at_item && j > j0 + (solo ? 1 : 0)) {
@@ -598,33 +599,47 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       return w;
     };
     uint32_t q_uses = 0, p_uses = 0, o_uses = 0, o_first = 0;  // parities and whether O was used, a bit a buffer
+    // O of buffer q from its P and the values
+    auto values = [&](int q, uint32_t v) {
+      if (v & kNew) {  // (O of the item before has been read)
+        if (o_first >> q & 1u) {
+          pr_wait(&o_free[q], o_uses >> q & 1u, dead);
+          o_uses ^= 1u << q;
+        }
+        o_first |= 1u << q;
+      }
+      // (A lane's wait that ran out is known to the others at the item's end: until
+      // then products go on over whatever the slots hold, and do not count.)
+      if (v & kFirst) pr_wait(&v_full[v & 1u], v >> 1 & 1u, dead);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        pr_wait(&p_full[2 * q + u], p_uses >> q & 1u, dead);
+        tc_after();
+        pr_mma4_pv(tmem + 256 + 128 * q, tmem + 128 * q + 32 * u,
+                   dv + (uint64_t)(((5 * v + 3 + u) % kPrRing) * (kPrUnit >> 4)), id_o, u > 0 || !(v & kNew));
+      }
+      if (v & kLast) tc_commit(&v_free[v & 1u]);
+      p_uses ^= 1u << q;
+      if (v & kEnd) tc_commit(&o_full[q]);
+    };
     // The jobs of the last two steps and of this one.
     uint32_t before[2] = {0, 0}, w = uniform(job(0, false));
-    for (int step = 0; !dead; ++step) {
+    for (int step = 0;; ++step) {
       const int q = step & 1;
       const uint32_t v = before[0];
-      if (v & kJob) {  // O of buffer q from its P and the values
-        if (v & kNew) {  // (O of the item before has been read)
-          if (o_first >> q & 1u) {
-            pr_wait(&o_free[q], o_uses >> q & 1u, dead);
-            o_uses ^= 1u << q;
+      if (v & kJob) values(q, v);
+      // Keys that no other query tile reads come as fast as memory gives them: where
+      // they are not there yet and the other buffer's weights are, its values go
+      // first, and so make room for the keys behind.
+      if ((w & (kJob | kFirst | kLast)) == (kJob | kFirst | kLast) && (before[1] & kJob)) {
+        const uint32_t y = uniform(before[1]);
+        const long long since = clock64();
+        while (!tc_ready(&k_full[w & 1u], w >> 1 & 1u) && clock64() - since < kTcWait)
+          if (tc_ready(&p_full[2 * (q ^ 1) + 1], p_uses >> (q ^ 1) & 1u)) {
+            values(q ^ 1, y);
+            before[1] &= ~kJob;
+            break;
           }
-          o_first |= 1u << q;
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t s = (v + 3 + u) & 15u, at = s & 7u;
-          // (A lane's wait that ran out is known to the others at the next vote: until
-          // then products go on over whatever the slots hold, and do not count.)
-          if (v & kFirst) pr_wait(&full[at], s >> 3, dead);
-          pr_wait(&p_full[2 * q + u], p_uses >> q & 1u, dead);
-          tc_after();
-          pr_mma4_pv(tmem + 256 + 128 * q, tmem + 128 * q + 32 * u, dv + (uint64_t)(at * (kPrUnit >> 4)), id_o,
-                     u > 0 || !(v & kNew));
-          if (v & kLast) tc_commit(&empty[at]);
-        }
-        p_uses ^= 1u << q;
-        if (v & kEnd) tc_commit(&o_full[q]);
       }
       if (w & kJob) {  // S of buffer q from the queries and the keys
         const int from = w & kPlace ? 1 : 0;
@@ -632,24 +647,23 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           pr_wait(&q_full[from], q_uses >> from & 1u, dead);
           q_uses ^= 1u << from;
         }
+        if (w & kFirst) pr_wait(&k_full[w & 1u], w >> 1 & 1u, dead);
+        tc_after();
 #pragma unroll
-        for (int u = 0; u < 3; ++u) {
-          const uint32_t s = (w + u) & 15u, at = s & 7u;
-          if (w & kFirst) pr_wait(&full[at], s >> 3, dead);
-          tc_after();
+        for (int u = 0; u < 3; ++u)
           tc_mma4_f16<2, 2>(tmem + 128 * q, dq + (uint64_t)((from * kPrQ + u * kPrUnit) >> 4),
-                            dk + (uint64_t)(at * (kPrUnit >> 4)), id_s, u > 0);
-          if (w & kLast) tc_commit(&empty[at]);
-        }
+                            dk + (uint64_t)(((5 * w + u) % kPrRing) * (kPrUnit >> 4)), id_s, u > 0);
         tc_commit(&s_full[q]);
+        if (w & kLast) tc_commit(&k_free[w & 1u]);
         if (w & kQFree) tc_commit(&q_free[from]);
       }
       before[0] = before[1];
       before[1] = w;
-      dead = __any_sync(0xFFFFFFFFu, dead);
+      if (w & kEnd) dead = __any_sync(0xFFFFFFFFu, dead);
       w = uniform(job(q ^ 1, (before[0] | before[1]) != 0));
-      if (over && !((before[0] | before[1] | w) & kJob)) break;
+      if (over && !((before[0] | before[1] | w) & kJob)) break;  // (also where a wait ran out)
     }
+    dead = __any_sync(0xFFFFFFFFu, dead);
     if (dead) {
       tc_commit(drain);
       (void)pr_wait_long(drain, 0u);
@@ -668,7 +682,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     uint32_t uses = 0;     // jobs of this buffer so far
     uint32_t o_reads = 0;  // parities of o_full, a bit a buffer
     uint32_t shares = 0;   // items whose keys were shared out
-    uint32_t ring = 0;     // ring slots of the items before
+    uint32_t tiles = 0;    // key tiles of the items before
     for (uint32_t it = 0; !dead; ++it) {
       const PrItem& k = item_wait(it);
       if (dead || !k.valid) break;
@@ -690,8 +704,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (solo) pr_wait(&s_full[q], uses & 1u, dead);
         if (look) {
           const int r = 32 * quad + lane;
-          const uint32_t u = ring + 5 * (uint32_t)(j - j0) + 3 + (r >> 6), slot = u % kPrRing;
-          pr_wait(&full[slot], (u / kPrRing) & 1u, dead);
+          const uint32_t t = tiles + (uint32_t)(j - j0), slot = (5 * t + 3 + (r >> 6)) % kPrRing;
+          pr_wait(&v_full[t & 1u], (t >> 1) & 1u, dead);
           if (pr_look_over(smem + S::oRing + slot * kPrUnit + (r & 63) * 128, lane, j * kPrTile + r >= k.nk))
             *reinterpret_cast<volatile uint32_t*>(const_cast<uint32_t*>(&k.odd)) = 1u;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -783,8 +797,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 #pragma unroll
         for (int c = 8; c < 128; c += 8)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], fmaxf(s[c + e], s[c + e + 4]));
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * unit2;
+          for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], s[c + e], s[c + e + 4]);
+        const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * unit2;
         // The reference: the first maximum; later only where it is passed by far.
         const bool grow = mx > ref + kPrRoom || (ref == -INFINITY && mx > -INFINITY);
         if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -954,7 +968,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       }
       if (used) o_reads ^= 1u << q;
       if (used1) o_reads ^= 1u << other;
-      if (j0 < end) ring += 5 * (uint32_t)(end - j0);
+      if (j0 < end) tiles += (uint32_t)(end - j0);
       dead = __any_sync(0xFFFFFFFFu, dead);
       item_done(it);
     }
