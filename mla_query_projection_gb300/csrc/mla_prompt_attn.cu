@@ -239,8 +239,9 @@ __device__ __noinline__ void pr_add_odd(const PromptArgs& a, const PrItem& k, in
   }
 }
 
-// CAP: scores are capped; BIAS: they lose by distance.
-template <bool CAP, bool BIAS>
+// CAP: scores are capped; BIAS: they lose by distance; LONG: a loop of its own for the
+// middle of long items.
+template <bool CAP, bool BIAS, bool LONG>
 __global__ void __launch_bounds__(kPrThreads, 1)
     mla_prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ PromptMaps maps) {
   using S = PrSmem;
@@ -599,7 +600,33 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       return w;
     };
     uint32_t q_uses = 0, p_uses = 0, o_uses = 0, o_first = 0;  // parities and whether O was used, a bit a buffer
-    // O of buffer q from its P and the values
+    // (A lane's wait that ran out is known to the others at the item's end: until
+    // then products go on over whatever the slots hold, and do not count.)
+    //
+    // O of buffer q from its P and the values of key tile t
+    auto pv = [&](int q, uint32_t t, bool add, bool first, bool last) {
+      if (first) pr_wait(&v_full[t & 1u], t >> 1 & 1u, dead);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        pr_wait(&p_full[2 * q + u], p_uses >> q & 1u, dead);
+        tc_after();
+        pr_mma4_pv(tmem + 256 + 128 * q, tmem + 128 * q + 32 * u,
+                   dv + (uint64_t)(((5 * t + 3 + u) % kPrRing) * (kPrUnit >> 4)), id_o, u > 0 || add);
+      }
+      if (last) tc_commit(&v_free[t & 1u]);
+      p_uses ^= 1u << q;
+    };
+    // S of buffer q from the queries in buffer `from` and the keys of key tile t
+    auto qk = [&](int q, int from, uint32_t t, bool first, bool last) {
+      if (first) pr_wait(&k_full[t & 1u], t >> 1 & 1u, dead);
+      tc_after();
+#pragma unroll
+      for (int u = 0; u < 3; ++u)
+        tc_mma4_f16<2, 2>(tmem + 128 * q, dq + (uint64_t)((from * kPrQ + u * kPrUnit) >> 4),
+                          dk + (uint64_t)(((5 * t + u) % kPrRing) * (kPrUnit >> 4)), id_s, u > 0);
+      tc_commit(&s_full[q]);
+      if (last) tc_commit(&k_free[t & 1u]);
+    };
     auto values = [&](int q, uint32_t v) {
       if (v & kNew) {  // (O of the item before has been read)
         if (o_first >> q & 1u) {
@@ -608,24 +635,35 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         }
         o_first |= 1u << q;
       }
-      // (A lane's wait that ran out is known to the others at the item's end: until
-      // then products go on over whatever the slots hold, and do not count.)
-      if (v & kFirst) pr_wait(&v_full[v & 1u], v >> 1 & 1u, dead);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        pr_wait(&p_full[2 * q + u], p_uses >> q & 1u, dead);
-        tc_after();
-        pr_mma4_pv(tmem + 256 + 128 * q, tmem + 128 * q + 32 * u,
-                   dv + (uint64_t)(((5 * v + 3 + u) % kPrRing) * (kPrUnit >> 4)), id_o, u > 0 || !(v & kNew));
-      }
-      if (v & kLast) tc_commit(&v_free[v & 1u]);
-      p_uses ^= 1u << q;
+      pv(q, v, !(v & kNew), (v & kFirst) != 0, (v & kLast) != 0);
       if (v & kEnd) tc_commit(&o_full[q]);
     };
     // The jobs of the last two steps and of this one.
     uint32_t before[2] = {0, 0}, w = uniform(job(0, false));
     for (int step = 0;; ++step) {
       const int q = step & 1;
+      // The middle of two query tiles' keys: nothing but waits and products.  (A job's
+      // bookkeeping takes this warp 500 cycles, its products take the tensor core 1,280:
+      // with the one in every job, 1,540 went by for each.)
+      if constexpr (LONG) {
+        if (fast > 2 && q == 0 && !solo && !((before[0] | before[1]) & (kNew | kEnd)) && (before[0] & before[1] & kJob)) {
+          const int rounds = (int)uniform((uint32_t)(fast + 1) / 2);
+          uint32_t t = uniform(before[0]) & 15u;
+#pragma unroll 1
+          for (int r = 0; r < rounds; ++r, ++t) {
+            pv(0, t, true, true, false);
+            qk(0, 0, t + 1, true, false);
+            pv(1, t, true, false, true);
+            qk(1, 1, t + 1, false, true);
+          }
+          before[0] = (t & 15u) | mid[0];
+          before[1] = (t & 15u) | mid[1];
+          j += rounds;  // (this step's job was the first of them)
+          tile = (tile + rounds) & 15u;
+          fast = 0;
+          w = uniform(job(0, true));
+        }
+      }
       const uint32_t v = before[0];
       if (v & kJob) values(q, v);
       // Keys that no other query tile reads come as fast as memory gives them: where
@@ -647,14 +685,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           pr_wait(&q_full[from], q_uses >> from & 1u, dead);
           q_uses ^= 1u << from;
         }
-        if (w & kFirst) pr_wait(&k_full[w & 1u], w >> 1 & 1u, dead);
-        tc_after();
-#pragma unroll
-        for (int u = 0; u < 3; ++u)
-          tc_mma4_f16<2, 2>(tmem + 128 * q, dq + (uint64_t)((from * kPrQ + u * kPrUnit) >> 4),
-                            dk + (uint64_t)(((5 * w + u) % kPrRing) * (kPrUnit >> 4)), id_s, u > 0);
-        tc_commit(&s_full[q]);
-        if (w & kLast) tc_commit(&k_free[w & 1u]);
+        qk(q, from, w, (w & kFirst) != 0, (w & kLast) != 0);
         if (w & kQFree) tc_commit(&q_free[from]);
       }
       before[0] = before[1];
@@ -1035,7 +1066,7 @@ bool encode_heads_map(CUtensorMap* map, const void* base, int64_t tokens, int he
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool CAP, bool BIAS>
+template <bool CAP, bool BIAS, bool LONG>
 cudaError_t launch_prompt_kernel(const PromptArgs& a, const PromptMaps& maps, int ctas, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
@@ -1047,12 +1078,34 @@ cudaError_t launch_prompt_kernel(const PromptArgs& a, const PromptMaps& maps, in
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mla_prompt_attn_kernel<CAP, BIAS>, a, maps);
+  return cudaLaunchKernelEx(&cfg, mla_prompt_attn_kernel<CAP, BIAS, LONG>, a, maps);
 }
+
+// Documents of so many keys on average (over the parts that they are split into) take
+// the loop for long items.  Us without and with it:
+//   24 of 100 to 1,000 rows, 64 heads         331   356
+//   24 of 100 to 1,000 rows, 64 heads, capped 394   401
+//   1 of 1,000 rows, 64 heads                  35.3  34.5
+//   4 of 1,001 to 2,000 rows, 40 heads, biased 179   184
+//   1 of 2,000 rows, 64 heads                  85.2  81.6
+//   2 of 300 rows on 16,000 keys, 16 heads    133   123   (7 parts)
+//   1 of 4,000 rows, 32 heads                 140   128
+//   1 of 8,192 rows, 16 heads                 253   226
+// (Its instructions drive others out of the cache where items are short.)
+constexpr int kLongKeys = 2000;
 
 template <bool CAP, bool BIAS>
 cudaError_t prepare_prompt_kernel() {
-  return cudaFuncSetAttribute(mla_prompt_attn_kernel<CAP, BIAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, PrSmem::kBytes);
+  const cudaError_t e = cudaFuncSetAttribute(mla_prompt_attn_kernel<CAP, BIAS, false>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, PrSmem::kBytes);
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(mla_prompt_attn_kernel<CAP, BIAS, true>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, PrSmem::kBytes);
+}
+template <bool CAP, bool BIAS>
+cudaError_t launch_prompt_long(const PromptArgs& a, const PromptMaps& maps, int ctas, cudaStream_t stream) {
+  return a.k_tokens / a.docs / a.splits >= kLongKeys ? launch_prompt_kernel<CAP, BIAS, true>(a, maps, ctas, stream)
+                                                     : launch_prompt_kernel<CAP, BIAS, false>(a, maps, ctas, stream);
 }
 
 }  // namespace
@@ -1075,10 +1128,10 @@ cudaError_t launch_prompt(const PromptArgs& a, const PromptInputs& in, int ctas,
       !encode_heads_map(&maps.v, in.v, keys, a.heads, kNope, in.v_ts, in.v_hs, kPrTile / 2))
     return cudaErrorInvalidValue;
   const bool cap = a.cap > 0.f, bias = a.slopes != nullptr;
-  cudaError_t e = cap ? (bias ? launch_prompt_kernel<true, true>(a, maps, ctas, stream)
-                              : launch_prompt_kernel<true, false>(a, maps, ctas, stream))
-                      : (bias ? launch_prompt_kernel<false, true>(a, maps, ctas, stream)
-                              : launch_prompt_kernel<false, false>(a, maps, ctas, stream));
+  const cudaError_t e = cap ? (bias ? launch_prompt_long<true, true>(a, maps, ctas, stream)
+                                    : launch_prompt_long<true, false>(a, maps, ctas, stream))
+                            : (bias ? launch_prompt_long<false, true>(a, maps, ctas, stream)
+                                    : launch_prompt_long<false, false>(a, maps, ctas, stream));
   if (e != cudaSuccess || a.splits == 1) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(((int64_t)a.q_tokens * a.heads + 7) / 8));
