@@ -791,7 +791,8 @@ MLA_API int mla_prompt_create(mla_prompt_t* out, int heads);
  *                 i) at t * token_stride + h * head_stride + i (elements; 0 means
  *                 contiguous; multiples of 8, below 2^38).  Views of [..][192]
  *                 queries and of [..][256] up-projected rows are fine.
- *   softmax_scale >= 0, finite.  softcap: 0 for none, at most MLA_MAX_SOFTCAP.
+ *   softmax_scale >= 0, finite.  softcap: 0 for none, else 1e-6 at least
+ *                 and MLA_MAX_SOFTCAP at most.
  *   slopes        device FP32 [heads], finite, or NULL for no bias.
  *   out           device BF16 [q_tokens][heads][128], strides alike; rows that do
  *                 not overlap one another or an input.

@@ -83,6 +83,7 @@ struct PromptArgs {
   float2* part_ml;  // [splits][heads][q_tokens] reference in base 2, sum
   const uint16_t* v;
   int64_t v_ts, v_hs;
+  int tiles;       // the most tiles of 256 query rows that the documents can have together
   int group;       // heads that are handed out together
   uint32_t* next;  // items handed out beside each CTA's first, CTAs that are done; zero between calls
   uint32_t* err;

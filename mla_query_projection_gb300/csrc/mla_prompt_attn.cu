@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     int sum = 0;
 #pragma unroll 1
     for (int d = tid * each, e = min(a.docs, d + each); d < e; ++d) sum += pr_tiles(a, d);
-    scan[tid] = sum;
+    scan[tid] = min(sum, a.tiles);  // (more only where the array descends)
   }
   tc_before();
   __syncthreads();
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const int v = __shfl_up_sync(0xFFFFFFFFu, before, o);
       if (lane >= o) before += v;
     }
-    const int tiles = __shfl_sync(0xFFFFFFFFu, before, 31);
+    const int tiles = min(__shfl_sync(0xFFFFFFFFu, before, 31), a.tiles);
     before -= mine;
     const uint32_t total = (uint32_t)tiles * (uint32_t)a.heads * (uint32_t)a.splits;
     uint32_t u = blockIdx.x;
@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const uint32_t st = tmem + lanes + 128 * q;
     const float scale2 = a.scale * 1.4426950408889634f;
     // capped: x = C - 2 C / (1 + 2^(s e)), e = 2 scale log2(e) / cap, in base 2
-    const float capC = CAP ? a.cap * 1.4426950408889634f : 0.f, capE = CAP ? 2.0f * scale2 / a.cap : 0.f;
+    const float capC = CAP ? a.cap * 1.4426950408889634f : 0.f, capE = CAP ? fminf(2.0f * scale2 / a.cap, 1e30f) : 0.f;
     const float unit2 = CAP || BIAS ? 1.0f : scale2;
     uint32_t uses = 0;     // jobs of this buffer so far
     uint32_t o_reads = 0;  // parities of o_full, a bit a buffer
@@ -726,14 +726,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const float slope = BIAS ? -a.slopes[k.head] * 1.4426950408889634f : 0.f;
       float ref = -INFINITY, l = 0.f;
       for (int j = jfirst; j < nt; j += step) {
+        pr_wait(&s_full[q], uses & 1u, dead);
         // An edge in this tile (for either query tile): its values are looked over by
-        // the first that has it, here, where it would wait for the scores (they do not
-        // wait for the values, nor these for them).  Where keys are shared out the
-        // slot's use before may still be to come, and its parity would be taken for
-        // this one's: there behind the wait, when all units before are known to be in.
-        const bool look = pr_edge(k, j) && (solo || q == 0 || j >= k.n[0]);
-        if (solo) pr_wait(&s_full[q], uses & 1u, dead);
-        if (look) {
+        // the first that has it.  (Behind the wait: the scores of a tile are formed after
+        // the values of the tile before the last were waited for, so that the parity
+        // waited for here is this tile's.)
+        if (pr_edge(k, j) && (solo || q == 0 || j >= k.n[0])) {
           const int r = 32 * quad + lane;
           const uint32_t t = tiles + (uint32_t)(j - j0), slot = (5 * t + 3 + (r >> 6)) % kPrRing;
           pr_wait(&v_full[t & 1u], (t >> 1) & 1u, dead);
@@ -742,7 +740,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
         }
-        if (!solo) pr_wait(&s_full[q], uses & 1u, dead);
         ++uses;
         tc_after();
         const uint32_t at_edge = j >= safe;
@@ -1231,7 +1228,7 @@ int mla_prompt_attn(mla_prompt_t h, int docs, int64_t q_tokens, int64_t k_tokens
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return mla::launched(cudaErrorInvalidDevice);
   if (dev != h->device) return MLA_EINVAL;  // its workspace lies elsewhere
-  if (!(softmax_scale >= 0.0f) || softmax_scale > 3.0e38f || !(softcap >= 0.0f) || softcap > MLA_MAX_SOFTCAP)
+  if (!(softmax_scale >= 0.0f) || softmax_scale > 3.0e38f || !(softcap == 0.0f || softcap >= 1e-6f) || softcap > MLA_MAX_SOFTCAP)
     return MLA_EINVAL;
   if (q_tokens == 0) return MLA_OK;
   if (q_nope == nullptr || q_pe == nullptr || cu_q == nullptr || cu_k == nullptr || out == nullptr) return MLA_EINVAL;
@@ -1288,6 +1285,7 @@ int mla_prompt_attn(mla_prompt_t h, int docs, int64_t q_tokens, int64_t k_tokens
   // stay in L2.
   const int64_t group = (4 * (int64_t)h->num_sms + tiles * a.splits - 1) / (tiles * a.splits);
   a.group = (int)(group < h->heads ? group : h->heads);
+  a.tiles = (int)tiles;
   a.next = h->err + 2;
   a.v = static_cast<const uint16_t*>(in.v);
   a.v_ts = in.v_ts;

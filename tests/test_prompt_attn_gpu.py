@@ -223,6 +223,37 @@ def test_values_that_are_not_seen_may_be_anything(bad, n, at, splits):
     attn.close()
 
 
+@pytest.mark.parametrize("docs", [
+    [(200, 50), (3, 3)] * 20 + [(256, 256), (7, 7), (500, 500)],  # whose first 128 rows see nothing, again and again
+    [(1, 1), (300, 20)] * 15 + [(140, 140), (2, 2)] * 8,
+    [(40, 9000), (64, 64), (1, 3000), (5, 5)],  # split keys
+    [(130, 300), (130, 131), (1, 129), (257, 100)] * 6,
+])
+def test_documents_beside_others_that_are_not_finite(docs):
+    """Every second document is NaN all over: the others' rows are as without it."""
+    heads = 6
+    nq, nk = zip(*docs)
+    cu_q, cu_k = np.concatenate([[0], np.cumsum(nq)]), np.concatenate([[0], np.cumsum(nk)])
+    q, kv, k_pe = inputs(16, int(cu_q[-1]), int(cu_k[-1]), heads)
+    for d in range(1, len(docs), 2):
+        kv[cu_k[d]:cu_k[d + 1]] = math.nan
+        k_pe[cu_k[d]:cu_k[d + 1]] = math.nan
+        q[cu_q[d]:cu_q[d + 1]] = math.nan
+    attn = R.PromptAttention(heads)
+    lse = torch.zeros(len(q), heads, device="cuda")
+    for causal in (True, False):
+        for _ in range(3):
+            out, _ = attn.attend(q[..., :128], q[..., 128:], kv[..., :128], k_pe, kv[..., 128:], i32(cu_q), SCALE, cu_k=i32(cu_k),
+                                 causal=causal, lse=lse)
+            assert attn.error_flags() == 0
+            for d in range(0, len(docs), 2):
+                a, b, c, e = cu_q[d], cu_q[d + 1], cu_k[d], cu_k[d + 1]
+                want = document64(q[a:b].double(), kv[c:e, :, :128].double(), k_pe[c:e].double(), kv[c:e, :, 128:].double(),
+                                  causal, 0, SCALE, 0.0, None)
+                check(out[a:b], lse[a:b], want, (d, docs[d], causal))
+    attn.close()
+
+
 def test_keys_and_queries_that_are_not_finite():
     """A NaN key that a row does not see leaves it alone; a NaN query makes its own row NaN."""
     q, kv, k_pe = inputs(6, 200, 200, 2)
@@ -271,8 +302,11 @@ def test_cu_beyond_the_tensors_is_flagged_and_cut():
     want, _ = attn.attend(q[..., :128], q[..., 128:], kv[..., :128], k_pe, kv[..., 128:], i32([0, 40, 100]), SCALE)
     assert attn.error_flags() == 0
     assert torch.equal(out, want)
-    attn.attend(q[..., :128], q[..., 128:], kv[..., :128], k_pe, kv[..., 128:], i32([0, 60, 30]), SCALE)
-    assert attn.error_flags() == B.MLA_DEVERR_BAD_SLOT
+    for odd in ([0, 60, 30], [0, 100] * 40, [-5, 50, 100], [2 ** 31 - 1, -2 ** 31, 7]):
+        attn.attend(q[..., :128], q[..., 128:], kv[..., :128], k_pe, kv[..., 128:], i32(odd), SCALE)
+        assert attn.error_flags() == B.MLA_DEVERR_BAD_SLOT
+    again, _ = attn.attend(q[..., :128], q[..., 128:], kv[..., :128], k_pe, kv[..., 128:], i32([0, 40, 100]), SCALE)
+    assert attn.error_flags() == 0 and torch.equal(again, want)
     attn.close()
 
 
@@ -301,7 +335,7 @@ def test_refusals_of_a_live_handle():
                 dict(k_nope=kv[:7, :, :128]), dict(k_pe=k_pe[:7]), dict(k_pe=k_pe[:, :63]), dict(v=kv[..., 129:]),
                 dict(v=kv[..., 128:].float()), dict(cu_q=cu.long()), dict(cu_q=cu[:1]), dict(cu_k=cu[:1]), dict(prefix=cu[:0]),
                 dict(softmax_scale=-1.0), dict(softmax_scale=math.nan), dict(softmax_scale="x"), dict(softcap=-1.0),
-                dict(softcap=math.inf), dict(softcap=1001.0), dict(slopes=torch.zeros(3, device="cuda")), dict(out=out[:7]),
+                dict(softcap=math.inf), dict(softcap=1001.0), dict(softcap=1e-7), dict(slopes=torch.zeros(3, device="cuda")), dict(out=out[:7]),
                 dict(out=torch.empty(8, 1, 128, dtype=torch.bfloat16, device="cuda").expand(8, 4, 128)),
                 dict(out=torch.empty(8 * 132 + 4 * 128, dtype=torch.bfloat16, device="cuda").as_strided((8, 4, 128), (136, 128, 1))),
                 dict(lse=torch.empty(8, 3, device="cuda")), dict(q_nope=q.cpu()[..., :128]),
