@@ -748,26 +748,28 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         // instructions (caps, and keys on both sides of a biased row): 32 columns at a
         // time and back to TMEM, in a loop.  (Its code for all 128 at once drove the rest
         // out of the instruction cache: 24 documents of 100 to 1,000 rows took 579 us
-        // capped, so 390.)
+        // capped, so 398; with 64 columns 433, but 8,192 rows 344 where 32 take 359.)
         const int near = base_row + (k.nk - k.nq) - j * kPrTile;  // the warp's first row among the tile's keys
         const bool apart = CAP || (BIAS && (at_edge || !(near >= kPrTile - 1 || near + 31 <= 0)));
         if (apart) {
+          constexpr int kPre = LONG ? 64 : 32;
 #pragma unroll 1
-          for (int c0 = 0; c0 < 128; c0 += 32) {
+          for (int c0 = 0; c0 < 128; c0 += kPre) {
             const int count = left - c0;
-            float s[32];
-            tc_ld(st + c0, s);
+            float s[kPre];
+#pragma unroll
+            for (int c = 0; c < kPre; c += 32) tc_ld(st + c0 + c, *reinterpret_cast<float(*)[32]>(s + c));
             tc_wait_ld();
             tc_landed(s);
             if constexpr (CAP) {
               if (opaque(at_edge)) {  // (neighbours share a reciprocal below)
 #pragma unroll
-                for (int c = 0; c < 32; ++c) s[c] = c < count ? s[c] : 0.f;
+                for (int c = 0; c < kPre; ++c) s[c] = c < count ? s[c] : 0.f;
               }
               // 1 / (1 + 2^y) for four at a time from one reciprocal of their product:
               // 2^30 as the largest power keeps that in range (and is 1 - 2^-29 as a tangent)
 #pragma unroll
-              for (int c = 0; c < 32; c += 4) {
+              for (int c = 0; c < kPre; c += 4) {
                 const float2 e2 = make_float2(capE, capE), one = make_float2(1.0f, 1.0f);
                 float2 x = fmul2_rn(make_float2(s[c], s[c + 1]), e2), y = fmul2_rn(make_float2(s[c + 2], s[c + 3]), e2);
                 x = add2(make_float2(ex2(min_nan(x.x, 30.0f)), ex2(min_nan(x.y, 30.0f))), one);
@@ -786,13 +788,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             if constexpr (BIAS) {  // by distance from this row's place
               const float own = (float)(near - c0 + lane);
 #pragma unroll
-              for (int c = 0; c < 32; ++c) s[c] = fmaf(slope, fabsf(own - (float)c), CAP ? s[c] : s[c] * scale2);
+              for (int c = 0; c < kPre; ++c) s[c] = fmaf(slope, fabsf(own - (float)c), CAP ? s[c] : s[c] * scale2);
             }
             if (opaque(at_edge)) {
 #pragma unroll
-              for (int c = 0; c < 32; ++c) s[c] = c < count ? s[c] : -INFINITY;
+              for (int c = 0; c < kPre; ++c) s[c] = c < count ? s[c] : -INFINITY;
             }
-            tc_st32(st + c0, s);
+#pragma unroll
+            for (int c = 0; c < kPre; c += 32) tc_st32(st + c0 + c, *reinterpret_cast<float(*)[32]>(s + c));
           }
           tc_wait_st();
         }
