@@ -810,10 +810,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             for (int c = 0; c < 128; ++c) s[c] = c < left ? s[c] : -INFINITY;
           }
         }
+        // What the scores below lack: the rounding of slope times place, the same for a
+        // row's keys (2^-24 of it, which for a steep slope is more than a near key's own).
+        float low = 0.f;
         if constexpr (BIAS && !CAP) {
           if (!apart) {  // keys on one side of the warp's rows: the distance is linear
             const float sg = near > 0 ? slope : -slope, own = (float)(near + lane);
             const float2 k0 = make_float2(sg * own, sg * own), k1 = make_float2(-sg, -sg), u2 = make_float2(scale2, scale2);
+            low = fmaf(sg, own, -k0.x);
 #pragma unroll
             for (int c = 0; c < 128; c += 2) {
               const float2 x = fma2(make_float2(s[c], s[c + 1]), u2, fma2(k1, make_float2((float)c, (float)(c + 1)), k0));
@@ -829,7 +833,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         for (int c = 8; c < 128; c += 8)
 #pragma unroll
           for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], s[c + e], s[c + e + 4]);
-        const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * unit2;
+        const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * unit2 + low;
         // The reference: the first maximum; later only where it is passed by far.
         const bool grow = mx > ref + kPrRoom || (ref == -INFINITY && mx > -INFINITY);
         if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -854,7 +858,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             }
           }
         }
-        const float minus = ref == -INFINITY ? 0.f : -ref;
+        const float minus = ref == -INFINITY ? 0.f : low - ref;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {

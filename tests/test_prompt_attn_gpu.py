@@ -459,3 +459,23 @@ def test_a_prompt_in_chunks_and_its_first_decoded_token():
             assert ((got - out[t].double()).abs() <= rough).all()
     for a in (attn, latent):
         a.close()
+
+
+def test_steep_slopes_near_the_row():
+    """A slope of 3,000 leaves a row its own key alone (the next weighs e^-3000 times more
+    than any score here, |x| < 100).  Its own distance is zero, so the bias has nothing to
+    be rounded: the logarithm of the sum is its score, off by the score's bound alone (the
+    sum of 192 products and its scaling), not by 2^-24 of slope times place."""
+    n, heads = 700, 2
+    q, kv, k_pe = inputs(31, n, n, heads)
+    attn = R.PromptAttention(heads)
+    lse = torch.empty(n, heads, device="cuda")
+    cu = i32([0, n])
+    out, _ = attn.attend(q[..., :128], q[..., 128:], kv[..., :128], k_pe, kv[..., 128:], cu, SCALE,
+                         slopes=torch.full((heads,), 3000.0, device="cuda"), lse=lse)
+    attn.close()
+    key = torch.cat([kv[..., :128], k_pe[:, None].expand(n, heads, 64)], -1).double()
+    score = (q.double() * key).sum(-1) * SCALE
+    mag = (q.double() * key).abs().sum(-1) * SCALE
+    assert ((lse.double() - score).abs() <= 2.0 ** -15.4 * mag + 2.0 ** -21 * (1 + score.abs())).all()
+    assert torch.equal(out, kv[..., 128:])
