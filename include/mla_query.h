@@ -689,7 +689,7 @@ MLA_API void mla_rope_destroy(mla_rope_t h);
  *   tokens        >= 0; heads 1..MLA_MAX_ROW_HEADS.
  *   x, out        device BF16 [tokens][heads][64]: element (t, h, i) at t *
  *                 token_stride + h * head_stride + i (elements; 0 means
- *                 contiguous; multiples of 8, 64 at least).  Gathered rows
+ *                 contiguous; multiples of 8, 64 at least, below 2^38).  Gathered rows
  *                 [tokens][q_heads][576] are rows + 512, strides q_heads * 576
  *                 and 576.  out may be x itself (with its strides), and must
  *                 overlap it in no other way; its own rows must not overlap.
@@ -759,7 +759,7 @@ typedef struct mla_prompt* mla_prompt_t;
 /*
  * mla_prompt_create - the workspace of prompt attention for `heads` heads
  * (1..MLA_MAX_ROW_HEADS).  Allocates, on the current device, room for the sums of
- * query rows whose keys several workers share: 3 * SMs * 256 rows of 128 FP32 (59
+ * query rows whose keys several workers share: 3 * SMs * 256 rows of 128 FP32 (58
  * MiB on 152 SMs).  Synchronises the legacy default stream; the handle may only be
  * used on that device.
  * Returns MLA_OK, MLA_EINVAL, MLA_ENOMEM or MLA_ECUDA.

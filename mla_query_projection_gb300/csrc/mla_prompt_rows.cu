@@ -532,11 +532,11 @@ int mla_rope_create(mla_rope_t* out, const double* inv_freq, const int32_t* axis
   // 1 / (2 pi) as the sum of two doubles: the turns a position to about 2^-64
   constexpr double kTurn = 0.15915494309189535, kTurnRest = -9.839338337591243e-18;
   for (int p = 0; p < mla::kRopePairs; ++p) {
-    const double hi = inv_freq[p] * kTurn;
-    const double lo = fma(inv_freq[p], kTurn, -hi) + inv_freq[p] * kTurnRest;
-    double whole = hi - floor(hi);  // exact, in [0, 1]
-    if (whole >= 1.0) whole = 0.0;
-    h->spec.turns[p] = (uint64_t)ldexp(whole, 64) + (uint64_t)(int64_t)llrint(ldexp(lo, 64));
+    const double f = fabs(inv_freq[p]), hi = f * kTurn;
+    const double lo = fma(f, kTurn, -hi) + f * kTurnRest;
+    const double part = hi - floor(hi);  // exact, in [0, 1)
+    const uint64_t turns = (uint64_t)ldexp(part, 64) + (uint64_t)(int64_t)llrint(ldexp(lo, 64));
+    h->spec.turns[p] = inv_freq[p] < 0.0 ? 0 - turns : turns;  // (1 less a small one would not be exact)
     h->spec.axis[p] = axis != nullptr ? (uint8_t)axis[p] : 0;
     if (h->spec.axis[p] >= h->spec.axes) h->spec.axes = h->spec.axis[p] + 1;
   }
@@ -558,6 +558,9 @@ int mla_rope_apply(mla_rope_t h, int64_t tokens, int heads, const void* x, int64
   if (x == nullptr || positions == nullptr || out == nullptr) return MLA_EINVAL;
   if (pos_stride == 0) pos_stride = tokens;
   if (pos_stride < tokens || pos_offset < INT32_MIN || pos_offset > INT32_MAX) return MLA_EINVAL;
+  constexpr int64_t most = (int64_t)1 << 38;
+  if (x_head_stride >= most || x_token_stride >= most || out_head_stride >= most || out_token_stride >= most)
+    return MLA_EINVAL;
   if (x_head_stride == 0) x_head_stride = mla::kRope;
   if (x_token_stride == 0) x_token_stride = heads * x_head_stride;
   if (out_head_stride == 0) out_head_stride = mla::kRope;
@@ -586,7 +589,7 @@ int mla_cache_write(int64_t tokens, const void* kv_c, int64_t kv_c_stride, const
                     int64_t pos_offset, const int64_t* slot_mapping, void* kv_cache, int64_t num_pages, int page_size,
                     int layout, const float* k_scale, void* rows, int64_t rows_stride, unsigned* device_flags,
                     void* stream) {
-  if (tokens < 0 || !mla::known_layout(layout) || (mla::row_scaled(layout) && k_scale == nullptr)) return MLA_EINVAL;
+  if (tokens < 0 || tokens > INT64_MAX / 2048 || !mla::known_layout(layout) || (mla::row_scaled(layout) && k_scale == nullptr)) return MLA_EINVAL;
   if (!mla::cache_fits(num_pages, page_size) || !(eps >= 0.0f)) return MLA_EINVAL;
   if ((rope == nullptr) != (positions == nullptr)) return MLA_EINVAL;
   if (tokens == 0) return MLA_OK;

@@ -70,6 +70,16 @@ def test_rope_apply_refuses(rope, change):
     assert B.mla_rope_apply(**{**dict(handle=rope), **APPLY, **change}) == B.MLA_EINVAL
 
 
+@pytest.mark.parametrize("change", [dict(x_head_stride=2 ** 62), dict(x_token_stride=2 ** 38), dict(out_head_stride=2 ** 61),
+                                    dict(out_token_stride=2 ** 38)])
+def test_rope_apply_refuses_strides_beyond_any_memory(rope, change):
+    assert B.mla_rope_apply(**{**dict(handle=rope), **APPLY, "heads": 128, **change}) == B.MLA_EINVAL
+
+
+def test_cache_write_refuses_tokens_beyond_any_memory():
+    assert B.mla_cache_write(**{**WRITE, "tokens": 2 ** 63 - 1}) == B.MLA_EINVAL
+
+
 def test_calls_of_nothing_do_nothing(rope):
     assert B.mla_rope_apply(**{**dict(handle=rope), **APPLY, "tokens": 0, "x": None, "out": None}) == B.MLA_OK
     assert B.mla_cache_write(**{**WRITE, "tokens": 0, "kv_c": None}) == B.MLA_OK

@@ -100,6 +100,14 @@ def test_rope_several_axes_scale_and_offset(interleaved):
     check_turned(out, x.double().cpu(), pos, inv, axis, interleaved, 0.75, -17)
 
 
+def test_rope_negative_frequencies_turn_as_negative_positions():
+    """The same turns, so the same bytes, however small the frequency and far the position."""
+    rng = np.random.default_rng(8)
+    x, inv = bf16(rng, 2000, 16, 64), 10.0 ** rng.uniform(-8, 0, 32)
+    pos = torch.from_numpy(rng.integers(-2 ** 31 + 1, 2 ** 31, 2000).astype(np.int32)).cuda()
+    assert torch.equal(R.Rotary(-inv).apply(x, pos), R.Rotary(inv).apply(x, -pos))
+
+
 def test_rope_far_positions_and_frequencies_from_none_to_many():
     rng = np.random.default_rng(6)
     pos = np.array([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 123456789, 2 ** 24 + 1], dtype=np.int32)
