@@ -1021,7 +1021,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 // --------------------------------------------------------------- joining
 //
 // A warp a (row, head): with M the largest reference of its parts,
-// out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  A lane has four columns.
+// out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  Lane i has the weights of parts i
+// and i + 32, and four columns of every part, eight parts on their way at a time
+// before their weights are known.  Bound by the trips to L2: 7 parts of 600 rows x
+// 16 heads are 34 MB.
+constexpr int kPrJoin = 8;
 __global__ void __launch_bounds__(256) mla_prompt_join_kernel(const __grid_constant__ PromptArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -1029,25 +1033,48 @@ __global__ void __launch_bounds__(256) mla_prompt_join_kernel(const __grid_const
   pdl_launch_dependents();
   const int64_t row = item / a.heads;
   const int head = (int)(item - row * a.heads);
-  // rows of no document are left as they are
-  if (row >= a.q_tokens || row < a.cu_q[0] || row >= a.cu_q[a.docs]) return;
+  if (row >= a.q_tokens) return;
   const int64_t step = (int64_t)a.heads * a.q_tokens, at = (int64_t)head * a.q_tokens + row;
-  float M = -INFINITY;
-#pragma unroll 4
-  for (int s = 0; s < a.splits; ++s) M = fmaxf(M, a.part_ml[s * step + at].x);
-  float l = 0.f;
+  const int begin = a.cu_q[0], end = a.cu_q[a.docs];
+  float2 ml[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int s = lane + 32 * i;
+    ml[i] = s < a.splits ? a.part_ml[s * step + at] : make_float2(-INFINITY, 0.f);
+  }
+  const float4* part = reinterpret_cast<const float4*>(a.part_o + at * 128) + lane;
+  float4 v[kPrJoin];
+  auto fetch = [&](int s0) {
+#pragma unroll
+    for (int i = 0; i < kPrJoin; ++i)
+      if (s0 + i < a.splits) v[i] = part[(s0 + i) * step * 32];
+  };
+  fetch(0);
+  if (row < begin || row >= end) return;  // rows of no document are left as they are
+  float M = fmaxf(ml[0].x, ml[1].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  float f[2];  // (what saw nothing may hold anything)
+#pragma unroll
+  for (int i = 0; i < 2; ++i) f[i] = ml[i].y == 0.f ? 0.f : exp2f(ml[i].x - M);
+  const float l = warp_sum(fmaf(f[0], ml[0].y, f[1] * ml[1].y));
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int s = 0; s < a.splits; ++s) {
-    const float2 ml = a.part_ml[s * step + at];
-    if (ml.y == 0.f) continue;  // saw nothing
-    const float f = exp2f(ml.x - M);
-    const float4 v = *reinterpret_cast<const float4*>(a.part_o + (s * step + at) * 128 + 4 * lane);
-    l = fmaf(f, ml.y, l);
-    o.x = fmaf(f, v.x, o.x);
-    o.y = fmaf(f, v.y, o.y);
-    o.z = fmaf(f, v.z, o.z);
-    o.w = fmaf(f, v.w, o.w);
+#pragma unroll 1
+  for (int s0 = 0;; fetch(s0)) {
+#pragma unroll
+    for (int i = 0; i < kPrJoin; ++i) {
+      const int s = s0 + i;
+      if (s >= a.splits) break;
+      const float w = __shfl_sync(0xFFFFFFFFu, s < 32 ? f[0] : f[1], s & 31);
+      const float some = __shfl_sync(0xFFFFFFFFu, s < 32 ? ml[0].y : ml[1].y, s & 31);
+      if (some == 0.f) continue;
+      o.x = fmaf(w, v[i].x, o.x);
+      o.y = fmaf(w, v[i].y, o.y);
+      o.z = fmaf(w, v[i].z, o.z);
+      o.w = fmaf(w, v[i].w, o.w);
+    }
+    s0 += kPrJoin;
+    if (s0 >= a.splits) break;
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   uint16_t* out = a.out + row * a.o_ts + (int64_t)head * a.o_hs + 4 * lane;
