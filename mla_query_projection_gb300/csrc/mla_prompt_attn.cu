@@ -11,7 +11,10 @@
 // are tcgen05 products with FP32 accumulators in TMEM; P goes back to TMEM as BF16
 // in the place of its S, and is read from there.  While the softmax of one tile
 // runs, the tensor core works for the other: O0 += P0 V, S0 of the next keys,
-// O1 += P1 V, S1.  The next item's queries and keys are loaded, and its first
+// O1 += P1 V, S1.  A warp for each tile issues its products.  (One for both spent
+// 500 cycles a job on what comes next, against 1,280 of the tensor core, and far
+// more where items are short: 24 documents of 100 to 1,000 rows took 325 us, so
+// 304; 4,096 rows of 64 heads that see all 383 and 379.)  The next item's queries and keys are loaded, and its first
 // scores formed, while the last item's sums are written.
 //
 //  * A softmax thread owns one query row: its maximum, its sum and its mask need
@@ -54,12 +57,12 @@ namespace {
 constexpr int kPrTile = 128;     // query rows and keys of a tile
 constexpr int kPrUnit = 16384;   // bytes of a ring slot
 constexpr int kPrRing = 8;
-constexpr int kPrThreads = 384;  // two softmax warpgroups; warps that load, multiply, hand out work (and one idle)
+constexpr int kPrThreads = 384;  // two softmax warpgroups; warps that load, multiply (two) and hand out work
 constexpr int kPrQ = 3 * kPrUnit;  // a query tile: planes of 64 columns
 constexpr float kPrRoom = 20.0f;  // base 2
 constexpr int kPrChunks = 96;    // sums of the documents' tiles
 constexpr int kPrItems = 4;      // items of work in flight
-constexpr int kPrReaders = 10;   // warps that read them
+constexpr int kPrReaders = 11;   // warps that read them
 
 // One item of work: up to 256 query rows of a head and document, and the tiles
 // of its keys that this CTA goes through.
@@ -81,13 +84,14 @@ struct PrSmem {
   static constexpr int oRing = 2 * kPrQ;
   static constexpr int oBar = oRing + kPrRing * kPrUnit;
   // k_full[2] v_full[2] k_free[2] v_free[2] q_full[2] q_free[2] s_full[2] p_full[4] o_full[2] o_free[2] ml_full[2]
-  // item_full[4] item_free[4] drain
-  static constexpr int kBars = 33;
+  // item_full[4] item_free[4] drain[2] looked[2] turn[2]
+  static constexpr int kBars = 38;
   static constexpr int oItem = oBar + kBars * 8;
   static constexpr int oMl = oItem + kPrItems * (int)sizeof(PrItem);  // [2][128] reference and sum of a shared row
   static constexpr int oScan = oMl + 2 * 128 * 8;                     // [96]
   static constexpr int oTmem = oScan + kPrChunks * 4;
-  static constexpr int kBytes = oTmem + 8;
+  static constexpr int oLoads = oTmem + 4;  // key tiles whose loads have begun
+  static constexpr int kBytes = oLoads + 4;
   static_assert(kBytes <= 232448 && oBar % 8 == 0 && oItem % 8 == 0 && oMl % 8 == 0, "shared memory budget");
 };
 
@@ -239,8 +243,8 @@ __device__ __noinline__ void pr_add_odd(const PromptArgs& a, const PrItem& k, in
   }
 }
 
-// CAP: scores are capped; BIAS: they lose by distance; LONG: a loop of its own for the
-// middle of long items.
+// CAP: scores are capped; BIAS: they lose by distance; LONG: capped scores in rounds of 64
+// columns, not 32.
 template <bool CAP, bool BIAS, bool LONG>
 __global__ void __launch_bounds__(kPrThreads, 1)
     mla_prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ PromptMaps maps) {
@@ -260,9 +264,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   uint64_t* item_full = ml_full + 2;
   uint64_t* item_free = item_full + kPrItems;
   uint64_t* drain = item_free + kPrItems;
+  uint64_t* looked = drain + 2;
+  uint64_t* turn = looked + 2;
   PrItem* items = reinterpret_cast<PrItem*>(smem + S::oItem);
   volatile float2* ml = reinterpret_cast<float2*>(smem + S::oMl);
   int* scan = reinterpret_cast<int*>(smem + S::oScan);
+  volatile uint32_t* begun = reinterpret_cast<uint32_t*>(smem + S::oLoads);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + S::oTmem);
 
   const int tid = threadIdx.x, lane = tid & 31;
@@ -273,10 +280,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     for (int q = 0; q < 2; ++q) {
       mbar_init(&k_full[q], 1);
       mbar_init(&v_full[q], 1);
-      mbar_init(&k_free[q], 1);
-      mbar_init(&v_free[q], 1);
+      mbar_init(&k_free[q], 2);
+      mbar_init(&v_free[q], 2);
       mbar_init(&q_full[q], 1);
-      mbar_init(&q_free[q], 1);
+      mbar_init(&q_free[q], 2);
       mbar_init(&s_full[q], 1);
       mbar_init(&p_full[2 * q], 4);
       mbar_init(&p_full[2 * q + 1], 4);
@@ -288,8 +295,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       mbar_init(&item_full[i], 1);
       mbar_init(&item_free[i], kPrReaders);
     }
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
+    mbar_init(&looked[0], 4);
+    mbar_init(&looked[1], 4);
+    mbar_init(&turn[0], 1);
+    mbar_init(&turn[1], 1);
     mbar_fence_init();
+    *begun = 0;
     if (smem_u32(smem) & 1023u) atomicOr(a.err, MLA_DEVERR_CHECK);
   }
   if (warp == 9) {
@@ -474,6 +487,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           const uint32_t b = tile & 1u, ring = smem_u32(smem + S::oRing);
           auto unit = [&](uint32_t u) { return ring + ((5 * tile + u) % kPrRing) * kPrUnit; };
           mbar_arrive_expect_tx(&k_full[b], 3 * kPrUnit);
+          __threadfence_block();
+          *begun = tile + 1;
           tma_g2s_3d(unit(0), &maps.k_nope, 0, k.head, row, &k_full[b]);  // (K of tile t - 2 has been waited for)
           if (tile >= 2) pr_wait(&v_free[b], ((tile >> 1) - 1) & 1u, dead);
           if (dead) break;
@@ -521,183 +536,122 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         (void)pr_wait_long(&v_full[t & 1u], (t >> 1) & 1u);
       }
     }
-  } else if (warp == 9) {
-    // ================= MMA issuer (the warp together, one elected lane issues)
+  } else {
+    // ================= products: warp 9 those of buffer 0, warp 11 of buffer 1 (a warp
+    // together, one elected lane issues)
     //
-    // A job is a key tile for a softmax warpgroup.  The jobs of an item, in order: key
-    // tile after key tile for both query tiles, or shared out in turn; the buffers
-    // take turns throughout (a job may be missing).  Each step forms O += P V of the
-    // job two steps before and then S of its own job, in the same buffer: the tensor
-    // core keeps the order.
+    // A job is a key tile for a softmax warpgroup: key tile after key tile for both query
+    // tiles, or shared out in turn.  S of a job follows O += P V of the job before in the
+    // same buffer, whose P lies in its place: a buffer's jobs are a chain, and the two
+    // chains need nothing of one another but that both give a slot back (what one of
+    // them does not read, the other gives back twice).
     constexpr uint32_t kBf16 = 1u << 7;
     constexpr uint32_t id_s = tc_idesc(128, 128, 1, false, false) | kBf16;
     constexpr uint32_t id_o = tc_idesc(128, 128, 1, false, true) | kBf16;
+    const uint32_t q = uniform(warp == 11 ? 1u : 0u);
     const uint64_t dq = tc_desc(smem_u32(smem + S::oQ), 1024, 2);
     const uint64_t dk = tc_desc(smem_u32(smem + S::oRing), 1024, 2);
     const uint64_t dv = tc_desc_wide(smem_u32(smem + S::oRing), 1024, kPrUnit / 2);
-    // A job in a word: the number of its key tile modulo 16, and
-    constexpr uint32_t kJob = 16, kFirst = 32, kLast = 64;  // there is one; reads these keys first, last
-    constexpr uint32_t kNew = 128, kEnd = 256;              // its buffer's first of the item, last
-    constexpr uint32_t kQWait = 512, kQFree = 1024, kPlace = 2048;  // queries: wait for, give back, which
-    uint32_t item = 0, tile = 0, mid[2] = {0, 0};
-    int j = 0, j0 = 0, n0 = 0, n1 = 0, solo = 0, fast = 0;
-    bool at_item = false, begun = false, over = false;
-    // The job of a step of buffer q.
-    auto job = [&](int q, bool pending) -> uint32_t {
-      if (fast > 0) {  // the middle of an item
-        --fast;
-        const uint32_t w = tile | (q ? mid[1] : mid[0]);
-        if (solo || q) {
-          ++j;
-          tile = (tile + 1) & 15u;
-        }
-        return w;
-      }
-      while (!at_item) {
-        if (over) return 0;
-        // (where work is pending the items behind may wait for it)
-        if (pending && !tc_ready(&item_full[item % kPrItems], (item / kPrItems) & 1u)) return 0;
-        const PrItem& k = item_wait(item);
-        if (dead || !k.valid) {
-          over = true;
-          return 0;
-        }
-        j = j0 = k.j0;
-        n0 = k.n[0];
-        n1 = k.n[1];
-        solo = k.solo;
-        item_done(item);
-        ++item;
-        at_item = j0 < max(n0, n1);
-        begun = false;
-      }
-      const int count = solo ? n0 : n1;  // key tiles up to here
-      if (!begun && q != (solo ? solo - 1 : 0)) return 0;  // the other buffer begins
-      begun = true;
-      uint32_t w = 0;
-      const int mine = solo || q == 0 ? n0 : n1, step = solo ? 2 : 1;
-      if (j < mine) {
-        w = tile | kJob;
-        if (solo || q == 0 || j >= n0) w |= kFirst;
-        if (solo || q == 1) w |= kLast;
-        if (j < j0 + step) w |= kNew;
-        if (j + step >= mine) w |= kEnd;
-        if (j == j0) w |= kQWait;
-        if (j + 1 >= mine) w |= kQFree;
-        if (solo ? solo == 2 : q == 1) w |= kPlace;
-      }
-      if (solo || q) {
-        ++j;
-        tile = (tile + 1) & 15u;
-        at_item = j < count;
-        // jobs in turn that neither begin nor end anything
-        if (at_item && j > j0 + (solo ? 1 : 0)) {
-          fast = solo ? n0 - 2 - j : 2 * (n0 - 1 - j);
-          mid[0] = kJob | kFirst | (solo ? kLast | (solo == 2 ? kPlace : 0) : 0);
-          mid[1] = kJob | kLast | (solo ? kFirst | (solo == 2 ? kPlace : 0) : kPlace);
-        }
-      }
-      return w;
+    uint32_t tile = 0;                   // key tiles of the items before
+    uint32_t q_uses = 0;                 // parities of q_full, a bit a buffer
+    uint32_t p_uses = 0, o_uses = 0;     // jobs of this buffer, items
+    uint32_t even = ~0u, odd = ~0u;      // the last such tiles whose keys were waited for
+    uint32_t looks = 0;                  // parities of looked, a bit each
+    auto give = [&](uint64_t* bar, bool alone) {
+      tc_commit(bar);
+      if (alone) tc_commit(bar);
     };
-    uint32_t q_uses = 0, p_uses = 0, o_uses = 0, o_first = 0;  // parities and whether O was used, a bit a buffer
+    // Where both chains read a key tile, they issue in turns, a job after the other's.
+    // (Where their products mixed, their scores came at the same time, and the tensor core
+    // idled while both took their softmax: 4,096 rows of 64 heads that see all took 520 us,
+    // so 379; 24 documents of 100 to 1,000 rows 298, so 304.)
+    uint32_t turns = 0;
+    auto turn_begins = [&] {
+      if (q || turns > 0) pr_wait(&turn[q], (q ? turns : turns - 1) & 1u, dead);
+    };
+    auto turn_ends = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&turn[q ^ 1u]);
+      ++turns;
+    };
     // (A lane's wait that ran out is known to the others at the item's end: until
     // then products go on over whatever the slots hold, and do not count.)
-    //
-    // O of buffer q from its P and the values of key tile t
-    auto pv = [&](int q, uint32_t t, bool add, bool first, bool last) {
-      if (first) pr_wait(&v_full[t & 1u], t >> 1 & 1u, dead);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        pr_wait(&p_full[2 * q + u], p_uses >> q & 1u, dead);
-        tc_after();
-        pr_mma4_pv(tmem + 256 + 128 * q, tmem + 128 * q + 32 * u,
-                   dv + (uint64_t)(((5 * t + 3 + u) % kPrRing) * (kPrUnit >> 4)), id_o, u > 0 || add);
-      }
-      if (last) tc_commit(&v_free[t & 1u]);
-      p_uses ^= 1u << q;
-    };
-    // S of buffer q from the queries in buffer `from` and the keys of key tile t
-    auto qk = [&](int q, int from, uint32_t t, bool first, bool last) {
-      if (first) pr_wait(&k_full[t & 1u], t >> 1 & 1u, dead);
-      tc_after();
-#pragma unroll
-      for (int u = 0; u < 3; ++u)
-        tc_mma4_f16<2, 2>(tmem + 128 * q, dq + (uint64_t)((from * kPrQ + u * kPrUnit) >> 4),
-                          dk + (uint64_t)(((5 * t + u) % kPrRing) * (kPrUnit >> 4)), id_s, u > 0);
-      tc_commit(&s_full[q]);
-      if (last) tc_commit(&k_free[t & 1u]);
-    };
-    auto values = [&](int q, uint32_t v) {
-      if (v & kNew) {  // (O of the item before has been read)
-        if (o_first >> q & 1u) {
-          pr_wait(&o_free[q], o_uses >> q & 1u, dead);
-          o_uses ^= 1u << q;
-        }
-        o_first |= 1u << q;
-      }
-      pv(q, v, !(v & kNew), (v & kFirst) != 0, (v & kLast) != 0);
-      if (v & kEnd) tc_commit(&o_full[q]);
-    };
-    // The jobs of the last two steps and of this one.
-    uint32_t before[2] = {0, 0}, w = uniform(job(0, false));
-    for (int step = 0;; ++step) {
-      const int q = step & 1;
-      // The middle of two query tiles' keys: nothing but waits and products.  (A job's
-      // bookkeeping takes this warp 500 cycles, its products take the tensor core 1,280:
-      // with the one in every job, 1,540 went by for each.)
-      if constexpr (LONG) {
-        if (fast > 2 && q == 0 && !solo && !((before[0] | before[1]) & (kNew | kEnd)) && (before[0] & before[1] & kJob)) {
-          const int rounds = (int)uniform((uint32_t)(fast + 1) / 2);
-          uint32_t t = uniform(before[0]) & 15u;
 #pragma unroll 1
-          for (int r = 0; r < rounds; ++r, ++t) {
-            pv(0, t, true, true, false);
-            qk(0, 0, t + 1, true, false);
-            pv(1, t, true, false, true);
-            qk(1, 1, t + 1, false, true);
-          }
-          before[0] = (t & 15u) | mid[0];
-          before[1] = (t & 15u) | mid[1];
-          j += rounds;  // (this step's job was the first of them)
-          tile = (tile + rounds) & 15u;
-          fast = 0;
-          w = uniform(job(0, true));
+    for (uint32_t i = 0; !dead; ++i) {
+      const PrItem& k = item_wait(i);
+      if (dead || !k.valid) break;
+      const int j0 = k.j0, n0 = k.n[0], n1 = k.n[1], edges = min(k.safe[0], k.safe[1]);
+      const uint32_t solo = uniform((uint32_t)k.solo);
+      item_done(i);
+      const int end = max(n0, n1);
+      const uint32_t place = solo ? solo - 1 : q;  // of its queries
+      const int first = j0 + (solo && place != q ? 1 : 0), step = solo ? 2 : 1;
+      const int mine = solo || q == 0 ? n0 : n1;
+      const int shared = solo ? 0 : min(n0, n1);  // key tiles below are read by both
+      // O from P and the values of key tile j, t of all
+      auto values = [&](int j, uint32_t t) {
+        pr_wait(&v_full[t & 1u], t >> 1 & 1u, dead);
+        if (q && j < shared && j >= edges) {  // (looked over by warpgroup 0)
+          pr_wait(&looked[t & 1u], looks >> (t & 1u) & 1u, dead);
+          looks ^= 1u << (t & 1u);
         }
-      }
-      const uint32_t v = before[0];
-      if (v & kJob) values(q, v);
-      // Keys that no other query tile reads come as fast as memory gives them: where
-      // they are not there yet and the other buffer's weights are, its values go
-      // first, and so make room for the keys behind.
-      if ((w & (kJob | kFirst | kLast)) == (kJob | kFirst | kLast) && (before[1] & kJob)) {
-        const uint32_t y = uniform(before[1]);
-        const long long since = clock64();
-        while (!tc_ready(&k_full[w & 1u], w >> 1 & 1u) && clock64() - since < kTcWait)
-          if (tc_ready(&p_full[2 * (q ^ 1) + 1], p_uses >> (q ^ 1) & 1u)) {
-            values(q ^ 1, y);
-            before[1] &= ~kJob;
-            break;
-          }
-      }
-      if (w & kJob) {  // S of buffer q from the queries and the keys
-        const int from = w & kPlace ? 1 : 0;
-        if (w & kQWait) {
-          pr_wait(&q_full[from], q_uses >> from & 1u, dead);
-          q_uses ^= 1u << from;
+        if (j + 1 < shared) turn_begins();
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          pr_wait(&p_full[2 * q + u], p_uses & 1u, dead);
+          tc_after();
+          pr_mma4_pv(tmem + 256 + 128 * q, tmem + 128 * q + 32 * u,
+                     dv + (uint64_t)(((5 * t + 3 + u) % kPrRing) * (kPrUnit >> 4)), id_o, u > 0 || j > first);
         }
-        qk(q, from, w, (w & kFirst) != 0, (w & kLast) != 0);
-        if (w & kQFree) tc_commit(&q_free[from]);
+        give(&v_free[t & 1u], j >= shared);
+        ++p_uses;
+      };
+      auto scores = [&](int j, uint32_t t) {
+        // A barrier tells this tile's loads from those two tiles before by a parity: those
+        // have been waited for, or these have begun, which is after them.
+        if ((t & 1u ? odd : even) != t - 2u) {
+          const long long since = clock64();
+          while (*begun <= t && !dead) dead = clock64() - since > kTcWait;
+          __threadfence_block();
+          dead = __any_sync(0xFFFFFFFFu, dead);
+        }
+        odd = t & 1u ? t : odd;
+        even = t & 1u ? even : t;
+        pr_wait(&k_full[t & 1u], t >> 1 & 1u, dead);
+        if (j == first) pr_wait(&q_full[place], q_uses >> place & 1u, dead);
+        tc_after();
+#pragma unroll
+        for (int u = 0; u < 3; ++u)
+          tc_mma4_f16<2, 2>(tmem + 128 * q, dq + (uint64_t)((place * kPrQ + u * kPrUnit) >> 4),
+                            dk + (uint64_t)(((5 * t + u) % kPrRing) * (kPrUnit >> 4)), id_s, u > 0);
+        tc_commit(&s_full[q]);
+        if (j < shared) turn_ends();
+        give(&k_free[t & 1u], j >= shared);
+      };
+      if (first < mine) {
+        uint32_t t = uniform(tile + (uint32_t)(first - j0));
+        if (first < shared) turn_begins();
+        scores(first, t);
+        if (o_uses > 0) pr_wait(&o_free[q], o_uses - 1 & 1u, dead);  // (O of the item before has been read)
+        ++o_uses;
+#pragma unroll 1
+        for (int j = first; j + step < mine; j += step) {
+          values(j, t);
+          t += step;
+          scores(j + step, t);
+        }
+        give(&q_free[place], !solo || n0 - j0 < 2);
+        values(mine - 1 - (solo ? (mine - 1 - first) & 1 : 0), t);
+        tc_commit(&o_full[q]);
       }
-      before[0] = before[1];
-      before[1] = w;
-      if (w & kEnd) dead = __any_sync(0xFFFFFFFFu, dead);
-      w = uniform(job(q ^ 1, (before[0] | before[1]) != 0));
-      if (over && !((before[0] | before[1] | w) & kJob)) break;  // (also where a wait ran out)
+      if (n0 > j0) q_uses ^= solo == 2 ? 2u : 1u;
+      if (n1 > j0) q_uses ^= 2u;
+      if (end > j0) tile += (uint32_t)(end - j0);
+      dead = __any_sync(0xFFFFFFFFu, dead);
     }
-    dead = __any_sync(0xFFFFFFFFu, dead);
     if (dead) {
-      tc_commit(drain);
-      (void)pr_wait_long(drain, 0u);
+      tc_commit(&drain[q]);
+      (void)pr_wait_long(&drain[q], 0u);
     }
     }
   } else {
@@ -728,9 +682,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       for (int j = jfirst; j < nt; j += step) {
         pr_wait(&s_full[q], uses & 1u, dead);
         // An edge in this tile (for either query tile): its values are looked over by
-        // the first that has it.  (Behind the wait: the scores of a tile are formed after
-        // the values of the tile before the last were waited for, so that the parity
-        // waited for here is this tile's.)
+        // the first that has it.  (Behind the wait: a tile's keys are loaded after the
+        // values of the tile before the last were used, so that the parity waited for
+        // here is this tile's.)
         if (pr_edge(k, j) && (solo || q == 0 || j >= k.n[0])) {
           const int r = 32 * quad + lane;
           const uint32_t t = tiles + (uint32_t)(j - j0), slot = (5 * t + 3 + (r >> 6)) % kPrRing;
@@ -739,16 +693,17 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             *reinterpret_cast<volatile uint32_t*>(const_cast<uint32_t*>(&k.odd)) = 1u;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
+          if (!solo && q == 0 && j < k.n[1] && lane == 0) mbar_arrive(&looked[t & 1u]);
         }
         ++uses;
         tc_after();
         const uint32_t at_edge = j >= safe;
         const int left = bound - j * kPrTile;  // keys of this tile that count
         // What is done to the scores before their maximum where it takes many
-        // instructions (caps, and keys on both sides of a biased row): 32 columns at a
+        // instructions (caps, and keys on both sides of a biased row): some columns at a
         // time and back to TMEM, in a loop.  (Its code for all 128 at once drove the rest
         // out of the instruction cache: 24 documents of 100 to 1,000 rows took 579 us
-        // capped, so 398; with 64 columns 433, but 8,192 rows 344 where 32 take 359.)
+        // capped, when 32 columns took 398.)
         const int near = base_row + (k.nk - k.nq) - j * kPrTile;  // the warp's first row among the tile's keys
         const bool apart = CAP || (BIAS && (at_edge || !(near >= kPrTile - 1 || near + 31 <= 0)));
         if (apart) {
@@ -1113,30 +1068,29 @@ cudaError_t launch_prompt_kernel(const PromptArgs& a, const PromptMaps& maps, in
 }
 
 // Documents of so many keys on average (over the parts that they are split into) take
-// the loop for long items.  Us without and with it:
-//   24 of 100 to 1,000 rows, 64 heads         331   356
-//   24 of 100 to 1,000 rows, 64 heads, capped 394   401
-//   1 of 1,000 rows, 64 heads                  35.3  34.5
-//   4 of 1,001 to 2,000 rows, 40 heads, biased 179   184
-//   1 of 2,000 rows, 64 heads                  85.2  81.6
-//   2 of 300 rows on 16,000 keys, 16 heads    133   123   (7 parts)
-//   1 of 4,000 rows, 32 heads                 140   128
-//   1 of 8,192 rows, 16 heads                 253   226
-// (Its instructions drive others out of the cache where items are short.)
+// capped scores in rounds of 64 columns.  Us with 32 and with 64:
+//   24 of 100 to 1,000 rows, 64 heads         382   421
+//   1 of 1,000 rows, 64 heads                  45.1  44.7
+//   1 of 2,000 rows, 64 heads                 112.7 110.1
+//   2 of 300 rows on 16,000 keys, 16 heads    168   165   (7 parts)
+//   1 of 4,000 rows, 32 heads                 196   191
+//   1 of 8,192 rows, 16 heads                 357   345
+// (More code drives other code out of the cache where items are short.)
 constexpr int kLongKeys = 2000;
 
 template <bool CAP, bool BIAS>
 cudaError_t prepare_prompt_kernel() {
   const cudaError_t e = cudaFuncSetAttribute(mla_prompt_attn_kernel<CAP, BIAS, false>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, PrSmem::kBytes);
-  return e != cudaSuccess ? e
-                          : cudaFuncSetAttribute(mla_prompt_attn_kernel<CAP, BIAS, true>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, PrSmem::kBytes);
+  return e != cudaSuccess || !CAP ? e
+                                  : cudaFuncSetAttribute(mla_prompt_attn_kernel<CAP, BIAS, CAP>,
+                                                         cudaFuncAttributeMaxDynamicSharedMemorySize, PrSmem::kBytes);
 }
 template <bool CAP, bool BIAS>
 cudaError_t launch_prompt_long(const PromptArgs& a, const PromptMaps& maps, int ctas, cudaStream_t stream) {
-  return a.k_tokens / a.docs / a.splits >= kLongKeys ? launch_prompt_kernel<CAP, BIAS, true>(a, maps, ctas, stream)
-                                                     : launch_prompt_kernel<CAP, BIAS, false>(a, maps, ctas, stream);
+  return CAP && a.k_tokens / a.docs / a.splits >= kLongKeys
+             ? launch_prompt_kernel<CAP, BIAS, CAP>(a, maps, ctas, stream)
+             : launch_prompt_kernel<CAP, BIAS, false>(a, maps, ctas, stream);
 }
 
 }  // namespace
