@@ -186,21 +186,23 @@ __device__ __forceinline__ int pr_tiles(const PromptArgs& a, int d) {
 // A key's row of values in a ring unit (two halves of 128 bytes): zeros where the
 // key lies behind its document; else what is not finite becomes zero.  Whether
 // there was any.
-__device__ __noinline__ bool pr_look_over(uint8_t* base, int lane, bool behind) {
+__device__ __forceinline__ bool pr_look_over(uint8_t* base, int lane, bool behind) {
+  auto piece = [&](int c) {
+    return reinterpret_cast<uint4*>(base + (c >> 3) * (kPrUnit / 2) + (((c + lane) & 7) << 4));
+  };
+  uint4 w[16];
   uint32_t odd = 0;
-#pragma unroll 1
-  for (int half = 0; half < kPrUnit; half += kPrUnit / 2) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c) w[c] = *piece(c);
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {  // an exponent of all ones carries into the place of its sign
+    const uint32_t g = 0x7F807F80u, one = 0x00800080u;
+    odd |= (((w[c].x & g) + one) | ((w[c].y & g) + one)) | (((w[c].z & g) + one) | ((w[c].w & g) + one));
+  }
+  if (behind) {
 #pragma unroll 4
-    for (int c = 0; c < 8; ++c) {
-      uint4* at = reinterpret_cast<uint4*>(base + half + (((c + lane) & 7) << 4));
-      if (behind) {
-        *at = make_uint4(0, 0, 0, 0);
-      } else {
-        const uint4 w = *at;  // an exponent of all ones carries into the place of its sign
-        const uint32_t g = 0x7F807F80u, one = 0x00800080u;
-        odd |= (((w.x & g) + one) | ((w.y & g) + one)) | (((w.z & g) + one) | ((w.w & g) + one));
-      }
-    }
+    for (int c = 0; c < 16; ++c) *piece(c) = make_uint4(0, 0, 0, 0);
+    return false;
   }
   if ((odd & 0x80008000u) == 0) return false;
 #pragma unroll 1
