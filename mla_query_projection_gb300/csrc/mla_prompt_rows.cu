@@ -55,17 +55,19 @@ __device__ __forceinline__ float2 turned(float x0, float x1, float c, float s) {
 }
 
 // A CTA takes 64 rows (tokens' heads, one after another) after another, four threads
-// each: thread j of four has pairs 8 j .. 8 j + 7, whose values are 32 bytes in a row
-// (neighbours as pairs) or 16 bytes of each half (halves as pairs).  The next rows'
-// values are on their way, and their tokens' sines and cosines worked out once, into
-// shared memory, while these are turned.  A thread reads all it turns before it
-// writes, so the output may be the input.  (Without the next rows under way, 4,096
-// tokens of 128 heads took 35 us.)
-constexpr int kRopeRows = 64;
+// for two neighbours: thread j of four has pairs 8 j .. 8 j + 7, whose values are 32
+// bytes in a row (neighbours as pairs) or 16 bytes of each half (halves as pairs), and
+// reads their sines and cosines once where both rows are one token's.  (A row a thread
+// took 9.9 us for 8,191 tokens of 16 heads, so 8.6: what bounds it is shared memory.)
+// The next rows' values are on their way, and their tokens' sines and cosines worked
+// out once, into shared memory, while these are turned.  (Without that, 4,096 tokens of
+// 128 heads took 35 us, so 27: 5.0 TB/s.)  A thread reads all it turns before it
+// writes, so the output may be the input.
+constexpr int kRopeRows = 64, kRopeThreads = 2 * kRopeRows;
 
 // MANY: a CTA has more than one round.
 template <bool INTERLEAVED, bool MANY>
-__global__ void __launch_bounds__(256, 5) mla_rope_kernel(const __grid_constant__ RopeArgs r, int64_t tokens, int heads,
+__global__ void __launch_bounds__(kRopeThreads, 6) mla_rope_kernel(const __grid_constant__ RopeArgs r, int64_t tokens, int heads,
                                                           const uint16_t* x, int64_t x_ts, int64_t x_hs, uint16_t* out,
                                                           int64_t o_ts, int64_t o_hs) {
   __shared__ float2 turns[MANY ? 2 : 1][(kRopeRows + 1) * kRopePairs];
@@ -79,24 +81,30 @@ __global__ void __launch_bounds__(256, 5) mla_rope_kernel(const __grid_constant_
   pdl_wait();
   pdl_launch_dependents();
   struct Part {
-    uint4 v0, v1;
-    int64_t t;
-    int h, n;  // head, the token's place among the CTA's
+    uint4 v[2][2];
+    int64_t t;   // the first row's token
+    int h, n;    // its head, its token's place among the CTA's
   };
   // a thread's values of the rows from row0 on, and the turns of their tokens
   auto fetch = [&](int64_t row0, float2* turn) -> Part {
     Part p = {};
-    const int64_t row = row0 + (tid >> 2), t0 = token_of(row0);
+    const int64_t row = row0 + 2 * (tid >> 2), t0 = token_of(row0);
     if (row < rows) {
       p.t = token_of(row);
       p.h = (int)(row - p.t * heads);
       p.n = (int)(p.t - t0);
-      const uint16_t* at = x + p.t * x_ts + (int64_t)p.h * x_hs;
-      p.v0 = *reinterpret_cast<const uint4*>(at + a0);
-      p.v1 = *reinterpret_cast<const uint4*>(at + a1);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const bool over = p.h + e >= heads;  // the next token's first head
+        const uint16_t* at = x + (p.t + over) * x_ts + (int64_t)(over ? 0 : p.h + e) * x_hs;
+        if (e == 0 || row + 1 < rows) {
+          p.v[e][0] = *reinterpret_cast<const uint4*>(at + a0);
+          p.v[e][1] = *reinterpret_cast<const uint4*>(at + a1);
+        }
+      }
     }
     const int count = (int)(token_of((row0 + kRopeRows < rows ? row0 + kRopeRows : rows) - 1) - t0);
-    for (int n = tid >> 5; n <= count; n += 8) turn[n * kRopePairs + (tid & 31)] = rope.at(t0 + n);
+    for (int n = tid >> 5; n <= count; n += kRopeThreads / 32) turn[n * kRopePairs + (tid & 31)] = rope.at(t0 + n);
     return p;
   };
   int64_t row0 = (int64_t)blockIdx.x * kRopeRows;
@@ -105,28 +113,39 @@ __global__ void __launch_bounds__(256, 5) mla_rope_kernel(const __grid_constant_
     __syncthreads();
     Part next = {};
     if (MANY && row0 + step < rows) next = fetch(row0 + step, turns[b ^ 1]);
-    if (row0 + (tid >> 2) < rows) {
-      const float4* cs = reinterpret_cast<const float4*>(turns[b] + p.n * kRopePairs + 8 * j);  // two pairs each
-      const uint32_t w[8] = {p.v0.x, p.v0.y, p.v0.z, p.v0.w, p.v1.x, p.v1.y, p.v1.z, p.v1.w};
-      uint32_t y[8];
+    const int64_t row = row0 + 2 * (tid >> 2);
+    if (row < rows) {
+      float4 f[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 f = cs[i];
-        if constexpr (INTERLEAVED) {
-          const float2 u = turned(bf16lo(w[2 * i]), bf16hi(w[2 * i]), f.x, f.y);
-          const float2 v = turned(bf16lo(w[2 * i + 1]), bf16hi(w[2 * i + 1]), f.z, f.w);
-          y[2 * i] = pack_bf16x2(u.x, u.y);
-          y[2 * i + 1] = pack_bf16x2(v.x, v.y);
-        } else {
-          const float2 u = turned(bf16lo(w[i]), bf16lo(w[i + 4]), f.x, f.y);
-          const float2 v = turned(bf16hi(w[i]), bf16hi(w[i + 4]), f.z, f.w);
-          y[i] = pack_bf16x2(u.x, v.x);
-          y[i + 4] = pack_bf16x2(u.y, v.y);
+      for (int e = 0; e < 2; ++e) {
+        if (e == 1 && row + 1 >= rows) break;
+        const bool over = p.h + e >= heads;
+        if (e == 0 || over) {
+          const float4* cs = reinterpret_cast<const float4*>(turns[b] + (p.n + over) * kRopePairs + 8 * j);  // two pairs each
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] = cs[i];
         }
+        const uint4 v0 = p.v[e][0], v1 = p.v[e][1];
+        const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        uint32_t y[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (INTERLEAVED) {
+            const float2 u = turned(bf16lo(w[2 * i]), bf16hi(w[2 * i]), f[i].x, f[i].y);
+            const float2 v = turned(bf16lo(w[2 * i + 1]), bf16hi(w[2 * i + 1]), f[i].z, f[i].w);
+            y[2 * i] = pack_bf16x2(u.x, u.y);
+            y[2 * i + 1] = pack_bf16x2(v.x, v.y);
+          } else {
+            const float2 u = turned(bf16lo(w[i]), bf16lo(w[i + 4]), f[i].x, f[i].y);
+            const float2 v = turned(bf16hi(w[i]), bf16hi(w[i + 4]), f[i].z, f[i].w);
+            y[i] = pack_bf16x2(u.x, v.x);
+            y[i + 4] = pack_bf16x2(u.y, v.y);
+          }
+        }
+        uint16_t* o = out + (p.t + over) * o_ts + (int64_t)(over ? 0 : p.h + e) * o_hs;
+        *reinterpret_cast<uint4*>(o + a0) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4*>(o + a1) = make_uint4(y[4], y[5], y[6], y[7]);
       }
-      uint16_t* o = out + p.t * o_ts + (int64_t)p.h * o_hs;
-      *reinterpret_cast<uint4*>(o + a0) = make_uint4(y[0], y[1], y[2], y[3]);
-      *reinterpret_cast<uint4*>(o + a1) = make_uint4(y[4], y[5], y[6], y[7]);
     }
     if (!MANY) break;
     p = next;
@@ -573,9 +592,9 @@ int mla_rope_apply(mla_rope_t h, int64_t tokens, int heads, const void* x, int64
   int sms = 0;
   if (!mla::sm_count(&sms)) return MLA_ECUDA;
   int64_t ctas = (tokens * heads + mla::kRopeRows - 1) / mla::kRopeRows;
-  const bool many = ctas > 5 * (int64_t)sms;  // (five CTAs an SM are resident)
-  if (many) ctas = 5 * (int64_t)sms;
-  mla::Launch l(dim3((unsigned)ctas), 256, stream);
+  const bool many = ctas > 6 * (int64_t)sms;  // (six CTAs an SM are resident)
+  if (many) ctas = 6 * (int64_t)sms;
+  mla::Launch l(dim3((unsigned)ctas), mla::kRopeThreads, stream);
   const mla::RopeArgs r{h->spec, positions, pos_stride, pos_offset};
   auto kernel = h->spec.interleaved ? (many ? mla::mla_rope_kernel<true, true> : mla::mla_rope_kernel<true, false>)
                                     : (many ? mla::mla_rope_kernel<false, true> : mla::mla_rope_kernel<false, false>);
