@@ -157,8 +157,7 @@ __global__ void __launch_bounds__(kRopeThreads, 6) mla_rope_kernel(const __grid_
 // One warp a token: the decode step's insert (the same sums in the same order,
 // so the same bytes), with the norm and the rotation optional, and the row
 // handed on in BF16 where the caller wants it.  A lane has latent columns
-// 8 lane .. and 256 + 8 lane ..; the first eight lanes have the rope part.  The
-// next token's row is on its way while this one is worked on.
+// 8 lane .. and 256 + 8 lane .., and two values of the rope part.  The next token's row is on its way while this one is worked on.
 
 __device__ __forceinline__ float2 fma2_rn(float2 a, float2 b, float2 c) {
   float2 d;
@@ -188,7 +187,12 @@ struct Divisor {
     const float2 r = fma2_rn(fma2_rn(make_float2(-q.x, -q.y), make_float2(b, b), a), y2, q);
     return make_float2(fabsf(q.x) < 0x1p20f ? r.x : q.x, fabsf(q.y) < 0x1p20f ? r.y : q.y);
   }
-  // the E4M3 codes of two pairs of BF16 values
+  // the E4M3 codes of a pair of BF16 values, of two pairs
+  __device__ __forceinline__ uint16_t codes(uint32_t w) const {
+    const float2 a = make_float2(bf16lo(w), bf16hi(w));
+    const float2 p = plain ? make_float2(__fdiv_rn(a.x, b), __fdiv_rn(a.y, b)) : quotients(a);
+    return e4m3x2(p.x, p.y);
+  }
   __device__ __forceinline__ uint32_t codes(uint32_t w0, uint32_t w1) const {
     float2 p = make_float2(bf16lo(w0), bf16hi(w0)), q = make_float2(bf16lo(w1), bf16hi(w1));
     if (plain) {
@@ -215,7 +219,8 @@ __global__ void __launch_bounds__(256, 4) mla_cache_write_kernel(const __grid_co
   pdl_launch_dependents();
   const float tensor_scale = LAYOUT == MLA_KV_FP8_E4M3 ? *w.k_scale : 1.0f;
   struct Token {
-    uint4 v[2], pe;
+    uint4 v[2];
+    uint32_t pe;
     int64_t slot;
     float2 turn;
     float scale;
@@ -225,8 +230,7 @@ __global__ void __launch_bounds__(256, 4) mla_cache_write_kernel(const __grid_co
     const uint16_t* kv = w.kv_c + t * w.kv_c_stride;
     k.v[0] = *reinterpret_cast<const uint4*>(kv + 8 * lane);
     k.v[1] = *reinterpret_cast<const uint4*>(kv + 256 + 8 * lane);
-    k.pe = make_uint4(0, 0, 0, 0);
-    if (lane < 8) k.pe = *reinterpret_cast<const uint4*>(w.k_pe + t * w.k_pe_stride + 8 * lane);
+    k.pe = *reinterpret_cast<const uint32_t*>(w.k_pe + t * w.k_pe_stride + 2 * lane);
     k.slot = w.slots[t];
     if (k.slot >= w.capacity) {
       if (lane == 0 && w.flags != nullptr) atomicOr(w.flags, MLA_DEVERR_BAD_SLOT);
@@ -245,32 +249,22 @@ __global__ void __launch_bounds__(256, 4) mla_cache_write_kernel(const __grid_co
     const int64_t after = t + warps;
     Token next;
     if (after < w.tokens) next = fetch(after);
-    uint4 pe = k.pe;
+    uint32_t pe = k.pe;
     if (rope_on) {
-      const uint32_t x[4] = {pe.x, pe.y, pe.z, pe.w};
-      uint32_t y[4];
-      if (w.rope.spec.interleaved) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // pair 4 lane + i
-          const float c = __shfl_sync(0xFFFFFFFFu, k.turn.x, (4 * lane + i) & 31);
-          const float s = __shfl_sync(0xFFFFFFFFu, k.turn.y, (4 * lane + i) & 31);
-          const float2 p = turned(bf16lo(x[i]), bf16hi(x[i]), c, s);
-          y[i] = pack_bf16x2(p.x, p.y);
+      if (w.rope.spec.interleaved) {  // the lane's pair
+        const float2 p = turned(bf16lo(pe), bf16hi(pe), k.turn.x, k.turn.y);
+        pe = pack_bf16x2(p.x, p.y);
+      } else {  // one value each of two pairs
+        const int p0 = 2 * (lane & 15);
+        const float c0 = __shfl_sync(0xFFFFFFFFu, k.turn.x, p0), c1 = __shfl_sync(0xFFFFFFFFu, k.turn.x, p0 + 1);
+        float s0 = __shfl_sync(0xFFFFFFFFu, k.turn.y, p0), s1 = __shfl_sync(0xFFFFFFFFu, k.turn.y, p0 + 1);
+        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, pe, 16);
+        if (lane < 16) {
+          s0 = -s0;
+          s1 = -s1;
         }
-      } else {
-        const bool second = (lane & 4) != 0;  // of its pairs
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, x[i], 4);
-          const int p0 = 8 * (lane & 3) + 2 * i;
-          const float c0 = __shfl_sync(0xFFFFFFFFu, k.turn.x, p0), s0 = __shfl_sync(0xFFFFFFFFu, k.turn.y, p0);
-          const float c1 = __shfl_sync(0xFFFFFFFFu, k.turn.x, p0 + 1), s1 = __shfl_sync(0xFFFFFFFFu, k.turn.y, p0 + 1);
-          const uint32_t x0 = second ? other : x[i], x1 = second ? x[i] : other;
-          const float2 p = turned(bf16lo(x0), bf16lo(x1), c0, s0), q = turned(bf16hi(x0), bf16hi(x1), c1, s1);
-          y[i] = second ? pack_bf16x2(p.y, q.y) : pack_bf16x2(p.x, q.x);
-        }
+        pe = pack_bf16x2(fmaf(bf16lo(pe), c0, bf16lo(other) * s0), fmaf(bf16hi(pe), c1, bf16hi(other) * s1));
       }
-      pe = make_uint4(y[0], y[1], y[2], y[3]);
     }
     uint32_t n[2][4] = {{k.v[0].x, k.v[0].y, k.v[0].z, k.v[0].w}, {k.v[1].x, k.v[1].y, k.v[1].z, k.v[1].w}};
     if (w.gamma != nullptr) {
@@ -291,11 +285,14 @@ __global__ void __launch_bounds__(256, 4) mla_cache_write_kernel(const __grid_co
 #pragma unroll
       for (int g = 0; g < 2; ++g)
         *reinterpret_cast<uint4*>(o + 256 * g + 8 * lane) = make_uint4(n[g][0], n[g][1], n[g][2], n[g][3]);
-      if (lane < 8) *reinterpret_cast<uint4*>(o + kKvLora + 8 * lane) = pe;
+      *reinterpret_cast<uint32_t*>(o + kKvLora + 2 * lane) = pe;
     }
     if (k.slot >= 0) {
       uint8_t* row = w.cache + k.slot * kBytes;
       if constexpr (kDs || kNv) {
+        uint32_t p[4];  // (as the step stores it: eight values for each of the first eight lanes)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = __shfl_sync(0xFFFFFFFFu, pe, (4 * lane + i) & 31);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           float x[8];
@@ -304,15 +301,14 @@ __global__ void __launch_bounds__(256, 4) mla_cache_write_kernel(const __grid_co
             x[2 * i] = bf16lo(n[g][i]);
             x[2 * i + 1] = bf16hi(n[g][i]);
           }
-          kv_store_group(none, row, x, g == 0 ? pe : make_uint4(0, 0, 0, 0), lane + 32 * g, kDs, kNv, 1.0f);
+          kv_store_group(none, row, x, g == 0 ? make_uint4(p[0], p[1], p[2], p[3]) : make_uint4(0, 0, 0, 0), lane + 32 * g, kDs, kNv, 1.0f);
         }
       } else {
         const Divisor d(k.scale);
 #pragma unroll
         for (int g = 0; g < 2; ++g)
           *reinterpret_cast<uint2*>(row + 256 * g + 8 * lane) = make_uint2(d.codes(n[g][0], n[g][1]), d.codes(n[g][2], n[g][3]));
-        if (lane < 8)
-          *reinterpret_cast<uint2*>(row + kKvLora + 8 * lane) = make_uint2(d.codes(pe.x, pe.y), d.codes(pe.z, pe.w));
+        *reinterpret_cast<uint16_t*>(row + kKvLora + 2 * lane) = d.codes(pe);
       }
     }
     if (after >= w.tokens) break;
