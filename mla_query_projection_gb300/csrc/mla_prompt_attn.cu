@@ -868,9 +868,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const bool used = solo ? jobs > (mine ? 0 : 1) : nt > j0;  // this buffer
       const bool used1 = solo ? jobs > (mine ? 1 : 0) : k.n[other] > j0;
       if (mine) {
-        if (used) pr_wait(&o_full[q], o_reads >> q & 1u, dead);
-        if (shared) pr_wait(&o_full[other], o_reads >> other & 1u, dead);
-        tc_after();
         const bool have = i < k.nq, part = a.splits > 1;
         const uint32_t used_ = used, shared_ = shared, part_ = part;
         const int64_t row = k.q0 + i;
@@ -889,6 +886,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const int left = k.nq - (i - sub);  // rows from the first of the four on
         float* po = a.part_o + (((int64_t)k.split * a.heads + k.head) * a.q_tokens + row) * 128;
         uint16_t* o = a.out + (row - sub) * a.o_ts + (int64_t)k.head * a.o_hs + 8 * sub;
+        if (used) pr_wait(&o_full[q], o_reads >> q & 1u, dead);
+        if (shared) pr_wait(&o_full[other], o_reads >> other & 1u, dead);
+        tc_after();
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32) {
           const bool used = opaque(used_), shared = opaque(shared_), part = opaque(part_);
