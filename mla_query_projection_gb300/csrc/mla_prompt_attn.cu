@@ -30,8 +30,8 @@
 //  * Keys and values come by TMA in units of 16 KiB through a ring of eight: 64
 //    columns of 128 keys, or 64 keys of 128 values.
 //  * A value that a row does not see may be an infinity or a NaN, and zero times
-//    it is not zero.  So on the tiles with an edge the softmax threads look their
-//    values over first: rows behind the document are zeroed; an infinity or a NaN
+//    it is not zero.  So on the tiles with an edge the warp that hands out items looks
+//    the values over first: rows behind the document are zeroed; an infinity or a NaN
 //    inside it is replaced by zero and added at the end to the rows that see it.
 //  * Items are handed out on the GPU as CTAs become free, the longest first: their
 //    lengths are known there alone.
@@ -84,7 +84,7 @@ struct PrSmem {
   static constexpr int oRing = 2 * kPrQ;
   static constexpr int oBar = oRing + kPrRing * kPrUnit;
   // k_full[2] v_full[2] k_free[2] v_free[2] q_full[2] q_free[2] s_full[2] p_full[4] o_full[2] o_free[2] ml_full[2]
-  // item_full[4] item_free[4] drain[2] looked[2] turn[2]
+  // item_full[4] item_free[4] drain[2] v_seen[2] turn[2]
   static constexpr int kBars = 38;
   static constexpr int oItem = oBar + kBars * 8;
   static constexpr int oMl = oItem + kPrItems * (int)sizeof(PrItem);  // [2][128] reference and sum of a shared row
@@ -190,21 +190,27 @@ __device__ __forceinline__ bool pr_look_over(uint8_t* base, int lane, bool behin
   auto piece = [&](int c) {
     return reinterpret_cast<uint4*>(base + (c >> 3) * (kPrUnit / 2) + (((c + lane) & 7) << 4));
   };
-  uint4 w[16];
-  uint32_t odd = 0;
+  uint32_t odd[2] = {0u, 0u};  // sums of zero times each value: NaN from what is not finite
+  auto times_zero = [](uint32_t w, uint32_t& sum) { asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(w), "r"(0u)); };
 #pragma unroll
-  for (int c = 0; c < 16; ++c) w[c] = *piece(c);
+  for (int c0 = 0; c0 < 16; c0 += 8) {
+    uint4 w[8];
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {  // an exponent of all ones carries into the place of its sign
-    const uint32_t g = 0x7F807F80u, one = 0x00800080u;
-    odd |= (((w[c].x & g) + one) | ((w[c].y & g) + one)) | (((w[c].z & g) + one) | ((w[c].w & g) + one));
+    for (int c = 0; c < 8; ++c) w[c] = *piece(c0 + c);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      times_zero(w[c].x, odd[0]);
+      times_zero(w[c].y, odd[1]);
+      times_zero(w[c].z, odd[0]);
+      times_zero(w[c].w, odd[1]);
+    }
   }
   if (behind) {
-#pragma unroll 4
+#pragma unroll 1
     for (int c = 0; c < 16; ++c) *piece(c) = make_uint4(0, 0, 0, 0);
     return false;
   }
-  if ((odd & 0x80008000u) == 0) return false;
+  if (((odd[0] | odd[1]) & 0x7FFF7FFFu) == 0) return false;
 #pragma unroll 1
   for (int c = 0; c < 128; ++c) {
     uint16_t* e = reinterpret_cast<uint16_t*>(base + (c >> 6) * (kPrUnit / 2)) + (c & 63);
@@ -266,8 +272,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   uint64_t* item_full = ml_full + 2;
   uint64_t* item_free = item_full + kPrItems;
   uint64_t* drain = item_free + kPrItems;
-  uint64_t* looked = drain + 2;
-  uint64_t* turn = looked + 2;
+  uint64_t* v_seen = drain + 2;
+  uint64_t* turn = v_seen + 2;
   PrItem* items = reinterpret_cast<PrItem*>(smem + S::oItem);
   volatile float2* ml = reinterpret_cast<float2*>(smem + S::oMl);
   int* scan = reinterpret_cast<int*>(smem + S::oScan);
@@ -299,8 +305,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     }
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
-    mbar_init(&looked[0], 4);
-    mbar_init(&looked[1], 4);
+    mbar_init(&v_seen[0], 1);
+    mbar_init(&v_seen[1], 1);
     mbar_init(&turn[0], 1);
     mbar_init(&turn[1], 1);
     mbar_fence_init();
@@ -347,7 +353,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 10) {
-    // ================= work: the items in order, each CTA the next one that is free
+    // ================= work: the items in order, each CTA the next one that is free; and the
+    // values of every key tile as they come, looked over before they are used
     constexpr int kOwn = kPrChunks / 32;  // sums a lane
     int mine = 0;
 #pragma unroll
@@ -361,22 +368,24 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const int tiles = min(__shfl_sync(0xFFFFFFFFu, before, 31), a.tiles);
     before -= mine;
     const uint32_t total = (uint32_t)tiles * (uint32_t)a.heads * (uint32_t)a.splits;
-    uint32_t u = blockIdx.x;
     int at = -1, doc = 0, tile = 0, last_q = 1;
-#pragma unroll 1
-    for (uint32_t i = 0;; ++i) {
-      // ahead: the answer is there by the time it is needed
-      uint32_t ahead = 0;
-      if (lane == 0 && u < total) ahead = atomicAdd(a.next, 1u) + gridDim.x;
-      if (i >= kPrItems) pr_wait_warp(&item_free[i % kPrItems], (i / kPrItems - 1) & 1u, dead);
-      PrItem& k = items[i % kPrItems];
-      if (u >= total || dead) {
+    uint32_t u = blockIdx.x, ahead = 0;  // this item's number; the next one's (lane 0), asked for ahead
+    uint32_t handed = 0, seen = 0;       // items handed out, gone through
+    uint32_t t = 0;                      // key tiles gone through
+    int j = 0, end = 0;                  // of item `seen`
+    bool more = true, within = false;
+    // The next item, or that there is none.
+    auto hand_out = [&] {
+      PrItem& k = items[handed % kPrItems];
+      if (u >= total) {
+        more = false;
         if (lane == 0) {
           k.valid = 0;
-          mbar_arrive(&item_full[i % kPrItems]);
+          mbar_arrive(&item_full[handed % kPrItems]);
         }
-        break;
+        return;
       }
+      if (lane == 0) ahead = atomicAdd(a.next, 1u) + gridDim.x;
       // groups of heads; of a group the last tiles first (the longest where rows see
       // what lies before them), head after head
       const uint32_t per_group = (uint32_t)a.group * (uint32_t)tiles * (uint32_t)a.splits;
@@ -450,9 +459,56 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         }
         k.odd = 0;
         k.valid = 1;
-        mbar_arrive(&item_full[i % kPrItems]);
+        mbar_arrive(&item_full[handed % kPrItems]);
       }
-      u = __shfl_sync(0xFFFFFFFFu, ahead, 0);
+      __syncwarp();
+      ++handed;
+    };
+    long long since = clock64();
+#pragma unroll 1
+    while (!dead && (more || seen < handed)) {
+      if (!within && seen < handed) {
+        const PrItem& k = items[seen % kPrItems];
+        j = k.j0;
+        end = max(k.n[0], k.n[1]);
+        within = j < end;
+        if (!within) ++seen;
+        continue;
+      }
+      if (within && __any_sync(0xFFFFFFFFu, tc_ready(&v_full[t & 1u], t >> 1 & 1u))) {
+        // the values of key tile t, looked over where they have an edge
+        PrItem& k = items[seen % kPrItems];
+        pr_wait_warp(&v_full[t & 1u], t >> 1 & 1u, dead);
+        if (pr_edge(k, j)) {
+          bool odd = false;
+#pragma unroll 1
+          for (int r = lane; r < kPrTile; r += 32)
+            odd = pr_look_over(smem + S::oRing + ((5 * t + 3 + (r >> 6)) % kPrRing) * kPrUnit + (r & 63) * 128, lane,
+                               j * kPrTile + r >= k.nk) || odd;
+          if (odd) *reinterpret_cast<volatile uint32_t*>(&k.odd) = 1u;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_seen[t & 1u]);
+        ++t;
+        within = ++j < end;
+        if (!within) ++seen;
+        since = clock64();
+        continue;
+      }
+      if (more && (handed < kPrItems || (handed - seen < kPrItems &&
+                                         __all_sync(0xFFFFFFFFu, tc_ready(&item_free[handed % kPrItems],
+                                                                          (handed / kPrItems - 1) & 1u))))) {
+        u = handed > 0 ? __shfl_sync(0xFFFFFFFFu, ahead, 0) : u;
+        hand_out();
+        since = clock64();
+        continue;
+      }
+      dead = __any_sync(0xFFFFFFFFu, clock64() - since > kTcWait);
+    }
+    if (dead && more && lane == 0) {
+      items[handed % kPrItems].valid = 0;
+      mbar_arrive(&item_full[handed % kPrItems]);
     }
     // the last CTA to come here leaves the count of items as it was
     if (lane == 0) {
@@ -558,7 +614,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     uint32_t q_uses = 0;                 // parities of q_full, a bit a buffer
     uint32_t p_uses = 0, o_uses = 0;     // jobs of this buffer, items
     uint32_t even = ~0u, odd = ~0u;      // the last such tiles whose keys were waited for
-    uint32_t looks = 0;                  // parities of looked, a bit each
     auto give = [&](uint64_t* bar, bool alone) {
       tc_commit(bar);
       if (alone) tc_commit(bar);
@@ -582,7 +637,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     for (uint32_t i = 0; !dead; ++i) {
       const PrItem& k = item_wait(i);
       if (dead || !k.valid) break;
-      const int j0 = k.j0, n0 = k.n[0], n1 = k.n[1], edges = min(k.safe[0], k.safe[1]);
+      const int j0 = k.j0, n0 = k.n[0], n1 = k.n[1];
       const uint32_t solo = uniform((uint32_t)k.solo);
       item_done(i);
       const int end = max(n0, n1);
@@ -592,11 +647,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const int shared = solo ? 0 : min(n0, n1);  // key tiles below are read by both
       // O from P and the values of key tile j, t of all
       auto values = [&](int j, uint32_t t) {
-        pr_wait(&v_full[t & 1u], t >> 1 & 1u, dead);
-        if (q && j < shared && j >= edges) {  // (looked over by warpgroup 0)
-          pr_wait(&looked[t & 1u], looks >> (t & 1u) & 1u, dead);
-          looks ^= 1u << (t & 1u);
-        }
+        pr_wait(&v_seen[t & 1u], t >> 1 & 1u, dead);
         if (j + 1 < shared) turn_begins();
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -669,7 +720,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     uint32_t uses = 0;     // jobs of this buffer so far
     uint32_t o_reads = 0;  // parities of o_full, a bit a buffer
     uint32_t shares = 0;   // items whose keys were shared out
-    uint32_t tiles = 0;    // key tiles of the items before
     for (uint32_t it = 0; !dead; ++it) {
       const PrItem& k = item_wait(it);
       if (dead || !k.valid) break;
@@ -683,20 +733,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       float ref = -INFINITY, l = 0.f;
       for (int j = jfirst; j < nt; j += step) {
         pr_wait(&s_full[q], uses & 1u, dead);
-        // An edge in this tile (for either query tile): its values are looked over by
-        // the first that has it.  (Behind the wait: a tile's keys are loaded after the
-        // values of the tile before the last were used, so that the parity waited for
-        // here is this tile's.)
-        if (pr_edge(k, j) && (solo || q == 0 || j >= k.n[0])) {
-          const int r = 32 * quad + lane;
-          const uint32_t t = tiles + (uint32_t)(j - j0), slot = (5 * t + 3 + (r >> 6)) % kPrRing;
-          pr_wait(&v_full[t & 1u], (t >> 1) & 1u, dead);
-          if (pr_look_over(smem + S::oRing + slot * kPrUnit + (r & 63) * 128, lane, j * kPrTile + r >= k.nk))
-            *reinterpret_cast<volatile uint32_t*>(const_cast<uint32_t*>(&k.odd)) = 1u;
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (!solo && q == 0 && j < k.n[1] && lane == 0) mbar_arrive(&looked[t & 1u]);
-        }
         ++uses;
         tc_after();
         const uint32_t at_edge = j >= safe;
@@ -960,7 +996,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       }
       if (used) o_reads ^= 1u << q;
       if (used1) o_reads ^= 1u << other;
-      if (j0 < end) tiles += (uint32_t)(end - j0);
       dead = __any_sync(0xFFFFFFFFu, dead);
       item_done(it);
     }
@@ -1270,10 +1305,23 @@ int mla_prompt_attn(mla_prompt_t h, int docs, int64_t q_tokens, int64_t k_tokens
   a.splits = mla::prompt_splits(tiles * h->heads, q_tokens * h->heads,
                                 (k_tokens / docs + mla::kPrTile - 1) / mla::kPrTile, h->num_sms);
   const int64_t items = tiles * h->heads * a.splits;
-  // Heads whose tiles are handed out together, longest first: enough for four items
-  // an SM, so that short ones are left for the end; no more, so that their keys
-  // stay in L2.
-  const int64_t group = (4 * (int64_t)h->num_sms + tiles * a.splits - 1) / (tiles * a.splits);
+  // Heads whose tiles are handed out together, the last tiles first, each for all of the
+  // group's heads.  Where rows see what lies before them: enough for four items an SM, so
+  // that short ones are left for the end; and as many as keep a document's keys and values
+  // in half of L2, since rows of memory hold neighbouring heads.  Where all rows see all:
+  // two items an SM, since only keys are shared.  Us with four items an SM throughout,
+  // and as it is:
+  //   24 of 100 to 1,000 rows, 64 heads, capped   380  358
+  //   4 of 1,001 to 2,000 rows, 40 heads, biased  163  153
+  //   20 of 600 rows, 128 heads                   515  448
+  //   1 of 4,096 rows, 64 heads                   264  232
+  //   1 of 4,096 rows, 64 heads, all to all       393  375
+  //   4 of 2,000 rows, 64 heads, all to all       422  416
+  //   16 of 500 rows, 64 heads, all to all        143  157
+  constexpr int64_t kKeys = (int64_t)64 << 20, row = 2 * mla::kNope * (int64_t)sizeof(uint16_t);
+  const int64_t each = tiles * a.splits, keys = (k_tokens / docs + 1) * row;
+  const int64_t even = ((causal ? 4 : 2) * (int64_t)h->num_sms + each - 1) / each;
+  const int64_t group = causal && kKeys / keys > even ? kKeys / keys : even;
   a.group = (int)(group < h->heads ? group : h->heads);
   a.tiles = (int)tiles;
   a.next = h->err + 2;
