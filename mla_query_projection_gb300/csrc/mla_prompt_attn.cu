@@ -13,8 +13,8 @@
 // runs, the tensor core works for the other: O0 += P0 V, S0 of the next keys,
 // O1 += P1 V, S1.  A warp for each tile issues its products.  (One for both spent
 // 500 cycles a job on what comes next, against 1,280 of the tensor core, and far
-// more where items are short: 24 documents of 100 to 1,000 rows took 325 us, so
-// 304; 4,096 rows of 64 heads that see all 383 and 379.)  The next item's queries and keys are loaded, and its first
+// more where items are short: 24 documents of 100 to 1,000 rows took 325 us, then
+// 304.)  The next item's queries and keys are loaded, and its first
 // scores formed, while the last item's sums are written.
 //
 //  * A softmax thread owns one query row: its maximum, its sum and its mask need
@@ -37,6 +37,12 @@
 //    lengths are known there alone.
 //  * Few query rows: the keys are split over several CTAs, whose sums a second
 //    kernel joins.
+//
+// Long documents are bound by the tensor pipe: 8,192 causal rows of 16 heads take 217
+// us (1,582 TFLOP/s), 4,096 rows of 64 heads that see all 375 (1,833).  One row on
+// 65,536 keys is bound by memory: 88 us, 6.2 TB/s.  Short documents are bound by the
+// chain of scores, softmax and sums, of which TMEM holds two: 24 of 100 to 1,000 rows,
+// 64 heads, take 283 us, where their bytes take 144.
 #include <stdlib.h>
 
 #include "mla_attn_tc.cuh"
@@ -620,8 +626,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     };
     // Where both chains read a key tile, they issue in turns, a job after the other's.
     // (Where their products mixed, their scores came at the same time, and the tensor core
-    // idled while both took their softmax: 4,096 rows of 64 heads that see all took 520 us,
-    // so 379; 24 documents of 100 to 1,000 rows 298, so 304.)
+    // idled while both took their softmax: 4,096 rows of 64 heads that see all took 520
+    // us, in turns 379; 24 documents of 100 to 1,000 rows 298 and 304.)
     uint32_t turns = 0;
     auto turn_begins = [&] {
       if (q || turns > 0) pr_wait(&turn[q], (q ? turns : turns - 1) & 1u, dead);

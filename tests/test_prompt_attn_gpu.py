@@ -479,3 +479,19 @@ def test_steep_slopes_near_the_row():
     mag = (q.double() * key).abs().sum(-1) * SCALE
     assert ((lse.double() - score).abs() <= 2.0 ** -15.4 * mag + 2.0 ** -21 * (1 + score.abs())).all()
     assert torch.equal(out, kv[..., 128:])
+
+
+@pytest.mark.parametrize("seed,causal,prefix,cap,bias", [(1, True, False, 0.0, False), (2, True, True, 0.0, False),
+                                                         (3, False, False, 0.0, False), (4, True, False, 30.0, False),
+                                                         (5, True, True, 0.0, True), (6, True, True, 20.0, True)])
+def test_many_items_of_all_kinds_one_after_another(seed, causal, prefix, cap, bias):
+    """Fifty items a worker: one query tile or two, one key tile or several, rows before all
+    keys, documents without rows or without keys, in random order."""
+    rng = np.random.default_rng(seed)
+    docs = []
+    for _ in range(45):
+        nq = int(rng.choice([0, 1, 5, 64, 127, 128, 129, 200, 255, 256, 257, 300, 400]))
+        more = int(rng.choice([0, 0, 0, 1, 100, 128, 300, -1, -100, -1000]))
+        docs.append((nq, max(0, nq + more)))
+    attend(seed, docs, 128, causal=causal, prefix=[int(x) for x in rng.integers(0, 300, 45)] if prefix else None, cap=cap,
+           slopes=[float(2.0 ** -(1 + h % 8)) for h in range(128)] if bias else None, pad=2)
