@@ -495,3 +495,20 @@ def test_many_items_of_all_kinds_one_after_another(seed, causal, prefix, cap, bi
         docs.append((nq, max(0, nq + more)))
     attend(seed, docs, 128, causal=causal, prefix=[int(x) for x in rng.integers(0, 300, 45)] if prefix else None, cap=cap,
            slopes=[float(2.0 ** -(1 + h % 8)) for h in range(128)] if bias else None, pad=2)
+
+
+def test_the_order_of_the_work_does_not_show():
+    """Items go to whichever worker is free: calls alike give the same bytes."""
+    rng = np.random.default_rng(12)
+    n = [int(x) for x in rng.choice([1, 60, 128, 130, 250, 300, 513], 20)]
+    heads, cu = 96, np.concatenate([[0], np.cumsum(n)])
+    q, kv, k_pe = inputs(12, int(cu[-1]), int(cu[-1]), heads)
+    attn, where = R.PromptAttention(heads), i32(cu)
+    got = []
+    for _ in range(6):
+        lse = torch.empty(len(q), heads, device="cuda")
+        out, _ = attn.attend(q[..., :128], q[..., 128:], kv[..., :128], k_pe, kv[..., 128:], where, SCALE, softcap=25.0, lse=lse)
+        got.append((out, lse))
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+    attn.close()
