@@ -172,7 +172,9 @@ __device__ __forceinline__ float2 fma2_rn(float2 a, float2 b, float2 c) {
 // them: by P. Markstein's theorem (IBM Journal of Research and Development 34, 1990),
 // with y the rounded reciprocal of b and q = a y rounded, q + (a - b q) y rounded once
 // is the rounded a / b.  Where the quotient is far beyond E4M3's range the product is
-// as good (and may be infinite); divisors near the ends of FP32's range are divided by.
+// as good (and may be infinite), and where it is zero the product alone has the sign of
+// a / b (a sum of zeros of both signs is +0); divisors near the ends of FP32's range are
+// divided by.
 struct Divisor {
   float b, y;
   bool plain;
@@ -181,11 +183,14 @@ struct Divisor {
     y = __frcp_rn(divisor);
     plain = !(fabsf(divisor) >= 0x1p-60f && fabsf(divisor) <= 0x1p60f);
   }
+  __device__ __forceinline__ static float corrected(float q, float r) {
+    return fabsf(q) < 0x1p20f && q != 0.0f ? r : q;
+  }
   // two, in packed arithmetic
   __device__ __forceinline__ float2 quotients(float2 a) const {
     const float2 y2 = make_float2(y, y), q = fmul2_rn(a, y2);
     const float2 r = fma2_rn(fma2_rn(make_float2(-q.x, -q.y), make_float2(b, b), a), y2, q);
-    return make_float2(fabsf(q.x) < 0x1p20f ? r.x : q.x, fabsf(q.y) < 0x1p20f ? r.y : q.y);
+    return make_float2(corrected(q.x, r.x), corrected(q.y, r.y));
   }
   // the E4M3 codes of a pair of BF16 values, of two pairs
   __device__ __forceinline__ uint16_t codes(uint32_t w) const {
