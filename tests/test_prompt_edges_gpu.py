@@ -11,7 +11,7 @@ import torch
 from mla_query_projection_gb300 import binding as B
 from mla_query_projection_gb300 import runner as R
 
-from .test_prompt_attn_gpu import cuda_device  # noqa: F401
+from .test_prompt_attn_gpu import attend, cuda_device  # noqa: F401
 from .test_prompt_rows_gpu import write_case
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +48,43 @@ def test_zeros_keep_their_sign_in_the_cache(layout, norm):
             want = torch.where(torch.signbit(x[keep].float()), 0x80, 0x00)
             assert torch.equal(codes[zero].int(), want[zero].int())
     step.close()
+
+
+# ---------------------------------------------------------------- attention
+
+
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("causal,prefix", [(True, None), (True, 700), (False, None)])
+@pytest.mark.parametrize("cap", [15.0, 400.0])
+def test_long_capped_documents(cap, causal, prefix, slopes):
+    """Whole query tiles over 2,000 keys and more that are not split: capped scores are taken
+    64 columns at a time, with and without biases, on the diagonal, in a prefix, on both sides."""
+    heads = 16
+    attend(41, [(2117, 2117)], heads, causal=causal, prefix=None if prefix is None else [prefix], cap=cap,
+           slopes=[0.3 * 2.0 ** -h for h in range(heads)] if slopes else None)
+
+
+@pytest.mark.parametrize("slopes", [False, True])
+def test_long_capped_documents_of_ragged_lengths(slopes):
+    docs = [(2500, 2500), (130, 2700), (1900, 1800), (257, 2300)]
+    attend(42, docs, 5, prefix=[0, 2650, 40, 1], cap=25.0, slopes=[0.2, -0.01, 0.0, 2.0 ** -7, 1.0] if slopes else None)
+
+
+@pytest.mark.parametrize("nq,nk,heads", [(3, 20000, 16), (300, 4000, 7), (129, 5000, 3)])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("causal,prefix", [(True, None), (True, 1500), (False, None)])
+def test_split_keys_with_biases_and_prefixes(nq, nk, heads, cap, causal, prefix):
+    attend(nk, [(nq, nk)], heads, causal=causal, prefix=None if prefix is None else [nk - nq + 20 if nq > 128 else prefix],
+           cap=cap, slopes=[0.05 * 2.0 ** -h for h in range(heads)])
+
+
+@pytest.mark.parametrize("docs,heads", [([(700, 700)], 3), ([(100, 900)], 2), ([(2, 6000)], 3), ([(260, 3000)], 4)])
+@pytest.mark.parametrize("cap", [0.0, 900.0])
+def test_references_that_move_with_every_key_tile(docs, heads, cap):
+    """Scores rise by 16 * 16 * 192^-0.5 = 18.5 a key tile, 26.6 in base 2: further than a
+    reference may lie below them, in every tile."""
+    def change(q, kv, k_pe):
+        q[..., 0] = 16.0
+        kv[:, :, 0] = (torch.arange(len(kv), device="cuda").float() / 8).to(torch.bfloat16)[:, None]
+
+    attend(43, docs, heads, cap=cap, change=change)
