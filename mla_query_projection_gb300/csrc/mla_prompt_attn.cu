@@ -32,7 +32,8 @@
 //  * A value that a row does not see may be an infinity or a NaN, and zero times
 //    it is not zero.  So on the tiles with an edge the warp that hands out items looks
 //    the values over first: rows behind the document are zeroed; an infinity or a NaN
-//    inside it is replaced by zero and added at the end to the rows that see it.
+//    inside it is replaced by zero and put at the end into the rows that see it.  So are
+//    those of the other tiles, wherever the sums come out infinite or NaN.
 //  * Items are handed out on the GPU as CTAs become free, the longest first: their
 //    lengths are known there alone.
 //  * Few query rows: the keys are split over several CTAs, whose sums a second
@@ -225,34 +226,46 @@ __device__ __forceinline__ bool pr_look_over(uint8_t* base, int lane, bool behin
   return true;
 }
 
-// Values that are not finite and lie in the tiles that were looked over (where they
-// count as zero in the products): added to a stored row that sees the first `bound`
-// keys, its sums (`part`) or its output.  Slow, and rare.
-__device__ __noinline__ void pr_add_odd(const PromptArgs& a, const PrItem& k, int j0, int end, int bound, float* part,
+// Infinities and NaN among the values: a row's column that sees any is their sum, however
+// small their weights (which are above zero, though FP32 may hold them as zero, and zero
+// times an infinity is NaN; in the tiles that were looked over they count as zero in the
+// products).  A warp for its 32 stored rows, `live` where a lane's counts: rows see
+// ascending numbers of keys, so the item's keys are gone through once, four columns a
+// lane, and each row takes the sums where its keys end.  Slow, and rare.
+__device__ __noinline__ void pr_put_odd(const PromptArgs& a, const PrItem& k, int j0, int end, int bound, bool live, float* part,
                                         uint16_t* out) {
+  constexpr int kAhead = 8;
+  const int lane = threadIdx.x & 31, last = min(end * kPrTile, k.nk);
+  const unsigned rows = __ballot_sync(0xFFFFFFFFu, live);
+  const uint16_t* v = a.v + (int64_t)k.k0 * a.v_ts + (int64_t)k.head * a.v_hs + 4 * lane;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  int key = j0 * kPrTile;
 #pragma unroll 1
-  for (int c = 0; c < 128; c += 4) {
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int r = 0; r < 32; ++r) {
+    const int upto = min(__shfl_sync(0xFFFFFFFFu, bound, r), last);
 #pragma unroll 1
-    for (int j = j0; j < end; ++j) {
-      if (!pr_edge(k, j)) continue;
-#pragma unroll 1
-      for (int key = j * kPrTile, e = min(min(key + kPrTile, bound), k.nk); key < e; ++key) {
-        const uint2 w =
-            *reinterpret_cast<const uint2*>(a.v + (int64_t)(k.k0 + key) * a.v_ts + (int64_t)k.head * a.v_hs + c);
-        const uint32_t x[4] = {w.x << 16, w.x & 0xFFFF0000u, w.y << 16, w.y & 0xFFFF0000u};
+    for (; key < upto; key += kAhead) {
+      uint2 w[kAhead];
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n)
+        w[n] = key + n < upto ? *reinterpret_cast<const uint2*>(v + (int64_t)(key + n) * a.v_ts) : make_uint2(0, 0);
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) {
+        const uint32_t x[4] = {w[n].x << 16, w[n].x & 0xFFFF0000u, w[n].y << 16, w[n].y & 0xFFFF0000u};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if ((x[i] & 0x7F800000u) == 0x7F800000u) sum[i] += __uint_as_float(x[i]);
       }
     }
+    key = max(j0 * kPrTile, min(key, upto));
+    if (!(rows >> r & 1u)) continue;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (sum[i] == 0.f) continue;
       if (part != nullptr)
-        part[c + i] += sum[i];
+        part[r * 128 + 4 * lane + i] = sum[i];
       else
-        out[c + i] = f2bf_bits(__uint_as_float((uint32_t)out[c + i] << 16) + sum[i]);
+        out[r * a.o_ts + 4 * lane + i] = f2bf_bits(sum[i]);
     }
   }
 }
@@ -931,6 +944,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (used) pr_wait(&o_full[q], o_reads >> q & 1u, dead);
         if (shared) pr_wait(&o_full[other], o_reads >> other & 1u, dead);
         tc_after();
+        float2 not_finite = make_float2(0.f, 0.f);  // sums of zero times each value: NaN from what is not finite
 #pragma unroll 1
         for (int c = 0; c < 128; c += 32) {
           const bool used = opaque(used_), shared = opaque(shared_), part = opaque(part_);
@@ -964,6 +978,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = 0.f;
           }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) not_finite = fma2(make_float2(v[e], v[e + 1]), make_float2(0.f, 0.f), not_finite);
           if (part) {
             if (have) {
 #pragma unroll
@@ -994,10 +1010,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                 *reinterpret_cast<uint4*>(o + p * a.o_ts + c) = make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
           }
         }
-        if (*reinterpret_cast<volatile uint32_t*>(const_cast<uint32_t*>(&k.odd)) != 0u) {
+        // (a row whose scores are NaN stays NaN)
+        const bool live = have && l == l && l != 0.f, spoilt = live && !(not_finite.x + not_finite.y == 0.f);
+        const bool odd = *reinterpret_cast<volatile uint32_t*>(const_cast<uint32_t*>(&k.odd)) != 0u;
+        if (__any_sync(0xFFFFFFFFu, odd || spoilt)) {
           __syncwarp();  // (the row's pieces are other lanes' stores)
           __threadfence_block();
-          if (have && l != 0.f) pr_add_odd(a, k, j0, end, bound, part ? po : nullptr, a.out + row * a.o_ts + (int64_t)k.head * a.o_hs);
+          pr_put_odd(a, k, j0, end, bound, live, part ? po - 128 * lane : nullptr,
+                     a.out + (row - lane) * a.o_ts + (int64_t)k.head * a.o_hs);
         }
       }
       if (used) o_reads ^= 1u << q;
@@ -1056,6 +1076,8 @@ __global__ void __launch_bounds__(256) mla_prompt_join_kernel(const __grid_const
 #pragma unroll
   for (int i = 0; i < 2; ++i) f[i] = ml[i].y == 0.f ? 0.f : exp2f(ml[i].x - M);
   const float l = warp_sum(fmaf(f[0], ml[0].y, f[1] * ml[1].y));
+  // (an infinity counts whatever its weight)
+  auto add = [](float w, float v, float o) { return fmaf(fabsf(v) < INFINITY ? w : 1.0f, v, o); };
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
   for (int s0 = 0;; fetch(s0)) {
@@ -1066,10 +1088,10 @@ __global__ void __launch_bounds__(256) mla_prompt_join_kernel(const __grid_const
       const float w = __shfl_sync(0xFFFFFFFFu, s < 32 ? f[0] : f[1], s & 31);
       const float some = __shfl_sync(0xFFFFFFFFu, s < 32 ? ml[0].y : ml[1].y, s & 31);
       if (some == 0.f) continue;
-      o.x = fmaf(w, v[i].x, o.x);
-      o.y = fmaf(w, v[i].y, o.y);
-      o.z = fmaf(w, v[i].z, o.z);
-      o.w = fmaf(w, v[i].w, o.w);
+      o.x = add(w, v[i].x, o.x);
+      o.y = add(w, v[i].y, o.y);
+      o.z = add(w, v[i].z, o.z);
+      o.w = add(w, v[i].w, o.w);
     }
     s0 += kPrJoin;
     if (s0 >= a.splits) break;

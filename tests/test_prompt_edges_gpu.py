@@ -4,6 +4,8 @@ Rows of the cache are compared byte by byte; tolerances of attention are those o
 test_prompt_attn_gpu (derived there).
 """
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -88,3 +90,23 @@ def test_references_that_move_with_every_key_tile(docs, heads, cap):
         kv[:, :, 0] = (torch.arange(len(kv), device="cuda").float() / 8).to(torch.bfloat16)[:, None]
 
     attend(43, docs, heads, cap=cap, change=change)
+
+
+@pytest.mark.parametrize("docs,heads", [([(1000, 1000)], 3), ([(90, 1000)], 3), ([(2, 9000)], 3), ([(300, 4000)], 3),
+                                        ([(700, 700), (40, 650), (650, 700)], 3)])
+@pytest.mark.parametrize("how", ["steep", "wide", "cap", "all"])
+def test_an_infinite_value_counts_whatever_its_weight(docs, heads, how):
+    """Keys that a row sees with a weight that underflows, in tiles on an edge and within: an
+    infinity is an infinity, infinities of both signs and NaN are NaN, in every row that sees them."""
+    def change(q, kv, k_pe):
+        if how == "wide":
+            q.mul_(60.0)
+        at = 0
+        for _, nk in docs:
+            for key, column, bad in ((100, 7, math.inf), (300, 9, -math.inf), (100, 11, math.inf), (300, 11, -math.inf),
+                                     (600, 13, math.nan), (639, 127, math.inf)):
+                kv[at + key, :, 128 + column] = bad
+            at += nk
+
+    attend(46, docs, heads, causal=how != "all", cap=30.0 if how == "cap" else 0.0,
+           slopes=None if how == "wide" else [3000.0, 20.0, 0.5], change=change)
