@@ -802,11 +802,12 @@ MLA_API int mla_prompt_create(mla_prompt_t* out, int heads);
  * A row that sees no key gets zeros and an lse of -infinity.  Query rows of no
  * document are left as they are.  What a row does not see is never used as a value,
  * infinities and NaN included; an infinity or a NaN that it does see counts however
- * small its weight (infinities of both signs are NaN).  Scores, sums, references and denominators are
- * FP32; the weights meet the values as BF16 (2^-8 of a weight at most); capped
- * scores are off by at most 2^-20 of the softcap more.  Results do not depend on
- * the order in which the GPU runs the work.  Calls sharing a handle, captured or
- * not, must be ordered on one stream: they share its workspace.
+ * small its weight (infinities of both signs are NaN).  Finite values of any size stay
+ * in range (an average next to BF16's largest value may round to infinity).  Scores,
+ * sums, references and denominators are FP32; the weights meet the values as BF16 (2^-8
+ * of a weight at most); capped scores are off by at most 2^-20 of the softcap more.
+ * Results do not depend on the order in which the GPU runs the work.  Calls sharing a
+ * handle, captured or not, must be ordered on one stream: they share its workspace.
  * Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.
  */
 MLA_API int mla_prompt_attn(mla_prompt_t h, int docs, int64_t q_tokens, int64_t k_tokens,

@@ -78,8 +78,9 @@ struct PromptArgs {
   uint16_t* out;
   int64_t o_ts, o_hs;
   float* lse;  // [q_tokens][heads] or null
+  float above, times;  // how much lower exponents are taken (base 2); 2 to that
   int splits;
-  float* part_o;    // [splits][heads][q_tokens][128]
+  float* part_o;    // [splits][heads][q_tokens][128], each part's output
   float2* part_ml;  // [splits][heads][q_tokens] reference in base 2, sum
   const uint16_t* v;
   int64_t v_ts, v_hs;

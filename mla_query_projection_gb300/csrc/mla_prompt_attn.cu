@@ -20,8 +20,12 @@
 //  * A softmax thread owns one query row: its maximum, its sum and its mask need
 //    no other lane.  The row's reference (what exponents are taken relative to)
 //    is its first tile's maximum, and moves only when a score passes it by more
-//    than 20 in base 2; only then is O rescaled.  P then reaches 2^20, as exact in
-//    BF16 as at 1, and what is summed stays far below FP32's limits.
+//    than 16 in base 2; only then is O rescaled.  All exponents are taken lower by as
+//    much (`above`) as keeps the weights of all keys together below 1, so that no sum of
+//    finite values leaves FP32's range; weights below 2^-80 of the largest are lost.
+//    (Weights of up to 2^20 overflowed with values of 2^108.  Exponents stay within 32,
+//    whose last bit is 2^-19, for 32,768 keys.  With a lower reference instead, by each
+//    document's own keys, 24 documents of 100 to 1,000 rows took 292 us, so 287.)
 //  * What a row sees are the first `bound` keys of its document: its own place
 //    and all before it, or its document's two-way prefix, or all.  Tiles that no
 //    row of theirs needs are not touched, and only those on an edge are masked.
@@ -44,6 +48,7 @@
 // 65,536 keys is bound by memory: 88 us, 6.2 TB/s.  Short documents are bound by the
 // chain of scores, softmax and sums, of which TMEM holds two: 24 of 100 to 1,000 rows,
 // 64 heads, take 283 us, where their bytes take 144.
+#include <math.h>
 #include <stdlib.h>
 
 #include "mla_attn_tc.cuh"
@@ -54,7 +59,7 @@ struct mla_prompt {
   int num_sms;
   int heads;
   uint32_t* err;    // flags, then (at 2 and 3) items handed out and CTAs done with them
-  float* part_o;    // sums of split rows
+  float* part_o;    // outputs of split rows' parts
   float2* part_ml;  // their references and denominators
 };
 
@@ -66,7 +71,7 @@ constexpr int kPrUnit = 16384;   // bytes of a ring slot
 constexpr int kPrRing = 8;
 constexpr int kPrThreads = 384;  // two softmax warpgroups; warps that load, multiply (two) and hand out work
 constexpr int kPrQ = 3 * kPrUnit;  // a query tile: planes of 64 columns
-constexpr float kPrRoom = 20.0f;  // base 2
+constexpr int kPrRoom = 16;  // base 2
 constexpr int kPrChunks = 96;    // sums of the documents' tiles
 constexpr int kPrItems = 4;      // items of work in flight
 constexpr int kPrReaders = 11;   // warps that read them
@@ -847,7 +852,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], s[c + e], s[c + e + 4]);
         const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * unit2 + low;
         // The reference: the first maximum; later only where it is passed by far.
-        const bool grow = mx > ref + kPrRoom || (ref == -INFINITY && mx > -INFINITY);
+        const bool grow = mx > ref + (float)kPrRoom || (ref == -INFINITY && mx > -INFINITY);
         if (__any_sync(0xFFFFFFFFu, grow)) {
           float f = 1.0f;
           if (grow) {
@@ -870,7 +875,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             }
           }
         }
-        const float minus = ref == -INFINITY ? 0.f : low - ref;
+        const float minus = ref == -INFINITY ? 0.f : low - ref - a.above;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -926,14 +931,15 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const bool have = i < k.nq, part = a.splits > 1;
         const uint32_t used_ = used, shared_ = shared, part_ = part;
         const int64_t row = k.q0 + i;
-        const float inv = part ? 1.0f : l == 0.f ? 0.f : rcp_approx(l);
+        const float inv = l == 0.f ? 0.f : rcp_approx(l);
         f0 *= inv;
         f1 *= inv;
         if (have) {
+          const float sum = l * a.times;
           if (part)
-            a.part_ml[((int64_t)k.split * a.heads + k.head) * a.q_tokens + row] = make_float2(ref, l);
+            a.part_ml[((int64_t)k.split * a.heads + k.head) * a.q_tokens + row] = make_float2(ref, sum);
           else if (a.lse != nullptr)
-            a.lse[row * a.heads + k.head] = l == 0.f ? -INFINITY : (ref + lg2_approx(l)) * 0.6931471805599453f;
+            a.lse[row * a.heads + k.head] = l == 0.f ? -INFINITY : (ref + lg2_approx(sum)) * 0.6931471805599453f;
         }
         // Four neighbouring lanes trade 16-byte pieces, so that they store 64 bytes of
         // one row after another: 8 rows an instruction, not 32.
@@ -1038,8 +1044,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 
 // --------------------------------------------------------------- joining
 //
-// A warp a (row, head): with M the largest reference of its parts,
-// out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  Lane i has the weights of parts i
+// A warp a (row, head): with M the largest reference of its parts and f_i = 2^(m_i - M) l_i,
+// out = sum (f_i / sum f) o_i, o_i a part's output.  Lane i has the weights of parts i
 // and i + 32, and four columns of every part, eight parts on their way at a time
 // before their weights are known.  Bound by the trips to L2: 7 parts of 600 rows x
 // 16 heads are 34 MB.
@@ -1074,8 +1080,10 @@ __global__ void __launch_bounds__(256) mla_prompt_join_kernel(const __grid_const
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
   float f[2];  // (what saw nothing may hold anything)
 #pragma unroll
-  for (int i = 0; i < 2; ++i) f[i] = ml[i].y == 0.f ? 0.f : exp2f(ml[i].x - M);
-  const float l = warp_sum(fmaf(f[0], ml[0].y, f[1] * ml[1].y));
+  for (int i = 0; i < 2; ++i) f[i] = ml[i].y == 0.f ? 0.f : exp2f(ml[i].x - M) * ml[i].y;
+  const float l = warp_sum(f[0] + f[1]), inv = l == 0.f ? 0.f : 1.0f / l;
+  f[0] *= inv;
+  f[1] *= inv;
   // (an infinity counts whatever its weight)
   auto add = [](float w, float v, float o) { return fmaf(fabsf(v) < INFINITY ? w : 1.0f, v, o); };
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1096,9 +1104,8 @@ __global__ void __launch_bounds__(256) mla_prompt_join_kernel(const __grid_const
     s0 += kPrJoin;
     if (s0 >= a.splits) break;
   }
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
   uint16_t* out = a.out + row * a.o_ts + (int64_t)head * a.o_hs + 4 * lane;
-  *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
   if (a.lse != nullptr && lane == 0)
     a.lse[row * a.heads + head] = l == 0.f ? -INFINITY : M * 0.6931471805599453f + logf(l);
 }
@@ -1326,6 +1333,10 @@ int mla_prompt_attn(mla_prompt_t h, int docs, int64_t q_tokens, int64_t k_tokens
   a.o_ts = out_token_stride;
   a.o_hs = out_head_stride;
   a.lse = lse;
+  int above = mla::kPrRoom + 1;  // (1 for the reference's rounding)
+  while (((int64_t)1 << (above - mla::kPrRoom - 1)) < k_tokens) ++above;
+  a.above = (float)above;
+  a.times = ldexpf(1.0f, above);
   a.part_o = h->part_o;
   a.part_ml = h->part_ml;
   a.err = h->err;

@@ -110,3 +110,27 @@ def test_an_infinite_value_counts_whatever_its_weight(docs, heads, how):
 
     attend(46, docs, heads, causal=how != "all", cap=30.0 if how == "cap" else 0.0,
            slopes=None if how == "wide" else [3000.0, 20.0, 0.5], change=change)
+
+
+@pytest.mark.parametrize("docs,heads", [([(700, 700)], 3), ([(100, 1500)], 2), ([(2, 9000)], 3), ([(260, 4000)], 4),
+                                        ([(40, 40), (300, 300)], 2)])
+@pytest.mark.parametrize("rising", [False, True])
+@pytest.mark.parametrize("signs", [False, True])
+def test_values_up_to_the_end_of_the_range(docs, heads, rising, signs):
+    """Values of 2^126: a thousand of them are beyond FP32, their average is not.  With scores
+    that rise a weight is taken relative to one far below it."""
+    def change(q, kv, k_pe):
+        v = kv[..., 128:].float().clamp(-1, 1)
+        kv[..., 128:] = ((v if signs else 0.5 + 0.5 * v.abs()) * 2.0 ** 126).to(torch.bfloat16)
+        if rising:
+            q[..., 0] = 7.0
+            kv[:, :, 0] = (torch.arange(len(kv), device="cuda").float() / 8).to(torch.bfloat16)[:, None]
+
+    attend(44, docs, heads, change=change)
+    attend(44, docs, heads, change=change, causal=False)
+
+
+@pytest.mark.parametrize("docs,heads", [([(700, 700)], 3), ([(3, 20000)], 16)])
+def test_small_values(docs, heads):
+    """Values of 2^-85, far above what the tolerance adds (2^-99.6)."""
+    attend(45, docs, heads, change=lambda q, kv, k_pe: kv[..., 128:].mul_(2.0 ** -85))
