@@ -793,7 +793,8 @@ MLA_API int mla_prompt_create(mla_prompt_t* out, int heads);
  *                 queries and of [..][256] up-projected rows are fine.
  *   softmax_scale >= 0, finite.  softcap: 0 for none, else 1e-6 at least
  *                 and MLA_MAX_SOFTCAP at most.
- *   slopes        device FP32 [heads], finite, or NULL for no bias.
+ *   slopes        device FP32 [heads], finite, or NULL for no bias.  (A bias beyond
+ *                 FP32's range is infinite.)
  *   out           device BF16 [q_tokens][heads][128], strides alike; rows that do
  *                 not overlap one another or an input.
  *   lse           device FP32 [q_tokens][heads], natural logarithm of the sum of

@@ -753,7 +753,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const int base_row = k.r0 + qt * kPrTile + 32 * quad;
       const int i = base_row + lane;  // this thread's row of the document
       const int bound = pr_bound(min(i, k.nq - 1), k.nq, k.nk, k.prefix, causal);
-      const float slope = BIAS ? -a.slopes[k.head] * 1.4426950408889634f : 0.f;
+      float slope = BIAS ? -a.slopes[k.head] * 1.4426950408889634f : 0.f;
+      if (BIAS && fabsf(slope) == INFINITY) slope = copysignf(3.4028234e38f, slope);  // (none at no distance)
       float ref = -INFINITY, l = 0.f;
       for (int j = jfirst; j < nt; j += step) {
         pr_wait(&s_full[q], uses & 1u, dead);
@@ -767,7 +768,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         // out of the instruction cache: 24 documents of 100 to 1,000 rows took 579 us
         // capped, when 32 columns took 398.)
         const int near = base_row + (k.nk - k.nq) - j * kPrTile;  // the warp's first row among the tile's keys
-        const bool apart = CAP || (BIAS && (at_edge || !(near >= kPrTile - 1 || near + 31 <= 0)));
+        const bool apart = CAP || (BIAS && (at_edge || !(near >= kPrTile || near + 31 <= 0)));
         if (apart) {
           constexpr int kPre = LONG ? 64 : 32;
 #pragma unroll 1
@@ -829,12 +830,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         }
         // What the scores below lack: the rounding of slope times place, the same for a
         // row's keys (2^-24 of it, which for a steep slope is more than a near key's own).
+        // From 2^24 on that is more than an exponent has room for (slopes of 1e31 gave
+        // infinite weights), and no two key tiles' keys that are so far weigh alike.
         float low = 0.f;
         if constexpr (BIAS && !CAP) {
           if (!apart) {  // keys on one side of the warp's rows: the distance is linear
             const float sg = near > 0 ? slope : -slope, own = (float)(near + lane);
             const float2 k0 = make_float2(sg * own, sg * own), k1 = make_float2(-sg, -sg), u2 = make_float2(scale2, scale2);
-            low = fmaf(sg, own, -k0.x);
+            low = fabsf(k0.x) < 0x1p24f ? fmaf(sg, own, -k0.x) : 0.f;
 #pragma unroll
             for (int c = 0; c < 128; c += 2) {
               const float2 x = fma2(make_float2(s[c], s[c + 1]), u2, fma2(k1, make_float2((float)c, (float)(c + 1)), k0));

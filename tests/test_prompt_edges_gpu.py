@@ -13,7 +13,7 @@ import torch
 from mla_query_projection_gb300 import binding as B
 from mla_query_projection_gb300 import runner as R
 
-from .test_prompt_attn_gpu import attend, cuda_device  # noqa: F401
+from .test_prompt_attn_gpu import SCALE, attend, cuda_device, i32, inputs  # noqa: F401
 from .test_prompt_rows_gpu import write_case
 
 pytestmark = pytest.mark.gpu
@@ -134,3 +134,25 @@ def test_values_up_to_the_end_of_the_range(docs, heads, rising, signs):
 def test_small_values(docs, heads):
     """Values of 2^-85, far above what the tolerance adds (2^-99.6)."""
     attend(45, docs, heads, change=lambda q, kv, k_pe: kv[..., 128:].mul_(2.0 ** -85))
+
+
+@pytest.mark.parametrize("slope", [1e5, 1e8, 1e31, 1e36, 3e38])
+@pytest.mark.parametrize("n,nq", [(700, 700), (827, 700), (9000, 3)])
+def test_slopes_up_to_the_end_of_the_range(slope, n, nq):
+    """Any key but a row's own has a weight of zero, its bias finite or not; the own one, at no
+    distance, has no bias (see test_steep_slopes_near_the_row)."""
+    heads = 2
+    q, kv, k_pe = inputs(47, nq, n, heads)
+    attn = R.PromptAttention(heads)
+    lse = torch.empty(nq, heads, device="cuda")
+    for cap in (0.0, 30.0):
+        out, _ = attn.attend(q[..., :128], q[..., 128:], kv[..., :128], k_pe, kv[..., 128:], i32([0, nq]), SCALE,
+                             cu_k=i32([0, n]), softcap=cap, slopes=torch.full((heads,), slope, device="cuda"), lse=lse)
+        key = torch.cat([kv[..., :128], k_pe[:, None].expand(n, heads, 64)], -1).double()[n - nq:]
+        score = (q.double() * key).sum(-1) * SCALE
+        mag = (q.double() * key).abs().sum(-1) * SCALE
+        score = cap * torch.tanh(score / cap) if cap else score
+        assert ((lse.double() - score).abs() <= 2.0 ** -15.4 * mag + 2.0 ** -20 * (1 + cap) + 2.0 ** -21 * score.abs()).all()
+        assert torch.equal(out, kv[n - nq:, :, 128:])
+    assert attn.error_flags() == 0
+    attn.close()
