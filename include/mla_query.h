@@ -791,8 +791,9 @@ MLA_API int mla_prompt_create(mla_prompt_t* out, int heads);
  *                 i) at t * token_stride + h * head_stride + i (elements; 0 means
  *                 contiguous; multiples of 8, below 2^38).  Views of [..][192]
  *                 queries and of [..][256] up-projected rows are fine.
- *   softmax_scale >= 0, finite.  softcap: 0 for none, else 1e-6 at least
- *                 and MLA_MAX_SOFTCAP at most.
+ *   softmax_scale >= 0, 3e38 at most; without a cap or slopes, scores of up to 1e7
+ *                 in magnitude (beyond, exponents are rounded by more than 1).
+ *                 softcap: 0 for none, else 1e-6 at least and MLA_MAX_SOFTCAP at most.
  *   slopes        device FP32 [heads], finite, or NULL for no bias.  (A bias beyond
  *                 FP32's range is infinite.)
  *   out           device BF16 [q_tokens][heads][128], strides alike; rows that do

@@ -737,7 +737,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const int q = warp >> 2, quad = warp & 3;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
     const uint32_t st = tmem + lanes + 128 * q;
-    const float scale2 = a.scale * 1.4426950408889634f;
+    const float scale2 = fminf(a.scale * 1.4426950408889634f, 3.4028234e38f);  // (finite: a score of zero stays zero)
     // capped: x = C - 2 C / (1 + 2^(s e)), e = 2 scale log2(e) / cap, in base 2
     const float capC = CAP ? a.cap * 1.4426950408889634f : 0.f, capE = CAP ? fminf(2.0f * scale2 / a.cap, 1e30f) : 0.f;
     const float unit2 = CAP || BIAS ? 1.0f : scale2;

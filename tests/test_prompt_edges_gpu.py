@@ -156,3 +156,8 @@ def test_slopes_up_to_the_end_of_the_range(slope, n, nq):
         assert torch.equal(out, kv[n - nq:, :, 128:])
     assert attn.error_flags() == 0
     attn.close()
+
+
+def test_the_largest_scale():
+    """Scores of zero stay zero."""
+    attend(48, [(300, 300)], 2, scale=2.9e38, change=lambda q, kv, k_pe: q.zero_())
