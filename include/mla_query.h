@@ -807,7 +807,8 @@ MLA_API int mla_prompt_create(mla_prompt_t* out, int heads);
  * small its weight (infinities of both signs are NaN).  Finite values of any size stay
  * in range (an average next to BF16's largest value may round to infinity).  Scores,
  * sums, references and denominators are FP32; the weights meet the values as BF16 (2^-8
- * of a weight at most); capped scores are off by at most 2^-20 of the softcap more.
+ * of a weight at most; finite values whose weight is below 2^-80 of the row's largest may
+ * not count); capped scores are off by at most 2^-20 of the softcap more.
  * Results do not depend on the order in which the GPU runs the work.  Calls sharing a
  * handle, captured or not, must be ordered on one stream: they share its workspace.
  * Returns MLA_OK, MLA_EINVAL or MLA_ECUDA.
