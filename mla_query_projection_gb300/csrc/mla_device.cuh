@@ -245,6 +245,16 @@ __device__ __forceinline__ float2 fmul2_rn(float2 a, float2 b) {
   return d;
 }
 
+// The same of two products and sums, each rounded once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mov.b64 rc, {%6, %7};\n\tfma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 // RMSNorm of a BF16 pair: (x * rr) * gamma in FP32, each product rounded to
 // nearest, then rounded to a BF16 pair.
 __device__ __forceinline__ uint32_t rms_scale_bf16x2(uint32_t x, float rr, uint32_t gamma) {

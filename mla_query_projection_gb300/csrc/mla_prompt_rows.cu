@@ -159,15 +159,6 @@ __global__ void __launch_bounds__(kRopeThreads, 6) mla_rope_kernel(const __grid_
 // handed on in BF16 where the caller wants it.  A lane has latent columns
 // 8 lane .. and 256 + 8 lane .., and two values of the rope part.  The next token's row is on its way while this one is worked on.
 
-__device__ __forceinline__ float2 fma2_rn(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-      "mov.b64 rc, {%6, %7};\n\tfma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-
 // Quotients of a token by one divisor, each correctly rounded, as a division gives
 // them: by P. Markstein's theorem (IBM Journal of Research and Development 34, 1990),
 // with y the rounded reciprocal of b and q = a y rounded, q + (a - b q) y rounded once
@@ -189,7 +180,7 @@ struct Divisor {
   // two, in packed arithmetic
   __device__ __forceinline__ float2 quotients(float2 a) const {
     const float2 y2 = make_float2(y, y), q = fmul2_rn(a, y2);
-    const float2 r = fma2_rn(fma2_rn(make_float2(-q.x, -q.y), make_float2(b, b), a), y2, q);
+    const float2 r = fma2(fma2(make_float2(-q.x, -q.y), make_float2(b, b), a), y2, q);
     return make_float2(corrected(q.x, r.x), corrected(q.y, r.y));
   }
   // the E4M3 codes of a pair of BF16 values, of two pairs
