@@ -159,29 +159,36 @@ __global__ void __launch_bounds__(kRopeThreads, 6) mla_rope_kernel(const __grid_
 // handed on in BF16 where the caller wants it.  A lane has latent columns
 // 8 lane .. and 256 + 8 lane .., and two values of the rope part.  The next token's row is on its way while this one is worked on.
 
+// a b + c of two, each rounded once, down: a sum of zeros of both signs is -0.
+__device__ __forceinline__ float2 fma2_rm(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mov.b64 rc, {%6, %7};\n\tfma.rm.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 // Quotients of a token by one divisor, each correctly rounded, as a division gives
 // them: by P. Markstein's theorem (IBM Journal of Research and Development 34, 1990),
 // with y the rounded reciprocal of b and q = a y rounded, q + (a - b q) y rounded once
-// is the rounded a / b.  Where the quotient is far beyond E4M3's range the product is
-// as good (and may be infinite), and where it is zero the product alone has the sign of
-// a / b (a sum of zeros of both signs is +0); divisors near the ends of FP32's range are
-// divided by.
+// is the rounded a / b.  What is in brackets is exact, so that its rounding decides
+// the sign of a zero alone: -0 leaves q its own.  Where the quotient is far beyond
+// E4M3's range the product is as good (and may be infinite); divisors near the ends of
+// FP32's range, and negative ones, are divided by.
 struct Divisor {
   float b, y;
   bool plain;
   __device__ __forceinline__ explicit Divisor(float divisor) {
     b = divisor;
     y = __frcp_rn(divisor);
-    plain = !(fabsf(divisor) >= 0x1p-60f && fabsf(divisor) <= 0x1p60f);
-  }
-  __device__ __forceinline__ static float corrected(float q, float r) {
-    return fabsf(q) < 0x1p20f && q != 0.0f ? r : q;
+    plain = !(divisor >= 0x1p-60f && divisor <= 0x1p60f);
   }
   // two, in packed arithmetic
   __device__ __forceinline__ float2 quotients(float2 a) const {
     const float2 y2 = make_float2(y, y), q = fmul2_rn(a, y2);
-    const float2 r = fma2(fma2(make_float2(-q.x, -q.y), make_float2(b, b), a), y2, q);
-    return make_float2(corrected(q.x, r.x), corrected(q.y, r.y));
+    const float2 r = fma2(fma2_rm(make_float2(-q.x, -q.y), make_float2(b, b), a), y2, q);
+    return make_float2(fabsf(q.x) < 0x1p20f ? r.x : q.x, fabsf(q.y) < 0x1p20f ? r.y : q.y);
   }
   // the E4M3 codes of a pair of BF16 values, of two pairs
   __device__ __forceinline__ uint16_t codes(uint32_t w) const {
