@@ -45,11 +45,12 @@
 //  * Few query rows: the keys are split over several CTAs, whose sums a second
 //    kernel joins.
 //
-// Long documents are bound by the tensor pipe: 8,192 causal rows of 16 heads take 217
-// us (1,582 TFLOP/s), 4,096 rows of 64 heads that see all 375 (1,833).  One row on
-// 65,536 keys is bound by memory: 88 us, 6.2 TB/s.  Short documents are bound by the
-// chain of scores, softmax and sums, of which TMEM holds two: 24 of 100 to 1,000 rows,
-// 64 heads, take 283 us, where their bytes take 144.
+// Long documents are bound by the tensor pipe: 8,192 causal rows of 16 heads take 218
+// us back to back in a graph (1,576 TFLOP/s) and 232 called one by one; 4,096 rows of 64
+// heads that see all 375 (1,833; up to 5 % more on a GPU that draws its power sooner).
+// One row on 65,536 keys is bound by memory: 88 us, 6.2 TB/s.  Short documents are bound
+// by the chain of scores, softmax and sums, of which TMEM holds two: 24 of 100 to 1,000
+// rows, 64 heads, take 285 us, where their bytes take 144.
 #include <math.h>
 #include <stdlib.h>
 

@@ -358,7 +358,8 @@ class PromptAttention:
         [documents + 1] say where the documents lie (``cu_k`` None: where the queries
         do).  ``out`` BF16 [tokens, heads, 128] is allocated, as memory of the call's
         stream, where it is not given; ``lse`` FP32 [tokens, heads] is written where it
-        is."""
+        is.  Rows of no document (padding behind the last one) are not written: those of
+        an ``out`` that was allocated here hold anything, NaN included."""
         if out is None and isinstance(q_nope, torch.Tensor) and q_nope.is_cuda:
             with _allocating_on(stream, q_nope.device):
                 out = torch.empty(q_nope.shape, dtype=torch.bfloat16, device=q_nope.device)
